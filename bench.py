@@ -1156,8 +1156,8 @@ def run_e2e(rn, wl, src, dev, ws, args, dist):
 # included: the streamed and row-wise norm kernels and dw_reduce for the
 # training shapes; plus the split-row forward for decode-sized batches (at
 # most 64 rows), the double backward, or the projection kernels.
-_NORM_SOURCES = ("api.cu", "common.cuh", "context.h", "params.h", "registry.h", "reduce.cuh",
-                 "rows.cuh", "rows_bf16_generic.cu", "rows_bf16_shaped.cu",
+_NORM_SOURCES = ("api.cu", "common.cuh", "context.h", "host.h", "params.h", "registry.h",
+                 "reduce.cuh", "rows.cuh", "rows_bf16_generic.cu", "rows_bf16_shaped.cu",
                  "rows_f16_generic.cu", "rows_f16_shaped.cu", "rows_f32.cu", "stream.cuh",
                  "stream_small.cuh", "stream.cu", "stream_f16.cu")
 KERNEL_SOURCES = {
