@@ -302,6 +302,95 @@ int rmsnorm_bwd_bwd(const void *dy, const void *x, const void *w,
                     int dtype, void *stream);
 
 /*
+ * 8-bit floating point. q tensors hold one byte an element, in one of two
+ * formats (their largest finite value F: 448 and 57344), with fp32 scales
+ * beside them; the value that an element stands for is q * scale. Scales are
+ * dense row-major: with G = ceil(H / 128) groups of 128 columns (the last may
+ * be shorter), [M, G] for rows, [ceil(M / 128), G] for blocks of 128 x 128.
+ */
+typedef enum { RMSNORM_E4M3 = 0, RMSNORM_E5M2 = 1 } rmsnorm_fp8_type;
+
+/* Limits of the calls below that are not bound by RMSNORM_MAX_H. */
+#define RMSNORM_FP8_MAX_K (1 << 24)
+#define RMSNORM_FP8_MAX_ROWS (1 << 30)
+
+/*
+ * Forward, plain (r and h NULL) or fused with the residual add, whose output
+ * is 8-bit: what the projections after the norm read when they run in 8 bits
+ * (rmsnorm_gemm_fp8). For each row, v = x or v = h = round(x + r) (rounded to
+ * the dtype and stored, as rmsnorm_residual_fwd does),
+ *   rstd = 1 / sqrt( (1/H) sum_j v_j^2 + eps )
+ *   y_j  = v_j * rstd * w_j                              (fp32, not stored)
+ * and for each group of 128 columns
+ *   scale = max( max |y_j|, 2^-100 ) / F
+ *   q_j   = y_j / scale rounded to nearest even in the format.
+ * y goes to 8 bits in one rounding: it is not rounded to the dtype first, as
+ * the norm followed by rmsnorm_quant_fp8 would. A group that holds a NaN or
+ * an infinity gets a NaN scale and NaN throughout.
+ *   x [M,H] (ldx) in; r [M,H] (ldr) in or NULL; w [H] in;
+ *   q [M,H] (ldq, in bytes) out; scale [M,G] out; h [M,H] (ldh) out, with r
+ *   only; rstd [M] fp32 out or NULL (with h, or x, what rmsnorm_bwd_strided
+ *   wants of the forward).
+ *   qtype: an rmsnorm_fp8_type. Row strides as in rmsnorm_fwd_strided; bytes
+ *   of q between the rows are left as they are.
+ * Aliasing: h may be exactly x or r; nothing else may share a byte.
+ * Errors: those of rmsnorm_fwd_strided; RMSNORM_ERR_BAD_DTYPE for qtype too.
+ * M == 0 launches nothing.
+ */
+int rmsnorm_fwd_fp8(const void *x, int64_t ldx, const void *r, int64_t ldr,
+                    const void *w, void *q, int64_t ldq, float *scale, void *h,
+                    int64_t ldh, float *rstd, int64_t M, int64_t H, float eps,
+                    int dtype, int qtype, void *stream);
+
+/*
+ * A matrix as it is rounded to 8 bits: scales and roundings as above with
+ * y = x. block_rows = 1: a scale for each 128 columns of a row (the input of
+ * a projection that no norm precedes); block_rows = 128: one for each block
+ * of 128 x 128 (a projection's weight, once when a model is loaded). Other
+ * values are RMSNORM_ERR_UNSUPPORTED.
+ *   x [M,H] (ldx) in; q [M,H] (ldq, in bytes) out; scale out.
+ * 1 <= H <= RMSNORM_FP8_MAX_K. Nothing may share a byte. Errors otherwise as
+ * for rmsnorm_fwd_fp8.
+ */
+int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
+                      float *scale, int64_t M, int64_t H, int block_rows,
+                      int dtype, int qtype, void *stream);
+
+/*
+ * The product of two 8-bit tensors, out = A B^T with their scales: a
+ * projection (B: a linear layer's weight, as rmsnorm_gemv_fwd's A) of rows
+ * that rmsnorm_fwd_fp8 or rmsnorm_quant_fp8 wrote.
+ *   out_mn = round( sum_g a_scale[m,g] b_scale[n / 128,g]
+ *                   sum_{k in group g} a_mk b_nk )
+ * with the products of a group accumulated in fp32 on the tensor cores, the
+ * groups in fp32, and one rounding to the dtype.
+ *   a [M,K] (lda) of format a_type, a_scale [M,G];
+ *   b [N,K] (ldb) of format b_type, b_scale [ceil(N / 128),G], where
+ *   G = ceil(K / 128);
+ *   out [M,N] (ldo) of dtype (RMSNORM_F32, RMSNORM_BF16 or RMSNORM_F16).
+ *   Elements of out between its rows are left as they are.
+ * Alignment: a and b 16-byte aligned, lda and ldb multiples of 16 (else
+ *   RMSNORM_ERR_MISALIGNED; K itself may be any, and the bytes past K are
+ *   not read into the result). Strides of tensors of one row are ignored.
+ * Limits (else RMSNORM_ERR_UNSUPPORTED): M, N <= RMSNORM_FP8_MAX_ROWS,
+ *   K <= RMSNORM_FP8_MAX_K, M * N / 2048 < 2^31; a driver that offers the
+ *   tensor-map encoder.
+ * Aliasing: out may share no byte with an input. Deterministic: no atomics,
+ *   sums in a fixed order. Any M from one token to a prompt's batch; M == 0
+ *   launches nothing.
+ * flags: 0, or RMSNORM_GEMM_FP8_STATIC_WEIGHTS: no work still in flight on
+ *   the stream when this call is enqueued writes b or b_scale; the kernel
+ *   then fetches them while the preceding kernel is still running, as with
+ *   RMSNORM_GEMV_STATIC_WEIGHTS. Unknown bits give RMSNORM_ERR_BAD_FLAGS.
+ */
+#define RMSNORM_GEMM_FP8_STATIC_WEIGHTS 1
+int rmsnorm_gemm_fp8(const void *a, int64_t lda, const float *a_scale,
+                     int a_type, const void *b, int64_t ldb,
+                     const float *b_scale, int b_type, void *out, int64_t ldo,
+                     int64_t M, int64_t N, int64_t K, int dtype, int flags,
+                     void *stream);
+
+/*
  * Bytes of workspace rmsnorm_bwd, rmsnorm_residual_bwd, rmsnorm_bwd_ex,
  * rmsnorm_bwd_strided and rmsnorm_bwd_bwd need for (M, H, dtype) on the
  * current CUDA device (one fp32 row of H per CTA of the backward grid; the
@@ -344,7 +433,9 @@ void rmsnorm_set_path_override(int path);
  * rows; 7: the product on tcgen05 with K split over a cluster, automatic
  * above 8 rows on rows narrower than 2048 features; 8: the persistent
  * product on tcgen05, automatic above 8 rows on rows of 2048 features or
- * more; each also takes the rows only it holds), 0 none. */
+ * more; each also takes the rows only it holds), 9 the 8-bit rows
+ * (rmsnorm_fwd_fp8, rmsnorm_quant_fp8), 10 the 8-bit blocks, 11 the 8-bit
+ * product, 0 none. */
 int rmsnorm_last_path(void);
 
 /*

@@ -1,6 +1,6 @@
 """Build librmsnorm.so (the C-ABI CUDA library) in-tree for sm_103a.
 
-Each translation unit under csrc/ is compiled by nvcc in parallel into
+Each translation unit under csrc/ (and csrc/fp8/) is compiled by nvcc in parallel into
 _build/, then linked into rmsnorm_fwd_bwd_02_gb300/librmsnorm.so. A unit is
 rebuilt when it, any header under csrc/ or include/, or this file is newer
 than its object. No cmake; plain nvcc with one -gencode.
@@ -16,6 +16,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+SOURCE_DIRS = (CSRC, os.path.join(CSRC, "fp8"))
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librmsnorm.so")
@@ -33,8 +34,9 @@ def _nvcc():
 
 
 def _newest_dep_mtime():
-    deps = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = glob.glob(os.path.join(INCLUDE, "*.h"))
+    for d in SOURCE_DIRS:
+        deps += glob.glob(os.path.join(d, "*.cuh")) + glob.glob(os.path.join(d, "*.h"))
     deps.append(os.path.abspath(__file__))
     return max(os.path.getmtime(d) for d in deps)
 
@@ -51,7 +53,7 @@ def _compile(src, obj, extra):
 
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int = 0) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    sources = sorted(s for d in SOURCE_DIRS for s in glob.glob(os.path.join(d, "*.cu")))
     dep_t = _newest_dep_mtime()
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     todo = []

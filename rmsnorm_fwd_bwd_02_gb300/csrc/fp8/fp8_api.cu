@@ -1,0 +1,328 @@
+// fp8_api.cu -- the 8-bit entry points of include/rmsnorm.h: host-side
+// argument checks, kernel choice and launches. No allocation, no
+// synchronisation, no host copies; everything is enqueued on the caller's
+// stream.
+#include <algorithm>
+#include <cmath>
+
+#include "../host.h"
+#include "../registry.h"
+#include "fp8.h"
+#include "fp8_gemm.cuh"
+#include "fp8_registry.h"
+
+using namespace rmsk;
+
+namespace {
+
+constexpr int kPathFp8Rows = 9, kPathFp8Blocks = 10, kPathFp8Gemm = 11;
+
+bool fp8_type(int t) { return t == RMSNORM_E4M3 || t == RMSNORM_E5M2; }
+
+const Fp8RowSet &fp8_set(int dtype)
+{
+    return dtype == RMSNORM_BF16 ? fp8_rows_bf16
+                                 : (dtype == RMSNORM_F16 ? fp8_rows_f16 : fp8_rows_f32);
+}
+
+// Whether rows of packs of E elements (es bytes each; one byte in q) start
+// aligned to the pack, up to 16 bytes for what is read through the cached
+// path, in every tensor.
+bool packs_fit(int E, size_t es, int64_t H, const void *x, int64_t ldx, const void *r, int64_t ldr,
+               const void *w, const void *q, int64_t ldq, const void *h, int64_t ldh)
+{
+    const size_t a = (size_t)E * es;
+    if (E == 1)
+        return true;
+    return H % E == 0 && aligned(x, a) && aligned(r, a) && aligned(h, a) && aligned(w, 16) &&
+           aligned(q, (size_t)E) && strides_multiple(a, es, {ldx, ldr, ldh}) &&
+           strides_multiple((size_t)E, 1, {ldq});
+}
+
+cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void *arg)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void *args[1] = {arg};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: the widest
+// packs that every row's alignment allows; of those, rows that share a warp
+// where they are short enough, else a CTA a row.
+const Fp8RowKernel &pick_fp8_rows(const Fp8RowSet &set, int wide, int mode, int64_t M, int64_t H,
+                                  int sms)
+{
+    if (wide == 2)
+        return set.k[7];
+    if (wide == 1)
+        return set.k[6];
+    for (int i = 0; i < 3; ++i)
+        if (H <= (int64_t)set.k[i].lanes * set.k[i].V * set.k[i].E)
+            return set.k[i];
+    if (M <= 2 * (int64_t)sms)
+        return set.k[3];
+    return mode == 2 ? set.k[4] : set.k[5];
+}
+
+int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream)
+{
+    Fp8RowsParams p = prm;
+    const Fp8RowSet &set = fp8_set(dtype);
+    const size_t es = elem_size(dtype);
+    int dev, sms, bps, st;
+    if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
+        return st;
+    int wide = 0;
+    while (!packs_fit(set.k[wide == 0 ? 0 : 5 + wide].E, es, p.H, p.x, p.ldx, p.r, p.ldr, p.w, p.q,
+                      p.ldq, p.h, p.ldh))
+        ++wide;
+    const int64_t Hw = std::min<int64_t>(p.H, kFp8Window);      // widest window
+    const int windows = (int)((p.H + kFp8Window - 1) / kFp8Window);
+    const Fp8RowKernel &k = pick_fp8_rows(set, wide, mode, p.M * windows, Hw, sms);
+    int threads = k.max_threads;
+    int64_t tile = k.G;
+    if (k.lanes) {
+        tile *= threads / k.lanes;
+    } else {
+        const int64_t lanes = ((Hw + k.E - 1) / k.E + k.V - 1) / k.V;
+        threads = (int)((lanes + 31) / 32 * 32);
+    }
+    if ((st = blocks_per_sm(k.fn[mode], threads, dev, &bps)))
+        return st;
+    const int64_t tiles = (p.M + tile - 1) / tile;
+    const int64_t cap = std::max<int64_t>((int64_t)bps * sms / windows, 1);
+    const cudaError_t e = launch1(k.fn[mode], dim3((unsigned)std::min(tiles, cap), (unsigned)windows),
+                                  threads, stream, &p);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    t_last_path = kPathFp8Rows;
+    return RMSNORM_OK;
+}
+
+int blocks_impl(const Fp8RowsParams &r, int dtype, cudaStream_t stream)
+{
+    Fp8BlocksParams p = {r.x, r.q, r.scale, r.M, r.H, r.G, r.e5m2, r.ldx, r.ldq};
+    const Fp8RowSet &set = fp8_set(dtype);
+    int wide = 0;
+    while (!packs_fit(set.blocks_E[wide], elem_size(dtype), p.H, p.x, p.ldx, nullptr, 0, nullptr, p.q,
+                      p.ldq, nullptr, 0))
+        ++wide;
+    const int64_t rb = (p.M + kFp8Group - 1) / kFp8Group;
+    const cudaError_t e =
+        launch1(set.blocks[wide], dim3((unsigned)p.G, (unsigned)std::min<int64_t>(rb, 65535)),
+                256, stream, &p);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    t_last_path = kPathFp8Blocks;
+    return RMSNORM_OK;
+}
+
+// ------------------------------------------------------------- the product
+int gemm_impl(const void *a, int64_t lda, const float *sa, int at, const void *b, int64_t ldb,
+              const float *sb, int bt, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
+              int dtype, int flags, cudaStream_t stream)
+{
+    static const int kBN[4] = {16, 32, 64, 128};
+    int dev, sms, bps, st;
+    if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
+        return st;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr)
+        return RMSNORM_ERR_UNSUPPORTED;
+    const int G = (int)((K + kFp8Group - 1) / kFp8Group);
+    // the narrowest column operand that holds the tokens, whose scales must
+    // fit in shared memory; else tokens in tiles of 128 rows
+    int v = 0;
+    Fp8GemmLayout L;
+    int KS = 1;
+    int64_t tiles_r = 0, tiles_c = 0;
+    for (;; ++v) {
+        const bool swap = v < 3;
+        const int BN = kBN[v];
+        if (swap && M > BN)
+            continue;
+        tiles_r = ((swap ? N : M) + kFp8TileR - 1) / kFp8TileR;
+        tiles_c = ((swap ? M : N) + BN - 1) / BN;
+        KS = (int)std::max<int64_t>(1, std::min<int64_t>({8, G, sms / (tiles_r * tiles_c)}));
+        const int ng = (G + KS - 1) / KS;
+        const int most = swap ? (v == 2 ? 8 : 6) : 6;
+        L = fp8_gemm_layout(BN, swap, std::min(ng, most), ng);
+        if (!swap || L.total <= 227u * 1024u)
+            break;
+    }
+    const bool swap = v < 3;
+    const int BN = kBN[v];
+    const int64_t ctas = tiles_r * tiles_c * KS;
+    if (ctas > INT32_MAX)
+        return RMSNORM_ERR_UNSUPPORTED;
+    // [rows][K] bytes, 128-byte swizzle, reads past the end zero: boxes of
+    // `box_rows` rows x 128 columns
+    auto make_map = [&](CUtensorMap *map, const void *base, int64_t rows, int64_t ld, int box_rows) {
+        const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)ld};
+        const cuuint32_t box[2] = {(cuuint32_t)kFp8Group, (cuuint32_t)box_rows};
+        const cuuint32_t estr[2] = {1, 1};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
+                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUtensorMap mapA, mapB;
+    if (make_map(&mapA, a, M, lda, swap ? BN : kFp8TileR) != CUDA_SUCCESS ||
+        make_map(&mapB, b, N, ldb, swap ? kFp8TileR : BN) != CUDA_SUCCESS)
+        return cuda_fail(cudaErrorInvalidValue);
+    unsigned int *tmo = stream_timeout_counter(dev);
+    if (tmo == nullptr)
+        return cuda_fail(cudaErrorInvalidSymbol);
+    const void *fn = fp8_gemm_kernels.fn[v][dtype];
+    const size_t es = elem_size(dtype);
+    Fp8GemmParams p = {sa, sb, out, ldo, (int)M, (int)N, G, KS, (int)tiles_r,
+                       swap ? umma_idesc_f8((uint32_t)bt, (uint32_t)at, kFp8TileR, BN)
+                            : umma_idesc_f8((uint32_t)at, (uint32_t)bt, kFp8TileR, BN),
+                       (flags & RMSNORM_GEMM_FP8_STATIC_WEIGHTS) ? 1 : 0,
+                       aligned(out, 4 * es) && ldo % 4 == 0 ? 1 : 0,
+                       g_test_extra_tx.load(std::memory_order_relaxed),
+                       g_test_wait_us.load(std::memory_order_relaxed), L};
+    if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)))
+        return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)fp8_gemm_threads(BN));
+    cfg.dynamicSmemBytes = L.total;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)KS;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = KS > 1 ? 2 : 1;
+    void *args[4] = {&p, swap ? &mapB : &mapA, swap ? &mapA : &mapB, &tmo};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    t_last_path = kPathFp8Gemm;
+    return RMSNORM_OK;
+}
+
+// Checks and the launch that rmsnorm_fwd_fp8 and the row form of
+// rmsnorm_quant_fp8 share. w null: x alone.
+int rows_checked(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *w, bool norm,
+                 void *q, int64_t ldq, float *scale, void *h, int64_t ldh, float *rstd, int64_t M,
+                 int64_t H, float eps, int dtype, int qtype, int block_rows, cudaStream_t stream)
+{
+    const bool res = r != nullptr || h != nullptr;
+    if (!stride_ok(ldx, M, H) || !stride_ok(ldq, M, H) ||
+        (res && (!stride_ok(ldr, M, H) || !stride_ok(ldh, M, H))))
+        return RMSNORM_ERR_BAD_STRIDE;
+    if (M == 0)
+        return RMSNORM_OK;
+    if (!x || (norm && !w) || !q || !scale || (res && (!r || !h)))
+        return RMSNORM_ERR_NULLPTR;
+    const size_t es = elem_size(dtype);
+    if (!aligned(x, es) || !aligned(r, es) || !aligned(w, es) || !aligned(h, es) ||
+        !aligned(scale, 4) || !aligned(rstd, 4))
+        return RMSNORM_ERR_MISALIGNED;
+    if (!res)
+        ldr = ldh = H;
+    const int64_t G = (H + kFp8Group - 1) / kFp8Group;
+    const int64_t srows = block_rows == 1 ? M : (M + kFp8Group - 1) / kFp8Group;
+    const Span sx = rows_span(x, M, H, ldx, es), sr = rows_span(r, M, H, ldr, es),
+               sw = flat(w, (size_t)H * es), sq = rows_span(q, M, H, ldq, 1),
+               ss = flat(scale, (size_t)(srows * G) * 4), sh = rows_span(h, M, H, ldh, es),
+               st = flat(rstd, (size_t)M * 4);
+    for (Span o : {sq, ss, st})
+        for (Span i : {sx, sr, sw, sh})
+            if (overlap(o, i))
+                return RMSNORM_ERR_ALIAS;
+    if (overlap(sq, ss) || overlap(sq, st) || overlap(ss, st) || overlap(sh, sw) ||
+        (!sh.empty() && (!same_or_disjoint(sh, sx) || !same_or_disjoint(sh, sr))))
+        return RMSNORM_ERR_ALIAS;
+    const Fp8RowsParams p = {x, r, w, q, scale, h, rstd, M, (int)H, (int)G, eps,
+                             qtype == RMSNORM_E5M2 ? 1 : 0, ldx, ldr, ldq, ldh};
+    if (block_rows != 1)
+        return blocks_impl(p, dtype, stream);
+    return rows_impl(p, norm ? (res ? 2 : 1) : 0, dtype, stream);
+}
+
+} // namespace
+
+extern "C" {
+
+int rmsnorm_fwd_fp8(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *w, void *q,
+                    int64_t ldq, float *scale, void *h, int64_t ldh, float *rstd, int64_t M,
+                    int64_t H, float eps, int dtype, int qtype, void *stream)
+{
+    const int st = check_common(M, H, eps, dtype);
+    if (st)
+        return st;
+    if (!fp8_type(qtype))
+        return RMSNORM_ERR_BAD_DTYPE;
+    return rows_checked(x, ldx, r, ldr, w, true, q, ldq, scale, h, ldh, rstd, M, H, eps, dtype,
+                        qtype, 1, static_cast<cudaStream_t>(stream));
+}
+
+int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq, float *scale, int64_t M,
+                      int64_t H, int block_rows, int dtype, int qtype, void *stream)
+{
+    if ((dtype != RMSNORM_F32 && dtype != RMSNORM_BF16 && dtype != RMSNORM_F16) || !fp8_type(qtype))
+        return RMSNORM_ERR_BAD_DTYPE;
+    if (M < 0 || H < 1 || M > INT64_MAX / 8 / H)
+        return RMSNORM_ERR_BAD_SHAPE;
+    if (H > RMSNORM_FP8_MAX_K || (block_rows != 1 && block_rows != kFp8Group))
+        return RMSNORM_ERR_UNSUPPORTED;
+    return rows_checked(x, ldx, nullptr, 0, nullptr, false, q, ldq, scale, nullptr, 0, nullptr, M, H,
+                        0.f, dtype, qtype, block_rows, static_cast<cudaStream_t>(stream));
+}
+
+int rmsnorm_gemm_fp8(const void *a, int64_t lda, const float *a_scale, int a_type, const void *b,
+                     int64_t ldb, const float *b_scale, int b_type, void *out, int64_t ldo,
+                     int64_t M, int64_t N, int64_t K, int dtype, int flags, void *stream)
+{
+    if (flags & ~RMSNORM_GEMM_FP8_STATIC_WEIGHTS)
+        return RMSNORM_ERR_BAD_FLAGS;
+    if ((dtype != RMSNORM_F32 && dtype != RMSNORM_BF16 && dtype != RMSNORM_F16) ||
+        !fp8_type(a_type) || !fp8_type(b_type))
+        return RMSNORM_ERR_BAD_DTYPE;
+    if (M < 0 || N < 1 || K < 1)
+        return RMSNORM_ERR_BAD_SHAPE;
+    if (M > RMSNORM_FP8_MAX_ROWS || N > RMSNORM_FP8_MAX_ROWS || K > RMSNORM_FP8_MAX_K)
+        return RMSNORM_ERR_UNSUPPORTED;
+    // a single row has no stride: any that a tensor map takes
+    if (M == 1)
+        lda = (K + 15) / 16 * 16;
+    if (N == 1)
+        ldb = (K + 15) / 16 * 16;
+    if (M == 1)
+        ldo = std::max(ldo, N);
+    if (!stride_ok(lda, M, K) || !stride_ok(ldb, N, K) || !stride_ok(ldo, M, N))
+        return RMSNORM_ERR_BAD_STRIDE;
+    if (M == 0)
+        return RMSNORM_OK;
+    if (!a || !a_scale || !b || !b_scale || !out)
+        return RMSNORM_ERR_NULLPTR;
+    const size_t es = elem_size(dtype);
+    if (!aligned(a, 16) || !aligned(b, 16) || lda % 16 || ldb % 16 || !aligned(a_scale, 4) ||
+        !aligned(b_scale, 4) || !aligned(out, es))
+        return RMSNORM_ERR_MISALIGNED;
+    const int64_t G = (K + kFp8Group - 1) / kFp8Group;
+    const Span so = rows_span(out, M, N, ldo, es);
+    for (Span i : {rows_span(a, M, K, lda, 1), rows_span(b, N, K, ldb, 1),
+                   flat(a_scale, (size_t)(M * G) * 4),
+                   flat(b_scale, (size_t)((N + kFp8Group - 1) / kFp8Group * G) * 4)})
+        if (overlap(so, i))
+            return RMSNORM_ERR_ALIAS;
+    return gemm_impl(a, lda, a_scale, a_type, b, ldb, b_scale, b_type, out, ldo, M, N, K, dtype,
+                     flags, static_cast<cudaStream_t>(stream));
+}
+
+} // extern "C"

@@ -1,0 +1,399 @@
+// fp8_gemm.cuh -- the product of two 8-bit tensors with fp32 scales: A [M,K]
+// with a scale for each 128 columns of a row, B [N,K] with one for each block
+// of 128 x 128, on the fifth-generation tensor cores.
+//
+// Mathematics. With groups g of 128 columns,
+//   out[m,n] = sum_g sa[m,g] sb[n / 128,g] P_g[m,n],
+//   P_g[m,n] = sum_{k in g} qa[m,k] qb[n,k],
+// so the scales are constant within one step of 128 in K. P_g is formed by
+// four tcgen05.mma (K = 32 each, kind::f8f6f4, accumulated in fp32 in tensor
+// memory), read back, and added to fp32 sums in registers with one fused
+// multiply-add an element. The sums over the groups are thus plain fp32 sums
+// of correctly scaled terms; the only rounding to fewer bits is the last, to
+// the output's type.
+//
+// Tiles. One CTA to a tile of 128 rows of the "row operand" (tensor-memory
+// lanes) by BN rows of the "column operand" (tensor-memory columns), its K
+// split over a cluster of KS CTAs:
+//  - few tokens (SWAP): the weight B is the row operand and the tokens are
+//    the columns (BN = 16, 32 or 64 >= M), so a tile wastes no tensor-core
+//    row and every SM streams its own rows of the weight;
+//  - more: the tokens are the rows, 128 rows of B the columns.
+//
+// Roles (64 + 32 EW threads): warp 0 feeds a ring of stages (tensor copies,
+// 128-byte swizzle: a stage is 128 columns, exactly one swizzle span, of both
+// operands), warp 1 issues the MMAs into NB buffers of tensor memory in turn,
+// the EW other warps read the buffers and keep the sums. At the end each CTA
+// puts its sums in shared memory (over the ring, which is drained), the
+// cluster meets, and each CTA adds a part of the tile over its KS peers in
+// rank order and stores it: the same bits on every run.
+//
+// Every wait is bounded (about one second, or the test limit); one that runs
+// out counts in the library's timeout counter, and the CTA skips its work,
+// still meets its cluster, waits (bounded) for its copies and MMAs in flight
+// and frees its tensor memory.
+#pragma once
+
+#include "../gemv_tc.cuh"
+#include "fp8.h"
+
+namespace rmsk {
+
+constexpr int kFp8TileR = 128;                          // rows of the row operand
+constexpr uint32_t kFp8StageR = kFp8TileR * kFp8Group;  // its bytes in a stage
+
+__host__ __device__ constexpr int fp8_epi_warps(int BN) { return BN >= 128 ? 8 : 4; }
+__host__ __device__ constexpr int fp8_gemm_threads(int BN) { return 64 + 32 * fp8_epi_warps(BN); }
+__host__ __device__ constexpr int fp8_acc_bufs(int BN) { return BN >= 64 ? 2 : 4; }
+__host__ __device__ constexpr int fp8_tmem_cols(int BN) { return BN * fp8_acc_bufs(BN); }
+
+// Shared memory of one CTA, byte offsets from a 1024-byte aligned base: the
+// ring (NSt stages of 128 + BN rows of 128 bytes; the sums [128][BN + 4]
+// over it at the end), the scales of the tokens with SWAP ([groups][BN]),
+// the mbarriers (full, empty a stage; full, empty a buffer; drain), eight
+// words (tensor-memory address, failure flag, stages issued, consumed).
+struct Fp8GemmLayout {
+    int NSt;
+    uint32_t stage, sc, bar, slots, total;              // total: with 1023 bytes of alignment
+};
+
+__host__ __device__ inline Fp8GemmLayout fp8_gemm_layout(int BN, bool swap, int NSt, int groups)
+{
+    Fp8GemmLayout L;
+    L.NSt = NSt;
+    L.stage = kFp8StageR + (uint32_t)BN * kFp8Group;
+    const uint32_t ring = (uint32_t)NSt * L.stage;
+    const uint32_t sums = (uint32_t)kFp8TileR * (uint32_t)(BN + 4) * 4u;
+    L.sc = ((ring > sums ? ring : sums) + 15u) & ~15u;
+    L.bar = L.sc + (swap ? (uint32_t)groups * (uint32_t)BN * 4u : 0u);
+    L.slots = L.bar + 8u * (uint32_t)(2 * NSt + 2 * fp8_acc_bufs(BN) + 1);
+    L.total = L.slots + 32u + 1023u;
+    // An SM has 512 columns of tensor memory. A CTA that waits for its
+    // columns while a peer of its cluster holds some elsewhere could wait
+    // for ever, so no more CTAs may share an SM than have columns: each
+    // takes at least its share of the SM's 228 KB of shared memory.
+    const uint32_t least = 228u * 1024u / 512u * (uint32_t)fp8_tmem_cols(BN);
+    if (L.total < least)
+        L.total = least;
+    return L;
+}
+
+struct Fp8GemmParams {
+    const float *sa;   // [M,G]
+    const float *sb;   // [ceil(N / 128),G]
+    void *out;         // [M,N], row stride ldo
+    int64_t ldo;
+    int M, N, G;
+    int KS;            // CTAs of a cluster, which split the G groups
+    int tiles_r;       // tiles along the row operand
+    uint32_t idesc;    // instruction descriptor of the MMAs
+    int static_w;      // B and sb may be read before the wait on the previous kernel
+    int vec;           // rows of out start at multiples of four elements
+    uint32_t extra_tx, wait_limit_us;   // test hook of the bounded waits
+    Fp8GemmLayout L;
+};
+
+// Instruction descriptor of kind::f8f6f4: as umma_idesc_f16, the formats of
+// A and B (0 e4m3, 1 e5m2) each on its own.
+__host__ __device__ constexpr uint32_t umma_idesc_f8(uint32_t a, uint32_t b, int M, int N)
+{
+    return (1u << 4) | (a << 7) | (b << 10) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// D (tensor memory) = A B^T (+ D when accumulate != 0), kind::f8f6f4, K = 32.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Four floats of a peer's shared memory (cluster address).
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <typename T> __device__ __forceinline__ void store_out1(T *p, float v)
+{
+    if constexpr (sizeof(T) == 4)
+        *p = v;
+    else
+        st_row_b16(p, Half16<T>::narrow1(v));
+}
+
+template <typename T> __device__ __forceinline__ void store_out4(T *p, float4 v)
+{
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(p) = v;
+    else
+        asm volatile("st.global.v2.b32 [%0], {%1,%2};" ::"l"(p), "r"(Half16<T>::narrow2(v.x, v.y)),
+                     "r"(Half16<T>::narrow2(v.z, v.w))
+                     : "memory");
+}
+
+// grid = tiles x KS CTAs (KS consecutive ones a cluster); the tiles along the
+// row operand follow one another.
+template <typename T, int BN, bool SWAP>
+__global__ void __launch_bounds__(fp8_gemm_threads(BN))
+rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
+             const __grid_constant__ CUtensorMap tmC, unsigned int *timeouts)
+{
+    constexpr int EW = fp8_epi_warps(BN), NB = fp8_acc_bufs(BN);
+    constexpr int CW = BN * 4 / EW;                     // columns a thread sums
+    constexpr int SROW = BN + 4;                        // floats a row of the sums
+    constexpr uint32_t kCols = fp8_tmem_cols(BN);
+    extern __shared__ __align__(1024) unsigned char fp8_smem[];
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int KS = p.KS, rank = KS > 1 ? (int)cluster_ctarank() : 0;
+    const int g0 = rank * p.G / KS, ng = (rank + 1) * p.G / KS - g0;   // this CTA's groups
+    const int tile = (int)(blockIdx.x / KS);
+    const int r0 = tile % p.tiles_r * kFp8TileR, c0 = tile / p.tiles_r * BN;
+    const Fp8GemmLayout &L = p.L;
+    const int NSt = L.NSt;
+    const uint32_t raw_s = smem_addr(fp8_smem);
+    unsigned char *base = fp8_smem + (((raw_s + 1023u) & ~1023u) - raw_s);
+    const uint32_t ring_s = smem_addr(base);
+    float *sums = reinterpret_cast<float *>(base);
+    float *sc = reinterpret_cast<float *>(base + L.sc);
+    const uint32_t full0 = smem_addr(base + L.bar), empty0 = full0 + 8u * (uint32_t)NSt;
+    const uint32_t accf0 = empty0 + 8u * (uint32_t)NSt, acce0 = accf0 + 8u * NB;
+    const uint32_t dbar = acce0 + 8u * NB;
+    int *slots = reinterpret_cast<int *>(base + L.slots);
+    volatile int *fail = slots + 1;
+    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+
+    if (warp == 0) {
+        tmem_alloc(smem_addr(slots), kCols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (int s = 0; s < NSt; ++s) {
+            mbar_init(full0 + 8u * s, 1);
+            mbar_init(empty0 + 8u * s, 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(accf0 + 8u * b, 1);
+            mbar_init(acce0 + 8u * b, EW);
+        }
+        mbar_init(dbar, 1);
+        slots[1] = slots[2] = slots[3] = 0;
+    }
+    if (tid == 64) {
+        prefetch_tmap(&tmR);
+        prefetch_tmap(&tmC);
+    }
+    mbar_init_fence();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = static_cast<uint32_t>(slots[0]);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------------- copies
+            const CUtensorMap *tmW = SWAP ? &tmR : &tmC, *tmA = SWAP ? &tmC : &tmR;
+            const uint32_t offW = SWAP ? 0u : kFp8StageR, offA = SWAP ? kFp8StageR : 0u;
+            const int w0 = SWAP ? r0 : c0, a0 = SWAP ? c0 : r0;
+            // the weight's first stages may start before the previous kernel
+            // is complete
+            const int early = p.static_w ? min(ng, NSt) : 0;
+            for (int q = 0; q < early; ++q) {
+                mbar_expect_tx(full0 + 8u * q, L.stage + p.extra_tx);
+                tma_load_2d(ring_s + (uint32_t)q * L.stage + offW, tmW, (g0 + q) * kFp8Group, w0,
+                            full0 + 8u * q);
+                slots[2] = q + 1;
+            }
+            griddep_wait();
+            for (int q = 0; q < ng; ++q) {
+                const int s = q % NSt, u = q / NSt;
+                const uint32_t dst = ring_s + (uint32_t)s * L.stage, bar = full0 + 8u * s;
+                const int x = (g0 + q) * kFp8Group;
+                if (q >= early) {
+                    if (u > 0 && !tc_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail))
+                        break;
+                    mbar_expect_tx(bar, L.stage + p.extra_tx);
+                    tma_load_2d(dst + offW, tmW, x, w0, bar);
+                }
+                tma_load_2d(dst + offA, tmA, x, a0, bar);
+                slots[2] = q + 1;
+            }
+            griddep_launch_dependents();
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------------------------------------------- MMAs
+            const uint64_t dr0 = umma_desc_sw128(ring_s);
+            for (int q = 0; q < ng; ++q) {
+                const int s = q % NSt, b = q % NB;
+                if (q >= NB &&
+                    !tc_wait(acce0 + 8u * b, (uint32_t)((q / NB - 1) & 1), limit, fail))
+                    break;
+                if (!tc_wait(full0 + 8u * s, (uint32_t)((q / NSt) & 1), limit, fail))
+                    break;
+                tc_fence_after_sync();
+                const uint64_t da = dr0 + (uint64_t)((uint32_t)s * (L.stage >> 4));
+                const uint64_t db = da + (kFp8StageR >> 4);
+#pragma unroll
+                for (int k4 = 0; k4 < kFp8Group / 32; ++k4)
+                    umma_f8(tmem + (uint32_t)(b * BN), da + 2 * k4, db + 2 * k4, p.idesc,
+                            k4 != 0 ? 1u : 0u);
+                umma_commit(empty0 + 8u * s);
+                umma_commit(accf0 + 8u * b);
+                slots[3] = q + 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ the sums
+        const int etid = tid - 64, q4 = warp & 3, half = (warp - 2) / 4;
+        const int row = q4 * 32 + lane;                 // of the row operand's tile
+        const int col0 = half * CW;
+        griddep_wait();
+        const float *sb = p.sb + (int64_t)((SWAP ? r0 : c0) / kFp8Group) * p.G + g0;
+        const float *sa = p.sa + (int64_t)min(r0 + row, p.M - 1) * p.G + g0;
+        if constexpr (SWAP) {
+            for (int i = etid; i < ng * BN; i += EW * 32) {
+                const int g = i / BN, t = c0 + i % BN;
+                sc[i] = t < p.M ? p.sa[(int64_t)t * p.G + g0 + g] * __ldg(sb + g) : 0.f;
+            }
+            named_bar_sync(1, EW * 32);
+        }
+        float2 acc[CW / 2];
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i)
+            acc[i] = make_float2(0.f, 0.f);
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        for (int q = 0; q < ng; ++q) {
+            const int b = q % NB;
+            float s = 0.f;
+            if constexpr (!SWAP)
+                s = sa[q] * __ldg(sb + q);
+            // warp-uniform (the loads from tensor memory need every lane)
+            if (!__all_sync(0xFFFFFFFFu,
+                            tc_wait(accf0 + 8u * b, (uint32_t)((q / NB) & 1), limit, fail)))
+                break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lanes + (uint32_t)(b * BN + col0 + c), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float2 s2;
+                    if constexpr (SWAP)
+                        s2 = *reinterpret_cast<const float2 *>(sc + q * BN + col0 + c + 2 * j);
+                    else
+                        s2 = make_float2(s, s);
+                    const float2 x =
+                        make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    acc[c / 2 + j] = vfma(x, s2, acc[c / 2 + j]);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(acce0 + 8u * b);
+        }
+        // the ring is drained: the last buffer was complete, so every copy
+        // has landed and every MMA has read it (or the CTA has failed, and
+        // its sums do not matter but copies may still land: write nothing)
+        named_bar_sync(1, EW * 32);
+        if (!*fail) {
+            float4 *to = reinterpret_cast<float4 *>(sums + row * SROW + col0);
+#pragma unroll
+            for (int i = 0; i < CW / 4; ++i)
+                to[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+        }
+    }
+
+    // every role has finished or given up
+    if (KS > 1) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    if (*fail) {
+        if (tid == 0) {
+            for (int q = slots[3]; q < slots[2]; ++q)
+                (void)mbar_wait_bounded(full0 + 8u * (q % NSt), (uint32_t)((q / NSt) & 1), limit);
+            atomicAdd(timeouts, 1u);
+        }
+        if (tid == 32) {
+            umma_commit(dbar);
+            (void)mbar_wait_bounded(dbar, 0, limit);
+        }
+    } else if (warp >= 2) {
+        // this CTA's part of the tile, four columns at a time, the sums of
+        // its peers added in rank order
+        const int etid = tid - 64;
+        const int nc = SWAP ? (min(BN, p.M - c0) + 3) / 4 : BN / 4;   // column quads wanted
+        const int units = kFp8TileR * nc;
+        const int u0 = rank * units / KS, u1 = (rank + 1) * units / KS;
+        const uint32_t sums_s = ring_s;
+        T *out = static_cast<T *>(p.out);
+        for (int u = u0 + etid; u < u1; u += EW * 32) {
+            const int row = SWAP ? u % kFp8TileR : u / nc, c4 = SWAP ? u / kFp8TileR : u % nc;
+            const uint32_t at = (uint32_t)(row * SROW + c4 * 4) * 4u;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (KS == 1) {
+                v = *reinterpret_cast<const float4 *>(base + at);
+            } else {
+                for (int k = 0; k < KS; ++k) {
+                    const float4 w = ld_cluster_v4(cluster_map(sums_s + at, (uint32_t)k));
+                    v.x += w.x;
+                    v.y += w.y;
+                    v.z += w.z;
+                    v.w += w.w;
+                }
+            }
+            const float e[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (SWAP) {                       // row: a feature, columns: tokens
+                const int n = r0 + row;
+                if (n < p.N) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c0 + c4 * 4 + j < p.M)
+                            store_out1<T>(out + (int64_t)(c0 + c4 * 4 + j) * p.ldo + n, e[j]);
+                }
+            } else {
+                const int m = r0 + row, n = c0 + c4 * 4;
+                if (m < p.M) {
+                    T *to = out + (int64_t)m * p.ldo + n;
+                    if (p.vec && n + 4 <= p.N) {
+                        store_out4<T>(to, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (n + j < p.N)
+                                store_out1<T>(to + j, e[j]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before_sync();
+    if (KS > 1) {               // no CTA leaves while a peer may still read its sums
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 0) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+} // namespace rmsk

@@ -24,6 +24,7 @@ PATH_GEMV = 5            # reported by last_path() after rmsnorm_gemv_fwd: the
 PATH_GEMV_TMA = 6        # weight in registers (5), fed by bulk copies (6), or
 PATH_GEMV_UMMA = 7       # the product on tcgen05 (7); 6 and 7 also force it
 PATH_GEMV_TC = 8         # persistent tcgen05 kernel, y held per CTA (8; forces it)
+PATH_FP8_ROWS, PATH_FP8_BLOCKS, PATH_FP8_GEMM = 9, 10, 11   # reported only
 
 # Entry points of include/rmsnorm.h with their ctypes signatures.
 _i64, _vp, _sz, _int, _f = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
@@ -58,6 +59,12 @@ SIGNATURES = {
                                _sz, _i64, _i64, _f, _int, _vp]),
     "rmsnorm_gemv_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                 _i64, _i64, _f, _int, _int, _vp]),
+    "rmsnorm_fwd_fp8": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                               _i64, _vp, _i64, _i64, _f, _int, _int, _vp]),
+    "rmsnorm_quant_fp8": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int,
+                                 _int, _int, _vp]),
+    "rmsnorm_gemm_fp8": (_int, [_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _vp,
+                                _i64, _i64, _i64, _i64, _int, _int, _vp]),
 }
 
 BWD_ACCUMULATE_DW = 1
@@ -412,6 +419,157 @@ def rmsnorm_gemv_fwd(x, w, A, r=None, out=None, h=None, want_h=True, y=None,
         GEMV_STATIC_WEIGHTS if static_weights else 0, _stream(stream)),
         "rmsnorm_gemv_fwd")
     return out, h, rstd
+
+
+FP8_GROUP = 128
+FP8_TYPES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}   # rmsnorm_fp8_type
+FP8_MAX_K, FP8_MAX_ROWS = 1 << 24, 1 << 30
+GEMM_FP8_STATIC_WEIGHTS = 1
+
+
+def _fp8_code(name, dtype):
+    if dtype not in FP8_TYPES:
+        raise ValueError(f"{name} must be one of {sorted(map(str, FP8_TYPES))}, got {dtype}")
+    return FP8_TYPES[dtype]
+
+
+def _one_device(**tensors):
+    """The device that every given tensor is on."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError(f"{', '.join(tensors)} must be on one CUDA device, got "
+                         f"{sorted(map(str, devs))}")
+    return devs.pop()
+
+
+class _on:
+    """Runs a call on `device` and `stream` (its current stream when None):
+    what the binding allocates belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        if self.stream.device != device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {device}")
+        self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *a):
+        return self.ctx.__exit__(*a)
+
+
+def _scales(name, t, rows, H, device):
+    """fp32 scales [rows, ceil(H / 128)], made when not given."""
+    shape = (rows, -(-H // FP8_GROUP))
+    if t is None:
+        return torch.empty(shape, device=device, dtype=torch.float32)
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
+    return t
+
+
+def _fp8_rows(name, t, M, H, qdtype, device):
+    """An 8-bit [M, H] tensor and its row stride, made when not given with
+    rows that start at multiples of 16 bytes (as rmsnorm_gemm_fp8 reads them)."""
+    if t is None:
+        t = torch.empty(M, -(-H // 16) * 16, device=device, dtype=qdtype)[:, :H]
+    Mt, ld = _strided(name, t, H, qdtype)
+    if Mt != M:
+        raise ValueError(f"{name} must have {M} rows, got {Mt}")
+    return t, ld
+
+
+def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-6,
+                    qdtype=torch.float8_e4m3fn, want_rstd=True, stream=None):
+    """RMSNorm(x [+ r]) * w rounded to 8 bits, with one fp32 scale for each
+    128 columns of a row (see rmsnorm.h). x [M, H] with any row stride.
+    Returns (q, scale, rstd or None), with r (h, q, scale, rstd or None). q
+    is [M, H] of qdtype (float8_e4m3fn or float8_e5m2), scale [M, ceil(H /
+    128)]; q times its group's scale is the norm's output."""
+    H = w.numel()
+    M, ldx = _strided("x", x, H)
+    code = _dtype_code(x)
+    _rows("w", w.view(-1), H, x.dtype)
+    dev = _one_device(x=x, w=w, r=r, q=q, scale=scale, h=h, rstd=rstd)
+    qcode = _fp8_code("qdtype", qdtype)
+    ldr = ldh = H
+    with _on(dev, stream) as s:
+        if r is not None:
+            Mr, ldr = _strided("r", r, H, x.dtype)
+            if h is None:
+                h = torch.empty(M, H, device=dev, dtype=x.dtype)
+            Mh, ldh = _strided("h", h, H, x.dtype)
+            if Mr != M or Mh != M:
+                raise ValueError(f"r and h must have {M} rows")
+        elif h is not None:
+            raise ValueError("h is the residual variant's output: pass r too")
+        q, ldq = _fp8_rows("q", q, M, H, qdtype, dev)
+        scale = _scales("scale", scale, M, H, dev)
+        if rstd is None and want_rstd:
+            rstd = torch.empty(M, device=dev, dtype=torch.float32)
+        if rstd is not None and (rstd.dtype != torch.float32 or rstd.numel() != M
+                                 or not rstd.is_contiguous()):
+            raise ValueError(f"rstd must be a contiguous float32 tensor of {M} entries")
+        _check(lib().rmsnorm_fwd_fp8(
+            _ptr(x), ldx, _ptr(r), ldr, _ptr(w), _ptr(q), ldq, _ptr(scale), _ptr(h), ldh,
+            _ptr(rstd), M, H, float(eps), code, qcode, _stream(s)), "rmsnorm_fwd_fp8")
+    return (q, scale, rstd) if r is None else (h, q, scale, rstd)
+
+
+def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e4m3fn,
+                      stream=None):
+    """x [M, H] (any row stride) rounded to 8 bits: (q, scale), with one fp32
+    scale for each 128 columns of a row (block_rows=1, activations) or each
+    block of 128 x 128 (block_rows=128, weights); see rmsnorm.h."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, H]")
+    H = x.shape[1]
+    M, ldx = _strided("x", x, H)
+    code = _dtype_code(x)
+    qcode = _fp8_code("qdtype", qdtype)
+    if block_rows not in (1, FP8_GROUP):
+        raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
+    dev = _one_device(x=x, q=q, scale=scale)
+    with _on(dev, stream) as s:
+        q, ldq = _fp8_rows("q", q, M, H, qdtype, dev)
+        scale = _scales("scale", scale, -(-M // block_rows), H, dev)
+        _check(lib().rmsnorm_quant_fp8(_ptr(x), ldx, _ptr(q), ldq, _ptr(scale), M, H,
+                                       int(block_rows), code, qcode, _stream(s)),
+               "rmsnorm_quant_fp8")
+    return q, scale
+
+
+def rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16,
+                     static_weights=False, stream=None):
+    """out [M, N] = A B^T of 8-bit a [M, K] with a_scale [M, ceil(K / 128)]
+    and b [N, K] with b_scale [ceil(N / 128), ceil(K / 128)], as
+    rmsnorm_fwd_fp8 / rmsnorm_quant_fp8 return them (rows that start at
+    multiples of 16 bytes). out: any row stride; out_dtype float32, bfloat16
+    or float16 when it is not given. static_weights: nothing in flight on the
+    stream writes b or b_scale (see RMSNORM_GEMM_FP8_STATIC_WEIGHTS)."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"a [M, K] and b [N, K] must be 2-D with one K, got {tuple(a.shape)} "
+                         f"and {tuple(b.shape)}")
+    K, N = a.shape[1], b.shape[0]
+    acode, bcode = _fp8_code("a", a.dtype), _fp8_code("b", b.dtype)
+    M, lda = _strided("a", a, K)
+    _, ldb = _strided("b", b, K)
+    dev = _one_device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
+    _scales("a_scale", a_scale, M, K, dev)
+    _scales("b_scale", b_scale, -(-N // FP8_GROUP), K, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(M, N, device=dev, dtype=out_dtype)
+        Mo, ldo = _strided("out", out, N)
+        if Mo != M:
+            raise ValueError(f"out must have {M} rows, got {Mo}")
+        _check(lib().rmsnorm_gemm_fp8(
+            _ptr(a), lda, _ptr(a_scale), acode, _ptr(b), ldb, _ptr(b_scale), bcode, _ptr(out),
+            ldo, M, N, K, _dtype_code(out), GEMM_FP8_STATIC_WEIGHTS if static_weights else 0,
+            _stream(s)), "rmsnorm_gemm_fp8")
+    return out
 
 
 STATIC_SCRATCH_BYTES = 16 << 20     # RMSNORM_STATIC_SCRATCH_BYTES

@@ -1,0 +1,555 @@
+"""GPU tier: the 8-bit entry points (rmsnorm_fwd_fp8, rmsnorm_quant_fp8,
+rmsnorm_gemm_fp8) against their definitions in 64 bits.
+
+Tolerances, from the arithmetic. The norm's y, rstd and a group's largest
+magnitude are computed in fp32 (a handful of roundings of 2^-24, rsqrtf
+within 2 ulp, and a sum of squares whose lanes add at most 64 terms each
+before a tree): DELTA = 1e-5 relative covers them. A q must be what rounding
+y / scale gives for some y within DELTA of the exact one: rounding is
+monotonic, so it lies between the roundings of the two ends. The product
+accumulates 128 products and then G groups in fp32, each addition off by at
+most 2^-22 of the terms' absolute sum T so far (one rounding is 2^-24; the
+tensor cores may truncate): (128 + G) 2^-22 T, and half a step of the
+output's type for the last rounding.
+"""
+import pytest
+import torch
+
+from rmsnorm_fwd_bwd_02_gb300 import rmsnorm as rn
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+F64 = torch.float64
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+LARGEST = {E4M3: 448.0, E5M2: 57344.0}
+BITS = {E4M3: (3, -6), E5M2: (2, -14)}       # fraction bits, least exponent
+DELTA = 1e-5
+AMAX_MIN = 2.0 ** -100
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("the gpu tier needs a CUDA device")
+    rn.lib()
+    rn.set_path_override(rn.PATH_AUTO)
+    rn.wait_timeouts(reset=True)
+    yield
+    assert rn.wait_timeouts(reset=True) == 0
+
+
+# ------------------------------------------------------------------ oracle
+def round8(v, to):
+    """v (float64) to the nearest value of the format, ties to even."""
+    bits, low = BITS[to]
+    _, e = torch.frexp(v)
+    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp(min=low) - bits)
+    return (torch.round(v / step) * step).clamp(-LARGEST[to], LARGEST[to])
+
+
+def group_amax(y, rows):
+    """Largest magnitude [ceil(M / rows), G] of y [M, H]."""
+    M, H = y.shape
+    p = torch.nn.functional.pad(y.abs(), (0, -H % 128, 0, -M % rows))
+    return p.view(p.shape[0] // rows, rows, -1, 128).amax(dim=(1, 3))
+
+
+def spread(s, rows, M, H):
+    """Scales [R, G] as [M, H]."""
+    return s.repeat_interleave(rows, 0)[:M].repeat_interleave(128, 1)[:, :H]
+
+
+def check_q(q, scale, y, rows, to):
+    """q, scale (GPU) against exact y [M, H] (float64, finite)."""
+    M, H = y.shape
+    assert q.dtype == to and tuple(q.shape) == (M, H)
+    s = scale.cpu().to(F64)
+    want = group_amax(y, rows).clamp(min=AMAX_MIN) / LARGEST[to]
+    assert tuple(s.shape) == tuple(want.shape)
+    assert bool(((s - want).abs() <= DELTA * want).all()), float(((s - want).abs() / want).max())
+    v = y / spread(s, rows, M, H)
+    got = q.float().cpu().to(F64)
+    a, b = round8(v * (1 - DELTA), to), round8(v * (1 + DELTA), to)
+    lo, hi = torch.minimum(a, b), torch.maximum(a, b)
+    bad = (got < lo) | (got > hi)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist(),
+                                 float(got[bad][0]), float(v[bad][0]))
+
+
+def norm64(v, w, eps):
+    v, w = v.to(F64), w.to(F64)
+    rstd = 1.0 / torch.sqrt((v * v).mean(dim=1) + eps)
+    return v * rstd[:, None] * w[None, :], rstd
+
+
+def data(M, H, dtype, seed, outliers=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, H, generator=g)
+    if outliers and M * H >= 1000:
+        at = torch.randint(M * H, (M * H // 1000,), generator=g)
+        x.view(-1)[at] *= 50.0
+    r = torch.randn(M, H, generator=g) * 2
+    w = 1 + 0.1 * torch.randn(H, generator=g)
+    return x.to(dtype), r.to(dtype), w.to(dtype)
+
+
+SHAPES = [(1, 1), (1, 7), (3, 31), (2, 64), (5, 127), (70, 128), (9, 129), (64, 256), (33, 384),
+          (2, 511), (17, 512), (1, 896), (64, 896), (400, 896), (13, 1000), (7, 1001), (5, 2056),
+          (320, 4096), (1, 4096), (6, 4100), (310, 5120), (2, 16384), (311, 16384), (3, 16381)]
+
+
+@pytest.mark.parametrize("M,H", SHAPES)
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm(M, H, dtype, residual):
+    x, r, w = data(M, H, dtype, seed=M * 7 + H)
+    to = E5M2 if (M + H) % 3 == 0 else E4M3
+    if residual:
+        h, q, s, rstd = rn.rmsnorm_fwd_fp8(x.to(DEV), w.to(DEV), r=r.to(DEV), qdtype=to)
+        v = (x.to(F64) + r.to(F64)).to(dtype)
+        assert torch.equal(h.cpu(), v)
+    else:
+        q, s, rstd = rn.rmsnorm_fwd_fp8(x.to(DEV), w.to(DEV), qdtype=to)
+        v = x
+    assert rn.last_path() == rn.PATH_FP8_ROWS
+    y, rs = norm64(v, w, 1e-6)
+    assert bool(((rstd.cpu().to(F64) - rs).abs() <= DELTA * rs).all())
+    check_q(q, s, y, 1, to)
+
+
+@pytest.mark.parametrize("M,H", SHAPES + [(3, 16385), (2, 40000), (1, 32768)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quant(M, H, dtype, rows):
+    x, _, _ = data(M, H, dtype, seed=M + 3 * H)
+    to = E5M2 if (M + H) % 3 == 1 else E4M3
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows, qdtype=to)
+    assert rn.last_path() == (rn.PATH_FP8_ROWS if rows == 1 else rn.PATH_FP8_BLOCKS)
+    check_q(q, s, x.to(F64), rows, to)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quant_tall(rows):
+    """More blocks down than the grid's y holds is out of reach of a test; a
+    tall narrow matrix takes many."""
+    x, _, _ = data(40000, 130, BF16, seed=5)
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows)
+    check_q(q, s, x.to(F64), rows, E4M3)
+
+
+@pytest.mark.parametrize("to", [E4M3, E5M2])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quant_every_magnitude(to, rows):
+    """fp32 values over the whole range of exponents: tiny groups keep the
+    least scale, the largest do not overflow, zeros stay zeros."""
+    g = torch.Generator().manual_seed(3)
+    e = torch.arange(-140, 127, dtype=torch.float32)
+    x = torch.randn(e.numel(), 256, generator=g).clamp(-1.9, 1.9) * torch.exp2(e)[:, None].float()
+    x[::7] = 0.0
+    x[5, :128] = 0.0
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows, qdtype=to)
+    want = group_amax(x.to(F64), rows).clamp(min=AMAX_MIN) / LARGEST[to]
+    assert bool(((s.cpu().to(F64) - want).abs() <= DELTA * want).all())
+    check_q(q, s, x.to(F64), rows, to)
+    assert bool((q.float()[5, :128] == 0).all())
+
+
+def test_quant_is_exact_where_the_values_are():
+    """Values of the format times a power of two whose group's largest is the
+    format's largest come back bit for bit."""
+    codes = torch.arange(256, dtype=torch.uint8)
+    for to in (E4M3, E5M2):
+        v = codes.view(to).float()
+        v = v[torch.isfinite(v)]
+        v = torch.cat([v, torch.full((-v.numel() % 128,), LARGEST[to])])
+        x = v.view(-1, 128).clone()
+        x[:, 0] = LARGEST[to]
+        q, s = rn.rmsnorm_quant_fp8((x * 0.25).to(DEV), qdtype=to)
+        assert bool((s == 0.25).all())
+        assert torch.equal(q.float().cpu(), x)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("H", [384, 301])
+def test_quant_of_nonfinite_groups(bad, rows, H):
+    x, _, _ = data(130, H, BF16, seed=11)
+    x[2, 130] = bad
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows)
+    s = s.cpu()
+    hit = torch.zeros_like(s, dtype=torch.bool)
+    hit[2 // rows, 1] = True
+    assert torch.equal(torch.isnan(s), hit)
+    wide = spread(hit, rows, 130, H)
+    qf = q.float().cpu()
+    assert bool(torch.isnan(qf[wide]).all()) and bool(torch.isfinite(qf[~wide]).all())
+
+
+@pytest.mark.parametrize("H", [512, 1001])
+def test_norm_of_nonfinite_rows(H):
+    """A row with an infinity has rstd 0 (the infinity itself is NaN); a NaN
+    takes the whole row. Other rows are untouched by either."""
+    x, _, w = data(6, H, F32, seed=12)
+    x[1, 5], x[3, 200] = float("inf"), float("nan")
+    q, s, rstd = rn.rmsnorm_fwd_fp8(x.to(DEV), w.to(DEV))
+    s, qf = s.cpu(), q.float().cpu()
+    assert bool(torch.isnan(s[3]).all()) and bool(torch.isnan(qf[3]).all())
+    assert bool(torch.isnan(s[1, 0])) and bool(torch.isnan(qf[1, :128]).all())
+    assert bool((qf[1, 128:] == 0).all()) and bool(torch.isfinite(s[1, 1:]).all())
+    ok = [0, 2, 4, 5]
+    y, _ = norm64(x[ok], w, 1e-6)
+    check_q(q[ok], s[ok], y, 1, E4M3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,ld", [(128, 256), (4096, 4608), (896, 904), (1001, 1003)])
+def test_strides_and_guards(dtype, H, ld):
+    """Row windows of wider buffers, everything around them NaN or a guard
+    that must survive; the results are those of dense tensors."""
+    M = 37
+    x, r, w = data(M, H, dtype, seed=21)
+
+    def window(t):
+        buf = torch.full((M, ld), float("nan"), device=DEV, dtype=dtype)
+        buf[:, :H] = t.to(DEV)
+        return buf, buf[:, :H]
+
+    _, xs = window(x)
+    _, rs = window(r)
+    hb, hs = window(torch.zeros(M, H, dtype=dtype))
+    qb = torch.full((M + 2, ld), 0x5A, device=DEV, dtype=torch.uint8)
+    qs = qb[1:M + 1, :H].view(E4M3)
+    h, q, s, _ = rn.rmsnorm_fwd_fp8(xs, w.to(DEV), r=rs, h=hs, q=qs)
+    h0, q0, s0, _ = rn.rmsnorm_fwd_fp8(x.to(DEV), w.to(DEV), r=r.to(DEV))
+    assert torch.equal(h, h0)
+    y, _ = norm64(h0.cpu(), w, 1e-6)
+    check_q(q, s, y, 1, E4M3)
+    check_q(q0, s0, y, 1, E4M3)
+    assert bool(torch.isnan(hb[:, H:]).all())
+    assert bool((qb[0] == 0x5A).all()) and bool((qb[-1] == 0x5A).all())
+    assert bool((qb[:, H:] == 0x5A).all())
+    for rows in (1, 128):
+        qb.fill_(0x5A)
+        q, s = rn.rmsnorm_quant_fp8(xs, q=qs, block_rows=rows)
+        check_q(q, s, x.to(F64), rows, E4M3)
+        assert bool((qb[0] == 0x5A).all()) and bool((qb[-1] == 0x5A).all())
+        assert bool((qb[:, H:] == 0x5A).all())
+
+
+def test_norm_in_place_and_empty():
+    x, r, w = data(40, 896, BF16, seed=31)
+    xd, rd = x.to(DEV), r.to(DEV)
+    h0, q0, s0, rs0 = rn.rmsnorm_fwd_fp8(xd, w.to(DEV), r=rd)
+    h, q, s, rs = rn.rmsnorm_fwd_fp8(xd, w.to(DEV), r=rd, h=xd)
+    assert h.data_ptr() == xd.data_ptr() and torch.equal(h, h0)
+    assert torch.equal(q.view(torch.uint8), q0.view(torch.uint8)) and torch.equal(s, s0)
+    e = torch.empty(0, 896, device=DEV, dtype=BF16)
+    q, s, _ = rn.rmsnorm_fwd_fp8(e, w.to(DEV))
+    assert q.shape == (0, 896) and s.shape == (0, 7)
+    q, s = rn.rmsnorm_quant_fp8(e)
+    assert q.shape == (0, 896)
+    out = rn.rmsnorm_gemm_fp8(q, s, q0, s0[:1])
+    assert out.shape == (0, 40)
+
+
+# ----------------------------------------------------------------- product
+def pair(M, N, K, seed, at=E4M3, bt=E4M3):
+    g = torch.Generator().manual_seed(seed)
+    a = torch.randn(M, K, generator=g)
+    if M * K >= 1000:
+        a.view(-1)[torch.randint(M * K, (M * K // 1000,), generator=g)] *= 50.0
+    b = torch.randn(N, K, generator=g) * 0.02
+    qa, sa = rn.rmsnorm_quant_fp8(a.to(BF16).to(DEV), qdtype=at)
+    qb, sb = rn.rmsnorm_quant_fp8(b.to(BF16).to(DEV), block_rows=128, qdtype=bt)
+    torch.cuda.synchronize()       # calls with static weights may follow
+    return qa, sa, qb, sb
+
+
+def gemm64(qa, sa, qb, sb):
+    """(the product, the absolute sum of its terms), on the GPU in 64 bits."""
+    M, K = qa.shape
+    N = qb.shape[0]
+    a = qa.float().to(F64) * spread(sa.to(F64), 1, M, K)
+    b = qb.float().to(F64) * spread(sb.to(F64), 128, N, K)
+    return a @ b.t(), a.abs() @ b.abs().t()
+
+
+HALF = {BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}     # eps / 2
+TINY = {BF16: 0.0, F16: 2.0 ** -25, F32: 0.0}                  # half a subnormal step
+
+
+def check_out(out, want, T, K, dtype):
+    assert out.dtype == dtype and out.shape == want.shape
+    err = (out.to(F64) - want).abs()
+    bound = HALF[dtype] * want.abs() + (128 + -(-K // 128)) * 2.0 ** -22 * T * (1 + HALF[dtype]) \
+        + TINY[dtype] + 1e-300
+    bad = ~(err <= bound)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist(),
+                                 float(out[bad][0]), float(want[bad][0]), float(bound[bad][0]))
+
+
+GEMMS = [(1, 1, 1), (1, 128, 128), (1, 2048, 896), (2, 129, 127), (3, 7, 300), (8, 9728, 896),
+         (15, 257, 129), (16, 128, 4096), (16, 6144, 4096), (17, 300, 512), (31, 1000, 1000),
+         (32, 4096, 640), (33, 130, 1024), (64, 128, 16384), (64, 2048, 896), (63, 999, 5121),
+         (65, 128, 128), (100, 1, 257), (128, 512, 512), (129, 129, 129), (200, 640, 1100),
+         (256, 2048, 4096), (333, 1001, 5121), (511, 777, 64), (1024, 1024, 1024),
+         (1030, 1500, 2000), (1, 200, 70000), (64, 200, 70000), (300, 260, 33000)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMMS)
+def test_gemm(M, N, K):
+    i = GEMMS.index((M, N, K))
+    at, bt = ((E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2))[i % 4]
+    qa, sa, qb, sb = pair(M, N, K, seed=i, at=at, bt=bt)
+    want, T = gemm64(qa, sa, qb, sb)
+    first = None
+    for dtype in (BF16, F16, F32):
+        for static in (False, True):
+            out = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=dtype, static_weights=static)
+            assert rn.last_path() >= rn.PATH_FP8_GEMM
+            check_out(out, want, T, K, dtype)
+            if dtype == F32:
+                first = out if first is None else first
+                assert torch.equal(first, out)            # the same bits every time
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 130, 1000), (20, 300, 130), (64, 200, 257), (90, 100, 300),
+                                   (300, 515, 1000), (600, 1030, 2050)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_reads_and_writes_only_its_rows(M, N, K, dtype):
+    """Operands inside larger buffers of NaN bytes, and scales of NaN behind
+    the last row: nothing outside [M, K] and [N, K] is read into the result,
+    nothing outside [M, N] is written."""
+    qa, sa, qb, sb = pair(M, N, K, seed=M)
+    ldk = -(-K // 16) * 16 + 32
+
+    def inside(q, s):
+        rows = q.shape[0]
+        big = torch.full((rows + 200, ldk), 0x7F, device=DEV, dtype=torch.uint8)
+        v = big[64:64 + rows, 16:16 + K]
+        v.copy_(q.view(torch.uint8))
+        bs = torch.full((s.shape[0] + 64, s.shape[1]), float("nan"), device=DEV)
+        bs[32:32 + s.shape[0]] = s
+        return v.view(E4M3), bs[32:32 + s.shape[0]]
+
+    a, asc = inside(qa, sa)
+    b, bsc = inside(qb, sb)
+    for ldo, off in ((N, 0), (N + 5, 0), (-(-N // 16) * 16 + 16, 0), (N + 3, 1)):
+        buf = torch.full((M + 3, ldo), -77.0, device=DEV, dtype=dtype)
+        out = buf[1:M + 1, off:off + N]
+        rn.rmsnorm_gemm_fp8(a, asc, b, bsc, out=out)
+        want, T = gemm64(qa, sa, qb, sb)
+        check_out(out, want, T, K, dtype)
+        buf[1:M + 1, off:off + N] = -77.0
+        assert bool((buf == -77.0).all())
+
+
+def test_gemm_scales_of_every_size():
+    """Zero rows, rows and blocks of very large and very small scales, and a
+    NaN scale that stays in its row or its columns."""
+    for M in (5, 200, 700):
+        qa, sa, qb, sb = pair(M, 400, 640, seed=9)
+        sa[1] = 0.0
+        sa[2, 1], sa[3] = 1e30, 1e-30
+        sb[1] *= 1e-6
+        out = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+        want, T = gemm64(qa, sa, qb, sb)
+        check_out(out, want, T, 640, F32)
+        assert bool((out[1] == 0).all())
+        sa[4, 2] = float("nan")
+        out2 = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+        assert bool(torch.isnan(out2[4]).all())
+        keep = [i for i in range(M) if i != 4]
+        assert torch.equal(out2[keep], out[keep])
+        sb[3, 0] = float("nan")
+        out3 = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+        assert bool(torch.isnan(out3[:, 384:]).all())
+        assert torch.equal(out3[keep][:, :384], out[keep][:, :384])
+
+
+@pytest.mark.parametrize("M", [1, 16, 64, 100, 700])
+def test_rows_do_not_depend_on_one_another(M):
+    """A row's result is that of its own call (the tokens of a batch share
+    nothing but the weight), to the tolerance of another kernel's order."""
+    qa, sa, qb, sb = pair(M, 384, 1024, seed=40)
+    out = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+    for i in {0, M // 2, M - 1}:
+        one = rn.rmsnorm_gemm_fp8(qa[i:i + 1], sa[i:i + 1], qb, sb, out_dtype=F32)
+        want, T = gemm64(qa[i:i + 1], sa[i:i + 1], qb, sb)
+        check_out(one, want, T, 1024, F32)
+        check_out(out[i:i + 1], want, T, 1024, F32)
+
+
+# ---------------------------------------------------------- used together
+def layer(x, r, w, W, sW, W2, sW2, static):
+    """The norm of a residual sum, its projection, and a second projection of
+    that projection's output quantised on its own."""
+    h, q, s, _ = rn.rmsnorm_fwd_fp8(x, w, r=r, want_rstd=False)
+    z = rn.rmsnorm_gemm_fp8(q, s, W, sW, static_weights=static)
+    qz, sz = rn.rmsnorm_quant_fp8(z)
+    return h, q, s, z, qz, sz, rn.rmsnorm_gemm_fp8(qz, sz, W2, sW2, static_weights=static)
+
+
+def check_layer(x, r, w, W, sW, W2, sW2, res):
+    h, q, s, z, qz, sz, o = res
+    v = (x.cpu().to(F64) + r.cpu().to(F64)).to(x.dtype)
+    assert torch.equal(h.cpu(), v)
+    y, _ = norm64(v, w.cpu(), 1e-6)
+    check_q(q, s, y, 1, E4M3)
+    check_out(z, *gemm64(q, s, W, sW), q.shape[1], BF16)
+    check_q(qz, sz, z.cpu().to(F64), 1, E4M3)
+    check_out(o, *gemm64(qz, sz, W2, sW2), qz.shape[1], BF16)
+
+
+def layer_inputs(M, seed, H=896, N=2432):
+    x, r, w = data(M, H, BF16, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    W, sW = rn.rmsnorm_quant_fp8((torch.randn(N, H, generator=g) * 0.02).to(BF16).to(DEV),
+                                 block_rows=128)
+    W2, sW2 = rn.rmsnorm_quant_fp8((torch.randn(H, N, generator=g) * 0.02).to(BF16).to(DEV),
+                                   block_rows=128)
+    return x.to(DEV), r.to(DEV), w.to(DEV), W, sW, W2, sW2
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 64, 130, 700])
+@pytest.mark.parametrize("static", [False, True])
+def test_chain(M, static):
+    """Back to back, so that each call starts while the one before it ends;
+    every iteration has inputs of its own."""
+    x, r, w, W, sW, W2, sW2 = layer_inputs(M, seed=50)
+    torch.cuda.synchronize()
+    xs = [torch.roll(x, i, 0) * (1 + i) for i in range(6)]
+    torch.cuda.synchronize()
+    res = [layer(xi, r, w, W, sW, W2, sW2, static) for xi in xs]
+    torch.cuda.synchronize()
+    for xi, ri in zip(xs, res):
+        check_layer(xi, r, w, W, sW, W2, sW2, ri)
+
+
+@pytest.mark.parametrize("M", [1, 24, 300])
+def test_chain_in_a_graph(M):
+    """Captured once, replayed on new inputs in place; two captured graphs
+    do not share anything that a replay of one could spoil for the other."""
+    x, r, w, W, sW, W2, sW2 = layer_inputs(M, seed=60)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, r, w, W, sW, W2, sW2, True)
+    torch.cuda.current_stream().wait_stream(side)
+    x2 = x.clone()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        res1 = layer(x, r, w, W, sW, W2, sW2, True)
+    with torch.cuda.graph(g2):
+        res2 = layer(x2, r, w, W, sW, W2, sW2, False)
+    for i in range(3):
+        x.copy_(torch.roll(x2, i + 1, 1) * 3)
+        x2.mul_(0.5)
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        for st in (s1, s2):
+            st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s1):
+            g1.replay()
+        with torch.cuda.stream(s2):
+            g2.replay()
+        torch.cuda.synchronize()
+        check_layer(x, r, w, W, sW, W2, sW2, res1)
+        check_layer(x2, r, w, W, sW, W2, sW2, res2)
+
+
+def test_two_streams_at_once():
+    ins = [layer_inputs(M, seed=70 + M) for M in (1, 64, 200, 16)]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    out = [[] for _ in ins]
+    for _ in range(5):
+        for k, (args, st) in enumerate(zip(ins, streams)):
+            with torch.cuda.stream(st):
+                out[k].append(layer(*args, True))
+    torch.cuda.synchronize()
+    for args, res in zip(ins, out):
+        check_layer(*args, res[0])
+        for other in res[1:]:
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+                       for a, b in zip(res[0], other))
+
+
+def test_stream_argument():
+    """What the call allocates belongs to the stream it is given."""
+    x, r, w, W, sW, W2, sW2 = layer_inputs(20, seed=80)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    h, q, s, _ = rn.rmsnorm_fwd_fp8(x, w, r=r, stream=st)
+    z = rn.rmsnorm_gemm_fp8(q, s, W, sW, stream=st)
+    qz, sz = rn.rmsnorm_quant_fp8(z, stream=st)
+    o = rn.rmsnorm_gemm_fp8(qz, sz, W2, sW2, stream=st)
+    st.synchronize()
+    check_layer(x, r, w, W, sW, W2, sW2, (h, q, s, z, qz, sz, o))
+
+
+def test_backward_takes_what_the_forward_returns():
+    """rstd and h of the 8-bit forward are those of the library's forward, so
+    its backward runs on them."""
+    x, r, w = (t.to(DEV) for t in data(300, 896, BF16, seed=90))
+    h, _, _, rstd = rn.rmsnorm_fwd_fp8(x, w, r=r)
+    h0, _, rstd0 = rn.rmsnorm_residual_fwd(x, r, w)
+    assert torch.equal(h, h0)
+    assert bool(((rstd - rstd0).abs() <= DELTA * rstd0).all())
+    dy = torch.randn(300, 896, device=DEV, dtype=F32).to(BF16)
+    dx, dw = rn.rmsnorm_residual_bwd(dy, None, h, w, rstd)
+    dx0, dw0 = rn.rmsnorm_residual_bwd(dy, None, h0, w, rstd0)
+    assert bool(((dx.float() - dx0.float()).abs() <= 2.0 ** -7 * dx0.float().abs() + 1e-4).all())
+    assert bool(((dw - dw0).abs() <= 1e-4 * (dw0.abs() + 1)).all())
+
+
+# ---------------------------------------------------------------- refusals
+def test_refusals_of_the_binding():
+    x, r, w, W, sW, W2, sW2 = layer_inputs(4, seed=95)
+    q, s = rn.rmsnorm_quant_fp8(x)
+    for call in (lambda: rn.rmsnorm_fwd_fp8(x, w, qdtype=torch.float16),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w.float()),
+                 lambda: rn.rmsnorm_fwd_fp8(x.t(), w),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w, r=r[:3]),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w, h=r),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w, scale=s[:, :6]),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w, q=q[:3]),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w, q=q, qdtype=E5M2),
+                 lambda: rn.rmsnorm_fwd_fp8(x, w.cpu()),
+                 lambda: rn.rmsnorm_quant_fp8(x, block_rows=64),
+                 lambda: rn.rmsnorm_quant_fp8(x.long()),
+                 lambda: rn.rmsnorm_gemm_fp8(q, s, W, sW.t().contiguous()),
+                 lambda: rn.rmsnorm_gemm_fp8(q, s, W, sW[:-1]),
+                 lambda: rn.rmsnorm_gemm_fp8(q, s.half(), W, sW),
+                 lambda: rn.rmsnorm_gemm_fp8(q, s, W, sW, out=x),
+                 lambda: rn.rmsnorm_gemm_fp8(x, s, W, sW),
+                 lambda: rn.rmsnorm_gemm_fp8(q, s, W, sW, out_dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            call()
+    odd = torch.zeros(4, 1001, device=DEV, dtype=torch.uint8).view(E4M3)
+    so = torch.ones(4, 8, device=DEV)
+    with pytest.raises(rn.RmsNormError) as e:      # rows that start at odd addresses
+        rn.rmsnorm_gemm_fp8(odd, so, odd, so[:1])
+    assert e.value.status == -5
+    with pytest.raises(rn.RmsNormError) as e:      # q over the residual
+        rn.rmsnorm_fwd_fp8(x, w, r=r, q=r.view(torch.uint8)[:, :896].view(E4M3))
+    assert e.value.status == -9
+
+
+@pytest.mark.parametrize("M", [8, 100, 700])
+def test_bounded_waits(M):
+    """A copy that never completes ends the kernel, is counted, and leaves
+    the context usable."""
+    qa, sa, qb, sb = pair(M, 300, 1024, seed=97)
+    good = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+    torch.cuda.synchronize()
+    assert rn.wait_timeouts(reset=True) == 0
+    try:
+        rn.set_stream_test_fault(16, 2000)
+        rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+        torch.cuda.synchronize()
+    finally:
+        rn.set_stream_test_fault(0, 0)
+    assert rn.wait_timeouts(reset=True) > 0
+    assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
