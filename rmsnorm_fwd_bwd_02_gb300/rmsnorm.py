@@ -427,58 +427,64 @@ FP8_MAX_K, FP8_MAX_ROWS = 1 << 24, 1 << 30
 GEMM_FP8_STATIC_WEIGHTS = 1
 
 
+# The 8-bit calls of a decode step run for a few microseconds on the GPU, so
+# their bindings are kept lean: one check a tensor, the current stream's handle
+# straight from torch (its stream object and context manager take 2 and 6 us
+# on a Grace core), and nothing allocated but the outputs.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _fp8_code(name, dtype):
-    if dtype not in FP8_TYPES:
+    code = FP8_TYPES.get(dtype)
+    if code is None:
         raise ValueError(f"{name} must be one of {sorted(map(str, FP8_TYPES))}, got {dtype}")
-    return FP8_TYPES[dtype]
+    return code
 
 
-def _one_device(**tensors):
-    """The device that every given tensor is on."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
-        raise ValueError(f"{', '.join(tensors)} must be on one CUDA device, got "
-                         f"{sorted(map(str, devs))}")
-    return devs.pop()
+def _elsewhere(name, t, stream):
+    """None when a call on t can run as it is: on the current device and,
+    stream being None, its current stream. Else the context to run it in, in
+    which the outputs that the binding allocates belong to that stream."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, {name} on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return None
 
 
-class _on:
-    """Runs a call on `device` and `stream` (its current stream when None):
-    what the binding allocates belongs to that stream."""
-
-    def __init__(self, device, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        if self.stream.device != device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {device}")
-        self.ctx = torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return self.stream
-
-    def __exit__(self, *a):
-        return self.ctx.__exit__(*a)
+def _ld(name, t, M, H, dtype, dev):
+    """Row stride (elements) of a [M, H] tensor of `dtype` on device `dev`
+    (an index) with unit column stride; H for one row."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (M, H):
+        raise ValueError(f"{name} must be of shape {(M, H)}, got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and H > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if M > 1 else H
 
 
-def _scales(name, t, rows, H, device):
-    """fp32 scales [rows, ceil(H / 128)], made when not given."""
-    shape = (rows, -(-H // FP8_GROUP))
-    if t is None:
-        return torch.empty(shape, device=device, dtype=torch.float32)
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
-    return t
+def _fp32(name, t, shape, dev):
+    """Checks contiguous fp32 `t` of `shape` on device `dev` (an index)."""
+    if t.get_device() != dev or t.dtype != torch.float32 or tuple(t.shape) != shape \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _fp8_rows(name, t, M, H, qdtype, device):
-    """An 8-bit [M, H] tensor and its row stride, made when not given with
-    rows that start at multiples of 16 bytes (as rmsnorm_gemm_fp8 reads them)."""
-    if t is None:
-        t = torch.empty(M, -(-H // 16) * 16, device=device, dtype=qdtype)[:, :H]
-    Mt, ld = _strided(name, t, H, qdtype)
-    if Mt != M:
-        raise ValueError(f"{name} must have {M} rows, got {Mt}")
-    return t, ld
+def _empty_fp8(M, H, qdtype, device):
+    """An 8-bit [M, H] tensor whose rows start at multiples of 16 bytes (as
+    rmsnorm_gemm_fp8 reads them)."""
+    if H % 16 == 0:
+        return torch.empty((M, H), device=device, dtype=qdtype)
+    return torch.empty((M, -(-H // 16) * 16), device=device, dtype=qdtype)[:, :H]
 
 
 def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-6,
@@ -488,33 +494,48 @@ def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-
     Returns (q, scale, rstd or None), with r (h, q, scale, rstd or None). q
     is [M, H] of qdtype (float8_e4m3fn or float8_e5m2), scale [M, ceil(H /
     128)]; q times its group's scale is the norm's output."""
+    ctx = _elsewhere("x", x, stream)
+    if ctx is not None:
+        with ctx:
+            return rmsnorm_fwd_fp8(x, w, r, q, scale, h, rstd, eps, qdtype, want_rstd)
     H = w.numel()
-    M, ldx = _strided("x", x, H)
-    code = _dtype_code(x)
-    _rows("w", w.view(-1), H, x.dtype)
-    dev = _one_device(x=x, w=w, r=r, q=q, scale=scale, h=h, rstd=rstd)
-    qcode = _fp8_code("qdtype", qdtype)
-    ldr = ldh = H
-    with _on(dev, stream) as s:
-        if r is not None:
-            Mr, ldr = _strided("r", r, H, x.dtype)
-            if h is None:
-                h = torch.empty(M, H, device=dev, dtype=x.dtype)
-            Mh, ldh = _strided("h", h, H, x.dtype)
-            if Mr != M or Mh != M:
-                raise ValueError(f"r and h must have {M} rows")
-        elif h is not None:
-            raise ValueError("h is the residual variant's output: pass r too")
-        q, ldq = _fp8_rows("q", q, M, H, qdtype, dev)
-        scale = _scales("scale", scale, M, H, dev)
-        if rstd is None and want_rstd:
-            rstd = torch.empty(M, device=dev, dtype=torch.float32)
-        if rstd is not None and (rstd.dtype != torch.float32 or rstd.numel() != M
-                                 or not rstd.is_contiguous()):
-            raise ValueError(f"rstd must be a contiguous float32 tensor of {M} entries")
-        _check(lib().rmsnorm_fwd_fp8(
-            _ptr(x), ldx, _ptr(r), ldr, _ptr(w), _ptr(q), ldq, _ptr(scale), _ptr(h), ldh,
-            _ptr(rstd), M, H, float(eps), code, qcode, _stream(s)), "rmsnorm_fwd_fp8")
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [M, {H}]")
+    M, dev, device, dtype = x.shape[0], x.get_device(), x.device, x.dtype
+    code, qcode = _dtype_code(x), _fp8_code("qdtype", qdtype)
+    ldx = _ld("x", x, M, H, dtype, dev)
+    if w.get_device() != dev or w.dtype != dtype or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {dtype} tensor on cuda:{dev}")
+    ldr = ldh = ldq = H
+    rp = hp = rsp = None
+    if r is not None:
+        ldr = _ld("r", r, M, H, dtype, dev)
+        if h is None:
+            h = torch.empty((M, H), device=device, dtype=dtype)
+        else:
+            ldh = _ld("h", h, M, H, dtype, dev)
+        rp, hp = r.data_ptr(), h.data_ptr()
+    elif h is not None:
+        raise ValueError("h is the residual variant's output: pass r too")
+    if q is None:
+        q = _empty_fp8(M, H, qdtype, device)
+        ldq = q.stride(0)
+    else:
+        ldq = _ld("q", q, M, H, qdtype, dev)
+    shape = (M, -(-H // FP8_GROUP))
+    if scale is None:
+        scale = torch.empty(shape, device=device, dtype=torch.float32)
+    else:
+        _fp32("scale", scale, shape, dev)
+    if rstd is not None:
+        _fp32("rstd", rstd, (M,), dev)
+    elif want_rstd:
+        rstd = torch.empty((M,), device=device, dtype=torch.float32)
+    if rstd is not None:
+        rsp = rstd.data_ptr()
+    _check(lib().rmsnorm_fwd_fp8(x.data_ptr(), ldx, rp, ldr, w.data_ptr(), q.data_ptr(), ldq,
+                                 scale.data_ptr(), hp, ldh, rsp, M, H, eps, code, qcode,
+                                 _raw_stream(dev)), "rmsnorm_fwd_fp8")
     return (q, scale, rstd) if r is None else (h, q, scale, rstd)
 
 
@@ -523,21 +544,31 @@ def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e
     """x [M, H] (any row stride) rounded to 8 bits: (q, scale), with one fp32
     scale for each 128 columns of a row (block_rows=1, activations) or each
     block of 128 x 128 (block_rows=128, weights); see rmsnorm.h."""
+    ctx = _elsewhere("x", x, stream)
+    if ctx is not None:
+        with ctx:
+            return rmsnorm_quant_fp8(x, q, scale, block_rows, qdtype)
     if x.dim() != 2:
         raise ValueError("x must be 2-D [M, H]")
-    H = x.shape[1]
-    M, ldx = _strided("x", x, H)
-    code = _dtype_code(x)
-    qcode = _fp8_code("qdtype", qdtype)
-    if block_rows not in (1, FP8_GROUP):
+    M, H = x.shape
+    dev, device = x.get_device(), x.device
+    code, qcode = _dtype_code(x), _fp8_code("qdtype", qdtype)
+    ldx = _ld("x", x, M, H, x.dtype, dev)
+    if block_rows != 1 and block_rows != FP8_GROUP:
         raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
-    dev = _one_device(x=x, q=q, scale=scale)
-    with _on(dev, stream) as s:
-        q, ldq = _fp8_rows("q", q, M, H, qdtype, dev)
-        scale = _scales("scale", scale, -(-M // block_rows), H, dev)
-        _check(lib().rmsnorm_quant_fp8(_ptr(x), ldx, _ptr(q), ldq, _ptr(scale), M, H,
-                                       int(block_rows), code, qcode, _stream(s)),
-               "rmsnorm_quant_fp8")
+    if q is None:
+        q = _empty_fp8(M, H, qdtype, device)
+        ldq = q.stride(0)
+    else:
+        ldq = _ld("q", q, M, H, qdtype, dev)
+    shape = (-(-M // block_rows), -(-H // FP8_GROUP))
+    if scale is None:
+        scale = torch.empty(shape, device=device, dtype=torch.float32)
+    else:
+        _fp32("scale", scale, shape, dev)
+    _check(lib().rmsnorm_quant_fp8(x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), M, H,
+                                   block_rows, code, qcode, _raw_stream(dev)),
+           "rmsnorm_quant_fp8")
     return q, scale
 
 
@@ -549,26 +580,31 @@ def rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16,
     multiples of 16 bytes). out: any row stride; out_dtype float32, bfloat16
     or float16 when it is not given. static_weights: nothing in flight on the
     stream writes b or b_scale (see RMSNORM_GEMM_FP8_STATIC_WEIGHTS)."""
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError(f"a [M, K] and b [N, K] must be 2-D with one K, got {tuple(a.shape)} "
-                         f"and {tuple(b.shape)}")
-    K, N = a.shape[1], b.shape[0]
-    acode, bcode = _fp8_code("a", a.dtype), _fp8_code("b", b.dtype)
-    M, lda = _strided("a", a, K)
-    _, ldb = _strided("b", b, K)
-    dev = _one_device(a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
-    _scales("a_scale", a_scale, M, K, dev)
-    _scales("b_scale", b_scale, -(-N // FP8_GROUP), K, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(M, N, device=dev, dtype=out_dtype)
-        Mo, ldo = _strided("out", out, N)
-        if Mo != M:
-            raise ValueError(f"out must have {M} rows, got {Mo}")
-        _check(lib().rmsnorm_gemm_fp8(
-            _ptr(a), lda, _ptr(a_scale), acode, _ptr(b), ldb, _ptr(b_scale), bcode, _ptr(out),
-            ldo, M, N, K, _dtype_code(out), GEMM_FP8_STATIC_WEIGHTS if static_weights else 0,
-            _stream(s)), "rmsnorm_gemm_fp8")
+    ctx = _elsewhere("a", a, stream)
+    if ctx is not None:
+        with ctx:
+            return rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError(f"a [M, K] and b [N, K] must be 2-D, got {tuple(a.shape)} and "
+                         f"{tuple(b.shape)}")
+    M, K = a.shape
+    N, dev, ta, tb = b.shape[0], a.get_device(), a.dtype, b.dtype
+    acode, bcode = _fp8_code("a", ta), _fp8_code("b", tb)
+    lda, ldb = _ld("a", a, M, K, ta, dev), _ld("b", b, N, K, tb, dev)
+    G = -(-K // FP8_GROUP)
+    _fp32("a_scale", a_scale, (M, G), dev)
+    _fp32("b_scale", b_scale, (-(-N // FP8_GROUP), G), dev)
+    ldo = N
+    if out is None:
+        if out_dtype not in DTYPES:
+            raise ValueError(f"unsupported dtype {out_dtype}")
+        out = torch.empty((M, N), device=a.device, dtype=out_dtype)
+    else:
+        ldo = _ld("out", out, M, N, out.dtype, dev)
+    _check(lib().rmsnorm_gemm_fp8(
+        a.data_ptr(), lda, a_scale.data_ptr(), acode, b.data_ptr(), ldb, b_scale.data_ptr(), bcode,
+        out.data_ptr(), ldo, M, N, K, _dtype_code(out),
+        GEMM_FP8_STATIC_WEIGHTS if static_weights else 0, _raw_stream(dev)), "rmsnorm_gemm_fp8")
     return out
 
 
