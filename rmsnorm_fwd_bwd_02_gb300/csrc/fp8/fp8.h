@@ -42,18 +42,21 @@ struct Fp8BlocksParams {
     int64_t ldx, ldq;
 };
 
-// The instantiations of one element type. Widths: [0] the widest pack (32
-// bytes), [1] 16 bytes, [2] one element; the host picks the widest that the
-// alignment of every row allows.
+// One shape of the row kernel: its instantiations for x alone, the norm, and
+// the norm of x + r.
 struct Fp8RowKernel {
-    const void *fn[3];   // [0] x alone, [1] the norm, [2] the norm of x + r
+    const void *fn[3];
     int E;               // elements a pack
     int V;               // packs a lane
-    int G;               // rows a group of lanes takes at a time
     int lanes;           // lanes a row (rows share a warp); 0: a whole CTA a row
     int max_threads;
+    int64_t max_cols() const { return (int64_t)E * V * (lanes ? lanes : max_threads); }
 };
 
+// The shapes of one element type: [0..2] 32-byte packs, rows that share a
+// warp; [3] 32-byte packs, a CTA a row, as many lanes as the row has packs
+// (few rows); [4], [5] the same with more packs a lane (many rows); [6]
+// 16-byte packs; [7] loose packs. Blocks: 32-byte, 16-byte, loose packs.
 constexpr int kFp8RowShapes = 8;
 struct Fp8RowSet {
     Fp8RowKernel k[kFp8RowShapes];

@@ -25,18 +25,21 @@ const Fp8RowSet &fp8_set(int dtype)
                                  : (dtype == RMSNORM_F16 ? fp8_rows_f16 : fp8_rows_f32);
 }
 
-// Whether rows of packs of E elements (es bytes each; one byte in q) start
-// aligned to the pack, up to 16 bytes for what is read through the cached
-// path, in every tensor.
-bool packs_fit(int E, size_t es, int64_t H, const void *x, int64_t ldx, const void *r, int64_t ldr,
-               const void *w, const void *q, int64_t ldq, const void *h, int64_t ldh)
+// The width of pack that the alignment of every row allows: 0 for `E0`
+// elements, 1 for `E1` (es bytes an element, one in q; w and 32-byte packs
+// are also read 16 bytes at a time), else 2, elements one at a time.
+int pack_width(int E0, int E1, size_t es, int64_t H, const void *x, int64_t ldx, const void *r,
+               int64_t ldr, const void *w, const void *q, int64_t ldq, const void *h, int64_t ldh)
 {
-    const size_t a = (size_t)E * es;
-    if (E == 1)
-        return true;
-    return H % E == 0 && aligned(x, a) && aligned(r, a) && aligned(h, a) && aligned(w, 16) &&
-           aligned(q, (size_t)E) && strides_multiple(a, es, {ldx, ldr, ldh}) &&
-           strides_multiple((size_t)E, 1, {ldq});
+    const int widths[2] = {E0, E1};
+    for (int i = 0; i < 2; ++i) {
+        const size_t E = (size_t)widths[i], a = E * es;
+        if (H % widths[i] == 0 && aligned(x, a) && aligned(r, a) && aligned(h, a) &&
+            aligned(w, 16) && aligned(q, E) && strides_multiple(a, es, {ldx, ldr, ldh}) &&
+            strides_multiple(E, 1, {ldq}))
+            return i;
+    }
+    return 2;
 }
 
 cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void *arg)
@@ -54,43 +57,40 @@ cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-// Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: the widest
-// packs that every row's alignment allows; of those, rows that share a warp
-// where they are short enough, else a CTA a row.
-const Fp8RowKernel &pick_fp8_rows(const Fp8RowSet &set, int wide, int mode, int64_t M, int64_t H,
-                                  int sms)
+// Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: rows that
+// share a warp where they are short enough (at 524288 x 128 37 us, where a
+// warp a row would leave three quarters of its lanes idle); a lane a pack
+// while the rows do not fill the SMs (latency: 1.75 us at 1 x 896); else two
+// packs a lane, in CTAs of up to 256 threads (80 registers a thread), or of
+// up to 512 for rows that need more lanes.
+const Fp8RowKernel &pick_fp8_rows(const Fp8RowSet &set, int width, int64_t M, int64_t H, int sms)
 {
-    if (wide == 2)
-        return set.k[7];
-    if (wide == 1)
-        return set.k[6];
+    if (width > 0)
+        return set.k[5 + width];
     for (int i = 0; i < 3; ++i)
-        if (H <= (int64_t)set.k[i].lanes * set.k[i].V * set.k[i].E)
+        if (H <= set.k[i].max_cols())
             return set.k[i];
     if (M <= 2 * (int64_t)sms)
         return set.k[3];
-    return mode == 2 ? set.k[4] : set.k[5];
+    return H <= set.k[4].max_cols() ? set.k[4] : set.k[5];
 }
 
 int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream)
 {
     Fp8RowsParams p = prm;
     const Fp8RowSet &set = fp8_set(dtype);
-    const size_t es = elem_size(dtype);
     int dev, sms, bps, st;
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
         return st;
-    int wide = 0;
-    while (!packs_fit(set.k[wide == 0 ? 0 : 5 + wide].E, es, p.H, p.x, p.ldx, p.r, p.ldr, p.w, p.q,
-                      p.ldq, p.h, p.ldh))
-        ++wide;
-    const int64_t Hw = std::min<int64_t>(p.H, kFp8Window);      // widest window
+    const int width = pack_width(set.k[0].E, set.k[6].E, elem_size(dtype), p.H, p.x, p.ldx, p.r,
+                                 p.ldr, p.w, p.q, p.ldq, p.h, p.ldh);
+    const int64_t Hw = std::min<int64_t>(p.H, kFp8Window);      // widest window of columns
     const int windows = (int)((p.H + kFp8Window - 1) / kFp8Window);
-    const Fp8RowKernel &k = pick_fp8_rows(set, wide, mode, p.M * windows, Hw, sms);
+    const Fp8RowKernel &k = pick_fp8_rows(set, width, p.M * windows, Hw, sms);
     int threads = k.max_threads;
-    int64_t tile = k.G;
+    int64_t tile = 1;
     if (k.lanes) {
-        tile *= threads / k.lanes;
+        tile = threads / k.lanes;
     } else {
         const int64_t lanes = ((Hw + k.E - 1) / k.E + k.V - 1) / k.V;
         threads = (int)((lanes + 31) / 32 * 32);
@@ -111,13 +111,11 @@ int blocks_impl(const Fp8RowsParams &r, int dtype, cudaStream_t stream)
 {
     Fp8BlocksParams p = {r.x, r.q, r.scale, r.M, r.H, r.G, r.e5m2, r.ldx, r.ldq};
     const Fp8RowSet &set = fp8_set(dtype);
-    int wide = 0;
-    while (!packs_fit(set.blocks_E[wide], elem_size(dtype), p.H, p.x, p.ldx, nullptr, 0, nullptr, p.q,
-                      p.ldq, nullptr, 0))
-        ++wide;
+    const int width = pack_width(set.blocks_E[0], set.blocks_E[1], elem_size(dtype), p.H, p.x, p.ldx,
+                                 nullptr, 0, nullptr, p.q, p.ldq, nullptr, 0);
     const int64_t rb = (p.M + kFp8Group - 1) / kFp8Group;
     const cudaError_t e =
-        launch1(set.blocks[wide], dim3((unsigned)p.G, (unsigned)std::min<int64_t>(rb, 65535)),
+        launch1(set.blocks[width], dim3((unsigned)p.G, (unsigned)std::min<int64_t>(rb, 65535)),
                 256, stream, &p);
     if (e != cudaSuccess)
         return cuda_fail(e);

@@ -28,8 +28,18 @@
 // is read once. 32-byte packs put 16 (16-bit types) or 8 (fp32) elements in a
 // lane, so a group of 128 columns is 8 or 16 neighbouring lanes and its
 // maximum takes 3 or 4 shuffles; the q of a lane is one 16- or 8-byte store.
-// Single elements (rows that start at any address) are dealt so that a group
-// is four elements of each lane of one warp.
+// Rows that may start at any address ("loose" packs) put four neighbouring
+// elements in a lane, read one at a time and written as one word.
+//
+// What it took (GB300, bf16, dispatch as in fp8_api.cu): the reduction, the
+// group maxima and the conversion form one chain per row, so a CTA that
+// loads a row only when it has stored the one before leaves DRAM idle.
+// Asking for the next row before working on this one (AHEAD) takes the norm
+// at 32768 x 4096 from 72 to 65 us (two packs a lane, w read again from L1
+// for each row instead of held: 80 registers, six CTAs an SM; one pack a lane
+// takes 72 us, four 68). With the residual there are twice the loads in flight
+// for the same chain and the registers are worth more as occupancy: 90 us
+// without AHEAD at 16384 x 5120, 97 to 105 with it.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -42,8 +52,6 @@ namespace rmsk {
 constexpr int kFp8ModeQuant = 0, kFp8ModeNorm = 1, kFp8ModeResidual = 2;
 
 constexpr float kFp8AmaxMin = 0x1p-100f;
-
-__device__ __forceinline__ float fp8_largest(int e5m2) { return e5m2 ? 57344.f : 448.f; }
 
 // max(a, |b|) that keeps a NaN of either
 __device__ __forceinline__ float amax_nan(float a, float b)
@@ -59,11 +67,11 @@ struct Fp8Scale {
     float s, inv;
     __device__ __forceinline__ Fp8Scale(float amax, int e5m2)
     {
-        const float big = fp8_largest(e5m2);
-        s = fmaxf(amax, kFp8AmaxMin) / big;
+        s = fmaxf(amax, kFp8AmaxMin) * (e5m2 ? 1.f / 57344.f : 1.f / 448.f);
         if (!(amax < __int_as_float(0x7f800000)))
             s = __int_as_float(0x7fffffff);
-        inv = 1.f / s;
+        // s is a normal number with a normal reciprocal (or NaN)
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     }
 };
 
@@ -76,38 +84,128 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, int e5m2)
                 : __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
-// The E values of one pack, times inv, as E bytes at q.
-template <int E>
-__device__ __forceinline__ void fp8_store(void *q, const Vals<E> &y, float inv, int e5m2)
-{
-    if constexpr (E == 1) {
-        const uint32_t b = fp8_pair(y.v[0] * inv, 0.f, e5m2);
-        asm volatile("st.global.b8 [%0], %1;" ::"l"(q), "r"(b & 0xFFu) : "memory");
-    } else {
-        uint32_t u[E / 4];
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-            const float2 a = vmul(y.v[2 * i], splat<float2>(inv));
-            const float2 b = vmul(y.v[2 * i + 1], splat<float2>(inv));
-            u[i] = fp8_pair(a.x, a.y, e5m2) | (fp8_pair(b.x, b.y, e5m2) << 16);
-        }
-        if constexpr (E == 16)
-            st_row_v4(q, make_uint4(u[0], u[1], u[2], u[3]));
-        else if constexpr (E == 8)
-            asm volatile("st.global.v2.b32 [%0], {%1,%2};" ::"l"(q), "r"(u[0]), "r"(u[1])
-                         : "memory");
+// Four neighbouring elements of a row that may start at any address: read and
+// written one at a time, those at or past column H left out (zero).
+template <typename T> struct Loose {
+    float2 v[2];
+    static constexpr int E = 4;
+    __device__ __forceinline__ static float get(const T *p)
+    {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(ld_row_b32(p));
         else
+            return Half16<T>::wide1(ld_row_b16(p));
+    }
+    __device__ __forceinline__ static Loose load(const void *row, int c, int H)
+    {
+        const T *p = static_cast<const T *>(row) + c;
+        Loose l;
+        l.v[0].x = c < H ? get(p) : 0.f;
+        l.v[0].y = c + 1 < H ? get(p + 1) : 0.f;
+        l.v[1].x = c + 2 < H ? get(p + 2) : 0.f;
+        l.v[1].y = c + 3 < H ? get(p + 3) : 0.f;
+        return l;
+    }
+    __device__ __forceinline__ static Loose zero()
+    {
+        Loose l;
+        l.v[0] = l.v[1] = make_float2(0.f, 0.f);
+        return l;
+    }
+    __device__ __forceinline__ void store(void *row, int c, int H) const
+    {
+        T *p = static_cast<T *>(row) + c;
+        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (c + i < H) {
+                if constexpr (sizeof(T) == 4)
+                    st_row_b32(p + i, __float_as_uint(f[i]));
+                else
+                    st_row_b16(p + i, Half16<T>::narrow1(f[i]));
+            }
+        }
+    }
+    __device__ __forceinline__ void widen(Vals<4> &f) const
+    {
+        f.v[0] = v[0];
+        f.v[1] = v[1];
+    }
+    __device__ __forceinline__ static float round(float f)
+    {
+        if constexpr (sizeof(T) == 4)
+            return f;
+        else
+            return Half16<T>::wide1(Half16<T>::narrow1(f));
+    }
+    __device__ __forceinline__ static Loose narrow(const Vals<4> &f)
+    {
+        Loose l;
+        l.v[0] = make_float2(round(f.v[0].x), round(f.v[0].y));
+        l.v[1] = make_float2(round(f.v[1].x), round(f.v[1].y));
+        return l;
+    }
+};
+
+template <typename T, int E, bool LOOSE>
+using Fp8Pack = typename std::conditional<LOOSE, Loose<T>, Pack<T, E>>::type;
+
+// Pack vi of a row of H elements that is `row` rows of `ld` elements from base.
+template <typename T, int E, bool LOOSE>
+__device__ __forceinline__ Fp8Pack<T, E, LOOSE> fp8_load(const void *base, int64_t row, uint32_t ld,
+                                                         int vi, int H)
+{
+    if constexpr (LOOSE)
+        return Loose<T>::load(static_cast<const T *>(base) + row * ld, vi * 4, H);
+    else
+        return Pack<T, E>::load(base, row * (ld / E) + vi);
+}
+
+// The E values of pack vi of a row, times inv, as bytes at q + vi E. With
+// LOOSE those past H are left out, and the word goes out whole only where
+// it may (`words`: the row starts at a multiple of four bytes).
+template <int E, bool LOOSE>
+__device__ __forceinline__ void fp8_store(char *qrow, int vi, int H, bool words, const Vals<E> &y,
+                                          float inv, int e5m2)
+{
+    char *q = qrow + (int64_t)vi * E;
+    uint32_t u[E / 4];
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        const float2 a = vmul(y.v[2 * i], splat<float2>(inv));
+        const float2 b = vmul(y.v[2 * i + 1], splat<float2>(inv));
+        u[i] = fp8_pair(a.x, a.y, e5m2) | (fp8_pair(b.x, b.y, e5m2) << 16);
+    }
+    if constexpr (LOOSE) {
+        if (words && vi * 4 + 4 <= H) {
             st_row_b32(q, u[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (vi * 4 + i < H)
+                    asm volatile("st.global.b8 [%0], %1;" ::"l"(q + i), "r"((u[0] >> (8 * i)) & 0xFFu)
+                                 : "memory");
+        }
+    } else if constexpr (E == 16) {
+        st_row_v4(q, make_uint4(u[0], u[1], u[2], u[3]));
+    } else if constexpr (E == 8) {
+        asm volatile("st.global.v2.b32 [%0], {%1,%2};" ::"l"(q), "r"(u[0]), "r"(u[1]) : "memory");
+    } else {
+        st_row_b32(q, u[0]);
     }
 }
 
-// Largest magnitude of a pack's values, a NaN kept.
+// Largest magnitude of a pack's values, a NaN kept; two values a step (the
+// sm_100 family's maximum takes three operands).
 template <int E>
-__device__ __forceinline__ float pack_amax(const Vals<E> &y, float a)
+__device__ __forceinline__ float pack_amax(const Vals<E> &y)
 {
+    float a = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        a = amax_nan(a, y.get(e));
+    for (int e = 0; e < E / 2; ++e)
+        asm("max.NaN.f32 %0, %1, %2, %3;"
+            : "=f"(a)
+            : "f"(a), "f"(fabsf(y.v[e].x)), "f"(fabsf(y.v[e].y)));
     return a;
 }
 
@@ -121,10 +219,12 @@ __device__ __forceinline__ float lanes_amax(float a)
     return a;
 }
 
-// E: elements a pack; V: packs a lane; NG: rows a group of lanes takes at a
-// time; LR: lanes a row when several rows share a warp, or 0: the whole CTA
-// (whole warps, as many as the host picks) takes a row. Grid: persistent.
-template <typename T, int E, int V, int NG, int LR, int MAXT, int MINB, int MODE>
+// E: elements a pack; V: packs a lane; LR: lanes a row when several rows
+// share a warp, or 0: the whole CTA (whole warps, as many as the host picks)
+// takes a row; AHEAD: the next row's loads are issued before this one is
+// worked on; HOLD: w stays in registers; LOOSE: as above. Grid: persistent.
+template <typename T, int E, int V, int LR, int MAXT, int MINB, int MODE, bool AHEAD, bool HOLD,
+          bool LOOSE>
 __global__ void __launch_bounds__(MAXT, MINB)
 rms_fp8_rows(const Fp8RowsParams prm)
 {
@@ -138,159 +238,160 @@ rms_fp8_rows(const Fp8RowsParams prm)
         p.scale += c0 / kFp8Group;
         p.H = min(p.H - c0, kFp8Window);
     }
-    using P = Pack<T, E>;
+    using P = Fp8Pack<T, E, LOOSE>;
     using X = Vals<E>;
-    using F = typename X::F;
     constexpr bool NORM = MODE != kFp8ModeQuant, RES = MODE == kFp8ModeResidual;
-    constexpr int KG = E == 1 ? 4 : 1;              // a lane's packs in one group of columns
-    constexpr int LG = E == 1 ? 32 : kFp8Group / E; // lanes in one group of columns
-    static_assert(V % KG == 0 && (LR == 0 || (LR % LG == 0 && E > 1)), "groups are whole lanes");
-    __shared__ float red[2][32 * NG];
+    constexpr int LG = kFp8Group / E;               // lanes in one group of columns
+    static_assert(LG <= 32 && (LR == 0 || LR % LG == 0) && (!LOOSE || E == 4), "lanes of a group");
+    __shared__ float red[2][32];
 
     const int L = LR ? LR : (int)blockDim.x;
     const int lane = LR ? (int)threadIdx.x % LR : (int)threadIdx.x;
     const int sub = LR ? (int)threadIdx.x / LR : 0;
-    const int S = LR ? (int)blockDim.x / LR : 1;    // groups of lanes in the CTA
-    const int NV = p.H / E;                         // packs a row (E divides H)
+    const int S = LR ? (int)blockDim.x / LR : 1;    // rows of the CTA at a time
+    const int NV = (p.H + E - 1) / E;               // packs a row (E divides H unless LOOSE)
     const float fH = (float)p.H;
-    const uint32_t sx = (uint32_t)p.ldx / E, sr = (uint32_t)p.ldr / E, sh = (uint32_t)p.ldh / E;
-    auto index = [&](int k) {
-        if constexpr (E == 1)
-            return ((k >> 2) * L + (lane & ~31)) * 4 + (k & 3) * 32 + (lane & 31);
+    const uint32_t ldx = (uint32_t)p.ldx, ldr = (uint32_t)p.ldr, ldh = (uint32_t)p.ldh;
+    const bool words = LOOSE && ((uintptr_t)p.q % 4 == 0) && p.ldq % 4 == 0;
+
+    auto load = [&](const void *base, uint32_t ld, int64_t row, P (&to)[V]) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int vi = lane + k * L;
+            to[k] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : P::zero();
+        }
+    };
+    auto load_w = [&](int vi) {
+        if (vi >= NV)
+            return P::zero();
+        if constexpr (LOOSE)
+            return Loose<T>::load(p.w, vi * 4, p.H);
         else
-            return lane + k * L;
+            return P::load_cached(p.w, vi);
     };
 
     griddep_wait();
-    P wv[NORM && E > 1 ? V : 1];
-    if constexpr (NORM && E > 1) {
+    constexpr bool kHold = NORM && HOLD;
+    P wv[kHold ? V : 1];
+    if constexpr (kHold) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            wv[k] = index(k) < NV ? P::load_cached(p.w, index(k)) : P::zero();
+            wv[k] = load_w(lane + k * L);
     }
 
-    const int64_t tile = (int64_t)S * NG;
-    const int64_t ntiles = (p.M + tile - 1) / tile;
+    const int64_t ntiles = (p.M + S - 1) / S;
     int buf = 0;
+    P xn[AHEAD ? V : 1], rn[AHEAD && RES ? V : 1];
+    if constexpr (AHEAD) {
+        const int64_t row = (int64_t)blockIdx.x * S + sub;
+        load(p.x, ldx, row, xn);
+        if constexpr (RES)
+            load(p.r, ldr, row, rn);
+    }
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
-        const int64_t row0 = t * tile + (int64_t)sub * NG;
-        P xv[NG][V];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
+        const int64_t row = t * S + sub;
+        P xv[V], rv[RES ? V : 1];
+        if constexpr (AHEAD) {
+            // this row was asked for a tile ago; now the next one
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                const int vi = index(k);
-                xv[g][k] = row0 + g < p.M && vi < NV ? P::load(p.x, (row0 + g) * sx + vi) : P::zero();
+                xv[k] = xn[k];
+                if constexpr (RES)
+                    rv[k] = rn[k];
             }
+            const int64_t next = row + (int64_t)gridDim.x * S;
+            load(p.x, ldx, next, xn);
+            if constexpr (RES)
+                load(p.r, ldr, next, rn);
+        } else {
+            load(p.x, ldx, row, xv);
+            if constexpr (RES)
+                load(p.r, ldr, row, rv);
+        }
         if constexpr (RES) {
-            P rv[NG][V];
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int vi = index(k);
-                    rv[g][k] =
-                        row0 + g < p.M && vi < NV ? P::load(p.r, (row0 + g) * sr + vi) : P::zero();
-                }
             // the stored h is what the norm sees
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int k = 0; k < V; ++k) {
+                const int vi = lane + k * L;
+                X a, b;
+                xv[k].widen(a);
+                rv[k].widen(b);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int vi = index(k);
-                    X a, b;
-                    xv[g][k].widen(a);
-                    rv[g][k].widen(b);
-#pragma unroll
-                    for (int i = 0; i < X::N; ++i)
-                        a.v[i] = vadd(a.v[i], b.v[i]);
-                    xv[g][k] = P::narrow(a);
-                    if (row0 + g < p.M && vi < NV)
-                        xv[g][k].store(p.h, (row0 + g) * sh + vi);
+                for (int i = 0; i < X::N; ++i)
+                    a.v[i] = vadd(a.v[i], b.v[i]);
+                xv[k] = P::narrow(a);
+                if (row < p.M && vi < NV) {
+                    if constexpr (LOOSE)
+                        xv[k].store(static_cast<T *>(p.h) + row * ldh, vi * 4, p.H);
+                    else
+                        xv[k].store(p.h, row * (ldh / E) + vi);
                 }
+            }
         }
 
-        float rs[NG];
+        float rs = 1.f;
         if constexpr (NORM) {
-            float ss[NG];
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                F acc = splat<F>(0.f);
+            for (int k = 0; k < V; ++k) {
+                X a;
+                xv[k].widen(a);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    X a;
-                    xv[g][k].widen(a);
-#pragma unroll
-                    for (int i = 0; i < X::N; ++i)
-                        acc = vfma(a.v[i], a.v[i], acc);
-                }
-                ss[g] = group_allreduce<LR ? LR : 32>(hsum(acc));
+                for (int i = 0; i < X::N; ++i)
+                    acc = vfma(a.v[i], a.v[i], acc);
             }
+            float ss = group_allreduce<LR ? LR : 32>(hsum(acc));
             if constexpr (LR == 0) {                // the warps' sums, added in warp order
                 const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
                 if (nw > 1) {
-                    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-                            red[buf][warp * NG + g] = ss[g];
-                    }
+                    if ((threadIdx.x & 31) == 0)
+                        red[buf][warp] = ss;
                     __syncthreads();
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        ss[g] = 0.f;
-                        for (int q = 0; q < nw; ++q)
-                            ss[g] += red[buf][q * NG + g];
-                    }
+                    ss = 0.f;
+                    for (int q = 0; q < nw; ++q)
+                        ss += red[buf][q];
                     buf ^= 1;                       // read again only after the next barrier
                 }
             }
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                rs[g] = rsqrtf(ss[g] / fH + p.eps);
-                if (p.rstd != nullptr && lane == 0 && row0 + g < p.M)
-                    p.rstd[row0 + g] = rs[g];
-            }
+            rs = rsqrtf(ss / fH + p.eps);
+            if (p.rstd != nullptr && lane == 0 && row < p.M)
+                p.rstd[row] = rs;
         }
 
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int64_t row = row0 + g;
+        for (int k = 0; k < V; ++k) {
+            const int vi = lane + k * L;
+            X y;
+            xv[k].widen(y);
+            if constexpr (NORM) {
+                X w;
+                if constexpr (kHold)
+                    wv[k].widen(w);
+                else
+                    load_w(vi).widen(w);
 #pragma unroll
-            for (int k0 = 0; k0 < V; k0 += KG) {
-                X y[KG];
-                float a = 0.f;
-#pragma unroll
-                for (int j = 0; j < KG; ++j) {
-                    xv[g][k0 + j].widen(y[j]);
-                    if constexpr (NORM) {
-                        X w;
-                        if constexpr (E > 1)
-                            wv[k0 + j].widen(w);
-                        else if (index(k0 + j) < NV)
-                            P::load_cached(p.w, index(k0 + j)).widen(w);
-                        else
-                            w = X::zero();
-#pragma unroll
-                        for (int i = 0; i < X::N; ++i)
-                            y[j].v[i] = vmul(vmul(y[j].v[i], splat<F>(rs[g])), w.v[i]);
-                    }
-                    // columns past H do not count (a row of infinities times
-                    // the padding's zero would)
-                    if (index(k0 + j) < NV)
-                        a = pack_amax<E>(y[j], a);
-                }
-                a = lanes_amax<LG>(a);
-                const int v0 = index(k0);
-                if (row < p.M && v0 < NV) {
-                    const Fp8Scale sc(a, p.e5m2);
-                    if (lane % LG == 0)
-                        p.scale[row * p.G + (E == 1 ? v0 / kFp8Group : v0 / LG)] = sc.s;
-                    char *qr = static_cast<char *>(p.q) + row * p.ldq;
-#pragma unroll
-                    for (int j = 0; j < KG; ++j)
-                        if (index(k0 + j) < NV)
-                            fp8_store<E>(qr + (int64_t)index(k0 + j) * E, y[j], sc.inv, p.e5m2);
-                }
+                for (int i = 0; i < X::N; ++i)
+                    y.v[i] = vmul(vmul(y.v[i], splat<float2>(rs)), w.v[i]);
+            }
+            if constexpr (NORM && LOOSE) {
+                // columns past H do not count: with rs not finite their zeros
+                // would be NaN
+                const int c = vi * 4;
+                y.v[0].x = c < p.H ? y.v[0].x : 0.f;
+                y.v[0].y = c + 1 < p.H ? y.v[0].y : 0.f;
+                y.v[1].x = c + 2 < p.H ? y.v[1].x : 0.f;
+                y.v[1].y = c + 3 < p.H ? y.v[1].y : 0.f;
+            }
+            float a = pack_amax<E>(y);
+            if (NORM && vi >= NV)                   // nor do whole packs past H
+                a = 0.f;
+            a = lanes_amax<LG>(a);
+            if (row < p.M && vi < NV) {
+                const Fp8Scale sc(a, p.e5m2);
+                if (lane % LG == 0)
+                    p.scale[row * p.G + vi / LG] = sc.s;
+                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, words, y, sc.inv,
+                                    p.e5m2);
             }
         }
     }
@@ -302,44 +403,39 @@ rms_fp8_rows(const Fp8RowsParams prm)
 // CTA takes 256 / LG rows and all passes' loads are in flight at once.
 constexpr int kFp8BlockThreads = 256;
 
-template <typename T, int E>
+template <typename T, int E, bool LOOSE>
 __global__ void __launch_bounds__(kFp8BlockThreads)
 rms_fp8_blocks(const Fp8BlocksParams p)
 {
-    using P = Pack<T, E>;
+    using P = Fp8Pack<T, E, LOOSE>;
     using X = Vals<E>;
-    constexpr int KG = E == 1 ? 4 : 1;
-    constexpr int LG = E == 1 ? 32 : kFp8Group / E;
+    constexpr int LG = kFp8Group / E;
     constexpr int ROWS = kFp8BlockThreads / LG;     // rows a pass
     constexpr int NP = kFp8Group / ROWS;            // passes
     __shared__ float red[kFp8BlockThreads / 32];
 
     const int lane = threadIdx.x % LG, sub = threadIdx.x / LG;
-    const int NV = p.H / E;
-    const uint32_t sx = (uint32_t)p.ldx / E;
-    const int v0 = (int)blockIdx.x * (kFp8Group / E);
-    auto index = [&](int j) { return v0 + lane + j * 32; };
+    const int NV = (p.H + E - 1) / E;
+    const uint32_t ldx = (uint32_t)p.ldx;
+    const int vi = (int)blockIdx.x * LG + lane;
+    const bool words = LOOSE && ((uintptr_t)p.q % 4 == 0) && p.ldq % 4 == 0;
 
     griddep_wait();
     for (int64_t rb = blockIdx.y; rb * kFp8Group < p.M; rb += gridDim.y) {
         const int64_t row0 = rb * kFp8Group + sub;
-        P xv[NP][KG];
+        P xv[NP];
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int j = 0; j < KG; ++j) {
-                const int64_t row = row0 + i * ROWS;
-                xv[i][j] = row < p.M && index(j) < NV ? P::load(p.x, row * sx + index(j)) : P::zero();
-            }
+        for (int i = 0; i < NP; ++i) {
+            const int64_t row = row0 + i * ROWS;
+            xv[i] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(p.x, row, ldx, vi, p.H) : P::zero();
+        }
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int j = 0; j < KG; ++j) {
-                X y;
-                xv[i][j].widen(y);
-                a = pack_amax<E>(y, a);
-            }
+        for (int i = 0; i < NP; ++i) {
+            X y;
+            xv[i].widen(y);
+            a = amax_nan(a, pack_amax<E>(y));
+        }
         a = lanes_amax<32>(a);
         if ((threadIdx.x & 31) == 0)
             red[threadIdx.x / 32] = a;
@@ -352,25 +448,24 @@ rms_fp8_blocks(const Fp8BlocksParams p)
         if (threadIdx.x == 0)
             p.scale[rb * p.G + blockIdx.x] = sc.s;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int j = 0; j < KG; ++j) {
-                const int64_t row = row0 + i * ROWS;
-                X y;
-                xv[i][j].widen(y);
-                if (row < p.M && index(j) < NV)
-                    fp8_store<E>(static_cast<char *>(p.q) + row * p.ldq + (int64_t)index(j) * E, y,
-                                 sc.inv, p.e5m2);
-            }
+        for (int i = 0; i < NP; ++i) {
+            const int64_t row = row0 + i * ROWS;
+            X y;
+            xv[i].widen(y);
+            if (row < p.M && vi < NV)
+                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, words, y, sc.inv,
+                                    p.e5m2);
+        }
     }
     griddep_launch_dependents();
 }
 
-// fn of one shape for the three modes
-#define RMSK_FP8_ROWS(T, E, V, NG, LR, MAXT, MINB)                                          \
-    {{(const void *)&rms_fp8_rows<T, E, V, NG, LR, MAXT, MINB, kFp8ModeQuant>,              \
-      (const void *)&rms_fp8_rows<T, E, V, NG, LR, MAXT, MINB, kFp8ModeNorm>,               \
-      (const void *)&rms_fp8_rows<T, E, V, NG, LR, MAXT, MINB, kFp8ModeResidual>},          \
-     E, V, NG, LR, MAXT}
+// fn of one shape for the three modes; the residual form does not load ahead
+#define RMSK_FP8_ROWS(T, E, V, LR, MAXT, MINB, AHEAD, HOLD, LOOSE)                             \
+    {{(const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeQuant, AHEAD, HOLD, LOOSE>, \
+      (const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeNorm, AHEAD, HOLD, LOOSE>,  \
+      (const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeResidual, false, HOLD,      \
+                                  LOOSE>},                                                     \
+     E, V, LR, MAXT}
 
 } // namespace rmsk

@@ -4,12 +4,16 @@
 namespace rmsk {
 
 const Fp8RowSet fp8_rows_f16 = {
-    {RMSK_FP8_ROWS(f16, 16, 1, 2, 8, 256, 2), RMSK_FP8_ROWS(f16, 16, 1, 2, 16, 256, 2),
-     RMSK_FP8_ROWS(f16, 16, 1, 2, 32, 256, 2), RMSK_FP8_ROWS(f16, 16, 1, 1, 0, 1024, 1),
-     RMSK_FP8_ROWS(f16, 16, 2, 1, 0, 512, 2), RMSK_FP8_ROWS(f16, 16, 4, 2, 0, 256, 2),
-     RMSK_FP8_ROWS(f16, 8, 4, 1, 0, 512, 1), RMSK_FP8_ROWS(f16, 1, 16, 1, 0, 1024, 1)},
-    {(const void *)&rms_fp8_blocks<f16, 16>, (const void *)&rms_fp8_blocks<f16, 8>,
-     (const void *)&rms_fp8_blocks<f16, 1>},
-    {16, 8, 1}};
+    {RMSK_FP8_ROWS(f16, 16, 1, 8, 256, 4, true, true, false),
+     RMSK_FP8_ROWS(f16, 16, 1, 16, 256, 4, true, true, false),
+     RMSK_FP8_ROWS(f16, 16, 1, 32, 256, 4, true, true, false),
+     RMSK_FP8_ROWS(f16, 16, 1, 0, 1024, 1, false, true, false),
+     RMSK_FP8_ROWS(f16, 16, 2, 0, 256, 3, true, false, false),
+     RMSK_FP8_ROWS(f16, 16, 2, 0, 512, 1, true, false, false),
+     RMSK_FP8_ROWS(f16, 8, 2, 0, 1024, 1, true, false, false),
+     RMSK_FP8_ROWS(f16, 4, 4, 0, 1024, 1, false, false, true)},
+    {(const void *)&rms_fp8_blocks<f16, 16, false>, (const void *)&rms_fp8_blocks<f16, 8, false>,
+     (const void *)&rms_fp8_blocks<f16, 4, true>},
+    {16, 8, 4}};
 
 } // namespace rmsk
