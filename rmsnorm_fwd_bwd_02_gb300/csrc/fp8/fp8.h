@@ -42,10 +42,9 @@ struct Fp8BlocksParams {
     int64_t ldx, ldq;
 };
 
-// One shape of the row kernel: its instantiations for x alone, the norm, and
-// the norm of x + r.
+// One shape of the row kernel.
 struct Fp8RowKernel {
-    const void *fn[3];
+    const void *fn;
     int E;               // elements a pack
     int V;               // packs a lane
     int lanes;           // lanes a row (rows share a warp); 0: a whole CTA a row
@@ -53,13 +52,13 @@ struct Fp8RowKernel {
     int64_t max_cols() const { return (int64_t)E * V * (lanes ? lanes : max_threads); }
 };
 
-// The shapes of one element type: [0..2] 32-byte packs, rows that share a
-// warp; [3] 32-byte packs, a CTA a row, as many lanes as the row has packs
-// (few rows); [4], [5] the same with more packs a lane (many rows); [6]
-// 16-byte packs; [7] loose packs. Blocks: 32-byte, 16-byte, loose packs.
-constexpr int kFp8RowShapes = 8;
+// The shapes of one element type, for x alone, the norm, and the norm of
+// x + r: 32-byte packs with rows that share a warp [0..3], with a CTA a row
+// for few rows [4], for many rows, narrow [5] and wide [6]; 16-byte packs
+// [7]; loose packs [8]. Blocks: 32-byte, 16-byte, loose packs.
+constexpr int kFp8SubShapes = 4, kFp8RowShapes = 9;
 struct Fp8RowSet {
-    Fp8RowKernel k[kFp8RowShapes];
+    Fp8RowKernel k[3][kFp8RowShapes];
     const void *blocks[3];
     int blocks_E[3];
 };

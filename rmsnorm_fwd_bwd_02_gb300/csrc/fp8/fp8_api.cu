@@ -58,21 +58,22 @@ cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void
 }
 
 // Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: rows that
-// share a warp where they are short enough (at 524288 x 128 37 us, where a
-// warp a row would leave three quarters of its lanes idle); a lane a pack
-// while the rows do not fill the SMs (latency: 1.75 us at 1 x 896); else two
-// packs a lane, in CTAs of up to 256 threads (80 registers a thread), or of
-// up to 512 for rows that need more lanes.
-const Fp8RowKernel &pick_fp8_rows(const Fp8RowSet &set, int width, int64_t M, int64_t H, int sms)
+// share a warp where they are short enough; a lane a pack while the rows do
+// not fill the SMs (latency); else more packs a lane. Measured (GB300, bf16,
+// the norm): at 524288 x 128 eight lanes a row take 37 us; at 262144 x 896 a
+// warp a row takes 117 us, a CTA of two warps 141; at 32768 x 4096 two packs
+// a lane take 65 us, one 72; at 16384 x 8192 four take 67 us, two 70 to 73.
+const Fp8RowKernel &pick_fp8_rows(const Fp8RowKernel *k, int width, int64_t M, int64_t H, int sms)
 {
     if (width > 0)
-        return set.k[5 + width];
-    for (int i = 0; i < 3; ++i)
-        if (H <= set.k[i].max_cols())
-            return set.k[i];
-    if (M <= 2 * (int64_t)sms)
-        return set.k[3];
-    return H <= set.k[4].max_cols() ? set.k[4] : set.k[5];
+        return k[6 + width];
+    const bool few = M <= 2 * (int64_t)sms;
+    for (int i = 0; i < kFp8SubShapes - (few ? 1 : 0); ++i)
+        if (H <= k[i].max_cols())
+            return k[i];
+    if (few)
+        return k[4];
+    return H <= k[5].max_cols() ? k[5] : k[6];
 }
 
 int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream)
@@ -82,11 +83,12 @@ int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream
     int dev, sms, bps, st;
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
         return st;
-    const int width = pack_width(set.k[0].E, set.k[6].E, elem_size(dtype), p.H, p.x, p.ldx, p.r,
+    const Fp8RowKernel *shapes = set.k[mode];
+    const int width = pack_width(shapes[0].E, shapes[7].E, elem_size(dtype), p.H, p.x, p.ldx, p.r,
                                  p.ldr, p.w, p.q, p.ldq, p.h, p.ldh);
     const int64_t Hw = std::min<int64_t>(p.H, kFp8Window);      // widest window of columns
     const int windows = (int)((p.H + kFp8Window - 1) / kFp8Window);
-    const Fp8RowKernel &k = pick_fp8_rows(set, width, p.M * windows, Hw, sms);
+    const Fp8RowKernel &k = pick_fp8_rows(shapes, width, p.M * windows, Hw, sms);
     int threads = k.max_threads;
     int64_t tile = 1;
     if (k.lanes) {
@@ -95,11 +97,11 @@ int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream
         const int64_t lanes = ((Hw + k.E - 1) / k.E + k.V - 1) / k.V;
         threads = (int)((lanes + 31) / 32 * 32);
     }
-    if ((st = blocks_per_sm(k.fn[mode], threads, dev, &bps)))
+    if ((st = blocks_per_sm(k.fn, threads, dev, &bps)))
         return st;
     const int64_t tiles = (p.M + tile - 1) / tile;
     const int64_t cap = std::max<int64_t>((int64_t)bps * sms / windows, 1);
-    const cudaError_t e = launch1(k.fn[mode], dim3((unsigned)std::min(tiles, cap), (unsigned)windows),
+    const cudaError_t e = launch1(k.fn, dim3((unsigned)std::min(tiles, cap), (unsigned)windows),
                                   threads, stream, &p);
     if (e != cudaSuccess)
         return cuda_fail(e);

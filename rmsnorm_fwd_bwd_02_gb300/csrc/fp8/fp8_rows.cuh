@@ -28,8 +28,8 @@
 // is read once. 32-byte packs put 16 (16-bit types) or 8 (fp32) elements in a
 // lane, so a group of 128 columns is 8 or 16 neighbouring lanes and its
 // maximum takes 3 or 4 shuffles; the q of a lane is one 16- or 8-byte store.
-// Rows that may start at any address ("loose" packs) put four neighbouring
-// elements in a lane, read one at a time and written as one word.
+// Rows that may start at any address ("loose" packs, 16 bytes) are read as
+// the aligned 16-byte words that hold them and shifted into place.
 //
 // What it took (GB300, bf16, dispatch as in fp8_api.cu): the reduction, the
 // group maxima and the conversion form one chain per row, so a CTA that
@@ -84,88 +84,133 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, int e5m2)
                 : __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
-// Four neighbouring elements of a row that may start at any address: read and
-// written one at a time, those at or past column H left out (zero).
-template <typename T> struct Loose {
-    float2 v[2];
-    static constexpr int E = 4;
-    __device__ __forceinline__ static float get(const T *p)
+// A 16-byte pack of a row that may start at any address, as it is read: the
+// aligned 16-byte words that hold it (the second only where the pack reaches
+// into it, so no word without a byte of the row is touched) and how far into
+// the first it starts. The words go through L1, where a neighbour's first is
+// this lane's second.
+template <typename T> struct LooseRaw {
+    static constexpr int E = 16 / (int)sizeof(T);
+    uint4 a, b;
+    int m, n;                                       // bytes: its start in a, its length
+    __device__ __forceinline__ static LooseRaw zero()
     {
-        if constexpr (sizeof(T) == 4)
-            return __uint_as_float(ld_row_b32(p));
-        else
-            return Half16<T>::wide1(ld_row_b16(p));
+        LooseRaw r;
+        r.a = r.b = make_uint4(0, 0, 0, 0);
+        r.m = r.n = 0;
+        return r;
     }
-    __device__ __forceinline__ static Loose load(const void *row, int c, int H)
+    __device__ __forceinline__ static uint4 ld(const void *p)
     {
-        const T *p = static_cast<const T *>(row) + c;
-        Loose l;
-        l.v[0].x = c < H ? get(p) : 0.f;
-        l.v[0].y = c + 1 < H ? get(p + 1) : 0.f;
-        l.v[1].x = c + 2 < H ? get(p + 2) : 0.f;
-        l.v[1].y = c + 3 < H ? get(p + 3) : 0.f;
-        return l;
+        uint4 v;
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+        return v;
     }
-    __device__ __forceinline__ static Loose zero()
+    // elements c .. c + E - 1 of a row of H (c < H)
+    __device__ __forceinline__ static LooseRaw load(const void *row, int c, int H)
     {
-        Loose l;
-        l.v[0] = l.v[1] = make_float2(0.f, 0.f);
-        return l;
+        const char *p = static_cast<const char *>(row) + (int64_t)c * (int)sizeof(T);
+        LooseRaw r;
+        r.m = (int)((uintptr_t)p & 15);
+        r.n = min(E, H - c) * (int)sizeof(T);
+        r.a = ld(p - r.m);
+        r.b = r.m + r.n > 16 ? ld(p - r.m + 16) : make_uint4(0, 0, 0, 0);
+        return r;
     }
-    __device__ __forceinline__ void store(void *row, int c, int H) const
+    // the pack, zero past the row's end
+    __device__ __forceinline__ uint4 words() const
     {
-        T *p = static_cast<T *>(row) + c;
-        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (m & 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (c + i < H) {
-                if constexpr (sizeof(T) == 4)
-                    st_row_b32(p + i, __float_as_uint(f[i]));
-                else
-                    st_row_b16(p + i, Half16<T>::narrow1(f[i]));
+            for (int i = 0; i < 6; ++i)
+                w[i] = w[i + 2];
+        }
+        if (m & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                w[i] = w[i + 1];
+        }
+        if constexpr (sizeof(T) == 2) {
+            if (m & 2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = __funnelshift_r(w[i], w[i + 1], 16);
             }
         }
-    }
-    __device__ __forceinline__ void widen(Vals<4> &f) const
-    {
-        f.v[0] = v[0];
-        f.v[1] = v[1];
-    }
-    __device__ __forceinline__ static float round(float f)
-    {
-        if constexpr (sizeof(T) == 4)
-            return f;
-        else
-            return Half16<T>::wide1(Half16<T>::narrow1(f));
-    }
-    __device__ __forceinline__ static Loose narrow(const Vals<4> &f)
-    {
-        Loose l;
-        l.v[0] = make_float2(round(f.v[0].x), round(f.v[0].y));
-        l.v[1] = make_float2(round(f.v[1].x), round(f.v[1].y));
-        return l;
+        if (n < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n <= 4 * i)
+                    w[i] = 0;
+                else if (n < 4 * i + 4)
+                    w[i] &= 0xFFFFu;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
-template <typename T, int E, bool LOOSE>
-using Fp8Pack = typename std::conditional<LOOSE, Loose<T>, Pack<T, E>>::type;
+// The first n bytes of a 16-byte pack to p, aligned to its element.
+template <typename T> __device__ __forceinline__ void store_loose(void *p, uint4 u, int n)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    char *q = static_cast<char *>(p);
+    if (sizeof(T) == 4 || n < 16 || ((uintptr_t)p & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (n >= 4 * i + 4 && (sizeof(T) == 4 || ((uintptr_t)p & 3) == 0)) {
+                st_row_b32(q + 4 * i, w[i]);
+            } else if (sizeof(T) == 2) {
+                if (n >= 4 * i + 2)
+                    st_row_b16(q + 4 * i, (uint16_t)(w[i] & 0xFFFFu));
+                if (n >= 4 * i + 4)
+                    st_row_b16(q + 4 * i + 2, (uint16_t)(w[i] >> 16));
+            }
+        }
+    } else {                                        // whole, two bytes past a word
+        st_row_b16(q, (uint16_t)(w[0] & 0xFFFFu));
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            st_row_b32(q + 4 * i + 2, __funnelshift_r(w[i], w[i + 1], 16));
+        st_row_b16(q + 14, (uint16_t)(w[3] >> 16));
+    }
+}
 
-// Pack vi of a row of H elements that is `row` rows of `ld` elements from base.
+// What a load leaves in registers, and its pack.
 template <typename T, int E, bool LOOSE>
-__device__ __forceinline__ Fp8Pack<T, E, LOOSE> fp8_load(const void *base, int64_t row, uint32_t ld,
-                                                         int vi, int H)
+using Fp8Raw = typename std::conditional<LOOSE, LooseRaw<T>, Pack<T, E>>::type;
+
+template <typename T, int E, typename R>
+__device__ __forceinline__ Pack<T, E> fp8_pack(const R &r)
+{
+    if constexpr (std::is_same<R, Pack<T, E>>::value) {
+        return r;
+    } else {
+        Pack<T, E> p;
+        p.u = r.words();
+        return p;
+    }
+}
+
+// Pack vi of the row that is `row` rows of `ld` elements from base.
+template <typename T, int E, bool LOOSE>
+__device__ __forceinline__ Fp8Raw<T, E, LOOSE> fp8_load(const void *base, int64_t row, uint32_t ld,
+                                                        int vi, int H)
 {
     if constexpr (LOOSE)
-        return Loose<T>::load(static_cast<const T *>(base) + row * ld, vi * 4, H);
+        return LooseRaw<T>::load(static_cast<const T *>(base) + row * ld, vi * E, H);
     else
         return Pack<T, E>::load(base, row * (ld / E) + vi);
 }
 
-// The E values of pack vi of a row, times inv, as bytes at q + vi E. With
-// LOOSE those past H are left out, and the word goes out whole only where
-// it may (`words`: the row starts at a multiple of four bytes).
+// The E values of pack vi of a row, times inv, as bytes at qrow + vi E. With
+// LOOSE those past H are left out, and the bytes go out as one word only
+// where they may (`whole`: the row starts at a multiple of E bytes).
 template <int E, bool LOOSE>
-__device__ __forceinline__ void fp8_store(char *qrow, int vi, int H, bool words, const Vals<E> &y,
+__device__ __forceinline__ void fp8_store(char *qrow, int vi, int H, bool whole, const Vals<E> &y,
                                           float inv, int e5m2)
 {
     char *q = qrow + (int64_t)vi * E;
@@ -176,16 +221,13 @@ __device__ __forceinline__ void fp8_store(char *qrow, int vi, int H, bool words,
         const float2 b = vmul(y.v[2 * i + 1], splat<float2>(inv));
         u[i] = fp8_pair(a.x, a.y, e5m2) | (fp8_pair(b.x, b.y, e5m2) << 16);
     }
-    if constexpr (LOOSE) {
-        if (words && vi * 4 + 4 <= H) {
-            st_row_b32(q, u[0]);
-        } else {
+    if (LOOSE && !(whole && vi * E + E <= H)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (vi * 4 + i < H)
-                    asm volatile("st.global.b8 [%0], %1;" ::"l"(q + i), "r"((u[0] >> (8 * i)) & 0xFFu)
-                                 : "memory");
-        }
+        for (int i = 0; i < E; ++i)
+            if (vi * E + i < H)
+                asm volatile("st.global.b8 [%0], %1;" ::"l"(q + i),
+                             "r"((u[i / 4] >> (8 * (i % 4))) & 0xFFu)
+                             : "memory");
     } else if constexpr (E == 16) {
         st_row_v4(q, make_uint4(u[0], u[1], u[2], u[3]));
     } else if constexpr (E == 8) {
@@ -238,11 +280,13 @@ rms_fp8_rows(const Fp8RowsParams prm)
         p.scale += c0 / kFp8Group;
         p.H = min(p.H - c0, kFp8Window);
     }
-    using P = Fp8Pack<T, E, LOOSE>;
+    using P = Pack<T, E>;
+    using R = Fp8Raw<T, E, LOOSE>;
     using X = Vals<E>;
     constexpr bool NORM = MODE != kFp8ModeQuant, RES = MODE == kFp8ModeResidual;
     constexpr int LG = kFp8Group / E;               // lanes in one group of columns
-    static_assert(LG <= 32 && (LR == 0 || LR % LG == 0) && (!LOOSE || E == 4), "lanes of a group");
+    static_assert(LG <= 32 && (LR == 0 || LR % LG == 0), "lanes of a group");
+    static_assert(!LOOSE || E * sizeof(T) == 16, "loose packs are 16 bytes");
     __shared__ float red[2][32];
 
     const int L = LR ? LR : (int)blockDim.x;
@@ -252,20 +296,20 @@ rms_fp8_rows(const Fp8RowsParams prm)
     const int NV = (p.H + E - 1) / E;               // packs a row (E divides H unless LOOSE)
     const float fH = (float)p.H;
     const uint32_t ldx = (uint32_t)p.ldx, ldr = (uint32_t)p.ldr, ldh = (uint32_t)p.ldh;
-    const bool words = LOOSE && ((uintptr_t)p.q % 4 == 0) && p.ldq % 4 == 0;
+    const bool whole = LOOSE && ((uintptr_t)p.q % E == 0) && p.ldq % E == 0;
 
-    auto load = [&](const void *base, uint32_t ld, int64_t row, P (&to)[V]) {
+    auto load = [&](const void *base, uint32_t ld, int64_t row, R (&to)[V]) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int vi = lane + k * L;
-            to[k] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : P::zero();
+            to[k] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : R::zero();
         }
     };
     auto load_w = [&](int vi) {
         if (vi >= NV)
             return P::zero();
         if constexpr (LOOSE)
-            return Loose<T>::load(p.w, vi * 4, p.H);
+            return fp8_pack<T, E>(LooseRaw<T>::load(p.w, vi * E, p.H));
         else
             return P::load_cached(p.w, vi);
     };
@@ -281,7 +325,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
 
     const int64_t ntiles = (p.M + S - 1) / S;
     int buf = 0;
-    P xn[AHEAD ? V : 1], rn[AHEAD && RES ? V : 1];
+    R xn[AHEAD ? V : 1], rn[AHEAD && RES ? V : 1];
     if constexpr (AHEAD) {
         const int64_t row = (int64_t)blockIdx.x * S + sub;
         load(p.x, ldx, row, xn);
@@ -290,12 +334,13 @@ rms_fp8_rows(const Fp8RowsParams prm)
     }
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
         const int64_t row = t * S + sub;
-        P xv[V], rv[RES ? V : 1];
+        P xv[V];
+        R rv[RES ? V : 1];
         if constexpr (AHEAD) {
             // this row was asked for a tile ago; now the next one
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                xv[k] = xn[k];
+                xv[k] = fp8_pack<T, E>(xn[k]);
                 if constexpr (RES)
                     rv[k] = rn[k];
             }
@@ -304,9 +349,13 @@ rms_fp8_rows(const Fp8RowsParams prm)
             if constexpr (RES)
                 load(p.r, ldr, next, rn);
         } else {
-            load(p.x, ldx, row, xv);
+            R xr[V];
+            load(p.x, ldx, row, xr);
             if constexpr (RES)
                 load(p.r, ldr, row, rv);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                xv[k] = fp8_pack<T, E>(xr[k]);
         }
         if constexpr (RES) {
             // the stored h is what the norm sees
@@ -315,14 +364,15 @@ rms_fp8_rows(const Fp8RowsParams prm)
                 const int vi = lane + k * L;
                 X a, b;
                 xv[k].widen(a);
-                rv[k].widen(b);
+                fp8_pack<T, E>(rv[k]).widen(b);
 #pragma unroll
                 for (int i = 0; i < X::N; ++i)
                     a.v[i] = vadd(a.v[i], b.v[i]);
                 xv[k] = P::narrow(a);
                 if (row < p.M && vi < NV) {
                     if constexpr (LOOSE)
-                        xv[k].store(static_cast<T *>(p.h) + row * ldh, vi * 4, p.H);
+                        store_loose<T>(static_cast<T *>(p.h) + row * ldh + vi * E, xv[k].u,
+                                       min(E, p.H - vi * E) * (int)sizeof(T));
                     else
                         xv[k].store(p.h, row * (ldh / E) + vi);
                 }
@@ -376,11 +426,15 @@ rms_fp8_rows(const Fp8RowsParams prm)
             if constexpr (NORM && LOOSE) {
                 // columns past H do not count: with rs not finite their zeros
                 // would be NaN
-                const int c = vi * 4;
-                y.v[0].x = c < p.H ? y.v[0].x : 0.f;
-                y.v[0].y = c + 1 < p.H ? y.v[0].y : 0.f;
-                y.v[1].x = c + 2 < p.H ? y.v[1].x : 0.f;
-                y.v[1].y = c + 3 < p.H ? y.v[1].y : 0.f;
+                if (vi * E + E > p.H) {
+#pragma unroll
+                    for (int i = 0; i < X::N; ++i) {
+                        if (vi * E + 2 * i >= p.H)
+                            y.v[i].x = 0.f;
+                        if (vi * E + 2 * i + 1 >= p.H)
+                            y.v[i].y = 0.f;
+                    }
+                }
             }
             float a = pack_amax<E>(y);
             if (NORM && vi >= NV)                   // nor do whole packs past H
@@ -390,7 +444,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
                 const Fp8Scale sc(a, p.e5m2);
                 if (lane % LG == 0)
                     p.scale[row * p.G + vi / LG] = sc.s;
-                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, words, y, sc.inv,
+                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, whole, y, sc.inv,
                                     p.e5m2);
             }
         }
@@ -407,7 +461,7 @@ template <typename T, int E, bool LOOSE>
 __global__ void __launch_bounds__(kFp8BlockThreads)
 rms_fp8_blocks(const Fp8BlocksParams p)
 {
-    using P = Fp8Pack<T, E, LOOSE>;
+    using R = Fp8Raw<T, E, LOOSE>;
     using X = Vals<E>;
     constexpr int LG = kFp8Group / E;
     constexpr int ROWS = kFp8BlockThreads / LG;     // rows a pass
@@ -418,22 +472,22 @@ rms_fp8_blocks(const Fp8BlocksParams p)
     const int NV = (p.H + E - 1) / E;
     const uint32_t ldx = (uint32_t)p.ldx;
     const int vi = (int)blockIdx.x * LG + lane;
-    const bool words = LOOSE && ((uintptr_t)p.q % 4 == 0) && p.ldq % 4 == 0;
+    const bool whole = LOOSE && ((uintptr_t)p.q % E == 0) && p.ldq % E == 0;
 
     griddep_wait();
     for (int64_t rb = blockIdx.y; rb * kFp8Group < p.M; rb += gridDim.y) {
         const int64_t row0 = rb * kFp8Group + sub;
-        P xv[NP];
+        R xv[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int64_t row = row0 + i * ROWS;
-            xv[i] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(p.x, row, ldx, vi, p.H) : P::zero();
+            xv[i] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(p.x, row, ldx, vi, p.H) : R::zero();
         }
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             X y;
-            xv[i].widen(y);
+            fp8_pack<T, E>(xv[i]).widen(y);
             a = amax_nan(a, pack_amax<E>(y));
         }
         a = lanes_amax<32>(a);
@@ -451,21 +505,16 @@ rms_fp8_blocks(const Fp8BlocksParams p)
         for (int i = 0; i < NP; ++i) {
             const int64_t row = row0 + i * ROWS;
             X y;
-            xv[i].widen(y);
+            fp8_pack<T, E>(xv[i]).widen(y);
             if (row < p.M && vi < NV)
-                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, words, y, sc.inv,
+                fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, whole, y, sc.inv,
                                     p.e5m2);
         }
     }
     griddep_launch_dependents();
 }
 
-// fn of one shape for the three modes; the residual form does not load ahead
-#define RMSK_FP8_ROWS(T, E, V, LR, MAXT, MINB, AHEAD, HOLD, LOOSE)                             \
-    {{(const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeQuant, AHEAD, HOLD, LOOSE>, \
-      (const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeNorm, AHEAD, HOLD, LOOSE>,  \
-      (const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, kFp8ModeResidual, false, HOLD,      \
-                                  LOOSE>},                                                     \
-     E, V, LR, MAXT}
+#define RMSK_FP8_ROWS(T, MODE, E, V, LR, MAXT, MINB, AHEAD, HOLD, LOOSE)                      \
+    {(const void *)&rms_fp8_rows<T, E, V, LR, MAXT, MINB, MODE, AHEAD, HOLD, LOOSE>, E, V, LR, MAXT}
 
 } // namespace rmsk

@@ -1,19 +1,43 @@
-// 8-bit rows and blocks (fp8_rows.cuh) of bf16 tensors.
+// 8-bit rows and blocks (fp8_rows.cuh) of bf16 tensors. Per mode: rows that
+// share a warp, a CTA a row (few rows; rows of up to 5120 columns for 16-bit
+// types; wider ones), 16-byte packs, loose packs.
 #include "fp8_rows.cuh"
 
 namespace rmsk {
 
 const Fp8RowSet fp8_rows_bf16 = {
-    {RMSK_FP8_ROWS(bf16, 16, 1, 8, 256, 4, true, true, false),
-     RMSK_FP8_ROWS(bf16, 16, 1, 16, 256, 4, true, true, false),
-     RMSK_FP8_ROWS(bf16, 16, 1, 32, 256, 4, true, true, false),
-     RMSK_FP8_ROWS(bf16, 16, 1, 0, 1024, 1, false, true, false),
-     RMSK_FP8_ROWS(bf16, 16, 2, 0, 256, 3, true, false, false),
-     RMSK_FP8_ROWS(bf16, 16, 2, 0, 512, 1, true, false, false),
-     RMSK_FP8_ROWS(bf16, 8, 2, 0, 1024, 1, true, false, false),
-     RMSK_FP8_ROWS(bf16, 4, 4, 0, 1024, 1, false, false, true)},
-    {(const void *)&rms_fp8_blocks<bf16, 16, false>, (const void *)&rms_fp8_blocks<bf16, 8, false>,
-     (const void *)&rms_fp8_blocks<bf16, 4, true>},
-    {16, 8, 4}};
+    {
+        {RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 1, 8, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 1, 16, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 1, 32, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 2, 32, 256, 3, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 1, 0, 1024, 1, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 2, 0, 160, 4, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 16, 2, 0, 512, 1, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, false, true)},
+        {RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 1, 8, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 1, 16, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 1, 32, 256, 4, true, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 2, 32, 256, 3, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 1, 0, 1024, 1, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 2, 0, 160, 4, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 16, 4, 0, 512, 1, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 8, 2, 0, 1024, 1, true, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeNorm, 8, 2, 0, 1024, 1, false, false, true)},
+        {RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 1, 8, 256, 4, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 1, 16, 256, 4, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 1, 32, 256, 4, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 2, 32, 256, 2, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 1, 0, 1024, 1, false, true, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 2, 0, 160, 4, false, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 16, 2, 0, 1024, 1, false, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, false, false),
+         RMSK_FP8_ROWS(bf16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, false, true)},
+    },
+    {(const void *)&rms_fp8_blocks<bf16, 16, false>,
+     (const void *)&rms_fp8_blocks<bf16, 8, false>,
+     (const void *)&rms_fp8_blocks<bf16, 8, true>},
+    {16, 8, 8}};
 
 } // namespace rmsk
