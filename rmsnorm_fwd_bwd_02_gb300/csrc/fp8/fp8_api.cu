@@ -151,7 +151,7 @@ int gemm_impl(const void *a, int64_t lda, const float *sa, int at, const void *b
             continue;
         tiles_r = ((swap ? N : M) + kFp8TileR - 1) / kFp8TileR;
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
-        KS = (int)std::max<int64_t>(1, std::min<int64_t>({8, G, sms / (tiles_r * tiles_c)}));
+        KS = (int)std::max<int64_t>(1, std::min<int64_t>({kFp8MaxCluster, G, sms / (tiles_r * tiles_c)}));
         const int ng = (G + KS - 1) / KS;
         const int most = swap ? (v == 2 ? 8 : 6) : 6;
         L = fp8_gemm_layout(BN, swap, std::min(ng, most), ng);

@@ -39,6 +39,7 @@
 
 namespace rmsk {
 
+constexpr int kFp8MaxCluster = 8;                      // CTAs that split K
 constexpr int kFp8TileR = 128;                          // rows of the row operand
 constexpr uint32_t kFp8StageR = kFp8TileR * kFp8Group;  // its bytes in a stage
 
@@ -49,7 +50,7 @@ __host__ __device__ constexpr int fp8_tmem_cols(int BN) { return BN * fp8_acc_bu
 
 // Shared memory of one CTA, byte offsets from a 1024-byte aligned base: the
 // ring (NSt stages of 128 + BN rows of 128 bytes; the sums [128][BN + 4]
-// over it at the end), the scales of the tokens with SWAP ([groups][BN]),
+// over it at the end), the scales of the tokens with SWAP ([groups][BN + 4]),
 // the mbarriers (full, empty a stage; full, empty a buffer; drain), eight
 // words (tensor-memory address, failure flag, stages issued, consumed).
 struct Fp8GemmLayout {
@@ -65,7 +66,7 @@ __host__ __device__ inline Fp8GemmLayout fp8_gemm_layout(int BN, bool swap, int 
     const uint32_t ring = (uint32_t)NSt * L.stage;
     const uint32_t sums = (uint32_t)kFp8TileR * (uint32_t)(BN + 4) * 4u;
     L.sc = ((ring > sums ? ring : sums) + 15u) & ~15u;
-    L.bar = L.sc + (swap ? (uint32_t)groups * (uint32_t)BN * 4u : 0u);
+    L.bar = L.sc + (swap ? (uint32_t)groups * (uint32_t)(BN + 4) * 4u : 0u);
     L.slots = L.bar + 8u * (uint32_t)(2 * NSt + 2 * fp8_acc_bufs(BN) + 1);
     L.total = L.slots + 32u + 1023u;
     // An SM has 512 columns of tensor memory. A CTA that waits for its
@@ -111,6 +112,64 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b,
                  : "memory");
 }
 
+// One lane of a converged warp. The roles' loops are run by whole warps and
+// only the instructions that one thread must issue sit under this predicate:
+// descriptors and barriers then stay in uniform registers. (With the loop
+// itself under `lane == 0` a group of 128 columns took some 1100 cycles to
+// issue.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait of a whole warp, as tc_wait, but the clock is only read once
+// in a while (each try already blocks for a time of the hardware's choice).
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, unsigned long long limit,
+                                         volatile int *fail)
+{
+    unsigned long long t0 = 0;
+    for (int i = 0;; ++i) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+            return true;
+        if ((i & 31) == 31) {
+            const unsigned long long t = global_ns();
+            if (t0 == 0)
+                t0 = t;
+            const bool stop = *fail || t - t0 > limit;
+            if (__any_sync(0xFFFFFFFFu, stop)) {
+                *fail = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// N consecutive fp32 columns of the warp's 32 lanes (lane = this thread);
+// complete only after tmem_wait on the same registers.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
+                   "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // Four floats of a peer's shared memory (cluster address).
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
 {
@@ -149,7 +208,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
 {
     constexpr int EW = fp8_epi_warps(BN), NB = fp8_acc_bufs(BN);
     constexpr int CW = BN * 4 / EW;                     // columns a thread sums
-    constexpr int SROW = BN + 4;                        // floats a row of the sums
+    constexpr int SROW = BN + 4, kScRow = BN + 4;       // floats a row of the sums, the scales
     constexpr uint32_t kCols = fp8_tmem_cols(BN);
     extern __shared__ __align__(1024) unsigned char fp8_smem[];
 
@@ -199,49 +258,53 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
     const uint32_t tmem = static_cast<uint32_t>(slots[0]);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // -------------------------------------------------- copies
-            const CUtensorMap *tmW = SWAP ? &tmR : &tmC, *tmA = SWAP ? &tmC : &tmR;
-            const uint32_t offW = SWAP ? 0u : kFp8StageR, offA = SWAP ? kFp8StageR : 0u;
-            const int w0 = SWAP ? r0 : c0, a0 = SWAP ? c0 : r0;
-            // the weight's first stages may start before the previous kernel
-            // is complete
-            const int early = p.static_w ? min(ng, NSt) : 0;
+        // ------------------------------------------------------ copies
+        const CUtensorMap *tmW = SWAP ? &tmR : &tmC, *tmA = SWAP ? &tmC : &tmR;
+        const uint32_t offW = SWAP ? 0u : kFp8StageR, offA = SWAP ? kFp8StageR : 0u;
+        const int w0 = SWAP ? r0 : c0, a0 = SWAP ? c0 : r0;
+        // the weight's first stages may start before the previous kernel is
+        // complete
+        const int early = p.static_w ? min(ng, NSt) : 0;
+        if (elect_one()) {
             for (int q = 0; q < early; ++q) {
                 mbar_expect_tx(full0 + 8u * q, L.stage + p.extra_tx);
                 tma_load_2d(ring_s + (uint32_t)q * L.stage + offW, tmW, (g0 + q) * kFp8Group, w0,
                             full0 + 8u * q);
-                slots[2] = q + 1;
             }
-            griddep_wait();
-            for (int q = 0; q < ng; ++q) {
-                const int s = q % NSt, u = q / NSt;
-                const uint32_t dst = ring_s + (uint32_t)s * L.stage, bar = full0 + 8u * s;
-                const int x = (g0 + q) * kFp8Group;
+        }
+        griddep_wait();
+        int q = 0;
+        for (int s = 0, u = 0; q < ng; ++q) {
+            const uint32_t dst = ring_s + (uint32_t)s * L.stage, bar = full0 + 8u * s;
+            const int x = (g0 + q) * kFp8Group;
+            if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail))
+                break;
+            if (elect_one()) {
                 if (q >= early) {
-                    if (u > 0 && !tc_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail))
-                        break;
                     mbar_expect_tx(bar, L.stage + p.extra_tx);
                     tma_load_2d(dst + offW, tmW, x, w0, bar);
                 }
                 tma_load_2d(dst + offA, tmA, x, a0, bar);
-                slots[2] = q + 1;
             }
-            griddep_launch_dependents();
+            if (++s == NSt) {
+                s = 0;
+                ++u;
+            }
         }
-        __syncwarp();
+        if (elect_one())
+            slots[2] = q;
+        griddep_launch_dependents();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------------------------------------------- MMAs
-            const uint64_t dr0 = umma_desc_sw128(ring_s);
-            for (int q = 0; q < ng; ++q) {
-                const int s = q % NSt, b = q % NB;
-                if (q >= NB &&
-                    !tc_wait(acce0 + 8u * b, (uint32_t)((q / NB - 1) & 1), limit, fail))
-                    break;
-                if (!tc_wait(full0 + 8u * s, (uint32_t)((q / NSt) & 1), limit, fail))
-                    break;
-                tc_fence_after_sync();
+        // -------------------------------------------------------- MMAs
+        const uint64_t dr0 = umma_desc_sw128(ring_s);
+        int q = 0;
+        for (int s = 0, us = 0, b = 0, ub = 0; q < ng; ++q) {
+            if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), limit, fail))
+                break;
+            if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), limit, fail))
+                break;
+            tc_fence_after_sync();
+            if (elect_one()) {
                 const uint64_t da = dr0 + (uint64_t)((uint32_t)s * (L.stage >> 4));
                 const uint64_t db = da + (kFp8StageR >> 4);
 #pragma unroll
@@ -250,10 +313,19 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
                             k4 != 0 ? 1u : 0u);
                 umma_commit(empty0 + 8u * s);
                 umma_commit(accf0 + 8u * b);
-                slots[3] = q + 1;
+            }
+            __syncwarp();
+            if (++s == NSt) {
+                s = 0;
+                ++us;
+            }
+            if (++b == NB) {
+                b = 0;
+                ++ub;
             }
         }
-        __syncwarp();
+        if (elect_one())
+            slots[3] = q;
     } else {
         // ------------------------------------------------------ the sums
         const int etid = tid - 64, q4 = warp & 3, half = (warp - 2) / 4;
@@ -263,9 +335,24 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         const float *sb = p.sb + (int64_t)((SWAP ? r0 : c0) / kFp8Group) * p.G + g0;
         const float *sa = p.sa + (int64_t)min(r0 + row, p.M - 1) * p.G + g0;
         if constexpr (SWAP) {
-            for (int i = etid; i < ng * BN; i += EW * 32) {
-                const int g = i / BN, t = c0 + i % BN;
-                sc[i] = t < p.M ? p.sa[(int64_t)t * p.G + g0 + g] * __ldg(sb + g) : 0.f;
+            // the products of the tokens' scales and the block's: each warp
+            // takes tokens, its lanes the groups (neighbours in memory), four
+            // tokens' loads in flight
+            const int w = warp - 2, nt = min(BN, p.M - c0);
+            for (int g = lane; g < ng; g += 32) {
+                const float sbg = __ldg(sb + g);
+                for (int t0 = w; t0 < BN; t0 += 4 * EW) {
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = t0 + j * EW;
+                        v[j] = t < nt ? p.sa[(int64_t)(c0 + t) * p.G + g0 + g] : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (t0 + j * EW < BN)
+                            sc[g * kScRow + t0 + j * EW] = v[j] * sbg;
+                }
             }
             named_bar_sync(1, EW * 32);
         }
@@ -274,36 +361,54 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         for (int i = 0; i < CW / 2; ++i)
             acc[i] = make_float2(0.f, 0.f);
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-        for (int q = 0; q < ng; ++q) {
-            const int b = q % NB;
-            float s = 0.f;
-            if constexpr (!SWAP)
-                s = sa[q] * __ldg(sb + q);
-            // warp-uniform (the loads from tensor memory need every lane)
-            if (!__all_sync(0xFFFFFFFFu,
-                            tc_wait(accf0 + 8u * b, (uint32_t)((q / NB) & 1), limit, fail)))
-                break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < CW; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(tmem + lanes + (uint32_t)(b * BN + col0 + c), v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float2 s2;
-                    if constexpr (SWAP)
-                        s2 = *reinterpret_cast<const float2 *>(sc + q * BN + col0 + c + 2 * j);
-                    else
-                        s2 = make_float2(s, s);
-                    const float2 x =
-                        make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                    acc[c / 2 + j] = vfma(x, s2, acc[c / 2 + j]);
+        float sa_next = 0.f, sb_next = 0.f;
+        if constexpr (!SWAP) {
+            sa_next = sa[0];
+            sb_next = __ldg(sb);
+        }
+        for (int q = 0, b = 0, ub = 0; q < ng; ++q) {
+            const float s = sa_next * sb_next;
+            if constexpr (!SWAP) {
+                if (q + 1 < ng) {                   // one group ahead
+                    sa_next = sa[q + 1];
+                    sb_next = __ldg(sb + q + 1);
                 }
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(acce0 + 8u * b);
+            if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), limit, fail))
+                break;
+            tc_fence_after_sync();
+            const uint32_t at = tmem + lanes + (uint32_t)(b * BN + col0);
+            uint32_t v[2][16];                      // the next 16 columns come while
+            tmem_ld_start(at, v[0]);                // these are added
+#pragma unroll
+            for (int c = 0; c < CW; c += 16) {
+                uint32_t(&w)[16] = v[(c / 16) & 1];
+                tmem_wait(w);
+                if (c + 16 < CW)
+                    tmem_ld_start(at + (uint32_t)(c + 16), v[(c / 16 + 1) & 1]);
+                if (c + 16 >= CW) {                 // all of the buffer is in registers
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(acce0 + 8u * b);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float4 s4 = make_float4(s, s, s, s);
+                    if constexpr (SWAP)
+                        s4 = *reinterpret_cast<const float4 *>(sc + q * kScRow + col0 + c + 4 * j);
+                    acc[c / 2 + 2 * j] = vfma(
+                        make_float2(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1])),
+                        make_float2(s4.x, s4.y), acc[c / 2 + 2 * j]);
+                    acc[c / 2 + 2 * j + 1] = vfma(
+                        make_float2(__uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3])),
+                        make_float2(s4.z, s4.w), acc[c / 2 + 2 * j + 1]);
+                }
+            }
+            if (++b == NB) {
+                b = 0;
+                ++ub;
+            }
         }
         // the ring is drained: the last buffer was complete, so every copy
         // has landed and every MMA has read it (or the CTA has failed, and
@@ -350,13 +455,19 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
             if (KS == 1) {
                 v = *reinterpret_cast<const float4 *>(base + at);
             } else {
-                for (int k = 0; k < KS; ++k) {
-                    const float4 w = ld_cluster_v4(cluster_map(sums_s + at, (uint32_t)k));
-                    v.x += w.x;
-                    v.y += w.y;
-                    v.z += w.z;
-                    v.w += w.w;
-                }
+                float4 w[kFp8MaxCluster];           // all loads, then the sum in rank order
+#pragma unroll
+                for (int k = 0; k < kFp8MaxCluster; ++k)
+                    if (k < KS)
+                        w[k] = ld_cluster_v4(cluster_map(sums_s + at, (uint32_t)k));
+#pragma unroll
+                for (int k = 0; k < kFp8MaxCluster; ++k)
+                    if (k < KS) {
+                        v.x += w[k].x;
+                        v.y += w[k].y;
+                        v.z += w[k].z;
+                        v.w += w[k].w;
+                    }
             }
             const float e[4] = {v.x, v.y, v.z, v.w};
             if constexpr (SWAP) {                       // row: a feature, columns: tokens
