@@ -435,7 +435,7 @@ void rmsnorm_set_path_override(int path);
  * product on tcgen05, automatic above 8 rows on rows of 2048 features or
  * more; each also takes the rows only it holds), 9 the 8-bit rows
  * (rmsnorm_fwd_fp8, rmsnorm_quant_fp8), 10 the 8-bit blocks, 11 the 8-bit
- * product, 0 none. */
+ * product a tile a CTA or cluster, 12 the same by pairs of CTAs, 0 none. */
 int rmsnorm_last_path(void);
 
 /*
@@ -475,6 +475,15 @@ void rmsnorm_set_stream_test_fault(unsigned int extra_tx_bytes,
  * up to the order of the fp32 sums.
  */
 void rmsnorm_set_gemv_cluster_test(int cluster_size);
+
+/*
+ * Test hook, process-wide, not thread-safe against concurrent calls: later
+ * rmsnorm_gemm_fp8 calls run the tile kernel (11) or the paired one (12; where
+ * its grid would not fit an int32, the tile kernel) at any size. Other values
+ * restore the choice by size. Results are the same up to the order of the
+ * fp32 sums.
+ */
+void rmsnorm_set_gemm_fp8_test(int path);
 
 /*
  * Backward that allocates nothing and needs no workspace from the caller.

@@ -9,13 +9,18 @@
 #include "../registry.h"
 #include "fp8.h"
 #include "fp8_gemm.cuh"
+#include "fp8_gemm_pair.cuh"
 #include "fp8_registry.h"
 
 using namespace rmsk;
 
 namespace {
 
-constexpr int kPathFp8Rows = 9, kPathFp8Blocks = 10, kPathFp8Gemm = 11;
+constexpr int kPathFp8Rows = 9, kPathFp8Blocks = 10, kPathFp8Gemm = 11,
+              kPathFp8Pair = 12;
+
+// Test hook: the product's kernel (see rmsnorm.h).
+std::atomic<int> g_test_gemm_fp8{0};
 
 bool fp8_type(int t) { return t == RMSNORM_E4M3 || t == RMSNORM_E5M2; }
 
@@ -126,18 +131,97 @@ int blocks_impl(const Fp8RowsParams &r, int dtype, cudaStream_t stream)
 }
 
 // ------------------------------------------------------------- the product
-int gemm_impl(const void *a, int64_t lda, const float *sa, int at, const void *b, int64_t ldb,
-              const float *sb, int bt, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
-              int dtype, int flags, cudaStream_t stream)
+struct Fp8GemmArgs {
+    const void *a, *b;
+    const float *sa, *sb;
+    void *out;
+    int64_t lda, ldb, ldo, M, N, K;
+    int at, bt, dtype, static_w;
+    int G() const { return (int)((K + kFp8Group - 1) / kFp8Group); }
+};
+
+// [rows][K] bytes, 128-byte swizzle, reads past the end zero: boxes of
+// `box_rows` rows x 128 columns.
+int fp8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int64_t ld, int box_rows)
 {
-    static const int kBN[4] = {16, 32, 64, 128};
-    int dev, sms, bps, st;
-    if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
-        return st;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr)
         return RMSNORM_ERR_UNSUPPORTED;
-    const int G = (int)((K + kFp8Group - 1) / kFp8Group);
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
+    const cuuint32_t box[2] = {(cuuint32_t)kFp8Group, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    if (encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cuda_fail(cudaErrorInvalidValue);
+    return RMSNORM_OK;
+}
+
+int launch_gemm(const void *fn, int64_t ctas, int threads, size_t smem, int cluster,
+                cudaStream_t stream, void *params, CUtensorMap *map0, CUtensorMap *map1, int dev)
+{
+    unsigned int *tmo = stream_timeout_counter(dev);
+    if (tmo == nullptr)
+        return cuda_fail(cudaErrorInvalidSymbol);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    void *args[4] = {params, map0, map1, &tmo};
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    return e == cudaSuccess ? RMSNORM_OK : cuda_fail(e);
+}
+
+// Pairs of CTAs on tiles of 256 x 256 (fp8_gemm_pair.cuh).
+int pair_impl(const Fp8GemmArgs &g, int dev, int64_t tiles_m, int64_t tiles_n, cudaStream_t stream)
+{
+    const void *fn = fp8_pair_kernels.fn[g.dtype];
+    int pairs, st;
+    if ((st = max_active_clusters(fn, kPairThreads, (int)kPairSmem, 2, dev, &pairs)))
+        return st;
+    CUtensorMap mapA, mapB;
+    if ((st = fp8_map(&mapA, g.a, g.M, g.K, g.lda, 128)) ||
+        (st = fp8_map(&mapB, g.b, g.N, g.K, g.ldb, 128)))
+        return st;
+    const size_t es = elem_size(g.dtype);
+    Fp8PairParams p = {g.sa, g.sb, g.out, g.ldo, (int)g.M, (int)g.N, g.G(), (int)tiles_m,
+                       (int)tiles_n,
+                       umma_idesc_f8((uint32_t)g.at, (uint32_t)g.bt, kPairTile, kPairTile),
+                       g.static_w, aligned(g.out, 16) && g.ldo * es % 16 == 0 ? 1 : 0,
+                       g_test_extra_tx.load(std::memory_order_relaxed),
+                       g_test_wait_us.load(std::memory_order_relaxed)};
+    if ((st = launch_gemm(fn, 2 * std::min<int64_t>(pairs, tiles_m * tiles_n), kPairThreads, kPairSmem,
+                          2, stream, &p, &mapA, &mapB, dev)))
+        return st;
+    t_last_path = kPathFp8Pair;
+    return RMSNORM_OK;
+}
+
+int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
+{
+    static const int kBN[4] = {16, 32, 64, 128};
+    const int64_t M = g.M, N = g.N;
+    int dev, sms, bps, st;
+    if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
+        return st;
+    const int64_t tm = (M + kPairTile - 1) / kPairTile, tn = (N + kPairTile - 1) / kPairTile;
+    const int ov = g_test_gemm_fp8.load(std::memory_order_relaxed);
+    const bool fits = tm * tn * g.G() < INT32_MAX;
+    if (fits && (ov == kPathFp8Pair || (ov != kPathFp8Gemm && tm * tn >= sms / 2)))
+        return pair_impl(g, dev, tm, tn, stream);
+    const int G = g.G();
     // the narrowest column operand that holds the tokens, whose scales must
     // fit in shared memory; else tokens in tiles of 128 rows
     int v = 0;
@@ -151,10 +235,23 @@ int gemm_impl(const void *a, int64_t lda, const float *sa, int at, const void *b
             continue;
         tiles_r = ((swap ? N : M) + kFp8TileR - 1) / kFp8TileR;
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
-        KS = (int)std::max<int64_t>(1, std::min<int64_t>({kFp8MaxCluster, G, sms / (tiles_r * tiles_c)}));
-        const int ng = (G + KS - 1) / KS;
-        const int most = swap ? (v == 2 ? 8 : 6) : 6;
-        L = fp8_gemm_layout(BN, swap, std::min(ng, most), ng);
+        // the largest cluster with which the whole grid runs at once
+        for (KS = std::min(kFp8MaxCluster, G); KS >= 1; --KS) {
+            const int ng = (G + KS - 1) / KS;
+            L = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
+            if (L.total > 227u * 1024u)
+                continue;
+            int n;
+            if ((st = max_active_clusters(fp8_gemm_kernels.fn[v][g.dtype], fp8_gemm_threads(BN),
+                                          (int)L.total, KS, dev, &n)))
+                return st;
+            if (tiles_r * tiles_c <= n)
+                break;
+        }
+        if (KS < 1) {
+            KS = 1;
+            L = fp8_gemm_layout(BN, swap, std::min(G, 6), G);
+        }
         if (!swap || L.total <= 227u * 1024u)
             break;
     }
@@ -163,53 +260,22 @@ int gemm_impl(const void *a, int64_t lda, const float *sa, int at, const void *b
     const int64_t ctas = tiles_r * tiles_c * KS;
     if (ctas > INT32_MAX)
         return RMSNORM_ERR_UNSUPPORTED;
-    // [rows][K] bytes, 128-byte swizzle, reads past the end zero: boxes of
-    // `box_rows` rows x 128 columns
-    auto make_map = [&](CUtensorMap *map, const void *base, int64_t rows, int64_t ld, int box_rows) {
-        const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-        const cuuint64_t strides[1] = {(cuuint64_t)ld};
-        const cuuint32_t box[2] = {(cuuint32_t)kFp8Group, (cuuint32_t)box_rows};
-        const cuuint32_t estr[2] = {1, 1};
-        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
-                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
     CUtensorMap mapA, mapB;
-    if (make_map(&mapA, a, M, lda, swap ? BN : kFp8TileR) != CUDA_SUCCESS ||
-        make_map(&mapB, b, N, ldb, swap ? kFp8TileR : BN) != CUDA_SUCCESS)
-        return cuda_fail(cudaErrorInvalidValue);
-    unsigned int *tmo = stream_timeout_counter(dev);
-    if (tmo == nullptr)
-        return cuda_fail(cudaErrorInvalidSymbol);
-    const void *fn = fp8_gemm_kernels.fn[v][dtype];
-    const size_t es = elem_size(dtype);
-    Fp8GemmParams p = {sa, sb, out, ldo, (int)M, (int)N, G, KS, (int)tiles_r,
-                       swap ? umma_idesc_f8((uint32_t)bt, (uint32_t)at, kFp8TileR, BN)
-                            : umma_idesc_f8((uint32_t)at, (uint32_t)bt, kFp8TileR, BN),
-                       (flags & RMSNORM_GEMM_FP8_STATIC_WEIGHTS) ? 1 : 0,
-                       aligned(out, 4 * es) && ldo % 4 == 0 ? 1 : 0,
+    if ((st = fp8_map(&mapA, g.a, M, g.K, g.lda, swap ? BN : kFp8TileR)) ||
+        (st = fp8_map(&mapB, g.b, N, g.K, g.ldb, swap ? kFp8TileR : BN)))
+        return st;
+    const void *fn = fp8_gemm_kernels.fn[v][g.dtype];
+    const size_t es = elem_size(g.dtype);
+    Fp8GemmParams p = {g.sa, g.sb, g.out, g.ldo, (int)M, (int)N, G, KS, (int)tiles_r,
+                       swap ? umma_idesc_f8((uint32_t)g.bt, (uint32_t)g.at, kFp8TileR, BN)
+                            : umma_idesc_f8((uint32_t)g.at, (uint32_t)g.bt, kFp8TileR, BN),
+                       g.static_w, aligned(g.out, 4 * es) && g.ldo % 4 == 0 ? 1 : 0,
                        g_test_extra_tx.load(std::memory_order_relaxed),
                        g_test_wait_us.load(std::memory_order_relaxed), L};
-    if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)))
+    if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)) ||
+        (st = launch_gemm(fn, ctas, fp8_gemm_threads(BN), L.total, KS, stream, &p,
+                          swap ? &mapB : &mapA, swap ? &mapA : &mapB, dev)))
         return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3((unsigned)fp8_gemm_threads(BN));
-    cfg.dynamicSmemBytes = L.total;
-    cfg.stream = stream;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = (unsigned)KS;
-    attrs[1].val.clusterDim.y = 1;
-    attrs[1].val.clusterDim.z = 1;
-    cfg.attrs = attrs;
-    cfg.numAttrs = KS > 1 ? 2 : 1;
-    void *args[4] = {&p, swap ? &mapB : &mapA, swap ? &mapA : &mapB, &tmo};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
-    if (e != cudaSuccess)
-        return cuda_fail(e);
     t_last_path = kPathFp8Gemm;
     return RMSNORM_OK;
 }
@@ -321,8 +387,11 @@ int rmsnorm_gemm_fp8(const void *a, int64_t lda, const float *a_scale, int a_typ
                    flat(b_scale, (size_t)((N + kFp8Group - 1) / kFp8Group * G) * 4)})
         if (overlap(so, i))
             return RMSNORM_ERR_ALIAS;
-    return gemm_impl(a, lda, a_scale, a_type, b, ldb, b_scale, b_type, out, ldo, M, N, K, dtype,
-                     flags, static_cast<cudaStream_t>(stream));
+    const Fp8GemmArgs g = {a, b, a_scale, b_scale, out, lda, ldb, ldo, M, N, K, a_type, b_type, dtype,
+                           (flags & RMSNORM_GEMM_FP8_STATIC_WEIGHTS) ? 1 : 0};
+    return gemm_impl(g, static_cast<cudaStream_t>(stream));
 }
+
+void rmsnorm_set_gemm_fp8_test(int path) { g_test_gemm_fp8.store(path); }
 
 } // extern "C"

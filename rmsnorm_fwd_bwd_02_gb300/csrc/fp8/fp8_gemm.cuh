@@ -336,23 +336,21 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         const float *sa = p.sa + (int64_t)min(r0 + row, p.M - 1) * p.G + g0;
         if constexpr (SWAP) {
             // the products of the tokens' scales and the block's: each warp
-            // takes tokens, its lanes the groups (neighbours in memory), four
-            // tokens' loads in flight
+            // takes every EW-th token, its lanes the groups (neighbours in
+            // memory); all of a lane's loads are in flight at once (a round
+            // trip takes 1 to 2 us while the weight streams in)
             const int w = warp - 2, nt = min(BN, p.M - c0);
             for (int g = lane; g < ng; g += 32) {
                 const float sbg = __ldg(sb + g);
-                for (int t0 = w; t0 < BN; t0 += 4 * EW) {
-                    float v[4];
+                float v[BN / EW];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t = t0 + j * EW;
-                        v[j] = t < nt ? p.sa[(int64_t)(c0 + t) * p.G + g0 + g] : 0.f;
-                    }
+                for (int j = 0; j < BN / EW; ++j)
+                    v[j] = w + j * EW < nt
+                               ? __ldcg(p.sa + (int64_t)(c0 + w + j * EW) * p.G + g0 + g)
+                               : 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (t0 + j * EW < BN)
-                            sc[g * kScRow + t0 + j * EW] = v[j] * sbg;
-                }
+                for (int j = 0; j < BN / EW; ++j)
+                    sc[g * kScRow + w + j * EW] = v[j] * sbg;
             }
             named_bar_sync(1, EW * 32);
         }

@@ -1,0 +1,388 @@
+// fp8_gemm_pair.cuh -- the product of fp8_gemm.cuh for many tokens: pairs of
+// CTAs that share one tile of 256 x 256 (tcgen05.mma with cta_group::2),
+// persistent over the tiles.
+//
+// Mathematics and rounding: as in fp8_gemm.cuh; each group of 128 columns is
+// four MMAs (m256 n256 k32) into one of two buffers of tensor memory, read
+// back and added to fp32 sums in registers with the group's scales.
+//
+// Why this shape. At M = 8192, N = 24576, K = 4096 the tensor cores' time is
+// the floor (422 us at twice the measured bf16 rate). An SM alone on a 128 x
+// 256 tile would read 48 KB of operands from L2 for every 512 cycles of MMAs
+// and as much from shared memory; a pair reads each row of A and of B once
+// for both SMs, 32 KB each. Reading the groups back is the other limit: 128 x
+// 256 sums a group and SM, 64 fp32 FMAs a cycle of the 128 an SM has, so the
+// tensor memory is loaded 16 columns at a time by sixteen warps (four on each
+// of the SM's quarters, to hide the loads' latency behind one another's
+// arithmetic), and the scale of a row and group is one product a thread. The
+// sums take 64 registers a thread.
+//
+// Roles (64 + 32 kPairEpi threads a CTA): warp 0 copies this CTA's 128 rows of
+// A and 128 rows of B into the ring; warp 1 of the leader (rank 0) issues the
+// MMAs of both; the others keep the sums of this CTA's 128 rows. The copies
+// of both CTAs complete on the leader's `full` barrier; the MMAs' completion
+// is sent to both CTAs' `empty` and `accf` barriers, and both CTAs' readers
+// hand a buffer back on the leader's `acce` barrier. The ring and the two
+// buffers run on across tiles, so the stores of one tile overlap the first
+// groups of the next.
+//
+// Waits are bounded as in fp8_gemm.cuh. A CTA that gives up still meets its
+// peer; the leader then waits (bounded) for copies in flight and MMAs.
+#pragma once
+
+#include "fp8_gemm.cuh"
+
+namespace rmsk {
+
+constexpr int kPairTile = 256;                          // rows of A and of B to a pair's tile
+constexpr int kPairEpi = 16;                            // epilogue warps of a CTA
+constexpr int kPairThreads = 64 + 32 * kPairEpi;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
+constexpr uint32_t kPairStage = 2u * kPairHalf;
+constexpr int kPairBufs = 2;                            // x 256 columns: all tensor memory
+constexpr int kPairTileRun = 8;                         // row tiles that are swept together
+// The ring, the mbarriers (full, empty; accf, acce; drain), eight words. All
+// of an SM's shared memory is taken: no other CTA may wait for tensor memory
+// beside this one.
+constexpr uint32_t kPairBar = kPairStages * kPairStage;
+constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 1);
+constexpr uint32_t kPairSmem = 227u * 1024u;
+static_assert(kPairSlots + 32u + 1023u <= kPairSmem, "shared memory of a pair's CTA");
+
+struct Fp8PairParams {
+    const float *sa;   // [M,G]
+    const float *sb;   // [ceil(N / 128),G]
+    void *out;         // [M,N], row stride ldo
+    int64_t ldo;
+    int M, N, G;
+    int tiles_m, tiles_n;
+    uint32_t idesc;
+    int static_w;
+    int vec;           // rows of out start at multiples of 16 bytes
+    uint32_t extra_tx, wait_limit_us;
+};
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// The mbarriers at this offset in both CTAs complete a phase once every
+// tcgen05 operation this thread issued before has.
+__device__ __forceinline__ void umma_commit_pair(uint32_t mbar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::"
+                 "cluster.b64 [%0], %1;" ::"r"(mbar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// As tma_load_2d, completing on a barrier of either CTA of the pair (`bar`: a
+// cluster address). x is a multiple of 128 one-byte elements.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                                 uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::"
+                 "complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+// 16 bytes of out from floats: four fp32 or eight 16-bit values.
+template <typename T> __device__ __forceinline__ void store_out16(T *p, const float *f)
+{
+    if constexpr (sizeof(T) == 4)
+        st_row_v4(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                __float_as_uint(f[3])));
+    else
+        st_row_v4(p, make_uint4(Half16<T>::narrow2(f[0], f[1]), Half16<T>::narrow2(f[2], f[3]),
+                                Half16<T>::narrow2(f[4], f[5]), Half16<T>::narrow2(f[6], f[7])));
+}
+
+// Tile t of the sweep: runs of kPairTileRun row tiles, each run over all
+// column tiles, so that the pairs at work at one time share rows of both
+// operands in L2.
+__device__ __forceinline__ void pair_tile(const Fp8PairParams &p, int t, int &m0, int &n0)
+{
+    const int run = t / (kPairTileRun * p.tiles_n);
+    const int first = run * kPairTileRun, rows = min(kPairTileRun, p.tiles_m - first);
+    const int r = t - first * p.tiles_n;
+    m0 = (first + r % rows) * kPairTile;
+    n0 = r / rows * kPairTile;
+}
+
+// grid = 2 x pairs, cluster (2, 1, 1), kPairThreads threads, kPairSmem bytes.
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1)
+rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA,
+                  const __grid_constant__ CUtensorMap tmB, unsigned int *timeouts)
+{
+    constexpr int CW = kPairTile * 4 / kPairEpi;        // columns a thread sums
+    extern __shared__ __align__(1024) unsigned char pair_smem[];
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = (int)blockIdx.x / 2, npairs = (int)gridDim.x / 2;
+    const int ntiles = p.tiles_m * p.tiles_n, G = p.G;
+    const uint32_t raw_s = smem_addr(pair_smem);
+    unsigned char *base = pair_smem + (((raw_s + 1023u) & ~1023u) - raw_s);
+    const uint32_t ring_s = smem_addr(base);
+    const uint32_t full0 = ring_s + kPairBar, empty0 = full0 + 8u * kPairStages;
+    const uint32_t accf0 = empty0 + 8u * kPairStages, acce0 = accf0 + 8u * kPairBufs;
+    const uint32_t dbar = acce0 + 8u * kPairBufs;
+    int *slots = reinterpret_cast<int *>(base + kPairSlots);
+    volatile int *fail = slots + 1;
+    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+
+    if (tid == 32) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(full0 + 8u * s, 1);               // the leader's own arrival
+            mbar_init(empty0 + 8u * s, 1);
+        }
+        for (int b = 0; b < kPairBufs; ++b) {
+            mbar_init(accf0 + 8u * b, 1);
+            mbar_init(acce0 + 8u * b, 2 * kPairEpi);
+        }
+        mbar_init(dbar, 1);
+        slots[1] = slots[2] = slots[3] = 0;
+    }
+    if (tid == 64) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+    }
+    if (warp == 0)
+        tmem_alloc_pair(smem_addr(slots), kPairBufs * kPairTile);
+    mbar_init_fence();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_arrive_release();                           // the peer's barriers exist
+    cluster_wait_acquire();
+    tc_fence_after_sync();
+    const uint32_t tmem = static_cast<uint32_t>(slots[0]);
+
+    if (warp == 0) {
+        // ------------------------------------------------------ copies
+        const uint32_t lead = cluster_map(full0, 0);
+        bool waited = p.static_w == 0;
+        if (waited)
+            griddep_wait();
+        int q = 0, s = 0, u = 0;
+        bool stop = false;
+        for (int t = pair; t < ntiles && !stop; t += npairs) {
+            int m0, n0;
+            pair_tile(p, t, m0, n0);
+            m0 += (int)rank * 128;
+            n0 += (int)rank * 128;
+            for (int g = 0; g < G; ++g, ++q) {
+                if (!waited) {
+                    // rows of B may come before the previous kernel is
+                    // complete, as many as the ring holds
+                    const int early = min(G, kPairStages);
+                    if (elect_one()) {
+                        for (int e = 0; e < early; ++e) {
+                            if (rank == 0)
+                                mbar_expect_tx(full0 + 8u * e, 2u * kPairStage + p.extra_tx);
+                            tma_load_2d_pair(ring_s + (uint32_t)e * kPairStage + kPairHalf, &tmB,
+                                             e * kFp8Group, n0, lead + 8u * e);
+                        }
+                    }
+                    __syncwarp();
+                    griddep_wait();
+                    waited = true;
+                }
+                if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail)) {
+                    stop = true;
+                    break;
+                }
+                const bool have_b = p.static_w && q < min(G, kPairStages);
+                if (elect_one()) {
+                    const uint32_t dst = ring_s + (uint32_t)s * kPairStage, bar = lead + 8u * s;
+                    if (!have_b) {
+                        if (rank == 0)
+                            mbar_expect_tx(full0 + 8u * s, 2u * kPairStage + p.extra_tx);
+                        tma_load_2d_pair(dst + kPairHalf, &tmB, g * kFp8Group, n0, bar);
+                    }
+                    tma_load_2d_pair(dst, &tmA, g * kFp8Group, m0, bar);
+                }
+                __syncwarp();
+                if (++s == kPairStages) {
+                    s = 0;
+                    ++u;
+                }
+            }
+        }
+        if (lane == 0)
+            slots[2] = q;
+        griddep_launch_dependents();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---------------------------------------------------- MMAs
+            const uint64_t dr0 = umma_desc_sw128(ring_s);
+            int q = 0, s = 0, us = 0, b = 0, ub = 0;
+            const int nq = (ntiles - pair + npairs - 1) / npairs * G;
+            for (; q < nq; ++q) {
+                if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), limit, fail))
+                    break;
+                if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), limit, fail))
+                    break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t da = dr0 + (uint64_t)((uint32_t)s * (kPairStage >> 4));
+                    const uint64_t db = da + (kPairHalf >> 4);
+#pragma unroll
+                    for (int k4 = 0; k4 < kFp8Group / 32; ++k4)
+                        umma_f8_pair(tmem + (uint32_t)(b * kPairTile), da + 2 * k4, db + 2 * k4,
+                                     p.idesc, k4 != 0 ? 1u : 0u);
+                    umma_commit_pair(empty0 + 8u * s);
+                    umma_commit_pair(accf0 + 8u * b);
+                }
+                __syncwarp();
+                if (++s == kPairStages) {
+                    s = 0;
+                    ++us;
+                }
+                if (++b == kPairBufs) {
+                    b = 0;
+                    ++ub;
+                }
+            }
+            if (lane == 0)
+                slots[3] = q;
+        }
+    } else {
+        // ------------------------------------------------------ the sums
+        const int q4 = warp & 3, part = (warp - 2) / 4;
+        const int row = (int)rank * 128 + q4 * 32 + lane, col0 = part * CW;
+        const uint32_t at0 = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)col0;
+        const uint32_t hand_back = cluster_map(acce0, 0);
+        const int nblocks = (p.N + 127) / 128;
+        T *out = static_cast<T *>(p.out);
+        griddep_wait();
+        int b = 0, ub = 0;
+        bool stop = false;
+        for (int t = pair; t < ntiles && !stop; t += npairs) {
+            int m0, n0;
+            pair_tile(p, t, m0, n0);
+            const int m = m0 + row, n = n0 + col0;
+            const float *sa = p.sa + (int64_t)min(m, p.M - 1) * G;
+            const float *sb = p.sb + (int64_t)min(n / 128, nblocks - 1) * G;
+            float2 acc[CW / 2];
+#pragma unroll
+            for (int i = 0; i < CW / 2; ++i)
+                acc[i] = make_float2(0.f, 0.f);
+            float sa_next = sa[0], sb_next = __ldg(sb);
+            for (int g = 0; g < G; ++g) {
+                const float s = sa_next * sb_next;
+                if (g + 1 < G) {                        // one group ahead
+                    sa_next = sa[g + 1];
+                    sb_next = __ldg(sb + g + 1);
+                }
+                if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), limit, fail)) {
+                    stop = true;
+                    break;
+                }
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < CW; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(at0 + (uint32_t)(b * kPairTile + c), v);
+                    if (c + 16 == CW) {                 // this warp is done with the buffer
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_remote_cta(hand_back + 8u * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[c / 2 + j] = vfma(
+                            make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
+                            make_float2(s, s), acc[c / 2 + j]);
+                }
+                if (++b == kPairBufs) {
+                    b = 0;
+                    ++ub;
+                }
+            }
+            if (stop || m >= p.M)
+                continue;
+            T *to = out + (int64_t)m * p.ldo + n;
+            constexpr int W = 16 / (int)sizeof(T);      // values a 16-byte store
+#pragma unroll
+            for (int i = 0; i < CW / W; ++i) {
+                float f[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    f[j] = j & 1 ? acc[(i * W + j) / 2].y : acc[(i * W + j) / 2].x;
+                if (p.vec && n + (i + 1) * W <= p.N) {
+                    store_out16<T>(to + i * W, f);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (n + i * W + j < p.N)
+                            store_out1<T>(to + i * W + j, f[j]);
+                }
+            }
+        }
+    }
+
+    // every role has finished or given up
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    int bad = *fail;
+    if (tid == 0 && bad)
+        atomicAdd(timeouts, 1u);
+    if (rank == 0 && warp == 1) {
+        // copies of either CTA that no MMA consumed, and the MMAs themselves.
+        // A stage that only one of the two asked for never completes: the
+        // wait for it is as long as any copy could take.
+        int mine = 0, peer = 0;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                     : "=r"(peer)
+                     : "r"(cluster_map(smem_addr(slots + 2), 1))
+                     : "memory");
+        mine = slots[2];
+        const int done = slots[3];
+        for (int q = done; q < max(mine, peer); ++q)
+            if (!mbar_wait_bounded(full0 + 8u * (q % kPairStages), (uint32_t)((q / kPairStages) & 1),
+                                   limit))
+                break;
+        if (max(mine, peer) > done) {
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 "
+                             "[%0];" ::"r"(dbar)
+                             : "memory");
+            __syncwarp();
+            (void)mbar_wait_bounded(dbar, 0, limit);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (warp == 0) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, kPairBufs * kPairTile);
+    }
+}
+
+} // namespace rmsk

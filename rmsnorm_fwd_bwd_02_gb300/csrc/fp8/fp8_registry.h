@@ -10,4 +10,10 @@ struct Fp8GemmKernels {
 };
 extern const Fp8GemmKernels fp8_gemm_kernels;
 
+// fn[RMSNORM_F32, BF16, F16 output]
+struct Fp8PairKernels {
+    const void *fn[3];
+};
+extern const Fp8PairKernels fp8_pair_kernels;
+
 } // namespace rmsk

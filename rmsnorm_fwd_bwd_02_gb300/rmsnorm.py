@@ -24,7 +24,8 @@ PATH_GEMV = 5            # reported by last_path() after rmsnorm_gemv_fwd: the
 PATH_GEMV_TMA = 6        # weight in registers (5), fed by bulk copies (6), or
 PATH_GEMV_UMMA = 7       # the product on tcgen05 (7); 6 and 7 also force it
 PATH_GEMV_TC = 8         # persistent tcgen05 kernel, y held per CTA (8; forces it)
-PATH_FP8_ROWS, PATH_FP8_BLOCKS, PATH_FP8_GEMM = 9, 10, 11   # reported only
+PATH_FP8_ROWS, PATH_FP8_BLOCKS = 9, 10            # reported only
+PATH_FP8_GEMM, PATH_FP8_PAIR = 11, 12             # the 8-bit product's kernels
 
 # Entry points of include/rmsnorm.h with their ctypes signatures.
 _i64, _vp, _sz, _int, _f = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
@@ -63,6 +64,7 @@ SIGNATURES = {
                                _i64, _vp, _i64, _i64, _f, _int, _int, _vp]),
     "rmsnorm_quant_fp8": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int,
                                  _int, _int, _vp]),
+    "rmsnorm_set_gemm_fp8_test": (None, [_int]),
     "rmsnorm_gemm_fp8": (_int, [_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _vp,
                                 _i64, _i64, _i64, _i64, _int, _int, _vp]),
 }
@@ -570,6 +572,12 @@ def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e
                                    block_rows, code, qcode, _raw_stream(dev)),
            "rmsnorm_quant_fp8")
     return q, scale
+
+
+def set_gemm_fp8_test(path: int):
+    """Test hook: run the 8-bit product's tile kernel (PATH_FP8_GEMM) or its
+    paired one (PATH_FP8_PAIR) at any size (0: by size; see rmsnorm.h)."""
+    lib().rmsnorm_set_gemm_fp8_test(int(path))
 
 
 def rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16,

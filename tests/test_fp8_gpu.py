@@ -315,6 +315,50 @@ def test_gemm(M, N, K):
                 assert torch.equal(first, out)            # the same bits every time
 
 
+class forced:
+    """One kernel of the product for the calls inside."""
+
+    def __init__(self, path):
+        self.path = path
+
+    def __enter__(self):
+        rn.set_gemm_fp8_test(self.path)
+
+    def __exit__(self, *a):
+        rn.set_gemm_fp8_test(0)
+
+
+PAIRS = [(1, 1, 1), (255, 130, 127), (256, 256, 128), (257, 257, 900), (300, 1000, 1000),
+         (2100, 2600, 700), (600, 8000, 130), (20000, 200, 300), (260, 9800, 384),
+         (4096, 4096, 4096), (513, 40000, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", PAIRS)
+@pytest.mark.parametrize("path", [rn.PATH_FP8_PAIR, rn.PATH_FP8_GEMM])
+def test_gemm_many_rows(M, N, K, path):
+    """Both kernels at sizes of many tiles (several a CTA, the last ones
+    ragged) and of less than one."""
+    i = PAIRS.index((M, N, K))
+    at, bt = ((E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2))[i % 4]
+    qa, sa, qb, sb = pair(M, N, K, seed=i, at=at, bt=bt)
+    want, T = gemm64(qa, sa, qb, sb)
+    for dtype in (BF16, F16, F32):
+        with forced(path):
+            out = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=dtype)
+            again = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=dtype, static_weights=True)
+            assert rn.last_path() == path
+        check_out(out, want, T, K, dtype)
+        assert torch.equal(out, again)
+
+
+def test_gemm_takes_pairs_by_size():
+    qa, sa, qb, sb = pair(2560, 2560, 256, seed=3)
+    rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+    assert rn.last_path() == rn.PATH_FP8_PAIR
+    rn.rmsnorm_gemm_fp8(qa[:64], sa[:64], qb, sb)
+    assert rn.last_path() == rn.PATH_FP8_GEMM
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 130, 1000), (20, 300, 130), (64, 200, 257), (90, 100, 300),
                                    (300, 515, 1000), (600, 1030, 2050)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -336,10 +380,12 @@ def test_gemm_reads_and_writes_only_its_rows(M, N, K, dtype):
 
     a, asc = inside(qa, sa)
     b, bsc = inside(qb, sb)
-    for ldo, off in ((N, 0), (N + 5, 0), (-(-N // 16) * 16 + 16, 0), (N + 3, 1)):
+    outs = ((N, 0), (N + 5, 0), (-(-N // 16) * 16 + 16, 0), (N + 3, 1))
+    for (ldo, off), path in [(o, p) for o in outs for p in (rn.PATH_FP8_GEMM, rn.PATH_FP8_PAIR)]:
         buf = torch.full((M + 3, ldo), -77.0, device=DEV, dtype=dtype)
         out = buf[1:M + 1, off:off + N]
-        rn.rmsnorm_gemm_fp8(a, asc, b, bsc, out=out)
+        with forced(path):
+            rn.rmsnorm_gemm_fp8(a, asc, b, bsc, out=out)
         want, T = gemm64(qa, sa, qb, sb)
         check_out(out, want, T, K, dtype)
         buf[1:M + 1, off:off + N] = -77.0
@@ -537,19 +583,20 @@ def test_refusals_of_the_binding():
     assert e.value.status == -9
 
 
-@pytest.mark.parametrize("M", [8, 100, 700])
-def test_bounded_waits(M):
+@pytest.mark.parametrize("M,path", [(8, 0), (100, 0), (700, 0), (700, rn.PATH_FP8_PAIR)])
+def test_bounded_waits(M, path):
     """A copy that never completes ends the kernel, is counted, and leaves
     the context usable."""
     qa, sa, qb, sb = pair(M, 300, 1024, seed=97)
-    good = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
-    torch.cuda.synchronize()
-    assert rn.wait_timeouts(reset=True) == 0
-    try:
-        rn.set_stream_test_fault(16, 2000)
-        rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+    with forced(path):
+        good = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
         torch.cuda.synchronize()
-    finally:
-        rn.set_stream_test_fault(0, 0)
-    assert rn.wait_timeouts(reset=True) > 0
-    assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
+        assert rn.wait_timeouts(reset=True) == 0
+        try:
+            rn.set_stream_test_fault(16, 2000)
+            rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+            torch.cuda.synchronize()
+        finally:
+            rn.set_stream_test_fault(0, 0)
+        assert rn.wait_timeouts(reset=True) > 0
+        assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
