@@ -17,9 +17,12 @@
 // arithmetic), and the scale of a row and group is one product a thread. The
 // sums take 64 registers a thread.
 //
-// Roles (64 + 32 kPairEpi threads a CTA): warp 0 copies this CTA's 128 rows of
+// Roles (kPairThreads threads a CTA): warp 0 copies this CTA's 128 rows of
 // A and 128 rows of B into the ring; warp 1 of the leader (rank 0) issues the
-// MMAs of both; the others keep the sums of this CTA's 128 rows. The copies
+// MMAs of both; the last two fetch the scales of this CTA's rows (a row's lie
+// beside one another in memory, a thread wants one of a row of its own: read
+// by the threads that use them, a warp's 32 came from 32 lines a group); the
+// others keep the sums of this CTA's 128 rows. The copies
 // of both CTAs complete on the leader's `full` barrier; the MMAs' completion
 // is sent to both CTAs' `empty` and `accf` barriers, and both CTAs' readers
 // hand a buffer back on the leader's `acce` barrier. The ring and the two
@@ -36,17 +39,22 @@ namespace rmsk {
 
 constexpr int kPairTile = 256;                          // rows of A and of B to a pair's tile
 constexpr int kPairEpi = 16;                            // epilogue warps of a CTA
-constexpr int kPairThreads = 64 + 32 * kPairEpi;
+constexpr int kPairScaleWarps = 2;                      // warps that fetch the rows' scales
+constexpr int kPairThreads = 64 + 32 * (kPairEpi + kPairScaleWarps);
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
 constexpr uint32_t kPairStage = 2u * kPairHalf;
 constexpr int kPairBufs = 2;                            // x 256 columns: all tensor memory
 constexpr int kPairTileRun = 8;                         // row tiles that are swept together
-// The ring, the mbarriers (full, empty; accf, acce; drain), eight words. All
-// of an SM's shared memory is taken: no other CTA may wait for tensor memory
-// beside this one.
-constexpr uint32_t kPairBar = kPairStages * kPairStage;
-constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 1);
+constexpr int kPairChunk = 16;                          // groups whose scales come together
+constexpr int kPairScRow = 129;                         // floats a group of them (no conflicts)
+// The ring, two chunks of the rows' scales, the mbarriers (full, empty; accf,
+// acce; scales full, empty; drain), eight words. All of an SM's shared memory
+// is taken: no other CTA may wait for tensor memory beside this one.
+constexpr uint32_t kPairSc = kPairStages * kPairStage;
+constexpr uint32_t kPairBar = kPairSc + 2u * kPairChunk * kPairScRow * 4u;
+constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 5);
+static_assert(kPairBar % 8 == 0, "barriers are 8-byte aligned");
 constexpr uint32_t kPairSmem = 227u * 1024u;
 static_assert(kPairSlots + 32u + 1023u <= kPairSmem, "shared memory of a pair's CTA");
 
@@ -148,7 +156,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
     const uint32_t ring_s = smem_addr(base);
     const uint32_t full0 = ring_s + kPairBar, empty0 = full0 + 8u * kPairStages;
     const uint32_t accf0 = empty0 + 8u * kPairStages, acce0 = accf0 + 8u * kPairBufs;
-    const uint32_t dbar = acce0 + 8u * kPairBufs;
+    const uint32_t scf0 = acce0 + 8u * kPairBufs, sce0 = scf0 + 16u, dbar = sce0 + 16u;
+    float *sc = reinterpret_cast<float *>(base + kPairSc);
     int *slots = reinterpret_cast<int *>(base + kPairSlots);
     volatile int *fail = slots + 1;
     const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
@@ -161,6 +170,10 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
         for (int b = 0; b < kPairBufs; ++b) {
             mbar_init(accf0 + 8u * b, 1);
             mbar_init(acce0 + 8u * b, 2 * kPairEpi);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(scf0 + 8u * b, kPairScaleWarps);
+            mbar_init(sce0 + 8u * b, kPairEpi);
         }
         mbar_init(dbar, 1);
         slots[1] = slots[2] = slots[3] = 0;
@@ -268,6 +281,42 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             if (lane == 0)
                 slots[3] = q;
         }
+    } else if (warp >= 2 + kPairEpi) {
+        // ------------------------------------------------ the rows' scales
+        // sc[chunk % 2][group][row]: half a warp reads 16 groups of a row,
+        // eight rows at a time
+        const int w = warp - 2 - kPairEpi, gl = lane % kPairChunk, rr = lane / kPairChunk;
+        griddep_wait();
+        int c = 0;
+        bool stop = false;
+        for (int t = pair; t < ntiles && !stop; t += npairs) {
+            int m0, n0;
+            pair_tile(p, t, m0, n0);
+            m0 += (int)rank * 128;
+            for (int g0 = 0; g0 < G; g0 += kPairChunk, ++c) {
+                if (c >= 2 &&
+                    !fp8_wait(sce0 + 8u * (c & 1), (uint32_t)((c / 2 - 1) & 1), limit, fail)) {
+                    stop = true;
+                    break;
+                }
+                float *to = sc + (c & 1) * (kPairChunk * kPairScRow) + gl * kPairScRow;
+                const float *from = p.sa + (int64_t)m0 * G + g0 + gl;
+                for (int i0 = w * 64; i0 < w * 64 + 64; i0 += 16) {
+                    float v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = i0 + 2 * j + rr;
+                        v[j] = m0 + r < p.M && g0 + gl < G ? __ldcg(from + (int64_t)r * G) : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        to[i0 + 2 * j + rr] = v[j];
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(scf0 + 8u * (c & 1));
+            }
+        }
     } else {
         // ------------------------------------------------------ the sums
         const int q4 = warp & 3, part = (warp - 2) / 4;
@@ -277,24 +326,34 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
         const int nblocks = (p.N + 127) / 128;
         T *out = static_cast<T *>(p.out);
         griddep_wait();
-        int b = 0, ub = 0;
+        int b = 0, ub = 0, chunk = 0;
         bool stop = false;
         for (int t = pair; t < ntiles && !stop; t += npairs) {
             int m0, n0;
             pair_tile(p, t, m0, n0);
             const int m = m0 + row, n = n0 + col0;
-            const float *sa = p.sa + (int64_t)min(m, p.M - 1) * G;
             const float *sb = p.sb + (int64_t)min(n / 128, nblocks - 1) * G;
             float2 acc[CW / 2];
 #pragma unroll
             for (int i = 0; i < CW / 2; ++i)
                 acc[i] = make_float2(0.f, 0.f);
-            float sa_next = sa[0], sb_next = __ldg(sb);
+            float sb_next = __ldg(sb);
             for (int g = 0; g < G; ++g) {
-                const float s = sa_next * sb_next;
-                if (g + 1 < G) {                        // one group ahead
-                    sa_next = sa[g + 1];
+                const int gl = g % kPairChunk;
+                if (gl == 0 && !fp8_wait(scf0 + 8u * (chunk & 1), (uint32_t)((chunk / 2) & 1), limit,
+                                         fail)) {
+                    stop = true;
+                    break;
+                }
+                const float s = sc[((chunk & 1) * kPairChunk + gl) * kPairScRow + q4 * 32 + lane] *
+                                sb_next;
+                if (g + 1 < G)                          // one group ahead
                     sb_next = __ldg(sb + g + 1);
+                if (gl == kPairChunk - 1 || g + 1 == G) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(sce0 + 8u * (chunk & 1));
+                    ++chunk;
                 }
                 if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), limit, fail)) {
                     stop = true;
