@@ -41,20 +41,23 @@ constexpr int kPairTile = 256;                          // rows of A and of B to
 constexpr int kPairEpi = 16;                            // epilogue warps of a CTA
 constexpr int kPairScaleWarps = 2;                      // warps that fetch the rows' scales
 constexpr int kPairThreads = 64 + 32 * (kPairEpi + kPairScaleWarps);
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
 constexpr uint32_t kPairStage = 2u * kPairHalf;
 constexpr int kPairBufs = 2;                            // x 256 columns: all tensor memory
 constexpr int kPairTileRun = 8;                         // row tiles that are swept together
 constexpr int kPairChunk = 16;                          // groups whose scales come together
 constexpr int kPairScRow = 129;                         // floats a group of them (no conflicts)
-// The ring, two chunks of the rows' scales, the mbarriers (full, empty; accf,
+constexpr uint32_t kPairRowBytes = 64;                  // of a row of out staged at a time
+// The ring, two chunks of the rows' scales, 32 rows of out for each epilogue
+// warp, the mbarriers (full, empty; accf,
 // acce; scales full, empty; drain), eight words. All of an SM's shared memory
 // is taken: no other CTA may wait for tensor memory beside this one.
 constexpr uint32_t kPairSc = kPairStages * kPairStage;
-constexpr uint32_t kPairBar = kPairSc + 2u * kPairChunk * kPairScRow * 4u;
+constexpr uint32_t kPairOut = kPairSc + 2u * kPairChunk * kPairScRow * 4u;
+constexpr uint32_t kPairBar = kPairOut + 32u * kPairRowBytes * kPairEpi;
 constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 5);
-static_assert(kPairBar % 8 == 0, "barriers are 8-byte aligned");
+static_assert(kPairOut % 128 == 0 && kPairBar % 8 == 0, "alignment");
 constexpr uint32_t kPairSmem = 227u * 1024u;
 static_assert(kPairSlots + 32u + 1023u <= kPairSmem, "shared memory of a pair's CTA");
 
@@ -116,14 +119,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 }
 
 // 16 bytes of out from floats: four fp32 or eight 16-bit values.
-template <typename T> __device__ __forceinline__ void store_out16(T *p, const float *f)
+template <typename T> __device__ __forceinline__ uint4 pack_out16(const float *f)
 {
     if constexpr (sizeof(T) == 4)
-        st_row_v4(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                __float_as_uint(f[3])));
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
     else
-        st_row_v4(p, make_uint4(Half16<T>::narrow2(f[0], f[1]), Half16<T>::narrow2(f[2], f[3]),
-                                Half16<T>::narrow2(f[4], f[5]), Half16<T>::narrow2(f[6], f[7])));
+        return make_uint4(Half16<T>::narrow2(f[0], f[1]), Half16<T>::narrow2(f[2], f[3]),
+                          Half16<T>::narrow2(f[4], f[5]), Half16<T>::narrow2(f[6], f[7]));
 }
 
 // Tile t of the sweep: runs of kPairTileRun row tiles, each run over all
@@ -320,7 +323,7 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
     } else {
         // ------------------------------------------------------ the sums
         const int q4 = warp & 3, part = (warp - 2) / 4;
-        const int row = (int)rank * 128 + q4 * 32 + lane, col0 = part * CW;
+        const int col0 = part * CW;
         const uint32_t at0 = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)col0;
         const uint32_t hand_back = cluster_map(acce0, 0);
         const int nblocks = (p.N + 127) / 128;
@@ -331,7 +334,7 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
         for (int t = pair; t < ntiles && !stop; t += npairs) {
             int m0, n0;
             pair_tile(p, t, m0, n0);
-            const int m = m0 + row, n = n0 + col0;
+            const int n = n0 + col0;
             const float *sb = p.sb + (int64_t)min(n / 128, nblocks - 1) * G;
             float2 acc[CW / 2];
 #pragma unroll
@@ -381,24 +384,47 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                     ++ub;
                 }
             }
-            if (stop || m >= p.M)
-                continue;
-            T *to = out + (int64_t)m * p.ldo + n;
-            constexpr int W = 16 / (int)sizeof(T);      // values a 16-byte store
+            if (stop)
+                break;
+            // 64 bytes of each of the warp's 32 rows at a time through shared
+            // memory (16-byte chunk c of row r at c ^ (r / 2) % 4: no
+            // conflicts either way), so that out is written in whole sectors
+            // of consecutive lanes
+            constexpr int W = 16 / (int)sizeof(T), VP = 4 * W;   // values a chunk, a row and pass
+            unsigned char *st = base + kPairOut + (uint32_t)(warp - 2) * 32u * kPairRowBytes;
+            const int mw = m0 + (int)rank * 128 + q4 * 32;       // the warp's first row
 #pragma unroll
-            for (int i = 0; i < CW / W; ++i) {
-                float f[W];
+            for (int c0 = 0; c0 < CW; c0 += VP) {
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    f[j] = j & 1 ? acc[(i * W + j) / 2].y : acc[(i * W + j) / 2].x;
-                if (p.vec && n + (i + 1) * W <= p.N) {
-                    store_out16<T>(to + i * W, f);
-                } else {
+                for (int i = 0; i < 4; ++i) {
+                    float f[W];
 #pragma unroll
                     for (int j = 0; j < W; ++j)
-                        if (n + i * W + j < p.N)
-                            store_out1<T>(to + i * W + j, f[j]);
+                        f[j] = j & 1 ? acc[(c0 + i * W + j) / 2].y : acc[(c0 + i * W + j) / 2].x;
+                    *reinterpret_cast<uint4 *>(st + lane * kPairRowBytes +
+                                               ((i ^ ((lane >> 1) & 3)) << 4)) = pack_out16<T>(f);
                 }
+                __syncwarp();
+                if (p.vec && n + c0 + VP <= p.N) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + lane / 4, c = lane % 4;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            st + r * kPairRowBytes + ((c ^ ((r >> 1) & 3)) << 4));
+                        if (mw + r < p.M)
+                            st_row_v4(out + (int64_t)(mw + r) * p.ldo + n + c0 + c * W, v);
+                    }
+                } else {
+                    for (int i = lane; i < 32 * VP; i += 32) {
+                        const int r = i / VP, e = i % VP;
+                        const T v = *reinterpret_cast<const T *>(
+                            st + r * kPairRowBytes + (((e / W) ^ ((r >> 1) & 3)) << 4) +
+                            (e % W) * sizeof(T));
+                        if (mw + r < p.M && n + c0 + e < p.N)
+                            out[(int64_t)(mw + r) * p.ldo + n + c0 + e] = v;
+                    }
+                }
+                __syncwarp();
             }
         }
     }
