@@ -184,12 +184,30 @@ int launch_gemm(const void *fn, int64_t ctas, int threads, size_t smem, int clus
     return e == cudaSuccess ? RMSNORM_OK : cuda_fail(e);
 }
 
+// Whether the paired kernel was compiled to the registers that its split
+// among the warps draws on (with fewer its wider warps would wait for ever).
+int pair_registers(const void *fn, int dtype)
+{
+    static std::atomic<int> checked[3];
+    if (checked[dtype].load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, fn);
+        if (e != cudaSuccess)
+            return cuda_fail(e);
+        if (fa.numRegs < kPairRegs)
+            return cuda_fail(cudaErrorInvalidConfiguration);
+        checked[dtype].store(1, std::memory_order_relaxed);
+    }
+    return RMSNORM_OK;
+}
+
 // Pairs of CTAs on tiles of 256 x 256 (fp8_gemm_pair.cuh).
 int pair_impl(const Fp8GemmArgs &g, int dev, int64_t tiles_m, int64_t tiles_n, cudaStream_t stream)
 {
     const void *fn = fp8_pair_kernels.fn[g.dtype];
     int pairs, st;
-    if ((st = max_active_clusters(fn, kPairThreads, (int)kPairSmem, 2, dev, &pairs)))
+    if ((st = pair_registers(fn, g.dtype)) ||
+        (st = max_active_clusters(fn, kPairThreads, (int)kPairSmem, 2, dev, &pairs)))
         return st;
     CUtensorMap mapA, mapB;
     if ((st = fp8_map(&mapA, g.a, g.M, g.K, g.lda, 128)) ||

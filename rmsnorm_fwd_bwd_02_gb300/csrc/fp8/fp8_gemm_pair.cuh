@@ -39,8 +39,14 @@ namespace rmsk {
 
 constexpr int kPairTile = 256;                          // rows of A and of B to a pair's tile
 constexpr int kPairEpi = 16;                            // epilogue warps of a CTA
-constexpr int kPairScaleWarps = 2;                      // warps that fetch the rows' scales
-constexpr int kPairThreads = 64 + 32 * (kPairEpi + kPairScaleWarps);
+constexpr int kPairLd = 32;                             // columns a load of tensor memory
+constexpr int kPairScaleWarps = 2;                      // warps that fetch the scales
+constexpr int kPairThreads = 128 + 32 * kPairEpi;
+// Registers a thread: what the kernel is launched with, and what its first
+// four warps (copies, MMAs, scales) and the eight others take of that.
+constexpr int kPairRegs = 96, kPairRegsCtl = 32, kPairRegsEpi = 112;
+static_assert(128 * kPairRegsCtl + 32 * kPairEpi * kPairRegsEpi <= kPairThreads * kPairRegs,
+              "the shares fit what the CTA is launched with");
 constexpr int kPairStages = 5;
 constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
 constexpr uint32_t kPairStage = 2u * kPairHalf;
@@ -49,12 +55,14 @@ constexpr int kPairTileRun = 8;                         // row tiles that are sw
 constexpr int kPairChunk = 16;                          // groups whose scales come together
 constexpr int kPairScRow = 129;                         // floats a group of them (no conflicts)
 constexpr uint32_t kPairRowBytes = 64;                  // of a row of out staged at a time
-// The ring, two chunks of the rows' scales, 32 rows of out for each epilogue
-// warp, the mbarriers (full, empty; accf,
+// The ring, two chunks of scales (for each of the tile's two blocks of columns,
+// group and row their product), 32 rows of out for each epilogue warp, the
+// mbarriers (full, empty; accf,
 // acce; scales full, empty; drain), eight words. All of an SM's shared memory
 // is taken: no other CTA may wait for tensor memory beside this one.
 constexpr uint32_t kPairSc = kPairStages * kPairStage;
-constexpr uint32_t kPairOut = kPairSc + 2u * kPairChunk * kPairScRow * 4u;
+constexpr uint32_t kPairScChunk = 2u * kPairChunk * kPairScRow;   // floats
+constexpr uint32_t kPairOut = kPairSc + 2u * kPairScChunk * 4u;
 constexpr uint32_t kPairBar = kPairOut + 32u * kPairRowBytes * kPairEpi;
 constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 5);
 static_assert(kPairOut % 128 == 0 && kPairBar % 8 == 0, "alignment");
@@ -129,6 +137,35 @@ template <typename T> __device__ __forceinline__ uint4 pack_out16(const float *f
                           Half16<T>::narrow2(f[4], f[5]), Half16<T>::narrow2(f[6], f[7]));
 }
 
+// 32 consecutive fp32 columns of the warp's 32 lanes, as for 16.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(v[30]), "+r"(v[31]));
+}
+
 // Tile t of the sweep: runs of kPairTileRun row tiles, each run over all
 // column tiles, so that the pairs at work at one time share rows of both
 // operands in L2.
@@ -195,6 +232,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
     tc_fence_after_sync();
     const uint32_t tmem = static_cast<uint32_t>(slots[0]);
 
+    if (warp < 4)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsCtl));
     if (warp == 0) {
         // ------------------------------------------------------ copies
         const uint32_t lead = cluster_map(full0, 0);
@@ -284,11 +323,12 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             if (lane == 0)
                 slots[3] = q;
         }
-    } else if (warp >= 2 + kPairEpi) {
-        // ------------------------------------------------ the rows' scales
-        // sc[chunk % 2][group][row]: half a warp reads 16 groups of a row,
-        // eight rows at a time
-        const int w = warp - 2 - kPairEpi, gl = lane % kPairChunk, rr = lane / kPairChunk;
+    } else if (warp < 4) {
+        // ------------------------------------------------------ scales
+        // sc[chunk % 2][block][group][row]: half a warp reads 16 groups of a
+        // row, eight rows at a time
+        const int w = warp - 2, gl = lane % kPairChunk, rr = lane / kPairChunk;
+        const int nblocks = (p.N + 127) / 128;
         griddep_wait();
         int c = 0;
         bool stop = false;
@@ -296,24 +336,30 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             int m0, n0;
             pair_tile(p, t, m0, n0);
             m0 += (int)rank * 128;
+            const float *sb0 = p.sb + (int64_t)(n0 / 128) * G + gl;
+            const float *sb1 = p.sb + (int64_t)min(n0 / 128 + 1, nblocks - 1) * G + gl;
             for (int g0 = 0; g0 < G; g0 += kPairChunk, ++c) {
+                const bool in = g0 + gl < G;
+                const float b0 = in ? __ldg(sb0 + g0) : 0.f, b1 = in ? __ldg(sb1 + g0) : 0.f;
                 if (c >= 2 &&
                     !fp8_wait(sce0 + 8u * (c & 1), (uint32_t)((c / 2 - 1) & 1), limit, fail)) {
                     stop = true;
                     break;
                 }
-                float *to = sc + (c & 1) * (kPairChunk * kPairScRow) + gl * kPairScRow;
+                float *to = sc + (c & 1) * kPairScChunk + gl * kPairScRow;
                 const float *from = p.sa + (int64_t)m0 * G + g0 + gl;
                 for (int i0 = w * 64; i0 < w * 64 + 64; i0 += 16) {
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int r = i0 + 2 * j + rr;
-                        v[j] = m0 + r < p.M && g0 + gl < G ? __ldcg(from + (int64_t)r * G) : 0.f;
+                        v[j] = m0 + r < p.M && in ? __ldcg(from + (int64_t)r * G) : 0.f;
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        to[i0 + 2 * j + rr] = v[j];
+                    for (int j = 0; j < 8; ++j) {
+                        to[i0 + 2 * j + rr] = v[j] * b0;
+                        to[kPairChunk * kPairScRow + i0 + 2 * j + rr] = v[j] * b1;
+                    }
                 }
                 __syncwarp();
                 if (lane == 0)
@@ -322,77 +368,71 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
         }
     } else {
         // ------------------------------------------------------ the sums
-        const int q4 = warp & 3, part = (warp - 2) / 4;
-        const int col0 = part * CW;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsEpi));
+        const int q4 = warp & 3, col0 = (warp - 4) / 4 * CW;
         const uint32_t at0 = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)col0;
         const uint32_t hand_back = cluster_map(acce0, 0);
-        const int nblocks = (p.N + 127) / 128;
+        const float *sc_row = sc + col0 / 128 * (kPairChunk * kPairScRow) + q4 * 32 + lane;
         T *out = static_cast<T *>(p.out);
         griddep_wait();
-        int b = 0, ub = 0, chunk = 0;
+        int q = 0, chunk = 0;                           // groups, chunks of scales so far
         bool stop = false;
         for (int t = pair; t < ntiles && !stop; t += npairs) {
-            int m0, n0;
-            pair_tile(p, t, m0, n0);
-            const int n = n0 + col0;
-            const float *sb = p.sb + (int64_t)min(n / 128, nblocks - 1) * G;
             float2 acc[CW / 2];
 #pragma unroll
             for (int i = 0; i < CW / 2; ++i)
                 acc[i] = make_float2(0.f, 0.f);
-            float sb_next = __ldg(sb);
-            for (int g = 0; g < G; ++g) {
-                const int gl = g % kPairChunk;
-                if (gl == 0 && !fp8_wait(scf0 + 8u * (chunk & 1), (uint32_t)((chunk / 2) & 1), limit,
-                                         fail)) {
+            for (int g0 = 0; g0 < G && !stop; g0 += kPairChunk, ++chunk) {
+                if (!fp8_wait(scf0 + 8u * (chunk & 1), (uint32_t)((chunk / 2) & 1), limit, fail)) {
                     stop = true;
                     break;
                 }
-                const float s = sc[((chunk & 1) * kPairChunk + gl) * kPairScRow + q4 * 32 + lane] *
-                                sb_next;
-                if (g + 1 < G)                          // one group ahead
-                    sb_next = __ldg(sb + g + 1);
-                if (gl == kPairChunk - 1 || g + 1 == G) {
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(sce0 + 8u * (chunk & 1));
-                    ++chunk;
-                }
-                if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), limit, fail)) {
-                    stop = true;
-                    break;
-                }
-                tc_fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < CW; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(at0 + (uint32_t)(b * kPairTile + c), v);
-                    if (c + 16 == CW) {                 // this warp is done with the buffer
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_remote_cta(hand_back + 8u * b);
+                const float *s_at = sc_row + (chunk & 1) * kPairScChunk;
+                const int ng = min(kPairChunk, G - g0);
+                for (int g = 0; g < ng; ++g, ++q, s_at += kPairScRow) {
+                    const float s = *s_at;
+                    const uint32_t b = (uint32_t)q & 1u;
+                    if (!fp8_wait(accf0 + 8u * b, (uint32_t)(q >> 1) & 1u, limit, fail)) {
+                        stop = true;
+                        break;
                     }
+                    tc_fence_after_sync();
+                    const uint32_t at = at0 + b * kPairTile;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[c / 2 + j] = vfma(
-                            make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                            make_float2(s, s), acc[c / 2 + j]);
+                    for (int c = 0; c < CW; c += kPairLd) {
+                        uint32_t w[kPairLd];
+                        tmem_ld_start(at + (uint32_t)c, w);
+                        tmem_wait(w);
+                        if (c + kPairLd == CW) {        // this warp is done with the buffer
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive_remote_cta(hand_back + 8u * b);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kPairLd / 2; ++j)
+                            acc[c / 2 + j] =
+                                vfma(make_float2(__uint_as_float(w[2 * j]),
+                                                 __uint_as_float(w[2 * j + 1])),
+                                     make_float2(s, s), acc[c / 2 + j]);
+                    }
                 }
-                if (++b == kPairBufs) {
-                    b = 0;
-                    ++ub;
-                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(sce0 + 8u * (chunk & 1));
             }
             if (stop)
                 break;
+            int m0, n0;
+            pair_tile(p, t, m0, n0);
             // 64 bytes of each of the warp's 32 rows at a time through shared
             // memory (16-byte chunk c of row r at c ^ (r / 2) % 4: no
             // conflicts either way), so that out is written in whole sectors
             // of consecutive lanes
             constexpr int W = 16 / (int)sizeof(T), VP = 4 * W;   // values a chunk, a row and pass
-            unsigned char *st = base + kPairOut + (uint32_t)(warp - 2) * 32u * kPairRowBytes;
+            unsigned char *st = base + kPairOut + (uint32_t)(warp - 4) * 32u * kPairRowBytes;
             const int mw = m0 + (int)rank * 128 + q4 * 32;       // the warp's first row
+            const int n = n0 + col0;
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += VP) {
 #pragma unroll
