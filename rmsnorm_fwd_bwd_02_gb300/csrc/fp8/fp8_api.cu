@@ -140,31 +140,38 @@ struct Fp8GemmArgs {
     int G() const { return (int)((K + kFp8Group - 1) / kFp8Group); }
 };
 
-// [rows][K] bytes, 128-byte swizzle, reads past the end zero: boxes of
-// `box_rows` rows x 128 columns.
-int fp8_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int64_t ld, int box_rows)
+// A [rows][cols] tensor of `es`-byte elements (row stride ld elements) in
+// boxes of box_rows x box_cols; reads past the end are zero, stores left out.
+int fp8_map(CUtensorMap *map, const void *base, size_t es, int64_t rows, int64_t cols, int64_t ld,
+            int box_rows, int box_cols, CUtensorMapSwizzle swizzle)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr)
         return RMSNORM_ERR_UNSUPPORTED;
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {(cuuint32_t)kFp8Group, (cuuint32_t)box_rows};
+    const CUtensorMapDataType type = es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    if (encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    if (encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cuda_fail(cudaErrorInvalidValue);
     return RMSNORM_OK;
 }
 
-int launch_gemm(const void *fn, int64_t ctas, int threads, size_t smem, int cluster,
-                cudaStream_t stream, void *params, CUtensorMap *map0, CUtensorMap *map1, int dev)
+// An operand of the product: boxes of one group of columns, 128-byte swizzle.
+int fp8_operand_map(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int64_t ld,
+                    int box_rows)
 {
-    unsigned int *tmo = stream_timeout_counter(dev);
-    if (tmo == nullptr)
-        return cuda_fail(cudaErrorInvalidSymbol);
+    return fp8_map(map, base, 1, rows, K, ld, box_rows, kFp8Group, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int launch_gemm(const void *fn, int64_t ctas, int threads, size_t smem, int cluster,
+                cudaStream_t stream, void **args)
+{
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
@@ -179,7 +186,6 @@ int launch_gemm(const void *fn, int64_t ctas, int threads, size_t smem, int clus
     attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    void *args[4] = {params, map0, map1, &tmo};
     const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     return e == cudaSuccess ? RMSNORM_OK : cuda_fail(e);
 }
@@ -209,19 +215,26 @@ int pair_impl(const Fp8GemmArgs &g, int dev, int64_t tiles_m, int64_t tiles_n, c
     if ((st = pair_registers(fn, g.dtype)) ||
         (st = max_active_clusters(fn, kPairThreads, (int)kPairSmem, 2, dev, &pairs)))
         return st;
-    CUtensorMap mapA, mapB;
-    if ((st = fp8_map(&mapA, g.a, g.M, g.K, g.lda, 128)) ||
-        (st = fp8_map(&mapB, g.b, g.N, g.K, g.ldb, 128)))
-        return st;
     const size_t es = elem_size(g.dtype);
+    const bool vec = aligned(g.out, 16) && g.ldo * (int64_t)es % 16 == 0;
+    CUtensorMap mapA, mapB, mapO = {};
+    unsigned int *tmo = stream_timeout_counter(dev);
+    if (tmo == nullptr)
+        return cuda_fail(cudaErrorInvalidSymbol);
+    if ((st = fp8_operand_map(&mapA, g.a, g.M, g.K, g.lda, 128)) ||
+        (st = fp8_operand_map(&mapB, g.b, g.N, g.K, g.ldb, 128)) ||
+        (vec && (st = fp8_map(&mapO, g.out, es, g.M, g.N, g.ldo, 32, (int)(kPairRowBytes / es),
+                              CU_TENSOR_MAP_SWIZZLE_64B))))
+        return st;
     Fp8PairParams p = {g.sa, g.sb, g.out, g.ldo, (int)g.M, (int)g.N, g.G(), (int)tiles_m,
                        (int)tiles_n,
                        umma_idesc_f8((uint32_t)g.at, (uint32_t)g.bt, kPairTile, kPairTile),
-                       g.static_w, aligned(g.out, 16) && g.ldo * es % 16 == 0 ? 1 : 0,
+                       g.static_w, vec ? (g.N * (int64_t)es % 16 == 0 ? 2 : 1) : 0,
                        g_test_extra_tx.load(std::memory_order_relaxed),
                        g_test_wait_us.load(std::memory_order_relaxed)};
+    void *args[5] = {&p, &mapA, &mapB, &mapO, &tmo};
     if ((st = launch_gemm(fn, 2 * std::min<int64_t>(pairs, tiles_m * tiles_n), kPairThreads, kPairSmem,
-                          2, stream, &p, &mapA, &mapB, dev)))
+                          2, stream, args)))
         return st;
     t_last_path = kPathFp8Pair;
     return RMSNORM_OK;
@@ -279,8 +292,11 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
     if (ctas > INT32_MAX)
         return RMSNORM_ERR_UNSUPPORTED;
     CUtensorMap mapA, mapB;
-    if ((st = fp8_map(&mapA, g.a, M, g.K, g.lda, swap ? BN : kFp8TileR)) ||
-        (st = fp8_map(&mapB, g.b, N, g.K, g.ldb, swap ? kFp8TileR : BN)))
+    unsigned int *tmo = stream_timeout_counter(dev);
+    if (tmo == nullptr)
+        return cuda_fail(cudaErrorInvalidSymbol);
+    if ((st = fp8_operand_map(&mapA, g.a, M, g.K, g.lda, swap ? BN : kFp8TileR)) ||
+        (st = fp8_operand_map(&mapB, g.b, N, g.K, g.ldb, swap ? kFp8TileR : BN)))
         return st;
     const void *fn = fp8_gemm_kernels.fn[v][g.dtype];
     const size_t es = elem_size(g.dtype);
@@ -290,9 +306,9 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
                        g.static_w, aligned(g.out, 4 * es) && g.ldo % 4 == 0 ? 1 : 0,
                        g_test_extra_tx.load(std::memory_order_relaxed),
                        g_test_wait_us.load(std::memory_order_relaxed), L};
+    void *args[4] = {&p, swap ? &mapB : &mapA, swap ? &mapA : &mapB, &tmo};
     if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)) ||
-        (st = launch_gemm(fn, ctas, fp8_gemm_threads(BN), L.total, KS, stream, &p,
-                          swap ? &mapB : &mapA, swap ? &mapA : &mapB, dev)))
+        (st = launch_gemm(fn, ctas, fp8_gemm_threads(BN), L.total, KS, stream, args)))
         return st;
     t_last_path = kPathFp8Gemm;
     return RMSNORM_OK;

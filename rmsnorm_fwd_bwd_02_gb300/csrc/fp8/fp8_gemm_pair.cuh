@@ -47,7 +47,7 @@ constexpr int kPairThreads = 128 + 32 * kPairEpi;
 constexpr int kPairRegs = 96, kPairRegsCtl = 32, kPairRegsEpi = 112;
 static_assert(128 * kPairRegsCtl + 32 * kPairEpi * kPairRegsEpi <= kPairThreads * kPairRegs,
               "the shares fit what the CTA is launched with");
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 4;
 constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
 constexpr uint32_t kPairStage = 2u * kPairHalf;
 constexpr int kPairBufs = 2;                            // x 256 columns: all tensor memory
@@ -55,17 +55,18 @@ constexpr int kPairTileRun = 8;                         // row tiles that are sw
 constexpr int kPairChunk = 16;                          // groups whose scales come together
 constexpr int kPairScRow = 129;                         // floats a group of them (no conflicts)
 constexpr uint32_t kPairRowBytes = 64;                  // of a row of out staged at a time
-// The ring, two chunks of scales (for each of the tile's two blocks of columns,
-// group and row their product), 32 rows of out for each epilogue warp, the
-// mbarriers (full, empty; accf,
-// acce; scales full, empty; drain), eight words. All of an SM's shared memory
-// is taken: no other CTA may wait for tensor memory beside this one.
-constexpr uint32_t kPairSc = kPairStages * kPairStage;
+// The ring, two times 32 rows of out for each epilogue warp, two chunks of
+// scales (for each of the tile's two blocks of columns, group and row their
+// product), the mbarriers (full, empty; accf, acce; scales full, empty;
+// drain), eight words. All of an SM's shared memory is taken: no other CTA may
+// wait for tensor memory beside this one.
+constexpr uint32_t kPairOut = kPairStages * kPairStage;
+constexpr uint32_t kPairOutSlot = 32u * kPairRowBytes;
+constexpr uint32_t kPairSc = kPairOut + 2u * kPairOutSlot * kPairEpi;
 constexpr uint32_t kPairScChunk = 2u * kPairChunk * kPairScRow;   // floats
-constexpr uint32_t kPairOut = kPairSc + 2u * kPairScChunk * 4u;
-constexpr uint32_t kPairBar = kPairOut + 32u * kPairRowBytes * kPairEpi;
+constexpr uint32_t kPairBar = kPairSc + 2u * kPairScChunk * 4u;
+static_assert(kPairOut % 512 == 0 && kPairOutSlot % 512 == 0 && kPairBar % 8 == 0, "alignment");
 constexpr uint32_t kPairSlots = kPairBar + 8u * (2 * kPairStages + 2 * kPairBufs + 5);
-static_assert(kPairOut % 128 == 0 && kPairBar % 8 == 0, "alignment");
 constexpr uint32_t kPairSmem = 227u * 1024u;
 static_assert(kPairSlots + 32u + 1023u <= kPairSmem, "shared memory of a pair's CTA");
 
@@ -78,7 +79,7 @@ struct Fp8PairParams {
     int tiles_m, tiles_n;
     uint32_t idesc;
     int static_w;
-    int vec;           // rows of out start at multiples of 16 bytes
+    int vec;           // rows of out start at multiples of 16 bytes (1), end there too (2)
     uint32_t extra_tx, wait_limit_us;
 };
 
@@ -182,7 +183,8 @@ __device__ __forceinline__ void pair_tile(const Fp8PairParams &p, int t, int &m0
 template <typename T>
 __global__ void __launch_bounds__(kPairThreads, 1)
 rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA,
-                  const __grid_constant__ CUtensorMap tmB, unsigned int *timeouts)
+                  const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmO, unsigned int *timeouts)
 {
     constexpr int CW = kPairTile * 4 / kPairEpi;        // columns a thread sums
     extern __shared__ __align__(1024) unsigned char pair_smem[];
@@ -425,16 +427,24 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                 break;
             int m0, n0;
             pair_tile(p, t, m0, n0);
-            // 64 bytes of each of the warp's 32 rows at a time through shared
-            // memory (16-byte chunk c of row r at c ^ (r / 2) % 4: no
-            // conflicts either way), so that out is written in whole sectors
-            // of consecutive lanes
+            // out goes through shared memory, 64 bytes of each of the warp's
+            // 32 rows a pass, two passes' room in turn: 16-byte chunk c of row
+            // r at c ^ (r / 2) % 4 (no conflicts; a tensor copy's 64-byte
+            // swizzle), then by one tensor copy, which leaves out what lies
+            // past M or N, while the warp goes on
             constexpr int W = 16 / (int)sizeof(T), VP = 4 * W;   // values a chunk, a row and pass
-            unsigned char *st = base + kPairOut + (uint32_t)(warp - 4) * 32u * kPairRowBytes;
             const int mw = m0 + (int)rank * 128 + q4 * 32;       // the warp's first row
             const int n = n0 + col0;
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += VP) {
+                unsigned char *st =
+                    base + kPairOut + (uint32_t)((warp - 4) * 2 + (c0 / VP & 1)) * kPairOutSlot;
+                if (lane == 0)                          // the copy before the last has read it
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+                // a copy leaves out whole 16-byte pieces past N: a row of out
+                // that ends inside one is written element by element there
+                const bool copy = p.vec == 2 || (p.vec == 1 && n + c0 + VP <= p.N);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float f[W];
@@ -444,17 +454,19 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                     *reinterpret_cast<uint4 *>(st + lane * kPairRowBytes +
                                                ((i ^ ((lane >> 1) & 3)) << 4)) = pack_out16<T>(f);
                 }
-                __syncwarp();
-                if (p.vec && n + c0 + VP <= p.N) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + lane / 4, c = lane % 4;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            st + r * kPairRowBytes + ((c ^ ((r >> 1) & 3)) << 4));
-                        if (mw + r < p.M)
-                            st_row_v4(out + (int64_t)(mw + r) * p.ldo + n + c0 + c * W, v);
+                if (copy) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && mw < p.M && n + c0 < p.N) {
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group "
+                                     "[%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(&tmO)),
+                                     "r"(n + c0), "r"(mw), "r"(smem_addr(st))
+                                     : "memory");
                     }
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 } else {
+                    __syncwarp();
                     for (int i = lane; i < 32 * VP; i += 32) {
                         const int r = i / VP, e = i % VP;
                         const T v = *reinterpret_cast<const T *>(
@@ -463,10 +475,13 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                         if (mw + r < p.M && n + c0 + e < p.N)
                             out[(int64_t)(mw + r) * p.ldo + n + c0 + e] = v;
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
+        if (lane == 0)                                  // out is written
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 
     // every role has finished or given up
