@@ -16,6 +16,7 @@ using namespace rmsk;
 
 namespace {
 
+constexpr uint32_t kFp8MaxSmem = 227 * 1024, kFp8HalfSmem = 113 * 1024;
 constexpr int kPathFp8Rows = 9, kPathFp8Blocks = 10, kPathFp8Gemm = 11,
               kPathFp8Pair = 12;
 
@@ -244,15 +245,21 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
 {
     static const int kBN[4] = {16, 32, 64, 128};
     const int64_t M = g.M, N = g.N;
+    const int G = g.G();
     int dev, sms, bps, st;
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
         return st;
+    // Pairs of CTAs where tiles of 128 x 128 would not all run at once and
+    // a pair's tile of 256 rows is not half empty. Measured (GB300, K = 4096,
+    // tile kernel / pairs): 256 x 6144 15 / 18 us, 256 x 12288 31 / 19 us,
+    // 128 x 24576 32 / 34 us, 1024 x 1024 12 / 18 us, 1024 x 4096 31 / 19 us,
+    // 2048 x 24576 319 / 158 us.
     const int64_t tm = (M + kPairTile - 1) / kPairTile, tn = (N + kPairTile - 1) / kPairTile;
+    const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128);
     const int ov = g_test_gemm_fp8.load(std::memory_order_relaxed);
-    const bool fits = tm * tn * g.G() < INT32_MAX;
-    if (fits && (ov == kPathFp8Pair || (ov != kPathFp8Gemm && tm * tn >= sms / 2)))
+    const bool fits = tm * tn * G < INT32_MAX;
+    if (fits && (ov == kPathFp8Pair || (ov != kPathFp8Gemm && M > 128 && t128 > sms)))
         return pair_impl(g, dev, tm, tn, stream);
-    const int G = g.G();
     // the narrowest column operand that holds the tokens, whose scales must
     // fit in shared memory; else tokens in tiles of 128 rows
     int v = 0;
@@ -266,11 +273,14 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
             continue;
         tiles_r = ((swap ? N : M) + kFp8TileR - 1) / kFp8TileR;
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
-        // the largest cluster with which the whole grid runs at once
+        // The largest cluster with which the whole grid runs at once (a few
+        // late clusters cost as much as all the others: 64 x 6144 x 4096 with
+        // three CTAs a cluster, of which 47 run at once, 21 us, with two 12),
+        // with a ring of up to six stages.
         for (KS = std::min(kFp8MaxCluster, G); KS >= 1; --KS) {
             const int ng = (G + KS - 1) / KS;
             L = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
-            if (L.total > 227u * 1024u)
+            if (L.total > kFp8MaxSmem)
                 continue;
             int n;
             if ((st = max_active_clusters(fp8_gemm_kernels.fn[v][g.dtype], fp8_gemm_threads(BN),
@@ -280,10 +290,17 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
                 break;
         }
         if (KS < 1) {
+            // more tiles than run at once: a tile a CTA, two CTAs an SM (one
+            // starts while the other ends) with the ring that this leaves
             KS = 1;
-            L = fp8_gemm_layout(BN, swap, std::min(G, 6), G);
+            int stages = std::min(G, 6);
+            do
+                L = fp8_gemm_layout(BN, swap, stages, G);
+            while (L.total > kFp8HalfSmem && --stages >= 3);
+            if (stages < 3)
+                L = fp8_gemm_layout(BN, swap, std::min(G, 3), G);
         }
-        if (!swap || L.total <= 227u * 1024u)
+        if (!swap || L.total <= kFp8MaxSmem)
             break;
     }
     const bool swap = v < 3;

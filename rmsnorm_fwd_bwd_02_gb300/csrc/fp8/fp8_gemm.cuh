@@ -72,8 +72,9 @@ __host__ __device__ inline Fp8GemmLayout fp8_gemm_layout(int BN, bool swap, int 
     // An SM has 512 columns of tensor memory. A CTA that waits for its
     // columns while a peer of its cluster holds some elsewhere could wait
     // for ever, so no more CTAs may share an SM than have columns: each
-    // takes at least its share of the SM's 228 KB of shared memory.
-    const uint32_t least = 228u * 1024u / 512u * (uint32_t)fp8_tmem_cols(BN);
+    // takes at least its share of the SM's 228 KB of shared memory (1 KB of
+    // it the system's own).
+    const uint32_t least = 228u * 1024u / 512u * (uint32_t)fp8_tmem_cols(BN) - 1024u;
     if (L.total < least)
         L.total = least;
     return L;
@@ -127,22 +128,28 @@ __device__ __forceinline__ bool elect_one()
 
 // Bounded wait of a whole warp, as tc_wait, but the clock is only read once
 // in a while (each try already blocks for a time of the hardware's choice).
-__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, unsigned long long limit,
-                                         volatile int *fail)
+// `fail` is the flag's shared address; the limit is worked out only where it
+// is needed (both to spare the loops' registers).
+__device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, uint32_t limit_us,
+                                         uint32_t fail)
 {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+        return true;
     unsigned long long t0 = 0;
-    for (int i = 0;; ++i) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
-            return true;
-        if ((i & 31) == 31) {
-            const unsigned long long t = global_ns();
-            if (t0 == 0)
-                t0 = t;
-            const bool stop = *fail || t - t0 > limit;
-            if (__any_sync(0xFFFFFFFFu, stop)) {
-                *fail = 1;
-                return false;
-            }
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+                return true;
+        int failed;
+        asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(failed) : "r"(fail) : "memory");
+        const unsigned long long t = global_ns();
+        if (t0 == 0)
+            t0 = t;
+        const bool stop = failed != 0 || t - t0 > wait_limit_ns(limit_us);
+        if (__any_sync(0xFFFFFFFFu, stop)) {
+            asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(fail), "r"(1) : "memory");
+            return false;
         }
     }
 }
@@ -229,7 +236,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
     const uint32_t dbar = acce0 + 8u * NB;
     int *slots = reinterpret_cast<int *>(base + L.slots);
     volatile int *fail = slots + 1;
-    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+    const uint32_t fail_s = smem_addr(slots + 1);
 
     if (warp == 0) {
         tmem_alloc(smem_addr(slots), kCols);
@@ -277,7 +284,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         for (int s = 0, u = 0; q < ng; ++q) {
             const uint32_t dst = ring_s + (uint32_t)s * L.stage, bar = full0 + 8u * s;
             const int x = (g0 + q) * kFp8Group;
-            if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail))
+            if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), p.wait_limit_us, fail_s))
                 break;
             if (elect_one()) {
                 if (q >= early) {
@@ -299,9 +306,9 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         const uint64_t dr0 = umma_desc_sw128(ring_s);
         int q = 0;
         for (int s = 0, us = 0, b = 0, ub = 0; q < ng; ++q) {
-            if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), limit, fail))
+            if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), p.wait_limit_us, fail_s))
                 break;
-            if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), limit, fail))
+            if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), p.wait_limit_us, fail_s))
                 break;
             tc_fence_after_sync();
             if (elect_one()) {
@@ -372,7 +379,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
                     sb_next = __ldg(sb + q + 1);
                 }
             }
-            if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), limit, fail))
+            if (!fp8_wait(accf0 + 8u * b, (uint32_t)(ub & 1), p.wait_limit_us, fail_s))
                 break;
             tc_fence_after_sync();
             const uint32_t at = tmem + lanes + (uint32_t)(b * BN + col0);
@@ -428,6 +435,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         __syncthreads();
     }
     if (*fail) {
+        const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
         if (tid == 0) {
             for (int q = slots[3]; q < slots[2]; ++q)
                 (void)mbar_wait_bounded(full0 + 8u * (q % NSt), (uint32_t)((q / NSt) & 1), limit);

@@ -201,8 +201,7 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
     const uint32_t scf0 = acce0 + 8u * kPairBufs, sce0 = scf0 + 16u, dbar = sce0 + 16u;
     float *sc = reinterpret_cast<float *>(base + kPairSc);
     int *slots = reinterpret_cast<int *>(base + kPairSlots);
-    volatile int *fail = slots + 1;
-    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+    const uint32_t fail_s = smem_addr(slots + 1);
 
     if (tid == 32) {
         for (int s = 0; s < kPairStages; ++s) {
@@ -266,7 +265,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                     griddep_wait();
                     waited = true;
                 }
-                if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), limit, fail)) {
+                if (u > 0 && !fp8_wait(empty0 + 8u * s, (uint32_t)((u - 1) & 1), p.wait_limit_us,
+                                       fail_s)) {
                     stop = true;
                     break;
                 }
@@ -297,9 +297,9 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             int q = 0, s = 0, us = 0, b = 0, ub = 0;
             const int nq = (ntiles - pair + npairs - 1) / npairs * G;
             for (; q < nq; ++q) {
-                if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), limit, fail))
+                if (ub > 0 && !fp8_wait(acce0 + 8u * b, (uint32_t)((ub - 1) & 1), p.wait_limit_us, fail_s))
                     break;
-                if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), limit, fail))
+                if (!fp8_wait(full0 + 8u * s, (uint32_t)(us & 1), p.wait_limit_us, fail_s))
                     break;
                 tc_fence_after_sync();
                 if (elect_one()) {
@@ -344,7 +344,7 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                 const bool in = g0 + gl < G;
                 const float b0 = in ? __ldg(sb0 + g0) : 0.f, b1 = in ? __ldg(sb1 + g0) : 0.f;
                 if (c >= 2 &&
-                    !fp8_wait(sce0 + 8u * (c & 1), (uint32_t)((c / 2 - 1) & 1), limit, fail)) {
+                    !fp8_wait(sce0 + 8u * (c & 1), (uint32_t)((c / 2 - 1) & 1), p.wait_limit_us, fail_s)) {
                     stop = true;
                     break;
                 }
@@ -374,7 +374,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
         const int q4 = warp & 3, col0 = (warp - 4) / 4 * CW;
         const uint32_t at0 = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)col0;
         const uint32_t hand_back = cluster_map(acce0, 0);
-        const float *sc_row = sc + col0 / 128 * (kPairChunk * kPairScRow) + q4 * 32 + lane;
+        const uint32_t sc_row =
+            ring_s + kPairSc + 4u * (uint32_t)(col0 / 128 * (kPairChunk * kPairScRow) + q4 * 32 + lane);
         T *out = static_cast<T *>(p.out);
         griddep_wait();
         int q = 0, chunk = 0;                           // groups, chunks of scales so far
@@ -385,16 +386,17 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             for (int i = 0; i < CW / 2; ++i)
                 acc[i] = make_float2(0.f, 0.f);
             for (int g0 = 0; g0 < G && !stop; g0 += kPairChunk, ++chunk) {
-                if (!fp8_wait(scf0 + 8u * (chunk & 1), (uint32_t)((chunk / 2) & 1), limit, fail)) {
+                if (!fp8_wait(scf0 + 8u * (chunk & 1), (uint32_t)((chunk / 2) & 1), p.wait_limit_us, fail_s)) {
                     stop = true;
                     break;
                 }
-                const float *s_at = sc_row + (chunk & 1) * kPairScChunk;
+                uint32_t s_at = sc_row + (uint32_t)(chunk & 1) * (kPairScChunk * 4u);
                 const int ng = min(kPairChunk, G - g0);
-                for (int g = 0; g < ng; ++g, ++q, s_at += kPairScRow) {
-                    const float s = *s_at;
+                for (int g = 0; g < ng; ++g, ++q, s_at += kPairScRow * 4u) {
+                    float s;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(s_at) : "memory");
                     const uint32_t b = (uint32_t)q & 1u;
-                    if (!fp8_wait(accf0 + 8u * b, (uint32_t)(q >> 1) & 1u, limit, fail)) {
+                    if (!fp8_wait(accf0 + 8u * b, (uint32_t)(q >> 1) & 1u, p.wait_limit_us, fail_s)) {
                         stop = true;
                         break;
                     }
@@ -437,8 +439,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
             const int n = n0 + col0;
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += VP) {
-                unsigned char *st =
-                    base + kPairOut + (uint32_t)((warp - 4) * 2 + (c0 / VP & 1)) * kPairOutSlot;
+                const uint32_t off =
+                    kPairOut + (uint32_t)((warp - 4) * 2 + (c0 / VP & 1)) * kPairOutSlot;
                 if (lane == 0)                          // the copy before the last has read it
                     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
@@ -451,8 +453,12 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
 #pragma unroll
                     for (int j = 0; j < W; ++j)
                         f[j] = j & 1 ? acc[(c0 + i * W + j) / 2].y : acc[(c0 + i * W + j) / 2].x;
-                    *reinterpret_cast<uint4 *>(st + lane * kPairRowBytes +
-                                               ((i ^ ((lane >> 1) & 3)) << 4)) = pack_out16<T>(f);
+                    const uint4 u = pack_out16<T>(f);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     ring_s + off + (uint32_t)lane * kPairRowBytes +
+                                     (uint32_t)((i ^ ((lane >> 1) & 3)) << 4)),
+                                 "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+                                 : "memory");
                 }
                 if (copy) {
                     fence_proxy_async_smem();
@@ -460,13 +466,14 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                     if (lane == 0 && mw < p.M && n + c0 < p.N) {
                         asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group "
                                      "[%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(&tmO)),
-                                     "r"(n + c0), "r"(mw), "r"(smem_addr(st))
+                                     "r"(n + c0), "r"(mw), "r"(ring_s + off)
                                      : "memory");
                     }
                     if (lane == 0)
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 } else {
                     __syncwarp();
+                    const unsigned char *st = base + off;
                     for (int i = lane; i < 32 * VP; i += 32) {
                         const int r = i / VP, e = i % VP;
                         const T v = *reinterpret_cast<const T *>(
@@ -488,8 +495,8 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
     __syncthreads();
     cluster_arrive_release();
     cluster_wait_acquire();
-    int bad = *fail;
-    if (tid == 0 && bad)
+    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+    if (tid == 0 && *reinterpret_cast<volatile int *>(slots + 1))
         atomicAdd(timeouts, 1u);
     if (rank == 0 && warp == 1) {
         // copies of either CTA that no MMA consumed, and the MMAs themselves.
