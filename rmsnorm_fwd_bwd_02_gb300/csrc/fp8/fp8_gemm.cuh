@@ -206,6 +206,38 @@ template <typename T> __device__ __forceinline__ void store_out4(T *p, float4 v)
                      : "memory");
 }
 
+// Quad u of the tile at (r0, c0) to out: with SWAP four tokens of a feature,
+// neighbouring quads neighbouring features, else four features of a token.
+template <typename T, bool SWAP>
+__device__ __forceinline__ void fp8_store_quad(const Fp8GemmParams &p, int r0, int c0, int nc, int u,
+                                               float4 v)
+{
+    T *out = static_cast<T *>(p.out);
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (SWAP) {
+        const int n = r0 + u % kFp8TileR, m = c0 + u / kFp8TileR * 4;
+        if (n < p.N) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (m + j < p.M)
+                    store_out1<T>(out + (int64_t)(m + j) * p.ldo + n, e[j]);
+        }
+    } else {
+        const int m = r0 + u / nc, n = c0 + u % nc * 4;
+        if (m < p.M) {
+            T *to = out + (int64_t)m * p.ldo + n;
+            if (p.vec && n + 4 <= p.N) {
+                store_out4<T>(to, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.N)
+                        store_out1<T>(to + j, e[j]);
+            }
+        }
+    }
+}
+
 // grid = tiles x KS CTAs (KS consecutive ones a cluster); the tiles along the
 // row operand follow one another.
 template <typename T, int BN, bool SWAP>
@@ -445,64 +477,66 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
             umma_commit(dbar);
             (void)mbar_wait_bounded(dbar, 0, limit);
         }
-    } else if (warp >= 2) {
+    } else {
         // this CTA's part of the tile, four columns at a time, the sums of
-        // its peers added in rank order
-        const int etid = tid - 64;
+        // its peers added in rank order. A round trip to a peer takes 0.4 us,
+        // so a thread asks for eight quads at a time: four units from two
+        // peers, or (clusters of more than two) two units from four.
         const int nc = SWAP ? (min(BN, p.M - c0) + 3) / 4 : BN / 4;   // column quads wanted
         const int units = kFp8TileR * nc;
         const int u0 = rank * units / KS, u1 = (rank + 1) * units / KS;
-        const uint32_t sums_s = ring_s;
-        T *out = static_cast<T *>(p.out);
-        for (int u = u0 + etid; u < u1; u += EW * 32) {
-            const int row = SWAP ? u % kFp8TileR : u / nc, c4 = SWAP ? u / kFp8TileR : u % nc;
-            const uint32_t at = (uint32_t)(row * SROW + c4 * 4) * 4u;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (KS == 1) {
-                v = *reinterpret_cast<const float4 *>(base + at);
-            } else {
-                float4 w[kFp8MaxCluster];           // all loads, then the sum in rank order
+        auto sum = [&](auto units_at_once, auto peers_at_once) {
+            constexpr int UB = decltype(units_at_once)::value, PB = decltype(peers_at_once)::value;
+            constexpr int kThreads = fp8_gemm_threads(BN);
+            for (int ub = u0 + tid; ub < u1; ub += UB * kThreads) {
+                uint32_t at[UB];
+                float4 v[UB];
 #pragma unroll
-                for (int k = 0; k < kFp8MaxCluster; ++k)
-                    if (k < KS)
-                        w[k] = ld_cluster_v4(cluster_map(sums_s + at, (uint32_t)k));
-#pragma unroll
-                for (int k = 0; k < kFp8MaxCluster; ++k)
-                    if (k < KS) {
-                        v.x += w[k].x;
-                        v.y += w[k].y;
-                        v.z += w[k].z;
-                        v.w += w[k].w;
-                    }
-            }
-            const float e[4] = {v.x, v.y, v.z, v.w};
-            if constexpr (SWAP) {                       // row: a feature, columns: tokens
-                const int n = r0 + row;
-                if (n < p.N) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c0 + c4 * 4 + j < p.M)
-                            store_out1<T>(out + (int64_t)(c0 + c4 * 4 + j) * p.ldo + n, e[j]);
+                for (int i = 0; i < UB; ++i) {
+                    const int u = min(ub + i * kThreads, u1 - 1);
+                    const int row = SWAP ? u % kFp8TileR : u / nc;
+                    const int c4 = SWAP ? u / kFp8TileR : u % nc;
+                    at[i] = (uint32_t)(row * SROW + c4 * 4) * 4u;
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-            } else {
-                const int m = r0 + row, n = c0 + c4 * 4;
-                if (m < p.M) {
-                    T *to = out + (int64_t)m * p.ldo + n;
-                    if (p.vec && n + 4 <= p.N) {
-                        store_out4<T>(to, v);
-                    } else {
+                for (int k0 = 0; k0 < KS; k0 += PB) {
+                    float4 w[UB][PB];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (n + j < p.N)
-                                store_out1<T>(to + j, e[j]);
+                    for (int k = 0; k < PB; ++k) {
+                        if (k0 + k >= KS)
+                            break;
+                        const uint32_t peer =
+                            KS > 1 ? cluster_map(ring_s, (uint32_t)(k0 + k)) : ring_s;
+#pragma unroll
+                        for (int i = 0; i < UB; ++i)
+                            w[i][k] = KS > 1 ? ld_cluster_v4(peer + at[i])
+                                             : *reinterpret_cast<const float4 *>(base + at[i]);
                     }
+#pragma unroll
+                    for (int k = 0; k < PB; ++k)
+#pragma unroll
+                        for (int i = 0; i < UB; ++i)
+                            if (k0 + k < KS) {
+                                v[i].x += w[i][k].x;
+                                v[i].y += w[i][k].y;
+                                v[i].z += w[i][k].z;
+                                v[i].w += w[i][k].w;
+                            }
                 }
+#pragma unroll
+                for (int i = 0; i < UB; ++i)
+                    if (ub + i * kThreads < u1)
+                        fp8_store_quad<T, SWAP>(p, r0, c0, nc, ub + i * kThreads, v[i]);
             }
-        }
+        };
+        if (KS <= 2)
+            sum(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+        else
+            sum(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
     }
     tc_fence_before_sync();
-    if (KS > 1) {               // no CTA leaves while a peer may still read its sums
-        cluster_arrive_release();
+    if (KS > 1) {               // no CTA leaves while a peer may still read its sums (what this
+        cluster_arrive_relaxed();   // one read it has used; its stores need not be waited for)
         cluster_wait_acquire();
     } else {
         __syncthreads();
