@@ -8,6 +8,8 @@ CUDA kernels. If the library has not been built this module raises at load
 time; there is no fallback.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -429,64 +431,39 @@ FP8_MAX_K, FP8_MAX_ROWS = 1 << 24, 1 << 30
 GEMM_FP8_STATIC_WEIGHTS = 1
 
 
-# The 8-bit calls of a decode step run for a few microseconds on the GPU, so
-# their bindings are kept lean: one check a tensor, the current stream's handle
-# straight from torch (its stream object and context manager take 2 and 6 us
-# on a Grace core), and nothing allocated but the outputs.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The 8-bit calls of a decode step run for 2 to 4 us on the GPU. Their checks,
+# output allocation and marshalling are in a small C++ module over the C ABI
+# (csrc/fp8/fp8_torch.cpp); in Python they took 13 to 18 us a call.
+FP8_LIB_PATH = os.path.join(PKG, "_fp8_torch.so")
+_fp8_mod = None
 
 
-def _fp8_code(name, dtype):
-    code = FP8_TYPES.get(dtype)
-    if code is None:
-        raise ValueError(f"{name} must be one of {sorted(map(str, FP8_TYPES))}, got {dtype}")
-    return code
+def _fp8():
+    """The loaded binding of the 8-bit calls (raises if it was not built)."""
+    global _fp8_mod
+    if _fp8_mod is None:
+        if not os.path.exists(FP8_LIB_PATH):
+            raise RuntimeError(
+                f"{FP8_LIB_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'` "
+                "(there is no CPU fallback)")
+        loader = importlib.machinery.ExtensionFileLoader("_fp8_torch", FP8_LIB_PATH)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_fp8_torch", loader))
+        loader.exec_module(mod)
+        l = lib()
+        mod.init(*(ctypes.cast(f, _vp).value for f in
+                   (l.rmsnorm_fwd_fp8, l.rmsnorm_quant_fp8, l.rmsnorm_gemm_fp8)), _check)
+        _fp8_mod = mod
+    return _fp8_mod
 
 
-def _elsewhere(name, t, stream):
-    """None when a call on t can run as it is: on the current device and,
-    stream being None, its current stream. Else the context to run it in, in
-    which the outputs that the binding allocates belong to that stream."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, {name} on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.get_device() != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return None
-
-
-def _ld(name, t, M, H, dtype, dev):
-    """Row stride (elements) of a [M, H] tensor of `dtype` on device `dev`
-    (an index) with unit column stride; H for one row."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (M, H):
-        raise ValueError(f"{name} must be of shape {(M, H)}, got {tuple(t.shape)}")
-    ld, one = t.stride()
-    if one != 1 and H > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld if M > 1 else H
-
-
-def _fp32(name, t, shape, dev):
-    """Checks contiguous fp32 `t` of `shape` on device `dev` (an index)."""
-    if t.get_device() != dev or t.dtype != torch.float32 or tuple(t.shape) != shape \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on "
-                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _empty_fp8(M, H, qdtype, device):
-    """An 8-bit [M, H] tensor whose rows start at multiples of 16 bytes (as
-    rmsnorm_gemm_fp8 reads them)."""
-    if H % 16 == 0:
-        return torch.empty((M, H), device=device, dtype=qdtype)
-    return torch.empty((M, -(-H // 16) * 16), device=device, dtype=qdtype)[:, :H]
+def _on_stream(t, stream):
+    """The context in which a call on tensor t runs on `stream`: what the
+    binding allocates then belongs to that stream."""
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-6,
@@ -496,49 +473,10 @@ def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-
     Returns (q, scale, rstd or None), with r (h, q, scale, rstd or None). q
     is [M, H] of qdtype (float8_e4m3fn or float8_e5m2), scale [M, ceil(H /
     128)]; q times its group's scale is the norm's output."""
-    ctx = _elsewhere("x", x, stream)
-    if ctx is not None:
-        with ctx:
-            return rmsnorm_fwd_fp8(x, w, r, q, scale, h, rstd, eps, qdtype, want_rstd)
-    H = w.numel()
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D [M, {H}]")
-    M, dev, device, dtype = x.shape[0], x.get_device(), x.device, x.dtype
-    code, qcode = _dtype_code(x), _fp8_code("qdtype", qdtype)
-    ldx = _ld("x", x, M, H, dtype, dev)
-    if w.get_device() != dev or w.dtype != dtype or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous {dtype} tensor on cuda:{dev}")
-    ldr = ldh = ldq = H
-    rp = hp = rsp = None
-    if r is not None:
-        ldr = _ld("r", r, M, H, dtype, dev)
-        if h is None:
-            h = torch.empty((M, H), device=device, dtype=dtype)
-        else:
-            ldh = _ld("h", h, M, H, dtype, dev)
-        rp, hp = r.data_ptr(), h.data_ptr()
-    elif h is not None:
-        raise ValueError("h is the residual variant's output: pass r too")
-    if q is None:
-        q = _empty_fp8(M, H, qdtype, device)
-        ldq = q.stride(0)
-    else:
-        ldq = _ld("q", q, M, H, qdtype, dev)
-    shape = (M, -(-H // FP8_GROUP))
-    if scale is None:
-        scale = torch.empty(shape, device=device, dtype=torch.float32)
-    else:
-        _fp32("scale", scale, shape, dev)
-    if rstd is not None:
-        _fp32("rstd", rstd, (M,), dev)
-    elif want_rstd:
-        rstd = torch.empty((M,), device=device, dtype=torch.float32)
-    if rstd is not None:
-        rsp = rstd.data_ptr()
-    _check(lib().rmsnorm_fwd_fp8(x.data_ptr(), ldx, rp, ldr, w.data_ptr(), q.data_ptr(), ldq,
-                                 scale.data_ptr(), hp, ldh, rsp, M, H, eps, code, qcode,
-                                 _raw_stream(dev)), "rmsnorm_fwd_fp8")
-    return (q, scale, rstd) if r is None else (h, q, scale, rstd)
+    if stream is not None:
+        with _on_stream(x, stream):
+            return _fp8().fwd_fp8(x, w, r, q, scale, h, rstd, eps, qdtype, want_rstd)
+    return _fp8().fwd_fp8(x, w, r, q, scale, h, rstd, eps, qdtype, want_rstd)
 
 
 def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e4m3fn,
@@ -546,32 +484,10 @@ def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e
     """x [M, H] (any row stride) rounded to 8 bits: (q, scale), with one fp32
     scale for each 128 columns of a row (block_rows=1, activations) or each
     block of 128 x 128 (block_rows=128, weights); see rmsnorm.h."""
-    ctx = _elsewhere("x", x, stream)
-    if ctx is not None:
-        with ctx:
-            return rmsnorm_quant_fp8(x, q, scale, block_rows, qdtype)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D [M, H]")
-    M, H = x.shape
-    dev, device = x.get_device(), x.device
-    code, qcode = _dtype_code(x), _fp8_code("qdtype", qdtype)
-    ldx = _ld("x", x, M, H, x.dtype, dev)
-    if block_rows != 1 and block_rows != FP8_GROUP:
-        raise ValueError(f"block_rows must be 1 or {FP8_GROUP}, got {block_rows}")
-    if q is None:
-        q = _empty_fp8(M, H, qdtype, device)
-        ldq = q.stride(0)
-    else:
-        ldq = _ld("q", q, M, H, qdtype, dev)
-    shape = (-(-M // block_rows), -(-H // FP8_GROUP))
-    if scale is None:
-        scale = torch.empty(shape, device=device, dtype=torch.float32)
-    else:
-        _fp32("scale", scale, shape, dev)
-    _check(lib().rmsnorm_quant_fp8(x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), M, H,
-                                   block_rows, code, qcode, _raw_stream(dev)),
-           "rmsnorm_quant_fp8")
-    return q, scale
+    if stream is not None:
+        with _on_stream(x, stream):
+            return _fp8().quant_fp8(x, q, scale, block_rows, qdtype)
+    return _fp8().quant_fp8(x, q, scale, block_rows, qdtype)
 
 
 def set_gemm_fp8_test(path: int):
@@ -588,32 +504,10 @@ def rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16,
     multiples of 16 bytes). out: any row stride; out_dtype float32, bfloat16
     or float16 when it is not given. static_weights: nothing in flight on the
     stream writes b or b_scale (see RMSNORM_GEMM_FP8_STATIC_WEIGHTS)."""
-    ctx = _elsewhere("a", a, stream)
-    if ctx is not None:
-        with ctx:
-            return rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
-    if a.dim() != 2 or b.dim() != 2:
-        raise ValueError(f"a [M, K] and b [N, K] must be 2-D, got {tuple(a.shape)} and "
-                         f"{tuple(b.shape)}")
-    M, K = a.shape
-    N, dev, ta, tb = b.shape[0], a.get_device(), a.dtype, b.dtype
-    acode, bcode = _fp8_code("a", ta), _fp8_code("b", tb)
-    lda, ldb = _ld("a", a, M, K, ta, dev), _ld("b", b, N, K, tb, dev)
-    G = -(-K // FP8_GROUP)
-    _fp32("a_scale", a_scale, (M, G), dev)
-    _fp32("b_scale", b_scale, (-(-N // FP8_GROUP), G), dev)
-    ldo = N
-    if out is None:
-        if out_dtype not in DTYPES:
-            raise ValueError(f"unsupported dtype {out_dtype}")
-        out = torch.empty((M, N), device=a.device, dtype=out_dtype)
-    else:
-        ldo = _ld("out", out, M, N, out.dtype, dev)
-    _check(lib().rmsnorm_gemm_fp8(
-        a.data_ptr(), lda, a_scale.data_ptr(), acode, b.data_ptr(), ldb, b_scale.data_ptr(), bcode,
-        out.data_ptr(), ldo, M, N, K, _dtype_code(out),
-        GEMM_FP8_STATIC_WEIGHTS if static_weights else 0, _raw_stream(dev)), "rmsnorm_gemm_fp8")
-    return out
+    if stream is not None:
+        with _on_stream(a, stream):
+            return _fp8().gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
+    return _fp8().gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
 
 
 STATIC_SCRATCH_BYTES = 16 << 20     # RMSNORM_STATIC_SCRATCH_BYTES
