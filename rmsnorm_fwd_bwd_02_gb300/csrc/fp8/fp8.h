@@ -55,8 +55,9 @@ struct Fp8RowKernel {
 // The shapes of one element type, for x alone, the norm, and the norm of
 // x + r: 32-byte packs with rows that share a warp [0..3], with a CTA a row
 // for few rows [4], for many rows, narrow [5] and wide [6]; 16-byte packs
-// [7]; loose packs [8]. Blocks: 32-byte, 16-byte, loose packs.
-constexpr int kFp8SubShapes = 4, kFp8RowShapes = 9;
+// [7]; loose packs, rows that share a warp [8], [9], a CTA a row [10].
+// Blocks: 32-byte, 16-byte, loose packs.
+constexpr int kFp8SubShapes = 4, kFp8RowShapes = 11;
 struct Fp8RowSet {
     Fp8RowKernel k[3][kFp8RowShapes];
     const void *blocks[3];

@@ -71,8 +71,13 @@ cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void
 // a lane take 65 us, one 72; at 16384 x 8192 four take 67 us, two 70 to 73.
 const Fp8RowKernel &pick_fp8_rows(const Fp8RowKernel *k, int width, int64_t M, int64_t H, int sms)
 {
-    if (width > 0)
-        return k[6 + width];
+    if (width > 0) {
+        // short rows share warps in loose packs, whose width is 16 bytes too
+        for (int i = 8; i < 10; ++i)
+            if (H <= k[i].max_cols())
+                return k[i];
+        return k[width == 1 ? 7 : 10];
+    }
     const bool few = M <= 2 * (int64_t)sms;
     for (int i = 0; i < kFp8SubShapes - (few ? 1 : 0); ++i)
         if (H <= k[i].max_cols())

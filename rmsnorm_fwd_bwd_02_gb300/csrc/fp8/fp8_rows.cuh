@@ -84,45 +84,39 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, int e5m2)
                 : __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
-// A 16-byte pack of a row that may start at any address, as it is read: the
-// aligned 16-byte words that hold it (the second only where the pack reaches
-// into it, so no word without a byte of the row is touched) and how far into
-// the first it starts. The words go through L1, where a neighbour's first is
-// this lane's second.
+// A 16-byte pack of a row that may start at any address ("loose"). Lane vi
+// reads the aligned 16-byte word in which its pack starts (no word without a
+// byte of the row is touched); what the pack has in the next word is the next
+// lane's, taken by a shuffle once both are there, so that a load in flight
+// holds four registers as an aligned one does. The last lane of a warp (or of
+// a row's lanes) reads that word itself, out of L1, where its neighbour in
+// the next warp has brought it.
 template <typename T> struct LooseRaw {
     static constexpr int E = 16 / (int)sizeof(T);
-    uint4 a, b;
-    int m, n;                                       // bytes: its start in a, its length
+    uint4 u;
     __device__ __forceinline__ static LooseRaw zero()
     {
         LooseRaw r;
-        r.a = r.b = make_uint4(0, 0, 0, 0);
-        r.m = r.n = 0;
+        r.u = make_uint4(0, 0, 0, 0);
         return r;
     }
-    __device__ __forceinline__ static uint4 ld(const void *p)
+    // Word vi of the row (row: its first byte), zero where it holds none of it.
+    __device__ __forceinline__ static LooseRaw word(const void *row, int vi, int H)
     {
-        uint4 v;
-        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(p));
-        return v;
-    }
-    // elements c .. c + E - 1 of a row of H (c < H)
-    __device__ __forceinline__ static LooseRaw load(const void *row, int c, int H)
-    {
-        const char *p = static_cast<const char *>(row) + (int64_t)c * (int)sizeof(T);
-        LooseRaw r;
-        r.m = (int)((uintptr_t)p & 15);
-        r.n = min(E, H - c) * (int)sizeof(T);
-        r.a = ld(p - r.m);
-        r.b = r.m + r.n > 16 ? ld(p - r.m + 16) : make_uint4(0, 0, 0, 0);
+        const int m = (int)((uintptr_t)row & 15);
+        LooseRaw r = zero();
+        if ((int64_t)vi * 16 < m + (int64_t)H * (int)sizeof(T))
+            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w)
+                         : "l"(static_cast<const char *>(row) - m + (int64_t)vi * 16));
         return r;
     }
-    // the pack, zero past the row's end
-    __device__ __forceinline__ uint4 words() const
+    // Bytes m.. of the word and `next`, zero past the row's end.
+    __device__ __forceinline__ uint4 join(uint4 next, const void *row, int vi, int H) const
     {
-        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const int m = (int)((uintptr_t)row & 15);
+        const int n = min(E, H - vi * E) * (int)sizeof(T);
+        uint32_t w[8] = {u.x, u.y, u.z, u.w, next.x, next.y, next.z, next.w};
         if (m & 8) {
 #pragma unroll
             for (int i = 0; i < 6; ++i)
@@ -150,6 +144,19 @@ template <typename T> struct LooseRaw {
             }
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // The pack; every lane of the warp takes part. `last`: the lane whose
+    // neighbour holds another row's word or another part of this one.
+    __device__ __forceinline__ uint4 pack(const void *row, int vi, int H, bool ok, bool last) const
+    {
+        uint4 next;
+        next.x = __shfl_down_sync(0xFFFFFFFFu, u.x, 1);
+        next.y = __shfl_down_sync(0xFFFFFFFFu, u.y, 1);
+        next.z = __shfl_down_sync(0xFFFFFFFFu, u.z, 1);
+        next.w = __shfl_down_sync(0xFFFFFFFFu, u.w, 1);
+        if (last && ok)
+            next = word(row, vi + 1, H).u;
+        return join(next, row, vi, H);
     }
 };
 
@@ -179,31 +186,33 @@ template <typename T> __device__ __forceinline__ void store_loose(void *p, uint4
     }
 }
 
-// What a load leaves in registers, and its pack.
+// What a load leaves in registers; the load of pack vi of the row that is
+// `row` rows of `ld` elements from base, and its pack.
 template <typename T, int E, bool LOOSE>
 using Fp8Raw = typename std::conditional<LOOSE, LooseRaw<T>, Pack<T, E>>::type;
 
-template <typename T, int E, typename R>
-__device__ __forceinline__ Pack<T, E> fp8_pack(const R &r)
-{
-    if constexpr (std::is_same<R, Pack<T, E>>::value) {
-        return r;
-    } else {
-        Pack<T, E> p;
-        p.u = r.words();
-        return p;
-    }
-}
-
-// Pack vi of the row that is `row` rows of `ld` elements from base.
 template <typename T, int E, bool LOOSE>
 __device__ __forceinline__ Fp8Raw<T, E, LOOSE> fp8_load(const void *base, int64_t row, uint32_t ld,
                                                         int vi, int H)
 {
     if constexpr (LOOSE)
-        return LooseRaw<T>::load(static_cast<const T *>(base) + row * ld, vi * E, H);
+        return LooseRaw<T>::word(static_cast<const T *>(base) + row * ld, vi, H);
     else
-        return Pack<T, E>::load(base, row * (ld / E) + vi);
+        return vi * E < H ? Pack<T, E>::load(base, row * (ld / E) + vi) : Pack<T, E>::zero();
+}
+
+template <typename T, int E, bool LOOSE>
+__device__ __forceinline__ Pack<T, E> fp8_pack(const Fp8Raw<T, E, LOOSE> &r, const void *base,
+                                               int64_t row, uint32_t ld, int vi, int H, bool ok,
+                                               bool last)
+{
+    if constexpr (LOOSE) {
+        Pack<T, E> p;
+        p.u = r.pack(static_cast<const T *>(base) + row * ld, vi, H, ok, last);
+        return p;
+    } else {
+        return r;
+    }
 }
 
 // The E values of pack vi of a row, times inv, as bytes at qrow + vi E. With
@@ -302,16 +311,24 @@ rms_fp8_rows(const Fp8RowsParams prm)
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int vi = lane + k * L;
-            to[k] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : R::zero();
+            to[k] = row < p.M ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : R::zero();
         }
+    };
+    const bool last = lane % (LR ? LR : 32) == (LR ? LR : 32) - 1;
+    auto pack = [&](const R &r, const void *base, uint32_t ld, int64_t row, int k) {
+        return fp8_pack<T, E, LOOSE>(r, base, row, ld, lane + k * L, p.H, row < p.M, last);
     };
     auto load_w = [&](int vi) {
         if (vi >= NV)
             return P::zero();
-        if constexpr (LOOSE)
-            return fp8_pack<T, E>(LooseRaw<T>::load(p.w, vi * E, p.H));
-        else
+        if constexpr (LOOSE) {
+            P w;
+            w.u = LooseRaw<T>::word(p.w, vi, p.H).join(LooseRaw<T>::word(p.w, vi + 1, p.H).u, p.w, vi,
+                                                       p.H);
+            return w;
+        } else {
             return P::load_cached(p.w, vi);
+        }
     };
 
     griddep_wait();
@@ -340,7 +357,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
             // this row was asked for a tile ago; now the next one
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                xv[k] = fp8_pack<T, E>(xn[k]);
+                xv[k] = pack(xn[k], p.x, ldx, row, k);
                 if constexpr (RES)
                     rv[k] = rn[k];
             }
@@ -355,7 +372,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
                 load(p.r, ldr, row, rv);
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                xv[k] = fp8_pack<T, E>(xr[k]);
+                xv[k] = pack(xr[k], p.x, ldx, row, k);
         }
         if constexpr (RES) {
             // the stored h is what the norm sees
@@ -364,7 +381,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
                 const int vi = lane + k * L;
                 X a, b;
                 xv[k].widen(a);
-                fp8_pack<T, E>(rv[k]).widen(b);
+                pack(rv[k], p.r, ldr, row, k).widen(b);
 #pragma unroll
                 for (int i = 0; i < X::N; ++i)
                     a.v[i] = vadd(a.v[i], b.v[i]);
@@ -461,6 +478,7 @@ template <typename T, int E, bool LOOSE>
 __global__ void __launch_bounds__(kFp8BlockThreads)
 rms_fp8_blocks(const Fp8BlocksParams p)
 {
+    using P = Pack<T, E>;
     using R = Fp8Raw<T, E, LOOSE>;
     using X = Vals<E>;
     constexpr int LG = kFp8Group / E;
@@ -481,13 +499,18 @@ rms_fp8_blocks(const Fp8BlocksParams p)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int64_t row = row0 + i * ROWS;
-            xv[i] = row < p.M && vi < NV ? fp8_load<T, E, LOOSE>(p.x, row, ldx, vi, p.H) : R::zero();
+            xv[i] = row < p.M ? fp8_load<T, E, LOOSE>(p.x, row, ldx, vi, p.H) : R::zero();
         }
         float a = 0.f;
+        P xp[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
+            const int64_t row = row0 + i * ROWS;
+            // a lane past the block reads no word: the block's last one reads
+            // its neighbour's word itself
+            xp[i] = fp8_pack<T, E, LOOSE>(xv[i], p.x, row, ldx, vi, p.H, row < p.M, lane == LG - 1);
             X y;
-            fp8_pack<T, E>(xv[i]).widen(y);
+            xp[i].widen(y);
             a = amax_nan(a, pack_amax<E>(y));
         }
         a = lanes_amax<32>(a);
@@ -505,7 +528,7 @@ rms_fp8_blocks(const Fp8BlocksParams p)
         for (int i = 0; i < NP; ++i) {
             const int64_t row = row0 + i * ROWS;
             X y;
-            fp8_pack<T, E>(xv[i]).widen(y);
+            xp[i].widen(y);
             if (row < p.M && vi < NV)
                 fp8_store<E, LOOSE>(static_cast<char *>(p.q) + row * p.ldq, vi, p.H, whole, y, sc.inv,
                                     p.e5m2);

@@ -1,6 +1,7 @@
 // 8-bit rows and blocks (fp8_rows.cuh) of fp16 tensors. Per mode: rows that
 // share a warp, a CTA a row (few rows; rows of up to 5120 columns for 16-bit
-// types; wider ones), 16-byte packs, loose packs.
+// types; wider ones), 16-byte packs; loose packs with rows that
+// share a warp and with a CTA a row.
 #include "fp8_rows.cuh"
 
 namespace rmsk {
@@ -15,7 +16,9 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 16, 2, 0, 160, 4, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 16, 2, 0, 512, 1, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, false, true)},
+         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 1, 16, 256, 4, true, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 32, 256, 4, true, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, true, true)},
         {RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 1, 8, 256, 4, true, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 1, 16, 256, 4, true, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 1, 32, 256, 4, true, true, false),
@@ -24,7 +27,9 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 2, 0, 160, 4, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 4, 0, 512, 1, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 0, 1024, 1, true, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 0, 1024, 1, false, false, true)},
+         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 1, 16, 256, 4, true, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 32, 256, 4, true, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 0, 1024, 1, true, true, true)},
         {RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 1, 8, 256, 4, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 1, 16, 256, 4, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 1, 32, 256, 4, false, true, false),
@@ -33,7 +38,9 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 2, 0, 160, 4, false, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 2, 0, 1024, 1, false, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, false, true)},
+         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 1, 16, 256, 4, false, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 32, 256, 4, false, true, true),
+         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, true, true)},
     },
     {(const void *)&rms_fp8_blocks<f16, 16, false>,
      (const void *)&rms_fp8_blocks<f16, 8, false>,
