@@ -29,7 +29,8 @@
 // lane, so a group of 128 columns is 8 or 16 neighbouring lanes and its
 // maximum takes 3 or 4 shuffles; the q of a lane is one 16- or 8-byte store.
 // Rows that may start at any address ("loose" packs, 16 bytes) are read as
-// the aligned 16-byte words that hold them and shifted into place.
+// the four-byte words that hold them, and h is written as aligned 16-byte
+// words, shifted into place in registers.
 //
 // What it took (GB300, bf16, dispatch as in fp8_api.cu): the reduction, the
 // group maxima and the conversion form one chain per row, so a CTA that
@@ -84,106 +85,130 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, int e5m2)
                 : __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
-// A 16-byte pack of a row that may start at any address ("loose"). Lane vi
-// reads the aligned 16-byte word in which its pack starts (no word without a
-// byte of the row is touched); what the pack has in the next word is the next
-// lane's, taken by a shuffle once both are there, so that a load in flight
-// holds four registers as an aligned one does. The last lane of a warp (or of
-// a row's lanes) reads that word itself, out of L1, where its neighbour in
-// the next warp has brought it.
+// A 16-byte pack of a row that may start at any address ("loose"), as the
+// four-byte words that hold it: five where elements of two bytes may start
+// inside a word, read through L1, where the lanes of a warp share the lines.
+// No word without a byte of the row is touched. (Aligned 16-byte words, the
+// neighbour's by shuffles, take a load where this takes five, but some 25
+// instructions more to put the bytes in their places: 59 against 41 us for
+// the norm at 8590 x 5597.)
 template <typename T> struct LooseRaw {
-    static constexpr int E = 16 / (int)sizeof(T);
-    uint4 u;
+    static constexpr int E = 16 / (int)sizeof(T), NW = sizeof(T) == 2 ? 5 : 4;
+    uint32_t w[NW];
     __device__ __forceinline__ static LooseRaw zero()
     {
         LooseRaw r;
-        r.u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            r.w[i] = 0;
         return r;
     }
-    // Word vi of the row (row: its first byte), zero where it holds none of it.
-    __device__ __forceinline__ static LooseRaw word(const void *row, int vi, int H)
+    // The words of pack vi of a row of H elements, zero where they hold none.
+    __device__ __forceinline__ static LooseRaw load(const void *row, int vi, int H)
     {
-        const int m = (int)((uintptr_t)row & 15);
+        const char *p = static_cast<const char *>(row) + (int64_t)vi * 16;
+        const int m = (int)((uintptr_t)row & 3), n = (H - vi * E) * (int)sizeof(T) + m;
         LooseRaw r = zero();
-        if ((int64_t)vi * 16 < m + (int64_t)H * (int)sizeof(T))
-            asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w)
-                         : "l"(static_cast<const char *>(row) - m + (int64_t)vi * 16));
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            if (4 * i < n && (i < 4 || m != 0))
+                asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.w[i]) : "l"(p - m + 4 * i));
         return r;
     }
-    // Bytes m.. of the word and `next`, zero past the row's end.
-    __device__ __forceinline__ uint4 join(uint4 next, const void *row, int vi, int H) const
+    // The pack, zero past the row's end.
+    __device__ __forceinline__ uint4 pack(const void *row, int vi, int H) const
     {
-        const int m = (int)((uintptr_t)row & 15);
-        const int n = min(E, H - vi * E) * (int)sizeof(T);
-        uint32_t w[8] = {u.x, u.y, u.z, u.w, next.x, next.y, next.z, next.w};
-        if (m & 8) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i)
-                w[i] = w[i + 2];
-        }
-        if (m & 4) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                w[i] = w[i + 1];
-        }
+        uint32_t o[4];
         if constexpr (sizeof(T) == 2) {
-            if (m & 2) {
+            const uint32_t sh = ((uint32_t)(uintptr_t)row & 2u) * 8u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = __funnelshift_r(w[i], w[i + 1], sh);
+            const int n = H - vi * E;
+            if (n < E) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                    o[i] = n <= 2 * i ? 0u : n == 2 * i + 1 ? o[i] & 0xFFFFu : o[i];
             }
-        }
-        if (n < 16) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (n <= 4 * i)
-                    w[i] = 0;
-                else if (n < 4 * i + 4)
-                    w[i] &= 0xFFFFu;
-            }
+            for (int i = 0; i < 4; ++i)
+                o[i] = w[i];
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    // The pack; every lane of the warp takes part. `last`: the lane whose
-    // neighbour holds another row's word or another part of this one.
-    __device__ __forceinline__ uint4 pack(const void *row, int vi, int H, bool ok, bool last) const
-    {
-        uint4 next;
-        next.x = __shfl_down_sync(0xFFFFFFFFu, u.x, 1);
-        next.y = __shfl_down_sync(0xFFFFFFFFu, u.y, 1);
-        next.z = __shfl_down_sync(0xFFFFFFFFu, u.z, 1);
-        next.w = __shfl_down_sync(0xFFFFFFFFu, u.w, 1);
-        if (last && ok)
-            next = word(row, vi + 1, H).u;
-        return join(next, row, vi, H);
+        return make_uint4(o[0], o[1], o[2], o[3]);
     }
 };
 
-// The first n bytes of a 16-byte pack to p, aligned to its element.
-template <typename T> __device__ __forceinline__ void store_loose(void *p, uint4 u, int n)
+// Bytes [from, to) of a 16-byte pack to p + from .. (p: where byte 0 would
+// go), whole elements.
+template <typename T>
+__device__ __forceinline__ void store_part(char *p, uint4 u, int from, int to)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    char *q = static_cast<char *>(p);
-    if (sizeof(T) == 4 || n < 16 || ((uintptr_t)p & 3) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (n >= 4 * i + 4 && (sizeof(T) == 4 || ((uintptr_t)p & 3) == 0)) {
-                st_row_b32(q + 4 * i, w[i]);
-            } else if (sizeof(T) == 2) {
-                if (n >= 4 * i + 2)
-                    st_row_b16(q + 4 * i, (uint16_t)(w[i] & 0xFFFFu));
-                if (n >= 4 * i + 4)
-                    st_row_b16(q + 4 * i + 2, (uint16_t)(w[i] >> 16));
-            }
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+        const int at = i * (int)sizeof(T);
+        if (at >= from && at < to) {
+            if constexpr (sizeof(T) == 4)
+                st_row_b32(p + at, w[i]);
+            else
+                st_row_b16(p + at, (uint16_t)(w[i / 2] >> (16 * (i & 1))));
         }
-    } else {                                        // whole, two bytes past a word
-        st_row_b16(q, (uint16_t)(w[0] & 0xFFFFu));
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            st_row_b32(q + 4 * i + 2, __funnelshift_r(w[i], w[i + 1], 16));
-        st_row_b16(q + 14, (uint16_t)(w[3] >> 16));
     }
+}
+
+// Pack vi of a row that may start at any address, written as aligned 16-byte
+// words: word vi is the end of the pack before (the lane before has it) and
+// the beginning of this one. The first lane of a warp (or of a row's lanes)
+// writes its own part of that word, the last also its pack's end; so do the
+// lanes at the row's ends. Every lane of the warp takes part; ok: the row
+// exists.
+template <typename T>
+__device__ __forceinline__ void store_loose(void *row, int vi, int H, uint4 u, bool ok, bool first,
+                                            bool last)
+{
+    const int m = (int)((uintptr_t)row & 15), n = H * (int)sizeof(T), at = vi * 16;
+    uint4 prev;
+    prev.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1);
+    prev.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1);
+    prev.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1);
+    prev.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1);
+    if (!ok)
+        return;
+    char *word = static_cast<char *>(row) - m + at;             // aligned
+    // bytes 16 - m .. of (prev, u): the word
+    uint32_t w[8] = {prev.x, prev.y, prev.z, prev.w, u.x, u.y, u.z, u.w};
+    const int sh = 16 - m;                                      // 1 .. 16
+    if (sh & 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = w[i + 4];
+    }
+    if (sh & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            w[i] = w[i + 2];
+    }
+    if (sh & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            w[i] = w[i + 1];
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (sh & 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+    }
+    const uint4 joined = make_uint4(w[0], w[1], w[2], w[3]);
+    const int lo = first || vi == 0 ? m : 0, hi = min(16, n + m - at);
+    if (lo == 0 && hi == 16)
+        st_row_v4(word, joined);
+    else
+        store_part<T>(word, joined, lo, hi);
+    if (last)
+        store_part<T>(word + m, u, 16 - m, min(16, n - at));
 }
 
 // What a load leaves in registers; the load of pack vi of the row that is
@@ -196,19 +221,18 @@ __device__ __forceinline__ Fp8Raw<T, E, LOOSE> fp8_load(const void *base, int64_
                                                         int vi, int H)
 {
     if constexpr (LOOSE)
-        return LooseRaw<T>::word(static_cast<const T *>(base) + row * ld, vi, H);
+        return LooseRaw<T>::load(static_cast<const T *>(base) + row * ld, vi, H);
     else
         return vi * E < H ? Pack<T, E>::load(base, row * (ld / E) + vi) : Pack<T, E>::zero();
 }
 
 template <typename T, int E, bool LOOSE>
 __device__ __forceinline__ Pack<T, E> fp8_pack(const Fp8Raw<T, E, LOOSE> &r, const void *base,
-                                               int64_t row, uint32_t ld, int vi, int H, bool ok,
-                                               bool last)
+                                               int64_t row, uint32_t ld, int vi, int H)
 {
     if constexpr (LOOSE) {
         Pack<T, E> p;
-        p.u = r.pack(static_cast<const T *>(base) + row * ld, vi, H, ok, last);
+        p.u = r.pack(static_cast<const T *>(base) + row * ld, vi, H);
         return p;
     } else {
         return r;
@@ -314,17 +338,16 @@ rms_fp8_rows(const Fp8RowsParams prm)
             to[k] = row < p.M ? fp8_load<T, E, LOOSE>(base, row, ld, vi, p.H) : R::zero();
         }
     };
-    const bool last = lane % (LR ? LR : 32) == (LR ? LR : 32) - 1;
+    const bool first = lane % (LR ? LR : 32) == 0, last = lane % (LR ? LR : 32) == (LR ? LR : 32) - 1;
     auto pack = [&](const R &r, const void *base, uint32_t ld, int64_t row, int k) {
-        return fp8_pack<T, E, LOOSE>(r, base, row, ld, lane + k * L, p.H, row < p.M, last);
+        return fp8_pack<T, E, LOOSE>(r, base, row, ld, lane + k * L, p.H);
     };
     auto load_w = [&](int vi) {
         if (vi >= NV)
             return P::zero();
         if constexpr (LOOSE) {
             P w;
-            w.u = LooseRaw<T>::word(p.w, vi, p.H).join(LooseRaw<T>::word(p.w, vi + 1, p.H).u, p.w, vi,
-                                                       p.H);
+            w.u = LooseRaw<T>::load(p.w, vi, p.H).pack(p.w, vi, p.H);
             return w;
         } else {
             return P::load_cached(p.w, vi);
@@ -386,13 +409,11 @@ rms_fp8_rows(const Fp8RowsParams prm)
                 for (int i = 0; i < X::N; ++i)
                     a.v[i] = vadd(a.v[i], b.v[i]);
                 xv[k] = P::narrow(a);
-                if (row < p.M && vi < NV) {
-                    if constexpr (LOOSE)
-                        store_loose<T>(static_cast<T *>(p.h) + row * ldh + vi * E, xv[k].u,
-                                       min(E, p.H - vi * E) * (int)sizeof(T));
-                    else
-                        xv[k].store(p.h, row * (ldh / E) + vi);
-                }
+                if constexpr (LOOSE)
+                    store_loose<T>(static_cast<T *>(p.h) + row * ldh, vi, p.H, xv[k].u, row < p.M,
+                                   first, last);
+                else if (row < p.M && vi < NV)
+                    xv[k].store(p.h, row * (ldh / E) + vi);
             }
         }
 
@@ -506,9 +527,7 @@ rms_fp8_blocks(const Fp8BlocksParams p)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int64_t row = row0 + i * ROWS;
-            // a lane past the block reads no word: the block's last one reads
-            // its neighbour's word itself
-            xp[i] = fp8_pack<T, E, LOOSE>(xv[i], p.x, row, ldx, vi, p.H, row < p.M, lane == LG - 1);
+            xp[i] = fp8_pack<T, E, LOOSE>(xv[i], p.x, row, ldx, vi, p.H);
             X y;
             xp[i].widen(y);
             a = amax_nan(a, pack_amax<E>(y));
