@@ -79,7 +79,7 @@ def build_torch(force: bool = False) -> str:
            "-isystem" + os.path.join(root, "include"),
            "-isystem" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
            TORCH_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {os.path.basename(TORCH_SRC)}:\n{' '.join(cmd)}\n"

@@ -51,7 +51,7 @@ constexpr int kPairStages = 4;
 constexpr uint32_t kPairHalf = 128u * kFp8Group;        // 128 rows of one operand
 constexpr uint32_t kPairStage = 2u * kPairHalf;
 constexpr int kPairBufs = 2;                            // x 256 columns: all tensor memory
-constexpr int kPairTileRun = 8;                         // row tiles that are swept together
+constexpr int kPairTileRun = 16;                        // row tiles that are swept together
 constexpr int kPairChunk = 16;                          // groups whose scales come together
 constexpr int kPairScRow = 129;                         // floats a group of them (no conflicts)
 constexpr uint32_t kPairRowBytes = 64;                  // of a row of out staged at a time

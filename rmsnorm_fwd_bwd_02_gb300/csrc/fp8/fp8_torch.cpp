@@ -12,8 +12,7 @@
 // addresses and the Python function that raises a status.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_strided.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -119,13 +118,20 @@ float *fp32(const Tensor &t, const char *name, at::IntArrayRef shape, at::Device
     return static_cast<float *>(t.data_ptr());
 }
 
+// A new tensor from torch's CUDA allocator (without the dispatcher, which
+// takes as long as the allocation).
+Tensor empty(at::IntArrayRef shape, ScalarType t, at::Device dev)
+{
+    return at::detail::empty_cuda(shape, t, dev, std::nullopt);
+}
+
 // An 8-bit [M, H] tensor whose rows start at multiples of 16 bytes (as the
 // product reads them).
-Tensor empty_fp8(int64_t M, int64_t H, at::TensorOptions o)
+Tensor empty_fp8(int64_t M, int64_t H, ScalarType t, at::Device dev)
 {
     if (H % 16 == 0)
-        return at::empty({M, H}, o);
-    return at::empty_strided({M, H}, {(H + 15) / 16 * 16, 1}, o);
+        return empty({M, H}, t, dev);
+    return at::detail::empty_strided_cuda({M, H}, {(H + 15) / 16 * 16, 1}, t, dev);
 }
 
 PyObject *raised(int status, const char *where)
@@ -182,14 +188,13 @@ PyObject *fwd_fp8(PyObject *, PyObject *const *a, Py_ssize_t n)
         fp32(*rstd_in, "rstd", {M}, dev);
 
     const c10::cuda::CUDAGuard guard(dev);
-    const at::TensorOptions o = at::TensorOptions().device(dev);
-    const Tensor h = h_in ? *h_in : r ? at::empty({M, H}, o.dtype(dtype)) : Tensor();
-    const Tensor q = q_in ? *q_in : empty_fp8(M, H, o.dtype(qtype));
+    const Tensor h = h_in ? *h_in : r ? empty({M, H}, dtype, dev) : Tensor();
+    const Tensor q = q_in ? *q_in : empty_fp8(M, H, qtype, dev);
     if (!q_in)
         ldq = q.stride(0);
-    const Tensor scale = scale_in ? *scale_in : at::empty({M, G}, o.dtype(at::kFloat));
+    const Tensor scale = scale_in ? *scale_in : empty({M, G}, at::kFloat, dev);
     const Tensor rstd = rstd_in     ? *rstd_in
-                        : want_rstd ? at::empty({M}, o.dtype(at::kFloat))
+                        : want_rstd ? empty({M}, at::kFloat, dev)
                                     : Tensor();
     const int st = g_fwd(x.data_ptr(), ldx, r ? r->data_ptr() : nullptr, ldr, w.data_ptr(),
                          q.data_ptr(), ldq, static_cast<float *>(scale.data_ptr()),
@@ -240,11 +245,10 @@ PyObject *quant_fp8(PyObject *, PyObject *const *a, Py_ssize_t n)
         fp32(*scale_in, "scale", {R, G}, dev);
 
     const c10::cuda::CUDAGuard guard(dev);
-    const at::TensorOptions o = at::TensorOptions().device(dev);
-    const Tensor q = q_in ? *q_in : empty_fp8(M, H, o.dtype(qtype));
+    const Tensor q = q_in ? *q_in : empty_fp8(M, H, qtype, dev);
     if (!q_in)
         ldq = q.stride(0);
-    const Tensor scale = scale_in ? *scale_in : at::empty({R, G}, o.dtype(at::kFloat));
+    const Tensor scale = scale_in ? *scale_in : empty({R, G}, at::kFloat, dev);
     const int st = g_quant(x.data_ptr(), ldx, q.data_ptr(), ldq,
                            static_cast<float *>(scale.data_ptr()), M, H, (int)rows, code, qcode,
                            c10::cuda::getCurrentCUDAStream(dev.index()).stream());
@@ -287,7 +291,7 @@ PyObject *gemm_fp8(PyObject *, PyObject *const *v, Py_ssize_t n)
     const int64_t ldo = out_in ? row_stride(*out_in, "out", M, N, dtype, dev) : N;
 
     const c10::cuda::CUDAGuard guard(dev);
-    const Tensor out = out_in ? *out_in : at::empty({M, N}, a.options().dtype(dtype));
+    const Tensor out = out_in ? *out_in : empty({M, N}, dtype, dev);
     const int st = g_gemm(a.data_ptr(), lda, sap, acode, b.data_ptr(), ldb, sbp, bcode,
                           out.data_ptr(), ldo, M, N, K, code,
                           static_w ? RMSNORM_GEMM_FP8_STATIC_WEIGHTS : 0,
