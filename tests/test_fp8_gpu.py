@@ -550,6 +550,69 @@ def test_backward_takes_what_the_forward_returns():
     assert bool(((dw - dw0).abs() <= 1e-4 * (dw0.abs() + 1)).all())
 
 
+# ---------------------------------------------------- offsets past 32 bits
+def test_rows_past_32_bits():
+    """2.3e9 elements in and out: the last rows are those of their own call."""
+    M, H = 140000, 16384
+    x = torch.zeros(M, H, device=DEV, dtype=BF16)
+    tail, _, w = data(70, H, BF16, seed=100)
+    x[-70:] = tail.to(DEV)
+    q, s, _ = rn.rmsnorm_fwd_fp8(x, w.to(DEV))
+    y, _ = norm64(tail, w, 1e-6)
+    check_q(q[-70:], s[-70:], y, 1, E4M3)
+    assert bool((q[:M - 70].view(torch.uint8)[::997] == 0).all())
+    for rows in (1, 128):
+        q, s = rn.rmsnorm_quant_fp8(x, q=q, block_rows=rows)
+        R = 70 if rows == 1 else 1              # 140000 = 1093 blocks and 96 rows
+        got = q[-70:].float().cpu().to(F64)
+        want = tail.to(F64) / spread(s[-R:].cpu().to(F64), rows, 70, H)
+        a, b = round8(want * (1 - DELTA), E4M3), round8(want * (1 + DELTA), E4M3)
+        assert bool(((got >= torch.minimum(a, b)) & (got <= torch.maximum(a, b))).all())
+
+
+@pytest.mark.parametrize("path", [rn.PATH_FP8_GEMM, rn.PATH_FP8_PAIR])
+def test_gemm_past_32_bits(path):
+    """An operand and an output of more than 2^31 elements."""
+    M, N, K = 70000, 32768, 128
+    qa, sa, qb, sb = pair(600, 700, K, seed=101)
+    a = torch.zeros(M, K, device=DEV, dtype=torch.uint8).view(E4M3)
+    asc = torch.ones(M, 1, device=DEV)
+    a.view(torch.uint8)[-600:], asc[-600:] = qa.view(torch.uint8), sa
+    b = torch.zeros(N, K, device=DEV, dtype=torch.uint8).view(E4M3)
+    bsc = torch.ones(N // 128, 1, device=DEV)
+    b.view(torch.uint8)[-640:], bsc[-5:] = qb.view(torch.uint8)[:640], sb[:5]
+    torch.cuda.synchronize()
+    with forced(path):
+        out = rn.rmsnorm_gemm_fp8(a, asc, b, bsc)
+    want, T = gemm64(qa, sa, qb[:640], sb[:5])
+    check_out(out[-600:, -640:], want, T, K, BF16)
+    assert bool((out[-600:, :-640] == 0).all()) and bool((out[:-600] == 0).all())
+    del out
+    M, N, K = 140000, 130, 16384                # A of 2.3e9 bytes
+    a = torch.zeros(M, K, device=DEV, dtype=torch.uint8).view(E4M3)
+    qa, sa, qb, sb = pair(300, N, K, seed=102)
+    asc = torch.ones(M, K // 128, device=DEV)
+    a.view(torch.uint8)[-300:], asc[-300:] = qa.view(torch.uint8), sa
+    torch.cuda.synchronize()
+    with forced(path):
+        out = rn.rmsnorm_gemm_fp8(a, asc, qb, sb)
+    check_out(out[-300:], *gemm64(qa, sa, qb, sb), K, BF16)
+    assert bool((out[:-300] == 0).all())
+
+
+def test_first_call_of_a_shape_inside_a_capture():
+    """Sizes that no call had before: what the library looks up for them it
+    may look up while a stream is being captured."""
+    x, r, w, W, sW, W2, sW2 = layer_inputs(11, seed=110, H=1280, N=1152)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = layer(x, r, w, W, sW, W2, sW2, True)
+    g.replay()
+    torch.cuda.synchronize()
+    check_layer(x, r, w, W, sW, W2, sW2, res)
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals_of_the_binding():
     x, r, w, W, sW, W2, sW2 = layer_inputs(4, seed=95)
