@@ -492,11 +492,15 @@ rms_fp8_rows(const Fp8RowsParams prm)
 
 // One CTA of 256 threads to a block of 128 x 128; grid (G, ceil(M / 128)). A
 // thread holds 64 elements: a row of the block is LG lanes, so a pass of the
-// CTA takes 256 / LG rows and all passes' loads are in flight at once.
+// CTA takes 256 / LG rows and all passes' loads are in flight at once. Bound
+// by DRAM, with three CTAs an SM (80 registers a thread): 44.5 us, all of the
+// copy bandwidth, at 24576 x 4096 bf16, where two take 51 us and four, which
+// spill, 48. Loose fp32 packs need more registers (76 us at 25921 x 3195
+// without the bound, 99 with it).
 constexpr int kFp8BlockThreads = 256;
 
 template <typename T, int E, bool LOOSE>
-__global__ void __launch_bounds__(kFp8BlockThreads)
+__global__ void __launch_bounds__(kFp8BlockThreads, LOOSE && sizeof(T) == 4 ? 1 : 3)
 rms_fp8_blocks(const Fp8BlocksParams p)
 {
     using P = Pack<T, E>;
