@@ -280,18 +280,20 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
         // The largest cluster with which the whole grid runs at once (a few
         // late clusters cost as much as all the others: 64 x 6144 x 4096 with
-        // three CTAs a cluster, of which 47 run at once, 21 us, with two 12),
-        // with a ring of up to six stages.
+        // three CTAs a cluster, of which 46 run at once, 21 us, with two 12),
+        // with a ring of up to six stages. The runtime's count of clusters is
+        // that of one CTA an SM.
         for (KS = std::min(kFp8MaxCluster, G); KS >= 1; --KS) {
             const int ng = (G + KS - 1) / KS;
             L = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
             if (L.total > kFp8MaxSmem)
                 continue;
+            const void *fn = fp8_gemm_kernels.fn[v][g.dtype];
             int n;
-            if ((st = max_active_clusters(fp8_gemm_kernels.fn[v][g.dtype], fp8_gemm_threads(BN),
-                                          (int)L.total, KS, dev, &n)))
+            if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)) ||
+                (st = max_active_clusters(fn, fp8_gemm_threads(BN), (int)L.total, KS, dev, &n)))
                 return st;
-            if (tiles_r * tiles_c <= n)
+            if (tiles_r * tiles_c <= (int64_t)n * bps)
                 break;
         }
         if (KS < 1) {
