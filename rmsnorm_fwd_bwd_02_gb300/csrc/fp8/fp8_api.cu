@@ -269,7 +269,7 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
     // fit in shared memory; else tokens in tiles of 128 rows
     int v = 0;
     Fp8GemmLayout L;
-    int KS = 1;
+    int KS = 0;
     int64_t tiles_r = 0, tiles_c = 0;
     for (;; ++v) {
         const bool swap = v < 3;
@@ -278,23 +278,34 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
             continue;
         tiles_r = ((swap ? N : M) + kFp8TileR - 1) / kFp8TileR;
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
-        // The largest cluster with which the whole grid runs at once (a few
-        // late clusters cost as much as all the others: 64 x 6144 x 4096 with
-        // three CTAs a cluster, of which 46 run at once, 21 us, with two 12),
-        // with a ring of up to six stages. The runtime's count of clusters is
-        // that of one CTA an SM.
-        for (KS = std::min(kFp8MaxCluster, G); KS >= 1; --KS) {
-            const int ng = (G + KS - 1) / KS;
-            L = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
-            if (L.total > kFp8MaxSmem)
+        // Clusters with which the whole grid runs at once (a few late ones
+        // cost as much as all the others: 64 x 6144 x 4096 with three CTAs a
+        // cluster, of which 46 run at once, 21 us, with two 12), with a ring
+        // of up to six stages. Of those the one for which a CTA's groups and
+        // the exchange with its peers take least (in units of 10 ns, fitted
+        // to 2048 x 896, 1024 x 4096 and 1024 x 1024 outputs and inputs at 8
+        // to 200 rows: 64 x 1024 x 4096 takes 9.2 us with eight CTAs, 7.9
+        // with four, 8.2 with three). The runtime's count of clusters is that
+        // of one CTA an SM.
+        static const int kGroup[4] = {25, 25, 27, 40}, kPeer[4] = {12, 25, 45, 40};
+        KS = 0;
+        int least = INT32_MAX;
+        for (int ks = std::min(kFp8MaxCluster, G); ks >= 1; --ks) {
+            const int ng = (G + ks - 1) / ks;
+            const Fp8GemmLayout l = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
+            const int64_t cost = (int64_t)ng * kGroup[v] + (ks > 1 ? ks * kPeer[v] : 0);
+            if (l.total > kFp8MaxSmem || cost >= least)
                 continue;
             const void *fn = fp8_gemm_kernels.fn[v][g.dtype];
             int n;
-            if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)L.total)) ||
-                (st = max_active_clusters(fn, fp8_gemm_threads(BN), (int)L.total, KS, dev, &n)))
+            if ((st = blocks_per_sm(fn, fp8_gemm_threads(BN), dev, &bps, (int)l.total)) ||
+                (st = max_active_clusters(fn, fp8_gemm_threads(BN), (int)l.total, ks, dev, &n)))
                 return st;
-            if (tiles_r * tiles_c <= (int64_t)n * bps)
-                break;
+            if (tiles_r * tiles_c <= (int64_t)n * bps) {
+                KS = ks;
+                L = l;
+                least = (int)cost;
+            }
         }
         if (KS < 1) {
             // more tiles than run at once: a tile a CTA, two CTAs an SM (one
