@@ -4,6 +4,9 @@
 // stream.
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "../host.h"
 #include "../registry.h"
@@ -63,6 +66,36 @@ cudaError_t launch1(const void *fn, dim3 grid, int threads, cudaStream_t s, void
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Resident CTAs per SM of a row kernel, whose CTAs are as wide as the rows
+// need (so blocks_per_sm, which keeps one figure a kernel, is not enough).
+int row_blocks_per_sm(const void *fn, int threads, int dev, int *out)
+{
+    static std::mutex mu;
+    static std::map<std::tuple<const void *, int, int, unsigned long long>, int> cache;
+    const auto key = std::make_tuple(fn, threads, dev, current_context_id());
+    const bool known = std::get<3>(key) != 0;
+    if (known) {
+        std::lock_guard<std::mutex> g(mu);
+        auto it = cache.find(key);
+        if (it != cache.end()) {
+            *out = it->second;
+            return RMSNORM_OK;
+        }
+    }
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, 0);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    if (n < 1)
+        return cuda_fail(cudaErrorInvalidConfiguration);
+    if (known) {
+        std::lock_guard<std::mutex> g(mu);
+        cache[key] = n;
+    }
+    *out = n;
+    return RMSNORM_OK;
+}
+
 // Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: rows that
 // share a warp where they are short enough; a lane a pack while the rows do
 // not fill the SMs (latency); else more packs a lane. Measured (GB300, bf16,
@@ -108,7 +141,7 @@ int rows_impl(const Fp8RowsParams &prm, int mode, int dtype, cudaStream_t stream
         const int64_t lanes = ((Hw + k.E - 1) / k.E + k.V - 1) / k.V;
         threads = (int)((lanes + 31) / 32 * 32);
     }
-    if ((st = blocks_per_sm(k.fn, threads, dev, &bps)))
+    if ((st = row_blocks_per_sm(k.fn, threads, dev, &bps)))
         return st;
     const int64_t tiles = (p.M + tile - 1) / tile;
     const int64_t cap = std::max<int64_t>((int64_t)bps * sms / windows, 1);

@@ -29,8 +29,8 @@
 // lane, so a group of 128 columns is 8 or 16 neighbouring lanes and its
 // maximum takes 3 or 4 shuffles; the q of a lane is one 16- or 8-byte store.
 // Rows that may start at any address ("loose" packs, 16 bytes) are read as
-// the four-byte words that hold them, and h is written as aligned 16-byte
-// words, shifted into place in registers.
+// the four-byte words that hold them, and h is written so, shifted into place
+// in registers.
 //
 // What it took (GB300, bf16, dispatch as in fp8_api.cu): the reduction, the
 // group maxima and the conversion form one chain per row, so a CTA that
@@ -139,76 +139,46 @@ template <typename T> struct LooseRaw {
     }
 };
 
-// Bytes [from, to) of a 16-byte pack to p + from .. (p: where byte 0 would
-// go), whole elements.
-template <typename T>
-__device__ __forceinline__ void store_part(char *p, uint4 u, int from, int to)
-{
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
-        const int at = i * (int)sizeof(T);
-        if (at >= from && at < to) {
-            if constexpr (sizeof(T) == 4)
-                st_row_b32(p + at, w[i]);
-            else
-                st_row_b16(p + at, (uint16_t)(w[i / 2] >> (16 * (i & 1))));
-        }
-    }
-}
-
-// Pack vi of a row that may start at any address, written as aligned 16-byte
-// words: word vi is the end of the pack before (the lane before has it) and
-// the beginning of this one. The first lane of a warp (or of a row's lanes)
-// writes its own part of that word, the last also its pack's end; so do the
-// lanes at the row's ends. Every lane of the warp takes part; ok: the row
-// exists.
+// Pack vi of a row that may start at any address, written as four-byte words.
+// Where elements of two bytes start inside a word, the first word is the end
+// of the pack before (the lane before has it) and the beginning of this one;
+// the first lane of a warp (or of a row's lanes) then writes its half alone,
+// the last also its pack's last element. Every lane of the warp takes part;
+// ok: the row exists.
 template <typename T>
 __device__ __forceinline__ void store_loose(void *row, int vi, int H, uint4 u, bool ok, bool first,
                                             bool last)
 {
-    const int m = (int)((uintptr_t)row & 15), n = H * (int)sizeof(T), at = vi * 16;
-    uint4 prev;
-    prev.x = __shfl_up_sync(0xFFFFFFFFu, u.x, 1);
-    prev.y = __shfl_up_sync(0xFFFFFFFFu, u.y, 1);
-    prev.z = __shfl_up_sync(0xFFFFFFFFu, u.z, 1);
-    prev.w = __shfl_up_sync(0xFFFFFFFFu, u.w, 1);
-    if (!ok)
-        return;
-    char *word = static_cast<char *>(row) - m + at;             // aligned
-    // bytes 16 - m .. of (prev, u): the word
-    uint32_t w[8] = {prev.x, prev.y, prev.z, prev.w, u.x, u.y, u.z, u.w};
-    const int sh = 16 - m;                                      // 1 .. 16
-    if (sh & 16) {
+    char *p = static_cast<char *>(row) + (int64_t)vi * 16;
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = w[i + 4];
-    }
-    if (sh & 8) {
+            if (ok && vi * 4 + i < H)
+                st_row_b32(p + 4 * i, w[i]);
+    } else {
+        const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, u.w, 1);
+        const int n = ok ? H - vi * 8 : -1;         // elements of the row from here on
+        const uint32_t odd = (uint32_t)(uintptr_t)row & 2u;
+        const uint32_t w[5] = {before, u.x, u.y, u.z, u.w};
+        // word i holds elements 2 i - 1 and 2 i of the pack (odd) or 2 i and
+        // 2 i + 1
+        const uint32_t sh = odd ? 16u : 0u;
+        const int in = n + (odd ? 1 : 0);           // whole word i: 2 i + 2 <= in
+        p -= odd;
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
-            w[i] = w[i + 2];
-    }
-    if (sh & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i)
-            w[i] = w[i + 1];
-    }
-    if constexpr (sizeof(T) == 2) {
-        if (sh & 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = odd ? __funnelshift_r(w[i], w[i + 1], sh) : w[i + 1];
+            if (2 * i + 2 <= in && !(i == 0 && odd && first))
+                st_row_b32(p + 4 * i, v);
+            else if (2 * i + 1 == in && !(i == 0 && odd && (first || n <= 0)))
+                st_row_b16(p + 4 * i, (uint16_t)(v & 0xFFFFu));     // the row's last element
         }
+        if (odd && n >= 1 && first)
+            st_row_b16(p + 2, (uint16_t)(u.x & 0xFFFFu));
+        if (odd && n >= 8 && (last || n == 8))
+            st_row_b16(p + 16, (uint16_t)(u.w >> 16));
     }
-    const uint4 joined = make_uint4(w[0], w[1], w[2], w[3]);
-    const int lo = first || vi == 0 ? m : 0, hi = min(16, n + m - at);
-    if (lo == 0 && hi == 16)
-        st_row_v4(word, joined);
-    else
-        store_part<T>(word, joined, lo, hi);
-    if (last)
-        store_part<T>(word + m, u, 16 - m, min(16, n - at));
 }
 
 // What a load leaves in registers; the load of pack vi of the row that is
