@@ -5,7 +5,8 @@ checked (CUDA, contiguous or row-strided, dtype, shape), outputs that the
 caller did not pass are allocated with torch, and raw device pointers, row
 strides and the current torch CUDA stream are handed to the library. Every arithmetic step runs in the
 CUDA kernels. If the library has not been built this module raises at load
-time; there is no fallback.
+time; there is no fallback. The 8-bit calls are marshalled in C++
+(csrc/fp8/fp8_torch.cpp) for their time on the host.
 """
 import ctypes
 import importlib.machinery
