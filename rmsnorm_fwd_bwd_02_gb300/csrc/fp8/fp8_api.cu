@@ -325,7 +325,12 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
         int least = INT32_MAX;
         for (int ks = std::min(kFp8MaxCluster, G); ks >= 1; --ks) {
             const int ng = (G + ks - 1) / ks;
-            const Fp8GemmLayout l = fp8_gemm_layout(BN, swap, std::min(ng, 6), ng);
+            Fp8GemmLayout l;
+            for (int stages = std::min(ng, 6);; --stages) {
+                l = fp8_gemm_layout(BN, swap, stages, ng, ks);
+                if (l.total <= kFp8MaxSmem || stages <= 3)
+                    break;
+            }
             const int64_t cost = (int64_t)ng * kGroup[v] + (ks > 1 ? ks * kPeer[v] : 0);
             if (l.total > kFp8MaxSmem || cost >= least)
                 continue;
@@ -346,10 +351,10 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
             KS = 1;
             int stages = std::min(G, 6);
             do
-                L = fp8_gemm_layout(BN, swap, stages, G);
+                L = fp8_gemm_layout(BN, swap, stages, G, 1);
             while (L.total > kFp8HalfSmem && --stages >= 3);
             if (stages < 3)
-                L = fp8_gemm_layout(BN, swap, std::min(G, 3), G);
+                L = fp8_gemm_layout(BN, swap, std::min(G, 3), G, 1);
         }
         if (!swap || L.total <= kFp8MaxSmem)
             break;

@@ -24,14 +24,17 @@
 // 128-byte swizzle: a stage is 128 columns, exactly one swizzle span, of both
 // operands), warp 1 issues the MMAs into NB buffers of tensor memory in turn,
 // the EW other warps read the buffers and keep the sums. At the end each CTA
-// puts its sums in shared memory (over the ring, which is drained), the
-// cluster meets, and each CTA adds a part of the tile over its KS peers in
-// rank order and stores it: the same bits on every run.
+// of a cluster owns some rows of the tile: every thread stores its row's sums
+// into the owner's shared memory (asynchronous 16-byte stores, counted on the
+// owner's barrier), and the owner adds them in rank order and writes out: the
+// same bits on every run. (Sums left in place, met at a cluster barrier and
+// read by the owners took 1 to 2 us longer: PUSH_FIGURES.)
 //
 // Every wait is bounded (about one second, or the test limit); one that runs
-// out counts in the library's timeout counter, and the CTA skips its work,
-// still meets its cluster, waits (bounded) for its copies and MMAs in flight
-// and frees its tensor memory.
+// out counts in the library's timeout counter, and the CTA skips its work but
+// still stores its (meaningless) sums into its peers, which count on them,
+// meets its cluster, waits (bounded) for its copies and MMAs in flight and
+// frees its tensor memory.
 #pragma once
 
 #include "../gemv_tc.cuh"
@@ -45,29 +48,39 @@ constexpr uint32_t kFp8StageR = kFp8TileR * kFp8Group;  // its bytes in a stage
 
 __host__ __device__ constexpr int fp8_epi_warps(int BN) { return BN >= 128 ? 8 : 4; }
 __host__ __device__ constexpr int fp8_gemm_threads(int BN) { return 64 + 32 * fp8_epi_warps(BN); }
+// Whether a cluster's sums travel by bulk copies (else by stores from
+// registers, which are quicker for few columns).
+__host__ __device__ constexpr bool fp8_bulk(int BN) { return BN >= 64; }
 __host__ __device__ constexpr int fp8_acc_bufs(int BN) { return BN >= 64 ? 2 : 4; }
 __host__ __device__ constexpr int fp8_tmem_cols(int BN) { return BN * fp8_acc_bufs(BN); }
 
 // Shared memory of one CTA, byte offsets from a 1024-byte aligned base: the
-// ring (NSt stages of 128 + BN rows of 128 bytes; the sums [128][BN + 4]
-// over it at the end), the scales of the tokens with SWAP ([groups][BN + 4]),
-// the mbarriers (full, empty a stage; full, empty a buffer; drain), eight
-// words (tensor-memory address, failure flag, stages issued, consumed).
+// ring (NSt stages of 128 + BN rows of 128 bytes; alone, the sums [128][BN +
+// 4] over it at the end), with a cluster the sums received ([rank][own rows]
+// [BN + 4]), the scales of the tokens with SWAP ([groups][BN + 4]), the
+// mbarriers (full, empty a stage; full, empty a buffer; drain; received),
+// eight words (tensor-memory address, failure flag, stages issued, consumed).
 struct Fp8GemmLayout {
-    int NSt;
-    uint32_t stage, sc, bar, slots, total;              // total: with 1023 bytes of alignment
+    int NSt, rpo;                                       // rpo: rows of the tile a CTA owns
+    uint32_t stage, recv, sc, bar, slots, total;        // total: with 1023 bytes of alignment
 };
 
-__host__ __device__ inline Fp8GemmLayout fp8_gemm_layout(int BN, bool swap, int NSt, int groups)
+__host__ __device__ inline Fp8GemmLayout fp8_gemm_layout(int BN, bool swap, int NSt, int groups,
+                                                         int KS)
 {
     Fp8GemmLayout L;
     L.NSt = NSt;
+    L.rpo = (kFp8TileR + KS - 1) / KS;
     L.stage = kFp8StageR + (uint32_t)BN * kFp8Group;
-    const uint32_t ring = (uint32_t)NSt * L.stage;
-    const uint32_t sums = (uint32_t)kFp8TileR * (uint32_t)(BN + 4) * 4u;
-    L.sc = ((ring > sums ? ring : sums) + 15u) & ~15u;
-    L.bar = L.sc + (swap ? (uint32_t)groups * (uint32_t)(BN + 4) * 4u : 0u);
-    L.slots = L.bar + 8u * (uint32_t)(2 * NSt + 2 * fp8_acc_bufs(BN) + 1);
+    const uint32_t ring = (uint32_t)NSt * L.stage, row = (uint32_t)(BN + 4) * 4u;
+    const uint32_t sums = (uint32_t)kFp8TileR * row;
+    // where the sums go over the ring before anything else: alone, and where
+    // they travel by bulk copies
+    const uint32_t first = (KS == 1 || fp8_bulk(BN)) && sums > ring ? sums : ring;
+    L.recv = KS > 1 ? first : 0u;
+    L.sc = first + (KS > 1 ? (uint32_t)(KS * L.rpo) * row : 0u);
+    L.bar = L.sc + (swap ? (uint32_t)groups * row : 0u);
+    L.slots = L.bar + 8u * (uint32_t)(2 * NSt + 2 * fp8_acc_bufs(BN) + 2);
     L.total = L.slots + 32u + 1023u;
     // An SM has 512 columns of tensor memory. A CTA that waits for its
     // columns while a peer of its cluster holds some elsewhere could wait
@@ -177,17 +190,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[16])
                  : "memory");
 }
 
-// Four floats of a peer's shared memory (cluster address).
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 template <typename T> __device__ __forceinline__ void store_out1(T *p, float v)
 {
     if constexpr (sizeof(T) == 4)
@@ -206,16 +208,16 @@ template <typename T> __device__ __forceinline__ void store_out4(T *p, float4 v)
                      : "memory");
 }
 
-// Quad u of the tile at (r0, c0) to out: with SWAP four tokens of a feature,
-// neighbouring quads neighbouring features, else four features of a token.
+// Columns 4 c4 .. of row `row` of the tile at (r0, c0) to out: with SWAP four
+// tokens of a feature, else four features of a token.
 template <typename T, bool SWAP>
-__device__ __forceinline__ void fp8_store_quad(const Fp8GemmParams &p, int r0, int c0, int nc, int u,
+__device__ __forceinline__ void fp8_store_quad(const Fp8GemmParams &p, int r0, int c0, int row, int c4,
                                                float4 v)
 {
     T *out = static_cast<T *>(p.out);
     const float e[4] = {v.x, v.y, v.z, v.w};
     if constexpr (SWAP) {
-        const int n = r0 + u % kFp8TileR, m = c0 + u / kFp8TileR * 4;
+        const int n = r0 + row, m = c0 + c4 * 4;
         if (n < p.N) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -223,7 +225,7 @@ __device__ __forceinline__ void fp8_store_quad(const Fp8GemmParams &p, int r0, i
                     store_out1<T>(out + (int64_t)(m + j) * p.ldo + n, e[j]);
         }
     } else {
-        const int m = r0 + u / nc, n = c0 + u % nc * 4;
+        const int m = r0 + row, n = c0 + c4 * 4;
         if (m < p.M) {
             T *to = out + (int64_t)m * p.ldo + n;
             if (p.vec && n + 4 <= p.N) {
@@ -238,6 +240,43 @@ __device__ __forceinline__ void fp8_store_quad(const Fp8GemmParams &p, int r0, i
     }
 }
 
+// Rows row0 .. row0 + own - 1 of the tile, four columns at a time, to out:
+// each the sum, in rank order, of what `KS` CTAs hold of it ([KS][rpo][BN +
+// 4]). NT threads, of which this is number t.
+template <typename T, int BN, bool SWAP, int NT>
+__device__ __forceinline__ void fp8_finish(const Fp8GemmParams &p, const float *sums, int KS, int rpo,
+                                           int r0, int c0, int row0, int own, int nc, int t)
+{
+    constexpr int SROW = BN + 4, UB = 4;                // quads a thread has in hand
+    const int units = own * nc;
+    for (int ub = t; ub < units; ub += UB * NT) {
+        int rl[UB], c4[UB];
+        float4 v[UB];
+#pragma unroll
+        for (int i = 0; i < UB; ++i) {
+            const int u = min(ub + i * NT, units - 1);
+            rl[i] = SWAP ? u % own : u / nc;
+            c4[i] = SWAP ? u / own : u % nc;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int i = 0; i < UB; ++i) {
+                const float4 w = *reinterpret_cast<const float4 *>(sums + (k * rpo + rl[i]) * SROW +
+                                                                   c4[i] * 4);
+                v[i].x += w.x;
+                v[i].y += w.y;
+                v[i].z += w.z;
+                v[i].w += w.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < UB; ++i)
+            if (ub + i * NT < units)
+                fp8_store_quad<T, SWAP>(p, r0, c0, row0 + rl[i], c4[i], v[i]);
+    }
+}
+
 // grid = tiles x KS CTAs (KS consecutive ones a cluster); the tiles along the
 // row operand follow one another.
 template <typename T, int BN, bool SWAP>
@@ -248,6 +287,8 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
     constexpr int EW = fp8_epi_warps(BN), NB = fp8_acc_bufs(BN);
     constexpr int CW = BN * 4 / EW;                     // columns a thread sums
     constexpr int SROW = BN + 4, kScRow = BN + 4;       // floats a row of the sums, the scales
+    constexpr uint32_t kRow = SROW * 4u;
+    constexpr bool BULK = fp8_bulk(BN);
     constexpr uint32_t kCols = fp8_tmem_cols(BN);
     extern __shared__ __align__(1024) unsigned char fp8_smem[];
 
@@ -260,12 +301,14 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
     const int NSt = L.NSt;
     const uint32_t raw_s = smem_addr(fp8_smem);
     unsigned char *base = fp8_smem + (((raw_s + 1023u) & ~1023u) - raw_s);
-    const uint32_t ring_s = smem_addr(base);
-    float *sums = reinterpret_cast<float *>(base);
+    const uint32_t ring_s = smem_addr(base), recv_s = ring_s + L.recv;
+    const int nc = SWAP ? (min(BN, p.M - c0) + 3) / 4 : BN / 4;        // column quads wanted
+    // the rows of the tile that this CTA adds up and writes
+    const int own = max(0, min(L.rpo, kFp8TileR - rank * L.rpo));
     float *sc = reinterpret_cast<float *>(base + L.sc);
     const uint32_t full0 = smem_addr(base + L.bar), empty0 = full0 + 8u * (uint32_t)NSt;
     const uint32_t accf0 = empty0 + 8u * (uint32_t)NSt, acce0 = accf0 + 8u * NB;
-    const uint32_t dbar = acce0 + 8u * NB;
+    const uint32_t dbar = acce0 + 8u * NB, rxbar = dbar + 8u;
     int *slots = reinterpret_cast<int *>(base + L.slots);
     volatile int *fail = slots + 1;
     const uint32_t fail_s = smem_addr(slots + 1);
@@ -284,6 +327,9 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
             mbar_init(acce0 + 8u * b, EW);
         }
         mbar_init(dbar, 1);
+        mbar_init(rxbar, 1);
+        if (KS > 1)             // every peer's sums of the own rows
+            mbar_expect_tx(rxbar, (uint32_t)((KS - 1) * own) * (BULK ? kRow : (uint32_t)nc * 16u));
         slots[1] = slots[2] = slots[3] = 0;
     }
     if (tid == 64) {
@@ -293,6 +339,8 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
     mbar_init_fence();
     tc_fence_before_sync();
     __syncthreads();
+    if (KS > 1)                 // the peers' barriers exist once all have arrived
+        cluster_arrive_release();
     tc_fence_after_sync();
     const uint32_t tmem = static_cast<uint32_t>(slots[0]);
 
@@ -447,25 +495,94 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
                 ++ub;
             }
         }
-        // the ring is drained: the last buffer was complete, so every copy
-        // has landed and every MMA has read it (or the CTA has failed, and
-        // its sums do not matter but copies may still land: write nothing)
-        named_bar_sync(1, EW * 32);
-        if (!*fail) {
-            float4 *to = reinterpret_cast<float4 *>(sums + row * SROW + col0);
+        if (KS > 1) {
+            cluster_wait_acquire();
+            if constexpr (BULK) {
+                // the tile's sums over the ring, then each owner's rows in one
+                // copy (should the CTA have failed, what still lands in the
+                // ring spoils sums that do not matter)
+                named_bar_sync(1, EW * 32);             // every warp has seen the last buffer
+                float4 *to = reinterpret_cast<float4 *>(base + (row * SROW + col0) * 4);
 #pragma unroll
-            for (int i = 0; i < CW / 4; ++i)
-                to[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                for (int i = 0; i < CW / 4; ++i)
+                    to[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x,
+                                        acc[2 * i + 1].y);
+                fence_proxy_async_smem();
+                named_bar_sync(1, EW * 32);
+                if (etid < KS && etid != rank) {
+                    const int theirs = min(L.rpo, kFp8TileR - etid * L.rpo);
+                    bulk_s2s_cluster(
+                        cluster_map(recv_s + (uint32_t)(rank * L.rpo) * kRow, (uint32_t)etid),
+                        ring_s + (uint32_t)(etid * L.rpo) * kRow, (uint32_t)theirs * kRow,
+                        cluster_map(rxbar, (uint32_t)etid));
+                }
+                // this CTA's own rows
+                for (int i = etid; i < own * (SROW / 4); i += EW * 32)
+                    reinterpret_cast<float4 *>(base + L.recv + (uint32_t)(rank * L.rpo) * kRow)[i] =
+                        reinterpret_cast<const float4 *>(base + (uint32_t)(rank * L.rpo) * kRow)[i];
+                if (etid < KS && etid != rank)
+                    bulk_wait_read_all();
+                __syncwarp();
+            } else {
+                // this row's sums to its owner
+                const int owner = row / L.rpo;
+                const uint32_t at =
+                    recv_s + (uint32_t)(((rank * L.rpo + row % L.rpo) * SROW + col0) * 4);
+                const uint32_t to = cluster_map(at, (uint32_t)owner);
+                const uint32_t bar = cluster_map(rxbar, (uint32_t)owner);
+#pragma unroll
+                for (int i = 0; i < CW / 4; ++i) {
+                    if (col0 / 4 + i >= nc)
+                        break;
+                    const float4 v =
+                        make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                    if (owner == rank)
+                        *reinterpret_cast<float4 *>(base + (at - ring_s) + 16 * i) = v;
+                    else
+                        st_async_v4(to + 16u * i, v, bar);
+                }
+            }
+            cluster_arrive_relaxed();                   // nothing more goes to a peer
+            named_bar_sync(1, EW * 32);                 // this CTA's own part is there
+            if (!mbar_wait_bounded_cluster(rxbar, 0, wait_limit_ns(p.wait_limit_us)))
+                *fail = 1;
+            if (!*fail)
+                fp8_finish<T, BN, SWAP, EW * 32>(p, reinterpret_cast<const float *>(base + L.recv),
+                                                 KS, L.rpo, r0, c0, rank * L.rpo, own, nc, etid);
+        } else if constexpr (SWAP) {
+            // alone with a feature a lane: neighbouring lanes write neighbours
+            if (!*fail) {
+#pragma unroll
+                for (int i = 0; i < CW / 4; ++i)
+                    if (col0 / 4 + i < nc)
+                        fp8_store_quad<T, SWAP>(p, r0, c0, row, col0 / 4 + i,
+                                                make_float4(acc[2 * i].x, acc[2 * i].y,
+                                                            acc[2 * i + 1].x, acc[2 * i + 1].y));
+            }
+        } else {
+            // the ring is drained: the last buffer was complete, so every
+            // copy has landed and every MMA has read it (or the CTA has
+            // failed, and copies may still land: write nothing)
+            named_bar_sync(1, EW * 32);
+            if (!*fail) {
+                float4 *to = reinterpret_cast<float4 *>(base + (row * SROW + col0) * 4);
+#pragma unroll
+                for (int i = 0; i < CW / 4; ++i)
+                    to[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x,
+                                        acc[2 * i + 1].y);
+            }
         }
+    }
+    if (KS > 1 && warp < 2) {
+        cluster_wait_acquire();
+        cluster_arrive_relaxed();
     }
 
     // every role has finished or given up
-    if (KS > 1) {
-        cluster_arrive_release();
-        cluster_wait_acquire();
-    } else {
-        __syncthreads();
-    }
+    __syncthreads();
+    if (!SWAP && KS == 1 && !*fail)
+        fp8_finish<T, BN, SWAP, fp8_gemm_threads(BN)>(p, reinterpret_cast<const float *>(base), 1,
+                                                      kFp8TileR, r0, c0, 0, kFp8TileR, nc, tid);
     if (*fail) {
         const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
         if (tid == 0) {
@@ -477,70 +594,12 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
             umma_commit(dbar);
             (void)mbar_wait_bounded(dbar, 0, limit);
         }
-    } else {
-        // this CTA's part of the tile, four columns at a time, the sums of
-        // its peers added in rank order. A round trip to a peer takes 0.4 us,
-        // so a thread asks for eight quads at a time: four units from two
-        // peers, or (clusters of more than two) two units from four.
-        const int nc = SWAP ? (min(BN, p.M - c0) + 3) / 4 : BN / 4;   // column quads wanted
-        const int units = kFp8TileR * nc;
-        const int u0 = rank * units / KS, u1 = (rank + 1) * units / KS;
-        auto sum = [&](auto units_at_once, auto peers_at_once) {
-            constexpr int UB = decltype(units_at_once)::value, PB = decltype(peers_at_once)::value;
-            constexpr int kThreads = fp8_gemm_threads(BN);
-            for (int ub = u0 + tid; ub < u1; ub += UB * kThreads) {
-                uint32_t at[UB];
-                float4 v[UB];
-#pragma unroll
-                for (int i = 0; i < UB; ++i) {
-                    const int u = min(ub + i * kThreads, u1 - 1);
-                    const int row = SWAP ? u % kFp8TileR : u / nc;
-                    const int c4 = SWAP ? u / kFp8TileR : u % nc;
-                    at[i] = (uint32_t)(row * SROW + c4 * 4) * 4u;
-                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-                for (int k0 = 0; k0 < KS; k0 += PB) {
-                    float4 w[UB][PB];
-#pragma unroll
-                    for (int k = 0; k < PB; ++k) {
-                        if (k0 + k >= KS)
-                            break;
-                        const uint32_t peer =
-                            KS > 1 ? cluster_map(ring_s, (uint32_t)(k0 + k)) : ring_s;
-#pragma unroll
-                        for (int i = 0; i < UB; ++i)
-                            w[i][k] = KS > 1 ? ld_cluster_v4(peer + at[i])
-                                             : *reinterpret_cast<const float4 *>(base + at[i]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < PB; ++k)
-#pragma unroll
-                        for (int i = 0; i < UB; ++i)
-                            if (k0 + k < KS) {
-                                v[i].x += w[i][k].x;
-                                v[i].y += w[i][k].y;
-                                v[i].z += w[i][k].z;
-                                v[i].w += w[i][k].w;
-                            }
-                }
-#pragma unroll
-                for (int i = 0; i < UB; ++i)
-                    if (ub + i * kThreads < u1)
-                        fp8_store_quad<T, SWAP>(p, r0, c0, nc, ub + i * kThreads, v[i]);
-            }
-        };
-        if (KS <= 2)
-            sum(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-        else
-            sum(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
     }
     tc_fence_before_sync();
-    if (KS > 1) {               // no CTA leaves while a peer may still read its sums (what this
-        cluster_arrive_relaxed();   // one read it has used; its stores need not be waited for)
+    if (KS > 1)                 // no CTA leaves while a peer may still store into it
         cluster_wait_acquire();
-    } else {
+    else
         __syncthreads();
-    }
     if (warp == 0) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kCols);
