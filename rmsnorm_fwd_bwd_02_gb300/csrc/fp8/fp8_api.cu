@@ -316,11 +316,11 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
         // cluster, of which 46 run at once, 21 us, with two 12), with a ring
         // of up to six stages. Of those the one for which a CTA's groups and
         // the exchange with its peers take least (in units of 10 ns, fitted
-        // to 2048 x 896, 1024 x 4096 and 1024 x 1024 outputs and inputs at 8
-        // to 200 rows: 64 x 1024 x 4096 takes 9.2 us with eight CTAs, 7.9
-        // with four, 8.2 with three). The runtime's count of clusters is that
-        // of one CTA an SM.
-        static const int kGroup[4] = {25, 25, 27, 40}, kPeer[4] = {12, 25, 45, 40};
+        // to 896 -> 2048, 4096 -> 1024 and 1024 -> 1024 features at 8 to 200
+        // rows: 64 x 2048 x 896 takes 4.7 us with four CTAs, 5.5 with three,
+        // 5.9 with one, 4.9 with six). The runtime's count of clusters is
+        // that of one CTA an SM.
+        static const int kGroup[4] = {25, 25, 27, 40}, kPeer[4] = {12, 15, 12, 40};
         KS = 0;
         int least = INT32_MAX;
         for (int ks = std::min(kFp8MaxCluster, G); ks >= 1; --ks) {

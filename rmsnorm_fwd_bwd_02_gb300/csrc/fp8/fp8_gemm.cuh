@@ -24,11 +24,13 @@
 // 128-byte swizzle: a stage is 128 columns, exactly one swizzle span, of both
 // operands), warp 1 issues the MMAs into NB buffers of tensor memory in turn,
 // the EW other warps read the buffers and keep the sums. At the end each CTA
-// of a cluster owns some rows of the tile: every thread stores its row's sums
-// into the owner's shared memory (asynchronous 16-byte stores, counted on the
-// owner's barrier), and the owner adds them in rank order and writes out: the
-// same bits on every run. (Sums left in place, met at a cluster barrier and
-// read by the owners took 1 to 2 us longer: PUSH_FIGURES.)
+// of a cluster owns some rows of the tile; the others send it theirs, counted
+// on its barrier, by asynchronous 16-byte stores straight from registers (up
+// to 32 columns) or through shared memory by one bulk copy an owner. The owner
+// adds them in rank order and writes out: the same bits on every run. (With
+// the sums left where they were and read by their owners after a cluster
+// barrier, 1 x 6144 x 4096 took 8.0 us against 6.7, 64 x 4096 x 4096 9.0
+// against 7.9.)
 //
 // Every wait is bounded (about one second, or the test limit); one that runs
 // out counts in the library's timeout counter, and the CTA skips its work but
