@@ -35,8 +35,8 @@
 // Every wait is bounded (about one second, or the test limit); one that runs
 // out counts in the library's timeout counter, and the CTA skips its work but
 // still stores its (meaningless) sums into its peers, which count on them,
-// meets its cluster, waits (bounded) for its copies and MMAs in flight and
-// frees its tensor memory.
+// meets its cluster, waits (bounded) for its copies, its peers' sums and its
+// MMAs in flight and frees its tensor memory.
 #pragma once
 
 #include "../gemv_tc.cuh"
@@ -543,6 +543,7 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
                     else
                         st_async_v4(to + 16u * i, v, bar);
                 }
+                __syncwarp();
             }
             cluster_arrive_relaxed();                   // nothing more goes to a peer
             named_bar_sync(1, EW * 32);                 // this CTA's own part is there
@@ -598,10 +599,13 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
         }
     }
     tc_fence_before_sync();
-    if (KS > 1)                 // no CTA leaves while a peer may still store into it
+    if (KS > 1) {               // no CTA leaves while a peer may still store into it
         cluster_wait_acquire();
-    else
+        if (*fail)              // (had its wait run out, what was on its way then)
+            (void)mbar_wait_bounded_cluster(rxbar, 0, wait_limit_ns(p.wait_limit_us));
+    } else {
         __syncthreads();
+    }
     if (warp == 0) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kCols);
