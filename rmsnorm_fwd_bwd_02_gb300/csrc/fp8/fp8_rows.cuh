@@ -287,6 +287,7 @@ rms_fp8_rows(const Fp8RowsParams prm)
     using R = Fp8Raw<T, E, LOOSE>;
     using X = Vals<E>;
     constexpr bool NORM = MODE != kFp8ModeQuant, RES = MODE == kFp8ModeResidual;
+    constexpr bool TREE = RES && !LOOSE;
     constexpr int LG = kFp8Group / E;               // lanes in one group of columns
     static_assert(LG <= 32 && (LR == 0 || LR % LG == 0), "lanes of a group");
     static_assert(!LOOSE || E * sizeof(T) == 16, "loose packs are 16 bytes");
@@ -399,15 +400,25 @@ rms_fp8_rows(const Fp8RowsParams prm)
                     acc = vfma(a.v[i], a.v[i], acc);
             }
             float ss = group_allreduce<LR ? LR : 32>(hsum(acc));
-            if constexpr (LR == 0) {                // the warps' sums, added in warp order
+            if constexpr (LR == 0) {                // the warps' sums, in a fixed order
                 const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
                 if (nw > 1) {
                     if ((threadIdx.x & 31) == 0)
                         red[buf][warp] = ss;
                     __syncthreads();
-                    ss = 0.f;
-                    for (int q = 0; q < nw; ++q)
-                        ss += red[buf][q];
+                    // By a tree in every warp for whole packs with a residual,
+                    // where few warps are there to hide the chain of sums
+                    // (32768 x 4096 bf16 146 us, 153 by the chain); else by
+                    // the chain (60000 x 1001 59 us, 67 by the tree; 11694 x
+                    // 2339 with a residual 48 and 71).
+                    if constexpr (TREE) {
+                        const int q = threadIdx.x & 31;
+                        ss = group_allreduce<32>(q < nw ? red[buf][q] : 0.f);
+                    } else {
+                        ss = 0.f;
+                        for (int q = 0; q < nw; ++q)
+                            ss += red[buf][q];
+                    }
                     buf ^= 1;                       // read again only after the next barrier
                 }
             }
@@ -465,12 +476,13 @@ rms_fp8_rows(const Fp8RowsParams prm)
 // CTA takes 256 / LG rows and all passes' loads are in flight at once. Bound
 // by DRAM, with three CTAs an SM (80 registers a thread): 44.5 us, all of the
 // copy bandwidth, at 24576 x 4096 bf16, where two take 51 us and four, which
-// spill, 48. Loose fp32 packs need more registers (76 us at 25921 x 3195
-// without the bound, 99 with it).
+// spill, 48. Loose fp32 packs need more registers: two CTAs (76 us at
+// 25921 x 3195, where three take 98 and one, with all the registers that the
+// compiler then uses, 118).
 constexpr int kFp8BlockThreads = 256;
 
 template <typename T, int E, bool LOOSE>
-__global__ void __launch_bounds__(kFp8BlockThreads, LOOSE && sizeof(T) == 4 ? 1 : 3)
+__global__ void __launch_bounds__(kFp8BlockThreads, LOOSE && sizeof(T) == 4 ? 2 : 3)
 rms_fp8_blocks(const Fp8BlocksParams p)
 {
     using P = Pack<T, E>;
