@@ -663,3 +663,43 @@ def test_bounded_waits(M, path):
             rn.set_stream_test_fault(0, 0)
         assert rn.wait_timeouts(reset=True) > 0
         assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
+
+
+@pytest.mark.parametrize("M,H", [(1, 1), (1, 896), (3, 130), (7, 1001), (16, 4096), (300, 896)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_new_outputs(M, H, dtype):
+    """Outputs that the call allocates: shapes, strides and devices as torch
+    makes them, apart in memory; one allocation for small calls, one each for
+    larger, and all of it free again with the last of them."""
+    x = torch.randn(M, H, device=DEV, dtype=dtype)
+    w = torch.ones(H, device=DEV, dtype=dtype)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    h, q, scale, rstd = rn.rmsnorm_fwd_fp8(x, w, r=x)
+    G, pitch = -(-H // 128), -(-H // 16) * 16
+    assert h.shape == (M, H) and h.dtype == dtype and h.is_contiguous()
+    assert q.shape == (M, H) and q.dtype == E4M3 and q.stride() == (pitch, 1)
+    assert scale.shape == (M, G) and scale.dtype == F32 and scale.is_contiguous()
+    assert rstd.shape == (M,) and rstd.dtype == F32 and rstd.is_contiguous()
+    outs = (h, q, scale, rstd)
+    spans = sorted((t.data_ptr(), t.data_ptr() + ((t.size(0) - 1) * t.stride(0) + t[0].numel())
+                    * t.element_size()) for t in outs)
+    for (_, end), (start, _) in zip(spans, spans[1:]):
+        assert end <= start
+    for t in outs:
+        assert t.device == DEV and not t.requires_grad and t.data_ptr() % 256 == 0
+        storage = t.untyped_storage()
+        last = t.data_ptr() - storage.data_ptr() + ((M - 1) * t.stride(0) + t[0].numel()) * t.element_size()
+        assert last <= storage.nbytes()
+    size = sum(-(-t.size(0) * t.stride(0) * t.element_size() // 256) * 256 for t in outs)
+    storages = {t.untyped_storage().data_ptr() for t in outs}
+    assert len(storages) == (1 if size <= 256 * 1024 else 4)
+    assert torch.equal(h, (x.float() + x.float()).to(dtype))
+    # one output alone keeps its values when the others are gone and their
+    # memory may be used again
+    want = scale.clone()
+    del h, q, rstd, outs, t, storage
+    rn.rmsnorm_fwd_fp8(x * 2, w, r=x)
+    assert torch.equal(scale, want)
+    del scale, want
+    assert torch.cuda.memory_allocated() == before
