@@ -287,11 +287,11 @@ rms_fp8_rows(const Fp8RowsParams prm)
     using R = Fp8Raw<T, E, LOOSE>;
     using X = Vals<E>;
     constexpr bool NORM = MODE != kFp8ModeQuant, RES = MODE == kFp8ModeResidual;
-    constexpr bool TREE = RES && !LOOSE;
+    constexpr bool TREE = RES && !LOOSE, FOURS = !TREE && MAXT > 160;
     constexpr int LG = kFp8Group / E;               // lanes in one group of columns
     static_assert(LG <= 32 && (LR == 0 || LR % LG == 0), "lanes of a group");
     static_assert(!LOOSE || E * sizeof(T) == 16, "loose packs are 16 bytes");
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
 
     const int L = LR ? LR : (int)blockDim.x;
     const int lane = LR ? (int)threadIdx.x % LR : (int)threadIdx.x;
@@ -325,6 +325,11 @@ rms_fp8_rows(const Fp8RowsParams prm)
         }
     };
 
+    if constexpr (NORM && LR == 0 && FOURS) {       // the sums that no warp writes
+        if (threadIdx.x < 32)
+            red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
+        __syncthreads();
+    }
     griddep_wait();
     constexpr bool kHold = NORM && HOLD;
     P wv[kHold ? V : 1];
@@ -407,13 +412,21 @@ rms_fp8_rows(const Fp8RowsParams prm)
                         red[buf][warp] = ss;
                     __syncthreads();
                     // By a tree in every warp for whole packs with a residual,
-                    // where few warps are there to hide the chain of sums
-                    // (32768 x 4096 bf16 146 us, 153 by the chain); else by
-                    // the chain (60000 x 1001 59 us, 67 by the tree; 11694 x
-                    // 2339 with a residual 48 and 71).
+                    // where few warps are there to hide the latency of a chain
+                    // (32768 x 4096 bf16 146 us, 153 by the chain); else by a
+                    // chain, over the sums of four warps where there may be
+                    // many (8590 x 5597 46 us, 48 without the fours, 51 by the
+                    // tree; at 32768 x 4096, four warps, 62 without, 64 with).
                     if constexpr (TREE) {
                         const int q = threadIdx.x & 31;
                         ss = group_allreduce<32>(q < nw ? red[buf][q] : 0.f);
+                    } else if constexpr (FOURS) {
+                        ss = 0.f;
+#pragma unroll 1
+                        for (int q = 0; q < nw; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&red[buf][q]);
+                            ss += (f.x + f.y) + (f.z + f.w);
+                        }
                     } else {
                         ss = 0.f;
                         for (int q = 0; q < nw; ++q)

@@ -15,7 +15,7 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 16, 1, 0, 1024, 1, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 16, 2, 0, 160, 4, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 16, 2, 0, 512, 1, true, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 4, 0, 512, 1, true, false, false),
+         RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 4, 0, 512, 2, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 1, 16, 256, 4, true, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 32, 256, 4, true, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeQuant, 8, 2, 0, 1024, 1, true, true, true)},
@@ -26,7 +26,7 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 1, 0, 1024, 1, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 2, 0, 160, 4, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 4, 0, 512, 1, true, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 4, 0, 512, 1, true, false, false),
+         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 4, 0, 512, 1, true, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 1, 16, 256, 4, true, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 32, 256, 4, true, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 0, 1024, 1, true, true, true)},
@@ -37,7 +37,7 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 1, 0, 1024, 1, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 2, 0, 160, 4, false, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 16, 2, 0, 1024, 1, false, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 4, 0, 512, 1, false, false, false),
+         RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 4, 0, 512, 2, false, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 1, 16, 256, 4, false, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 32, 256, 4, false, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeResidual, 8, 2, 0, 1024, 1, false, true, true)},
