@@ -101,7 +101,9 @@ int row_blocks_per_sm(const void *fn, int threads, int dev, int *out)
 // not fill the SMs (latency); else more packs a lane. Measured (GB300, bf16,
 // the norm): at 524288 x 128 eight lanes a row take 37 us; at 262144 x 896 a
 // warp a row takes 117 us, a CTA of two warps 141; at 32768 x 4096 two packs
-// a lane take 65 us, one 72; at 16384 x 8192 four take 67 us, two 70 to 73.
+// a lane take 65 us, one 72. Wider rows take two packs a lane in 64 registers:
+// at 12160 x 11008 72 us (four packs a lane 76, three 70), at 16264 x 8192
+// 63.5 (64 and 71), at 8056 x 16384 66.2 (65.5 and 72).
 const Fp8RowKernel &pick_fp8_rows(const Fp8RowKernel *k, int width, int64_t M, int64_t H, int sms)
 {
     if (width > 0) {

@@ -25,7 +25,7 @@ const Fp8RowSet fp8_rows_f16 = {
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 2, 32, 256, 3, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 1, 0, 1024, 1, false, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 2, 0, 160, 4, true, false, false),
-         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 4, 0, 512, 1, true, false, false),
+         RMSK_FP8_ROWS(f16, kFp8ModeNorm, 16, 2, 0, 512, 2, true, false, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 4, 0, 512, 1, true, true, false),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 1, 16, 256, 4, true, true, true),
          RMSK_FP8_ROWS(f16, kFp8ModeNorm, 8, 2, 32, 256, 4, true, true, true),
