@@ -381,7 +381,7 @@ int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
  *   tensor-map encoder.
  * Performance: two kernels on tcgen05. Up to 64 tokens the weight's rows are
  *   the tensor cores' rows and K is split over clusters (one token, 896 ->
- *   2048: 2.9 us; 16 tokens, 4096 -> 24576: 18.3 us, 83 % of the copy
+ *   2048: 2.7 us; 16 tokens, 4096 -> 24576: 18.3 us, 83 % of the copy
  *   bandwidth); more tokens take 128 x 128 tiles while these run at once, then
  *   256 x 256 tiles by pairs of CTAs (8192 tokens, 4096 -> 24576: 590 us,
  *   2.8 PFLOP/s).
