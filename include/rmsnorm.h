@@ -382,9 +382,9 @@ int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
  * Performance: two kernels on tcgen05. Up to 64 tokens the weight's rows are
  *   the tensor cores' rows and K is split over clusters (one token, 896 ->
  *   2048: 2.7 us; 16 tokens, 4096 -> 24576: 18.3 us, 83 % of the copy
- *   bandwidth); more tokens take 128 x 128 tiles while these run at once, then
- *   256 x 256 tiles by pairs of CTAs (8192 tokens, 4096 -> 24576: 590 us,
- *   2.8 PFLOP/s).
+ *   bandwidth); more tokens take 128 x 128 tiles while these run at once (two
+ *   to an SM where K < 4096), then 256 x 256 tiles by pairs of CTAs (8192
+ *   tokens, 4096 -> 24576: 590 us, 2.8 PFLOP/s).
  * Aliasing: out may share no byte with an input. Deterministic: no atomics,
  *   sums in a fixed order. Any M from one token to a prompt's batch; M == 0
  *   launches nothing.

@@ -281,6 +281,8 @@ int pair_impl(const Fp8GemmArgs &g, int dev, int64_t tiles_m, int64_t tiles_n, c
     return RMSNORM_OK;
 }
 
+constexpr int kPairLongK = 32;          // groups of a long K (see gemm_impl)
+
 int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
 {
     static const int kBN[4] = {16, 32, 64, 128};
@@ -289,16 +291,20 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
     int dev, sms, bps, st;
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
         return st;
-    // Pairs of CTAs where tiles of 128 x 128 would not all run at once and
-    // a pair's tile of 256 rows is not half empty. Measured (GB300, K = 4096,
-    // tile kernel / pairs): 256 x 6144 15 / 18 us, 256 x 12288 31 / 19 us,
-    // 128 x 24576 32 / 34 us, 1024 x 1024 12 / 18 us, 1024 x 4096 31 / 19 us,
-    // 2048 x 24576 319 / 158 us.
+    // Pairs of CTAs where tiles of 128 x 128 would not all run at once, two to
+    // an SM, or, with a long K, one to an SM (two share its tensor cores), and
+    // a pair's tile of 256 rows is not half empty. Measured (GB300, tile kernel
+    // / pairs): one tile an SM, 256 x 6144 x 4096 15 / 18 us, 1024 x 1024 x
+    // 4096 12 / 18; two, 1024 x 2560 at K = 384 5.5 / 7.6, 2048 11.4 / 12.7,
+    // 5120 22.1 / 21.8, 1024 x 4096 at 768 7.5 / 9.5, 5120 24.6 / 22.8;
+    // more, 4096 x 1280 x 2048 19.9 / 19.9, 2048 x 24576 x 4096 319 / 158;
+    // 128 x 24576 x 4096 32 / 34.
     const int64_t tm = (M + kPairTile - 1) / kPairTile, tn = (N + kPairTile - 1) / kPairTile;
     const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128);
     const int ov = g_test_gemm_fp8.load(std::memory_order_relaxed);
     const bool fits = tm * tn * G < INT32_MAX;
-    if (fits && (ov == kPathFp8Pair || (ov != kPathFp8Gemm && M > 128 && t128 > sms)))
+    const int64_t at_once = (G < kPairLongK ? 2 : 1) * (int64_t)sms;
+    if (fits && (ov == kPathFp8Pair || (ov != kPathFp8Gemm && M > 128 && t128 > at_once)))
         return pair_impl(g, dev, tm, tn, stream);
     // the narrowest column operand that holds the tokens, whose scales must
     // fit in shared memory; else tokens in tiles of 128 rows
