@@ -469,8 +469,6 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                                      "r"(n + c0), "r"(mw), "r"(ring_s + off)
                                      : "memory");
                     }
-                    if (lane == 0)
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 } else {
                     __syncwarp();
                     const unsigned char *st = base + off;
@@ -484,6 +482,10 @@ rms_fp8_gemm_pair(const Fp8PairParams p, const __grid_constant__ CUtensorMap tmA
                     }
                     __syncwarp();
                 }
+                // one group a pass, with a copy in it or without: that is what
+                // the wait for all but the last counts
+                if (lane == 0)
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
         }
         if (lane == 0)                                  // out is written

@@ -705,3 +705,31 @@ def test_new_outputs(M, H, dtype):
     assert torch.equal(scale, want)
     del scale, want
     assert torch.cuda.memory_allocated() == before
+
+
+# ------------------------------------------------ the paired kernel's output
+@pytest.mark.parametrize("N", [1001, 1043, 1045, 1055, 1071, 2077])
+@pytest.mark.parametrize("K", [128, 1024])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_pairs_into_a_padded_output(N, K, dtype):
+    """out inside a buffer whose rows start at multiples of 16 bytes while N
+    ends inside 16 bytes: a warp then writes some of its passes by tensor
+    copies and some element by element, from the same two slots of shared
+    memory in turn. N mod 64 is 17 to 47, so that an element-wise pass follows
+    a copy; several tiles a pair, called again and again."""
+    assert 16 < N % 64 < 48
+    M = 4 * 76 * 256 // -(-N // 256)                    # some four tiles a pair
+    qa, sa, qb, sb = pair(M, N, K, seed=N + K)
+    want, T = gemm64(qa, sa, qb, sb)
+    ldo = -(-N // 8) * 8 + 8
+    buf = torch.full((M + 2, ldo), -77.0, device=DEV, dtype=dtype)
+    out = buf[1:M + 1, :N]
+    assert out.data_ptr() % 16 == 0
+    for _ in range(5):
+        buf[1:M + 1, :N] = float("nan")
+        with forced(rn.PATH_FP8_PAIR):
+            rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out=out)
+            assert rn.last_path() == rn.PATH_FP8_PAIR
+        check_out(out, want, T, K, dtype)
+    assert bool((buf[1:M + 1, N:] == -77.0).all())
+    assert bool((buf[0] == -77.0).all()) and bool((buf[M + 1] == -77.0).all())
