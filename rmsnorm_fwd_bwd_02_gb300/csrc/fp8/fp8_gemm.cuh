@@ -593,8 +593,10 @@ rms_fp8_gemm(const Fp8GemmParams p, const __grid_constant__ CUtensorMap tmR,
                 (void)mbar_wait_bounded(full0 + 8u * (q % NSt), (uint32_t)((q / NSt) & 1), limit);
             atomicAdd(timeouts, 1u);
         }
-        if (tid == 32) {
-            umma_commit(dbar);
+        if (warp == 1) {        // the lane that issued the MMAs commits them
+            if (elect_one())
+                umma_commit(dbar);
+            __syncwarp();
             (void)mbar_wait_bounded(dbar, 0, limit);
         }
     }

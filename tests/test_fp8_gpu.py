@@ -733,3 +733,30 @@ def test_pairs_into_a_padded_output(N, K, dtype):
         check_out(out, want, T, K, dtype)
     assert bool((buf[1:M + 1, N:] == -77.0).all())
     assert bool((buf[0] == -77.0).all()) and bool((buf[M + 1] == -77.0).all())
+
+
+@pytest.mark.parametrize("M", [1, 17, 64, 128])
+@pytest.mark.parametrize("N,K", [(256, 128), (300, 2048), (5000, 640)])
+def test_tensor_memory_is_free_after_a_timeout(M, N, K):
+    """The tile kernel of every width, alone and in clusters, gives up on
+    copies that never complete, again and again; each time all of its tensor
+    memory is free for the paired kernel, which takes all columns of an SM."""
+    qa, sa, qb, sb = pair(M, N, K, seed=98)
+    qc, sc, qd, sd = pair(2100, 2600, 256, seed=99)
+    good, many = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), rn.rmsnorm_gemm_fp8(qc, sc, qd, sd)
+    assert rn.last_path() == rn.PATH_FP8_PAIR
+    torch.cuda.synchronize()
+    assert rn.wait_timeouts(reset=True) == 0
+    for _ in range(4):
+        try:
+            rn.set_stream_test_fault(16, 1000)
+            rn.rmsnorm_gemm_fp8(qa, sa, qb, sb)
+            assert rn.last_path() == rn.PATH_FP8_GEMM
+            torch.cuda.synchronize()
+        finally:
+            rn.set_stream_test_fault(0, 0)
+        assert rn.wait_timeouts(reset=True) > 0
+        assert torch.equal(rn.rmsnorm_gemm_fp8(qc, sc, qd, sd), many)
+        assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
+    torch.cuda.synchronize()
+    assert rn.wait_timeouts() == 0
