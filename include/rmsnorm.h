@@ -322,8 +322,10 @@ typedef enum { RMSNORM_E4M3 = 0, RMSNORM_E5M2 = 1 } rmsnorm_fp8_type;
  *   rstd = 1 / sqrt( (1/H) sum_j v_j^2 + eps )
  *   y_j  = v_j * rstd * w_j                              (fp32, not stored)
  * and for each group of 128 columns
- *   scale = max( max |y_j|, 2^-100 ) / F
- *   q_j   = y_j / scale rounded to nearest even in the format.
+ *   scale = max( max |y_j|, 2^-100 ) / F                 (rounded once)
+ *   q_j   = y_j / scale rounded to nearest even in the format, the quotient
+ *           formed in fp32 to within 2^-22 of its value: one that lies so
+ *           near the middle between two values may go to either.
  * y goes to 8 bits in one rounding: it is not rounded to the dtype first, as
  * the norm followed by rmsnorm_quant_fp8 would. A group that holds a NaN or
  * an infinity gets a NaN scale and NaN throughout.

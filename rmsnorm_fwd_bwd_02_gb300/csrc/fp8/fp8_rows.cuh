@@ -15,9 +15,13 @@
 // values flush towards zero. A group that holds a NaN or an infinity has no
 // scale: its scale and all of its q are NaN, so that what is computed from
 // it shows it.
-// q_j is formed as y_j (1 / s_g): the reciprocal and the product are each
-// rounded once in fp32 (2^-24), which can turn a quotient within 2^-22 of the
-// middle between two 8-bit values to the other neighbour, and nothing else.
+// s_g is that quotient, rounded once. q_j is formed as y_j (1 / s_g) with an
+// approximate reciprocal (1 ulp, 2^-23 of it at most) and a product rounded in
+// fp32 (2^-24): together within 2^-22 of the quotient, which can turn one that
+// lies so near the middle between two 8-bit values to the other neighbour, and
+// nothing else. (A division rounded in fp32 does the same within 2^-24: of
+// rows of bf16 values, whose quotients meet such middles often, 1.3 in 1000
+// elements come out otherwise than from the exact quotient, and 1.1 here.)
 //
 // What bounds it: DRAM. The plain norm reads 2 bytes and writes 1 an element
 // (bf16), with the residual it reads 4 and writes 3; the arithmetic is some
@@ -68,7 +72,17 @@ struct Fp8Scale {
     float s, inv;
     __device__ __forceinline__ Fp8Scale(float amax, int e5m2)
     {
-        s = fmaxf(amax, kFp8AmaxMin) * (e5m2 ? 1.f / 57344.f : 1.f / 448.f);
+        // m / F, correctly rounded. Both F are 448 times a power of two, and the
+        // quotient by the constant 448 is the product with its rounded
+        // reciprocal c, corrected once by its remainder (N. Brisebarre, J.-M.
+        // Muller, S. K. Raina, "Accelerating correctly rounded floating-point
+        // division when the divisor is known in advance", IEEE Trans. Computers
+        // 53, 2004; right for each of the 2^23 significands, and from 2^-100 on
+        // no step underflows). It takes no time that shows; a general division
+        // takes the norm at 262144 x 896 from 114 to 124 us.
+        constexpr float c = 1.f / 448.f;
+        const float m = fmaxf(amax, kFp8AmaxMin), t = m * c;
+        s = __fmaf_rn(__fmaf_rn(-448.f, t, m), c, t) * (e5m2 ? 0x1p-7f : 1.f);
         if (!(amax < __int_as_float(0x7f800000)))
             s = __int_as_float(0x7fffffff);
         // s is a normal number with a normal reciprocal (or NaN)

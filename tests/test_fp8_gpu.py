@@ -760,3 +760,26 @@ def test_tensor_memory_is_free_after_a_timeout(M, N, K):
         assert torch.equal(rn.rmsnorm_gemm_fp8(qa, sa, qb, sb), good)
     torch.cuda.synchronize()
     assert rn.wait_timeouts() == 0
+
+
+# ------------------------------------------------------- scales bit for bit
+@pytest.mark.parametrize("M,H", [(130, 1001), (300, 4096), (2, 16384), (257, 130)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("to", [E4M3, E5M2])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_scales_are_the_rounded_quotient(M, H, dtype, to, rows):
+    """scale = max / F rounded once to fp32: the bits of a division. q is the
+    quotient by it, formed to within 2^-22 (the reciprocal is off by 2^-23 at
+    most, the product by 2^-24), rounded to nearest even."""
+    x, _, _ = data(M, H, dtype, seed=M + H)
+    if dtype == F32:                              # every binade that has a scale of its own
+        e = torch.arange(M, dtype=F32) * (220.0 / M) - 99
+        x = x.clamp(-60, 60) * torch.exp2(e.round())[:, None]
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows, qdtype=to)
+    amax = group_amax(x.to(F64), rows).clamp(min=AMAX_MIN).to(F32)      # exact in fp32
+    want = amax / torch.tensor(LARGEST[to], dtype=F32)
+    assert torch.equal(s.cpu(), want)
+    v = x.to(F64) / spread(want.to(F64), rows, M, H)
+    a, b = round8(v * (1 - 2.0 ** -22), to), round8(v * (1 + 2.0 ** -22), to)
+    got = q.float().cpu().to(F64)
+    assert bool(((got >= torch.minimum(a, b)) & (got <= torch.maximum(a, b))).all())
