@@ -369,7 +369,10 @@ int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
  *   out_mn = round( sum_g a_scale[m,g] b_scale[n / 128,g]
  *                   sum_{k in group g} a_mk b_nk )
  * with the products of a group accumulated in fp32 on the tensor cores, the
- * groups in fp32, and one rounding to the dtype.
+ * groups in fp32, and one rounding to the dtype. The two scales of a term are
+ * multiplied first, in fp32: where that product is below 2^-126 and not zero
+ * the term loses precision, and where it passes fp32's range the term is
+ * infinite, or NaN if the group's sum is zero.
  *   a [M,K] (lda) of format a_type, a_scale [M,G];
  *   b [N,K] (ldb) of format b_type, b_scale [ceil(N / 128),G], where
  *   G = ceil(K / 128);

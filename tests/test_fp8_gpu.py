@@ -783,3 +783,36 @@ def test_scales_are_the_rounded_quotient(M, H, dtype, to, rows):
     a, b = round8(v * (1 - 2.0 ** -22), to), round8(v * (1 + 2.0 ** -22), to)
     got = q.float().cpu().to(F64)
     assert bool(((got >= torch.minimum(a, b)) & (got <= torch.maximum(a, b))).all())
+
+
+@pytest.mark.parametrize("M,path", [(5, 0), (60, 0), (200, 0), (700, rn.PATH_FP8_PAIR)])
+def test_products_of_scales_at_the_edges_of_their_range(M, path):
+    """Two scales may lie anywhere as long as their product is zero or a
+    normal number: at 2^-126 the terms are exact to fp32's precision, at 2^127
+    a group whose sum is zero adds zero. Past the range it is NaN, and only
+    in the row and the columns that meet there."""
+    qa, sa, qb, sb = pair(M, 400, 640, seed=96)
+    sa[0], sb[0] = 2.0 ** -100, 2.0 ** -26            # 2^-126 together
+    sa[1], sb[1] = 2.0 ** 100, 2.0 ** 27              # 2^127, of zeros
+    qa.view(torch.uint8)[1] = 0
+    sa[2] = 0.0
+    sb[2] *= 2.0 ** -20
+    sa[3] = 1.3 * 2.0 ** -116                         # below 2^-126 with all blocks but one
+    with forced(path):
+        out = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+        want, T = gemm64(qa, sa, qb, sb)
+        rows = [i for i in range(M) if i != 3]
+        check_out(out[rows], want[rows], T[rows], 640, F32)
+        # row 3: below 2^-126 a product of scales is a multiple of 2^-149, off by
+        # 2^-150 at most, which its group's sum (of terms T0 together, over the
+        # groups) multiplies; each of the five additions is off by 2^-150 more
+        _, T0 = gemm64(qa, torch.ones_like(sa), qb, torch.ones_like(sb))
+        bound = (128 + 5) * 2.0 ** -22 * T[3] + 2.0 ** -150 * (T0[3] + 5)
+        assert bool(((out[3].to(F64) - want[3]).abs() <= bound).all())
+        assert bool((out[1] == 0).all()) and bool((out[2] == 0).all())
+        sa[1, 2] = 2.0 ** 101
+        far = rn.rmsnorm_gemm_fp8(qa, sa, qb, sb, out_dtype=F32)
+    assert bool(torch.isnan(far[1, 128:256]).all())
+    keep = [i for i in range(M) if i != 1]
+    assert torch.equal(far[keep], out[keep])
+    assert torch.equal(far[:, :128], out[:, :128]) and torch.equal(far[:, 256:], out[:, 256:])
