@@ -382,8 +382,8 @@ int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
  *   RMSNORM_ERR_MISALIGNED; K itself may be any, and the bytes past K are
  *   not read into the result). Strides of tensors of one row are ignored.
  * Limits (else RMSNORM_ERR_UNSUPPORTED): M, N <= RMSNORM_FP8_MAX_ROWS,
- *   K <= RMSNORM_FP8_MAX_K, M * N / 2048 < 2^31; a driver that offers the
- *   tensor-map encoder.
+ *   K <= RMSNORM_FP8_MAX_K, ceil(M / 128) * ceil(N / 128) < 2^31; a driver
+ *   that offers the tensor-map encoder.
  * Performance: two kernels on tcgen05. Up to 64 tokens the weight's rows are
  *   the tensor cores' rows and K is split over clusters (one token, 896 ->
  *   2048: 2.7 us; 16 tokens, 4096 -> 24576: 18.3 us, 83 % of the copy

@@ -370,8 +370,6 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
     const bool swap = v < 3;
     const int BN = kBN[v];
     const int64_t ctas = tiles_r * tiles_c * KS;
-    if (ctas > INT32_MAX)
-        return RMSNORM_ERR_UNSUPPORTED;
     CUtensorMap mapA, mapB;
     unsigned int *tmo = stream_timeout_counter(dev);
     if (tmo == nullptr)
@@ -476,7 +474,10 @@ int rmsnorm_gemm_fp8(const void *a, int64_t lda, const float *a_scale, int a_typ
         return RMSNORM_ERR_BAD_DTYPE;
     if (M < 0 || N < 1 || K < 1)
         return RMSNORM_ERR_BAD_SHAPE;
-    if (M > RMSNORM_FP8_MAX_ROWS || N > RMSNORM_FP8_MAX_ROWS || K > RMSNORM_FP8_MAX_K)
+    // the grid: at most a CTA to a tile of 128 x 128 (clusters only where all
+    // of them run at once)
+    if (M > RMSNORM_FP8_MAX_ROWS || N > RMSNORM_FP8_MAX_ROWS || K > RMSNORM_FP8_MAX_K ||
+        ((M + 127) / 128) * ((N + 127) / 128) > INT32_MAX)
         return RMSNORM_ERR_UNSUPPORTED;
     // a single row has no stride: any that a tensor map takes
     if (M == 1)

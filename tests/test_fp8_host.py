@@ -119,3 +119,15 @@ def test_binding_refuses_cpu_tensors_and_types():
         rn.rmsnorm_gemm_fp8(x, s, q, s[:1])             # not an 8-bit type
     with pytest.raises(ValueError):
         rn.rmsnorm_gemm_fp8(q, s, q[:, :128], s[:1])    # two K
+
+
+def test_gemm_refuses_more_tiles_than_a_grid_holds(lib):  # noqa: F811
+    """ceil(M / 128) * ceil(N / 128) is below 2^31, whatever the addresses:
+    the refusal comes before any of them is looked at (a null output says
+    that the size itself was taken)."""
+    m, n = 1 << 23, 1 << 22                                   # 2^16 and 2^15 tiles
+    assert gemm(lib, M=m, N=n, ldo=n) == UNSUPPORTED
+    assert gemm(lib, M=m - 128, N=n, ldo=n, out=None) == NULLPTR
+    assert gemm(lib, M=m - 127, N=n, ldo=n, out=None) == UNSUPPORTED
+    assert gemm(lib, M=m, N=n - 128, ldo=n, out=None) == NULLPTR
+    assert gemm(lib, M=1 << 30, N=1 << 30, ldo=1 << 30) == UNSUPPORTED
