@@ -816,3 +816,24 @@ def test_products_of_scales_at_the_edges_of_their_range(M, path):
     keep = [i for i in range(M) if i != 1]
     assert torch.equal(far[keep], out[keep])
     assert torch.equal(far[:, :128], out[:, :128]) and torch.equal(far[:, 256:], out[:, 256:])
+
+
+@pytest.mark.parametrize("H", [1, 3])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_blocks_down_than_the_grid_holds(H, dtype):
+    """65537 blocks of 128 rows on 65535 CTAs: the first two CTAs take a second
+    block, with the shared sums of the first. Every block is checked."""
+    M = 65535 * 128 + 130
+    g = torch.Generator(device=DEV).manual_seed(120)
+    x = torch.randn(M, H, generator=g, device=DEV)
+    x *= torch.exp2(torch.arange(M, device=DEV) // 128 % 7 - 3.0)[:, None]
+    x = x.to(dtype)
+    q, s = rn.rmsnorm_quant_fp8(x, block_rows=128)
+    assert rn.last_path() == rn.PATH_FP8_BLOCKS and s.shape == (65537, 1)
+    amax = torch.nn.functional.pad(x.float().abs(), (0, 0, 0, -M % 128)).view(65537, -1).amax(dim=1)
+    want = amax / torch.tensor(LARGEST[E4M3], dtype=F32, device=DEV)
+    assert torch.equal(s[:, 0], want)
+    v = (x.to(F64) / want.to(F64).repeat_interleave(128)[:M, None]).cpu()
+    a, b = round8(v * (1 - 2.0 ** -22), E4M3), round8(v * (1 + 2.0 ** -22), E4M3)
+    got = q.float().cpu().to(F64)
+    assert bool(((got >= torch.minimum(a, b)) & (got <= torch.maximum(a, b))).all())
