@@ -475,7 +475,8 @@ def rmsnorm_fwd_fp8(x, w, r=None, q=None, scale=None, h=None, rstd=None, eps=1e-
     is [M, H] of qdtype (float8_e4m3fn or float8_e5m2), scale [M, ceil(H /
     128)]; q times its group's scale is the norm's output. The outputs that
     are not passed share one allocation where they take 256 KB or less
-    together (it is freed with the last of them)."""
+    together: keeping one keeps all of it, and torch.save, which refuses
+    tensors of two types in one storage, wants clones of them."""
     if stream is not None:
         with _on_stream(x, stream):
             return _fp8().fwd_fp8(x, w, r, q, scale, h, rstd, eps, qdtype, want_rstd)
@@ -486,8 +487,8 @@ def rmsnorm_quant_fp8(x, q=None, scale=None, block_rows=1, qdtype=torch.float8_e
                       stream=None):
     """x [M, H] (any row stride) rounded to 8 bits: (q, scale), with one fp32
     scale for each 128 columns of a row (block_rows=1, activations) or each
-    block of 128 x 128 (block_rows=128, weights); see rmsnorm.h. Outputs that
-    are not passed are allocated as rmsnorm_fwd_fp8's."""
+    block of 128 x 128 (block_rows=128, weights); see rmsnorm.h. An output
+    that is not passed has an allocation of its own, of any size."""
     if stream is not None:
         with _on_stream(x, stream):
             return _fp8().quant_fp8(x, q, scale, block_rows, qdtype)

@@ -13,6 +13,7 @@ tensor cores may truncate): (128 + G) 2^-22 T, and half a step of the
 output's type for the last rounding.
 """
 import gc
+import io
 
 import pytest
 import torch
@@ -837,3 +838,34 @@ def test_more_blocks_down_than_the_grid_holds(H, dtype):
     a, b = round8(v * (1 - 2.0 ** -22), E4M3), round8(v * (1 + 2.0 ** -22), E4M3)
     got = q.float().cpu().to(F64)
     assert bool(((got >= torch.minimum(a, b)) & (got <= torch.maximum(a, b))).all())
+
+
+@pytest.mark.parametrize("M,H", [(1, 128), (128, 896), (200, 1001), (4096, 896)])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantised_weights_can_be_saved(M, H, rows):
+    """A checkpoint of quantised weights: each output has a storage of its
+    own, which holds nothing else, and comes back from torch.save as it was."""
+    x, _, _ = data(M, H, BF16, seed=130)
+    q, s = rn.rmsnorm_quant_fp8(x.to(DEV), block_rows=rows)
+    assert q.untyped_storage().data_ptr() != s.untyped_storage().data_ptr()
+    file = io.BytesIO()
+    torch.save({"weight": q, "scale": s}, file)
+    file.seek(0)
+    back = torch.load(file, weights_only=True)
+    assert torch.equal(back["scale"], s) and back["weight"].dtype == q.dtype
+    assert torch.equal(back["weight"].view(torch.uint8), q.view(torch.uint8))
+    keep = q.view(torch.uint8).clone()
+    del s, back
+    rn.rmsnorm_quant_fp8(x.to(DEV) * 2, block_rows=rows)
+    assert torch.equal(q.view(torch.uint8), keep)
+
+
+def test_small_outputs_of_the_norm_are_saved_as_clones():
+    x, r, w = (t.to(DEV) for t in data(8, 896, BF16, seed=131))
+    outs = rn.rmsnorm_fwd_fp8(x, w, r=r)
+    file = io.BytesIO()
+    torch.save([t.clone() for t in outs], file)
+    file.seek(0)
+    for a, b in zip(outs, torch.load(file, weights_only=True)):
+        assert a.dtype == b.dtype and torch.equal(a.contiguous().view(torch.uint8),
+                                                  b.contiguous().view(torch.uint8))
