@@ -339,9 +339,9 @@ typedef enum { RMSNORM_E4M3 = 0, RMSNORM_E5M2 = 1 } rmsnorm_fp8_type;
  * Errors: those of rmsnorm_fwd_strided; RMSNORM_ERR_BAD_DTYPE for qtype too.
  * M == 0 launches nothing.
  * Performance: bound by DRAM where rows start at multiples of 32 bytes (and
- *   q's at 16): 32768 x 4096 bf16 in 62 us, 97 % of the measured copy
- *   bandwidth, 16384 x 5120 with the residual in 87 us, all of it. Rows at
- *   other addresses are read four bytes at a time, at about half of it.
+ *   q's at 16): 32768 x 4096 bf16 in 62.5 us, 96 % of the measured copy
+ *   bandwidth, 16384 x 5120 with the residual in 88 us, 98 %. Rows at other
+ *   addresses are read four bytes at a time, at about half of it.
  */
 int rmsnorm_fwd_fp8(const void *x, int64_t ldx, const void *r, int64_t ldr,
                     const void *w, void *q, int64_t ldq, float *scale, void *h,
@@ -386,10 +386,11 @@ int rmsnorm_quant_fp8(const void *x, int64_t ldx, void *q, int64_t ldq,
  *   that offers the tensor-map encoder.
  * Performance: two kernels on tcgen05. Up to 64 tokens the weight's rows are
  *   the tensor cores' rows and K is split over clusters (one token, 896 ->
- *   2048: 2.7 us; 16 tokens, 4096 -> 24576: 18.3 us, 83 % of the copy
- *   bandwidth); more tokens take 128 x 128 tiles while these run at once (two
- *   to an SM where K < 4096), then 256 x 256 tiles by pairs of CTAs (8192
- *   tokens, 4096 -> 24576: 590 us, 2.8 PFLOP/s).
+ *   2048: 2.7 us on the GPU, less than its launch on the host; 16 tokens,
+ *   4096 -> 24576: 18.3 us, 82 % of the copy bandwidth); more tokens take 128 x
+ *   128 tiles while these run at once (two to an SM where K < 4096; 256
+ *   tokens, 4096 -> 6144: 15 us), then 256 x 256 tiles by pairs of CTAs (8192
+ *   tokens, 4096 -> 24576: 645 to 662 us back to back, 2.5 PFLOP/s).
  * Aliasing: out may share no byte with an input. Deterministic: no atomics,
  *   sums in a fixed order. Any M from one token to a prompt's batch; M == 0
  *   launches nothing.

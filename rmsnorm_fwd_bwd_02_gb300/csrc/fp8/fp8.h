@@ -1,7 +1,6 @@
 // fp8.h -- argument blocks and kernel tables of the 8-bit path: rows or
 // blocks rounded to 8-bit floating point with a scale for every 128 columns
-// (fp8_rows.cuh, fp8_blocks.cuh), shared by the kernels and the host code
-// that launches them.
+// (fp8_rows.cuh), shared by the kernels and the host code that launches them.
 #pragma once
 
 #include <cuda_runtime.h>

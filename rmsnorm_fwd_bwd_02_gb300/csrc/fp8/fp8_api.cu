@@ -99,11 +99,12 @@ int row_blocks_per_sm(const void *fn, int threads, int dev, int *out)
 // Shape of a row kernel (fp8_rows.cuh) for M rows of H columns: rows that
 // share a warp where they are short enough; a lane a pack while the rows do
 // not fill the SMs (latency); else more packs a lane. Measured (GB300, bf16,
-// the norm): at 524288 x 128 eight lanes a row take 37 us; at 262144 x 896 a
-// warp a row takes 117 us, a CTA of two warps 141; at 32768 x 4096 two packs
-// a lane take 65 us, one 72. Wider rows take two packs a lane in 64 registers:
-// at 12160 x 11008 72 us (four packs a lane 76, three 70), at 16264 x 8192
-// 63.5 (64 and 71), at 8056 x 16384 66.2 (65.5 and 72).
+// the norm): at 524288 x 128 eight lanes a row take 35 us, sixteen 66, a warp
+// 126; at 262144 x 896 a warp a row takes 115 us, a CTA of one with two packs a
+// lane 112, of two with one pack 147; at 32768 x 4096 two packs a lane take
+// 62.5 us, one 90, and at 300 rows one takes 2.0, two 2.3. Wider rows take two
+// packs a lane in 64 registers: at 12160 x 11008 72 us (four packs a lane 76,
+// three 70), at 16264 x 8192 63 (64 and 71), at 8056 x 16384 66 (65.5 and 72).
 const Fp8RowKernel &pick_fp8_rows(const Fp8RowKernel *k, int width, int64_t M, int64_t H, int sms)
 {
     if (width > 0) {
@@ -293,12 +294,12 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
         return st;
     // Pairs of CTAs where tiles of 128 x 128 would not all run at once, two to
     // an SM, or, with a long K, one to an SM (two share its tensor cores), and
-    // a pair's tile of 256 rows is not half empty. Measured (GB300, tile kernel
-    // / pairs): one tile an SM, 256 x 6144 x 4096 15 / 18 us, 1024 x 1024 x
-    // 4096 12 / 18; two, 1024 x 2560 at K = 384 5.5 / 7.6, 2048 11.4 / 12.7,
-    // 5120 22.1 / 21.8, 1024 x 4096 at 768 7.5 / 9.5, 5120 24.6 / 22.8;
-    // more, 4096 x 1280 x 2048 19.9 / 19.9, 2048 x 24576 x 4096 319 / 158;
-    // 128 x 24576 x 4096 32 / 34.
+    // a pair's tile of 256 rows is not half empty. Measured (GB300, weights from
+    // DRAM, tile kernel / pairs): one tile an SM, 256 x 6144 x 4096 15.1 / 20.1
+    // us, 1024 x 1024 x 4096 10.9 / 19.4; two, 1024 x 2560 at K = 384 6.0 / 8.2,
+    // 2048 11.8 / 14.1, 5120 22.5 / 23.5, 1024 x 4096 at 768 7.8 / 10.3, 5120
+    // 24.8 / 24.0; more, 4096 x 1280 x 2048 20.4 / 21.9, 2048 x 24576 x 4096
+    // 210 / 161; one row of tiles, 128 x 24576 x 4096 23 / 37.
     const int64_t tm = (M + kPairTile - 1) / kPairTile, tn = (N + kPairTile - 1) / kPairTile;
     const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128);
     const int ov = g_test_gemm_fp8.load(std::memory_order_relaxed);
@@ -321,12 +322,12 @@ int gemm_impl(const Fp8GemmArgs &g, cudaStream_t stream)
         tiles_c = ((swap ? M : N) + BN - 1) / BN;
         // Clusters with which the whole grid runs at once (a few late ones
         // cost as much as all the others: 64 x 6144 x 4096 with three CTAs a
-        // cluster, of which 46 run at once, 21 us, with two 12), with a ring
+        // cluster, of which 46 run at once, 17 us, with two 10), with a ring
         // of up to six stages. Of those the one for which a CTA's groups and
         // the exchange with its peers take least (in units of 10 ns, fitted
         // to 896 -> 2048, 4096 -> 1024 and 1024 -> 1024 features at 8 to 200
-        // rows: 64 x 2048 x 896 takes 4.7 us with four CTAs, 5.5 with three,
-        // 5.9 with one, 4.9 with six). The runtime's count of clusters is
+        // rows: 64 x 2048 x 896 takes 4.9 us with four CTAs, 5.8 with three,
+        // 6.2 with one, 5.1 with six). The runtime's count of clusters is
         // that of one CTA an SM.
         static const int kGroup[4] = {25, 25, 27, 40}, kPeer[4] = {12, 15, 12, 40};
         KS = 0;

@@ -12,17 +12,17 @@
 // and as much from shared memory; a pair reads each row of A and of B once
 // for both SMs, 32 KB each. Reading the groups back is the other limit: 128 x
 // 256 sums a group and SM, 64 fp32 FMAs a cycle of the 128 an SM has, so the
-// tensor memory is loaded 16 columns at a time by sixteen warps (four on each
+// tensor memory is loaded 32 columns at a time by sixteen warps (four on each
 // of the SM's quarters, to hide the loads' latency behind one another's
 // arithmetic), and the scale of a row and group is one product a thread. The
 // sums take 64 registers a thread.
 //
 // Roles (kPairThreads threads a CTA): warp 0 copies this CTA's 128 rows of
 // A and 128 rows of B into the ring; warp 1 of the leader (rank 0) issues the
-// MMAs of both; the last two fetch the scales of this CTA's rows (a row's lie
+// MMAs of both; warps 2 and 3 fetch the scales of this CTA's rows (a row's lie
 // beside one another in memory, a thread wants one of a row of its own: read
 // by the threads that use them, a warp's 32 came from 32 lines a group); the
-// others keep the sums of this CTA's 128 rows. The copies
+// sixteen others keep the sums of this CTA's 128 rows. The copies
 // of both CTAs complete on the leader's `full` barrier; the MMAs' completion
 // is sent to both CTAs' `empty` and `accf` barriers, and both CTAs' readers
 // hand a buffer back on the leader's `acce` barrier. The ring and the two
@@ -43,7 +43,7 @@ constexpr int kPairLd = 32;                             // columns a load of ten
 constexpr int kPairScaleWarps = 2;                      // warps that fetch the scales
 constexpr int kPairThreads = 128 + 32 * kPairEpi;
 // Registers a thread: what the kernel is launched with, and what its first
-// four warps (copies, MMAs, scales) and the eight others take of that.
+// four warps (copies, MMAs, scales) and the sixteen others take of that.
 constexpr int kPairRegs = 96, kPairRegsCtl = 32, kPairRegsEpi = 112;
 static_assert(128 * kPairRegsCtl + 32 * kPairEpi * kPairRegsEpi <= kPairThreads * kPairRegs,
               "the shares fit what the CTA is launched with");

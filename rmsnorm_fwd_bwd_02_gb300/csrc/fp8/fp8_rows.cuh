@@ -40,11 +40,11 @@
 // group maxima and the conversion form one chain per row, so a CTA that
 // loads a row only when it has stored the one before leaves DRAM idle.
 // Asking for the next row before working on this one (AHEAD) takes the norm
-// at 32768 x 4096 from 72 to 65 us (two packs a lane, w read again from L1
-// for each row instead of held: 80 registers, six CTAs an SM; one pack a lane
-// takes 72 us, four 68). With the residual there are twice the loads in flight
-// for the same chain and the registers are worth more as occupancy: 90 us
-// without AHEAD at 16384 x 5120, 97 to 105 with it.
+// at 32768 x 4096 from 71 to 62.5 us (two packs a lane, w read again from L1
+// for each row instead of held: 80 registers, six CTAs an SM). With the
+// residual there are twice the loads in flight for the same chain and the
+// registers are worth more as occupancy: 88 us without AHEAD at 16384 x 5120,
+// 100 with it.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -105,8 +105,8 @@ __device__ __forceinline__ uint32_t fp8_pair(float lo, float hi, int e5m2)
 // inside a word, read through L1, where the lanes of a warp share the lines.
 // No word without a byte of the row is touched. (Aligned 16-byte words, the
 // neighbour's by shuffles, take a load where this takes five, but some 25
-// instructions more to put the bytes in their places: 59 against 41 us for
-// the norm at 8590 x 5597.)
+// instructions more to put the bytes in their places: the norm at 8590 x 5597,
+// 46 us, took some 18 us longer.)
 template <typename T> struct LooseRaw {
     static constexpr int E = 16 / (int)sizeof(T), NW = sizeof(T) == 2 ? 5 : 4;
     uint32_t w[NW];
