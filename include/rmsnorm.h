@@ -407,6 +407,159 @@ int rmsnorm_gemm_fp8(const void *a, int64_t lda, const float *a_scale,
                      void *stream);
 
 /*
+ * Attention heads: what follows a decoder block's q|k|v projection. Heads are
+ * given as rows of D features: row (t, h), token t of T and head h, starts at
+ * x + t x_token + h x_head (elements; any strides >= 0 for inputs, rows that
+ * do not overlap for outputs; the features of a row lie side by side). q, k
+ * and v may thus be windows of one fused projection's output, token-major or
+ * head-major. Strides of a direction of one step are ignored.
+ * 1 <= D <= RMSNORM_ROPE_MAX_D, T < 2^31 (else RMSNORM_ERR_UNSUPPORTED).
+ */
+#define RMSNORM_ROPE_MAX_D 256
+
+typedef struct {
+    const void *x;              /* in: [T, heads, D] */
+    int64_t x_token, x_head;
+    const void *w;              /* in: [D] weight of the heads' norm, or NULL: none */
+    void *y;                    /* out: [T, heads, D] */
+    int64_t y_token, y_head;
+    int64_t heads;
+} rmsnorm_heads;
+
+typedef struct {
+    const void *dy;             /* in: gradient of y */
+    int64_t dy_token, dy_head;
+    const void *x;              /* in: the forward's x (read only with w) */
+    int64_t x_token, x_head;
+    const void *w;              /* in: [D] or NULL, as in the forward */
+    void *dx;                   /* out: gradient of x */
+    int64_t dx_token, dx_head;
+    float *dw;                  /* out: [D] fp32 gradient of w (with w) */
+    int64_t heads;
+} rmsnorm_heads_grad;
+
+/*
+ * A rotation by positions. Of a row's first `rot` columns pair i turns by
+ * position * freq[i] radians; the columns past rot stay. Scaled contexts are
+ * other freq (and an amplitude); freq is finite, in 64 bits, in device
+ * memory. The angle is exact for every 64-bit position, negative ones too:
+ * freq / 2 pi is held as a 64-bit fraction of a turn and the product taken
+ * modulo whole turns, so the only error is freq's own rounding (2^-53) and
+ * 2^-32 of a turn. A NULL rotation, or rot 0, turns nothing.
+ */
+typedef struct {
+    const void *positions;      /* [T] int32 or int64 */
+    int position_bits;          /* 32 or 64 (else RMSNORM_ERR_BAD_DTYPE) */
+    const double *freq;         /* [rot / 2] radians a position */
+    int64_t rot;                /* even, 0 <= rot <= D (else RMSNORM_ERR_BAD_SHAPE) */
+    int adjacent;               /* 1: pairs (2i, 2i + 1); 0: (i, i + rot / 2)
+                                   (else RMSNORM_ERR_BAD_FLAGS) */
+    float amplitude;            /* factor of the turned columns; 1 unless a scaled
+                                   context wants another (finite, else
+                                   RMSNORM_ERR_BAD_EPS) */
+} rmsnorm_rotation;
+
+/*
+ * The heads' RMSNorm, where w is not NULL (QK-norm: rstd = 1 / sqrt((1/D)
+ * sum x^2 + eps), z = x rstd w; else z = x), then the rotation: for a pair
+ * (a, b) of z and its angle t, amplitude * (a cos t - b sin t, b cos t +
+ * a sin t), in fp32 and rounded once to the dtype.
+ *   q in and out; k the same, or NULL (or with no heads) for q alone; q and k
+ *   may have a weight each, or one of them none;
+ *   rstd [T, q heads + k heads] fp32 out or NULL (rows of heads without a
+ *   weight are left as they are).
+ * Aliasing: y may be exactly x (same strides); nothing else may share a byte.
+ * T == 0 launches nothing.
+ * Performance: one launch, one pass. See the kernel's notes in rope.cuh.
+ */
+int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k,
+                     const rmsnorm_rotation *rot, float *rstd, int64_t T,
+                     int64_t D, float eps, int dtype, void *stream);
+
+/*
+ * Its backward: dy turned back, then the norm's backward,
+ *   g = the transposed rotation of dy;  c = (1/D) sum_j w_j g_j x_j
+ *   dx = rstd (w g - x rstd^2 c)   (g without w), rounded once
+ *   dw = sum over tokens and heads of g x rstd, in fp32: one partial row per
+ *   CTA, added in a fixed order (deterministic).
+ *   rstd: the forward's, or NULL: computed from x again.
+ *   workspace: rmsnorm_rope_bwd_workspace_bytes(D) bytes of device memory,
+ *   16-byte aligned, the call's own until it is done (not read where no part
+ *   has a weight; it may then be NULL).
+ * Aliasing: dx may be exactly dy or exactly x; nothing else may share a byte.
+ * T == 0 sets dw to zero.
+ */
+int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k,
+                     const rmsnorm_rotation *rot, const float *rstd,
+                     void *workspace, size_t workspace_bytes, int64_t T,
+                     int64_t D, float eps, int dtype, void *stream);
+
+/* Bytes of rmsnorm_rope_bwd's workspace on the current device (0 on invalid
+ * arguments or without a device). */
+size_t rmsnorm_rope_bwd_workspace_bytes(int64_t D);
+
+/*
+ * New tokens into a paged cache: q (or NULL) and k as rmsnorm_rope_fwd, q to
+ * its y, k and v to the cache's rows for the tokens' slots. v is stored as it
+ * is (its w is NULL, else RMSNORM_ERR_UNSUPPORTED).
+ *   slots [T] int32 or int64 (slot_bits): page * page_size + place in the
+ *   page. A token whose slot is negative or past the cache is not stored (the
+ *   padding of a batch); its q is computed all the same. Slots are distinct:
+ *   of two tokens with one slot either may be stored, or parts of both.
+ *   cache rows of the dtype: row (page, place, head) of k at k->y + page
+ *   k_page + place k->y_token + head k->y_head (elements), of v likewise; both
+ *   tensors [pages, page_size, heads, D] in any order of strides. They may
+ *   interleave in one buffer, but share no byte (only their starts are
+ *   checked).
+ * Rows of other slots are left as they are. T == 0 launches nothing.
+ */
+int rmsnorm_rope_append(const rmsnorm_heads *q, const rmsnorm_heads *k,
+                        const rmsnorm_heads *v, const rmsnorm_rotation *rot,
+                        const void *slots, int slot_bits, int64_t pages,
+                        int64_t page_size, int64_t k_page, int64_t v_page,
+                        int64_t T, int64_t D, float eps, int dtype, void *stream);
+
+/*
+ * The same into a cache held in 4 bits. A value stands for code * scale * g:
+ * a code of four bits (sign, two bits of exponent, one of fraction: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives), an e4m3 scale for each 16 features
+ * of a row, and an fp32 scale g for each head (k_scale, v_scale [heads],
+ * positive; NULL: 1), which brings values far below 2^-6 or above 2688 into
+ * the range of the e4m3 scales. 4.5 bits a value. Rounding, from the fp32
+ * values of k after the rotation and from v:
+ *   scale = max |x| / (6 g), rounded once to e4m3, within 2^-9 and 448;
+ *   code  = x / (scale g), the quotient in fp32, rounded to nearest even, at
+ *   most 6 in magnitude. A NaN counts for nothing in the maximum and is
+ *   stored as 6: a cache that this call writes holds no NaN.
+ * Layout: [pages, heads, page_size / 16, 18 D] bytes, dense, 16-byte aligned;
+ * the 18 D bytes of 16 tokens: keys' codes [16][D / 2], keys' scales
+ * [16][D / 16], values' codes [D / 16][16][8], values' scales [D / 16][16];
+ * a byte holds two neighbouring features, the even one in its low half.
+ * D is 64 or 128, page_size a multiple of 16 (else RMSNORM_ERR_UNSUPPORTED).
+ * k and v: y is not looked at.
+ */
+int rmsnorm_rope_append_kv4(const rmsnorm_heads *q, const rmsnorm_heads *k,
+                            const rmsnorm_heads *v, const rmsnorm_rotation *rot,
+                            const void *slots, int slot_bits, void *cache,
+                            int64_t pages, int64_t page_size,
+                            const float *k_scale, const float *v_scale,
+                            int64_t T, int64_t D, float eps, int dtype,
+                            void *stream);
+
+/*
+ * Rows of a 4-bit cache as 8-bit rows with their scales, exactly (to hand a
+ * sequence on to another cache, or to look at it): for slot slots[i], k
+ * [n, heads, D] and v the codes' values as e4m3, k_scale [n, heads, D / 16]
+ * and v_scale the scales as e4m3 (a value is the product, times the head's
+ * g). Zeros for a slot outside the cache. All outputs dense; k and v 16-byte
+ * aligned.
+ */
+int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
+                     int64_t heads, int64_t D, const void *slots, int slot_bits,
+                     int64_t n, void *k, void *k_scale, void *v, void *v_scale,
+                     void *stream);
+
+/*
  * Bytes of workspace rmsnorm_bwd, rmsnorm_residual_bwd, rmsnorm_bwd_ex,
  * rmsnorm_bwd_strided and rmsnorm_bwd_bwd need for (M, H, dtype) on the
  * current CUDA device (one fp32 row of H per CTA of the backward grid; the
@@ -451,7 +604,9 @@ void rmsnorm_set_path_override(int path);
  * product on tcgen05, automatic above 8 rows on rows of 2048 features or
  * more; each also takes the rows only it holds), 9 the 8-bit rows
  * (rmsnorm_fwd_fp8, rmsnorm_quant_fp8), 10 the 8-bit blocks, 11 the 8-bit
- * product a tile a CTA or cluster, 12 the same by pairs of CTAs, 0 none. */
+ * product a tile a CTA or cluster, 12 the same by pairs of CTAs, 13 the
+ * rotation of heads and its backward, 14 the append to a cache, 15 the reading
+ * of a 4-bit cache, 0 none. */
 int rmsnorm_last_path(void);
 
 /*

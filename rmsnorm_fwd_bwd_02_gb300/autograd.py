@@ -135,6 +135,54 @@ class ResidualRMSNormFunction(torch.autograd.Function):
         return gx, gr, dw, None
 
 
+class RMSNormRopeFunction(torch.autograd.Function):
+    """q and k heads [T, heads, D] after their RMSNorm (where a weight is
+    given), turned by their positions; returns (yq, yk). The backward is one
+    kernel over both and their weights' partial sums; it is differentiable
+    once."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, positions, freq, eps: float, interleaved: bool, amplitude: float):
+        yq, yk, rstd = _rn.rmsnorm_rope_fwd(_heads3d(q), positions, freq, k=_heads3d(k), wq=wq, wk=wk,
+                                            eps=float(eps), interleaved=interleaved, amplitude=amplitude)
+        ctx.save_for_backward(q if wq is not None else None, k if wk is not None else None, wq, wk,
+                              positions, freq, rstd)
+        ctx.how = (float(eps), interleaved, amplitude)
+        ctx.shapes = (q.shape, k.shape, q.dtype, q.device)
+        return yq, yk
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, positions, freq, rstd = ctx.saved_tensors
+        sq, sk, dtype, dev = ctx.shapes
+        eps, interleaved, amplitude = ctx.how
+        # an output that nothing used brings no gradient
+        dyq = torch.zeros(sq, dtype=dtype, device=dev) if dyq is None else dyq
+        dyk = torch.zeros(sk, dtype=dtype, device=dev) if dyk is None else dyk
+        dq, dk, dwq, dwk = _rn.rmsnorm_rope_bwd(
+            _heads3d(dyq), None if q is None else _heads3d(q), positions, freq, dyk=_heads3d(dyk),
+            k=None if k is None else _heads3d(k), wq=wq, wk=wk, rstd=rstd, eps=eps,
+            interleaved=interleaved, amplitude=amplitude)
+        need = ctx.needs_input_grad
+        return (dq if need[0] else None, dk if need[1] else None,
+                dwq.to(wq.dtype) if need[2] and wq is not None else None,
+                dwk.to(wk.dtype) if need[3] and wk is not None else None, None, None, None, None, None)
+
+
+def _heads3d(t):
+    """t [T, heads, D] with unit stride over the features: itself, or a copy."""
+    if not t.is_cuda:
+        raise ValueError("rms_norm_rope: tensors must be on a CUDA device")
+    return t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def rms_norm_rope(q, k, positions, freq, wq=None, wk=None, eps: float = 1e-6, interleaved: bool = False,
+                  amplitude: float = 1.0):
+    """(yq, yk) of rmsnorm_rope_fwd, differentiable in q, k, wq and wk."""
+    return RMSNormRopeFunction.apply(q, k, wq, wk, positions, freq, eps, interleaved, amplitude)
+
+
 def rms_norm(x, weight, eps: float = 1e-6):
     return RMSNormFunction.apply(x, weight, eps)
 

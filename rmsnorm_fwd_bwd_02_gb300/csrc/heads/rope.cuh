@@ -1,0 +1,613 @@
+// rope.cuh -- heads turned by their positions, after the heads' RMSNorm where
+// there is one (QK-norm): forward, on the way into a paged cache, backward.
+//
+// Mathematics. A head's row x of D features is z = x, or z = x r w with
+// r = 1 / sqrt(mean x^2 + eps); of its first `rot` columns pair i, (a, b) =
+// (z_i, z_{i + rot/2}) or (z_{2i}, z_{2i+1}), becomes
+//     (s (a cos t - b sin t), s (b cos t + a sin t)),   t = position * freq_i,
+// with an amplitude s; the other columns stay. The backward turns dy back
+// (g = the transposed map) and goes on as the norm's: c = mean(w g x),
+// dx = r (w g - x r^2 c), dw = sum over tokens and heads of g x r.
+//
+// Angles. A float product position * freq has lost the angle's fraction at
+// far positions (2^-24 of 10^5 radians is 0.006), and 64-bit floating point
+// is slow on this GPU. Here freq / 2 pi becomes once, per thread, a 64-bit
+// fixed-point fraction of a turn; position * fraction modulo 2^64 is then
+// plain integer arithmetic in which whole turns drop out by themselves: three
+// integer multiply-adds give the top 32 bits for any 64-bit position. Their
+// top two bits, rounded, are the quadrant; the rest is an angle of at most
+// pi / 4, for which the Taylor polynomials (to x^9 and x^10, within 3e-9)
+// give sine and cosine. No table of positions is kept or read.
+//
+// Layout. Packs of 16 bytes; a lane holds the two packs of a row whose
+// elements pair up (i and i + rot/2, or neighbours), so a row takes D / 16
+// lanes (16-bit types) and no data crosses lanes but the norm's sum. A group
+// of lanes takes a piece of HC heads of one token, four of them at a time (to
+// have enough loads in flight), and computes the sines once for the piece.
+// Bound by DRAM: one pass, every row read and written once.
+#pragma once
+
+#include "../common.cuh"
+#include "heads.h"
+
+namespace rmsk {
+
+// 16-bit formats, 8-byte packs (heads whose halves are no multiple of 16 bytes).
+template <typename T> struct Pack<T, 4, typename Half16<T>::Tag> {
+    using C = Half16<T>;
+    uint2 u;
+    static constexpr int E = 4;
+    __device__ __forceinline__ static Pack load(const void *base, int64_t idx)
+    {
+        Pack p;
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(p.u.x), "=r"(p.u.y)
+                     : "l"(static_cast<const uint2 *>(base) + idx));
+        return p;
+    }
+    __device__ __forceinline__ static Pack load_cached(const void *base, int64_t idx)
+    {
+        Pack p; p.u = __ldg(static_cast<const uint2 *>(base) + idx); return p;
+    }
+    __device__ __forceinline__ void store(void *base, int64_t idx) const
+    {
+        asm volatile("st.global.v2.u32 [%0], {%1,%2};" ::"l"(static_cast<uint2 *>(base) + idx),
+                     "r"(u.x), "r"(u.y)
+                     : "memory");
+    }
+    __device__ __forceinline__ void widen(Vals<4> &f) const
+    {
+        f.v[0] = C::wide2(u.x);
+        f.v[1] = C::wide2(u.y);
+    }
+    __device__ __forceinline__ static Pack narrow(const Vals<4> &f)
+    {
+        Pack p;
+        p.u.x = C::narrow2(f.v[0].x, f.v[0].y); p.u.y = C::narrow2(f.v[1].x, f.v[1].y);
+        return p;
+    }
+    __device__ __forceinline__ static Pack zero() { Pack p; p.u = make_uint2(0, 0); return p; }
+};
+
+__device__ __forceinline__ int64_t ld_index(const void *p, int64_t i, int wide)
+{
+    return wide ? __ldg(static_cast<const long long *>(p) + i)
+                : (int64_t)__ldg(static_cast<const int *>(p) + i);
+}
+
+// freq (radians a position) as a fraction of a turn, 2^64 to the turn.
+__device__ __forceinline__ uint64_t turn_fraction(double freq)
+{
+    double t = freq * 0.15915494309189533577;            // 1 / (2 pi)
+    t -= floor(t);
+    return (uint64_t)__double2ull_rz(t * 18446744073709551616.0);
+}
+
+// sine and cosine of 2 pi * fraction * pos
+__device__ __forceinline__ void sincos_turn(uint64_t fraction, int64_t pos, float &s, float &c)
+{
+    const uint32_t fl = (uint32_t)fraction, fh = (uint32_t)(fraction >> 32);
+    const uint32_t pl = (uint32_t)pos, ph = (uint32_t)((uint64_t)pos >> 32);
+    const uint32_t t = __umulhi(fl, pl) + fh * pl + fl * ph;
+    const uint32_t quad = (t + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(t - (quad << 30)) * 1.46291807926715968e-9f;   // 2 pi / 2^32
+    const float x2 = x * x;
+    float ps = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+    ps = fmaf(x2, ps, 1.f / 120.f);
+    ps = fmaf(x2, ps, -1.f / 6.f);
+    ps = fmaf(x2 * x, ps, x);
+    float pc = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+    pc = fmaf(x2, pc, -1.f / 720.f);
+    pc = fmaf(x2, pc, 1.f / 24.f);
+    pc = fmaf(x2, pc, -0.5f);
+    pc = fmaf(x2, pc, 1.f);
+    const bool swap = quad & 1u;
+    s = swap ? pc : ps;
+    c = swap ? ps : pc;
+    if (quad & 2u)
+        s = -s;
+    if ((quad + 1u) & 2u)
+        c = -c;
+}
+
+// The packs that a lane holds of a row, and how many of its pairs turn. Slot
+// v of a lane is pair of packs number lane + v L.
+struct RopeSlot {
+    int a, b;            // pack indices; the row has `np`
+    int turns;           // of its E pairs the first `turns` turn
+};
+
+template <int E, bool ADJ>
+__device__ __forceinline__ RopeSlot rope_slot(int pair, int rot, int adjacent)
+{
+    const int half = rot / (2 * E);
+    const int n = rot / 2 - pair * E;
+    RopeSlot s;
+    s.turns = n < 0 ? 0 : (n > E ? E : n);
+    // past the turning pairs the packs follow in order (2 pair, 2 pair + 1)
+    const bool halves = !ADJ && !(E == 1 && adjacent) && pair < half;
+    s.a = halves ? pair : 2 * pair;
+    s.b = halves ? pair + half : 2 * pair + 1;
+    return s;
+}
+
+// (a, b) turned by the E angles of a slot; sn negated turns back.
+template <int E, bool ADJ>
+__device__ __forceinline__ void rope_turn(Vals<E> &a, Vals<E> &b, const float (&cs)[E],
+                                          const float (&sn)[E], int turns)
+{
+    if constexpr (ADJ) {
+        // pairs lie within a pack: a has the first E / 2, b the others
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float2 &v = e < E / 2 ? a.v[e] : b.v[e - E / 2];
+            const float2 t = make_float2(fmaf(v.x, cs[e], -(v.y * sn[e])), fmaf(v.y, cs[e], v.x * sn[e]));
+            if (e < turns)
+                v = t;
+        }
+    } else if (turns) {
+        using F = typename Vals<E>::F;
+#pragma unroll
+        for (int i = 0; i < Vals<E>::N; ++i) {
+            F c, s, m;
+            if constexpr (E == 1) {
+                c = cs[0]; s = sn[0]; m = -sn[0];
+            } else {
+                c = make_float2(cs[2 * i], cs[2 * i + 1]);
+                s = make_float2(sn[2 * i], sn[2 * i + 1]);
+                m = make_float2(-sn[2 * i], -sn[2 * i + 1]);
+            }
+            const F x = a.v[i], y = b.v[i];
+            a.v[i] = vfma(x, c, vmul(y, m));
+            b.v[i] = vfma(y, c, vmul(x, s));
+        }
+    }
+}
+
+// Sum over the 2^shift lanes of a group; all lanes of the warp take part.
+__device__ __forceinline__ float lanes_sum(float v, int shift)
+{
+    for (int o = (1 << shift) >> 1; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+template <int E, int V>
+struct RopeAngles {
+    uint64_t f[V][E];
+    float cs[V][E], sn[V][E];
+    __device__ __forceinline__ void init(const RopeTurn &t, const RopeSlot (&s)[V], const int (&pair)[V])
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[v][e] = e < s[v].turns ? turn_fraction(__ldg(t.freq + pair[v] * E + e)) : 0;
+    }
+    // sign: 1 to turn, -1 to turn back
+    __device__ __forceinline__ void at(int64_t pos, float amp, float sign)
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                sincos_turn(f[v][e], pos, sn[v][e], cs[v][e]);
+                sn[v][e] *= amp * sign;
+                cs[v][e] *= amp;
+            }
+    }
+};
+
+// ------------------------------------------------------------ 4-bit rows
+// 16 values of a group as eight bytes of e2m1 codes (the even one in a byte's
+// low half) and one e4m3 scale (fp32 g: the head's own): the scale is
+// max / (6 g) rounded once, between 2^-9 and 448; a code is the quotient
+// x / (scale g) in fp32 rounded to nearest even, at most 6. A NaN counts for
+// nothing in the maximum and is stored as the largest code.
+__device__ __forceinline__ uint2 quant4(const float (&x)[16], float g, uint8_t &scale)
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        m = fmaxf(m, fabsf(x[i]));
+    const float t = fminf(fmaxf(__fdiv_rn(m, 6.f * g), 0.001953125f), 448.f);
+    uint16_t s8;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s8) : "f"(0.f), "f"(t));
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(s8));
+    const float d = Half16<f16>::wide1((uint16_t)h2) * g;
+    scale = (uint8_t)s8;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t b;
+        const float lo = __fdiv_rn(x[2 * i], d), hi = __fdiv_rn(x[2 * i + 1], d);
+        asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+            : "=r"(b)
+            : "f"(hi), "f"(lo));
+        w[i >> 2] |= b << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Byte offsets in a tile of 16 tokens of one head (18 D bytes): the keys'
+// codes [16][D / 2] and scales [16][D / 16], the values' codes [D / 16][16][8]
+// and scales [D / 16][16].
+__host__ __device__ constexpr int kv4_tile_bytes(int D) { return 18 * D; }
+__host__ __device__ constexpr int kv4_kscale(int D) { return 8 * D; }
+__host__ __device__ constexpr int kv4_v(int D) { return 9 * D; }
+__host__ __device__ constexpr int kv4_vscale(int D) { return 17 * D; }
+
+constexpr int kRopeStage = 640;            // floats of a warp's staged rows (append)
+
+// Rows of a warp in shared memory as fp32, a group of 16 in 20 words (reads
+// of whole groups then meet no bank twice); lane g of a row's lanes rounds
+// group g and writes it to its tile.
+__device__ __forceinline__ void store_tile4(const float *stage, int D, int lane, uint8_t *tile, int t,
+                                            bool is_v, float g)
+{
+    const int G = D / kKv4Group;
+    if (lane >= G)
+        return;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(stage + lane * 20 + 4 * i);
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    }
+    uint8_t s;
+    const uint2 c = quant4(x, g, s);
+    uint8_t *codes = is_v ? tile + kv4_v(D) + lane * 128 + t * 8 : tile + t * (D / 2) + lane * 8;
+    uint8_t *scale = is_v ? tile + kv4_vscale(D) + lane * 16 + t : tile + kv4_kscale(D) + t * G + lane;
+    *reinterpret_cast<uint2 *>(codes) = c;
+    *scale = s;
+}
+
+template <typename T, int E, bool ADJ, bool APP>
+__global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
+{
+    constexpr int V = E == 1 ? 4 : 1, U = E == 1 ? 1 : 4;
+    using P = Pack<T, E>;
+    __shared__ __align__(16) float stage_all[APP ? (kRopeThreads / 32) * kRopeStage : 4];
+
+    const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
+    const int chunks = p.part[0].chunks + p.part[1].chunks + (APP ? p.part[2].chunks : 0);
+    RopeSlot slot[V];
+    int pair[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        pair[v] = lane + v * L;
+        slot[v] = rope_slot<E, ADJ>(pair[v], p.turn.rot, p.turn.adjacent);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    RopeAngles<E, V> ang;
+    ang.init(p.turn, slot, pair);
+
+    const int64_t items = p.T * chunks;
+    const int64_t step = (int64_t)gridDim.x * (kRopeThreads >> p.shift);
+    // the warp's first group decides when the warp is done (its lanes stay
+    // together in the sums' shuffles)
+    const int64_t g0 = ((int64_t)blockIdx.x * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
+    int64_t item = g0 + ((threadIdx.x & 31) >> p.shift);
+    int64_t t = item / chunks;
+    int c = (int)(item - t * chunks);
+    const int64_t dt = step / chunks;
+    const int dc = (int)(step - dt * chunks);
+    for (int64_t first = g0; first < items; first += step, item += step) {
+        const bool live = item < items;
+        // which heads
+        int ci = c, part = 0;
+        if (ci >= p.part[0].chunks) {
+            ci -= p.part[0].chunks;
+            part = 1;
+            if (APP && ci >= p.part[1].chunks) {
+                ci -= p.part[1].chunks;
+                part = 2;
+            }
+        }
+        const RopeRows &r = p.part[part];
+        const int h0 = ci * p.HC, h1 = live ? min(r.heads, h0 + p.HC) : 0;
+        const bool turn = p.turn.rot > 0 && part < 2;
+        if (turn && live)
+            ang.at(ld_index(p.turn.pos, t, p.turn.pos64), p.turn.amp, 1.f);
+        P wa[V], wb[V];
+        const bool norm = r.w != nullptr && live;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (norm) {
+                wa[v] = slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
+                wb[v] = slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
+            }
+        // the cache's rows of this token
+        int64_t page = 0, within = 0;
+        bool kept = true;
+        if (APP && part > 0 && live) {
+            const int64_t s = ld_index(p.cache.slots, t, p.cache.slot64);
+            kept = s >= 0 && s < p.cache.limit;
+            page = kept ? s / p.cache.page_size : 0;
+            within = kept ? s - page * p.cache.page_size : 0;
+        }
+        const char *xr = static_cast<const char *>(r.x) + (live ? t * r.xt * (int64_t)sizeof(T) : 0);
+        for (int hc = 0; hc < p.HC; hc += U) {
+            P xa[U][V], xb[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + hc + u;
+                if (h < h1 && hc + u < p.HC && kept) {
+                    const char *x = xr + h * r.xh * (int64_t)sizeof(T);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        xa[u][v] = slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
+                        xb[u][v] = slot[v].b < np ? P::load(x, slot[v].b) : P::zero();
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        xa[u][v] = xb[u][v] = P::zero();
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (hc + u >= p.HC)
+                    break;                       // the same for all lanes
+                const int h = h0 + hc + u;
+                const bool on = h < h1 && kept;
+                Vals<E> a[V], b[V];
+                using F = typename Vals<E>::F;
+                F ss = splat<F>(0.f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    xa[u][v].widen(a[v]);
+                    xb[u][v].widen(b[v]);
+                }
+                if (p.part[0].w != nullptr || p.part[1].w != nullptr) {      // the same for all lanes
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int i = 0; i < Vals<E>::N; ++i)
+                            ss = vfma(b[v].v[i], b[v].v[i], vfma(a[v].v[i], a[v].v[i], ss));
+                    const float rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
+                    if (norm) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            Vals<E> fa, fb;
+                            wa[v].widen(fa);
+                            wb[v].widen(fb);
+#pragma unroll
+                            for (int i = 0; i < Vals<E>::N; ++i) {
+                                a[v].v[i] = vmul(vmul(a[v].v[i], splat<F>(rs)), fa.v[i]);
+                                b[v].v[i] = vmul(vmul(b[v].v[i], splat<F>(rs)), fb.v[i]);
+                            }
+                        }
+                        if (on && lane == 0 && p.rstd != nullptr && part < 2)
+                            p.rstd[t * (p.part[0].heads + p.part[1].heads) + (part ? p.part[0].heads : 0) +
+                                   h] = rs;
+                    }
+                }
+                if (turn)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+                if (APP && p.cache.bits4) {
+                    // k and v go through shared memory, a group a lane
+                    float *stage = stage_all + (threadIdx.x >> 5) * kRopeStage +
+                                   ((threadIdx.x & 31) >> p.shift) * (p.D / kKv4Group) * 20;
+                    __syncwarp();
+                    if (on && part > 0) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                const int ia = slot[v].a * E + e, ib = slot[v].b * E + e;
+                                if (ia < p.D)
+                                    stage[(ia >> 4) * 20 + (ia & 15)] = a[v].get(e);
+                                if (ib < p.D)
+                                    stage[(ib >> 4) * 20 + (ib & 15)] = b[v].get(e);
+                            }
+                    }
+                    __syncwarp();
+                    if (on && part > 0) {
+                        const float *gs = part == 1 ? p.cache.kscale : p.cache.vscale;
+                        uint8_t *tile = static_cast<uint8_t *>(p.part[1].y) + page * p.cache.kpage +
+                                        (h * (p.cache.page_size / kKv4Tile) + within / kKv4Tile) *
+                                            kv4_tile_bytes(p.D);
+                        store_tile4(stage, p.D, lane, tile, (int)(within % kKv4Tile), part == 2,
+                                    gs ? __ldg(gs + h) : 1.f);
+                        continue;
+                    }
+                }
+                if (on) {
+                    char *y = static_cast<char *>(r.y);
+                    if (APP && part > 0)
+                        y += (page * (part == 1 ? p.cache.kpage : p.cache.vpage) + within * r.yt + h * r.yh) *
+                             (int64_t)sizeof(T);
+                    else
+                        y += (t * r.yt + h * r.yh) * (int64_t)sizeof(T);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (slot[v].a < np)
+                            P::narrow(a[v]).store(y, slot[v].a);
+                        if (slot[v].b < np)
+                            P::narrow(b[v]).store(y, slot[v].b);
+                    }
+                }
+            }
+        }
+        t += dt;
+        c += dc;
+        if (c >= chunks) {
+            c -= chunks;
+            ++t;
+        }
+    }
+}
+
+// The backward. A CTA works on the q heads or on the k heads alone, so that it
+// has one dw; its partial row is summed over its groups in a fixed order and
+// added up by rope_dw_reduce.
+template <typename T, int E, bool ADJ>
+__global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p)
+{
+    constexpr int V = E == 1 ? 4 : 1, U = E == 1 ? 1 : 2;
+    using P = Pack<T, E>;
+    using F = typename Vals<E>::F;
+    __shared__ float sums[kRopeThreads * 2 * E * V];
+
+    const int part = blockIdx.x >= p.ctas_q ? 1 : 0;
+    const RopeGradRows &r = p.part[part];
+    const int64_t ctas = part ? (int)gridDim.x - p.ctas_q : p.ctas_q;
+    const int cta = part ? (int)blockIdx.x - p.ctas_q : (int)blockIdx.x;
+    const int heads_all = p.part[0].heads + p.part[1].heads, head0 = part ? p.part[0].heads : 0;
+    const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
+    const bool norm = r.w != nullptr;                          // the same for the CTA
+    RopeSlot slot[V];
+    int pair[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        pair[v] = lane + v * L;
+        slot[v] = rope_slot<E, ADJ>(pair[v], p.turn.rot, p.turn.adjacent);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    RopeAngles<E, V> ang;
+    ang.init(p.turn, slot, pair);
+    P wa[V], wb[V];
+    Vals<E> da[V], db[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        wa[v] = norm && slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
+        wb[v] = norm && slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
+        da[v] = Vals<E>::zero();
+        db[v] = Vals<E>::zero();
+    }
+
+    const int chunks = r.chunks;
+    const int64_t items = p.T * chunks, step = ctas * (kRopeThreads >> p.shift);
+    const int64_t g0 = ((int64_t)cta * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
+    int64_t item = g0 + ((threadIdx.x & 31) >> p.shift);
+    int64_t t = item / chunks;
+    int c = (int)(item - t * chunks);
+    const int64_t dt = step / chunks;
+    const int dc = (int)(step - dt * chunks);
+    for (int64_t first = g0; first < items; first += step, item += step) {
+        const bool live = item < items;
+        const int h0 = c * p.HC, h1 = live ? min(r.heads, h0 + p.HC) : 0;
+        if (p.turn.rot > 0 && live)
+            ang.at(ld_index(p.turn.pos, t, p.turn.pos64), p.turn.amp, -1.f);
+        for (int hc = 0; hc < p.HC; hc += U) {
+            P ya[U][V], yb[U][V], xa[U][V], xb[U][V];
+            float rsv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + hc + u;
+                const bool on = h < h1 && hc + u < p.HC;
+                const char *y = static_cast<const char *>(r.dy) + (t * r.yt + h * r.yh) * (int64_t)sizeof(T);
+                const char *x = static_cast<const char *>(r.x) + (t * r.xt + h * r.xh) * (int64_t)sizeof(T);
+                rsv[u] = on && norm && p.rstd != nullptr ? __ldg(p.rstd + t * heads_all + head0 + h) : 0.f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    ya[u][v] = on && slot[v].a < np ? P::load(y, slot[v].a) : P::zero();
+                    yb[u][v] = on && slot[v].b < np ? P::load(y, slot[v].b) : P::zero();
+                    if (norm) {
+                        xa[u][v] = on && slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
+                        xb[u][v] = on && slot[v].b < np ? P::load(x, slot[v].b) : P::zero();
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (hc + u >= p.HC)
+                    break;
+                const int h = h0 + hc + u;
+                const bool on = h < h1;
+                Vals<E> a[V], b[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    ya[u][v].widen(a[v]);
+                    yb[u][v].widen(b[v]);
+                    if (p.turn.rot > 0)
+                        rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+                }
+                if (norm) {
+                    Vals<E> fa[V], fb[V];
+                    F ss = splat<F>(0.f), sc = splat<F>(0.f);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        Vals<E> ga, gb;
+                        xa[u][v].widen(fa[v]);
+                        xb[u][v].widen(fb[v]);
+                        wa[v].widen(ga);
+                        wb[v].widen(gb);
+#pragma unroll
+                        for (int i = 0; i < Vals<E>::N; ++i) {
+                            const F tx = vmul(a[v].v[i], fa[v].v[i]), ty = vmul(b[v].v[i], fb[v].v[i]);
+                            sc = vfma(ty, gb.v[i], vfma(tx, ga.v[i], sc));
+                            ss = vfma(fb[v].v[i], fb[v].v[i], vfma(fa[v].v[i], fa[v].v[i], ss));
+                        }
+                    }
+                    float rs = rsv[u];
+                    if (p.rstd == nullptr)
+                        rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
+                    const float cm = lanes_sum(hsum(sc), p.shift) / (float)p.D;
+                    const float k = -rs * rs * rs * cm;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        Vals<E> ga, gb;
+                        wa[v].widen(ga);
+                        wb[v].widen(gb);
+#pragma unroll
+                        for (int i = 0; i < Vals<E>::N; ++i) {
+                            const F xa1 = vmul(fa[v].v[i], splat<F>(rs)), xb1 = vmul(fb[v].v[i], splat<F>(rs));
+                            if (on) {
+                                da[v].v[i] = vfma(a[v].v[i], xa1, da[v].v[i]);
+                                db[v].v[i] = vfma(b[v].v[i], xb1, db[v].v[i]);
+                            }
+                            a[v].v[i] = vfma(vmul(a[v].v[i], ga.v[i]), splat<F>(rs),
+                                             vmul(fa[v].v[i], splat<F>(k)));
+                            b[v].v[i] = vfma(vmul(b[v].v[i], gb.v[i]), splat<F>(rs),
+                                             vmul(fb[v].v[i], splat<F>(k)));
+                        }
+                    }
+                }
+                if (on) {
+                    char *d = static_cast<char *>(r.dx) + (t * r.dt + h * r.dh) * (int64_t)sizeof(T);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (slot[v].a < np)
+                            P::narrow(a[v]).store(d, slot[v].a);
+                        if (slot[v].b < np)
+                            P::narrow(b[v]).store(d, slot[v].b);
+                    }
+                }
+            }
+        }
+        t += dt;
+        c += dc;
+        if (c >= chunks) {
+            c -= chunks;
+            ++t;
+        }
+    }
+    if (!norm)
+        return;
+    const int grp = threadIdx.x >> p.shift, groups = kRopeThreads >> p.shift;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (slot[v].a < np)
+                sums[grp * p.D + slot[v].a * E + e] = da[v].get(e);
+            if (slot[v].b < np)
+                sums[grp * p.D + slot[v].b * E + e] = db[v].get(e);
+        }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.D; d += kRopeThreads) {
+        float s = 0.f;
+        for (int g = 0; g < groups; ++g)
+            s += sums[g * p.D + d];
+        p.partial[(int64_t)blockIdx.x * p.D + d] = s;
+    }
+}
+
+} // namespace rmsk

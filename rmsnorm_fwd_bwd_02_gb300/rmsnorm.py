@@ -5,12 +5,14 @@ checked (CUDA, contiguous or row-strided, dtype, shape), outputs that the
 caller did not pass are allocated with torch, and raw device pointers, row
 strides and the current torch CUDA stream are handed to the library. Every arithmetic step runs in the
 CUDA kernels. If the library has not been built this module raises at load
-time; there is no fallback. The 8-bit calls are marshalled in C++
-(csrc/fp8/fp8_torch.cpp) for their time on the host.
+time; there is no fallback. The 8-bit calls and those on attention heads are
+marshalled in C++ (csrc/fp8/fp8_torch.cpp, csrc/heads/heads_torch.cpp) for
+their time on the host.
 """
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 
 import torch
@@ -29,6 +31,7 @@ PATH_GEMV_UMMA = 7       # the product on tcgen05 (7); 6 and 7 also force it
 PATH_GEMV_TC = 8         # persistent tcgen05 kernel, y held per CTA (8; forces it)
 PATH_FP8_ROWS, PATH_FP8_BLOCKS = 9, 10            # reported only
 PATH_FP8_GEMM, PATH_FP8_PAIR = 11, 12             # the 8-bit product's kernels
+PATH_ROPE, PATH_ROPE_APPEND, PATH_KV4_READ = 13, 14, 15      # reported only
 
 # Entry points of include/rmsnorm.h with their ctypes signatures.
 _i64, _vp, _sz, _int, _f = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
@@ -71,6 +74,18 @@ SIGNATURES = {
     "rmsnorm_gemm_fp8": (_int, [_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _vp,
                                 _i64, _i64, _i64, _i64, _int, _int, _vp]),
 }
+
+SIGNATURES.update({
+    "rmsnorm_rope_fwd": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _f, _int, _vp]),
+    "rmsnorm_rope_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _f, _int, _vp]),
+    "rmsnorm_rope_bwd_workspace_bytes": (_sz, [_i64]),
+    "rmsnorm_rope_append": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _i64, _i64,
+                                   _i64, _f, _int, _vp]),
+    "rmsnorm_rope_append_kv4": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp, _vp,
+                                       _i64, _i64, _f, _int, _vp]),
+    "rmsnorm_kv4_read": (_int, [_vp, _i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp,
+                                _vp]),
+})
 
 BWD_ACCUMULATE_DW = 1
 
@@ -432,31 +447,45 @@ FP8_MAX_K, FP8_MAX_ROWS = 1 << 24, 1 << 30
 GEMM_FP8_STATIC_WEIGHTS = 1
 
 
-# The 8-bit calls of a decode step run for 2 to 4 us on the GPU. Their checks,
-# output allocation and marshalling are in a small C++ module over the C ABI
-# (csrc/fp8/fp8_torch.cpp); in Python they took 13 to 18 us a call.
+# The 8-bit calls of a decode step, and those on its heads, run for 2 to 4 us
+# on the GPU. Their checks, output allocation and marshalling are in small C++
+# modules over the C ABI (csrc/fp8/fp8_torch.cpp, csrc/heads/heads_torch.cpp);
+# in Python they took 13 to 18 us a call.
 FP8_LIB_PATH = os.path.join(PKG, "_fp8_torch.so")
-_fp8_mod = None
+HEADS_LIB_PATH = os.path.join(PKG, "_heads_torch.so")
+_fp8_mod = _heads_mod = None
+
+
+def _binding(path, functions):
+    """The loaded binding at `path`, handed the library's functions (raises if
+    it was not built)."""
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build it with "
+            "`python -c 'import __graft_entry__ as g; g.build()'` "
+            "(there is no CPU fallback)")
+    name = os.path.basename(path)[:-3]
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(mod)
+    mod.init(*(ctypes.cast(getattr(lib(), f), _vp).value for f in functions), _check)
+    return mod
 
 
 def _fp8():
-    """The loaded binding of the 8-bit calls (raises if it was not built)."""
     global _fp8_mod
     if _fp8_mod is None:
-        if not os.path.exists(FP8_LIB_PATH):
-            raise RuntimeError(
-                f"{FP8_LIB_PATH} is missing: build it with "
-                "`python -c 'import __graft_entry__ as g; g.build()'` "
-                "(there is no CPU fallback)")
-        loader = importlib.machinery.ExtensionFileLoader("_fp8_torch", FP8_LIB_PATH)
-        mod = importlib.util.module_from_spec(
-            importlib.util.spec_from_loader("_fp8_torch", loader))
-        loader.exec_module(mod)
-        l = lib()
-        mod.init(*(ctypes.cast(f, _vp).value for f in
-                   (l.rmsnorm_fwd_fp8, l.rmsnorm_quant_fp8, l.rmsnorm_gemm_fp8)), _check)
-        _fp8_mod = mod
+        _fp8_mod = _binding(FP8_LIB_PATH, ("rmsnorm_fwd_fp8", "rmsnorm_quant_fp8", "rmsnorm_gemm_fp8"))
     return _fp8_mod
+
+
+def _heads():
+    global _heads_mod
+    if _heads_mod is None:
+        _heads_mod = _binding(HEADS_LIB_PATH, (
+            "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
+            "rmsnorm_rope_append", "rmsnorm_rope_append_kv4", "rmsnorm_kv4_read"))
+    return _heads_mod
 
 
 def _on_stream(t, stream):
@@ -513,6 +542,128 @@ def rmsnorm_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16,
         with _on_stream(a, stream):
             return _fp8().gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
     return _fp8().gemm_fp8(a, a_scale, b, b_scale, out, out_dtype, static_weights)
+
+
+ROPE_MAX_D = 256
+KV4_TILE = 16                       # tokens of a 4-bit cache stored together
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=None,
+                     beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """(freq, amplitude) of a rotation of `rot` columns: freq is a float64
+    tensor [rot / 2] of radians a position, base^(-2i / rot), for contexts
+    longer than `original` positions scaled by `factor`:
+    None       as they are;
+    "linear"   positions compressed: every frequency / factor;
+    "ntk"      another base, base * factor^(rot / (rot - 2)), which leaves the
+               fastest pair alone and slows the slowest by `factor`;
+    "yarn"     pairs that turn more than beta_fast times in `original`
+               positions as they are, those that turn fewer than beta_slow
+               times / factor, a ramp over the pairs between them; amplitude
+               0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and at least 2, got {rot}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    n, amplitude = rot // 2, 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    freq = [base ** (-2.0 * i / rot) for i in range(n)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if original is None or original <= 0:
+            raise ValueError("'yarn' needs original, the positions that the model was trained on")
+
+        def pair(turns):        # the pair (as a real number) that turns so often in `original`
+            return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low = max(math.floor(pair(beta_fast)), 0)
+        high = min(math.ceil(pair(beta_slow)), rot - 1)
+        ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(n)]
+        freq = [f * (1 - r) + f / factor * r for f, r in zip(freq, ramp)]
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return torch.tensor(freq, dtype=torch.float64, device=device), amplitude
+
+
+def rmsnorm_rope_fwd(q, positions, freq, k=None, wq=None, wk=None, yq=None, yk=None, eps=1e-6,
+                     interleaved=False, amplitude=1.0, want_rstd=True, stream=None):
+    """Heads q [T, heads, D] (and k) after the heads' RMSNorm, where wq (wk)
+    is given, turned by their positions (see rmsnorm.h). Any strides over
+    tokens and heads. positions [T] int32 or int64; freq float64 [rot / 2]
+    radians a position (rope_frequencies), which turns the first rot columns
+    in pairs (i, i + rot / 2), or (2i, 2i + 1) when interleaved. positions and
+    freq None: no rotation. Returns (yq, yk or None, rstd or None); rstd
+    [T, q heads + k heads] is what the backward wants of a norm. Outputs that
+    are not passed are dense and may share one allocation."""
+    if stream is not None:
+        with _on_stream(q, stream):
+            return _heads().rope_fwd(q, positions, freq, k, wq, wk, yq, yk, eps, interleaved, amplitude,
+                                     want_rstd)
+    return _heads().rope_fwd(q, positions, freq, k, wq, wk, yq, yk, eps, interleaved, amplitude, want_rstd)
+
+
+def rmsnorm_rope_bwd(dyq, q, positions, freq, dyk=None, k=None, wq=None, wk=None, rstd=None, dq=None,
+                     dk=None, eps=1e-6, interleaved=False, amplitude=1.0, stream=None):
+    """(dq, dk or None, dwq or None, dwk or None) of rmsnorm_rope_fwd for the
+    gradients dyq and dyk of its outputs; dw in float32. q (k) is read only
+    where it has a norm, and may be None without one; rstd None: computed
+    again."""
+    if stream is not None:
+        with _on_stream(dyq, stream):
+            return _heads().rope_bwd(dyq, q, positions, freq, dyk, k, wq, wk, rstd, dq, dk, eps,
+                                     interleaved, amplitude)
+    return _heads().rope_bwd(dyq, q, positions, freq, dyk, k, wq, wk, rstd, dq, dk, eps, interleaved,
+                             amplitude)
+
+
+def rmsnorm_rope_append(k, v, positions, freq, slots, cache_k, cache_v, q=None, wq=None, wk=None, yq=None,
+                        eps=1e-6, interleaved=False, amplitude=1.0, stream=None):
+    """k and v [T, heads, D] into the slots of a paged cache, k (and q) on the
+    way through rmsnorm_rope_fwd. cache_k, cache_v [pages, page_size, heads,
+    D] of k's dtype, any strides but the last. slots [T] int32 or int64: page
+    * page_size + place, distinct; tokens with a negative slot, or one past the
+    cache, are not stored. Returns q's output (yq), or None without q."""
+    if stream is not None:
+        with _on_stream(k, stream):
+            return _heads().append(k, v, positions, freq, slots, cache_k, cache_v, q, wq, wk, yq, eps,
+                                   interleaved, amplitude, None, None, False)
+    return _heads().append(k, v, positions, freq, slots, cache_k, cache_v, q, wq, wk, yq, eps, interleaved,
+                           amplitude, None, None, False)
+
+
+def kv4_cache(pages, heads, page_size, head_dim, device="cuda"):
+    """A 4-bit cache of zeros for rmsnorm_rope_append_kv4: uint8 [pages,
+    heads, page_size / 16, 18 head_dim] (the layout is in rmsnorm.h)."""
+    if page_size < 1 or page_size % KV4_TILE:
+        raise ValueError(f"page_size must be a multiple of {KV4_TILE}, got {page_size}")
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    return torch.zeros(pages, heads, page_size // KV4_TILE, 18 * head_dim, dtype=torch.uint8, device=device)
+
+
+def rmsnorm_rope_append_kv4(k, v, positions, freq, slots, cache, q=None, wq=None, wk=None, yq=None, eps=1e-6,
+                            interleaved=False, amplitude=1.0, k_scale=None, v_scale=None, stream=None):
+    """rmsnorm_rope_append into a 4-bit cache (kv4_cache): e2m1 codes with an
+    e4m3 scale for each 16 features of a row, and an optional float32 scale
+    for each head (k_scale, v_scale [heads]); see rmsnorm.h."""
+    if stream is not None:
+        with _on_stream(k, stream):
+            return _heads().append(k, v, positions, freq, slots, cache, None, q, wq, wk, yq, eps,
+                                   interleaved, amplitude, k_scale, v_scale, True)
+    return _heads().append(k, v, positions, freq, slots, cache, None, q, wq, wk, yq, eps, interleaved,
+                           amplitude, k_scale, v_scale, True)
+
+
+def rmsnorm_kv4_read(cache, slots, stream=None):
+    """Rows of a 4-bit cache as 8-bit rows: (k, k_scale, v, v_scale), all
+    float8_e4m3fn and exact, k and v [n, heads, D], the scales [n, heads,
+    D / 16]; zeros for slots outside the cache."""
+    if stream is not None:
+        with _on_stream(cache, stream):
+            return _heads().kv4_read(cache, slots)
+    return _heads().kv4_read(cache, slots)
 
 
 STATIC_SCRATCH_BYTES = 16 << 20     # RMSNORM_STATIC_SCRATCH_BYTES
