@@ -560,6 +560,54 @@ int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
                      void *stream);
 
 /*
+ * Attention over a 4-bit cache: for query token i of a sequence's n, a head h
+ * of `heads` and its key head h / (heads / kv_heads),
+ *   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j),
+ * over the sequence's cached tokens j < len - n + i + 1: the last of the n
+ * query tokens is the last one cached (rmsnorm_rope_append_kv4 first, then
+ * this call). Products in fp16 on the tensor cores with fp32 sums: the cached
+ * values are exact in fp16, q is scaled by a power of two for each row, the
+ * softmax's terms are rounded to fp16 in the sum over v (not in their own).
+ *   q [T, heads, D], out [T, heads, D]: bf16 or fp16 (else
+ *   RMSNORM_ERR_BAD_DTYPE), strides as for rmsnorm_heads;
+ *   lse [T, heads] fp32 out or NULL: log sum_j exp(scale q . k_j), with which
+ *   results over several caches can be joined;
+ *   cache, pages, page_size, kv_heads, k_scale, v_scale: as written by
+ *   rmsnorm_rope_append_kv4;
+ *   block_table [B, blocks] int32, rows table_stride apart: the pages of a
+ *   sequence in order. Tokens in a page outside the cache count as masked;
+ *   seq_lens [B] int32: tokens cached, at most blocks * page_size count;
+ *   q_starts [B + 1] int32: sequence b has the query tokens q_starts[b] to
+ *   q_starts[b + 1] - 1; NULL: one token each (T == B, else
+ *   RMSNORM_ERR_BAD_SHAPE). Rows of q that belong to no sequence are not
+ *   read, and those of out and lse are left as they are.
+ * A row that sees no token gives zeros, and lse -infinity. The lengths, starts
+ * and table are read on the device: a captured call replays with others.
+ *   workspace: rmsnorm_kv4_attention_workspace_bytes(D) bytes, 16-byte
+ *   aligned, the call's own until it is done; nothing in it needs clearing.
+ * Limits (else RMSNORM_ERR_UNSUPPORTED): D 64 or 128; page_size a multiple of
+ * 16; blocks * page_size < 2^31 - 1024; B <= 2^20; heads <= 2^20; (T + B) *
+ * heads < 2^31. scale is finite (else RMSNORM_ERR_BAD_EPS).
+ * Aliasing: outputs may share no byte with an input or each other.
+ * Deterministic: parts of a long sequence are joined in a fixed order.
+ */
+int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
+                          void *out, int64_t out_token, int64_t out_head,
+                          float *lse, const void *cache, int64_t pages,
+                          int64_t page_size, int64_t kv_heads,
+                          const float *k_scale, const float *v_scale,
+                          const int *block_table, int64_t table_stride,
+                          int64_t blocks, const int *seq_lens,
+                          const int *q_starts, int64_t B, int64_t T,
+                          int64_t heads, int64_t D, float scale,
+                          void *workspace, size_t workspace_bytes, int dtype,
+                          void *stream);
+
+/* Bytes of rmsnorm_kv4_attention's workspace on the current device (0 for
+ * another D, or without a device). */
+size_t rmsnorm_kv4_attention_workspace_bytes(int64_t D);
+
+/*
  * Bytes of workspace rmsnorm_bwd, rmsnorm_residual_bwd, rmsnorm_bwd_ex,
  * rmsnorm_bwd_strided and rmsnorm_bwd_bwd need for (M, H, dtype) on the
  * current CUDA device (one fp32 row of H per CTA of the backward grid; the
@@ -606,7 +654,7 @@ void rmsnorm_set_path_override(int path);
  * (rmsnorm_fwd_fp8, rmsnorm_quant_fp8), 10 the 8-bit blocks, 11 the 8-bit
  * product a tile a CTA or cluster, 12 the same by pairs of CTAs, 13 the
  * rotation of heads and its backward, 14 the append to a cache, 15 the reading
- * of a 4-bit cache, 0 none. */
+ * of a 4-bit cache, 16 the attention over one, 0 none. */
 int rmsnorm_last_path(void);
 
 /*

@@ -107,4 +107,50 @@ struct Kv4ReadParams {
 };
 extern const void *const kv4_read_kernel;
 
+// Attention over a 4-bit cache (kv4_attend.cuh).
+struct Kv4Params {
+    const void *q;             // rows (t, h) at q + t qt + h qh (elements)
+    int64_t qt, qh;
+    void *out;
+    int64_t ot, oh;
+    float *lse;                // [T, heads] or nullptr
+    const uint8_t *cache;
+    int64_t pages;
+    int tpp;                   // tiles a page
+    const float *kscale, *vscale;
+    const int *table;          // [B, blocks], rows table_ld apart
+    int64_t table_ld;
+    int blocks;
+    const int *lens;           // [B]
+    const int *starts;         // [B + 1] first rows of the sequences, or nullptr: one each
+    int B, T, Hk, G;           // G query heads to a key head
+    float scale;
+    int vec;                   // q and out rows start at 16 bytes
+    float *ws;                 // partial results, two a CTA
+    uint32_t extra_tx, wait_limit_us;
+    unsigned int *timeouts;
+};
+
+constexpr int kKv4Warps = 8;
+constexpr int kKv4Slot = 32;               // tokens a stage
+constexpr int kKv4Unit = kKv4Warps * kKv4Slot;
+// Shared memory of a CTA: the warps' rings, then their mbarriers.
+__host__ __device__ constexpr int kv4_stages(int D) { return D == 128 ? 3 : 6; }
+__host__ __device__ constexpr int kv4_slot_bytes(int D) { return kKv4Slot / kKv4Tile * 18 * D; }
+__host__ __device__ constexpr int kv4_smem(int D)
+{
+    return kKv4Warps * kv4_stages(D) * (kv4_slot_bytes(D) + 8);
+}
+// CTAs of a grid to an SM: the ring and the registers allow two of 8 rows.
+__host__ __device__ constexpr int kv4_ctas_per_sm(int NT) { return NT == 1 ? 2 : 1; }
+// Floats of one partial result: NT * 8 rows of D sums, then their maxima and
+// denominators.
+__host__ __device__ constexpr int kv4_partial(int D, int NT) { return 8 * NT * (D + 2); }
+
+// [dtype: bf16, fp16][D: 64, 128][NT - 1]
+struct Kv4Kernels {
+    const void *attend[2][2][2], *combine[2][2][2];
+};
+extern const Kv4Kernels kv4_kernels;
+
 } // namespace rmsk

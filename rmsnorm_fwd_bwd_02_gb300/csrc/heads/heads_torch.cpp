@@ -8,6 +8,9 @@
 // addresses and the Python function that raises a status.
 #include "../binding.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace {
 
 decltype(&rmsnorm_rope_fwd) g_fwd = nullptr;
@@ -16,6 +19,8 @@ decltype(&rmsnorm_rope_bwd_workspace_bytes) g_bwd_bytes = nullptr;
 decltype(&rmsnorm_rope_append) g_append = nullptr;
 decltype(&rmsnorm_rope_append_kv4) g_append4 = nullptr;
 decltype(&rmsnorm_kv4_read) g_read = nullptr;
+decltype(&rmsnorm_kv4_attention) g_attend = nullptr;
+decltype(&rmsnorm_kv4_attention_workspace_bytes) g_attend_bytes = nullptr;
 
 void on_cuda(const Tensor &t, const char *name)
 {
@@ -394,12 +399,94 @@ PyObject *kv4_read(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// init(addresses of rope_fwd, rope_bwd, rope_bwd_workspace_bytes, rope_append, rope_append_kv4, kv4_read, check)
+// A contiguous int32 tensor of one dimension.
+const int *int32s(const Tensor &t, const char *name, int64_t n, at::Device dev)
+{
+    on_device(t, name, dev);
+    if (t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) != n || !t.is_contiguous())
+        refuse(c10::str(name, " must be a contiguous int32 tensor of shape [", n, "], got ", t.scalar_type(), " ",
+                        t.sizes()));
+    return static_cast<const int *>(t.data_ptr());
+}
+
+// kv4_attention(q, cache, block_table, seq_lens, q_starts, k_scale, v_scale, scale, out, lse, want_lse, workspace)
+PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (!count(n, 12))
+        return nullptr;
+    const Tensor &q = tensor(a[0], "q"), &c = tensor(a[1], "cache"), &table = tensor(a[2], "block_table"),
+                 &lens = tensor(a[3], "seq_lens");
+    const Tensor *starts = optional(a[4], "q_starts"), *ks = optional(a[5], "k_scale"),
+                 *vs = optional(a[6], "v_scale"), *out_in = optional(a[8], "out"), *lse_in = optional(a[9], "lse"),
+                 *ws_in = optional(a[11], "workspace");
+    const int want = PyObject_IsTrue(a[10]);
+    if (want < 0)
+        return nullptr;
+    three_d(q, "q");
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+    const ScalarType dtype = q.scalar_type();
+    const int code = row_code(dtype);
+    const at::Device dev = q.device();
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)std::max<int64_t>(D, 1)) : number(a[7]);
+    int64_t qt, qh;
+    heads(q, "q", T, H, D, dtype, dev, qt, qh);
+    const Cache4 s = cache4(c, "cache", -1, dev);
+    const int64_t Hk = c.size(1);
+    if (s.D != D)
+        refuse(c10::str("cache has heads of ", s.D, " features, q of ", D));
+    on_device(table, "block_table", dev);
+    if (table.scalar_type() != at::kInt || table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+        refuse(c10::str("block_table must be an int32 tensor of shape [sequences, blocks] with unit stride over "
+                        "its blocks, got ", table.scalar_type(), " ", table.sizes()));
+    const int64_t B = table.size(0), blocks = table.size(1), ld = B > 1 ? table.stride(0) : blocks;
+    const int *lensp = int32s(lens, "seq_lens", B, dev);
+    const int *startsp = starts ? int32s(*starts, "q_starts", B + 1, dev) : nullptr;
+    if (!starts && T != B)
+        refuse(c10::str("q has ", T, " tokens for ", B, " sequences: pass q_starts"));
+    const float *ksp = head_scale(ks, "k_scale", Hk, dev), *vsp = head_scale(vs, "v_scale", Hk, dev);
+    int64_t ot = H * D, oh = D;
+    if (out_in)
+        heads(*out_in, "out", T, H, D, dtype, dev, ot, oh);
+    if (lse_in)
+        fp32(*lse_in, "lse", {T, H}, dev);
+    if (ws_in) {
+        on_device(*ws_in, "workspace", dev);
+        if (!ws_in->is_contiguous())
+            refuse("workspace must be contiguous");
+    }
+
+    const c10::cuda::CUDAGuard guard(dev);
+    const bool new_lse = want && !lse_in;
+    Outputs made((out_in ? 0 : bytes_of(q.numel(), dtype)) + (new_lse ? bytes_of(T * H, at::kFloat) : 0));
+    const Tensor out = out_in ? *out_in : made.dense({T, H, D}, dtype);
+    const Tensor lse = lse_in ? *lse_in : new_lse ? made.dense({T, H}, at::kFloat) : Tensor();
+    // the call's own memory of this stream, free again for what runs behind it
+    const Tensor ws = ws_in ? *ws_in : Outputs().dense({(int64_t)g_attend_bytes(D)}, at::kByte);
+    const int st = g_attend(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                            lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr, c.data_ptr(), s.pages,
+                            s.page_size, Hk, ksp, vsp, static_cast<const int *>(table.data_ptr()), ld, blocks,
+                            lensp, startsp, B, T, H, D, (float)scale, ws.data_ptr(), ws.nbytes(), code,
+                            stream_of(dev));
+    if (st != RMSNORM_OK)
+        return raised(st, "rmsnorm_kv4_attention");
+    PyObject *r = PyTuple_New(2);
+    if (r == nullptr)
+        return nullptr;
+    PyTuple_SET_ITEM(r, 0, given(a[8], out));
+    PyTuple_SET_ITEM(r, 1, given(a[9], lse));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// init(addresses of rope_fwd, rope_bwd, rope_bwd_workspace_bytes, rope_append, rope_append_kv4, kv4_read,
+// kv4_attention, kv4_attention_workspace_bytes, check)
 PyObject *init(PyObject *, PyObject *args)
 {
-    unsigned long long f[6];
+    unsigned long long f[8];
     PyObject *check;
-    if (!PyArg_ParseTuple(args, "KKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &check))
+    if (!PyArg_ParseTuple(args, "KKKKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7],
+                          &check))
         return nullptr;
     g_fwd = reinterpret_cast<decltype(g_fwd)>((uintptr_t)f[0]);
     g_bwd = reinterpret_cast<decltype(g_bwd)>((uintptr_t)f[1]);
@@ -407,6 +494,8 @@ PyObject *init(PyObject *, PyObject *args)
     g_append = reinterpret_cast<decltype(g_append)>((uintptr_t)f[3]);
     g_append4 = reinterpret_cast<decltype(g_append4)>((uintptr_t)f[4]);
     g_read = reinterpret_cast<decltype(g_read)>((uintptr_t)f[5]);
+    g_attend = reinterpret_cast<decltype(g_attend)>((uintptr_t)f[6]);
+    g_attend_bytes = reinterpret_cast<decltype(g_attend_bytes)>((uintptr_t)f[7]);
     Py_INCREF(check);
     Py_XSETREF(g_check, check);
     Py_RETURN_NONE;
@@ -422,6 +511,7 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          {"rope_bwd", as_function(rope_bwd), METH_FASTCALL, nullptr},
                          {"append", as_function(append), METH_FASTCALL, nullptr},
                          {"kv4_read", as_function(kv4_read), METH_FASTCALL, nullptr},
+                         {"kv4_attention", as_function(kv4_attention), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_heads_torch", nullptr, -1, methods,

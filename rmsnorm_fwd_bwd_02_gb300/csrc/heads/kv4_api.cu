@@ -1,0 +1,126 @@
+// kv4_api.cu -- attention over a 4-bit cache: host-side argument checks, kernel
+// choice and launches of include/rmsnorm.h's rmsnorm_kv4_attention. No
+// allocation, no synchronisation, no host copies.
+#include "heads_host.h"
+
+#include "../registry.h"
+
+using namespace rmsk;
+
+namespace {
+
+constexpr int kPathKv4Attend = 16;
+
+size_t workspace_bytes(int sms, int64_t D)
+{
+    size_t most = 0;
+    for (int NT = 1; NT <= 2; ++NT)
+        most = std::max(most, (size_t)sms * kv4_ctas_per_sm(NT) * 2 * kv4_partial((int)D, NT) * 4);
+    return most;
+}
+
+} // namespace
+
+extern "C" {
+
+size_t rmsnorm_kv4_attention_workspace_bytes(int64_t D)
+{
+    int dev, sms;
+    if ((D != 64 && D != 128) || current_device(&dev) || sm_count(dev, &sms))
+        return 0;
+    return workspace_bytes(sms, D);
+}
+
+int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *out, int64_t out_token,
+                          int64_t out_head, float *lse, const void *cache, int64_t pages, int64_t page_size,
+                          int64_t kv_heads, const float *k_scale, const float *v_scale, const int *block_table,
+                          int64_t table_stride, int64_t blocks, const int *seq_lens, const int *q_starts,
+                          int64_t B, int64_t T, int64_t heads, int64_t D, float scale, void *workspace,
+                          size_t workspace_size, int dtype, void *stream)
+{
+    if (dtype != RMSNORM_BF16 && dtype != RMSNORM_F16)
+        return RMSNORM_ERR_BAD_DTYPE;
+    if (B < 0 || T < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || pages < 0 || page_size < 1 ||
+        blocks < 0 || (q_starts == nullptr && T != B))
+        return RMSNORM_ERR_BAD_SHAPE;
+    if (!std::isfinite(scale))
+        return RMSNORM_ERR_BAD_EPS;
+    if ((D != 64 && D != 128) || page_size % kKv4Tile || page_size > INT32_MAX || heads > (1 << 20) ||
+        pages > INT32_MAX || blocks > INT32_MAX || B > (1 << 20) || T > INT32_MAX ||
+        blocks > (INT32_MAX - 1024) / page_size || (T + B) > INT32_MAX / heads)
+        return RMSNORM_ERR_UNSUPPORTED;
+    if (!rows_within({T, heads, 1}, {q_token, q_head, 0}, D) ||
+        !rows_apart({T, heads, 1}, {out_token, out_head, 0}, D) ||
+        (B > 1 && (table_stride < blocks || table_stride > INT32_MAX)))
+        return RMSNORM_ERR_BAD_STRIDE;
+    if (T == 0 || B == 0)
+        return RMSNORM_OK;
+    if (!q || !out || !seq_lens || (blocks && !block_table) || (pages && !cache))
+        return RMSNORM_ERR_NULLPTR;
+    if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(cache, 16) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(q_starts, 4) ||
+        !aligned(workspace, 16))
+        return RMSNORM_ERR_MISALIGNED;
+    int dev, sms, st;
+    const Span so = heads_span(out, T, heads, D, out_token, out_head, 2);
+    const Span sl = flat(lse, (size_t)(T * heads) * 4), sw = flat(workspace, workspace_size);
+    const Span in[7] = {heads_span(q, T, heads, D, q_token, q_head, 2),
+                        flat(cache, (size_t)(pages * page_size * kv_heads * (D * 9 / 8))),
+                        flat(k_scale, (size_t)kv_heads * 4),
+                        flat(v_scale, (size_t)kv_heads * 4),
+                        blocks ? flat(block_table, (size_t)((B - 1) * (B > 1 ? table_stride : 0) + blocks) * 4)
+                               : Span{nullptr, 0, 0, 0},
+                        flat(seq_lens, (size_t)B * 4),
+                        flat(q_starts, (size_t)(B + 1) * 4)};
+    for (const Span &i : in)
+        if (overlap(so, i) || overlap(sl, i) || overlap(sw, i))
+            return RMSNORM_ERR_ALIAS;
+    if (overlap(so, sl) || overlap(so, sw) || overlap(sl, sw))
+        return RMSNORM_ERR_ALIAS;
+    if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)))
+        return st;
+    if (workspace == nullptr || workspace_size < workspace_bytes(sms, D))
+        return RMSNORM_ERR_WORKSPACE;
+
+    unsigned int *tmo = stream_timeout_counter(dev);
+    if (tmo == nullptr)
+        return cuda_fail(cudaErrorInvalidSymbol);
+    const int64_t G = heads / kv_heads;
+    // eight query rows a tile where a sequence's rows of one key head fit,
+    // else sixteen: the cache's bytes are widened once for both halves
+    const int64_t rows = (T + B - 1) / B * G;
+    const int NT = rows <= 8 ? 1 : 2, di = D == 128 ? 1 : 0, ti = dtype == RMSNORM_BF16 ? 0 : 1;
+    Kv4Params p = {q, q_token, q_head, out, out_token, out_head, lse, static_cast<const uint8_t *>(cache), pages,
+                   (int)(page_size / kKv4Tile), k_scale, v_scale, block_table, table_stride, (int)blocks, seq_lens,
+                   q_starts, (int)B, (int)T, (int)kv_heads, (int)G, scale,
+                   aligned(q, 16) && aligned(out, 16) &&
+                           strides_multiple(16, 2, {T > 1 ? q_token : 0, heads > 1 ? q_head : 0,
+                                                    T > 1 ? out_token : 0, heads > 1 ? out_head : 0})
+                       ? 1
+                       : 0,
+                   static_cast<float *>(workspace), g_test_extra_tx.load(std::memory_order_relaxed),
+                   g_test_wait_us.load(std::memory_order_relaxed), tmo};
+    const void *fn = kv4_kernels.attend[ti][di][NT - 1];
+    const int smem = kv4_smem((int)D);
+    int bps;
+    if ((st = blocks_per_sm(fn, kKv4Warps * 32, dev, &bps, smem)))
+        return st;
+    int ctas = sms * std::min(bps, kv4_ctas_per_sm(NT));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    void *args[1] = {&p};
+    cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kKv4Warps * 32, (size_t)smem, s, args);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    // the parts of segments that were split; none is, where one unit covers any length
+    if (blocks * page_size > kKv4Unit) {
+        const int64_t tiles = q_starts ? (T * G) / (8 * NT) + B : B * ((G + 8 * NT - 1) / (8 * NT));
+        void *cargs[2] = {&p, &ctas};
+        e = launch_pdl(kv4_kernels.combine[ti][di][NT - 1], dim3((unsigned)(tiles * kv_heads)), 256, 0, s, cargs);
+        if (e != cudaSuccess)
+            return cuda_fail(e);
+    }
+    t_last_path = kPathKv4Attend;
+    return RMSNORM_OK;
+}
+
+} // extern "C"

@@ -31,7 +31,7 @@ PATH_GEMV_UMMA = 7       # the product on tcgen05 (7); 6 and 7 also force it
 PATH_GEMV_TC = 8         # persistent tcgen05 kernel, y held per CTA (8; forces it)
 PATH_FP8_ROWS, PATH_FP8_BLOCKS = 9, 10            # reported only
 PATH_FP8_GEMM, PATH_FP8_PAIR = 11, 12             # the 8-bit product's kernels
-PATH_ROPE, PATH_ROPE_APPEND, PATH_KV4_READ = 13, 14, 15      # reported only
+PATH_ROPE, PATH_ROPE_APPEND, PATH_KV4_READ, PATH_KV4_ATTENTION = 13, 14, 15, 16   # reported only
 
 # Entry points of include/rmsnorm.h with their ctypes signatures.
 _i64, _vp, _sz, _int, _f = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
@@ -83,6 +83,10 @@ SIGNATURES.update({
                                    _i64, _f, _int, _vp]),
     "rmsnorm_rope_append_kv4": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp, _vp,
                                        _i64, _i64, _f, _int, _vp]),
+    "rmsnorm_kv4_attention": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64,
+                                     _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64,
+                                     _f, _vp, _sz, _int, _vp]),
+    "rmsnorm_kv4_attention_workspace_bytes": (_sz, [_i64]),
     "rmsnorm_kv4_read": (_int, [_vp, _i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp,
                                 _vp]),
 })
@@ -484,7 +488,8 @@ def _heads():
     if _heads_mod is None:
         _heads_mod = _binding(HEADS_LIB_PATH, (
             "rmsnorm_rope_fwd", "rmsnorm_rope_bwd", "rmsnorm_rope_bwd_workspace_bytes",
-            "rmsnorm_rope_append", "rmsnorm_rope_append_kv4", "rmsnorm_kv4_read"))
+            "rmsnorm_rope_append", "rmsnorm_rope_append_kv4", "rmsnorm_kv4_read",
+            "rmsnorm_kv4_attention", "rmsnorm_kv4_attention_workspace_bytes"))
     return _heads_mod
 
 
@@ -664,6 +669,23 @@ def rmsnorm_kv4_read(cache, slots, stream=None):
         with _on_stream(cache, stream):
             return _heads().kv4_read(cache, slots)
     return _heads().kv4_read(cache, slots)
+
+
+def rmsnorm_kv4_attention(q, cache, block_table, seq_lens, q_starts=None, k_scale=None, v_scale=None,
+                          scale=None, out=None, lse=None, want_lse=False, workspace=None, stream=None):
+    """(out, lse or None): attention of q [T, heads, D] (bfloat16 or float16)
+    over the 4-bit cache that rmsnorm_rope_append_kv4 writes; see rmsnorm.h.
+    block_table [B, blocks] and seq_lens [B] int32; q_starts [B + 1] int32
+    where sequences have other than one query token each, the last ones
+    cached, each of which sees the tokens up to itself. scale: 1 / sqrt(D)
+    where it is None. Rows of no sequence are not written (in an out that was
+    not passed they hold anything). lse [T, heads] float32."""
+    if stream is not None:
+        with _on_stream(q, stream):
+            return _heads().kv4_attention(q, cache, block_table, seq_lens, q_starts, k_scale, v_scale, scale,
+                                          out, lse, want_lse, workspace)
+    return _heads().kv4_attention(q, cache, block_table, seq_lens, q_starts, k_scale, v_scale, scale, out, lse,
+                                  want_lse, workspace)
 
 
 STATIC_SCRATCH_BYTES = 16 << 20     # RMSNORM_STATIC_SCRATCH_BYTES
