@@ -126,14 +126,13 @@ struct Kv4Params {
     int B, T, Hk, G;           // G query heads to a key head
     float scale;
     int vec;                   // q and out rows start at 16 bytes
-    float *ws;                 // partial results, two a CTA
+    float *ws;                 // partial results, two a warp
     uint32_t extra_tx, wait_limit_us;
     unsigned int *timeouts;
 };
 
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Slot = 32;               // tokens a stage
-constexpr int kKv4Unit = kKv4Warps * kKv4Slot;
 // Shared memory of a CTA: the warps' rings, then their mbarriers.
 __host__ __device__ constexpr int kv4_stages(int D) { return D == 128 ? 3 : 6; }
 __host__ __device__ constexpr int kv4_slot_bytes(int D) { return kKv4Slot / kKv4Tile * 18 * D; }

@@ -15,7 +15,7 @@ size_t workspace_bytes(int sms, int64_t D)
 {
     size_t most = 0;
     for (int NT = 1; NT <= 2; ++NT)
-        most = std::max(most, (size_t)sms * kv4_ctas_per_sm(NT) * 2 * kv4_partial((int)D, NT) * 4);
+        most = std::max(most, (size_t)sms * kv4_ctas_per_sm(NT) * kKv4Warps * 2 * kv4_partial((int)D, NT) * 4);
     return most;
 }
 
@@ -111,8 +111,8 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
     cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kKv4Warps * 32, (size_t)smem, s, args);
     if (e != cudaSuccess)
         return cuda_fail(e);
-    // the parts of segments that were split; none is, where one unit covers any length
-    if (blocks * page_size > kKv4Unit) {
+    // the parts of segments that were split; none is, where one stage covers any length
+    if (blocks * page_size > kKv4Slot) {
         const int64_t tiles = q_starts ? (T * G) / (8 * NT) + B : B * ((G + 8 * NT - 1) / (8 * NT));
         void *cargs[2] = {&p, &ctas};
         e = launch_pdl(kv4_kernels.combine[ti][di][NT - 1], dim3((unsigned)(tiles * kv_heads)), 256, 0, s, cargs);

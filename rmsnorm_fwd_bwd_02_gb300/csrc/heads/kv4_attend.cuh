@@ -40,13 +40,14 @@
 // lane issues as soon as the warp has emptied a stage; no barrier between
 // warps.
 //
-// Split. The work of a call is a list of units of 256 tokens (one stage for
-// each of the eight warps) of segments (sequence, key head, tile of query
-// rows). Every CTA computes from the lengths, which only the device knows,
-// an equal run of consecutive units. A CTA that has the whole of a segment
-// writes its output; of the first and the last it may have a part, which goes
-// to the workspace, and kv4_combine joins the parts of a segment in order.
-// Lengths may thus differ at will, and a captured call replays with others.
+// Split. The work of a call is a list of stages of 32 tokens of segments
+// (sequence, key head, tile of query rows), with one more entry a segment for
+// what a segment costs besides. Every warp computes from the lengths, which
+// only the device knows, its equal run of the list, so lengths may differ at
+// will and a captured call replays with others. A warp that has the whole of
+// a segment writes its output. A CTA whose eight runs lie in one segment joins
+// their sums in shared memory; what is still a part of a segment goes to the
+// workspace, and kv4_combine joins a segment's parts in their order.
 #pragma once
 
 #include "../stream.cuh"
@@ -56,7 +57,7 @@ namespace rmsk {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -97,34 +98,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
     return d;
 }
 
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint16_t lds16(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds8(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-
 // ------------------------------------------------------------ work list
 struct Kv4Seq {
     int q0, n;           // first row, rows
     int len;             // tokens in the cache
     int tiles;           // of 8 NT query rows
-    int units;           // of a tile of a head: at least one, which writes the zeros of empty rows
-    __device__ __forceinline__ int64_t total(int Hk) const { return (int64_t)tiles * Hk * units; }
+    int stages;          // of 32 tokens
+    __device__ __forceinline__ int cost() const { return stages + 1; }
+    __device__ __forceinline__ int64_t total(int Hk) const { return (int64_t)tiles * Hk * cost(); }
 };
 
 // Sequence b as far as its lengths are sound: rows within [0, T), tokens
@@ -133,6 +114,8 @@ template <int NT>
 __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Params &p, int b)
 {
     Kv4Seq s;
+    const int reach = p.blocks * p.tpp * kKv4Tile;             // below 2^31
+    s.len = max(0, min(__ldg(p.lens + b), reach));
     if (p.starts != nullptr) {
         s.q0 = min(max(__ldg(p.starts + b), 0), p.T);
         s.n = max(min(__ldg(p.starts + b + 1), p.T) - s.q0, 0);
@@ -140,56 +123,82 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Params &p, int b)
         s.q0 = b;
         s.n = 1;
     }
-    const int64_t reach = (int64_t)p.blocks * p.tpp * kKv4Tile;
-    s.len = (int)max((int64_t)0, min((int64_t)__ldg(p.lens + b), reach));
-    s.tiles = (int)(((int64_t)s.n * p.G + 8 * NT - 1) / (8 * NT));
-    s.units = max(1, (s.len + kKv4Unit - 1) / kKv4Unit);
+    s.tiles = (s.n * p.G + 8 * NT - 1) / (8 * NT);             // T heads is below 2^31
+    s.stages = (s.len + kKv4Slot - 1) / kKv4Slot;
     return s;
 }
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
+// Where in the list the sequences begin: the sums of 32 sequences at a time,
+// the last such run of them in the lanes.
+struct Kv4List {
+    int base;            // first sequence in the lanes
+    int64_t mine, sum;   // this lane's entries, and all up to and with it
+    int64_t before;      // entries before `base`
+    int64_t total;       // of the whole call
 
-// Units of the whole call; every warp finds the same.
-template <int NT>
-__device__ __forceinline__ int64_t kv4_units(const Kv4Params &p, int to)
-{
-    int64_t v = 0;
-    for (int b = threadIdx.x & 31; b < to; b += 32)
-        v += kv4_seq<NT>(p, b).total(p.Hk);
-    return warp_sum64(v);
-}
-
-// The sequence that holds unit u, and the units before it.
-template <int NT>
-__device__ __forceinline__ void kv4_find(const Kv4Params &p, int64_t u, int &seq, int64_t &before)
-{
-    const int lane = threadIdx.x & 31;
-    before = 0;
-    for (int base = 0; base < p.B; base += 32) {
-        const int64_t v = base + lane < p.B ? kv4_seq<NT>(p, base + lane).total(p.Hk) : 0;
-        int64_t sum = v;
+    template <int NT>
+    __device__ __forceinline__ void load(const Kv4Params &p, int from)
+    {
+        const int b = from + (threadIdx.x & 31);
+        base = from;
+        mine = b < p.B ? kv4_seq<NT>(p, b).total(p.Hk) : 0;
+        sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o)
+            if ((threadIdx.x & 31) >= o)
                 sum += t;
         }
-        const unsigned at = __ballot_sync(0xFFFFFFFFu, before + sum > u);
-        if (at) {
-            const int l = __ffs(at) - 1;
-            seq = base + l;
-            before += __shfl_sync(0xFFFFFFFFu, sum - v, l);
-            return;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    seq = p.B;
+    __device__ __forceinline__ int64_t all() const { return __shfl_sync(0xFFFFFFFFu, sum, 31); }
+    template <int NT> __device__ __forceinline__ void init(const Kv4Params &p)
+    {
+        before = total = 0;
+        for (int from = 32; from < p.B; from += 32) {
+            load<NT>(p, from);
+            total += all();
+        }
+        load<NT>(p, 0);
+        total += all();
+    }
+    // The sequence that holds entry u < total, and the entries before it.
+    template <int NT>
+    __device__ __forceinline__ int find(const Kv4Params &p, int64_t u, int64_t &first)
+    {
+        if (u < before) {
+            before = 0;
+            load<NT>(p, 0);
+        }
+        for (;;) {
+            const unsigned at = __ballot_sync(0xFFFFFFFFu, before + sum > u);
+            if (at) {
+                const int l = __ffs(at) - 1;
+                first = before + __shfl_sync(0xFFFFFFFFu, sum - mine, l);
+                return base + l;
+            }
+            before += all();
+            load<NT>(p, base + 32);
+            if (base >= p.B)
+                return -1;                                      // lengths that change under the call
+        }
+    }
+};
+
+// A segment in the list: its first entry stands for what it costs besides, its
+// stages follow.
+struct Kv4Segment {
+    int h, tile;
+    int64_t at;          // entry of its first stage
+};
+
+__device__ __forceinline__ Kv4Segment kv4_segment(const Kv4Seq &s, int64_t first, int64_t u)
+{
+    const int seg = (int)((u - first) / s.cost());
+    Kv4Segment g;
+    g.h = seg / s.tiles;
+    g.tile = seg - g.h * s.tiles;
+    g.at = first + (int64_t)seg * s.cost() + 1;
+    return g;
 }
 
 // Four features of a row of the output.
@@ -217,6 +226,12 @@ __device__ __forceinline__ float exp2_of(float x)
     return y;
 }
 
+// log sum exp of a row from its reference and denominator.
+__device__ __forceinline__ float kv4_lse(float m, float l)
+{
+    return l > 0.f ? (m - 8.f + log2f(l)) * 0.69314718055994531f : (l != l ? l : kKv4Least);
+}
+
 // What the rows of one tile of a segment share, in each lane.
 template <typename T, int D, int NT>
 struct Kv4Query {
@@ -233,9 +248,9 @@ struct Kv4Query {
         least = INT32_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int64_t row = (int64_t)tile * 8 * NT + nt * 8 + r;
-            const bool real = row < (int64_t)s.n * p.G;
-            const int i = real ? (int)(row / p.G) : 0, hq = h * p.G + (real ? (int)(row - (int64_t)i * p.G) : 0);
+            const int row = tile * 8 * NT + nt * 8 + r;
+            const bool real = row < s.n * p.G;
+            const int i = real ? row / p.G : 0, hq = h * p.G + (real ? row - i * p.G : 0);
             const char *q = static_cast<const char *>(p.q) +
                             ((int64_t)(s.q0 + i) * p.qt + hq * p.qh + c * (D / 4)) * (int64_t)sizeof(T);
             uint32_t w[D / 8];
@@ -288,19 +303,24 @@ struct Kv4Query {
     }
 };
 
+// The parts of a segment in the workspace: of each warp two at most, the first
+// of its run and the last; a CTA that joined its warps' sums uses its first.
+__device__ __forceinline__ int64_t kv4_part(int64_t warp, bool later) { return 2 * warp + (later ? 1 : 0); }
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv4Params p)
+__global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_attend(Kv4Params p)
 {
-    constexpr int kTile = kv4_tile_bytes(D), kSlot = kv4_slot_bytes(D), R = kv4_stages(D);
+    constexpr int kTile = kv4_tile_bytes(D), kSlot = kv4_slot_bytes(D), R = kv4_stages(D), W = D / 8;
     constexpr int kRow = D + 4;                                // floats of a merged row (bank offset)
+    constexpr bool kLow = std::is_same<T, f16>::value;         // p in two halves (see below)
     static_assert(8 * NT * kRow * 4 <= R * kSlot, "a warp's sums fit in its ring");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sm_m[kKv4Warps][8 * NT], sm_l[kKv4Warps][8 * NT];
     __shared__ int sm_bad;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_addr(smem) + warp * R * kSlot;
-    const uint32_t bars = smem_addr(smem) + kKv4Warps * R * kSlot + warp * R * 8;
+    uint8_t *const ring = smem + warp * R * kSlot;
+    const uint32_t ring_s = smem_addr(ring), bars = smem_addr(smem) + kKv4Warps * R * kSlot + warp * R * 8;
     if (lane == 0) {
         for (int i = 0; i < R; ++i)
             mbar_init(bars + 8 * i, 1);
@@ -312,117 +332,140 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv
     griddep_wait();
     griddep_launch_dependents();
 
-    const int64_t total = kv4_units<NT>(p, p.B);
-    const int64_t C = (total + gridDim.x - 1) / gridDim.x;
-    int64_t u = (int64_t)blockIdx.x * C;
-    const int64_t u_end = min(u + C, total);
-    if (u >= u_end)
+    Kv4List list = {};
+    list.init<NT>(p);
+    const int64_t C = (list.total + (int64_t)gridDim.x * kKv4Warps - 1) / ((int64_t)gridDim.x * kKv4Warps);
+    const int64_t cta0 = (int64_t)blockIdx.x * kKv4Warps * C, cta1 = min(cta0 + kKv4Warps * C, list.total);
+    if (cta0 >= cta1)
+        return;                                                 // for the whole CTA
+    const int64_t gw = (int64_t)blockIdx.x * kKv4Warps + warp;
+    const int64_t run0 = gw * C, run1 = min(run0 + C, list.total);
+    int64_t first;
+    int seq = list.find<NT>(p, cta0, first);
+    if (seq < 0)
         return;
-    int seq;
-    int64_t before;
-    kv4_find<NT>(p, u, seq, before);
-    const int64_t u_first = u;
+    Kv4Seq s = kv4_seq<NT>(p, seq);
+    // whether the CTA's runs lie in one segment
+    Kv4Segment g = kv4_segment(s, first, cta0);
+    const bool joined = cta1 <= g.at + s.stages;
     const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
-    uint32_t used = 0;                                          // stages filled and emptied so far
+    uint32_t st_fill = 0, st_use = 0, phase = 0;                // stages of the ring; a phase bit for each
     bool ok = true;
 
-    while (u < u_end && seq < p.B) {
-        const Kv4Seq s = kv4_seq<NT>(p, seq);
-        const int64_t mine = s.total(p.Hk);
-        if (u >= before + mine) {
-            before += mine;
-            ++seq;
-            continue;
-        }
-        const int64_t within = u - before;
-        const int seg = (int)(within / s.units), unit = (int)(within - (int64_t)seg * s.units);
-        const int h = seg / s.tiles, tile = seg - h * s.tiles;
-        const int units = (int)min((int64_t)(s.units - unit), u_end - u);
-        Kv4Query<T, D, NT> q;
-        q.load(p, s, h, tile);
-        // the stages of this run that some row sees, every eighth one this warp's
-        const int from = unit * kKv4Warps + warp;
-        const int stages = min((unit + units) * kKv4Warps, (q.most + kKv4Slot - 1) / kKv4Slot);
-        const int count = stages > from ? (stages - from + kKv4Warps - 1) / kKv4Warps : 0;
-        const int *row = p.table + seq * p.table_ld;
-        const uint8_t *head = p.cache + (int64_t)h * p.tpp * kTile;
-        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
-        const int last = (q.most + kKv4Tile - 1) / kKv4Tile;    // tiles that hold seen tokens
-
-        // a stage's two tiles: their pages (-1: none)
-        auto pages = [&](int i, int (&pg)[2]) {
-            const int t0 = (from + i * kKv4Warps) * 2;
+    Kv4Query<T, D, NT> q;
+    float o[NT][D / 16][4], l[NT][2], m[NT][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                pg[j] = -1;
-                if (i < count && t0 + j < last) {
-                    const int v = __ldg(row + (t0 + j) / p.tpp);
-                    pg[j] = v >= 0 && v < p.pages ? v : -1;
-                }
+    for (int nt = 0; nt < NT; ++nt)
+        m[nt][0] = m[nt][1] = kKv4Least;
+
+    for (int64_t u = run0; u < run1 && ok;) {
+        if (u >= first + s.total(p.Hk)) {
+            seq = list.find<NT>(p, u, first);
+            if (seq < 0)
+                break;
+            s = kv4_seq<NT>(p, seq);
+        }
+        g = kv4_segment(s, first, u);
+        if ((unsigned)g.h >= (unsigned)p.Hk)
+            break;
+        const int from = (int)max((int64_t)0, u - g.at);        // this run's stages
+        const int to = (int)min((int64_t)s.stages, run1 - g.at);
+        u = g.at + s.stages;                                    // the next segment
+        if (from >= to && s.stages > 0)
+            continue;                                           // its first entry alone
+        // pages of the stages ahead
+        const int *row = p.table + seq * p.table_ld;
+        const int t0 = 2 * from;
+        int blk = t0 / p.tpp, tin = t0 - blk * p.tpp;
+        const int lastblk = min(p.blocks, (2 * to + p.tpp - 1) / p.tpp);
+        auto page_of = [&](int b) {
+            const int v = b < lastblk ? __ldg(row + b) : -1;
+            return v < p.pages ? v : -1;
+        };
+        int p0 = page_of(blk), p1 = page_of(blk + 1);
+        q.load(p, s, g.h, g.tile);
+        const int seen = min(to, (q.most + kKv4Slot - 1) / kKv4Slot);
+        const int count = max(0, seen - from);
+        const int last = (q.most + kKv4Tile - 1) / kKv4Tile;    // tiles that hold seen tokens
+        const uint8_t *head = p.cache + (int64_t)g.h * p.tpp * kTile;
+        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
+        uint32_t there = 0;                                     // two bits a stage of the ring: its tiles are there
+        auto next_tile = [&]() {
+            if (++tin == p.tpp) {
+                tin = 0;
+                p0 = p1;
+                ++blk;
+                p1 = page_of(blk + 1);
             }
         };
-        auto fill = [&](int i, const int (&pg)[2]) {
-            if (i >= count || lane != 0)
+        auto fill = [&](int i) {
+            if (i >= count)
                 return;
-            const int t0 = (from + i * kKv4Warps) * 2;
-            const uint32_t st = (used + i) % R, bar = bars + 8 * st;
-            mbar_expect_tx(bar, ((pg[0] >= 0) + (pg[1] >= 0)) * kTile + p.extra_tx);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (pg[j] >= 0)
-                    bulk_g2s(ring + st * kSlot + j * kTile,
-                             head + pg[j] * page_bytes + (int64_t)((t0 + j) % p.tpp) * kTile, kTile, bar);
+            const int ta = tin, pa = p0;
+            next_tile();
+            const int tb = tin, pb = t0 + 2 * i + 1 < last ? p0 : -1;
+            next_tile();
+            there = (there & ~(3u << (2 * st_fill))) | ((pa >= 0 ? 1u : 0u) | (pb >= 0 ? 2u : 0u)) << (2 * st_fill);
+            if (lane == 0) {
+                const uint32_t dst = ring_s + st_fill * kSlot, bar = bars + 8 * st_fill;
+                mbar_expect_tx(bar, ((pa >= 0) + (pb >= 0)) * kTile + p.extra_tx);
+                if (pa >= 0)
+                    bulk_g2s(dst, head + pa * page_bytes + ta * kTile, kTile, bar);
+                if (pb >= 0)
+                    bulk_g2s(dst + kTile, head + pb * page_bytes + tb * kTile, kTile, bar);
+            }
+            st_fill = st_fill + 1 == R ? 0 : st_fill + 1;
         };
-        // which tiles of the stages in flight are there: two bits each, the oldest lowest
-        uint32_t there = 0;
-        int pg[2];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            pages(i, pg);
-            there |= ((pg[0] >= 0 ? 1u : 0u) | (pg[1] >= 0 ? 2u : 0u)) << (2 * i);
-            fill(i, pg);
-        }
-        pages(R, pg);                                           // fetched ahead of their use
-
-        float o[NT][D / 16][4] = {}, l[NT][2] = {}, m[NT][2];
+        for (int i = 0; i < R; ++i)
+            fill(i);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kKv4Least;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+                o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
+        }
 
         for (int i = 0; i < count; ++i) {
-            const uint32_t st = (used + i) % R, at = ring + st * kSlot;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + 8 * st, ((used + i) / R) & 1, limit));
+            const uint8_t *at = ring + st_use * kSlot;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bars + 8 * st_use, (phase >> st_use) & 1u, limit));
             if (!ok) {
                 // a copy never came: wait, with a limit again, for the others in flight
-                for (int n = i + 1; n < min(i + R, count); ++n)
-                    (void)mbar_wait_bounded(bars + 8 * ((used + n) % R), ((used + n) / R) & 1, limit);
+                for (int n = i + 1; n < min(i + R, count); ++n) {
+                    st_use = st_use + 1 == R ? 0 : st_use + 1;
+                    (void)mbar_wait_bounded(bars + 8 * st_use, (phase >> st_use) & 1u, limit);
+                }
                 __syncwarp();
                 break;
             }
-            const int tok = (from + i * kKv4Warps) * kKv4Slot;
-            const bool whole = tok + kKv4Slot <= q.least && (there & 3u) == 3u;
+            phase ^= 1u << st_use;
+            const int tok = (from + i) * kKv4Slot;
+            const uint32_t here = there >> (2 * st_use) & 3u;
+            const bool whole = tok + kKv4Slot <= q.least && here == 3u;
             float x[NT][2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // S^T of 16 tokens
                 uint32_t k0[D / 32], k1[D / 32], s0[D / 64], s1[D / 64];
-                const uint32_t ka = at + j * kTile + r * (D / 2) + c * (D / 8), kb = ka + 8 * (D / 2);
-                const uint32_t sa = at + j * kTile + kv4_kscale(D) + r * (D / 16) + c * (D / 64),
-                               sb = sa + 8 * (D / 16);
+                const uint8_t *ka = at + j * kTile + r * (D / 2) + c * (D / 8), *kb = ka + 8 * (D / 2);
+                const uint8_t *sa = at + j * kTile + kv4_kscale(D) + r * (D / 16) + c * (D / 64),
+                              *sb = sa + 8 * (D / 16);
                 if constexpr (D == 128) {
-                    const uint4 a = lds128(ka), b = lds128(kb);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(ka), b = *reinterpret_cast<const uint4 *>(kb);
                     k0[0] = a.x; k0[1] = a.y; k0[2] = a.z; k0[3] = a.w;
                     k1[0] = b.x; k1[1] = b.y; k1[2] = b.z; k1[3] = b.w;
-                    const uint32_t u0 = scales2(lds16(sa)), u1 = scales2(lds16(sb));
+                    const uint32_t u0 = scales2(*reinterpret_cast<const uint16_t *>(sa)),
+                                   u1 = scales2(*reinterpret_cast<const uint16_t *>(sb));
                     s0[0] = __byte_perm(u0, u0, 0x1010); s0[1] = __byte_perm(u0, u0, 0x3232);
                     s1[0] = __byte_perm(u1, u1, 0x1010); s1[1] = __byte_perm(u1, u1, 0x3232);
                 } else {
-                    const uint2 a = lds64(ka), b = lds64(kb);
+                    const uint2 a = *reinterpret_cast<const uint2 *>(ka), b = *reinterpret_cast<const uint2 *>(kb);
                     k0[0] = a.x; k0[1] = a.y;
                     k1[0] = b.x; k1[1] = b.y;
-                    const uint32_t v0 = lds8(sa), v1 = lds8(sb);
-                    s0[0] = scales2((uint16_t)(v0 * 0x0101u));
-                    s1[0] = scales2((uint16_t)(v1 * 0x0101u));
+                    s0[0] = scales2((uint16_t)(*sa * 0x0101u));
+                    s1[0] = scales2((uint16_t)(*sb * 0x0101u));
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -447,19 +490,27 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 4; ++e)
                         x[nt][j][e] *= q.mul[nt][e & 1];
-                        if (!whole && (tok + j * 16 + r + (e & 2) * 4 >= q.lim[nt][e & 1] || !(there & (1u << j))))
-                            x[nt][j][e] = kKv4Least;
-                    }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (tok + j * 16 + r + (e & 2) * 4 >= q.lim[nt][e & 1] || !(here & (1u << j)))
+                                x[nt][j][e] = kKv4Least;
             }
             // a new reference where a score has left the old one's range
             bool far = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    far |= fmaxf(x[nt][0][e], x[nt][1][e]) > m[nt][e & 1] + 7.f;
+                for (int e = 0; e < 2; ++e)
+                    far |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2])) >
+                           m[nt][e] + 7.f;
             if (__any_sync(0xFFFFFFFFu, far)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -480,57 +531,59 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv
                         }
                     }
             }
-            uint32_t pb[NT][2][2];
+            // p, transposed for the second product. One rounding to fp16 is
+            // as large as an fp16 output's own: there a second half holds what
+            // the first has lost, and the weights are good to 2^-22.
+            uint32_t pb[NT][2][2], pl[kLow ? NT : 1][2][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float b0 = m[nt][0] == kKv4Least ? 0.f : m[nt][0] - 8.f;
                 const float b1 = m[nt][1] == kKv4Least ? 0.f : m[nt][1] - 8.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = exp2_of(x[nt][j][0] - b0), p1 = exp2_of(x[nt][j][1] - b1);
-                    const float p2 = exp2_of(x[nt][j][2] - b0), p3 = exp2_of(x[nt][j][3] - b1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    pb[nt][j][0] = movmatrix(Half16<f16>::narrow2(p0, p1));
-                    pb[nt][j][1] = movmatrix(Half16<f16>::narrow2(p2, p3));
-                }
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x0 = exp2_of(x[nt][j][2 * e] - b0), x1 = exp2_of(x[nt][j][2 * e + 1] - b1);
+                        l[nt][0] += x0;
+                        l[nt][1] += x1;
+                        const uint32_t hi = Half16<f16>::narrow2(x0, x1);
+                        pb[nt][j][e] = movmatrix(hi);
+                        if constexpr (kLow) {
+                            const float2 w = Half16<f16>::wide2(hi);
+                            pl[nt][j][e] = movmatrix(Half16<f16>::narrow2(x0 - w.x, x1 - w.y));
+                        }
+                    }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // O^T of 16 tokens
-                constexpr int W = D / 64;                       // words of a token's features
-                uint32_t v[4][W];
-                const uint32_t base = at + j * kTile + kv4_v(D);
-                uint32_t f0, f1;
+                uint32_t v[4][D / 64];
+                const uint8_t *base = at + j * kTile + kv4_v(D);
+                const uint8_t *sc;
                 if constexpr (D == 128) {
-                    const uint4 a = lds128(base + r * 128 + c * 16), b = lds128(base + r * 128 + c * 16 + 64);
+                    const uint4 a = *reinterpret_cast<const uint4 *>(base + r * 128 + c * 16),
+                                b = *reinterpret_cast<const uint4 *>(base + r * 128 + c * 16 + 64);
                     v[0][0] = a.x; v[0][1] = a.y; v[1][0] = a.z; v[1][1] = a.w;
                     v[2][0] = b.x; v[2][1] = b.y; v[3][0] = b.z; v[3][1] = b.w;
-                    const uint32_t sc = at + j * kTile + kv4_vscale(D) + r * 16 + 2 * c;
-                    f0 = scales2(lds16(sc));
-                    f1 = scales2(lds16(sc + 8));
+                    sc = at + j * kTile + kv4_vscale(D) + r * 16 + 2 * c;
                 } else {
-                    const uint32_t a = base + (r >> 1) * 128 + c * 16 + (r & 1) * 4;
+                    const uint8_t *a = base + (r >> 1) * 128 + c * 16 + (r & 1) * 4;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t t;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t) : "r"(a + (e & 1) * 8 + (e & 2) * 32));
-                        v[e][0] = t;
-                    }
-                    const uint32_t sc = at + j * kTile + kv4_vscale(D) + (r >> 1) * 16 + 2 * c;
-                    f0 = scales2(lds16(sc));
-                    f1 = scales2(lds16(sc + 8));
+                    for (int e = 0; e < 4; ++e)
+                        v[e][0] = *reinterpret_cast<const uint32_t *>(a + (e & 1) * 8 + (e & 2) * 32);
+                    sc = at + j * kTile + kv4_vscale(D) + (r >> 1) * 16 + 2 * c;
                 }
+                uint32_t f0 = scales2(*reinterpret_cast<const uint16_t *>(sc));
+                uint32_t f1 = scales2(*reinterpret_cast<const uint16_t *>(sc + 8));
                 if (!whole) {
                     // tokens that are not there count as zeros, whatever bytes lie in their place
-                    const int t0 = tok + j * 16 + 2 * c;
-                    const bool in = there & (1u << j);
-                    f0 = (in && t0 < s.len ? f0 & 0xFFFFu : 0u) | (in && t0 + 1 < s.len ? f0 & 0xFFFF0000u : 0u);
-                    f1 = (in && t0 + 8 < s.len ? f1 & 0xFFFFu : 0u) |
-                         (in && t0 + 9 < s.len ? f1 & 0xFFFF0000u : 0u);
+                    const int k = tok + j * 16 + 2 * c;
+                    const bool in = here & (1u << j);
+                    f0 = (in && k < s.len ? f0 & 0xFFFFu : 0u) | (in && k + 1 < s.len ? f0 & 0xFFFF0000u : 0u);
+                    f1 = (in && k + 8 < s.len ? f1 & 0xFFFFu : 0u) | (in && k + 9 < s.len ? f1 & 0xFFFF0000u : 0u);
                 }
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
+                for (int w = 0; w < D / 64; ++w) {
                     uint32_t e0[4], e1[4], e2[4], e3[4];        // even and odd features, tokens 2c.. and 2c + 8..
                     widen4((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), e0);
                     widen4(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), e1);
@@ -541,20 +594,22 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv
                         const uint32_t a[4] = {hmul2(e0[t], f0), hmul2(e1[t], f0), hmul2(e2[t], f1),
                                                hmul2(e3[t], f1)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
                             mma_f16(o[nt][4 * w + t], a, pb[nt][j][0], pb[nt][j][1]);
+                            if constexpr (kLow)
+                                mma_f16(o[nt][4 * w + t], a, pl[nt][j][0], pl[nt][j][1]);
+                        }
                     }
                 }
             }
             // the stage is read: refill it
             fence_proxy_async_smem();
             __syncwarp();
-            there >>= 2;
-            there |= ((pg[0] >= 0 ? 1u : 0u) | (pg[1] >= 0 ? 2u : 0u)) << (2 * (R - 1));
-            fill(i + R, pg);
-            pages(i + R + 1, pg);
+            st_use = st_use + 1 == R ? 0 : st_use + 1;
+            fill(i + R);
         }
-        used += count;
+        if (!ok)
+            break;
         // a row's terms lie in the eight lanes of its column
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -563,90 +618,120 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_attend(Kv
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], d);
-
-        // join the warps' sums in their rings, which are empty now
-        float *sums = reinterpret_cast<float *>(smem + warp * R * kSlot);
+        if (joined)
+            break;
+        // the row's D / 8 features of this lane: to the output, or to the workspace as a part
+        const bool all = from == 0 && to == s.stages;
+        const float gv = p.vscale ? __ldg(p.vscale + g.h) : 1.f;
+        float *part = p.ws + kv4_part(gw, g.at - 1 > run0) * kv4_partial(D, NT);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int n = nt * 8 + 2 * c + e;
-                if (r == 0) {
-                    sm_m[warp][n] = m[nt][e];
-                    sm_l[warp][n] = l[nt][e];
+                const int n = nt * 8 + 2 * c + e, qrow = g.tile * 8 * NT + n;
+                if (all && qrow >= s.n * p.G)
+                    continue;
+                const int i = qrow / p.G, hq = g.h * p.G + qrow - i * p.G;
+                const float f = all ? (l[nt][e] > 0.f || l[nt][e] != l[nt][e] ? gv / l[nt][e] : 0.f) : 1.f;
+#pragma unroll
+                for (int t = 0; t < D / 16; t += 2) {
+                    const float4 v = make_float4(o[nt][t][e] * f, o[nt][t][e + 2] * f, o[nt][t + 1][e] * f,
+                                                 o[nt][t + 1][e + 2] * f);
+                    if (all)
+                        kv4_store<T>(p, s.q0 + i, hq, r * W + 2 * t, v);
+                    else
+                        *reinterpret_cast<float4 *>(part + n * D + r * W + 2 * t) = v;
                 }
-                float *d = sums + n * kRow + r * (D / 8);
+                if (r == 0 && all && p.lse != nullptr)
+                    p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] = kv4_lse(m[nt][e], l[nt][e]);
+                if (r == 0 && !all) {
+                    part[8 * NT * D + n] = m[nt][e];
+                    part[8 * NT * (D + 1) + n] = l[nt][e];
+                }
+            }
+    }
+    if (!ok && lane == 0) {
+        atomicAdd(p.timeouts, 1u);
+        sm_bad = 1;
+    }
+    if (!joined)
+        return;
+
+    // join the warps' sums in their rings, which are empty now
+    float *sums = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = nt * 8 + 2 * c + e;
+            if (r == 0) {
+                sm_m[warp][n] = m[nt][e];
+                sm_l[warp][n] = l[nt][e];
+            }
+            float *d = sums + n * kRow + r * W;
+            if (m[nt][e] != kKv4Least)
 #pragma unroll
                 for (int t = 0; t < D / 16; t += 2)
                     *reinterpret_cast<float4 *>(d + 2 * t) =
                         make_float4(o[nt][t][e], o[nt][t][e + 2], o[nt][t + 1][e], o[nt][t + 1][e + 2]);
-            }
-        if (!ok)
-            sm_bad = 1;
-        __syncthreads();
-        const bool all = unit == 0 && units == s.units;
-        const float gv = p.vscale ? __ldg(p.vscale + h) : 1.f;
-        float *part = p.ws + (2 * (int64_t)blockIdx.x + (u - unit > u_first ? 1 : 0)) * kv4_partial(D, NT);
-        for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += kKv4Warps * 32) {
-            const int n = k / (D / 4), d = (k - n * (D / 4)) * 4;
-            float mm = kKv4Least, ll = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kKv4Warps; ++w)
-                mm = fmaxf(mm, sm_m[w][n]);
-#pragma unroll
-            for (int w = 0; w < kKv4Warps; ++w) {
-                const float f = sm_m[w][n] == kKv4Least ? 0.f : exp2_of(sm_m[w][n] - mm);
-                const float4 v = *reinterpret_cast<const float4 *>(
-                    reinterpret_cast<const float *>(smem + w * R * kSlot) + n * kRow + d);
-                if (f != 0.f) {
-                    ll = fmaf(f, sm_l[w][n], ll);
-                    a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
-                    a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
-                }
-            }
-            const int64_t qrow = (int64_t)tile * 8 * NT + n;
-            if (!all) {
-                *reinterpret_cast<float4 *>(part + n * D + d) = a;
-                if (d == 0) {
-                    part[8 * NT * D + n] = mm;
-                    part[8 * NT * (D + 1) + n] = ll;
-                }
-            } else if (qrow < (int64_t)s.n * p.G && !sm_bad) {
-                const int i = (int)(qrow / p.G), hq = h * p.G + (int)(qrow - (int64_t)i * p.G);
-                const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
-                kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
-                if (d == 0 && p.lse != nullptr)
-                    p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] =
-                        ll > 0.f ? (mm - 8.f + log2f(ll)) * 0.69314718055994531f : (ll != ll ? ll : kKv4Least);
-            }
         }
-        fence_proxy_async_smem();
-        __syncthreads();
-        if (sm_bad) {
-            if (threadIdx.x == 0)
-                atomicAdd(p.timeouts, 1u);
-            break;
+    __syncthreads();
+    if (sm_bad)
+        return;
+    g = kv4_segment(s, first, cta0);
+    const bool all = cta0 <= g.at && cta1 == g.at + s.stages;
+    const float gv = p.vscale ? __ldg(p.vscale + g.h) : 1.f;
+    float *part = p.ws + kv4_part((int64_t)blockIdx.x * kKv4Warps, false) * kv4_partial(D, NT);
+    for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += kKv4Warps * 32) {
+        const int n = k / (D / 4), d = (k - n * (D / 4)) * 4;
+        float mm = kKv4Least, ll = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kKv4Warps; ++w)
+            mm = fmaxf(mm, sm_m[w][n]);
+#pragma unroll
+        for (int w = 0; w < kKv4Warps; ++w) {
+            if (sm_m[w][n] == kKv4Least)
+                continue;
+            const float f = exp2_of(sm_m[w][n] - mm);
+            const float4 v = *reinterpret_cast<const float4 *>(
+                reinterpret_cast<const float *>(smem + w * R * kSlot) + n * kRow + d);
+            ll = fmaf(f, sm_l[w][n], ll);
+            a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
+            a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
         }
-        u += units;
+        const int qrow = g.tile * 8 * NT + n;
+        if (!all) {
+            *reinterpret_cast<float4 *>(part + n * D + d) = a;
+            if (d == 0) {
+                part[8 * NT * D + n] = mm;
+                part[8 * NT * (D + 1) + n] = ll;
+            }
+        } else if (qrow < s.n * p.G) {
+            const int i = qrow / p.G, hq = g.h * p.G + qrow - i * p.G;
+            const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
+            kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
+            if (d == 0 && p.lse != nullptr)
+                p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] = kv4_lse(mm, ll);
+        }
     }
 }
 
-// Joins the parts of the segments that several CTAs worked on, in the order of
-// the CTAs. CTA x: segment x of the call (a sequence's segments side by side);
-// `ctas` is the grid of kv4_attend.
+// Joins the parts of the segments that several warps or CTAs worked on, in the
+// order of the list. CTA x: segment x of the call (a sequence's segments side
+// by side); `ctas` is the grid of kv4_attend.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
 {
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    // the sequence of this segment, and the units before the segment
-    int64_t segs = 0, units = 0, seg = -1, u0 = 0, total = 0;
+    // the sequence of this segment, and the entries before it
+    int64_t segs = 0, entries = 0, seg = -1, first = 0;
     Kv4Seq s = {};
     for (int base = 0; base < p.B; base += 32) {
         const Kv4Seq t = base + lane < p.B ? kv4_seq<NT>(p, base + lane) : Kv4Seq{};
-        const int64_t n = (int64_t)t.tiles * p.Hk, v = n * t.units;
+        const int64_t n = (int64_t)t.tiles * p.Hk, v = base + lane < p.B ? t.total(p.Hk) : 0;
         int64_t sn = n, sv = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -660,50 +745,79 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
         if (at && seg < 0) {
             const int l = __ffs(at) - 1;
             seg = blockIdx.x - (segs + __shfl_sync(0xFFFFFFFFu, sn - n, l));
-            u0 = units + __shfl_sync(0xFFFFFFFFu, sv - v, l);
+            first = entries + __shfl_sync(0xFFFFFFFFu, sv - v, l);
             s.q0 = __shfl_sync(0xFFFFFFFFu, t.q0, l);
             s.n = __shfl_sync(0xFFFFFFFFu, t.n, l);
             s.tiles = __shfl_sync(0xFFFFFFFFu, t.tiles, l);
-            s.units = __shfl_sync(0xFFFFFFFFu, t.units, l);
+            s.stages = __shfl_sync(0xFFFFFFFFu, t.stages, l);
         }
         segs += __shfl_sync(0xFFFFFFFFu, sn, 31);
-        units += __shfl_sync(0xFFFFFFFFu, sv, 31);
+        entries += __shfl_sync(0xFFFFFFFFu, sv, 31);
     }
-    total = units;
-    if (seg < 0)
+    if (seg < 0 || s.stages == 0)
         return;
-    u0 += seg * s.units;
-    const int64_t C = (total + ctas - 1) / ctas;
-    const int first = (int)(u0 / C), last = (int)((u0 + s.units - 1) / C);
-    if (first == last)
+    const int64_t C = (entries + (int64_t)ctas * kKv4Warps - 1) / ((int64_t)ctas * kKv4Warps);
+    const int64_t start = first + seg * s.cost(), end = start + s.cost();
+    const int64_t w0 = (start + 1) / C, w1 = (end - 1) / C;      // the warps that have stages of it
+    if (w0 == w1)
+        return;                                                 // one warp had all of it
+    const int64_t c0 = w0 / kKv4Warps, c1 = w1 / kKv4Warps;
+    // CTAs whose runs all lie in the segment have one part; only the first and
+    // the last may have others
+    auto inside = [&](int64_t cta) {
+        return cta * kKv4Warps * C >= start && min((cta + 1) * kKv4Warps * C, entries) <= end;
+    };
+    const bool in0 = inside(c0), in1 = inside(c1);
+    if (c0 == c1 && in0)
         return;                                                 // one CTA had all of it
+    const int n0 = in0 ? 1 : (int)(min(w1, c0 * kKv4Warps + kKv4Warps - 1) - w0 + 1);
+    const int n1 = c0 == c1 ? 0 : (in1 ? 1 : (int)(w1 - c1 * kKv4Warps + 1));
+    const int parts = n0 + n1 + (c0 == c1 ? 0 : (int)(c1 - c0 - 1));
+    auto part_at = [&](int i) {
+        int64_t w;
+        if (i < n0)
+            w = in0 ? c0 * kKv4Warps : w0 + i;
+        else if (i < parts - n1)
+            w = (c0 + 1 + i - n0) * kKv4Warps;
+        else
+            w = c1 * kKv4Warps + (i - (parts - n1));
+        return p.ws + kv4_part(w, w * C < start) * kv4_partial(D, NT);
+    };
     const int h = (int)seg / s.tiles, tile = (int)seg - h * s.tiles;
     const float gv = p.vscale ? __ldg(p.vscale + h) : 1.f;
     for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += 256) {
-        const int n = k / (D / 4), d = (k - n * (D / 4)) * 4;
-        const int64_t qrow = (int64_t)tile * 8 * NT + n;
-        if (qrow >= (int64_t)s.n * p.G)
+        const int n = k / (D / 4), d = (k - n * (D / 4)) * 4, qrow = tile * 8 * NT + n;
+        if (qrow >= s.n * p.G)
             continue;
         float mm = kKv4Least, ll = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = first; i <= last; ++i) {
-            const float *part = p.ws + (2 * (int64_t)i + ((int64_t)i * C >= u0 ? 0 : 1)) * kv4_partial(D, NT);
-            const float m = __ldcg(part + 8 * NT * D + n), l = __ldcg(part + 8 * NT * (D + 1) + n);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + n * D + d));
-            if (m == kKv4Least)
-                continue;
-            const float up = fmaxf(mm, m), f0 = mm == kKv4Least ? 0.f : exp2_of(mm - up), f1 = exp2_of(m - up);
-            mm = up;
-            ll = ll * f0 + l * f1;
-            a.x = a.x * f0 + v.x * f1; a.y = a.y * f0 + v.y * f1;
-            a.z = a.z * f0 + v.z * f1; a.w = a.w * f0 + v.w * f1;
+        for (int i = 0; i < parts; i += 4) {
+            float m[4], l[4];
+            float4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float *part = part_at(min(i + j, parts - 1));
+                m[j] = i + j < parts ? __ldcg(part + 8 * NT * D + n) : kKv4Least;
+                l[j] = __ldcg(part + 8 * NT * (D + 1) + n);
+                v[j] = __ldcg(reinterpret_cast<const float4 *>(part + n * D + d));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (m[j] == kKv4Least)
+                    continue;
+                const float up = fmaxf(mm, m[j]);
+                const float f0 = mm == kKv4Least ? 0.f : exp2_of(mm - up), f1 = exp2_of(m[j] - up);
+                mm = up;
+                ll = ll * f0 + l[j] * f1;
+                a.x = a.x * f0 + v[j].x * f1; a.y = a.y * f0 + v[j].y * f1;
+                a.z = a.z * f0 + v[j].z * f1; a.w = a.w * f0 + v[j].w * f1;
+            }
         }
-        const int i = (int)(qrow / p.G), hq = h * p.G + (int)(qrow - (int64_t)i * p.G);
+        const int i = qrow / p.G, hq = h * p.G + qrow - i * p.G;
         const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
         kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
         if (d == 0 && p.lse != nullptr)
-            p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] =
-                ll > 0.f ? (mm - 8.f + log2f(ll)) * 0.69314718055994531f : (ll != ll ? ll : kKv4Least);
+            p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] = kv4_lse(mm, ll);
     }
 }
 
