@@ -442,10 +442,10 @@ typedef struct {
  * A rotation by positions. Of a row's first `rot` columns pair i turns by
  * position * freq[i] radians; the columns past rot stay. Scaled contexts are
  * other freq (and an amplitude); freq is finite, in 64 bits, in device
- * memory. The angle is exact for every 64-bit position, negative ones too:
- * freq / 2 pi is held as a 64-bit fraction of a turn and the product taken
- * modulo whole turns, so the only error is freq's own rounding (2^-53) and
- * 2^-32 of a turn. A NULL rotation, or rot 0, turns nothing.
+ * memory. No position loses the angle's fraction, far or negative: freq / 2
+ * pi is held as a 64-bit fraction of a turn, and the product with the 64-bit
+ * position is taken modulo whole turns, within |position| 2^-64 + 2^-32 of a
+ * turn. A NULL rotation, or rot 0, turns nothing.
  */
 typedef struct {
     const void *positions;      /* [T] int32 or int64 */

@@ -35,11 +35,11 @@ struct RopeTurn {
     float amp;
 };
 
-// A paged cache behind k and v (part[1], part[2]).
+// A paged cache behind k and v: rows at part[1].y and part[2].y, or 4-bit tiles
+// at part[1].y.
 struct RopeCache {
     const void *slots;         // [T] int32 or int64
     int slot64;
-    int bits4;                 // 4-bit tiles at part[1].y; else rows of the dtype
     int64_t page_size, limit;  // limit: slots of the cache
     int64_t kpage, vpage;      // page strides (elements; bytes of the whole for 4 bits)
     const float *kscale, *vscale;   // [heads] or nullptr: 1
@@ -84,10 +84,14 @@ struct RopeGradParams {
 };
 
 // The kernels of one element type: packs of 16 bytes, of half of it (16-bit
-// types), of one element; [1]: adjacent pairs. E: elements a pack.
+// types), of one element. fwd[form][adjacent pairs]: the forward, the append
+// of rows, the append in 4 bits; with their shared memory. E: elements a pack.
 struct RopeKernel {
     int E;
-    const void *fwd[2], *append[2], *bwd[2];
+    const void *fwd[3][2];
+    int fwd_smem[3];
+    const void *bwd[2];
+    int bwd_smem;
 };
 struct RopeSet {
     int n;

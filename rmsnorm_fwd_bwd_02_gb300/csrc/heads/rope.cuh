@@ -22,9 +22,8 @@
 // Layout. Packs of 16 bytes; a lane holds the two packs of a row whose
 // elements pair up (i and i + rot/2, or neighbours), so a row takes D / 16
 // lanes (16-bit types) and no data crosses lanes but the norm's sum. A group
-// of lanes takes a piece of HC heads of one token, four of them at a time (to
-// have enough loads in flight), and computes the sines once for the piece.
-// Bound by DRAM: one pass, every row read and written once.
+// of lanes takes a piece of HC heads of one token and computes the sines once
+// for it. One pass, every row read and written once.
 #pragma once
 
 #include "../common.cuh"
@@ -75,12 +74,26 @@ __device__ __forceinline__ int64_t ld_index(const void *p, int64_t i, int wide)
                 : (int64_t)__ldg(static_cast<const int *>(p) + i);
 }
 
-// freq (radians a position) as a fraction of a turn, 2^64 to the turn.
+// freq (radians a position) as a fraction of a turn, 2^64 to the turn: its 53
+// bits times 1 / (2 pi) in 66, shifted by its exponent, whole turns dropped.
+// In integers: a product in 64-bit floating point takes this GPU some 0.4 us,
+// and a lane needs eight (one token of 16 heads took 5.0 us with them).
 __device__ __forceinline__ uint64_t turn_fraction(double freq)
 {
-    double t = freq * 0.15915494309189533577;            // 1 / (2 pi)
-    t -= floor(t);
-    return (uint64_t)__double2ull_rz(t * 18446744073709551616.0);
+    const uint64_t bits = (uint64_t)__double_as_longlong(freq);
+    const int e = (int)(bits >> 52) & 0x7FF;
+    const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+    const uint64_t k = 11743562013128004906ull;          // 2^66 / (2 pi)
+    const uint64_t hi = __umul64hi(m, k), lo = m * k;
+    const int right = 1077 - e;                          // of the 128-bit product
+    uint64_t t = right >= 128 ? 0
+                 : right >= 64 ? hi >> (right - 64)
+                 : right > 0   ? hi << (64 - right) | lo >> right
+                 : right > -64 ? lo << -right
+                               : 0;
+    if (e == 0)
+        t = 0;                                           // zero and what is no normal number
+    return bits >> 63 ? 0 - t : t;
 }
 
 // sine and cosine of 2 pi * fraction * pos
@@ -238,7 +251,97 @@ __host__ __device__ constexpr int kv4_kscale(int D) { return 8 * D; }
 __host__ __device__ constexpr int kv4_v(int D) { return 9 * D; }
 __host__ __device__ constexpr int kv4_vscale(int D) { return 17 * D; }
 
-constexpr int kRopeStage = 640;            // floats of a warp's staged rows (append)
+// ------------------------------------------------------------- the pipeline
+// Rows on their way: a lane copies its packs of the next batches of heads into
+// slots of its own in shared memory (asynchronous copies of 16 or 8 bytes) and
+// reads them back when their group of copies is done; no other lane looks at
+// them, so nothing is synchronised, and what is in flight takes no registers.
+// Single elements (E = 1) are loaded where they are used.
+constexpr int kRopeDepth = 3;                          // batches in the ring
+template <int E> __host__ __device__ constexpr int rope_fwd_heads(int form)
+{
+    return E == 1 ? 1 : (form == 2 ? 2 : 4);           // heads a batch; 4-bit rows want room beside the ring
+}
+template <int E> __host__ __device__ constexpr int rope_bwd_heads() { return E == 1 ? 1 : 2; }
+constexpr int kRopeStage = 640;                        // floats of a warp's staged rows (append in 4 bits)
+template <int E>
+__host__ __device__ constexpr int rope_fwd_smem(int form, size_t es)
+{
+    return (E == 1 ? 0 : kRopeDepth * rope_fwd_heads<E>(form) * 2 * E * (int)es * kRopeThreads) +
+           (form == 2 ? kRopeThreads / 32 * kRopeStage * 4 : 0);
+}
+template <int E>
+__host__ __device__ constexpr int rope_bwd_smem(size_t es)
+{
+    const int ring = E == 1 ? 0 : kRopeDepth * rope_bwd_heads<E>() * 4 * E * (int)es * kRopeThreads;
+    const int sums = kRopeThreads * 2 * E * (E == 1 ? 4 : 1) * 4;
+    return ring > sums ? ring : sums;
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The ring of one lane: slot i of batch b at base + ((b % depth) N + i) of the
+// CTA's lanes' packs.
+template <typename T, int E, int N>
+struct RopeRing {
+    static constexpr int kBytes = E * (int)sizeof(T);
+    uint8_t *base;
+    __device__ __forceinline__ uint8_t *at(int stage, int i) const
+    {
+        return base + (stage * N + i) * (kRopeThreads * kBytes);
+    }
+    __device__ __forceinline__ void fetch(int stage, int i, const void *row, int pack) const
+    {
+        copy_async<kBytes>((uint32_t)__cvta_generic_to_shared(at(stage, i)),
+                           static_cast<const char *>(row) + pack * kBytes);
+    }
+    __device__ __forceinline__ Pack<T, E> get(int stage, int i) const
+    {
+        Pack<T, E> p;
+        p.u = *reinterpret_cast<const decltype(p.u) *>(at(stage, i));
+        return p;
+    }
+};
+
+// Where a group of lanes is in the call's list: token t, piece c of its heads,
+// head hc of the piece.
+struct RopeCursor {
+    int64_t item, t;
+    int c, hc;
+    __device__ __forceinline__ void start(int64_t i, int chunks)
+    {
+        item = i;
+        t = i / chunks;
+        c = (int)(i - t * chunks);
+        hc = 0;
+    }
+    __device__ __forceinline__ void next(int U, int HC, int64_t step, int64_t dt, int dc, int chunks)
+    {
+        hc += U;
+        if (hc < HC)
+            return;
+        hc = 0;
+        item += step;
+        t += dt;
+        c += dc;
+        if (c >= chunks) {
+            c -= chunks;
+            ++t;
+        }
+    }
+};
 
 // Rows of a warp in shared memory as fp32, a group of 16 in 20 words (reads
 // of whole groups then meet no bank twice); lane g of a row's lanes rounds
@@ -263,12 +366,18 @@ __device__ __forceinline__ void store_tile4(const float *stage, int D, int lane,
     *scale = s;
 }
 
-template <typename T, int E, bool ADJ, bool APP>
+// FORM 0: the forward; 1: the append, rows of the dtype; 2: the append, 4 bits.
+template <typename T, int E, bool ADJ, int FORM>
 __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
 {
-    constexpr int V = E == 1 ? 4 : 1, U = E == 1 ? 1 : 4;
+    constexpr bool APP = FORM > 0;
+    constexpr int V = E == 1 ? 4 : 1, U = rope_fwd_heads<E>(FORM);
     using P = Pack<T, E>;
-    __shared__ __align__(16) float stage_all[APP ? (kRopeThreads / 32) * kRopeStage : 4];
+    extern __shared__ __align__(16) uint8_t smem[];
+    // the staged rows first, then the ring
+    float *stage_all = reinterpret_cast<float *>(smem);
+    const RopeRing<T, E, 2 * U> ring = {smem + (FORM == 2 ? kRopeThreads / 32 * kRopeStage * 4 : 0) +
+                                        threadIdx.x * (E * sizeof(T))};
 
     const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
     const int chunks = p.part[0].chunks + p.part[1].chunks + (APP ? p.part[2].chunks : 0);
@@ -281,165 +390,192 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     }
     griddep_wait();
     griddep_launch_dependents();
-    RopeAngles<E, V> ang;
-    ang.init(p.turn, slot, pair);
 
     const int64_t items = p.T * chunks;
     const int64_t step = (int64_t)gridDim.x * (kRopeThreads >> p.shift);
     // the warp's first group decides when the warp is done (its lanes stay
     // together in the sums' shuffles)
     const int64_t g0 = ((int64_t)blockIdx.x * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
-    int64_t item = g0 + ((threadIdx.x & 31) >> p.shift);
-    int64_t t = item / chunks;
-    int c = (int)(item - t * chunks);
     const int64_t dt = step / chunks;
     const int dc = (int)(step - dt * chunks);
-    for (int64_t first = g0; first < items; first += step, item += step) {
-        const bool live = item < items;
-        // which heads
-        int ci = c, part = 0;
-        if (ci >= p.part[0].chunks) {
-            ci -= p.part[0].chunks;
-            part = 1;
-            if (APP && ci >= p.part[1].chunks) {
-                ci -= p.part[1].chunks;
-                part = 2;
+    RopeCursor cur, ahead;
+    cur.start(g0 + ((threadIdx.x & 31) >> p.shift), chunks);
+    ahead = cur;
+
+    // which heads a piece has: q's, k's or v's
+    auto part_of = [&](int &ci) {
+        if (ci < p.part[0].chunks)
+            return 0;
+        ci -= p.part[0].chunks;
+        if (!APP || ci < p.part[1].chunks)
+            return 1;
+        ci -= p.part[1].chunks;
+        return 2;
+    };
+    auto fetch = [&](int stage) {
+        if constexpr (E > 1) {
+            if (ahead.item < items) {
+                int ci = ahead.c;
+                const RopeRows &r = p.part[part_of(ci)];
+                const int h0 = ci * p.HC + ahead.hc, h1 = min(r.heads, ci * p.HC + p.HC);
+                const char *x = static_cast<const char *>(r.x) + (ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (h0 + u < h1) {
+                        if (slot[0].a < np)
+                            ring.fetch(stage, 2 * u, x, slot[0].a);
+                        if (slot[0].b < np)
+                            ring.fetch(stage, 2 * u + 1, x, slot[0].b);
+                    }
+                    x += r.xh * (int64_t)sizeof(T);
+                }
+            }
+            ahead.next(U, p.HC, step, dt, dc, chunks);
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kRopeDepth - 1; ++i)
+        fetch(i);
+    RopeAngles<E, V> ang;
+    ang.init(p.turn, slot, pair);
+
+    P wa[V], wb[V];
+    int64_t page = 0, within = 0;
+    bool kept = true, turn = false, norm = false;
+    int stage = 0, part = 0, ci = 0;
+    for (int64_t first = g0; first < items; first += (cur.hc == 0 ? step : 0)) {
+        fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
+        const bool live = cur.item < items;
+        if (cur.hc == 0) {
+            // a new piece: its part, its token's angles and its row of the cache
+            ci = cur.c;
+            part = part_of(ci);
+            const RopeRows &r = p.part[part];
+            turn = p.turn.rot > 0 && part < 2;
+            if (turn && live)
+                ang.at(ld_index(p.turn.pos, cur.t, p.turn.pos64), p.turn.amp, 1.f);
+            norm = r.w != nullptr && live;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (norm) {
+                    wa[v] = slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
+                    wb[v] = slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
+                }
+            if (APP) {
+                kept = true;
+                if (part > 0 && live) {
+                    const int64_t s = ld_index(p.cache.slots, cur.t, p.cache.slot64);
+                    kept = s >= 0 && s < p.cache.limit;
+                    page = kept ? s / p.cache.page_size : 0;
+                    within = kept ? s - page * p.cache.page_size : 0;
+                }
             }
         }
         const RopeRows &r = p.part[part];
-        const int h0 = ci * p.HC, h1 = live ? min(r.heads, h0 + p.HC) : 0;
-        const bool turn = p.turn.rot > 0 && part < 2;
-        if (turn && live)
-            ang.at(ld_index(p.turn.pos, t, p.turn.pos64), p.turn.amp, 1.f);
-        P wa[V], wb[V];
-        const bool norm = r.w != nullptr && live;
+        const int h0 = ci * p.HC + cur.hc, h1 = live ? min(r.heads, ci * p.HC + p.HC) : 0;
+        char *yr = static_cast<char *>(r.y);
+        if (!APP || part == 0)
+            yr += (cur.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
+        else
+            yr += (page * (part == 1 ? p.cache.kpage : p.cache.vpage) + within * r.yt + h0 * r.yh) *
+                  (int64_t)sizeof(T);
+        if constexpr (E > 1)
+            copies_wait<kRopeDepth - 1>();
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (norm) {
-                wa[v] = slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
-                wb[v] = slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
-            }
-        // the cache's rows of this token
-        int64_t page = 0, within = 0;
-        bool kept = true;
-        if (APP && part > 0 && live) {
-            const int64_t s = ld_index(p.cache.slots, t, p.cache.slot64);
-            kept = s >= 0 && s < p.cache.limit;
-            page = kept ? s / p.cache.page_size : 0;
-            within = kept ? s - page * p.cache.page_size : 0;
-        }
-        const char *xr = static_cast<const char *>(r.x) + (live ? t * r.xt * (int64_t)sizeof(T) : 0);
-        for (int hc = 0; hc < p.HC; hc += U) {
-            P xa[U][V], xb[U][V];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + hc + u;
-                if (h < h1 && hc + u < p.HC && kept) {
-                    const char *x = xr + h * r.xh * (int64_t)sizeof(T);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        xa[u][v] = slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
-                        xb[u][v] = slot[v].b < np ? P::load(x, slot[v].b) : P::zero();
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        xa[u][v] = xb[u][v] = P::zero();
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (hc + u >= p.HC)
-                    break;                       // the same for all lanes
-                const int h = h0 + hc + u;
-                const bool on = h < h1 && kept;
-                Vals<E> a[V], b[V];
-                using F = typename Vals<E>::F;
-                F ss = splat<F>(0.f);
+        for (int u = 0; u < U; ++u) {
+            if (cur.hc + u >= p.HC)
+                break;                       // the same for all lanes
+            const int h = h0 + u;
+            const bool on = h < h1 && kept;
+            P xa[V], xb[V];
+            if constexpr (E > 1) {
+                xa[0] = on && slot[0].a < np ? ring.get(stage, 2 * u) : P::zero();
+                xb[0] = on && slot[0].b < np ? ring.get(stage, 2 * u + 1) : P::zero();
+            } else {
+                const char *x = static_cast<const char *>(r.x) + (cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    xa[u][v].widen(a[v]);
-                    xb[u][v].widen(b[v]);
+                    xa[v] = on && slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
+                    xb[v] = on && slot[v].b < np ? P::load(x, slot[v].b) : P::zero();
                 }
-                if (p.part[0].w != nullptr || p.part[1].w != nullptr) {      // the same for all lanes
+            }
+            Vals<E> a[V], b[V];
+            using F = typename Vals<E>::F;
+            F ss = splat<F>(0.f);
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v) {
+                xa[v].widen(a[v]);
+                xb[v].widen(b[v]);
+            }
+            if (p.part[0].w != nullptr || p.part[1].w != nullptr) {      // the same for all lanes
 #pragma unroll
-                        for (int i = 0; i < Vals<E>::N; ++i)
-                            ss = vfma(b[v].v[i], b[v].v[i], vfma(a[v].v[i], a[v].v[i], ss));
-                    const float rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
-                    if (norm) {
+                for (int v = 0; v < V; ++v)
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            Vals<E> fa, fb;
-                            wa[v].widen(fa);
-                            wb[v].widen(fb);
-#pragma unroll
-                            for (int i = 0; i < Vals<E>::N; ++i) {
-                                a[v].v[i] = vmul(vmul(a[v].v[i], splat<F>(rs)), fa.v[i]);
-                                b[v].v[i] = vmul(vmul(b[v].v[i], splat<F>(rs)), fb.v[i]);
-                            }
-                        }
-                        if (on && lane == 0 && p.rstd != nullptr && part < 2)
-                            p.rstd[t * (p.part[0].heads + p.part[1].heads) + (part ? p.part[0].heads : 0) +
-                                   h] = rs;
-                    }
-                }
-                if (turn)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
-                if (APP && p.cache.bits4) {
-                    // k and v go through shared memory, a group a lane
-                    float *stage = stage_all + (threadIdx.x >> 5) * kRopeStage +
-                                   ((threadIdx.x & 31) >> p.shift) * (p.D / kKv4Group) * 20;
-                    __syncwarp();
-                    if (on && part > 0) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v)
-#pragma unroll
-                            for (int e = 0; e < E; ++e) {
-                                const int ia = slot[v].a * E + e, ib = slot[v].b * E + e;
-                                if (ia < p.D)
-                                    stage[(ia >> 4) * 20 + (ia & 15)] = a[v].get(e);
-                                if (ib < p.D)
-                                    stage[(ib >> 4) * 20 + (ib & 15)] = b[v].get(e);
-                            }
-                    }
-                    __syncwarp();
-                    if (on && part > 0) {
-                        const float *gs = part == 1 ? p.cache.kscale : p.cache.vscale;
-                        uint8_t *tile = static_cast<uint8_t *>(p.part[1].y) + page * p.cache.kpage +
-                                        (h * (p.cache.page_size / kKv4Tile) + within / kKv4Tile) *
-                                            kv4_tile_bytes(p.D);
-                        store_tile4(stage, p.D, lane, tile, (int)(within % kKv4Tile), part == 2,
-                                    gs ? __ldg(gs + h) : 1.f);
-                        continue;
-                    }
-                }
-                if (on) {
-                    char *y = static_cast<char *>(r.y);
-                    if (APP && part > 0)
-                        y += (page * (part == 1 ? p.cache.kpage : p.cache.vpage) + within * r.yt + h * r.yh) *
-                             (int64_t)sizeof(T);
-                    else
-                        y += (t * r.yt + h * r.yh) * (int64_t)sizeof(T);
+                    for (int i = 0; i < Vals<E>::N; ++i)
+                        ss = vfma(b[v].v[i], b[v].v[i], vfma(a[v].v[i], a[v].v[i], ss));
+                const float rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
+                if (norm) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        if (slot[v].a < np)
-                            P::narrow(a[v]).store(y, slot[v].a);
-                        if (slot[v].b < np)
-                            P::narrow(b[v]).store(y, slot[v].b);
+                        Vals<E> fa, fb;
+                        wa[v].widen(fa);
+                        wb[v].widen(fb);
+#pragma unroll
+                        for (int i = 0; i < Vals<E>::N; ++i) {
+                            a[v].v[i] = vmul(vmul(a[v].v[i], splat<F>(rs)), fa.v[i]);
+                            b[v].v[i] = vmul(vmul(b[v].v[i], splat<F>(rs)), fb.v[i]);
+                        }
                     }
+                    if (on && lane == 0 && p.rstd != nullptr && part < 2)
+                        p.rstd[cur.t * (p.part[0].heads + p.part[1].heads) + (part ? p.part[0].heads : 0) + h] =
+                            rs;
+                }
+            }
+            if (turn)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+            if constexpr (FORM == 2) {
+                // k and v go through shared memory, a group a lane
+                float *st = stage_all + (threadIdx.x >> 5) * kRopeStage +
+                            ((threadIdx.x & 31) >> p.shift) * (p.D / kKv4Group) * 20;
+                __syncwarp();
+                if (on && part > 0) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int ia = slot[v].a * E + e, ib = slot[v].b * E + e;
+                            if (ia < p.D)
+                                st[(ia >> 4) * 20 + (ia & 15)] = a[v].get(e);
+                            if (ib < p.D)
+                                st[(ib >> 4) * 20 + (ib & 15)] = b[v].get(e);
+                        }
+                }
+                __syncwarp();
+                if (on && part > 0) {
+                    const float *gs = part == 1 ? p.cache.kscale : p.cache.vscale;
+                    uint8_t *tile = static_cast<uint8_t *>(p.part[1].y) + page * p.cache.kpage +
+                                    (h * (p.cache.page_size / kKv4Tile) + within / kKv4Tile) *
+                                        kv4_tile_bytes(p.D);
+                    store_tile4(st, p.D, lane, tile, (int)(within % kKv4Tile), part == 2,
+                                gs ? __ldg(gs + h) : 1.f);
+                }
+            }
+            if (on && (FORM != 2 || part == 0)) {
+                char *y = yr + u * r.yh * (int64_t)sizeof(T);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (slot[v].a < np)
+                        P::narrow(a[v]).store(y, slot[v].a);
+                    if (slot[v].b < np)
+                        P::narrow(b[v]).store(y, slot[v].b);
                 }
             }
         }
-        t += dt;
-        c += dc;
-        if (c >= chunks) {
-            c -= chunks;
-            ++t;
-        }
+        stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
+        cur.next(U, p.HC, step, dt, dc, chunks);
     }
 }
 
@@ -449,10 +585,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
 template <typename T, int E, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p)
 {
-    constexpr int V = E == 1 ? 4 : 1, U = E == 1 ? 1 : 2;
+    constexpr int V = E == 1 ? 4 : 1, U = rope_bwd_heads<E>();
     using P = Pack<T, E>;
     using F = typename Vals<E>::F;
-    __shared__ float sums[kRopeThreads * 2 * E * V];
+    extern __shared__ __align__(16) uint8_t smem[];
+    const RopeRing<T, E, 4 * U> ring = {smem + threadIdx.x * (E * sizeof(T))};
 
     const int part = blockIdx.x >= p.ctas_q ? 1 : 0;
     const RopeGradRows &r = p.part[part];
@@ -470,6 +607,46 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     }
     griddep_wait();
     griddep_launch_dependents();
+
+    const int chunks = r.chunks;
+    const int64_t items = p.T * chunks, step = ctas * (kRopeThreads >> p.shift);
+    const int64_t g0 = ((int64_t)cta * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
+    const int64_t dt = step / chunks;
+    const int dc = (int)(step - dt * chunks);
+    RopeCursor cur, ahead;
+    cur.start(g0 + ((threadIdx.x & 31) >> p.shift), chunks);
+    ahead = cur;
+    auto fetch = [&](int stage) {
+        if constexpr (E > 1) {
+            if (ahead.item < items) {
+                const int h0 = ahead.c * p.HC + ahead.hc, h1 = min(r.heads, ahead.c * p.HC + p.HC);
+                const char *y = static_cast<const char *>(r.dy) + (ahead.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
+                const char *x = static_cast<const char *>(r.x) + (ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (h0 + u < h1) {
+                        if (slot[0].a < np) {
+                            ring.fetch(stage, 4 * u, y, slot[0].a);
+                            if (norm)
+                                ring.fetch(stage, 4 * u + 2, x, slot[0].a);
+                        }
+                        if (slot[0].b < np) {
+                            ring.fetch(stage, 4 * u + 1, y, slot[0].b);
+                            if (norm)
+                                ring.fetch(stage, 4 * u + 3, x, slot[0].b);
+                        }
+                    }
+                    y += r.yh * (int64_t)sizeof(T);
+                    x += r.xh * (int64_t)sizeof(T);
+                }
+            }
+            ahead.next(U, p.HC, step, dt, dc, chunks);
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kRopeDepth - 1; ++i)
+        fetch(i);
     RopeAngles<E, V> ang;
     ang.init(p.turn, slot, pair);
     P wa[V], wb[V];
@@ -482,115 +659,121 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
         db[v] = Vals<E>::zero();
     }
 
-    const int chunks = r.chunks;
-    const int64_t items = p.T * chunks, step = ctas * (kRopeThreads >> p.shift);
-    const int64_t g0 = ((int64_t)cta * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
-    int64_t item = g0 + ((threadIdx.x & 31) >> p.shift);
-    int64_t t = item / chunks;
-    int c = (int)(item - t * chunks);
-    const int64_t dt = step / chunks;
-    const int dc = (int)(step - dt * chunks);
-    for (int64_t first = g0; first < items; first += step, item += step) {
-        const bool live = item < items;
-        const int h0 = c * p.HC, h1 = live ? min(r.heads, h0 + p.HC) : 0;
-        if (p.turn.rot > 0 && live)
-            ang.at(ld_index(p.turn.pos, t, p.turn.pos64), p.turn.amp, -1.f);
-        for (int hc = 0; hc < p.HC; hc += U) {
-            P ya[U][V], yb[U][V], xa[U][V], xb[U][V];
-            float rsv[U];
+    int stage = 0;
+    for (int64_t first = g0; first < items; first += (cur.hc == 0 ? step : 0)) {
+        fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
+        const bool live = cur.item < items;
+        const int h0 = cur.c * p.HC + cur.hc, h1 = live ? min(r.heads, cur.c * p.HC + p.HC) : 0;
+        if (cur.hc == 0 && p.turn.rot > 0 && live)
+            ang.at(ld_index(p.turn.pos, cur.t, p.turn.pos64), p.turn.amp, -1.f);
+        float rsv[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + hc + u;
-                const bool on = h < h1 && hc + u < p.HC;
-                const char *y = static_cast<const char *>(r.dy) + (t * r.yt + h * r.yh) * (int64_t)sizeof(T);
-                const char *x = static_cast<const char *>(r.x) + (t * r.xt + h * r.xh) * (int64_t)sizeof(T);
-                rsv[u] = on && norm && p.rstd != nullptr ? __ldg(p.rstd + t * heads_all + head0 + h) : 0.f;
+        for (int u = 0; u < U; ++u)
+            rsv[u] = h0 + u < h1 && norm && p.rstd != nullptr
+                         ? __ldg(p.rstd + cur.t * heads_all + head0 + h0 + u) : 0.f;
+        if constexpr (E > 1)
+            copies_wait<kRopeDepth - 1>();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (cur.hc + u >= p.HC)
+                break;
+            const int h = h0 + u;
+            const bool on = h < h1;
+            Vals<E> a[V], b[V], fa[V], fb[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                P ya = P::zero(), yb = P::zero(), xa = P::zero(), xb = P::zero();
+                if constexpr (E > 1) {
+                    if (on && slot[0].a < np) {
+                        ya = ring.get(stage, 4 * u);
+                        if (norm)
+                            xa = ring.get(stage, 4 * u + 2);
+                    }
+                    if (on && slot[0].b < np) {
+                        yb = ring.get(stage, 4 * u + 1);
+                        if (norm)
+                            xb = ring.get(stage, 4 * u + 3);
+                    }
+                } else if (on) {
+                    const char *y = static_cast<const char *>(r.dy) + (cur.t * r.yt + h * r.yh) * (int64_t)sizeof(T);
+                    const char *x = static_cast<const char *>(r.x) + (cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
+                    if (slot[v].a < np) {
+                        ya = P::load(y, slot[v].a);
+                        if (norm)
+                            xa = P::load(x, slot[v].a);
+                    }
+                    if (slot[v].b < np) {
+                        yb = P::load(y, slot[v].b);
+                        if (norm)
+                            xb = P::load(x, slot[v].b);
+                    }
+                }
+                ya.widen(a[v]);
+                yb.widen(b[v]);
+                xa.widen(fa[v]);
+                xb.widen(fb[v]);
+                if (p.turn.rot > 0)
+                    rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+            }
+            if (norm) {
+                F ss = splat<F>(0.f), sc = splat<F>(0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    ya[u][v] = on && slot[v].a < np ? P::load(y, slot[v].a) : P::zero();
-                    yb[u][v] = on && slot[v].b < np ? P::load(y, slot[v].b) : P::zero();
-                    if (norm) {
-                        xa[u][v] = on && slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
-                        xb[u][v] = on && slot[v].b < np ? P::load(x, slot[v].b) : P::zero();
+                    Vals<E> ga, gb;
+                    wa[v].widen(ga);
+                    wb[v].widen(gb);
+#pragma unroll
+                    for (int i = 0; i < Vals<E>::N; ++i) {
+                        const F tx = vmul(a[v].v[i], fa[v].v[i]), ty = vmul(b[v].v[i], fb[v].v[i]);
+                        sc = vfma(ty, gb.v[i], vfma(tx, ga.v[i], sc));
+                        ss = vfma(fb[v].v[i], fb[v].v[i], vfma(fa[v].v[i], fa[v].v[i], ss));
+                    }
+                }
+                float rs = rsv[u];
+                if (p.rstd == nullptr)
+                    rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
+                const float cm = lanes_sum(hsum(sc), p.shift) / (float)p.D;
+                const float k = -rs * rs * rs * cm;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    Vals<E> ga, gb;
+                    wa[v].widen(ga);
+                    wb[v].widen(gb);
+#pragma unroll
+                    for (int i = 0; i < Vals<E>::N; ++i) {
+                        const F xa1 = vmul(fa[v].v[i], splat<F>(rs)), xb1 = vmul(fb[v].v[i], splat<F>(rs));
+                        if (on) {
+                            da[v].v[i] = vfma(a[v].v[i], xa1, da[v].v[i]);
+                            db[v].v[i] = vfma(b[v].v[i], xb1, db[v].v[i]);
+                        }
+                        a[v].v[i] = vfma(vmul(a[v].v[i], ga.v[i]), splat<F>(rs),
+                                         vmul(fa[v].v[i], splat<F>(k)));
+                        b[v].v[i] = vfma(vmul(b[v].v[i], gb.v[i]), splat<F>(rs),
+                                         vmul(fb[v].v[i], splat<F>(k)));
                     }
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (hc + u >= p.HC)
-                    break;
-                const int h = h0 + hc + u;
-                const bool on = h < h1;
-                Vals<E> a[V], b[V];
+            if (on) {
+                char *d = static_cast<char *>(r.dx) + (cur.t * r.dt + h * r.dh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    ya[u][v].widen(a[v]);
-                    yb[u][v].widen(b[v]);
-                    if (p.turn.rot > 0)
-                        rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
-                }
-                if (norm) {
-                    Vals<E> fa[V], fb[V];
-                    F ss = splat<F>(0.f), sc = splat<F>(0.f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        Vals<E> ga, gb;
-                        xa[u][v].widen(fa[v]);
-                        xb[u][v].widen(fb[v]);
-                        wa[v].widen(ga);
-                        wb[v].widen(gb);
-#pragma unroll
-                        for (int i = 0; i < Vals<E>::N; ++i) {
-                            const F tx = vmul(a[v].v[i], fa[v].v[i]), ty = vmul(b[v].v[i], fb[v].v[i]);
-                            sc = vfma(ty, gb.v[i], vfma(tx, ga.v[i], sc));
-                            ss = vfma(fb[v].v[i], fb[v].v[i], vfma(fa[v].v[i], fa[v].v[i], ss));
-                        }
-                    }
-                    float rs = rsv[u];
-                    if (p.rstd == nullptr)
-                        rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
-                    const float cm = lanes_sum(hsum(sc), p.shift) / (float)p.D;
-                    const float k = -rs * rs * rs * cm;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        Vals<E> ga, gb;
-                        wa[v].widen(ga);
-                        wb[v].widen(gb);
-#pragma unroll
-                        for (int i = 0; i < Vals<E>::N; ++i) {
-                            const F xa1 = vmul(fa[v].v[i], splat<F>(rs)), xb1 = vmul(fb[v].v[i], splat<F>(rs));
-                            if (on) {
-                                da[v].v[i] = vfma(a[v].v[i], xa1, da[v].v[i]);
-                                db[v].v[i] = vfma(b[v].v[i], xb1, db[v].v[i]);
-                            }
-                            a[v].v[i] = vfma(vmul(a[v].v[i], ga.v[i]), splat<F>(rs),
-                                             vmul(fa[v].v[i], splat<F>(k)));
-                            b[v].v[i] = vfma(vmul(b[v].v[i], gb.v[i]), splat<F>(rs),
-                                             vmul(fb[v].v[i], splat<F>(k)));
-                        }
-                    }
-                }
-                if (on) {
-                    char *d = static_cast<char *>(r.dx) + (t * r.dt + h * r.dh) * (int64_t)sizeof(T);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (slot[v].a < np)
-                            P::narrow(a[v]).store(d, slot[v].a);
-                        if (slot[v].b < np)
-                            P::narrow(b[v]).store(d, slot[v].b);
-                    }
+                    if (slot[v].a < np)
+                        P::narrow(a[v]).store(d, slot[v].a);
+                    if (slot[v].b < np)
+                        P::narrow(b[v]).store(d, slot[v].b);
                 }
             }
         }
-        t += dt;
-        c += dc;
-        if (c >= chunks) {
-            c -= chunks;
-            ++t;
-        }
+        stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
+        cur.next(U, p.HC, step, dt, dc, chunks);
     }
     if (!norm)
         return;
+    // the ring is empty: its place holds the groups' sums
+    float *sums = reinterpret_cast<float *>(smem);
+    if constexpr (E > 1)
+        copies_wait<0>();
+    __syncthreads();
     const int grp = threadIdx.x >> p.shift, groups = kRopeThreads >> p.shift;
 #pragma unroll
     for (int v = 0; v < V; ++v)

@@ -143,12 +143,13 @@ bool touches_inputs(Span o, const rmsnorm_rotation *r, int64_t T, int64_t D, siz
             overlap(o, flat(r->freq, (size_t)r->rot / 2 * 8)));
 }
 
-int launch_rows(RopeParams &p, const RopeKernel &k, bool append, int kind, cudaStream_t stream)
+// form: 0 the forward, 1 the append of rows, 2 the append in 4 bits.
+int launch_rows(RopeParams &p, const RopeKernel &k, int form, cudaStream_t stream)
 {
     int dev, sms, bps, st;
-    const void *fn = append ? k.append[kind] : k.fwd[kind];
+    const void *fn = k.fwd[form][p.turn.adjacent];
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)) ||
-        (st = blocks_per_sm(fn, kRopeThreads, dev, &bps)))
+        (st = blocks_per_sm(fn, kRopeThreads, dev, &bps, k.fwd_smem[form])))
         return st;
     p.shift = lane_shift(k.E, p.D);
     const int64_t per = kRopeThreads >> p.shift;
@@ -158,10 +159,11 @@ int launch_rows(RopeParams &p, const RopeKernel &k, bool append, int kind, cudaS
         n += r.chunks = (r.heads + p.HC - 1) / p.HC;
     const int64_t ctas = std::min<int64_t>((p.T * n + per - 1) / per, (int64_t)sms * bps);
     void *args[1] = {&p};
-    const cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kRopeThreads, 0, stream, args);
+    const cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kRopeThreads, (size_t)k.fwd_smem[form], stream,
+                                     args);
     if (e != cudaSuccess)
         return cuda_fail(e);
-    t_last_path = append ? kPathRopeAppend : kPathRope;
+    t_last_path = form ? kPathRopeAppend : kPathRope;
     return RMSNORM_OK;
 }
 
@@ -247,7 +249,7 @@ int append_impl(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsnorm_he
     p.T = T;
     p.D = (int)D;
     p.eps = eps;
-    p.cache = {slots, slot_bits == 64 ? 1 : 0, c.bits4 ? 1 : 0, c.page_size, c.pages * c.page_size,
+    p.cache = {slots, slot_bits == 64 ? 1 : 0, c.page_size, c.pages * c.page_size,
                c.bits4 ? Hk * (c.page_size / kKv4Tile) * 18 * D : c.k_page, c.v_page, c.k_scale, c.v_scale};
     Strided rows[6];
     int n = 0;
@@ -263,7 +265,7 @@ int append_impl(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsnorm_he
     }
     const RopeSet &set = rope_set(dtype);
     const RopeKernel &kern = set.k[pick_packs(set, D, p.turn, es, rows, n, wq, k->w)];
-    return launch_rows(p, kern, true, p.turn.adjacent, stream);
+    return launch_rows(p, kern, c.bits4 ? 2 : 1, stream);
 }
 
 } // namespace
@@ -322,7 +324,7 @@ int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsno
         }
     const RopeSet &set = rope_set(dtype);
     const RopeKernel &kern = set.k[pick_packs(set, D, p.turn, es, rows, n, q->w, wk)];
-    return launch_rows(p, kern, false, p.turn.adjacent, static_cast<cudaStream_t>(stream));
+    return launch_rows(p, kern, 0, static_cast<cudaStream_t>(stream));
 }
 
 size_t rmsnorm_rope_bwd_workspace_bytes(int64_t D)
@@ -429,7 +431,7 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
     const void *fn = kern.bwd[p.turn.adjacent];
     int bps;
     if ((st = current_device(&dev)) || (st = sm_count(dev, &sms)) ||
-        (st = blocks_per_sm(fn, kRopeThreads, dev, &bps)))
+        (st = blocks_per_sm(fn, kRopeThreads, dev, &bps, kern.bwd_smem)))
         return st;
     p.shift = lane_shift(kern.E, D);
     const int64_t per = kRopeThreads >> p.shift;
@@ -451,7 +453,7 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
     const int ctas = (int)(cq + ck);
     if (ctas > 0) {
         void *args[1] = {&p};
-        const cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kRopeThreads, 0, s, args);
+        const cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kRopeThreads, (size_t)kern.bwd_smem, s, args);
         if (e != cudaSuccess)
             return cuda_fail(e);
     }

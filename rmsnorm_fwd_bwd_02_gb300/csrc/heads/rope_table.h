@@ -3,12 +3,12 @@
 #pragma once
 
 #define ROPE_ADJ(E) ((E) > 1)
+#define ROPE_FORMS(T, E, F)                                                                             \
+    {(const void *)rms_rope_fwd<T, E, false, F>, (const void *)rms_rope_fwd<T, E, ROPE_ADJ(E), F>}
 #define ROPE_KERNELS(T, E)                                                                              \
     {                                                                                                   \
-        E,                                                                                              \
-            {(const void *)rms_rope_fwd<T, E, false, false>,                                            \
-             (const void *)rms_rope_fwd<T, E, ROPE_ADJ(E), false>},                                     \
-            {(const void *)rms_rope_fwd<T, E, false, true>,                                             \
-             (const void *)rms_rope_fwd<T, E, ROPE_ADJ(E), true>},                                      \
-            {(const void *)rms_rope_bwd<T, E, false>, (const void *)rms_rope_bwd<T, E, ROPE_ADJ(E)>}    \
+        E, {ROPE_FORMS(T, E, 0), ROPE_FORMS(T, E, 1), ROPE_FORMS(T, E, 2)},                             \
+            {rope_fwd_smem<E>(0, sizeof(T)), rope_fwd_smem<E>(1, sizeof(T)), rope_fwd_smem<E>(2, sizeof(T))},  \
+            {(const void *)rms_rope_bwd<T, E, false>, (const void *)rms_rope_bwd<T, E, ROPE_ADJ(E)>},   \
+            rope_bwd_smem<E>(sizeof(T))                                                                 \
     }

@@ -11,6 +11,9 @@ many roundings again of its own magnitude: 64 * 2^-24 of the terms' sum. dw: a
 lane adds its rows one after another (at most R of them), then a tree over the
 groups and the CTAs: (R + 64) 2^-24 of the sum of magnitudes.
 """
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -166,26 +169,31 @@ def test_scaled_frequencies_definitions():
     assert bool((ratio[1:] >= ratio[:-1] - 1e-12).all())
 
 
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
 def test_far_and_negative_positions():
-    """The angle keeps its fraction at any position: against exact whole
-    fractions of a turn, and against 64 bits where those still hold it."""
-    quarter = torch.tensor([torch.pi / 2, torch.pi / 4, torch.pi, 2 * torch.pi], dtype=F64, device=DEV)
-    x = normal((6, 2, 8), F32, 7)
-    pos = torch.tensor([0, 1 << 40, (1 << 40) + 1, -1, -(1 << 50) - 3, (1 << 62) + 2], device=DEV)
-    small = pos % 8                              # whole turns drop out
-    y, _, _ = rn.rmsnorm_rope_fwd(x, pos, quarter)
-    want, size = turn(x.to(F64), small, quarter, False)
-    # quarter * 2^50 / 2 pi: 64-bit freq is within 2^-54 of pi / 2
-    near = (pos.abs() <= 1 << 41)[:, None, None]
-    close(y, want, torch.where(near, 2.0 ** -10, 1e9) * size + 24 * ULP * size)
-    # the first three are exact in the fixed point: freq / 2 pi rounds to 1/4, 1/8, 1/2
-    close(y[..., :3], want[..., :3], 24 * ULP * size[..., :3])
-    f = freqs(128)
-    q = normal((4, 3, 128), F32, 8)
-    pos = torch.tensor([(1 << 24) + 1, -(1 << 24) - 5, 1 << 20, -77], device=DEV, dtype=torch.int32)
-    y, _, _ = rn.rmsnorm_rope_fwd(q, pos, f)
-    want, size = turn(q.to(F64), pos, f, False)
-    close(y, want, (24 * ULP + 2.0 ** -52 * (1 << 24)) * size)
+    """The angle keeps its fraction at any position: against exact rational
+    arithmetic on the 64-bit freq. The kernel's fraction of a turn is within
+    2^-64 (half a unit and the truncation of the product's), so |position|
+    2^-64 of a turn, and 2^-32 for its top half alone."""
+    freq = [math.pi / 2, 1.0, 0.1, 2 * math.pi, 1e-4, 7.5, -0.3, 0.0]
+    pos = [0, 1 << 40, (1 << 40) + 1, -1, -(1 << 41) - 3, (1 << 33) + 2, -77, 123456789]
+    f = torch.tensor(freq, dtype=F64, device=DEV)
+    for adjacent in (False, True):
+        for kind in (torch.int64, torch.int32):
+            at = [p for p in pos if kind == torch.int64 or abs(p) < 1 << 31]
+            x = normal((len(at), 2, 16), F32, 7)
+            y, _, _ = rn.rmsnorm_rope_fwd(x, torch.tensor(at, dtype=kind, device=DEV), f, interleaved=adjacent)
+            turns = [[Fraction(w) * t / (2 * PI) % 1 for w in freq] for t in at]
+            angle = torch.tensor([[float(t * 2 * PI) for t in row] for row in turns], dtype=F64, device=DEV)
+            # angles below a turn: position 1 at these frequencies, each token its own
+            want = torch.cat([turn(x[i:i + 1].to(F64), torch.ones(1, device=DEV), angle[i], adjacent)[0]
+                              for i in range(len(at))])
+            size = torch.cat([turn(x[i:i + 1].to(F64), torch.ones(1, device=DEV), angle[i], adjacent)[1]
+                              for i in range(len(at))])
+            off = torch.tensor([abs(t) * 2.0 ** -64 + 2.0 ** -32 for t in at], dtype=F64, device=DEV) * 2 * math.pi
+            close(y, want, (24 * ULP + off[:, None, None]) * size)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
