@@ -54,7 +54,7 @@ struct RopeParams {
     int D;
     int shift;                 // log2 of the lanes a row
     int HC;                    // heads a piece
-    float eps;
+    float eps, inv_d;          // 1 / D
 };
 
 struct RopeGradRows {
@@ -80,7 +80,7 @@ struct RopeGradParams {
     int shift;
     int HC;
     int ctas_q;                // CTAs that work on part[0]; the others on part[1]
-    float eps;
+    float eps, inv_d;
 };
 
 // The kernels of one element type: packs of 16 bytes, of half of it (16-bit

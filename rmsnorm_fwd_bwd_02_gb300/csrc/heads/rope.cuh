@@ -76,8 +76,8 @@ __device__ __forceinline__ int64_t ld_index(const void *p, int64_t i, int wide)
 
 // freq (radians a position) as a fraction of a turn, 2^64 to the turn: its 53
 // bits times 1 / (2 pi) in 66, shifted by its exponent, whole turns dropped.
-// In integers: a product in 64-bit floating point takes this GPU some 0.4 us,
-// and a lane needs eight (one token of 16 heads took 5.0 us with them).
+// In integers: 64-bit floating point is slow here (one token of 16 heads took
+// 5.0 us with it, 3.6 without).
 __device__ __forceinline__ uint64_t turn_fraction(double freq)
 {
     const uint64_t bits = (uint64_t)__double_as_longlong(freq);
@@ -144,72 +144,113 @@ __device__ __forceinline__ RopeSlot rope_slot(int pair, int rot, int adjacent)
     return s;
 }
 
-// (a, b) turned by the E angles of a slot; sn negated turns back.
-template <int E, bool ADJ>
-__device__ __forceinline__ void rope_turn(Vals<E> &a, Vals<E> &b, const float (&cs)[E],
-                                          const float (&sn)[E], int turns)
-{
-    if constexpr (ADJ) {
-        // pairs lie within a pack: a has the first E / 2, b the others
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float2 &v = e < E / 2 ? a.v[e] : b.v[e - E / 2];
-            const float2 t = make_float2(fmaf(v.x, cs[e], -(v.y * sn[e])), fmaf(v.y, cs[e], v.x * sn[e]));
-            if (e < turns)
-                v = t;
-        }
-    } else if (turns) {
-        using F = typename Vals<E>::F;
-#pragma unroll
-        for (int i = 0; i < Vals<E>::N; ++i) {
-            F c, s, m;
-            if constexpr (E == 1) {
-                c = cs[0]; s = sn[0]; m = -sn[0];
-            } else {
-                c = make_float2(cs[2 * i], cs[2 * i + 1]);
-                s = make_float2(sn[2 * i], sn[2 * i + 1]);
-                m = make_float2(-sn[2 * i], -sn[2 * i + 1]);
-            }
-            const F x = a.v[i], y = b.v[i];
-            a.v[i] = vfma(x, c, vmul(y, m));
-            b.v[i] = vfma(y, c, vmul(x, s));
-        }
-    }
-}
-
 // Sum over the 2^shift lanes of a group; all lanes of the warp take part.
 __device__ __forceinline__ float lanes_sum(float v, int shift)
 {
-    for (int o = (1 << shift) >> 1; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+#pragma unroll
+    for (int i = 4; i >= 0; --i)
+        if (shift > i)                                   // the same for all lanes
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1 << i);
     return v;
 }
 
-template <int E, int V>
-struct RopeAngles {
-    uint64_t f[V][E];
-    float cs[V][E], sn[V][E];
-    __device__ __forceinline__ void init(const RopeTurn &t, const RopeSlot (&s)[V], const int (&pair)[V])
+__device__ __forceinline__ float swapped(float v) { return v; }
+__device__ __forceinline__ float2 swapped(float2 v) { return make_float2(v.y, v.x); }
+
+// The map of a slot's two packs, the weight before the rotation:
+//   halves:   a' = a m[0] + b n[0],  b' = b m[1] + a n[1]
+//   adjacent: a' = a m[0] + swapped(a) n[0], and b' likewise (pairs lie within
+//   the two-element words)
+// with m = w cos and n = -+ w sin, made once for a token and a part, so that a
+// head takes two operations an element. Elements that do not turn have m = w.
+template <int E, bool ADJ>
+struct RopeMap {
+    using F = typename Vals<E>::F;
+    static constexpr int N = Vals<E>::N;
+    F m[2][N], n[2][N];
+
+    __device__ __forceinline__ void make(const float (&cs)[E], const float (&sn)[E], const Vals<E> &wa,
+                                         const Vals<E> &wb, int turns)
     {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[v][e] = e < s[v].turns ? turn_fraction(__ldg(t.freq + pair[v] * E + e)) : 0;
-    }
-    // sign: 1 to turn, -1 to turn back
-    __device__ __forceinline__ void at(int64_t pos, float amp, float sign)
-    {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
+        if constexpr (ADJ) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                sincos_turn(f[v][e], pos, sn[v][e], cs[v][e]);
-                sn[v][e] *= amp * sign;
-                cs[v][e] *= amp;
+                const float2 w = e < E / 2 ? wa.v[e] : wb.v[e - E / 2];
+                const bool on = e < turns;
+                m[e / (E / 2)][e % (E / 2)] = on ? make_float2(w.x * cs[e], w.y * cs[e]) : w;
+                n[e / (E / 2)][e % (E / 2)] = make_float2(-w.y * sn[e], w.x * sn[e]);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                F c, s;
+                if constexpr (E == 1) {
+                    c = cs[0];
+                    s = sn[0];
+                } else {
+                    c = make_float2(cs[2 * i], cs[2 * i + 1]);
+                    s = make_float2(sn[2 * i], sn[2 * i + 1]);
+                }
+                const F none = splat<F>(0.f);
+                m[0][i] = turns ? vmul(wa.v[i], c) : wa.v[i];
+                m[1][i] = turns ? vmul(wb.v[i], c) : wb.v[i];
+                n[0][i] = vfma(vmul(wb.v[i], s), splat<F>(-1.f), none);
+                n[1][i] = vmul(wa.v[i], s);
+            }
+        }
+    }
+    __device__ __forceinline__ void apply(Vals<E> &a, Vals<E> &b, int turns) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const F x = a.v[i], y = b.v[i];
+            a.v[i] = vmul(x, m[0][i]);
+            b.v[i] = vmul(y, m[1][i]);
+            if constexpr (ADJ) {
+                // what does not turn is not touched by its neighbour, an infinity for instance
+                if (i < turns)
+                    a.v[i] = vfma(swapped(x), n[0][i], a.v[i]);
+                if (i + E / 2 < turns)
+                    b.v[i] = vfma(swapped(y), n[1][i], b.v[i]);
+            } else if (turns) {
+                a.v[i] = vfma(y, n[0][i], a.v[i]);
+                b.v[i] = vfma(x, n[1][i], b.v[i]);
+            }
+        }
     }
 };
+
+template <int E>
+__device__ __forceinline__ Vals<E> rope_ones()
+{
+    Vals<E> r;
+#pragma unroll
+    for (int i = 0; i < Vals<E>::N; ++i)
+        r.v[i] = splat<typename Vals<E>::F>(1.f);
+    return r;
+}
+
+// The frequencies' fractions, one copy a CTA (a lane's own would take it
+// sixteen registers).
+__device__ __forceinline__ void rope_fractions(const RopeTurn &t, uint64_t *f)
+{
+    for (int i = threadIdx.x; i < t.rot / 2; i += kRopeThreads)
+        f[i] = turn_fraction(__ldg(t.freq + i));
+    __syncthreads();
+}
+
+// cs and sn of the slot's pairs; sign: 1 to turn, -1 to turn back.
+template <int E>
+__device__ __forceinline__ void rope_angles(const uint64_t *f, int pair, int turns, int64_t pos, float amp,
+                                            float sign, float (&cs)[E], float (&sn)[E])
+{
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        sincos_turn(e < turns ? f[pair * E + e] : 0, pos, sn[e], cs[e]);
+        sn[e] *= amp * sign;
+        cs[e] *= amp;
+    }
+}
 
 // ------------------------------------------------------------ 4-bit rows
 // 16 values of a group as eight bytes of e2m1 codes (the even one in a byte's
@@ -263,11 +304,12 @@ template <int E> __host__ __device__ constexpr int rope_fwd_heads(int form)
     return E == 1 ? 1 : (form == 2 ? 2 : 4);           // heads a batch; 4-bit rows want room beside the ring
 }
 template <int E> __host__ __device__ constexpr int rope_bwd_heads() { return E == 1 ? 1 : 2; }
+constexpr int kRopeFractions = kRopeMaxD / 2 * 8;      // bytes of the frequencies' fractions
 constexpr int kRopeStage = 640;                        // floats of a warp's staged rows (append in 4 bits)
 template <int E>
 __host__ __device__ constexpr int rope_fwd_smem(int form, size_t es)
 {
-    return (E == 1 ? 0 : kRopeDepth * rope_fwd_heads<E>(form) * 2 * E * (int)es * kRopeThreads) +
+    return kRopeFractions + (E == 1 ? 0 : kRopeDepth * rope_fwd_heads<E>(form) * 2 * E * (int)es * kRopeThreads) +
            (form == 2 ? kRopeThreads / 32 * kRopeStage * 4 : 0);
 }
 template <int E>
@@ -275,7 +317,7 @@ __host__ __device__ constexpr int rope_bwd_smem(size_t es)
 {
     const int ring = E == 1 ? 0 : kRopeDepth * rope_bwd_heads<E>() * 4 * E * (int)es * kRopeThreads;
     const int sums = kRopeThreads * 2 * E * (E == 1 ? 4 : 1) * 4;
-    return ring > sums ? ring : sums;
+    return kRopeFractions + (ring > sums ? ring : sums);
 }
 
 template <int N>
@@ -316,30 +358,30 @@ struct RopeRing {
 };
 
 // Where a group of lanes is in the call's list: token t, piece c of its heads,
-// head hc of the piece.
+// head hc of the piece. Done at t >= T (T is below 2^31, and so is a step).
 struct RopeCursor {
-    int64_t item, t;
+    uint32_t t;
     int c, hc;
     __device__ __forceinline__ void start(int64_t i, int chunks)
     {
-        item = i;
-        t = i / chunks;
-        c = (int)(i - t * chunks);
+        const int64_t q = i / chunks;
+        t = (uint32_t)min(q, (int64_t)0x7FFFFFFF);
+        c = (int)(i - q * chunks);
         hc = 0;
     }
-    __device__ __forceinline__ void next(int U, int HC, int64_t step, int64_t dt, int dc, int chunks)
+    __device__ __forceinline__ void next(int U, int HC, uint32_t dt, int dc, int chunks)
     {
         hc += U;
         if (hc < HC)
             return;
         hc = 0;
-        item += step;
         t += dt;
         c += dc;
         if (c >= chunks) {
             c -= chunks;
             ++t;
         }
+        t = min(t, 0x7FFFFFFFu);
     }
 };
 
@@ -374,9 +416,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     constexpr int V = E == 1 ? 4 : 1, U = rope_fwd_heads<E>(FORM);
     using P = Pack<T, E>;
     extern __shared__ __align__(16) uint8_t smem[];
-    // the staged rows first, then the ring
-    float *stage_all = reinterpret_cast<float *>(smem);
-    const RopeRing<T, E, 2 * U> ring = {smem + (FORM == 2 ? kRopeThreads / 32 * kRopeStage * 4 : 0) +
+    uint64_t *fractions = reinterpret_cast<uint64_t *>(smem);
+    // the fractions first, the staged rows, then the ring
+    float *stage_all = reinterpret_cast<float *>(smem + kRopeFractions);
+    const RopeRing<T, E, 2 * U> ring = {smem + kRopeFractions + (FORM == 2 ? kRopeThreads / 32 * kRopeStage * 4 : 0) +
                                         threadIdx.x * (E * sizeof(T))};
 
     const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
@@ -391,15 +434,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     griddep_wait();
     griddep_launch_dependents();
 
-    const int64_t items = p.T * chunks;
-    const int64_t step = (int64_t)gridDim.x * (kRopeThreads >> p.shift);
-    // the warp's first group decides when the warp is done (its lanes stay
-    // together in the sums' shuffles)
-    const int64_t g0 = ((int64_t)blockIdx.x * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
-    const int64_t dt = step / chunks;
+    const uint32_t T_ = (uint32_t)p.T, step = gridDim.x * (kRopeThreads >> p.shift);
+    const uint32_t dt = step / chunks;
     const int dc = (int)(step - dt * chunks);
     RopeCursor cur, ahead;
-    cur.start(g0 + ((threadIdx.x & 31) >> p.shift), chunks);
+    cur.start(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> p.shift, chunks);
     ahead = cur;
 
     // which heads a piece has: q's, k's or v's
@@ -414,11 +453,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     };
     auto fetch = [&](int stage) {
         if constexpr (E > 1) {
-            if (ahead.item < items) {
+            if (ahead.t < T_) {
                 int ci = ahead.c;
                 const RopeRows &r = p.part[part_of(ci)];
                 const int h0 = ci * p.HC + ahead.hc, h1 = min(r.heads, ci * p.HC + p.HC);
-                const char *x = static_cast<const char *>(r.x) + (ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
+                const char *x = static_cast<const char *>(r.x) + ((int64_t)ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 + u < h1) {
@@ -430,38 +469,48 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
                     x += r.xh * (int64_t)sizeof(T);
                 }
             }
-            ahead.next(U, p.HC, step, dt, dc, chunks);
+            ahead.next(U, p.HC, dt, dc, chunks);
             copies_commit();
         }
     };
 #pragma unroll
     for (int i = 0; i < kRopeDepth - 1; ++i)
         fetch(i);
-    RopeAngles<E, V> ang;
-    ang.init(p.turn, slot, pair);
+    rope_fractions(p.turn, fractions);
 
-    P wa[V], wb[V];
+    const bool any_norm = p.part[0].w != nullptr || p.part[1].w != nullptr;
+    RopeMap<E, ADJ> map[V];
     int64_t page = 0, within = 0;
-    bool kept = true, turn = false, norm = false;
+    bool kept = true, mapped = false, norm = false;
     int stage = 0, part = 0, ci = 0;
-    for (int64_t first = g0; first < items; first += (cur.hc == 0 ? step : 0)) {
+    // the lanes of a warp stay together in the sums' shuffles: done when all are
+    while (__any_sync(0xFFFFFFFFu, cur.t < T_)) {
         fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
-        const bool live = cur.item < items;
+        const bool live = cur.t < T_;
         if (cur.hc == 0) {
-            // a new piece: its part, its token's angles and its row of the cache
+            // a new piece: its part, its token's rotation and its row of the cache
             ci = cur.c;
             part = part_of(ci);
             const RopeRows &r = p.part[part];
-            turn = p.turn.rot > 0 && part < 2;
-            if (turn && live)
-                ang.at(ld_index(p.turn.pos, cur.t, p.turn.pos64), p.turn.amp, 1.f);
             norm = r.w != nullptr && live;
+            mapped = live && (norm || (p.turn.rot > 0 && part < 2));
+            if (mapped) {
+                const bool turn = p.turn.rot > 0;
+                const int64_t pos = turn ? ld_index(p.turn.pos, cur.t, p.turn.pos64) : 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (norm) {
-                    wa[v] = slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
-                    wb[v] = slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
+                for (int v = 0; v < V; ++v) {
+                    Vals<E> wa = rope_ones<E>(), wb = rope_ones<E>();
+                    if (norm) {
+                        if (slot[v].a < np)
+                            P::load_cached(r.w, slot[v].a).widen(wa);
+                        if (slot[v].b < np)
+                            P::load_cached(r.w, slot[v].b).widen(wb);
+                    }
+                    float cs[E], sn[E];
+                    rope_angles<E>(fractions, pair[v], slot[v].turns, pos, p.turn.amp, 1.f, cs, sn);
+                    map[v].make(cs, sn, wa, wb, slot[v].turns);
                 }
+            }
             if (APP) {
                 kept = true;
                 if (part > 0 && live) {
@@ -476,7 +525,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
         const int h0 = ci * p.HC + cur.hc, h1 = live ? min(r.heads, ci * p.HC + p.HC) : 0;
         char *yr = static_cast<char *>(r.y);
         if (!APP || part == 0)
-            yr += (cur.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
+            yr += ((int64_t)cur.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
         else
             yr += (page * (part == 1 ? p.cache.kpage : p.cache.vpage) + within * r.yt + h0 * r.yh) *
                   (int64_t)sizeof(T);
@@ -493,7 +542,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
                 xa[0] = on && slot[0].a < np ? ring.get(stage, 2 * u) : P::zero();
                 xb[0] = on && slot[0].b < np ? ring.get(stage, 2 * u + 1) : P::zero();
             } else {
-                const char *x = static_cast<const char *>(r.x) + (cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
+                const char *x = static_cast<const char *>(r.x) + ((int64_t)cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     xa[v] = on && slot[v].a < np ? P::load(x, slot[v].a) : P::zero();
@@ -508,34 +557,30 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
                 xa[v].widen(a[v]);
                 xb[v].widen(b[v]);
             }
-            if (p.part[0].w != nullptr || p.part[1].w != nullptr) {      // the same for all lanes
+            if (any_norm) {                                              // the same for all lanes
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < Vals<E>::N; ++i)
                         ss = vfma(b[v].v[i], b[v].v[i], vfma(a[v].v[i], a[v].v[i], ss));
-                const float rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
+                const float rs = rsqrtf(fmaf(lanes_sum(hsum(ss), p.shift), p.inv_d, p.eps));
                 if (norm) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        Vals<E> fa, fb;
-                        wa[v].widen(fa);
-                        wb[v].widen(fb);
+                    for (int v = 0; v < V; ++v)
 #pragma unroll
                         for (int i = 0; i < Vals<E>::N; ++i) {
-                            a[v].v[i] = vmul(vmul(a[v].v[i], splat<F>(rs)), fa.v[i]);
-                            b[v].v[i] = vmul(vmul(b[v].v[i], splat<F>(rs)), fb.v[i]);
+                            a[v].v[i] = vmul(a[v].v[i], splat<F>(rs));
+                            b[v].v[i] = vmul(b[v].v[i], splat<F>(rs));
                         }
-                    }
                     if (on && lane == 0 && p.rstd != nullptr && part < 2)
-                        p.rstd[cur.t * (p.part[0].heads + p.part[1].heads) + (part ? p.part[0].heads : 0) + h] =
+                        p.rstd[(int64_t)cur.t * (p.part[0].heads + p.part[1].heads) + (part ? p.part[0].heads : 0) + h] =
                             rs;
                 }
             }
-            if (turn)
+            if (mapped)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+                    map[v].apply(a[v], b[v], slot[v].turns);
             if constexpr (FORM == 2) {
                 // k and v go through shared memory, a group a lane
                 float *st = stage_all + (threadIdx.x >> 5) * kRopeStage +
@@ -575,7 +620,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
             }
         }
         stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
-        cur.next(U, p.HC, step, dt, dc, chunks);
+        cur.next(U, p.HC, dt, dc, chunks);
     }
 }
 
@@ -589,11 +634,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     using P = Pack<T, E>;
     using F = typename Vals<E>::F;
     extern __shared__ __align__(16) uint8_t smem[];
-    const RopeRing<T, E, 4 * U> ring = {smem + threadIdx.x * (E * sizeof(T))};
+    uint64_t *fractions = reinterpret_cast<uint64_t *>(smem);
+    const RopeRing<T, E, 4 * U> ring = {smem + kRopeFractions + threadIdx.x * (E * sizeof(T))};
 
     const int part = blockIdx.x >= p.ctas_q ? 1 : 0;
     const RopeGradRows &r = p.part[part];
-    const int64_t ctas = part ? (int)gridDim.x - p.ctas_q : p.ctas_q;
+    const uint32_t ctas = part ? gridDim.x - p.ctas_q : p.ctas_q;
     const int cta = part ? (int)blockIdx.x - p.ctas_q : (int)blockIdx.x;
     const int heads_all = p.part[0].heads + p.part[1].heads, head0 = part ? p.part[0].heads : 0;
     const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
@@ -609,19 +655,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     griddep_launch_dependents();
 
     const int chunks = r.chunks;
-    const int64_t items = p.T * chunks, step = ctas * (kRopeThreads >> p.shift);
-    const int64_t g0 = ((int64_t)cta * kRopeThreads + (threadIdx.x & ~31)) >> p.shift;
-    const int64_t dt = step / chunks;
+    const uint32_t T_ = (uint32_t)p.T, step = ctas * (kRopeThreads >> p.shift);
+    const uint32_t dt = step / chunks;
     const int dc = (int)(step - dt * chunks);
     RopeCursor cur, ahead;
-    cur.start(g0 + ((threadIdx.x & 31) >> p.shift), chunks);
+    cur.start(((int64_t)cta * kRopeThreads + threadIdx.x) >> p.shift, chunks);
     ahead = cur;
     auto fetch = [&](int stage) {
         if constexpr (E > 1) {
-            if (ahead.item < items) {
+            if (ahead.t < T_) {
                 const int h0 = ahead.c * p.HC + ahead.hc, h1 = min(r.heads, ahead.c * p.HC + p.HC);
-                const char *y = static_cast<const char *>(r.dy) + (ahead.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
-                const char *x = static_cast<const char *>(r.x) + (ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
+                const char *y = static_cast<const char *>(r.dy) + ((int64_t)ahead.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
+                const char *x = static_cast<const char *>(r.x) + ((int64_t)ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 + u < h1) {
@@ -640,37 +685,45 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                     x += r.xh * (int64_t)sizeof(T);
                 }
             }
-            ahead.next(U, p.HC, step, dt, dc, chunks);
+            ahead.next(U, p.HC, dt, dc, chunks);
             copies_commit();
         }
     };
 #pragma unroll
     for (int i = 0; i < kRopeDepth - 1; ++i)
         fetch(i);
-    RopeAngles<E, V> ang;
-    ang.init(p.turn, slot, pair);
-    P wa[V], wb[V];
-    Vals<E> da[V], db[V];
+    rope_fractions(p.turn, fractions);
+    Vals<E> wa[V], wb[V], da[V], db[V];
+    RopeMap<E, ADJ> map[V];
+    const Vals<E> one = rope_ones<E>();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        wa[v] = norm && slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero();
-        wb[v] = norm && slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero();
+        (norm && slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero()).widen(wa[v]);
+        (norm && slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero()).widen(wb[v]);
         da[v] = Vals<E>::zero();
         db[v] = Vals<E>::zero();
     }
 
     int stage = 0;
-    for (int64_t first = g0; first < items; first += (cur.hc == 0 ? step : 0)) {
+    // the lanes of a warp stay together in the sums' shuffles: done when all are
+    while (__any_sync(0xFFFFFFFFu, cur.t < T_)) {
         fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
-        const bool live = cur.item < items;
+        const bool live = cur.t < T_;
         const int h0 = cur.c * p.HC + cur.hc, h1 = live ? min(r.heads, cur.c * p.HC + p.HC) : 0;
-        if (cur.hc == 0 && p.turn.rot > 0 && live)
-            ang.at(ld_index(p.turn.pos, cur.t, p.turn.pos64), p.turn.amp, -1.f);
+        if (cur.hc == 0 && p.turn.rot > 0 && live) {
+            const int64_t pos = ld_index(p.turn.pos, cur.t, p.turn.pos64);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float cs[E], sn[E];
+                rope_angles<E>(fractions, pair[v], slot[v].turns, pos, p.turn.amp, -1.f, cs, sn);
+                map[v].make(cs, sn, one, one, slot[v].turns);
+            }
+        }
         float rsv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             rsv[u] = h0 + u < h1 && norm && p.rstd != nullptr
-                         ? __ldg(p.rstd + cur.t * heads_all + head0 + h0 + u) : 0.f;
+                         ? __ldg(p.rstd + (int64_t)cur.t * heads_all + head0 + h0 + u) : 0.f;
         if constexpr (E > 1)
             copies_wait<kRopeDepth - 1>();
 #pragma unroll
@@ -695,8 +748,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                             xb = ring.get(stage, 4 * u + 3);
                     }
                 } else if (on) {
-                    const char *y = static_cast<const char *>(r.dy) + (cur.t * r.yt + h * r.yh) * (int64_t)sizeof(T);
-                    const char *x = static_cast<const char *>(r.x) + (cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
+                    const char *y = static_cast<const char *>(r.dy) + ((int64_t)cur.t * r.yt + h * r.yh) * (int64_t)sizeof(T);
+                    const char *x = static_cast<const char *>(r.x) + ((int64_t)cur.t * r.xt + h * r.xh) * (int64_t)sizeof(T);
                     if (slot[v].a < np) {
                         ya = P::load(y, slot[v].a);
                         if (norm)
@@ -713,48 +766,39 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                 xa.widen(fa[v]);
                 xb.widen(fb[v]);
                 if (p.turn.rot > 0)
-                    rope_turn<E, ADJ>(a[v], b[v], ang.cs[v], ang.sn[v], slot[v].turns);
+                    map[v].apply(a[v], b[v], slot[v].turns);
             }
             if (norm) {
                 F ss = splat<F>(0.f), sc = splat<F>(0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    Vals<E> ga, gb;
-                    wa[v].widen(ga);
-                    wb[v].widen(gb);
+                for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < Vals<E>::N; ++i) {
-                        const F tx = vmul(a[v].v[i], fa[v].v[i]), ty = vmul(b[v].v[i], fb[v].v[i]);
-                        sc = vfma(ty, gb.v[i], vfma(tx, ga.v[i], sc));
-                        ss = vfma(fb[v].v[i], fb[v].v[i], vfma(fa[v].v[i], fa[v].v[i], ss));
+                        sc = vfma(vmul(a[v].v[i], fa[v].v[i]), wa[v].v[i], sc);
+                        sc = vfma(vmul(b[v].v[i], fb[v].v[i]), wb[v].v[i], sc);
+                        if (p.rstd == nullptr)
+                            ss = vfma(fb[v].v[i], fb[v].v[i], vfma(fa[v].v[i], fa[v].v[i], ss));
                     }
-                }
                 float rs = rsv[u];
                 if (p.rstd == nullptr)
-                    rs = rsqrtf(lanes_sum(hsum(ss), p.shift) / (float)p.D + p.eps);
-                const float cm = lanes_sum(hsum(sc), p.shift) / (float)p.D;
-                const float k = -rs * rs * rs * cm;
+                    rs = rsqrtf(fmaf(lanes_sum(hsum(ss), p.shift), p.inv_d, p.eps));
+                const float k = -rs * rs * rs * (lanes_sum(hsum(sc), p.shift) * p.inv_d);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    Vals<E> ga, gb;
-                    wa[v].widen(ga);
-                    wb[v].widen(gb);
+                for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int i = 0; i < Vals<E>::N; ++i) {
-                        const F xa1 = vmul(fa[v].v[i], splat<F>(rs)), xb1 = vmul(fb[v].v[i], splat<F>(rs));
-                        if (on) {
-                            da[v].v[i] = vfma(a[v].v[i], xa1, da[v].v[i]);
-                            db[v].v[i] = vfma(b[v].v[i], xb1, db[v].v[i]);
+                        a[v].v[i] = vmul(a[v].v[i], splat<F>(rs));
+                        b[v].v[i] = vmul(b[v].v[i], splat<F>(rs));
+                        if (on) {                        // other lanes' maps may hold anything
+                            da[v].v[i] = vfma(a[v].v[i], fa[v].v[i], da[v].v[i]);
+                            db[v].v[i] = vfma(b[v].v[i], fb[v].v[i], db[v].v[i]);
                         }
-                        a[v].v[i] = vfma(vmul(a[v].v[i], ga.v[i]), splat<F>(rs),
-                                         vmul(fa[v].v[i], splat<F>(k)));
-                        b[v].v[i] = vfma(vmul(b[v].v[i], gb.v[i]), splat<F>(rs),
-                                         vmul(fb[v].v[i], splat<F>(k)));
+                        a[v].v[i] = vfma(a[v].v[i], wa[v].v[i], vmul(fa[v].v[i], splat<F>(k)));
+                        b[v].v[i] = vfma(b[v].v[i], wb[v].v[i], vmul(fb[v].v[i], splat<F>(k)));
                     }
-                }
             }
             if (on) {
-                char *d = static_cast<char *>(r.dx) + (cur.t * r.dt + h * r.dh) * (int64_t)sizeof(T);
+                char *d = static_cast<char *>(r.dx) + ((int64_t)cur.t * r.dt + h * r.dh) * (int64_t)sizeof(T);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     if (slot[v].a < np)
@@ -765,12 +809,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
             }
         }
         stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
-        cur.next(U, p.HC, step, dt, dc, chunks);
+        cur.next(U, p.HC, dt, dc, chunks);
     }
     if (!norm)
         return;
     // the ring is empty: its place holds the groups' sums
-    float *sums = reinterpret_cast<float *>(smem);
+    float *sums = reinterpret_cast<float *>(smem + kRopeFractions);
     if constexpr (E > 1)
         copies_wait<0>();
     __syncthreads();

@@ -249,6 +249,7 @@ int append_impl(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsnorm_he
     p.T = T;
     p.D = (int)D;
     p.eps = eps;
+    p.inv_d = 1.f / (float)D;
     p.cache = {slots, slot_bits == 64 ? 1 : 0, c.page_size, c.pages * c.page_size,
                c.bits4 ? Hk * (c.page_size / kKv4Tile) * 18 * D : c.k_page, c.v_page, c.k_scale, c.v_scale};
     Strided rows[6];
@@ -315,6 +316,7 @@ int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsno
     p.T = T;
     p.D = (int)D;
     p.eps = eps;
+    p.inv_d = 1.f / (float)D;
     Strided rows[4];
     int n = 0;
     for (const RopeRows &r : {p.part[0], p.part[1]})
@@ -426,6 +428,7 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
     p.T = T;
     p.D = (int)D;
     p.eps = eps;
+    p.inv_d = 1.f / (float)D;
     const RopeSet &set = rope_set(dtype);
     const RopeKernel &kern = set.k[pick_packs(set, D, p.turn, es, rows, n, w0, w1)];
     const void *fn = kern.bwd[p.turn.adjacent];
