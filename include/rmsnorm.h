@@ -654,7 +654,8 @@ void rmsnorm_set_path_override(int path);
  * (rmsnorm_fwd_fp8, rmsnorm_quant_fp8), 10 the 8-bit blocks, 11 the 8-bit
  * product a tile a CTA or cluster, 12 the same by pairs of CTAs, 13 the
  * rotation of heads and its backward, 14 the append to a cache, 15 the reading
- * of a 4-bit cache, 16 the attention over one, 0 none. */
+ * of a 4-bit cache, 16 the attention over one, 17 the same for pieces of
+ * prompts, 0 none. */
 int rmsnorm_last_path(void);
 
 /*
@@ -703,6 +704,14 @@ void rmsnorm_set_gemv_cluster_test(int cluster_size);
  * fp32 sums.
  */
 void rmsnorm_set_gemm_fp8_test(int path);
+
+/*
+ * Test hook, process-wide, not thread-safe against concurrent calls: later
+ * rmsnorm_kv4_attention calls run the kernel for few rows a sequence (1) or,
+ * where q_starts is given, the one for pieces of prompts (2) at any size.
+ * Other values restore the choice by size.
+ */
+void rmsnorm_set_kv4_test(int kernel);
 
 /*
  * Backward that allocates nothing and needs no workspace from the caller.

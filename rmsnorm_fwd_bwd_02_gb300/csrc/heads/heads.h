@@ -156,4 +156,13 @@ struct Kv4Kernels {
 };
 extern const Kv4Kernels kv4_kernels;
 
+// Pieces of prompts (kv4_prompt.cuh): [dtype][D], and their shared memory [D].
+struct Kv4PromptKernels {
+    const void *fn[2][2];
+    int smem[2];
+    int rows;                  // of a CTA
+    int threads;
+};
+extern const Kv4PromptKernels kv4_prompt_kernels;
+
 } // namespace rmsk

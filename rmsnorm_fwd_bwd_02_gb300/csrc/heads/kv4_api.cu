@@ -9,7 +9,10 @@ using namespace rmsk;
 
 namespace {
 
-constexpr int kPathKv4Attend = 16;
+constexpr int kPathKv4Attend = 16, kPathKv4Prompt = 17;
+
+// Test hook: the kernel (see rmsnorm.h).
+std::atomic<int> g_test_kv4{0};
 
 size_t workspace_bytes(int sms, int64_t D)
 {
@@ -100,13 +103,32 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
                        : 0,
                    static_cast<float *>(workspace), g_test_extra_tx.load(std::memory_order_relaxed),
                    g_test_wait_us.load(std::memory_order_relaxed), tmo};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Pieces of prompts: as many rows a sequence as half fill a CTA's, and
+    // enough CTAs for most SMs; the other kernel splits long sequences, which
+    // this one does not.
+    const int64_t wide = q_starts ? T * G / kv4_prompt_kernels.rows * kv_heads : 0;
+    const int ov = g_test_kv4.load(std::memory_order_relaxed);
+    if (q_starts && (ov == 2 || (ov == 0 && rows * 2 >= kv4_prompt_kernels.rows && wide * 2 >= sms))) {
+        const void *fn = kv4_prompt_kernels.fn[ti][di];
+        int bps;
+        if ((st = blocks_per_sm(fn, kv4_prompt_kernels.threads, dev, &bps, kv4_prompt_kernels.smem[di])))
+            return st;
+        void *args[1] = {&p};
+        const int64_t tiles = T * G / kv4_prompt_kernels.rows + B;
+        const cudaError_t e = launch_pdl(fn, dim3((unsigned)(tiles * kv_heads)), kv4_prompt_kernels.threads,
+                                         (size_t)kv4_prompt_kernels.smem[di], s, args);
+        if (e != cudaSuccess)
+            return cuda_fail(e);
+        t_last_path = kPathKv4Prompt;
+        return RMSNORM_OK;
+    }
     const void *fn = kv4_kernels.attend[ti][di][NT - 1];
     const int smem = kv4_smem((int)D);
     int bps;
     if ((st = blocks_per_sm(fn, kKv4Warps * 32, dev, &bps, smem)))
         return st;
     int ctas = sms * std::min(bps, kv4_ctas_per_sm(NT));
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     void *args[1] = {&p};
     cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kKv4Warps * 32, (size_t)smem, s, args);
     if (e != cudaSuccess)
@@ -122,5 +144,7 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
     t_last_path = kPathKv4Attend;
     return RMSNORM_OK;
 }
+
+void rmsnorm_set_kv4_test(int kernel) { g_test_kv4.store(kernel); }
 
 } // extern "C"

@@ -1,0 +1,545 @@
+// kv4_prompt.cuh -- attention over a 4-bit cache for pieces of prompts: many
+// query rows of a sequence and key head. Same result as kv4_attend.cuh (its
+// mathematics: the cache exact in fp16, q scaled by a power of two a row, the
+// softmax in powers of two with a reference that moves rarely), on the
+// fifth-generation tensor cores.
+//
+// Why this shape. With hundreds of rows the products bound the call, and
+// widening the cache's bytes anew for every 16 rows costs more than they do.
+// A CTA holds 256 rows (tokens times heads of one key head) as two tiles of
+// 128 and goes through the sequence 128 tokens at a time; the widened keys and
+// values in shared memory serve both tiles. Warps have one task each:
+//   0-3, 4-7    the softmax of tile 0, of tile 1: a thread a row, which reads
+//               its scores from tensor memory (lane = row), keeps the row's
+//               reference and denominator, and writes p as fp16;
+//   8-11        keys: a thread a token, bytes from global memory a tile ahead;
+//   12-15       values, transposed on the way: a thread eight tokens of 16
+//               features, whose nibbles it interleaves in pairs of tokens;
+//   16          the products: S_t = Q_t K^T and O_t += P_t V, m128 n128 k16
+//               (n64 for O with heads of 64), issued by one thread.
+// While tile 0's rows are in the softmax the tensor cores work on tile 1's
+// scores, and the other way round. Tensor memory: two tiles of scores, two of
+// outputs, 512 columns. All operands are K-major in the 128-byte swizzled
+// layout (gemv_umma.cuh): P and the transposed values have the tokens as K.
+// A row's output is scaled in tensor memory when its reference moves, after
+// the product before has ended.
+//
+// Every wait is bounded; one that runs out sets a flag that ends the others,
+// counts in the timeout counter and leaves the rows unwritten.
+#pragma once
+
+#include "../gemv_umma.cuh"
+#include "kv4_attend.cuh"
+
+namespace rmsk {
+
+constexpr int kPromptRows = 256, kPromptTokens = 128, kPromptThreads = 17 * 32;
+
+// Shared memory: q of both tiles, keys, values, p of both tiles, then the
+// barriers, the tensor-memory address and the keys' tiles that are there.
+template <int D>
+struct PromptLayout {
+    static constexpr uint32_t kQ = 128 * D * 2, kK = 128 * D * 2, kV = D * 128 * 2, kP = 128 * 128 * 2;
+    static constexpr uint32_t q = 0, k = 2 * kQ, v = k + kK, p = v + kV, bar = p + 2 * kP;
+    static constexpr uint32_t kBars = 12;
+    static constexpr uint32_t total = bar + 8 * kBars + 32 + 1023;       // with the alignment
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
+{
+    uint32_t u[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+                   "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+                   "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+                   "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+                   "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                 "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+                 "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]),
+                 "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]),
+                 "f"(v[30]), "f"(v[31])
+                 : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A bounded wait that also ends when another warp's has run out.
+__device__ __forceinline__ bool prompt_wait(uint32_t bar, uint32_t parity, volatile int *bad,
+                                            unsigned long long limit)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const unsigned long long t0 = global_ns();
+    for (int i = 1; !mbar_try_wait(bar, parity); ++i)
+        if ((i & 15) == 0 && (*bad || global_ns() - t0 > limit)) {
+            *bad = 1;
+            return false;
+        }
+    return true;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
+{
+    using L = PromptLayout<D>;
+    constexpr int kTile = kv4_tile_bytes(D), G16 = D / 16;
+    extern __shared__ uint8_t raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    uint8_t *const sm = raw + (base - smem_addr(raw));
+    // barriers: keys full, free; values full, free; scores full [2]; p full [2]; product done [2]; all done
+    const uint32_t kfull = base + L::bar, kfree = kfull + 8, vfull = kfull + 16, vfree = kfull + 24,
+                   sfull = kfull + 32, pfull = kfull + 48, pvdone = kfull + 64, done = kfull + 80;
+    volatile uint32_t *slots = reinterpret_cast<volatile uint32_t *>(sm + L::bar + 8 * L::kBars);
+    volatile int *bad = reinterpret_cast<volatile int *>(slots + 1);
+    volatile uint8_t *present = reinterpret_cast<volatile uint8_t *>(sm + L::bar + 8 * L::kBars + 8);   // [2][4]
+
+    griddep_wait();
+    griddep_launch_dependents();
+    // the segment of this CTA: sequences' segments side by side, a key head's
+    // tiles from the last (which sees most) to the first
+    int64_t segs = 0, seg = -1;
+    int seq = 0;
+    for (int b0 = 0; b0 < p.B && seg < 0; b0 += 32) {
+        int64_t n = 0;
+        if (b0 + lane < p.B) {
+            const Kv4Seq t = kv4_seq<kPromptRows / 8>(p, b0 + lane);
+            n = (int64_t)t.tiles * p.Hk;
+        }
+        int64_t sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o)
+                sum += v;
+        }
+        const unsigned at = __ballot_sync(0xFFFFFFFFu, segs + sum > blockIdx.x);
+        if (at) {
+            const int l = __ffs(at) - 1;
+            seq = b0 + l;
+            seg = blockIdx.x - (segs + __shfl_sync(0xFFFFFFFFu, sum - n, l));
+        }
+        segs += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (seg < 0)
+        return;                                                 // for the whole CTA
+    const Kv4Seq s = kv4_seq<kPromptRows / 8>(p, seq);
+    const int h = (int)(seg % p.Hk), tile = s.tiles - 1 - (int)(seg / p.Hk);
+    if (tile < 0)
+        return;                                                 // lengths that change under the call
+    const int rows = s.n * p.G;                                 // of this sequence and key head
+    const int row0 = tile * kPromptRows, row_last = min(rows, row0 + kPromptRows) - 1;
+    const int most = max(0, s.len - s.n + row_last / p.G + 1);  // tokens that the last row sees
+    const int count = (most + kPromptTokens - 1) / kPromptTokens;
+    const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
+
+    if (warp == 16) {
+        if (lane == 0) {
+            // the test hook: one arrival more than there are, so that the waits run out
+            mbar_init(kfull, p.extra_tx ? 129 : 128); mbar_init(kfree, 1);
+            mbar_init(vfull, 128); mbar_init(vfree, 1);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(sfull + 8 * t, 1);
+                mbar_init(pfull + 8 * t, 128);
+                mbar_init(pvdone + 8 * t, 1);
+            }
+            mbar_init(done, 1);
+            mbar_init_fence();
+            *bad = 0;
+        }
+        __syncwarp();
+        tmem_alloc(base + L::bar + 8 * L::kBars, 512);
+        tmem_relinquish();
+    }
+
+    // q, a thread a row: to fp16 with the largest element at 2^14
+    float mul = 0.f;
+    int lim = 0, row_i = 0, row_h = 0;
+    bool real = false;
+    if (warp < 8) {
+        const int t = tid >> 7, r = tid & 127, row = row0 + t * 128 + r;
+        real = row < rows;
+        row_i = real ? row / p.G : 0;
+        row_h = h * p.G + (real ? row - row_i * p.G : 0);
+        lim = real ? max(0, s.len - s.n + row_i + 1) : 0;
+        const char *q = static_cast<const char *>(p.q) +
+                        ((int64_t)(s.q0 + row_i) * p.qt + row_h * p.qh) * (int64_t)sizeof(T);
+        auto word = [&](int j) {
+            return (uint32_t)ld_row_b16(q + 4 * j) | (uint32_t)ld_row_b16(q + 4 * j + 2) << 16;
+        };
+        auto chunk = [&](int c) {
+            if (!real)
+                return make_uint4(0, 0, 0, 0);
+            if (p.vec)
+                return __ldg(reinterpret_cast<const uint4 *>(q) + c);
+            return make_uint4(word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
+        };
+        float m = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = chunk(c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Half16<T>::wide2(w[j]);
+                m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        }
+        const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
+        const float k = p.scale * 1.4426950408889634f * (p.kscale ? __ldg(p.kscale + h) : 1.f);
+        // the factor's sign goes into q: the largest score is then the largest power
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), k);
+        mul = fabsf(k) * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = chunk(c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Half16<T>::wide2(w[j]);
+                o[j] = Half16<f16>::narrow2(f.x * up, f.y * up);
+            }
+            sts128(base + L::q + t * L::kQ + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1],
+                   o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = slots[0];
+
+    if (warp < 8) {
+        // ------------------------------------------------------ the softmax
+        const int t = tid >> 7, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // (32 (warp % 4)) << 16
+        const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        const uint32_t ps = base + L::p + t * L::kP + r * 128;
+        float m = kKv4Least, l = 0.f;
+        int least = real ? lim : INT32_MAX;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+        bool ok = true;
+        for (int j = 0; j < count; ++j) {
+            ok = __all_sync(0xFFFFFFFFu, prompt_wait(sfull + 8 * t, j & 1, bad, limit));
+            if (!ok)
+                break;
+            tc_fence_after_sync();
+            const uint32_t there = *reinterpret_cast<volatile uint32_t *>(sm + L::bar + 8 * L::kBars + 8 + 4 * (j & 1));
+            const int tok = j * kPromptTokens;
+            const bool whole = tok + kPromptTokens <= least && there == 0x03030303u;
+            // column c's token is seen: past neither the row's limit nor in a tile that is not there
+            auto seen = [&](int c) { return tok + c < lim && (there >> (8 * (c >> 5) + ((c >> 4) & 1)) & 1u); };
+            float x[32], mx = kKv4Least;
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                tmem_ld32(ts + 32 * ch, x);
+                if (whole) {
+                    float a = x[0], b = x[1];
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) {
+                        a = fmaxf(a, x[i]);
+                        b = fmaxf(b, x[i + 1]);
+                    }
+                    mx = fmaxf(mx, fmaxf(a, b));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (seen(32 * ch + i))
+                            mx = fmaxf(mx, x[i]);
+                }
+            }
+            const float top = mx == kKv4Least ? kKv4Least : mx * mul;
+            float f = 1.f;
+            if (top > m + 7.f) {
+                f = exp2_of(m - top);
+                m = top;
+                l *= f;
+            }
+            if (j > 0) {
+                // p's place, and O, are the product's before until it has ended
+                ok = __all_sync(0xFFFFFFFFu, prompt_wait(pvdone + 8 * t, (j - 1) & 1, bad, limit));
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        tmem_ld32(to + 32 * ch, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            x[i] *= f;
+                        tmem_st32(to + 32 * ch, x);
+                    }
+                }
+            }
+            const float b = m == kKv4Least ? 0.f : m - 8.f;
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+                tmem_ld32(ts + 32 * ch, x);
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    x[i] = exp2_of(fmaf(x[i], mul, -b));
+                    x[i + 1] = exp2_of(fmaf(x[i + 1], mul, -b));
+                    if (!whole) {
+                        x[i] = seen(32 * ch + i) ? x[i] : 0.f;
+                        x[i + 1] = seen(32 * ch + i + 1) ? x[i + 1] : 0.f;
+                    }
+                    s0 += x[i];
+                    s1 += x[i + 1];
+                }
+                l += s0 + s1;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4),
+                           Half16<f16>::narrow2(x[8 * c], x[8 * c + 1]), Half16<f16>::narrow2(x[8 * c + 2], x[8 * c + 3]),
+                           Half16<f16>::narrow2(x[8 * c + 4], x[8 * c + 5]),
+                           Half16<f16>::narrow2(x[8 * c + 6], x[8 * c + 7]));
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            bar_arrive(pfull + 8 * t);
+        }
+        if (ok && count > 0)
+            ok = __all_sync(0xFFFFFFFFu, prompt_wait(pvdone + 8 * t, (count - 1) & 1, bad, limit));
+        if (ok) {
+            tc_fence_after_sync();
+            const float gv = p.vscale ? __ldg(p.vscale + h) : 1.f;
+            const float f = l > 0.f || l != l ? gv / l : 0.f;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float x[32];
+                if (count > 0)
+                    tmem_ld32(to + 32 * ch, x);
+                if (real)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        kv4_store<T>(p, s.q0 + row_i, row_h, 32 * ch + i,
+                                     f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                              : make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f));
+            }
+            if (real && p.lse != nullptr)
+                p.lse[(int64_t)(s.q0 + row_i) * p.Hk * p.G + row_h] = kv4_lse(m, l);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------- keys, a thread a token
+        const int r = tid & 127;
+        const int *row = p.table + seq * p.table_ld;
+        const uint8_t *head = p.cache + (int64_t)h * p.tpp * kTile;
+        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
+        const int tiles = (most + kKv4Tile - 1) / kKv4Tile;
+        uint4 code[D / 32];
+        uint2 sc = make_uint2(0, 0);
+        bool have = false;
+        auto page_of = [&](int j) {
+            const int t16 = j * 8 + (r >> 4);
+            if (j >= count || t16 >= tiles)
+                return -1;
+            const int v = __ldg(row + t16 / p.tpp);
+            return v < p.pages ? v : -1;
+        };
+        auto fetch = [&](int j, int pg) {
+            have = pg >= 0;
+            if (!have)
+                return;
+            const uint8_t *at = head + pg * page_bytes + (int64_t)((j * 8 + (r >> 4)) % p.tpp) * kTile;
+            const uint4 *c = reinterpret_cast<const uint4 *>(at + (r & 15) * (D / 2));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                code[i] = __ldg(c + i);
+            if constexpr (D == 128)
+                sc = __ldg(reinterpret_cast<const uint2 *>(at + kv4_kscale(D) + (r & 15) * 8));
+            else
+                sc.x = __ldg(reinterpret_cast<const uint32_t *>(at + kv4_kscale(D) + (r & 15) * 4));
+        };
+        fetch(0, page_of(0));
+        int next = page_of(1);
+        for (int j = 0; j < count; ++j) {
+            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(kfree, (j - 1) & 1, bad, limit)))
+                break;
+            const unsigned in = __ballot_sync(0xFFFFFFFFu, have);
+            if (lane == 0)
+                present[4 * (j & 1) + (warp - 8)] = (in & 1u) | (in >> 15 & 2u);
+#pragma unroll
+            for (int g = 0; g < G16; ++g) {
+                const uint4 u = code[g >> 1];
+                const uint32_t w[2] = {have ? (g & 1 ? u.z : u.x) : 0u, have ? (g & 1 ? u.w : u.y) : 0u};
+                const uint32_t sb = ((g & 4) ? sc.y : sc.x) >> (8 * (g & 3)) & 0xFFu;
+                const uint32_t f = have ? scales2((uint16_t)(sb * 0x0101u)) : 0u;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t e[4];
+                    widen4(w[k], e);
+                    const int c = 2 * g + k;
+                    sts128(base + L::k + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), hmul2(e[0], f),
+                           hmul2(e[1], f), hmul2(e[2], f), hmul2(e[3], f));
+                }
+            }
+            fence_proxy_async_smem();
+            bar_arrive(kfull);
+            fetch(j + 1, next);
+            next = page_of(j + 2);
+        }
+    } else if (warp < 16) {
+        // -------------------- values: eight tokens of a group of 16 features a thread
+        const int v = tid & 127, g = v >> 4, oct = v & 15;
+        const int *row = p.table + seq * p.table_ld;
+        const uint8_t *head = p.cache + (int64_t)h * p.tpp * kTile;
+        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
+        const int tiles = (most + kKv4Tile - 1) / kKv4Tile;
+        uint4 code[4];
+        uint2 sc = make_uint2(0, 0);
+        bool have = false;
+        auto page_of = [&](int j) {
+            const int t16 = j * 8 + (oct >> 1);
+            if (j >= count || t16 >= tiles || g >= G16)
+                return -1;
+            const int x = __ldg(row + t16 / p.tpp);
+            return x < p.pages ? x : -1;
+        };
+        auto fetch = [&](int j, int pg) {
+            have = pg >= 0;
+            if (!have)
+                return;
+            const uint8_t *at = head + pg * page_bytes + (int64_t)((j * 8 + (oct >> 1)) % p.tpp) * kTile;
+            const uint4 *c = reinterpret_cast<const uint4 *>(at + kv4_v(D) + g * 128 + (oct & 1) * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                code[i] = __ldg(c + i);
+            sc = __ldg(reinterpret_cast<const uint2 *>(at + kv4_vscale(D) + g * 16 + (oct & 1) * 8));
+        };
+        fetch(0, page_of(0));
+        int next = page_of(1);
+        for (int j = 0; j < count; ++j) {
+            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(vfree, (j - 1) & 1, bad, limit)))
+                break;
+            if (g < G16) {
+                // tokens past the sequence's end, and those of a page that is
+                // not there, count as zeros whatever their bytes
+                const int left = have ? s.len - (j * kPromptTokens + oct * 8) : 0;
+                uint32_t f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = scales2((uint16_t)((i & 2 ? sc.y : sc.x) >> (16 * (i & 1))));
+                    f[i] = (2 * i < left ? two & 0xFFFFu : 0u) | (2 * i + 1 < left ? two & 0xFFFF0000u : 0u);
+                }
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t e[4][4], o[4][4];                  // [pair of tokens][pair of features]
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a = have ? (w ? code[i].y : code[i].x) : 0u,
+                                       b = have ? (w ? code[i].w : code[i].z) : 0u;
+                        widen4((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), e[i]);
+                        widen4(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), o[i]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int d = g * 16 + 8 * w + 2 * k;
+                        const uint32_t at = base + L::v + (oct >> 3) * (D * 128) + d * 128;
+                        sts128(at + (((oct & 7) ^ (d & 7)) << 4), hmul2(e[0][k], f[0]), hmul2(e[1][k], f[1]),
+                               hmul2(e[2][k], f[2]), hmul2(e[3][k], f[3]));
+                        sts128(at + 128 + (((oct & 7) ^ ((d + 1) & 7)) << 4), hmul2(o[0][k], f[0]),
+                               hmul2(o[1][k], f[1]), hmul2(o[2][k], f[2]), hmul2(o[3][k], f[3]));
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            bar_arrive(vfull);
+            fetch(j + 1, next);
+            next = page_of(j + 2);
+        }
+    } else if (lane == 0 && count > 0) {
+        // ------------------------------------------------------ the products
+        const uint32_t is = umma_idesc_f16(0, 128, 128), io = umma_idesc_f16(0, 128, D);
+        const uint64_t dq = umma_desc_sw128(base + L::q), dk = umma_desc_sw128(base + L::k),
+                       dv = umma_desc_sw128(base + L::v), dp = umma_desc_sw128(base + L::p);
+        auto scores = [&](int t) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t step = (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3));
+                umma_f16(tmem + t * 128, dq + t * (L::kQ >> 4) + step, dk + step, is, k > 0);
+            }
+            umma_commit(sfull + 8 * t);
+        };
+        bool ok = prompt_wait(kfull, 0, bad, limit);
+        if (ok) {
+            tc_fence_after_sync();
+            scores(0);
+            scores(1);
+            umma_commit(kfree);
+        }
+        for (int j = 0; ok && j < count; ++j) {
+            ok = prompt_wait(vfull, j & 1, bad, limit);
+            for (int t = 0; ok && t < 2; ++t) {
+                ok = prompt_wait(pfull + 8 * t, j & 1, bad, limit);
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < kPromptTokens / 16; ++k)
+                    umma_f16(tmem + 256 + t * 128, dp + t * (L::kP >> 4) + (k >> 2) * (16384 >> 4) + 2 * (k & 3),
+                             dv + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, j > 0 || k > 0);
+                umma_commit(pvdone + 8 * t);
+                if (t == 1)
+                    umma_commit(vfree);
+                if (j + 1 < count) {
+                    if (t == 0)
+                        ok = prompt_wait(kfull, (j + 1) & 1, bad, limit);
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    scores(t);
+                    if (t == 1)
+                        umma_commit(kfree);
+                }
+            }
+        }
+        // nothing may be in flight when the tensor memory is given back
+        umma_commit(done);
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(done, 0))
+            if (global_ns() - t0 > limit) {
+                *bad = 1;
+                break;
+            }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after_sync();
+        if (*bad && lane == 0)
+            atomicAdd(p.timeouts, 1u);
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+} // namespace rmsk

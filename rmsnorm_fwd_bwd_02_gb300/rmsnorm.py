@@ -31,7 +31,8 @@ PATH_GEMV_UMMA = 7       # the product on tcgen05 (7); 6 and 7 also force it
 PATH_GEMV_TC = 8         # persistent tcgen05 kernel, y held per CTA (8; forces it)
 PATH_FP8_ROWS, PATH_FP8_BLOCKS = 9, 10            # reported only
 PATH_FP8_GEMM, PATH_FP8_PAIR = 11, 12             # the 8-bit product's kernels
-PATH_ROPE, PATH_ROPE_APPEND, PATH_KV4_READ, PATH_KV4_ATTENTION = 13, 14, 15, 16   # reported only
+PATH_ROPE, PATH_ROPE_APPEND, PATH_KV4_READ = 13, 14, 15                  # reported only
+PATH_KV4_ATTENTION, PATH_KV4_PROMPT = 16, 17
 
 # Entry points of include/rmsnorm.h with their ctypes signatures.
 _i64, _vp, _sz, _int, _f = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
@@ -87,6 +88,7 @@ SIGNATURES.update({
                                      _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64,
                                      _f, _vp, _sz, _int, _vp]),
     "rmsnorm_kv4_attention_workspace_bytes": (_sz, [_i64]),
+    "rmsnorm_set_kv4_test": (None, [_int]),
     "rmsnorm_kv4_read": (_int, [_vp, _i64, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp,
                                 _vp]),
 })
@@ -669,6 +671,12 @@ def rmsnorm_kv4_read(cache, slots, stream=None):
         with _on_stream(cache, stream):
             return _heads().kv4_read(cache, slots)
     return _heads().kv4_read(cache, slots)
+
+
+def set_kv4_test(kernel: int):
+    """Test hook: attention over a 4-bit cache by the kernel for few rows a
+    sequence (1) or for pieces of prompts (2) at any size (0: by size)."""
+    lib().rmsnorm_set_kv4_test(int(kernel))
 
 
 def rmsnorm_kv4_attention(q, cache, block_table, seq_lens, q_starts=None, k_scale=None, v_scale=None,

@@ -23,6 +23,7 @@ from tests.test_rope_gpu import BF16, DEV, F16, F32, F64, check_fwd, freqs, norm
 
 pytestmark = pytest.mark.gpu
 
+PATHS = {1: rn.PATH_KV4_ATTENTION, 2: rn.PATH_KV4_PROMPT}
 HALF = {BF16: 2.0 ** -8, F16: 2.0 ** -11}
 TINY = {BF16: 2.0 ** -134, F16: 2.0 ** -25}
 
@@ -115,12 +116,19 @@ def table_of(B, blocks, pages, seed):
     return torch.randperm(pages, generator=g)[:B * blocks].to(torch.int32).view(B, blocks)
 
 
-def run(T, H, D, dtype, cache, table, lens, starts=None, seed=5, **kw):
+@pytest.fixture(params=[1, 2], ids=["few", "prompt"])
+def kernel(request):
+    rn.set_kv4_test(request.param)
+    yield request.param
+    rn.set_kv4_test(0)
+
+
+def run(T, H, D, dtype, cache, table, lens, starts=None, seed=5, path=None, **kw):
     q = normal((T, H, D), dtype, seed)
     s = None if starts is None else torch.tensor(starts, dtype=torch.int32, device=DEV)
     out, lse = rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
                                         q_starts=s, want_lse=True, **kw)
-    assert rn.last_path() == rn.PATH_KV4_ATTENTION
+    assert rn.last_path() == (path or rn.PATH_KV4_ATTENTION)
     check(out, lse, q, cache, table, lens, starts, scale=kw.get("scale"), ks=kw.get("k_scale"),
           vs=kw.get("v_scale"))
     return q, out, lse
@@ -140,7 +148,7 @@ def test_one_token(dtype, D, Hk, G):
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D,Hk,G", [(64, 2, 7), (128, 2, 4), (128, 1, 8)])
 @pytest.mark.parametrize("counts", [(1, 2, 3, 0, 5, 4), (17, 1, 40, 0, 33, 9), (64, 130, 0, 1, 65, 128)])
-def test_several_tokens(dtype, D, Hk, G, counts):
+def test_several_tokens(dtype, D, Hk, G, counts, kernel):
     """Rows see the tokens up to their own; more query tokens than cached ones
     leave the first rows nothing."""
     page, lens = 32, [700, 2, 3, 50, 1, 333]
@@ -149,7 +157,8 @@ def test_several_tokens(dtype, D, Hk, G, counts):
     for c in counts:
         starts.append(starts[-1] + c)
     cache = make_cache(B * blocks + 3, Hk, page, D, G)
-    run(starts[-1], Hk * G, D, dtype, cache, table_of(B, blocks, B * blocks + 3, 4), lens, starts)
+    run(starts[-1], Hk * G, D, dtype, cache, table_of(B, blocks, B * blocks + 3, 4), lens, starts,
+        path=PATHS[kernel])
 
 
 def test_long_and_one_unit():
@@ -197,7 +206,7 @@ def test_peaked_and_shifted_scores():
         check(out, lse, q, cache, table, [1000], None)
 
 
-def test_garbage_where_nothing_is_seen():
+def test_garbage_where_nothing_is_seen(kernel):
     """Bytes that stand for NaN behind a sequence's end, in a page's rest and
     in pages that the table does not reach change nothing; neither do pages
     outside the cache, whose tokens are masked."""
@@ -221,12 +230,12 @@ def test_garbage_where_nothing_is_seen():
         bad[6, :, 1] = 0x7F                          # tokens 80 .. 95 of sequence 2: seen
         cache[6, :, 1] = 0
         bad[6, :, 1] = 0
-        _, a, la = run(9, 4, D, BF16, cache, table, lens, starts)
-        _, b, lb = run(9, 4, D, BF16, bad, table, lens, starts)
+        _, a, la = run(9, 4, D, BF16, cache, table, lens, starts, path=PATHS[kernel])
+        _, b, lb = run(9, 4, D, BF16, bad, table, lens, starts, path=PATHS[kernel])
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
-def test_rows_of_no_sequence_and_unsound_starts():
+def test_rows_of_no_sequence_and_unsound_starts(kernel):
     D, page = 64, 16
     cache = make_cache(8, 1, page, D, 3)
     table = torch.arange(8, dtype=torch.int32).view(2, 4)
@@ -361,23 +370,63 @@ def test_two_streams_at_once():
     assert all(torch.equal(o, w) for i, w in enumerate(want) for o in got[i])
 
 
-def test_waits_that_run_out():
+def test_waits_that_run_out(kernel):
     """The test hook makes the stages' waits run out: the call ends, counts
     them, and the next one is right again."""
     D, page = 128, 16
     cache = make_cache(60, 1, page, D, 3)
     table = torch.arange(60, dtype=torch.int32)[None]
     q, lens = normal((1, 4, D), BF16, 4), torch.tensor([900], dtype=torch.int32, device=DEV)
+    s = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
     rn.wait_timeouts(reset=True)
     rn.set_stream_test_fault(16, 2000)
     try:
-        rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), lens)
+        rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), lens, q_starts=s)
         torch.cuda.synchronize()
     finally:
         rn.set_stream_test_fault(0, 0)
     assert rn.wait_timeouts(reset=True) > 0
-    out, lse = rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), lens, want_lse=True)
+    out, lse = rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), lens, q_starts=s, want_lse=True)
     check(out, lse, q, cache, table, [900], None)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D,Hk,G,page", [(128, 8, 4, 64), (64, 2, 7, 16), (128, 2, 1, 48)])
+def test_pieces_of_prompts(dtype, D, Hk, G, page):
+    """Sizes that the rule gives to the kernel for many rows, ragged ones, a
+    prompt from its first token, scores that move the reference."""
+    lens, counts = [1500, 640, 333, 777], [600, 640, 64, 300]
+    B, blocks = 4, -(-1536 // page)
+    starts = [0]
+    for c in counts:
+        starts.append(starts[-1] + c)
+    cache = make_cache(B * blocks, Hk, page, D, G)
+    table = table_of(B, blocks, B * blocks, 3)
+    wide = starts[-1] * G // 256 * Hk * 2 >= torch.cuda.get_device_properties(0).multi_processor_count
+    rn.set_kv4_test(0 if wide else 2)
+    try:
+        run(starts[-1], Hk * G, D, dtype, cache, table, lens, starts, path=rn.PATH_KV4_PROMPT)
+        ks, vs = torch.rand(Hk, device=DEV) + 0.1, torch.rand(Hk, device=DEV) + 0.1
+        run(starts[-1], Hk * G, D, dtype, cache, table, lens, starts, path=rn.PATH_KV4_PROMPT, scale=-0.4,
+            k_scale=ks, v_scale=vs)
+        # the largest scores late: one key grows along the sequence
+        k = normal((B * blocks * page, Hk, D), F32, 3, 0.2) + \
+            torch.linspace(-3, 3, B * blocks * page, device=DEV)[:, None, None]
+        rn.rmsnorm_rope_append_kv4(k, k, None, None, torch.arange(B * blocks * page, device=DEV), cache)
+        q = (normal((starts[-1], Hk * G, D), dtype, 3, 0.2).float() + 0.7).to(dtype)
+        s = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        plain = torch.arange(B * blocks, dtype=torch.int32).view(B, blocks)
+        out, lse = rn.rmsnorm_kv4_attention(q, cache, plain.to(DEV), dl, q_starts=s, want_lse=True)
+        check(out, lse, q, cache, plain, lens, starts)
+        # the same bits again, and from a window that is not aligned
+        again, _ = rn.rmsnorm_kv4_attention(q, cache, plain.to(DEV), dl, q_starts=s)
+        assert torch.equal(out, again)
+        odd = torch.nn.functional.pad(q, (1, 1))[..., 1:1 + D]
+        again, _ = rn.rmsnorm_kv4_attention(odd, cache, plain.to(DEV), dl, q_starts=s)
+        assert torch.equal(out, again)
+    finally:
+        rn.set_kv4_test(0)
 
 
 def test_decode_step_in_a_run():
