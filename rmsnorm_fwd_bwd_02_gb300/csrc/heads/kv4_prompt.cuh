@@ -12,10 +12,11 @@
 //   0-3, 4-7    the softmax of tile 0, of tile 1: a thread a row, which reads
 //               its scores from tensor memory (lane = row), keeps the row's
 //               reference and denominator, and writes p as fp16;
-//   8-11        keys: a thread a token, bytes from global memory a tile ahead;
-//   12-15       values, transposed on the way: a thread eight tokens of 16
-//               features, whose nibbles it interleaves in pairs of tokens;
-//   16          the products: S_t = Q_t K^T and O_t += P_t V, m128 n128 k16
+//   8-11        keys, a thread a token, and values, transposed on the way, a
+//               thread eight tokens of 16 features, whose nibbles it
+//               interleaves in pairs of tokens; bytes from global memory a
+//               tile ahead;
+//   12          the products: S_t = Q_t K^T and O_t += P_t V, m128 n128 k16
 //               (n64 for O with heads of 64), issued by one thread.
 // While tile 0's rows are in the softmax the tensor cores work on tile 1's
 // scores, and the other way round. Tensor memory: two tiles of scores, two of
@@ -33,7 +34,7 @@
 
 namespace rmsk {
 
-constexpr int kPromptRows = 256, kPromptTokens = 128, kPromptThreads = 17 * 32;
+constexpr int kPromptRows = 256, kPromptTokens = 128, kPromptThreads = 13 * 32;
 
 // Shared memory: q of both tiles, keys, values, p of both tiles, then the
 // barriers, the tensor-memory address and the keys' tiles that are there.
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
     const int count = (most + kPromptTokens - 1) / kPromptTokens;
     const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
 
-    if (warp == 16) {
+    if (warp == 12) {
         if (lane == 0) {
             // the test hook: one arrival more than there are, so that the waits run out
             mbar_init(kfull, p.extra_tx ? 129 : 128); mbar_init(kfree, 1);
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // (32 (warp % 4)) << 16
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         const uint32_t ps = base + L::p + t * L::kP + r * 128;
-        float m = kKv4Least, l = 0.f;
+        // (a row that sees nothing wants no reference)
+        float m = lim > 0 ? kKv4Least : 0.f, l = 0.f;
         int least = real ? lim : INT32_MAX;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -257,39 +259,64 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             const bool whole = tok + kPromptTokens <= least && there == 0x03030303u;
             // column c's token is seen: past neither the row's limit nor in a tile that is not there
             auto seen = [&](int c) { return tok + c < lim && (there >> (8 * (c >> 5) + ((c >> 4) & 1)) & 1u); };
-            float x[32], mx = kKv4Least;
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-                tmem_ld32(ts + 32 * ch, x);
-                if (whole) {
-                    float a = x[0], b = x[1];
-#pragma unroll
-                    for (int i = 2; i < 32; i += 2) {
-                        a = fmaxf(a, x[i]);
-                        b = fmaxf(b, x[i + 1]);
-                    }
-                    mx = fmaxf(mx, fmaxf(a, b));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (seen(32 * ch + i))
-                            mx = fmaxf(mx, x[i]);
-                }
-            }
-            const float top = mx == kKv4Least ? kKv4Least : mx * mul;
-            float f = 1.f;
-            if (top > m + 7.f) {
-                f = exp2_of(m - top);
-                m = top;
-                l *= f;
-            }
             if (j > 0) {
                 // p's place, and O, are the product's before until it has ended
                 ok = __all_sync(0xFFFFFFFFu, prompt_wait(pvdone + 8 * t, (j - 1) & 1, bad, limit));
                 if (!ok)
                     break;
                 tc_fence_after_sync();
-                if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
+            }
+            // p from the reference as it is; most tiles do not pass it
+            const float l0 = l;
+            bool far = m == kKv4Least;
+            if (!__any_sync(0xFFFFFFFFu, far)) {
+                const float2 mul2 = make_float2(mul, mul), b2 = make_float2(8.f - m, 8.f - m);
+                float2 sum = make_float2(0.f, 0.f);
+                uint32_t top = 0;                               // of the packed p: positive halves compare as integers
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    float x[32];
+                    tmem_ld32(ts + 32 * ch, x);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), mul2, b2);
+                        float2 e = make_float2(exp2_of(y.x), exp2_of(y.y));
+                        if (!whole) {
+                            e.x = seen(32 * ch + 2 * i) ? e.x : 0.f;
+                            e.y = seen(32 * ch + 2 * i + 1) ? e.y : 0.f;
+                        }
+                        sum = __fadd2_rn(sum, e);
+                        w[i] = Half16<f16>::narrow2(e.x, e.y);
+                        top = __vmaxu2(top, w[i]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4), w[4 * c], w[4 * c + 1],
+                               w[4 * c + 2], w[4 * c + 3]);
+                }
+                l += sum.x + sum.y;
+                far = max(top & 0xFFFFu, top >> 16) > 0x7800u;  // above 2^15, or not a number
+            }
+            if (__any_sync(0xFFFFFFFFu, far)) {
+                // a new reference for the rows that want one, and p again
+                float x[32], mx = kKv4Least, f = 1.f;
+                l = l0;
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    tmem_ld32(ts + 32 * ch, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (seen(32 * ch + i))
+                            mx = fmaxf(mx, x[i]);
+                }
+                const float top = mx == kKv4Least ? kKv4Least : mx * mul;
+                if (top > m + 7.f) {
+                    f = exp2_of(m - top);
+                    m = top;
+                    l *= f;
+                }
+                if (j > 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
                         tmem_ld32(to + 32 * ch, x);
@@ -299,30 +326,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                         tmem_st32(to + 32 * ch, x);
                     }
                 }
-            }
-            const float b = m == kKv4Least ? 0.f : m - 8.f;
+                const float b = m == kKv4Least ? 0.f : m - 8.f;
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-                tmem_ld32(ts + 32 * ch, x);
-                float s0 = 0.f, s1 = 0.f;
+                for (int ch = 0; ch < 4; ++ch) {
+                    tmem_ld32(ts + 32 * ch, x);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    x[i] = exp2_of(fmaf(x[i], mul, -b));
-                    x[i + 1] = exp2_of(fmaf(x[i + 1], mul, -b));
-                    if (!whole) {
-                        x[i] = seen(32 * ch + i) ? x[i] : 0.f;
-                        x[i + 1] = seen(32 * ch + i + 1) ? x[i + 1] : 0.f;
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = seen(32 * ch + i) ? exp2_of(fmaf(x[i], mul, -b)) : 0.f;
+                        l += x[i];
                     }
-                    s0 += x[i];
-                    s1 += x[i + 1];
-                }
-                l += s0 + s1;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4),
-                           Half16<f16>::narrow2(x[8 * c], x[8 * c + 1]), Half16<f16>::narrow2(x[8 * c + 2], x[8 * c + 3]),
-                           Half16<f16>::narrow2(x[8 * c + 4], x[8 * c + 5]),
-                           Half16<f16>::narrow2(x[8 * c + 6], x[8 * c + 7]));
+                    for (int c = 0; c < 4; ++c)
+                        sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4),
+                               Half16<f16>::narrow2(x[8 * c], x[8 * c + 1]),
+                               Half16<f16>::narrow2(x[8 * c + 2], x[8 * c + 3]),
+                               Half16<f16>::narrow2(x[8 * c + 4], x[8 * c + 5]),
+                               Half16<f16>::narrow2(x[8 * c + 6], x[8 * c + 7]));
+                }
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
@@ -350,105 +370,82 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                 p.lse[(int64_t)(s.q0 + row_i) * p.Hk * p.G + row_h] = kv4_lse(m, l);
         }
     } else if (warp < 12) {
-        // ---------------------------------------------- keys, a thread a token
-        const int r = tid & 127;
+        // ------------------------------------------------ keys and values
+        const int r = tid & 127, g = r >> 4, oct = r & 15;      // a token's keys; a group of eight tokens' values
         const int *row = p.table + seq * p.table_ld;
         const uint8_t *head = p.cache + (int64_t)h * p.tpp * kTile;
         const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
         const int tiles = (most + kKv4Tile - 1) / kKv4Tile;
-        uint4 code[D / 32];
-        uint2 sc = make_uint2(0, 0);
-        bool have = false;
-        auto page_of = [&](int j) {
-            const int t16 = j * 8 + (r >> 4);
+        uint4 kcode[D / 32], vcode[4];
+        uint2 ksc = make_uint2(0, 0), vsc = make_uint2(0, 0);
+        bool khave = false, vhave = false;
+        // the page of tile t16 of tile j's eight
+        auto page_of = [&](int j, int t16) {
+            t16 += j * 8;
             if (j >= count || t16 >= tiles)
                 return -1;
             const int v = __ldg(row + t16 / p.tpp);
             return v < p.pages ? v : -1;
         };
-        auto fetch = [&](int j, int pg) {
-            have = pg >= 0;
-            if (!have)
+        auto at = [&](int j, int t16, int pg) {
+            return head + pg * page_bytes + (int64_t)((j * 8 + t16) % p.tpp) * kTile;
+        };
+        auto fetch_k = [&](int j, int pg) {
+            khave = pg >= 0;
+            if (!khave)
                 return;
-            const uint8_t *at = head + pg * page_bytes + (int64_t)((j * 8 + (r >> 4)) % p.tpp) * kTile;
-            const uint4 *c = reinterpret_cast<const uint4 *>(at + (r & 15) * (D / 2));
+            const uint8_t *a = at(j, r >> 4, pg);
+            const uint4 *c = reinterpret_cast<const uint4 *>(a + (r & 15) * (D / 2));
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-                code[i] = __ldg(c + i);
+                kcode[i] = __ldg(c + i);
             if constexpr (D == 128)
-                sc = __ldg(reinterpret_cast<const uint2 *>(at + kv4_kscale(D) + (r & 15) * 8));
+                ksc = __ldg(reinterpret_cast<const uint2 *>(a + kv4_kscale(D) + (r & 15) * 8));
             else
-                sc.x = __ldg(reinterpret_cast<const uint32_t *>(at + kv4_kscale(D) + (r & 15) * 4));
+                ksc.x = __ldg(reinterpret_cast<const uint32_t *>(a + kv4_kscale(D) + (r & 15) * 4));
         };
-        fetch(0, page_of(0));
-        int next = page_of(1);
-        for (int j = 0; j < count; ++j) {
-            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(kfree, (j - 1) & 1, bad, limit)))
-                break;
-            const unsigned in = __ballot_sync(0xFFFFFFFFu, have);
+        auto fetch_v = [&](int j, int pg) {
+            vhave = pg >= 0 && g < G16;
+            if (!vhave)
+                return;
+            const uint8_t *a = at(j, oct >> 1, pg);
+            const uint4 *c = reinterpret_cast<const uint4 *>(a + kv4_v(D) + g * 128 + (oct & 1) * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                vcode[i] = __ldg(c + i);
+            vsc = __ldg(reinterpret_cast<const uint2 *>(a + kv4_vscale(D) + g * 16 + (oct & 1) * 8));
+        };
+        auto keys = [&](int j) {
+            const unsigned in = __ballot_sync(0xFFFFFFFFu, khave);
             if (lane == 0)
                 present[4 * (j & 1) + (warp - 8)] = (in & 1u) | (in >> 15 & 2u);
 #pragma unroll
-            for (int g = 0; g < G16; ++g) {
-                const uint4 u = code[g >> 1];
-                const uint32_t w[2] = {have ? (g & 1 ? u.z : u.x) : 0u, have ? (g & 1 ? u.w : u.y) : 0u};
-                const uint32_t sb = ((g & 4) ? sc.y : sc.x) >> (8 * (g & 3)) & 0xFFu;
-                const uint32_t f = have ? scales2((uint16_t)(sb * 0x0101u)) : 0u;
+            for (int gg = 0; gg < G16; ++gg) {
+                const uint4 u = kcode[gg >> 1];
+                const uint32_t w[2] = {khave ? (gg & 1 ? u.z : u.x) : 0u, khave ? (gg & 1 ? u.w : u.y) : 0u};
+                const uint32_t sb = ((gg & 4) ? ksc.y : ksc.x) >> (8 * (gg & 3)) & 0xFFu;
+                const uint32_t f = khave ? scales2((uint16_t)(sb * 0x0101u)) : 0u;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     uint32_t e[4];
                     widen4(w[k], e);
-                    const int c = 2 * g + k;
+                    const int c = 2 * gg + k;
                     sts128(base + L::k + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), hmul2(e[0], f),
                            hmul2(e[1], f), hmul2(e[2], f), hmul2(e[3], f));
                 }
             }
             fence_proxy_async_smem();
             bar_arrive(kfull);
-            fetch(j + 1, next);
-            next = page_of(j + 2);
-        }
-    } else if (warp < 16) {
-        // -------------------- values: eight tokens of a group of 16 features a thread
-        const int v = tid & 127, g = v >> 4, oct = v & 15;
-        const int *row = p.table + seq * p.table_ld;
-        const uint8_t *head = p.cache + (int64_t)h * p.tpp * kTile;
-        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
-        const int tiles = (most + kKv4Tile - 1) / kKv4Tile;
-        uint4 code[4];
-        uint2 sc = make_uint2(0, 0);
-        bool have = false;
-        auto page_of = [&](int j) {
-            const int t16 = j * 8 + (oct >> 1);
-            if (j >= count || t16 >= tiles || g >= G16)
-                return -1;
-            const int x = __ldg(row + t16 / p.tpp);
-            return x < p.pages ? x : -1;
         };
-        auto fetch = [&](int j, int pg) {
-            have = pg >= 0;
-            if (!have)
-                return;
-            const uint8_t *at = head + pg * page_bytes + (int64_t)((j * 8 + (oct >> 1)) % p.tpp) * kTile;
-            const uint4 *c = reinterpret_cast<const uint4 *>(at + kv4_v(D) + g * 128 + (oct & 1) * 64);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                code[i] = __ldg(c + i);
-            sc = __ldg(reinterpret_cast<const uint2 *>(at + kv4_vscale(D) + g * 16 + (oct & 1) * 8));
-        };
-        fetch(0, page_of(0));
-        int next = page_of(1);
-        for (int j = 0; j < count; ++j) {
-            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(vfree, (j - 1) & 1, bad, limit)))
-                break;
+        auto values = [&](int j) {
             if (g < G16) {
                 // tokens past the sequence's end, and those of a page that is
                 // not there, count as zeros whatever their bytes
-                const int left = have ? s.len - (j * kPromptTokens + oct * 8) : 0;
+                const int left = vhave ? s.len - (j * kPromptTokens + oct * 8) : 0;
                 uint32_t f[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = scales2((uint16_t)((i & 2 ? sc.y : sc.x) >> (16 * (i & 1))));
+                    const uint32_t two = scales2((uint16_t)((i & 2 ? vsc.y : vsc.x) >> (16 * (i & 1))));
                     f[i] = (2 * i < left ? two & 0xFFFFu : 0u) | (2 * i + 1 < left ? two & 0xFFFF0000u : 0u);
                 }
 #pragma unroll
@@ -456,26 +453,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                     uint32_t e[4][4], o[4][4];                  // [pair of tokens][pair of features]
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t a = have ? (w ? code[i].y : code[i].x) : 0u,
-                                       b = have ? (w ? code[i].w : code[i].z) : 0u;
+                        const uint32_t a = vhave ? (w ? vcode[i].y : vcode[i].x) : 0u,
+                                       b = vhave ? (w ? vcode[i].w : vcode[i].z) : 0u;
                         widen4((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), e[i]);
                         widen4(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), o[i]);
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int d = g * 16 + 8 * w + 2 * k;
-                        const uint32_t at = base + L::v + (oct >> 3) * (D * 128) + d * 128;
-                        sts128(at + (((oct & 7) ^ (d & 7)) << 4), hmul2(e[0][k], f[0]), hmul2(e[1][k], f[1]),
+                        const uint32_t to = base + L::v + (oct >> 3) * (D * 128) + d * 128;
+                        sts128(to + (((oct & 7) ^ (d & 7)) << 4), hmul2(e[0][k], f[0]), hmul2(e[1][k], f[1]),
                                hmul2(e[2][k], f[2]), hmul2(e[3][k], f[3]));
-                        sts128(at + 128 + (((oct & 7) ^ ((d + 1) & 7)) << 4), hmul2(o[0][k], f[0]),
+                        sts128(to + 128 + (((oct & 7) ^ ((d + 1) & 7)) << 4), hmul2(o[0][k], f[0]),
                                hmul2(o[1][k], f[1]), hmul2(o[2][k], f[2]), hmul2(o[3][k], f[3]));
                     }
                 }
             }
             fence_proxy_async_smem();
             bar_arrive(vfull);
-            fetch(j + 1, next);
-            next = page_of(j + 2);
+        };
+        int kpage = page_of(1, r >> 4), vpage = page_of(1, oct >> 1);
+        fetch_k(0, page_of(0, r >> 4));
+        fetch_v(0, page_of(0, oct >> 1));
+        if (count > 0)
+            keys(0);
+        fetch_k(1, kpage);
+        kpage = page_of(2, r >> 4);
+        for (int j = 0; j < count; ++j) {
+            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(vfree, (j - 1) & 1, bad, limit)))
+                break;
+            values(j);
+            fetch_v(j + 1, vpage);
+            vpage = page_of(j + 2, oct >> 1);
+            if (j + 1 < count) {
+                if (!__all_sync(0xFFFFFFFFu, prompt_wait(kfree, j & 1, bad, limit)))
+                    break;
+                keys(j + 1);
+                fetch_k(j + 2, kpage);
+                kpage = page_of(j + 3, r >> 4);
+            }
         }
     } else if (lane == 0 && count > 0) {
         // ------------------------------------------------------ the products
@@ -497,10 +513,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             scores(1);
             umma_commit(kfree);
         }
+        // the next scores before this tile's product: the softmax waits for them
         for (int j = 0; ok && j < count; ++j) {
-            ok = prompt_wait(vfull, j & 1, bad, limit);
             for (int t = 0; ok && t < 2; ++t) {
                 ok = prompt_wait(pfull + 8 * t, j & 1, bad, limit);
+                if (ok && j + 1 < count) {
+                    if (t == 0)
+                        ok = prompt_wait(kfull, (j + 1) & 1, bad, limit);
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    scores(t);
+                    if (t == 1)
+                        umma_commit(kfree);
+                }
+                if (ok && t == 0)
+                    ok = prompt_wait(vfull, j & 1, bad, limit);
                 if (!ok)
                     break;
                 tc_fence_after_sync();
@@ -511,16 +539,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                 umma_commit(pvdone + 8 * t);
                 if (t == 1)
                     umma_commit(vfree);
-                if (j + 1 < count) {
-                    if (t == 0)
-                        ok = prompt_wait(kfull, (j + 1) & 1, bad, limit);
-                    if (!ok)
-                        break;
-                    tc_fence_after_sync();
-                    scores(t);
-                    if (t == 1)
-                        umma_commit(kfree);
-                }
             }
         }
         // nothing may be in flight when the tensor memory is given back
@@ -534,7 +552,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 12) {
         tc_fence_after_sync();
         if (*bad && lane == 0)
             atomicAdd(p.timeouts, 1u);
