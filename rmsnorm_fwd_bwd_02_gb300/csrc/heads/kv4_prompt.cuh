@@ -19,11 +19,14 @@
 //   12          the products: S_t = Q_t K^T and O_t += P_t V, m128 n128 k16
 //               (n64 for O with heads of 64), issued by one thread.
 // While tile 0's rows are in the softmax the tensor cores work on tile 1's
-// scores, and the other way round. Tensor memory: two tiles of scores, two of
-// outputs, 512 columns. All operands are K-major in the 128-byte swizzled
-// layout (gemv_umma.cuh): P and the transposed values have the tokens as K.
-// A row's output is scaled in tensor memory when its reference moves, after
-// the product before has ended.
+// scores, and the other way round. Operands from shared memory are K-major in
+// the 128-byte swizzled layout (gemv_umma.cuh); the transposed values have the
+// tokens as K. Two m128 n128 k16 operands from shared memory take all of its
+// bandwidth, and p would be written there besides: p stays in tensor memory,
+// over its tile's scores, and is the product's first operand from there
+// (tensor memory: two tiles of scores and p, two of outputs, 512 columns).
+// That leaves room for keys and values in two buffers each. A row's output is
+// scaled in tensor memory when its reference moves.
 //
 // Every wait is bounded; one that runs out sets a flag that ends the others,
 // counts in the timeout counter and leaves the rows unwritten.
@@ -36,13 +39,13 @@ namespace rmsk {
 
 constexpr int kPromptRows = 256, kPromptTokens = 128, kPromptThreads = 13 * 32;
 
-// Shared memory: q of both tiles, keys, values, p of both tiles, then the
+// Shared memory: q of both tiles, keys and values (two in turn each), then the
 // barriers, the tensor-memory address and the keys' tiles that are there.
 template <int D>
 struct PromptLayout {
-    static constexpr uint32_t kQ = 128 * D * 2, kK = 128 * D * 2, kV = D * 128 * 2, kP = 128 * 128 * 2;
-    static constexpr uint32_t q = 0, k = 2 * kQ, v = k + kK, p = v + kV, bar = p + 2 * kP;
-    static constexpr uint32_t kBars = 12;
+    static constexpr uint32_t kQ = 128 * D * 2, kK = 128 * D * 2, kV = D * 128 * 2;
+    static constexpr uint32_t q = 0, k = 2 * kQ, v = k + 2 * kK, bar = v + 2 * kV;
+    static constexpr uint32_t kBars = 14;
     static constexpr uint32_t total = bar + 8 * kBars + 32 + 1023;       // with the alignment
 };
 
@@ -79,6 +82,33 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 32 words to as many columns of the warp's lanes, without the wait.
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+                 "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+                 "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+                 "r"(v[30]), "r"(v[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (tensor memory) = A B^T (+ D), kind::f16, with A in tensor memory: a lane a
+// row, a column two elements along K.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -113,12 +143,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     uint8_t *const sm = raw + (base - smem_addr(raw));
-    // barriers: keys full, free; values full, free; scores full [2]; p full [2]; product done [2]; all done
-    const uint32_t kfull = base + L::bar, kfree = kfull + 8, vfull = kfull + 16, vfree = kfull + 24,
-                   sfull = kfull + 32, pfull = kfull + 48, pvdone = kfull + 64, done = kfull + 80;
+    // barriers: keys full [2], free [2]; values full [2], free [2]; scores full [2]; p full [2]; all done
+    const uint32_t kfull = base + L::bar, kfree = kfull + 16, vfull = kfull + 32, vfree = kfull + 48,
+                   sfull = kfull + 64, pfull = kfull + 80, done = kfull + 96;
     volatile uint32_t *slots = reinterpret_cast<volatile uint32_t *>(sm + L::bar + 8 * L::kBars);
     volatile int *bad = reinterpret_cast<volatile int *>(slots + 1);
-    volatile uint8_t *present = reinterpret_cast<volatile uint8_t *>(sm + L::bar + 8 * L::kBars + 8);   // [2][4]
+    volatile uint8_t *present = reinterpret_cast<volatile uint8_t *>(sm + L::bar + 8 * L::kBars + 8);   // [4][4]
 
     griddep_wait();
     griddep_launch_dependents();
@@ -161,13 +191,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
 
     if (warp == 12) {
         if (lane == 0) {
-            // the test hook: one arrival more than there are, so that the waits run out
-            mbar_init(kfull, p.extra_tx ? 129 : 128); mbar_init(kfree, 1);
-            mbar_init(vfull, 128); mbar_init(vfree, 1);
             for (int t = 0; t < 2; ++t) {
+                // the test hook: one arrival more than there are, so that the waits run out
+                mbar_init(kfull + 8 * t, p.extra_tx ? 129 : 128);
+                mbar_init(kfree + 8 * t, 1);
+                mbar_init(vfull + 8 * t, 128);
+                mbar_init(vfree + 8 * t, 1);
                 mbar_init(sfull + 8 * t, 1);
                 mbar_init(pfull + 8 * t, 128);
-                mbar_init(pvdone + 8 * t, 1);
             }
             mbar_init(done, 1);
             mbar_init_fence();
@@ -241,7 +272,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
         const int t = tid >> 7, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // (32 (warp % 4)) << 16
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-        const uint32_t ps = base + L::p + t * L::kP + r * 128;
         // (a row that sees nothing wants no reference)
         float m = lim > 0 ? kKv4Least : 0.f, l = 0.f;
         int least = real ? lim : INT32_MAX;
@@ -254,54 +284,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             if (!ok)
                 break;
             tc_fence_after_sync();
-            const uint32_t there = *reinterpret_cast<volatile uint32_t *>(sm + L::bar + 8 * L::kBars + 8 + 4 * (j & 1));
+            const uint32_t there = *reinterpret_cast<volatile uint32_t *>(sm + L::bar + 8 * L::kBars + 8 + 4 * (j & 3));
             const int tok = j * kPromptTokens;
             const bool whole = tok + kPromptTokens <= least && there == 0x03030303u;
             // column c's token is seen: past neither the row's limit nor in a tile that is not there
             auto seen = [&](int c) { return tok + c < lim && (there >> (8 * (c >> 5) + ((c >> 4) & 1)) & 1u); };
-            if (j > 0) {
-                // p's place, and O, are the product's before until it has ended
-                ok = __all_sync(0xFFFFFFFFu, prompt_wait(pvdone + 8 * t, (j - 1) & 1, bad, limit));
-                if (!ok)
-                    break;
-                tc_fence_after_sync();
-            }
-            // p from the reference as it is; most tiles do not pass it
-            const float l0 = l;
-            bool far = m == kKv4Least;
+            // p from the reference as it is, where all tokens are seen: most
+            // tiles do not pass it
+            bool far = m == kKv4Least || !whole;
             if (!__any_sync(0xFFFFFFFFu, far)) {
                 const float2 mul2 = make_float2(mul, mul), b2 = make_float2(8.f - m, 8.f - m);
                 float2 sum = make_float2(0.f, 0.f);
-                uint32_t top = 0;                               // of the packed p: positive halves compare as integers
+                uint32_t top = 0, w[64];                        // packed p; positive halves compare as integers
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     float x[32];
                     tmem_ld32(ts + 32 * ch, x);
-                    uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), mul2, b2);
-                        float2 e = make_float2(exp2_of(y.x), exp2_of(y.y));
-                        if (!whole) {
-                            e.x = seen(32 * ch + 2 * i) ? e.x : 0.f;
-                            e.y = seen(32 * ch + 2 * i + 1) ? e.y : 0.f;
-                        }
+                        const float2 e = make_float2(exp2_of(y.x), exp2_of(y.y));
                         sum = __fadd2_rn(sum, e);
-                        w[i] = Half16<f16>::narrow2(e.x, e.y);
-                        top = __vmaxu2(top, w[i]);
+                        w[16 * ch + i] = Half16<f16>::narrow2(e.x, e.y);
+                        top = __vmaxu2(top, w[16 * ch + i]);
                     }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4), w[4 * c], w[4 * c + 1],
-                               w[4 * c + 2], w[4 * c + 3]);
                 }
-                l += sum.x + sum.y;
                 far = max(top & 0xFFFFu, top >> 16) > 0x7800u;  // above 2^15, or not a number
+                // over the scores, unless they are wanted again
+                if (!__any_sync(0xFFFFFFFFu, far)) {
+                    l += sum.x + sum.y;
+                    tmem_put32(ts, w);
+                    tmem_put32(ts + 32, w + 32);
+                }
             }
             if (__any_sync(0xFFFFFFFFu, far)) {
                 // a new reference for the rows that want one, and p again
                 float x[32], mx = kKv4Least, f = 1.f;
-                l = l0;
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
                     tmem_ld32(ts + 32 * ch, x);
@@ -327,29 +345,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                     }
                 }
                 const float b = m == kKv4Least ? 0.f : m - 8.f;
+                // (a chunk's p takes columns of scores that have been read)
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    tmem_ld32(ts + 32 * ch, x);
+                for (int ch = 0; ch < 4; ch += 2) {
+                    uint32_t w[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        x[i] = seen(32 * ch + i) ? exp2_of(fmaf(x[i], mul, -b)) : 0.f;
-                        l += x[i];
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_ld32(ts + 32 * (ch + k), x);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            x[i] = seen(32 * (ch + k) + i) ? exp2_of(fmaf(x[i], mul, -b)) : 0.f;
+                            x[i + 1] = seen(32 * (ch + k) + i + 1) ? exp2_of(fmaf(x[i + 1], mul, -b)) : 0.f;
+                            l += x[i] + x[i + 1];
+                            w[16 * k + i / 2] = Half16<f16>::narrow2(x[i], x[i + 1]);
+                        }
                     }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        sts128(ps + (ch >> 1) * 16384 + ((((ch & 1) * 4 + c) ^ (r & 7)) << 4),
-                               Half16<f16>::narrow2(x[8 * c], x[8 * c + 1]),
-                               Half16<f16>::narrow2(x[8 * c + 2], x[8 * c + 3]),
-                               Half16<f16>::narrow2(x[8 * c + 4], x[8 * c + 5]),
-                               Half16<f16>::narrow2(x[8 * c + 6], x[8 * c + 7]));
+                    tmem_put32(ts + 16 * ch, w);
                 }
             }
-            fence_proxy_async_smem();
+            tmem_put_wait();
             tc_fence_before_sync();
             bar_arrive(pfull + 8 * t);
         }
         if (ok && count > 0)
-            ok = __all_sync(0xFFFFFFFFu, prompt_wait(pvdone + 8 * t, (count - 1) & 1, bad, limit));
+            ok = __all_sync(0xFFFFFFFFu, prompt_wait(done, 0, bad, limit)) && !*bad;
         if (ok) {
             tc_fence_after_sync();
             const float gv = p.vscale ? __ldg(p.vscale + h) : 1.f;
@@ -379,22 +398,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
         uint4 kcode[D / 32], vcode[4];
         uint2 ksc = make_uint2(0, 0), vsc = make_uint2(0, 0);
         bool khave = false, vhave = false;
-        // the page of tile t16 of tile j's eight
-        auto page_of = [&](int j, int t16) {
-            t16 += j * 8;
-            if (j >= count || t16 >= tiles)
-                return -1;
-            const int v = __ldg(row + t16 / p.tpp);
-            return v < p.pages ? v : -1;
+        // The cache's tiles of 16 tokens that a thread goes through, eight
+        // apart: their block in the table and place in its page, advanced
+        // without a division. A page is looked at when it is used, a tile after
+        // it was loaded, so that nothing waits for it.
+        const int by_blk = 8 / p.tpp, by_in = 8 - by_blk * p.tpp;
+        struct Walk {
+            int t16, blk, in;                                   // the tile whose page comes next
+            int page, place;                                    // the tile before: its page, its place there
         };
-        auto at = [&](int j, int t16, int pg) {
-            return head + pg * page_bytes + (int64_t)((j * 8 + t16) % p.tpp) * kTile;
+        auto ahead = [&](Walk &w) {
+            w.place = w.in;
+            w.page = w.t16 < tiles ? __ldg(row + w.blk) : -1;
+            w.t16 += 8;
+            w.blk += by_blk;
+            w.in += by_in;
+            if (w.in >= p.tpp) {
+                w.in -= p.tpp;
+                ++w.blk;
+            }
         };
-        auto fetch_k = [&](int j, int pg) {
-            khave = pg >= 0;
+        auto at = [&](const Walk &w) { return head + w.page * page_bytes + w.place * kTile; };
+        Walk kw = {r >> 4, (r >> 4) / p.tpp, (r >> 4) % p.tpp, -1, 0},
+             vw = {oct >> 1, (oct >> 1) / p.tpp, (oct >> 1) % p.tpp, -1, 0};
+        auto fetch_k = [&]() {
+            khave = kw.page >= 0 && kw.page < p.pages;
             if (!khave)
                 return;
-            const uint8_t *a = at(j, r >> 4, pg);
+            const uint8_t *a = at(kw);
             const uint4 *c = reinterpret_cast<const uint4 *>(a + (r & 15) * (D / 2));
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -404,11 +435,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             else
                 ksc.x = __ldg(reinterpret_cast<const uint32_t *>(a + kv4_kscale(D) + (r & 15) * 4));
         };
-        auto fetch_v = [&](int j, int pg) {
-            vhave = pg >= 0 && g < G16;
+        auto fetch_v = [&]() {
+            vhave = vw.page >= 0 && vw.page < p.pages && g < G16;
             if (!vhave)
                 return;
-            const uint8_t *a = at(j, oct >> 1, pg);
+            const uint8_t *a = at(vw);
             const uint4 *c = reinterpret_cast<const uint4 *>(a + kv4_v(D) + g * 128 + (oct & 1) * 64);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -418,7 +449,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
         auto keys = [&](int j) {
             const unsigned in = __ballot_sync(0xFFFFFFFFu, khave);
             if (lane == 0)
-                present[4 * (j & 1) + (warp - 8)] = (in & 1u) | (in >> 15 & 2u);
+                present[4 * (j & 3) + (warp - 8)] = (in & 1u) | (in >> 15 & 2u);
 #pragma unroll
             for (int gg = 0; gg < G16; ++gg) {
                 const uint4 u = kcode[gg >> 1];
@@ -430,12 +461,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                     uint32_t e[4];
                     widen4(w[k], e);
                     const int c = 2 * gg + k;
-                    sts128(base + L::k + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), hmul2(e[0], f),
+                    sts128(base + L::k + (j & 1) * L::kK + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), hmul2(e[0], f),
                            hmul2(e[1], f), hmul2(e[2], f), hmul2(e[3], f));
                 }
             }
             fence_proxy_async_smem();
-            bar_arrive(kfull);
+            bar_arrive(kfull + 8 * (j & 1));
         };
         auto values = [&](int j) {
             if (g < G16) {
@@ -461,7 +492,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int d = g * 16 + 8 * w + 2 * k;
-                        const uint32_t to = base + L::v + (oct >> 3) * (D * 128) + d * 128;
+                        const uint32_t to = base + L::v + (j & 1) * L::kV + (oct >> 3) * (D * 128) + d * 128;
                         sts128(to + (((oct & 7) ^ (d & 7)) << 4), hmul2(e[0][k], f[0]), hmul2(e[1][k], f[1]),
                                hmul2(e[2][k], f[2]), hmul2(e[3][k], f[3]));
                         sts128(to + 128 + (((oct & 7) ^ ((d + 1) & 7)) << 4), hmul2(o[0][k], f[0]),
@@ -470,75 +501,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                 }
             }
             fence_proxy_async_smem();
-            bar_arrive(vfull);
+            bar_arrive(vfull + 8 * (j & 1));
         };
-        int kpage = page_of(1, r >> 4), vpage = page_of(1, oct >> 1);
-        fetch_k(0, page_of(0, r >> 4));
-        fetch_v(0, page_of(0, oct >> 1));
-        if (count > 0)
-            keys(0);
-        fetch_k(1, kpage);
-        kpage = page_of(2, r >> 4);
+        ahead(kw);
+        ahead(vw);
+        fetch_k();
+        fetch_v();
+        ahead(kw);
+        ahead(vw);
         for (int j = 0; j < count; ++j) {
-            if (j > 0 && !__all_sync(0xFFFFFFFFu, prompt_wait(vfree, (j - 1) & 1, bad, limit)))
+            const uint32_t again = ((j >> 1) - 1) & 1;          // the phase that frees a buffer
+            if (j > 1 && !__all_sync(0xFFFFFFFFu, prompt_wait(kfree + 8 * (j & 1), again, bad, limit)))
+                break;
+            keys(j);
+            fetch_k();
+            ahead(kw);
+            if (j > 1 && !__all_sync(0xFFFFFFFFu, prompt_wait(vfree + 8 * (j & 1), again, bad, limit)))
                 break;
             values(j);
-            fetch_v(j + 1, vpage);
-            vpage = page_of(j + 2, oct >> 1);
-            if (j + 1 < count) {
-                if (!__all_sync(0xFFFFFFFFu, prompt_wait(kfree, j & 1, bad, limit)))
-                    break;
-                keys(j + 1);
-                fetch_k(j + 2, kpage);
-                kpage = page_of(j + 3, r >> 4);
-            }
+            fetch_v();
+            ahead(vw);
         }
     } else if (lane == 0 && count > 0) {
         // ------------------------------------------------------ the products
         const uint32_t is = umma_idesc_f16(0, 128, 128), io = umma_idesc_f16(0, 128, D);
         const uint64_t dq = umma_desc_sw128(base + L::q), dk = umma_desc_sw128(base + L::k),
-                       dv = umma_desc_sw128(base + L::v), dp = umma_desc_sw128(base + L::p);
-        auto scores = [&](int t) {
+                       dv = umma_desc_sw128(base + L::v);
+        auto scores = [&](int t, int j) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint64_t step = (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3));
-                umma_f16(tmem + t * 128, dq + t * (L::kQ >> 4) + step, dk + step, is, k > 0);
+                umma_f16(tmem + t * 128, dq + t * (L::kQ >> 4) + step, dk + (j & 1) * (L::kK >> 4) + step, is, k > 0);
             }
             umma_commit(sfull + 8 * t);
+            if (t == 1)
+                umma_commit(kfree + 8 * (j & 1));
         };
         bool ok = prompt_wait(kfull, 0, bad, limit);
         if (ok) {
             tc_fence_after_sync();
-            scores(0);
-            scores(1);
-            umma_commit(kfree);
+            scores(0, 0);
+            scores(1, 0);
         }
-        // the next scores before this tile's product: the softmax waits for them
         for (int j = 0; ok && j < count; ++j) {
             for (int t = 0; ok && t < 2; ++t) {
-                ok = prompt_wait(pfull + 8 * t, j & 1, bad, limit);
-                if (ok && j + 1 < count) {
-                    if (t == 0)
-                        ok = prompt_wait(kfull, (j + 1) & 1, bad, limit);
-                    if (!ok)
-                        break;
-                    tc_fence_after_sync();
-                    scores(t);
-                    if (t == 1)
-                        umma_commit(kfree);
-                }
-                if (ok && t == 0)
-                    ok = prompt_wait(vfull, j & 1, bad, limit);
+                ok = prompt_wait(pfull + 8 * t, j & 1, bad, limit) &&
+                     (t == 1 || prompt_wait(vfull + 8 * (j & 1), (j >> 1) & 1, bad, limit));
                 if (!ok)
                     break;
                 tc_fence_after_sync();
 #pragma unroll
                 for (int k = 0; k < kPromptTokens / 16; ++k)
-                    umma_f16(tmem + 256 + t * 128, dp + t * (L::kP >> 4) + (k >> 2) * (16384 >> 4) + 2 * (k & 3),
-                             dv + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, j > 0 || k > 0);
-                umma_commit(pvdone + 8 * t);
+                    umma_f16_ta(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                                dv + (j & 1) * (L::kV >> 4) + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io,
+                                j > 0 || k > 0);
                 if (t == 1)
-                    umma_commit(vfree);
+                    umma_commit(vfree + 8 * (j & 1));
+                if (j + 1 < count) {
+                    ok = t == 1 || prompt_wait(kfull + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, bad, limit);
+                    if (!ok)
+                        break;
+                    tc_fence_after_sync();
+                    scores(t, j + 1);
+                }
             }
         }
         // nothing may be in flight when the tensor memory is given back

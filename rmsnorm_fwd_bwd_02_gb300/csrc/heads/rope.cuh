@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     constexpr bool APP = FORM > 0;
     constexpr int V = E == 1 ? 4 : 1, U = rope_fwd_heads<E>(FORM);
     using P = Pack<T, E>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *fractions = reinterpret_cast<uint64_t *>(smem);
     // the fractions first, the staged rows, then the ring
     float *stage_all = reinterpret_cast<float *>(smem + kRopeFractions);
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     constexpr int V = E == 1 ? 4 : 1, U = rope_bwd_heads<E>();
     using P = Pack<T, E>;
     using F = typename Vals<E>::F;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *fractions = reinterpret_cast<uint64_t *>(smem);
     const RopeRing<T, E, 4 * U> ring = {smem + kRopeFractions + threadIdx.x * (E * sizeof(T))};
 
