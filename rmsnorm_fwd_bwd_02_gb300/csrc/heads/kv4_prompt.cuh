@@ -17,7 +17,7 @@
 //               interleaves in pairs of tokens; bytes from global memory a
 //               tile ahead;
 //   12          the products: S_t = Q_t K^T and O_t += P_t V, m128 n128 k16
-//               (n64 for O with heads of 64), issued by one thread.
+//               (n64 for O with heads of 64).
 // While tile 0's rows are in the softmax the tensor cores work on tile 1's
 // scores, and the other way round. Operands from shared memory are K-major in
 // the 128-byte swizzled layout (gemv_umma.cuh); the transposed values have the
@@ -107,6 +107,14 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
                  "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
+}
+
+// One lane of the warp, always the same; all lanes take part.
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
@@ -522,43 +530,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             fetch_v();
             ahead(vw);
         }
-    } else if (lane == 0 && count > 0) {
+    } else if (count > 0) {
         // ------------------------------------------------------ the products
+        // The whole warp goes through this, so that the descriptors are
+        // computed in uniform registers; one elected lane issues.
+        const bool one = elect_lane();
         const uint32_t is = umma_idesc_f16(0, 128, 128), io = umma_idesc_f16(0, 128, D);
         const uint64_t dq = umma_desc_sw128(base + L::q), dk = umma_desc_sw128(base + L::k),
                        dv = umma_desc_sw128(base + L::v);
-        auto scores = [&](int t, int j) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint64_t step = (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3));
-                umma_f16(tmem + t * 128, dq + t * (L::kQ >> 4) + step, dk + (j & 1) * (L::kK >> 4) + step, is, k > 0);
-            }
-            umma_commit(sfull + 8 * t);
-            if (t == 1)
-                umma_commit(kfree + 8 * (j & 1));
+        auto wait = [&](uint32_t bar, int phase) {
+            return __all_sync(0xFFFFFFFFu, prompt_wait(bar, (uint32_t)phase & 1u, bad, limit));
         };
-        bool ok = prompt_wait(kfull, 0, bad, limit);
+        auto scores = [&](int t, int j) {
+            const uint64_t a = dq + t * (L::kQ >> 4), b = dk + (j & 1) * (L::kK >> 4);
+            if (one) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t step = (uint64_t)((k >> 2) * (16384 >> 4) + 2 * (k & 3));
+                    if (k == 0)
+                        umma_f16(tmem + t * 128, a, b, is, 0);
+                    else
+                        umma_f16(tmem + t * 128, a + step, b + step, is, 1);
+                }
+                umma_commit(sfull + 8 * t);
+                if (t == 1)
+                    umma_commit(kfree + 8 * (j & 1));
+            }
+            __syncwarp();
+        };
+        bool ok = wait(kfull, 0);
         if (ok) {
             tc_fence_after_sync();
             scores(0, 0);
             scores(1, 0);
         }
         for (int j = 0; ok && j < count; ++j) {
-            for (int t = 0; ok && t < 2; ++t) {
-                ok = prompt_wait(pfull + 8 * t, j & 1, bad, limit) &&
-                     (t == 1 || prompt_wait(vfull + 8 * (j & 1), (j >> 1) & 1, bad, limit));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                ok = ok && wait(pfull + 8 * t, j) && (t == 1 || wait(vfull + 8 * (j & 1), j >> 1));
                 if (!ok)
                     break;
                 tc_fence_after_sync();
+                if (one) {
+                    const uint64_t b = dv + (j & 1) * (L::kV >> 4);
 #pragma unroll
-                for (int k = 0; k < kPromptTokens / 16; ++k)
-                    umma_f16_ta(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                                dv + (j & 1) * (L::kV >> 4) + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io,
-                                j > 0 || k > 0);
-                if (t == 1)
-                    umma_commit(vfree + 8 * (j & 1));
+                    for (int k = 0; k < kPromptTokens / 16; ++k)
+                        umma_f16_ta(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                                    b + (k >> 2) * (D * 128 >> 4) + 2 * (k & 3), io, k == 0 ? j > 0 : 1);
+                    if (t == 1)
+                        umma_commit(vfree + 8 * (j & 1));
+                }
+                __syncwarp();
                 if (j + 1 < count) {
-                    ok = t == 1 || prompt_wait(kfull + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, bad, limit);
+                    ok = t == 1 || wait(kfull + 8 * ((j + 1) & 1), (j + 1) >> 1);
                     if (!ok)
                         break;
                     tc_fence_after_sync();
@@ -567,7 +591,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             }
         }
         // nothing may be in flight when the tensor memory is given back
-        umma_commit(done);
+        if (one)
+            umma_commit(done);
+        __syncwarp();
         const unsigned long long t0 = global_ns();
         while (!mbar_try_wait(done, 0))
             if (global_ns() - t0 > limit) {
