@@ -150,7 +150,7 @@ __host__ __device__ constexpr int kv4_ctas_per_sm(int NT) { return NT == 1 ? 2 :
 // denominators.
 __host__ __device__ constexpr int kv4_partial(int D, int NT) { return 8 * NT * (D + 2); }
 
-// [dtype: bf16, fp16][D: 64, 128][NT - 1]
+// [dtype: bf16, fp16][D: 64, 128][NT - 1]; heads of 64 in tiles of 8 rows only.
 struct Kv4Kernels {
     const void *attend[2][2][2], *combine[2][2][2];
 };

@@ -50,7 +50,8 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
         return RMSNORM_ERR_BAD_EPS;
     if ((D != 64 && D != 128) || page_size % kKv4Tile || page_size > INT32_MAX || heads > (1 << 20) ||
         pages > INT32_MAX || blocks > INT32_MAX || B > (1 << 20) || T > INT32_MAX ||
-        blocks > (INT32_MAX - 1024) / page_size || (T + B) > INT32_MAX / heads)
+        blocks > (INT32_MAX - 1024) / page_size || (T + B) > INT32_MAX / heads ||
+        page_size * kv_heads > INT32_MAX / (D * 9 / 8))
         return RMSNORM_ERR_UNSUPPORTED;
     if (!rows_within({T, heads, 1}, {q_token, q_head, 0}, D) ||
         !rows_apart({T, heads, 1}, {out_token, out_head, 0}, D) ||
@@ -89,10 +90,12 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
     if (tmo == nullptr)
         return cuda_fail(cudaErrorInvalidSymbol);
     const int64_t G = heads / kv_heads;
-    // eight query rows a tile where a sequence's rows of one key head fit,
-    // else sixteen: the cache's bytes are widened once for both halves
+    // Eight query rows a tile where a sequence's rows of one key head fit, and
+    // for heads of 64, whose kernel then runs twice on an SM (16 x 5 tokens of
+    // 14 heads over up to 3000: 17.8 us, with sixteen rows 21.3); else sixteen:
+    // the cache's bytes are widened once for both halves.
     const int64_t rows = (T + B - 1) / B * G;
-    const int NT = rows <= 8 ? 1 : 2, di = D == 128 ? 1 : 0, ti = dtype == RMSNORM_BF16 ? 0 : 1;
+    const int NT = rows <= 8 || D == 64 ? 1 : 2, di = D == 128 ? 1 : 0, ti = dtype == RMSNORM_BF16 ? 0 : 1;
     Kv4Params p = {q, q_token, q_head, out, out_token, out_head, lse, static_cast<const uint8_t *>(cache), pages,
                    (int)(page_size / kKv4Tile), k_scale, v_scale, block_table, table_stride, (int)blocks, seq_lens,
                    q_starts, (int)B, (int)T, (int)kv_heads, (int)G, scale,
@@ -123,6 +126,9 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
         t_last_path = kPathKv4Prompt;
         return RMSNORM_OK;
     }
+    const int64_t tiles = q_starts ? (T * G) / (8 * NT) + B : B * ((G + 8 * NT - 1) / (8 * NT));
+    if (tiles * kv_heads > INT32_MAX / (blocks * page_size / kKv4Slot + 2))
+        return RMSNORM_ERR_UNSUPPORTED;
     const void *fn = kv4_kernels.attend[ti][di][NT - 1];
     const int smem = kv4_smem((int)D);
     int bps;
@@ -135,7 +141,6 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
         return cuda_fail(e);
     // the parts of segments that were split; none is, where one stage covers any length
     if (blocks * page_size > kKv4Slot) {
-        const int64_t tiles = q_starts ? (T * G) / (8 * NT) + B : B * ((G + 8 * NT - 1) / (8 * NT));
         void *cargs[2] = {&p, &ctas};
         e = launch_pdl(kv4_kernels.combine[ti][di][NT - 1], dim3((unsigned)(tiles * kv_heads)), 256, 0, s, cargs);
         if (e != cudaSuccess)

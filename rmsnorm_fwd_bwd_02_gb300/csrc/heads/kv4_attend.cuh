@@ -105,7 +105,7 @@ struct Kv4Seq {
     int tiles;           // of 8 NT query rows
     int stages;          // of 32 tokens
     __device__ __forceinline__ int cost() const { return stages + 1; }
-    __device__ __forceinline__ int64_t total(int Hk) const { return (int64_t)tiles * Hk * cost(); }
+    __device__ __forceinline__ uint32_t total(int Hk) const { return (uint32_t)tiles * Hk * cost(); }
 };
 
 // Sequence b as far as its lengths are sound: rows within [0, T), tokens
@@ -128,13 +128,13 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Params &p, int b)
     return s;
 }
 
-// Where in the list the sequences begin: the sums of 32 sequences at a time,
-// the last such run of them in the lanes.
+// Where in the list (of fewer than 2^31 entries) the sequences begin: the sums
+// of 32 sequences at a time, the last such run of them in the lanes.
 struct Kv4List {
     int base;            // first sequence in the lanes
-    int64_t mine, sum;   // this lane's entries, and all up to and with it
-    int64_t before;      // entries before `base`
-    int64_t total;       // of the whole call
+    uint32_t mine, sum;   // this lane's entries, and all up to and with it
+    uint32_t before;      // entries before `base`
+    uint32_t total;       // of the whole call
 
     template <int NT>
     __device__ __forceinline__ void load(const Kv4Params &p, int from)
@@ -145,12 +145,12 @@ struct Kv4List {
         sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if ((threadIdx.x & 31) >= o)
                 sum += t;
         }
     }
-    __device__ __forceinline__ int64_t all() const { return __shfl_sync(0xFFFFFFFFu, sum, 31); }
+    __device__ __forceinline__ uint32_t all() const { return __shfl_sync(0xFFFFFFFFu, sum, 31); }
     template <int NT> __device__ __forceinline__ void init(const Kv4Params &p)
     {
         before = total = 0;
@@ -163,7 +163,7 @@ struct Kv4List {
     }
     // The sequence that holds entry u < total, and the entries before it.
     template <int NT>
-    __device__ __forceinline__ int find(const Kv4Params &p, int64_t u, int64_t &first)
+    __device__ __forceinline__ int find(const Kv4Params &p, uint32_t u, uint32_t &first)
     {
         if (u < before) {
             before = 0;
@@ -188,16 +188,16 @@ struct Kv4List {
 // stages follow.
 struct Kv4Segment {
     int h, tile;
-    int64_t at;          // entry of its first stage
+    uint32_t at;          // entry of its first stage
 };
 
-__device__ __forceinline__ Kv4Segment kv4_segment(const Kv4Seq &s, int64_t first, int64_t u)
+__device__ __forceinline__ Kv4Segment kv4_segment(const Kv4Seq &s, uint32_t first, uint32_t u)
 {
-    const int seg = (int)((u - first) / s.cost());
+    const uint32_t seg = (u - first) / (uint32_t)s.cost();
     Kv4Segment g;
-    g.h = seg / s.tiles;
-    g.tile = seg - g.h * s.tiles;
-    g.at = first + (int64_t)seg * s.cost() + 1;
+    g.h = (int)(seg / (uint32_t)s.tiles);
+    g.tile = (int)seg - g.h * s.tiles;
+    g.at = first + seg * s.cost() + 1;
     return g;
 }
 
@@ -236,7 +236,7 @@ __device__ __forceinline__ float kv4_lse(float m, float l)
 template <typename T, int D, int NT>
 struct Kv4Query {
     uint32_t b[NT][D / 16][2];     // q as the MMAs' B
-    float mul[NT][2];              // scores to powers of two, for the lane's two rows of a tile of 8
+    float2 mul[NT];                // scores to powers of two (not negative), for the lane's two rows of a tile of 8
     int lim[NT][2];                // tokens that they see
     int most, least;               // of all rows of the tile: most seen, and fewest of the real ones
 
@@ -277,8 +277,9 @@ struct Kv4Query {
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             const int e = max((int)(__float_as_uint(m) >> 23) - 127, -100);
-            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            const float mine = base * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+            // the factor's sign goes into q: the largest score is then the largest power
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), base);
+            const float mine = fabsf(base) * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
                 const float2 v = Half16<T>::wide2(w[j]);
@@ -289,11 +290,10 @@ struct Kv4Query {
                 most = max(most, see);
                 least = min(least, see);
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mul[nt][j] = __shfl_sync(0xFFFFFFFFu, mine, 4 * (2 * c + j));
-                lim[nt][j] = __shfl_sync(0xFFFFFFFFu, see, 4 * (2 * c + j));
-            }
+            mul[nt].x = __shfl_sync(0xFFFFFFFFu, mine, 8 * c);
+            mul[nt].y = __shfl_sync(0xFFFFFFFFu, mine, 8 * c + 4);
+            lim[nt][0] = __shfl_sync(0xFFFFFFFFu, see, 8 * c);
+            lim[nt][1] = __shfl_sync(0xFFFFFFFFu, see, 8 * c + 4);
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
@@ -305,7 +305,7 @@ struct Kv4Query {
 
 // The parts of a segment in the workspace: of each warp two at most, the first
 // of its run and the last; a CTA that joined its warps' sums uses its first.
-__device__ __forceinline__ int64_t kv4_part(int64_t warp, bool later) { return 2 * warp + (later ? 1 : 0); }
+__device__ __forceinline__ int64_t kv4_part(uint32_t warp, bool later) { return 2 * (int64_t)warp + (later ? 1 : 0); }
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_attend(Kv4Params p)
@@ -334,13 +334,14 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
 
     Kv4List list = {};
     list.init<NT>(p);
-    const int64_t C = (list.total + (int64_t)gridDim.x * kKv4Warps - 1) / ((int64_t)gridDim.x * kKv4Warps);
-    const int64_t cta0 = (int64_t)blockIdx.x * kKv4Warps * C, cta1 = min(cta0 + kKv4Warps * C, list.total);
+    const uint32_t warps = gridDim.x * kKv4Warps, C = (list.total + warps - 1) / warps;
+    // (unsigned sums below 2^31 + 2^12 each)
+    const uint32_t cta0 = min(blockIdx.x * kKv4Warps * C, list.total), cta1 = min(cta0 + kKv4Warps * C, list.total);
     if (cta0 >= cta1)
         return;                                                 // for the whole CTA
-    const int64_t gw = (int64_t)blockIdx.x * kKv4Warps + warp;
-    const int64_t run0 = gw * C, run1 = min(run0 + C, list.total);
-    int64_t first;
+    const uint32_t gw = blockIdx.x * kKv4Warps + warp;
+    const uint32_t run0 = min(gw * C, list.total), run1 = min(run0 + C, list.total);
+    uint32_t first;
     int seq = list.find<NT>(p, cta0, first);
     if (seq < 0)
         return;
@@ -354,11 +355,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
 
     Kv4Query<T, D, NT> q;
     float o[NT][D / 16][4], l[NT][2], m[NT][2];
+    float2 less[NT];                                            // 8 - m, 0 before there is one
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         m[nt][0] = m[nt][1] = kKv4Least;
 
-    for (int64_t u = run0; u < run1 && ok;) {
+    for (uint32_t u = run0; u < run1 && ok;) {
         if (u >= first + s.total(p.Hk)) {
             seq = list.find<NT>(p, u, first);
             if (seq < 0)
@@ -368,8 +370,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         g = kv4_segment(s, first, u);
         if ((unsigned)g.h >= (unsigned)p.Hk)
             break;
-        const int from = (int)max((int64_t)0, u - g.at);        // this run's stages
-        const int to = (int)min((int64_t)s.stages, run1 - g.at);
+        const int from = u > g.at ? (int)(u - g.at) : 0;        // this run's stages
+        const int to = run1 > g.at ? min(s.stages, (int)(run1 - g.at)) : 0;
         u = g.at + s.stages;                                    // the next segment
         if (from >= to && s.stages > 0)
             continue;                                           // its first entry alone
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         const int count = max(0, seen - from);
         const int last = (q.most + kKv4Tile - 1) / kKv4Tile;    // tiles that hold seen tokens
         const uint8_t *head = p.cache + (int64_t)g.h * p.tpp * kTile;
-        const int64_t page_bytes = (int64_t)p.Hk * p.tpp * kTile;
+        const uint32_t page_bytes = (uint32_t)p.Hk * p.tpp * kTile;      // below 2^31
         uint32_t there = 0;                                     // two bits a stage of the ring: its tiles are there
         auto next_tile = [&]() {
             if (++tin == p.tpp) {
@@ -398,22 +400,45 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
                 p1 = page_of(blk + 1);
             }
         };
+        const bool pairs = (p.tpp & 1) == 0;                    // a stage's two tiles lie side by side in a page
         auto fill = [&](int i) {
             if (i >= count)
                 return;
-            const int ta = tin, pa = p0;
-            next_tile();
-            const int tb = tin, pb = t0 + 2 * i + 1 < last ? p0 : -1;
-            next_tile();
-            there = (there & ~(3u << (2 * st_fill))) | ((pa >= 0 ? 1u : 0u) | (pb >= 0 ? 2u : 0u)) << (2 * st_fill);
-            if (lane == 0) {
-                const uint32_t dst = ring_s + st_fill * kSlot, bar = bars + 8 * st_fill;
-                mbar_expect_tx(bar, ((pa >= 0) + (pb >= 0)) * kTile + p.extra_tx);
-                if (pa >= 0)
-                    bulk_g2s(dst, head + pa * page_bytes + ta * kTile, kTile, bar);
-                if (pb >= 0)
-                    bulk_g2s(dst + kTile, head + pb * page_bytes + tb * kTile, kTile, bar);
+            const uint32_t dst = ring_s + st_fill * kSlot, bar = bars + 8 * st_fill;
+            const bool second = t0 + 2 * i + 1 < last;
+            const int pa = p0;
+            const uint8_t *src = head + (uint64_t)(uint32_t)pa * (uint32_t)page_bytes + (uint32_t)tin * kTile;
+            uint32_t bits;
+            if (pairs) {
+                bits = pa >= 0 ? (second ? 3u : 1u) : 0u;
+                if (lane == 0) {
+                    const uint32_t bytes = bits == 0 ? 0u : (second ? 2u * kTile : (uint32_t)kTile);
+                    mbar_expect_tx(bar, bytes + p.extra_tx);
+                    if (bits)
+                        bulk_g2s(dst, src, bytes, bar);
+                }
+                tin += 2;
+                if (tin == p.tpp) {
+                    tin = 0;
+                    p0 = p1;
+                    ++blk;
+                    p1 = page_of(blk + 1);
+                }
+            } else {
+                next_tile();
+                const int pb = second ? p0 : -1;
+                bits = (pa >= 0 ? 1u : 0u) | (pb >= 0 ? 2u : 0u);
+                if (lane == 0) {
+                    mbar_expect_tx(bar, ((pa >= 0) + (pb >= 0)) * kTile + p.extra_tx);
+                    if (pa >= 0)
+                        bulk_g2s(dst, src, kTile, bar);
+                    if (pb >= 0)
+                        bulk_g2s(dst + kTile, head + (uint64_t)(uint32_t)pb * (uint32_t)page_bytes + (uint32_t)tin * kTile,
+                                 kTile, bar);
+                }
+                next_tile();
             }
+            there = (there & ~(3u << (2 * st_fill))) | bits << (2 * st_fill);
             st_fill = st_fill + 1 == R ? 0 : st_fill + 1;
         };
 #pragma unroll
@@ -423,6 +448,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kKv4Least;
             l[nt][0] = l[nt][1] = 0.f;
+            less[nt] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int t = 0; t < D / 16; ++t)
                 o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
@@ -487,12 +513,18 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
                             mma_f16(x[nt][j], a, q.b[nt][2 * w + t][0], q.b[nt][2 * w + t][1]);
                     }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[nt][j][e] *= q.mul[nt][e & 1];
             }
+            // powers of two less the reference, which p = 2^8 stands for
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(x[nt][j][e], x[nt][j][e + 1]), q.mul[nt], less[nt]);
+                        x[nt][j][e] = y.x;
+                        x[nt][j][e + 1] = y.y;
+                    }
             if (!whole) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -504,32 +536,44 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
                                 x[nt][j][e] = kKv4Least;
             }
             // a new reference where a score has left the old one's range
-            bool far = false;
+            float top = kKv4Least;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    far |= fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2])) >
-                           m[nt][e] + 7.f;
+                for (int e = 0; e < 4; ++e)
+                    top = fmaxf(top, fmaxf(x[nt][0][e], x[nt][1][e]));
+            bool far = top > 15.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)                     // a row without one: its first scores
+                far |= m[nt][0] == kKv4Least || m[nt][1] == kKv4Least;
             if (__any_sync(0xFFFFFFFFu, far)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float n = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1)
                             n = fmaxf(n, __shfl_xor_sync(0xFFFFFFFFu, n, d));
-                        n = fmaxf(n, m[nt][e]);
-                        const float f = n == kKv4Least ? 1.f : exp2_of(m[nt][e] - n);
-                        m[nt][e] = n;
+                        // the scores are relative to what was taken off
+                        const float off = e ? less[nt].y : less[nt].x, was = m[nt][e], now = fmaxf(was, n - off);
+                        const float f = now == kKv4Least ? 1.f : exp2_of(was - now);
+                        const float take = now == kKv4Least ? off : 8.f - now, by = take - off;
+                        m[nt][e] = now;
+                        (e ? less[nt].y : less[nt].x) = take;
                         l[nt][e] *= f;
 #pragma unroll
                         for (int t = 0; t < D / 16; ++t) {
                             o[nt][t][e] *= f;
                             o[nt][t][e + 2] *= f;
                         }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            x[nt][j][e] += by;
+                            x[nt][j][e + 2] += by;
+                        }
                     }
+                }
             }
             // p, transposed for the second product. One rounding to fp16 is
             // as large as an fp16 output's own: there a second half holds what
@@ -537,15 +581,14 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
             uint32_t pb[NT][2][2], pl[kLow ? NT : 1][2][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float b0 = m[nt][0] == kKv4Least ? 0.f : m[nt][0] - 8.f;
-                const float b1 = m[nt][1] == kKv4Least ? 0.f : m[nt][1] - 8.f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float x0 = exp2_of(x[nt][j][2 * e] - b0), x1 = exp2_of(x[nt][j][2 * e + 1] - b1);
-                        l[nt][0] += x0;
-                        l[nt][1] += x1;
+                        const float x0 = exp2_of(x[nt][j][2 * e]), x1 = exp2_of(x[nt][j][2 * e + 1]);
+                        const float2 sum = __fadd2_rn(make_float2(l[nt][0], l[nt][1]), make_float2(x0, x1));
+                        l[nt][0] = sum.x;
+                        l[nt][1] = sum.y;
                         const uint32_t hi = Half16<f16>::narrow2(x0, x1);
                         pb[nt][j][e] = movmatrix(hi);
                         if constexpr (kLow) {
@@ -681,7 +724,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
     g = kv4_segment(s, first, cta0);
     const bool all = cta0 <= g.at && cta1 == g.at + s.stages;
     const float gv = p.vscale ? __ldg(p.vscale + g.h) : 1.f;
-    float *part = p.ws + kv4_part((int64_t)blockIdx.x * kKv4Warps, false) * kv4_partial(D, NT);
+    float *part = p.ws + kv4_part(blockIdx.x * kKv4Warps, false) * kv4_partial(D, NT);
     for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += kKv4Warps * 32) {
         const int n = k / (D / 4), d = (k - n * (D / 4)) * 4;
         float mm = kKv4Least, ll = 0.f;
@@ -727,22 +770,24 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     // the sequence of this segment, and the entries before it
-    int64_t segs = 0, entries = 0, seg = -1, first = 0;
+    uint32_t segs = 0, entries = 0, seg = 0, first = 0;
+    bool found = false;
     Kv4Seq s = {};
     for (int base = 0; base < p.B; base += 32) {
         const Kv4Seq t = base + lane < p.B ? kv4_seq<NT>(p, base + lane) : Kv4Seq{};
-        const int64_t n = (int64_t)t.tiles * p.Hk, v = base + lane < p.B ? t.total(p.Hk) : 0;
-        int64_t sn = n, sv = v;
+        const uint32_t n = (uint32_t)t.tiles * p.Hk, v = base + lane < p.B ? t.total(p.Hk) : 0;
+        uint32_t sn = n, sv = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t a = __shfl_up_sync(0xFFFFFFFFu, sn, o), b = __shfl_up_sync(0xFFFFFFFFu, sv, o);
+            const uint32_t a = __shfl_up_sync(0xFFFFFFFFu, sn, o), b = __shfl_up_sync(0xFFFFFFFFu, sv, o);
             if (lane >= o) {
                 sn += a;
                 sv += b;
             }
         }
         const unsigned at = __ballot_sync(0xFFFFFFFFu, segs + sn > blockIdx.x);
-        if (at && seg < 0) {
+        if (at && !found) {
+            found = true;
             const int l = __ffs(at) - 1;
             seg = blockIdx.x - (segs + __shfl_sync(0xFFFFFFFFu, sn - n, l));
             first = entries + __shfl_sync(0xFFFFFFFFu, sv - v, l);
@@ -754,17 +799,17 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
         segs += __shfl_sync(0xFFFFFFFFu, sn, 31);
         entries += __shfl_sync(0xFFFFFFFFu, sv, 31);
     }
-    if (seg < 0 || s.stages == 0)
+    if (!found || s.stages == 0)
         return;
-    const int64_t C = (entries + (int64_t)ctas * kKv4Warps - 1) / ((int64_t)ctas * kKv4Warps);
-    const int64_t start = first + seg * s.cost(), end = start + s.cost();
-    const int64_t w0 = (start + 1) / C, w1 = (end - 1) / C;      // the warps that have stages of it
+    const uint32_t warps = ctas * kKv4Warps, C = (entries + warps - 1) / warps;
+    const uint32_t start = first + seg * s.cost(), end = start + s.cost();
+    const uint32_t w0 = (start + 1) / C, w1 = (end - 1) / C;      // the warps that have stages of it
     if (w0 == w1)
         return;                                                 // one warp had all of it
-    const int64_t c0 = w0 / kKv4Warps, c1 = w1 / kKv4Warps;
+    const uint32_t c0 = w0 / kKv4Warps, c1 = w1 / kKv4Warps;
     // CTAs whose runs all lie in the segment have one part; only the first and
     // the last may have others
-    auto inside = [&](int64_t cta) {
+    auto inside = [&](uint32_t cta) {
         return cta * kKv4Warps * C >= start && min((cta + 1) * kKv4Warps * C, entries) <= end;
     };
     const bool in0 = inside(c0), in1 = inside(c1);
@@ -774,7 +819,7 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
     const int n1 = c0 == c1 ? 0 : (in1 ? 1 : (int)(w1 - c1 * kKv4Warps + 1));
     const int parts = n0 + n1 + (c0 == c1 ? 0 : (int)(c1 - c0 - 1));
     auto part_at = [&](int i) {
-        int64_t w;
+        uint32_t w;
         if (i < n0)
             w = in0 ? c0 * kKv4Warps : w0 + i;
         else if (i < parts - n1)
@@ -791,18 +836,18 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
             continue;
         float mm = kKv4Least, ll = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < parts; i += 4) {
-            float m[4], l[4];
-            float4 v[4];
+        for (int i = 0; i < parts; i += 8) {
+            float m[8], l[8];
+            float4 v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float *part = part_at(min(i + j, parts - 1));
                 m[j] = i + j < parts ? __ldcg(part + 8 * NT * D + n) : kKv4Least;
                 l[j] = __ldcg(part + 8 * NT * (D + 1) + n);
                 v[j] = __ldcg(reinterpret_cast<const float4 *>(part + n * D + d));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 if (m[j] == kKv4Least)
                     continue;
                 const float up = fmaxf(mm, m[j]);
