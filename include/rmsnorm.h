@@ -709,8 +709,9 @@ void rmsnorm_set_gemm_fp8_test(int path);
 
 /*
  * Test hook, process-wide, not thread-safe against concurrent calls: later
- * rmsnorm_kv4_attention calls run the kernel for few rows a sequence (1) or,
- * where q_starts is given, the one for pieces of prompts (2) at any size.
+ * rmsnorm_kv4_attention calls run the kernel for few rows a sequence with its
+ * work list (1), or by clusters where the segments are few enough (3), or,
+ * where q_starts is given, the one for pieces of prompts (2), at any size.
  * Other values restore the choice by size.
  */
 void rmsnorm_set_kv4_test(int kernel);

@@ -131,10 +131,12 @@ struct Kv4Params {
     float scale;
     int vec;                   // q and out rows start at 16 bytes
     float *ws;                 // partial results, two a warp
+    int cluster;               // CTAs that share a segment; 0: the list
     uint32_t extra_tx, wait_limit_us;
     unsigned int *timeouts;
 };
 
+constexpr int kKv4Cluster = 8;             // most CTAs to a segment
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Slot = 32;               // tokens a stage
 // Shared memory of a CTA: the warps' rings, then their mbarriers.

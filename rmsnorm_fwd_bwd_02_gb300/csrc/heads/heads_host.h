@@ -63,19 +63,25 @@ inline bool dtype_ok(int dtype)
 
 inline bool index_bits_ok(int bits) { return bits == 32 || bits == 64; }
 
-// A launch that may begin while the kernel before it ends.
-inline cudaError_t launch_pdl(const void *fn, dim3 grid, int threads, size_t smem, cudaStream_t s, void **args)
+// A launch that may begin while the kernel before it ends, of clusters of
+// `cluster` CTAs.
+inline cudaError_t launch_pdl(const void *fn, dim3 grid, int threads, size_t smem, cudaStream_t s, void **args,
+                              int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

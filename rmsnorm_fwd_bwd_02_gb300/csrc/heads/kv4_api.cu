@@ -11,6 +11,8 @@ namespace {
 
 constexpr int kPathKv4Attend = 16, kPathKv4Prompt = 17;
 
+constexpr int kClusterStages = 8;        // most stages a warp in clusters (see below)
+
 // Test hook: the kernel (see rmsnorm.h).
 std::atomic<int> g_test_kv4{0};
 
@@ -104,7 +106,7 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
                                                     T > 1 ? out_token : 0, heads > 1 ? out_head : 0})
                        ? 1
                        : 0,
-                   static_cast<float *>(workspace), g_test_extra_tx.load(std::memory_order_relaxed),
+                   static_cast<float *>(workspace), 0, g_test_extra_tx.load(std::memory_order_relaxed),
                    g_test_wait_us.load(std::memory_order_relaxed), tmo};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Pieces of prompts: as many rows a sequence as half fill a CTA's, and
@@ -136,7 +138,35 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
         return st;
     int ctas = sms * std::min(bps, kv4_ctas_per_sm(NT));
     void *args[1] = {&p};
-    cudaError_t e = launch_pdl(fn, dim3((unsigned)ctas), kKv4Warps * 32, (size_t)smem, s, args);
+    cudaError_t e;
+    // A cluster a segment, the largest with which all run at once, where a
+    // warp then has few stages. Measured (GB300, 32 heads of 128 on 8, all
+    // lengths alike, list / clusters): one sequence of 64 tokens 7.9 / 4.3 us,
+    // 4096 12.7 / 8.3, 16384 (8 stages a warp) 20.0 / 15.2, 65536 (32) 27 / 42;
+    // 16 of 4096 (8) 24.4 / 21.4, of 16384 (32) 61 / 66; 32 of 4096 (16) 40.9 /
+    // 36.4, of 16384 (64) 110 / 120. Lengths that differ favour the list,
+    // which is even whatever they are.
+    const int64_t segs = tiles * kv_heads, stages = (blocks * page_size + kKv4Slot - 1) / kKv4Slot;
+    if (ov != 1 && segs <= ctas) {
+        int cs = kKv4Cluster, n = 0;
+        for (; cs > 1; cs /= 2) {
+            if (stages <= (int64_t)(cs / 2) * kKv4Warps)
+                continue;                                       // half as many would have a stage a warp
+            if ((st = max_active_clusters(fn, kKv4Warps * 32, smem, cs, dev, &n)))
+                return st;
+            if (segs <= n)
+                break;
+        }
+        if (ov == 3 || stages <= cs * kKv4Warps * kClusterStages) {
+            p.cluster = cs;
+            e = launch_pdl(fn, dim3((unsigned)(segs * cs)), kKv4Warps * 32, (size_t)smem, s, args, cs);
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+            t_last_path = kPathKv4Attend;
+            return RMSNORM_OK;
+        }
+    }
+    e = launch_pdl(fn, dim3((unsigned)ctas), kKv4Warps * 32, (size_t)smem, s, args);
     if (e != cudaSuccess)
         return cuda_fail(e);
     // the parts of segments that were split; none is, where one stage covers any length

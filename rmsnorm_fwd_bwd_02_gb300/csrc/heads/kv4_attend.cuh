@@ -47,9 +47,13 @@
 // will and a captured call replays with others. A warp that has the whole of
 // a segment writes its output. A CTA whose eight runs lie in one segment joins
 // their sums in shared memory; what is still a part of a segment goes to the
-// workspace, and kv4_combine joins a segment's parts in their order.
+// workspace, and kv4_combine joins a segment's parts in their order. Where the
+// segments are few and short enough to run at once, each gets a cluster of
+// CTAs instead, which joins its sums through distributed shared memory: one
+// launch, no workspace.
 #pragma once
 
+#include "../split.cuh"
 #include "../stream.cuh"
 #include "rope.cuh"
 
@@ -183,6 +187,33 @@ struct Kv4List {
         }
     }
 };
+
+// The sequence of segment `id` of the call (a sequence's segments side by
+// side), and the segment within it; -1: there is none.
+template <int NT>
+__device__ __forceinline__ int kv4_segment_of(const Kv4Params &p, uint32_t id, uint32_t &seg)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t before = 0;
+    for (int base = 0; base < p.B; base += 32) {
+        const uint32_t n = base + lane < p.B ? (uint32_t)kv4_seq<NT>(p, base + lane).tiles * p.Hk : 0;
+        uint32_t sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o)
+                sum += t;
+        }
+        const unsigned at = __ballot_sync(0xFFFFFFFFu, before + sum > id);
+        if (at) {
+            const int l = __ffs(at) - 1;
+            seg = id - before - __shfl_sync(0xFFFFFFFFu, sum - n, l);
+            return base + l;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    return -1;
+}
 
 // A segment in the list: its first entry stands for what it costs besides, its
 // stages follow.
@@ -332,23 +363,45 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
     griddep_wait();
     griddep_launch_dependents();
 
+    // The list, or a segment for each cluster of CTAs, whose warps have equal
+    // runs of its stages (its own list: an entry besides, then the stages).
     Kv4List list = {};
-    list.init<NT>(p);
-    const uint32_t warps = gridDim.x * kKv4Warps, C = (list.total + warps - 1) / warps;
-    // (unsigned sums below 2^31 + 2^12 each)
-    const uint32_t cta0 = min(blockIdx.x * kKv4Warps * C, list.total), cta1 = min(cta0 + kKv4Warps * C, list.total);
-    if (cta0 >= cta1)
-        return;                                                 // for the whole CTA
+    uint32_t cta0 = 0, cta1 = 0, run0, run1, first = 0;
     const uint32_t gw = blockIdx.x * kKv4Warps + warp;
-    const uint32_t run0 = min(gw * C, list.total), run1 = min(run0 + C, list.total);
-    uint32_t first;
-    int seq = list.find<NT>(p, cta0, first);
-    if (seq < 0)
-        return;
-    Kv4Seq s = kv4_seq<NT>(p, seq);
-    // whether the CTA's runs lie in one segment
-    Kv4Segment g = kv4_segment(s, first, cta0);
-    const bool joined = cta1 <= g.at + s.stages;
+    int seq;
+    Kv4Seq s;
+    Kv4Segment g;
+    bool joined = true;
+    if (p.cluster) {
+        uint32_t seg;
+        seq = kv4_segment_of<NT>(p, blockIdx.x / p.cluster, seg);
+        if (seq < 0)
+            return;                                             // for the whole cluster
+        s = kv4_seq<NT>(p, seq);
+        g.h = (int)(seg / (uint32_t)s.tiles);
+        g.tile = (int)seg - g.h * s.tiles;
+        g.at = 1;
+        const uint32_t n = (uint32_t)p.cluster * kKv4Warps, each = ((uint32_t)s.stages + n - 1) / n;
+        run0 = 1 + min((blockIdx.x % p.cluster * kKv4Warps + warp) * each, (uint32_t)s.stages);
+        run1 = min(run0 + each, 1 + (uint32_t)s.stages);
+    } else {
+        list.init<NT>(p);
+        const uint32_t warps = gridDim.x * kKv4Warps, C = (list.total + warps - 1) / warps;
+        // (unsigned sums below 2^31 + 2^15 each)
+        cta0 = min(blockIdx.x * kKv4Warps * C, list.total);
+        cta1 = min(cta0 + kKv4Warps * C, list.total);
+        if (cta0 >= cta1)
+            return;                                             // for the whole CTA
+        run0 = min(gw * C, list.total);
+        run1 = min(run0 + C, list.total);
+        seq = list.find<NT>(p, cta0, first);
+        if (seq < 0)
+            return;
+        s = kv4_seq<NT>(p, seq);
+        // whether the CTA's runs lie in one segment
+        g = kv4_segment(s, first, cta0);
+        joined = cta1 <= g.at + s.stages;
+    }
     const unsigned long long limit = wait_limit_ns(p.wait_limit_us);
     uint32_t st_fill = 0, st_use = 0, phase = 0;                // stages of the ring; a phase bit for each
     bool ok = true;
@@ -361,15 +414,17 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         m[nt][0] = m[nt][1] = kKv4Least;
 
     for (uint32_t u = run0; u < run1 && ok;) {
-        if (u >= first + s.total(p.Hk)) {
-            seq = list.find<NT>(p, u, first);
-            if (seq < 0)
-                break;
-            s = kv4_seq<NT>(p, seq);
+        if (p.cluster == 0) {
+            if (u >= first + s.total(p.Hk)) {
+                seq = list.find<NT>(p, u, first);
+                if (seq < 0)
+                    break;
+                s = kv4_seq<NT>(p, seq);
+            }
+            g = kv4_segment(s, first, u);
         }
-        g = kv4_segment(s, first, u);
         if ((unsigned)g.h >= (unsigned)p.Hk)
-            break;
+            break;                                              // lengths that change under the call
         const int from = u > g.at ? (int)(u - g.at) : 0;        // this run's stages
         const int to = run1 > g.at ? min(s.stages, (int)(run1 - g.at)) : 0;
         u = g.at + s.stages;                                    // the next segment
@@ -719,45 +774,123 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
                         make_float4(o[nt][t][e], o[nt][t][e + 2], o[nt][t + 1][e], o[nt][t + 1][e + 2]);
         }
     __syncthreads();
-    if (sm_bad)
+    const bool several = p.cluster > 1;
+    if (sm_bad && !several)
         return;
-    g = kv4_segment(s, first, cta0);
-    const bool all = cta0 <= g.at && cta1 == g.at + s.stages;
+    if (p.cluster == 0)
+        g = kv4_segment(s, first, cta0);
+    const bool all = p.cluster > 0 || (cta0 <= g.at && cta1 == g.at + s.stages);
     const float gv = p.vscale ? __ldg(p.vscale + g.h) : 1.f;
     float *part = p.ws + kv4_part(blockIdx.x * kKv4Warps, false) * kv4_partial(D, NT);
-    for (int k = threadIdx.x; k < 8 * NT * (D / 4); k += kKv4Warps * 32) {
-        const int n = k / (D / 4), d = (k - n * (D / 4)) * 4;
-        float mm = kKv4Least, ll = 0.f;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto write = [&](int n, int d, float4 a, float mm, float ll) {
+        const int qrow = g.tile * 8 * NT + n;
+        if (qrow >= s.n * p.G)
+            return;
+        const int i = qrow / p.G, hq = g.h * p.G + qrow - i * p.G;
+        const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
+        kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
+        if (d == 0 && p.lse != nullptr)
+            p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] = kv4_lse(mm, ll);
+    };
+    constexpr int kItems = 8 * NT * (D / 4), kThreads = kKv4Warps * 32, kEach = (kItems + kThreads - 1) / kThreads;
+    float4 a[kEach];
+    float mm[kEach], ll[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int k = threadIdx.x + i * kThreads, n = k / (D / 4), d = (k - n * (D / 4)) * 4;
+        mm[i] = kKv4Least;
+        ll[i] = 0.f;
+        a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k >= kItems)
+            continue;
 #pragma unroll
         for (int w = 0; w < kKv4Warps; ++w)
-            mm = fmaxf(mm, sm_m[w][n]);
+            mm[i] = fmaxf(mm[i], sm_m[w][n]);
 #pragma unroll
         for (int w = 0; w < kKv4Warps; ++w) {
             if (sm_m[w][n] == kKv4Least)
                 continue;
-            const float f = exp2_of(sm_m[w][n] - mm);
+            const float f = exp2_of(sm_m[w][n] - mm[i]);
             const float4 v = *reinterpret_cast<const float4 *>(
                 reinterpret_cast<const float *>(smem + w * R * kSlot) + n * kRow + d);
-            ll = fmaf(f, sm_l[w][n], ll);
-            a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
-            a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
+            ll[i] = fmaf(f, sm_l[w][n], ll[i]);
+            a[i].x = fmaf(f, v.x, a[i].x); a[i].y = fmaf(f, v.y, a[i].y);
+            a[i].z = fmaf(f, v.z, a[i].z); a[i].w = fmaf(f, v.w, a[i].w);
         }
-        const int qrow = g.tile * 8 * NT + n;
-        if (!all) {
-            *reinterpret_cast<float4 *>(part + n * D + d) = a;
+        if (several)
+            continue;
+        if (all) {
+            write(n, d, a[i], mm[i], ll[i]);
+        } else {
+            *reinterpret_cast<float4 *>(part + n * D + d) = a[i];
             if (d == 0) {
-                part[8 * NT * D + n] = mm;
-                part[8 * NT * (D + 1) + n] = ll;
+                part[8 * NT * D + n] = mm[i];
+                part[8 * NT * (D + 1) + n] = ll[i];
             }
-        } else if (qrow < s.n * p.G) {
-            const int i = qrow / p.G, hq = g.h * p.G + qrow - i * p.G;
-            const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
-            kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));
-            if (d == 0 && p.lse != nullptr)
-                p.lse[(int64_t)(s.q0 + i) * p.Hk * p.G + hq] = kv4_lse(mm, ll);
         }
     }
+    if (!several)
+        return;
+
+    // join the cluster's sums: each CTA leaves its own where the first warp's
+    // were and adds up its share of the rows' features, in rank order, out of
+    // its peers' shared memory
+    __syncthreads();
+    float *mine = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int k = threadIdx.x + i * kThreads, n = k / (D / 4), d = (k - n * (D / 4)) * 4;
+        if (k < kItems) {
+            *reinterpret_cast<float4 *>(mine + n * kRow + d) = a[i];
+            if (d == 0) {
+                sm_m[0][n] = mm[i];
+                sm_l[0][n] = ll[i];
+            }
+        }
+    }
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    const int share = kItems / p.cluster;
+    const uint32_t rank = blockIdx.x % p.cluster;
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+        const int k = rank * share + i, n = k / (D / 4), d = (k - n * (D / 4)) * 4;
+        float pm[kKv4Cluster], pll[kKv4Cluster], top = kKv4Least, sum = 0.f;
+        float4 v[kKv4Cluster], out = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint32_t failed = 0;
+#pragma unroll
+        for (int r2 = 0; r2 < kKv4Cluster; ++r2) {
+            pm[r2] = kKv4Least;
+            if (r2 < p.cluster) {
+                const uint32_t at = cluster_map(smem_addr(mine + n * kRow + d), r2);
+                pm[r2] = ld_cluster_f32(&sm_m[0][n], r2);
+                pll[r2] = ld_cluster_f32(&sm_l[0][n], r2);
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(v[r2].x), "=f"(v[r2].y), "=f"(v[r2].z), "=f"(v[r2].w)
+                             : "r"(at)
+                             : "memory");
+                uint32_t f;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f) : "r"(cluster_map(smem_addr(&sm_bad), r2)) : "memory");
+                failed |= f;
+            }
+        }
+#pragma unroll
+        for (int r2 = 0; r2 < kKv4Cluster; ++r2)
+            top = fmaxf(top, pm[r2]);
+#pragma unroll
+        for (int r2 = 0; r2 < kKv4Cluster; ++r2) {
+            if (pm[r2] == kKv4Least)
+                continue;
+            const float f = exp2_of(pm[r2] - top);
+            sum = fmaf(f, pll[r2], sum);
+            out.x = fmaf(f, v[r2].x, out.x); out.y = fmaf(f, v[r2].y, out.y);
+            out.z = fmaf(f, v[r2].z, out.z); out.w = fmaf(f, v[r2].w, out.w);
+        }
+        if (!failed)
+            write(n, d, out, top, sum);
+    }
+    // no CTA leaves while a peer may still read from it
+    cluster_arrive_release();
+    cluster_wait_acquire();
 }
 
 // Joins the parts of the segments that several warps or CTAs worked on, in the

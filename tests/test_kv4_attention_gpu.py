@@ -23,7 +23,7 @@ from tests.test_rope_gpu import BF16, DEV, F16, F32, F64, check_fwd, freqs, norm
 
 pytestmark = pytest.mark.gpu
 
-PATHS = {1: rn.PATH_KV4_ATTENTION, 2: rn.PATH_KV4_PROMPT}
+PATHS = {1: rn.PATH_KV4_ATTENTION, 3: rn.PATH_KV4_ATTENTION, 2: rn.PATH_KV4_PROMPT}
 HALF = {BF16: 2.0 ** -8, F16: 2.0 ** -11}
 TINY = {BF16: 2.0 ** -134, F16: 2.0 ** -25}
 
@@ -116,8 +116,15 @@ def table_of(B, blocks, pages, seed):
     return torch.randperm(pages, generator=g)[:B * blocks].to(torch.int32).view(B, blocks)
 
 
-@pytest.fixture(params=[1, 2], ids=["few", "prompt"])
+@pytest.fixture(params=[1, 3, 2], ids=["list", "clusters", "prompt"])
 def kernel(request):
+    rn.set_kv4_test(request.param)
+    yield request.param
+    rn.set_kv4_test(0)
+
+
+@pytest.fixture(params=[1, 3], ids=["list", "clusters"])
+def few(request):
     rn.set_kv4_test(request.param)
     yield request.param
     rn.set_kv4_test(0)
@@ -137,7 +144,7 @@ def run(T, H, D, dtype, cache, table, lens, starts=None, seed=5, path=None, **kw
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hk,G", [(1, 1), (2, 7), (8, 4), (2, 9), (1, 40)])
-def test_one_token(dtype, D, Hk, G):
+def test_one_token(dtype, D, Hk, G, few):
     page = 16 if G % 2 else 48
     lens = [1, 0, 15, 16, 17, 31, 32, 33, 255, 256, 257, 300, 513, 767]
     B, blocks = len(lens), -(-768 // page)
@@ -161,7 +168,7 @@ def test_several_tokens(dtype, D, Hk, G, counts, kernel):
         path=PATHS[kernel])
 
 
-def test_long_and_one_unit():
+def test_long_and_one_unit(few):
     """A length that every CTA has a part of; and a table of one unit, where
     nothing is joined."""
     page = 64
@@ -172,7 +179,7 @@ def test_long_and_one_unit():
     run(3, 8, 128, F16, cache, table_of(3, 0, 640, 1).view(3, 0), [0, 5, -3])
 
 
-def test_many_sequences():
+def test_many_sequences(few):
     B, page, blocks = 333, 16, 5
     cache = make_cache(B * blocks, 1, page, 64, 2)
     g = torch.Generator().manual_seed(9)
@@ -180,7 +187,7 @@ def test_many_sequences():
     run(B, 3, 64, BF16, cache, table_of(B, blocks, B * blocks, 6), lens)
 
 
-def test_scales_and_softmax_scale():
+def test_scales_and_softmax_scale(few):
     Hk, G, D, page = 3, 2, 64, 16
     ks, vs = torch.tensor([0.5, 3.0, 1e-3], device=DEV), torch.tensor([2.0, 1e-4, 7.0], device=DEV)
     cache = rn.kv4_cache(20, Hk, page, D, device=DEV)
@@ -190,7 +197,7 @@ def test_scales_and_softmax_scale():
         run(2, Hk * G, D, BF16, cache, table_of(2, 10, 20, 2), [150, 77], k_scale=ks, v_scale=vs, scale=scale)
 
 
-def test_peaked_and_shifted_scores():
+def test_peaked_and_shifted_scores(few):
     """Scores that grow along the sequence (the reference moves again and
     again), and ones far from zero."""
     D, page = 128, 16
@@ -260,7 +267,7 @@ def test_rows_of_no_sequence_and_unsound_starts(kernel):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-def test_layouts(dtype):
+def test_layouts(dtype, few):
     """Windows of a fused projection, head-major and unaligned q and out; a
     table with a row stride."""
     D, page, Hk, G, B = 64, 16, 2, 3, 5
@@ -281,7 +288,7 @@ def test_layouts(dtype):
         assert torch.equal(got, out)
 
 
-def test_magnitudes_of_q():
+def test_magnitudes_of_q(few):
     """Rows scaled by any power of two within the type; zeros."""
     D, page = 128, 16
     cache = make_cache(8, 1, page, D, 3)
@@ -298,7 +305,7 @@ def test_magnitudes_of_q():
     check(out, lse, q, cache, table, [111], None, scale=2.0 ** -63)
 
 
-def test_long_offsets():
+def test_long_offsets(few):
     """Pages whose byte offset passes 2^32."""
     D, page, Hk = 128, 64, 8
     pages = (1 << 32) // (Hk * page * 9 * D // 8) + 40
@@ -320,7 +327,7 @@ def test_long_offsets():
     assert torch.equal(rv.view(torch.uint8), sv.view(torch.uint8))
 
 
-def test_repeats_and_captured_calls():
+def test_repeats_and_captured_calls(few):
     """The same bits again; two captured graphs, replayed in turn with other
     lengths, tables and queries."""
     D, page, Hk, G, B = 128, 16, 2, 4, 3
@@ -353,7 +360,7 @@ def test_repeats_and_captured_calls():
     check(outs[0], None, qs[0], cache, tables[0].cpu(), [5, 1300, 1599], None)
 
 
-def test_two_streams_at_once():
+def test_two_streams_at_once(few):
     D, page, Hk = 128, 16, 2
     cache = make_cache(400, Hk, page, D, 3)
     q = [normal((4, 8, D), BF16, i) for i in range(2)]
