@@ -109,12 +109,16 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
                    static_cast<float *>(workspace), 0, g_test_extra_tx.load(std::memory_order_relaxed),
                    g_test_wait_us.load(std::memory_order_relaxed), tmo};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Pieces of prompts: as many rows a sequence as half fill a CTA's, and
-    // enough CTAs for most SMs; the other kernel splits long sequences, which
-    // this one does not.
-    const int64_t wide = q_starts ? T * G / kv4_prompt_kernels.rows * kv_heads : 0;
+    // Pieces of prompts. For 128 tokens of every sequence the kernel for few
+    // rows takes 0.4 ns a row and key head (0.3 with heads of 64), the one for
+    // many 1.75 us for each time that its CTAs of 256 rows fill the SMs, however
+    // few they are; both grow with the lengths alike. Measured (GB300, 32 heads
+    // of 128 on 8): 1 x 128 tokens over 8192 87 / 120 us, 1 x 256 160 / 121; 4 x
+    // 32 over 4096 52 / 65, 4 x 64 89 / 70; 16 x 16 over 2048 54 / 39; 14 heads of
+    // 64 on 2: 4 x 64 over 4096 36 / 56, 4 x 256 121 / 58, 16 x 64 over 2048 69 / 35.
+    const int64_t wide = B * ((rows + kv4_prompt_kernels.rows - 1) / kv4_prompt_kernels.rows) * kv_heads;
     const int ov = g_test_kv4.load(std::memory_order_relaxed);
-    if (q_starts && (ov == 2 || (ov == 0 && rows * 2 >= kv4_prompt_kernels.rows && wide * 2 >= sms))) {
+    if (q_starts && (ov == 2 || (ov == 0 && T * heads >= (D == 128 ? 4400 : 5800) * ((wide + sms - 1) / sms)))) {
         const void *fn = kv4_prompt_kernels.fn[ti][di];
         int bps;
         if ((st = blocks_per_sm(fn, kv4_prompt_kernels.threads, dev, &bps, kv4_prompt_kernels.smem[di])))

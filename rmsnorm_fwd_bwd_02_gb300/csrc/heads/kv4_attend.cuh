@@ -257,10 +257,11 @@ __device__ __forceinline__ float exp2_of(float x)
     return y;
 }
 
-// log sum exp of a row from its reference and denominator.
-__device__ __forceinline__ float kv4_lse(float m, float l)
+// log sum exp of a row from its reference m, which 2^base stands for, and
+// denominator.
+__device__ __forceinline__ float kv4_lse(float m, float l, float base = 8.f)
 {
-    return l > 0.f ? (m - 8.f + log2f(l)) * 0.69314718055994531f : (l != l ? l : kKv4Least);
+    return l > 0.f ? (m - base + log2f(l)) * 0.69314718055994531f : (l != l ? l : kKv4Least);
 }
 
 // What the rows of one tile of a segment share, in each lane.

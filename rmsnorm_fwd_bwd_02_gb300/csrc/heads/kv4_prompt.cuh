@@ -37,6 +37,10 @@
 
 namespace rmsk {
 
+// p = 2^(x - m + kPromptBase), and a reference holds up to x = m + kPromptRoom,
+// p = 2^15. A wider room than the other kernel's 8 and 7: a tile that passes it
+// is done twice, for all of its warp's rows.
+constexpr float kPromptBase = 4.f, kPromptRoom = 11.f;
 constexpr int kPromptRows = 256, kPromptTokens = 128, kPromptThreads = 13 * 32;
 
 // Shared memory: q of both tiles, keys and values (two in turn each), then the
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
             // tiles do not pass it
             bool far = m == kKv4Least || !whole;
             if (!__any_sync(0xFFFFFFFFu, far)) {
-                const float2 mul2 = make_float2(mul, mul), b2 = make_float2(8.f - m, 8.f - m);
+                const float2 mul2 = make_float2(mul, mul), b2 = make_float2(kPromptBase - m, kPromptBase - m);
                 float2 sum = make_float2(0.f, 0.f);
                 uint32_t top = 0, w[64];                        // packed p; positive halves compare as integers
 #pragma unroll
@@ -325,19 +329,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                     tmem_put32(ts + 32, w + 32);
                 }
             }
-            if (__any_sync(0xFFFFFFFFu, far)) {
-                // a new reference for the rows that want one, and p again
-                float x[32], mx = kKv4Least, f = 1.f;
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    tmem_ld32(ts + 32 * ch, x);
+            // a new reference for the rows that want one, and p again
+            auto again = [&](auto masked) {
+                constexpr bool kMasked = decltype(masked)::value;
+                float mx = kKv4Least, f = 1.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (seen(32 * ch + i))
-                            mx = fmaxf(mx, x[i]);
+                for (int ch = 0; ch < 4; ++ch) {
+                    float x[32];
+                    tmem_ld32(ts + 32 * ch, x);
+                    float a = kKv4Least, b = kKv4Least;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        if (!kMasked || seen(32 * ch + i))
+                            a = fmaxf(a, x[i]);
+                        if (!kMasked || seen(32 * ch + i + 1))
+                            b = fmaxf(b, x[i + 1]);
+                    }
+                    mx = fmaxf(mx, fmaxf(a, b));
                 }
                 const float top = mx == kKv4Least ? kKv4Least : mx * mul;
-                if (top > m + 7.f) {
+                if (top > m + kPromptRoom) {
                     f = exp2_of(m - top);
                     m = top;
                     l *= f;
@@ -345,6 +356,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                 if (j > 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
+                        float x[32];
                         tmem_ld32(to + 32 * ch, x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -352,24 +364,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                         tmem_st32(to + 32 * ch, x);
                     }
                 }
-                const float b = m == kKv4Least ? 0.f : m - 8.f;
+                const float2 mul2 = make_float2(mul, mul);
+                const float2 b2 = m == kKv4Least ? make_float2(0.f, 0.f)
+                                                 : make_float2(kPromptBase - m, kPromptBase - m);
+                float2 sum = make_float2(0.f, 0.f);
                 // (a chunk's p takes columns of scores that have been read)
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ch += 2) {
                     uint32_t w[32];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
+                        float x[32];
                         tmem_ld32(ts + 32 * (ch + k), x);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            x[i] = seen(32 * (ch + k) + i) ? exp2_of(fmaf(x[i], mul, -b)) : 0.f;
-                            x[i + 1] = seen(32 * (ch + k) + i + 1) ? exp2_of(fmaf(x[i + 1], mul, -b)) : 0.f;
-                            l += x[i] + x[i + 1];
-                            w[16 * k + i / 2] = Half16<f16>::narrow2(x[i], x[i + 1]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), mul2, b2);
+                            float2 e = make_float2(exp2_of(y.x), exp2_of(y.y));
+                            if (kMasked) {
+                                e.x = seen(32 * (ch + k) + 2 * i) ? e.x : 0.f;
+                                e.y = seen(32 * (ch + k) + 2 * i + 1) ? e.y : 0.f;
+                            }
+                            sum = __fadd2_rn(sum, e);
+                            w[16 * k + i] = Half16<f16>::narrow2(e.x, e.y);
                         }
                     }
                     tmem_put32(ts + 16 * ch, w);
                 }
+                l += sum.x + sum.y;
+            };
+            if (__any_sync(0xFFFFFFFFu, far)) {
+                if (whole)
+                    again(std::false_type{});
+                else
+                    again(std::true_type{});
             }
             tmem_put_wait();
             tc_fence_before_sync();
@@ -394,7 +421,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
                                               : make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f));
             }
             if (real && p.lse != nullptr)
-                p.lse[(int64_t)(s.q0 + row_i) * p.Hk * p.G + row_h] = kv4_lse(m, l);
+                p.lse[(int64_t)(s.q0 + row_i) * p.Hk * p.G + row_h] = kv4_lse(m, l, kPromptBase);
         }
     } else if (warp < 12) {
         // ------------------------------------------------ keys and values
