@@ -357,31 +357,55 @@ struct RopeRing {
     }
 };
 
-// Where a group of lanes is in the call's list: token t, piece c of its heads,
-// head hc of the piece. Done at t >= T (T is below 2^31, and so is a step).
+// The order of a call's pieces: those of `first` (every token's), then those of
+// `then`, so that the rows a warp works on at a time are of one kind; a step
+// leads from one into the other. T is below 2^31, and so is a step.
+struct RopeOrder {
+    uint32_t T;
+    int first, then;             // pieces a token
+    uint32_t dt0, dt1;           // a step in tokens, and the pieces left over
+    int dc0, dc1;
+    __device__ __forceinline__ RopeOrder(uint32_t T, int first, int then, uint32_t step)
+        : T(T), first(first), then(then), dt0(first ? step / first : 0), dt1(then ? step / then : 0),
+          dc0(first ? step - dt0 * first : 0), dc1(then ? step - dt1 * then : 0)
+    {
+    }
+};
+
+// Where a group of lanes is: token t, piece c of its heads (of the first kind's
+// or of the second's), head hc of the piece. Done at t >= T.
 struct RopeCursor {
     uint32_t t;
-    int c, hc;
-    __device__ __forceinline__ void start(int64_t i, int chunks)
+    int c, hc, second;
+    __device__ __forceinline__ void cross(const RopeOrder &o, uint32_t over)
     {
-        const int64_t q = i / chunks;
-        t = (uint32_t)min(q, (int64_t)0x7FFFFFFF);
-        c = (int)(i - q * chunks);
-        hc = 0;
+        second = 1;
+        t = o.then ? over / o.then : o.T;
+        c = o.then ? over - t * o.then : 0;
     }
-    __device__ __forceinline__ void next(int U, int HC, uint32_t dt, int dc, int chunks)
+    __device__ __forceinline__ void start(const RopeOrder &o, uint32_t i)
+    {
+        hc = second = 0;
+        t = o.first ? i / o.first : 0;
+        c = o.first ? i - t * o.first : 0;
+        if (t >= o.T || o.first == 0)
+            cross(o, i - o.T * o.first);
+    }
+    __device__ __forceinline__ void next(const RopeOrder &o, int U, int HC)
     {
         hc += U;
         if (hc < HC)
             return;
         hc = 0;
-        t += dt;
-        c += dc;
-        if (c >= chunks) {
-            c -= chunks;
+        const int n = second ? o.then : o.first;
+        t = min(t + (second ? o.dt1 : o.dt0), 0x80000000u);
+        c += second ? o.dc1 : o.dc0;
+        if (c >= n) {
+            c -= n;
             ++t;
         }
-        t = min(t, 0x7FFFFFFFu);
+        if (!second && t >= o.T)
+            cross(o, (t - o.T) * o.first + c);
     }
 };
 
@@ -423,7 +447,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
                                         threadIdx.x * (E * sizeof(T))};
 
     const int L = 1 << p.shift, lane = threadIdx.x & (L - 1), np = p.D / E;
-    const int chunks = p.part[0].chunks + p.part[1].chunks + (APP ? p.part[2].chunks : 0);
     RopeSlot slot[V];
     int pair[V];
 #pragma unroll
@@ -434,18 +457,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     griddep_wait();
     griddep_launch_dependents();
 
-    const uint32_t T_ = (uint32_t)p.T, step = gridDim.x * (kRopeThreads >> p.shift);
-    const uint32_t dt = step / chunks;
-    const int dc = (int)(step - dt * chunks);
+    // q's pieces, then k's and v's
+    const RopeOrder order((uint32_t)p.T, p.part[0].chunks, p.part[1].chunks + (APP ? p.part[2].chunks : 0),
+                          gridDim.x * (kRopeThreads >> p.shift));
     RopeCursor cur, ahead;
-    cur.start(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> p.shift, chunks);
+    cur.start(order, (blockIdx.x * kRopeThreads + threadIdx.x) >> p.shift);
     ahead = cur;
 
-    // which heads a piece has: q's, k's or v's
-    auto part_of = [&](int &ci) {
-        if (ci < p.part[0].chunks)
+    // which heads a piece has, and its number among theirs
+    auto part_of = [&](const RopeCursor &at, int &ci) {
+        ci = at.c;
+        if (!at.second)
             return 0;
-        ci -= p.part[0].chunks;
         if (!APP || ci < p.part[1].chunks)
             return 1;
         ci -= p.part[1].chunks;
@@ -453,9 +476,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     };
     auto fetch = [&](int stage) {
         if constexpr (E > 1) {
-            if (ahead.t < T_) {
-                int ci = ahead.c;
-                const RopeRows &r = p.part[part_of(ci)];
+            if (ahead.t < order.T) {
+                int ci;
+                const RopeRows &r = p.part[part_of(ahead, ci)];
                 const int h0 = ci * p.HC + ahead.hc, h1 = min(r.heads, ci * p.HC + p.HC);
                 const char *x = static_cast<const char *>(r.x) + ((int64_t)ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
 #pragma unroll
@@ -469,7 +492,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
                     x += r.xh * (int64_t)sizeof(T);
                 }
             }
-            ahead.next(U, p.HC, dt, dc, chunks);
+            ahead.next(order, U, p.HC);
             copies_commit();
         }
     };
@@ -484,13 +507,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     bool kept = true, mapped = false, norm = false;
     int stage = 0, part = 0, ci = 0;
     // the lanes of a warp stay together in the sums' shuffles: done when all are
-    while (__any_sync(0xFFFFFFFFu, cur.t < T_)) {
+    while (__any_sync(0xFFFFFFFFu, cur.t < order.T)) {
         fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
-        const bool live = cur.t < T_;
+        const bool live = cur.t < order.T;
         if (cur.hc == 0) {
             // a new piece: its part, its token's rotation and its row of the cache
-            ci = cur.c;
-            part = part_of(ci);
+            part = part_of(cur, ci);
             const RopeRows &r = p.part[part];
             norm = r.w != nullptr && live;
             mapped = live && (norm || (p.turn.rot > 0 && part < 2));
@@ -620,7 +642,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
             }
         }
         stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
-        cur.next(U, p.HC, dt, dc, chunks);
+        cur.next(order, U, p.HC);
     }
 }
 
@@ -654,16 +676,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     griddep_wait();
     griddep_launch_dependents();
 
-    const int chunks = r.chunks;
-    const uint32_t T_ = (uint32_t)p.T, step = ctas * (kRopeThreads >> p.shift);
-    const uint32_t dt = step / chunks;
-    const int dc = (int)(step - dt * chunks);
+    const RopeOrder order((uint32_t)p.T, r.chunks, 0, ctas * (kRopeThreads >> p.shift));
     RopeCursor cur, ahead;
-    cur.start(((int64_t)cta * kRopeThreads + threadIdx.x) >> p.shift, chunks);
+    cur.start(order, (cta * kRopeThreads + threadIdx.x) >> p.shift);
     ahead = cur;
     auto fetch = [&](int stage) {
         if constexpr (E > 1) {
-            if (ahead.t < T_) {
+            if (ahead.t < order.T) {
                 const int h0 = ahead.c * p.HC + ahead.hc, h1 = min(r.heads, ahead.c * p.HC + p.HC);
                 const char *y = static_cast<const char *>(r.dy) + ((int64_t)ahead.t * r.yt + h0 * r.yh) * (int64_t)sizeof(T);
                 const char *x = static_cast<const char *>(r.x) + ((int64_t)ahead.t * r.xt + h0 * r.xh) * (int64_t)sizeof(T);
@@ -685,7 +704,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                     x += r.xh * (int64_t)sizeof(T);
                 }
             }
-            ahead.next(U, p.HC, dt, dc, chunks);
+            ahead.next(order, U, p.HC);
             copies_commit();
         }
     };
@@ -698,6 +717,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
     const Vals<E> one = rope_ones<E>();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        {
+            const float none[E] = {};
+            map[v].make(none, none, one, one, 0);        // a group without a row turns zeros
+        }
         (norm && slot[v].a < np ? P::load_cached(r.w, slot[v].a) : P::zero()).widen(wa[v]);
         (norm && slot[v].b < np ? P::load_cached(r.w, slot[v].b) : P::zero()).widen(wb[v]);
         da[v] = Vals<E>::zero();
@@ -706,9 +729,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
 
     int stage = 0;
     // the lanes of a warp stay together in the sums' shuffles: done when all are
-    while (__any_sync(0xFFFFFFFFu, cur.t < T_)) {
+    while (__any_sync(0xFFFFFFFFu, cur.t < order.T)) {
         fetch(stage == 0 ? kRopeDepth - 1 : stage - 1);
-        const bool live = cur.t < T_;
+        const bool live = cur.t < order.T;
         const int h0 = cur.c * p.HC + cur.hc, h1 = live ? min(r.heads, cur.c * p.HC + p.HC) : 0;
         if (cur.hc == 0 && p.turn.rot > 0 && live) {
             const int64_t pos = ld_index(p.turn.pos, cur.t, p.turn.pos64);
@@ -782,6 +805,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                 float rs = rsv[u];
                 if (p.rstd == nullptr)
                     rs = rsqrtf(fmaf(lanes_sum(hsum(ss), p.shift), p.inv_d, p.eps));
+                if (!on)
+                    rs = 0.f;                            // no row: nothing to add
                 const float k = -rs * rs * rs * (lanes_sum(hsum(sc), p.shift) * p.inv_d);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -789,10 +814,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                     for (int i = 0; i < Vals<E>::N; ++i) {
                         a[v].v[i] = vmul(a[v].v[i], splat<F>(rs));
                         b[v].v[i] = vmul(b[v].v[i], splat<F>(rs));
-                        if (on) {                        // other lanes' maps may hold anything
-                            da[v].v[i] = vfma(a[v].v[i], fa[v].v[i], da[v].v[i]);
-                            db[v].v[i] = vfma(b[v].v[i], fb[v].v[i], db[v].v[i]);
-                        }
+                        da[v].v[i] = vfma(a[v].v[i], fa[v].v[i], da[v].v[i]);
+                        db[v].v[i] = vfma(b[v].v[i], fb[v].v[i], db[v].v[i]);
                         a[v].v[i] = vfma(a[v].v[i], wa[v].v[i], vmul(fa[v].v[i], splat<F>(k)));
                         b[v].v[i] = vfma(b[v].v[i], wb[v].v[i], vmul(fb[v].v[i], splat<F>(k)));
                     }
@@ -809,7 +832,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
             }
         }
         stage = stage + 1 == kRopeDepth ? 0 : stage + 1;
-        cur.next(U, p.HC, dt, dc, chunks);
+        cur.next(order, U, p.HC);
     }
     if (!norm)
         return;
