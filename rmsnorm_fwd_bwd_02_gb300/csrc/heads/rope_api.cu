@@ -281,11 +281,11 @@ int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsno
         return st;
     if (!q)
         return RMSNORM_ERR_NULLPTR;
+    if (q->heads < 1)
+        return RMSNORM_ERR_BAD_SHAPE;
     const size_t es = elem_size(dtype);
     if ((st = check_rows(q, T, D, es, true)) || (k && (st = check_rows(k, T, D, es, true))))
         return st;
-    if (q->heads < 1)
-        return RMSNORM_ERR_BAD_SHAPE;
     if (T == 0)
         return RMSNORM_OK;
     if (!aligned(rstd, 4))

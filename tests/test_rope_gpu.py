@@ -156,19 +156,6 @@ def test_amplitude_and_scaled_frequencies(dtype, adjacent):
         check_bwd(q, q, w, dq, dw, pos, f, adjacent, float(torch.tensor(amp, dtype=F32)))
 
 
-def test_scaled_frequencies_definitions():
-    f, a = rn.rope_frequencies(8, 100.0, device="cpu")
-    assert a == 1.0 and torch.allclose(f, torch.tensor([100.0 ** (-i / 4) for i in range(4)], dtype=F64))
-    assert torch.allclose(rn.rope_frequencies(8, 100.0, "linear", 4.0, device="cpu")[0], f / 4)
-    g = rn.rope_frequencies(8, 100.0, "ntk", 4.0, device="cpu")[0]
-    assert g[0] == f[0] and abs(float(g[-1] / f[-1]) - 0.25) < 1e-12
-    y, a = rn.rope_frequencies(128, 1e4, "yarn", 16.0, original=4096, device="cpu")
-    p = rn.rope_frequencies(128, 1e4, device="cpu")[0]
-    assert torch.equal(y[:20], p[:20]) and torch.allclose(y[-10:], p[-10:] / 16) and abs(a - 1.2772588722) < 1e-9
-    ratio = p / y
-    assert bool((ratio[1:] >= ratio[:-1] - 1e-12).all())
-
-
 PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
 
 
