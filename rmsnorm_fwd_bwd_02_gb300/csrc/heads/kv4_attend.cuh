@@ -717,6 +717,13 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], d);
+        // a row of NaN alone never had a reference; its sums are to be joined all the same
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (l[nt][e] != l[nt][e] && m[nt][e] == kKv4Least)
+                    m[nt][e] = 0.f;
         if (joined)
             break;
         // the row's D / 8 features of this lane: to the output, or to the workspace as a part

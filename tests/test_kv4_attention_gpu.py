@@ -306,6 +306,24 @@ def test_magnitudes_of_q(few):
     check(out, lse, q, cache, table, [111], None, scale=2.0 ** -63)
 
 
+def test_rows_of_nan_and_infinity(kernel):
+    """A NaN or an infinity in a row of q makes that row NaN (or what the
+    softmax of infinities is) and leaves its neighbours as they are."""
+    D, page, L = 128, 16, 900
+    cache = make_cache(60, 1, page, D, 3)
+    table = torch.arange(60, dtype=torch.int32, device=DEV)[None]
+    lens, s = torch.tensor([L], dtype=torch.int32, device=DEV), torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    q = normal((3, 4, D), BF16, 4)
+    want, want_lse = rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, want_lse=True)
+    q[1, 2, 7], q[2, 0, 100] = float("nan"), float("inf")
+    out, lse = rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, want_lse=True)
+    bad = torch.zeros(3, 4, dtype=torch.bool, device=DEV)
+    bad[1, 2] = bad[2, 0] = True
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+    assert bool(out[1, 2].isnan().all()) and bool(lse[1, 2].isnan())
+    assert bool(out[2, 0].isnan().all())
+
+
 def test_long_offsets(few):
     """Pages whose byte offset passes 2^32."""
     D, page, Hk = 128, 64, 8
