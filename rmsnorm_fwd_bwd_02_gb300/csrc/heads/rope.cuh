@@ -144,9 +144,12 @@ __device__ __forceinline__ RopeSlot rope_slot(int pair, int rot, int adjacent)
     return s;
 }
 
-// Sum over the 2^shift lanes of a group; all lanes of the warp take part.
+// Sum over the 2^shift lanes of a group; all lanes of the warp take part. Eight
+// lanes (heads of 128 in 16 bits) have their own code, without branches.
 __device__ __forceinline__ float lanes_sum(float v, int shift)
 {
+    if (shift == 3)
+        return group_allreduce<8>(v);
 #pragma unroll
     for (int i = 4; i >= 0; --i)
         if (shift > i)                                   // the same for all lanes
@@ -457,8 +460,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     griddep_wait();
     griddep_launch_dependents();
 
-    // q's pieces, then k's and v's
-    const RopeOrder order((uint32_t)p.T, p.part[0].chunks, p.part[1].chunks + (APP ? p.part[2].chunks : 0),
+    // in 4 bits q's pieces before k's and v's, which take several times as long
+    constexpr bool kApart = FORM == 2;
+    const int kv = p.part[1].chunks + (APP ? p.part[2].chunks : 0);
+    const RopeOrder order((uint32_t)p.T, p.part[0].chunks + (kApart ? 0 : kv), kApart ? kv : 0,
                           gridDim.x * (kRopeThreads >> p.shift));
     RopeCursor cur, ahead;
     cur.start(order, (blockIdx.x * kRopeThreads + threadIdx.x) >> p.shift);
@@ -467,8 +472,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_fwd(RopeParams p)
     // which heads a piece has, and its number among theirs
     auto part_of = [&](const RopeCursor &at, int &ci) {
         ci = at.c;
-        if (!at.second)
+        if (kApart ? !at.second : ci < p.part[0].chunks)
             return 0;
+        if (!kApart)
+            ci -= p.part[0].chunks;
         if (!APP || ci < p.part[1].chunks)
             return 1;
         ci -= p.part[1].chunks;
