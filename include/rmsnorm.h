@@ -588,7 +588,7 @@ int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
  * Limits (else RMSNORM_ERR_UNSUPPORTED): D 64 or 128; page_size a multiple of
  * 16; a page of the cache below 2^31 bytes; blocks * page_size < 2^31 - 1024;
  * B <= 2^20; heads <= 2^20; (T + B) * heads < 2^31; and, but for pieces of
- * prompts, fewer than 2^31 stages of 32 tokens: (blocks * page_size / 32 + 2) *
+ * prompts, fewer than 2^31 stages of 32 tokens: (blocks * page_size / 32 + 4) *
  * kv_heads for each sequence and 8 (or 16) of its query rows of a key head. scale is finite (else RMSNORM_ERR_BAD_EPS).
  * Aliasing: outputs may share no byte with an input or each other.
  * Deterministic: parts of a long sequence are joined in a fixed order.

@@ -92,10 +92,11 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
     if (tmo == nullptr)
         return cuda_fail(cudaErrorInvalidSymbol);
     const int64_t G = heads / kv_heads;
-    // Eight query rows a tile where a sequence's rows of one key head fit, and
-    // for heads of 64, whose kernel then runs twice on an SM (16 x 5 tokens of
-    // 14 heads over up to 3000: 17.8 us, with sixteen rows 21.3); else sixteen:
-    // the cache's bytes are widened once for both halves.
+    // Eight query rows a tile where a sequence's rows of one key head fit; else
+    // sixteen, for which the cache's bytes are widened once (16 x 4 tokens of 32
+    // heads of 128 on 8 over 8192: 56 us, in tiles of eight 65; 4 x 4 of 64 heads:
+    // 35.9, 38.2). Not for heads of 64, whose kernel of eight rows runs twice on an
+    // SM (16 x 5 tokens of 14 heads on 2 over up to 3000: 17.8 us, of sixteen 21.3).
     const int64_t rows = (T + B - 1) / B * G;
     const int NT = rows <= 8 || D == 64 ? 1 : 2, di = D == 128 ? 1 : 0, ti = dtype == RMSNORM_BF16 ? 0 : 1;
     Kv4Params p = {q, q_token, q_head, out, out_token, out_head, lse, static_cast<const uint8_t *>(cache), pages,
@@ -133,7 +134,7 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
         return RMSNORM_OK;
     }
     const int64_t tiles = q_starts ? (T * G) / (8 * NT) + B : B * ((G + 8 * NT - 1) / (8 * NT));
-    if (tiles * kv_heads > INT32_MAX / (blocks * page_size / kKv4Slot + 2))
+    if (tiles * kv_heads > INT32_MAX / (blocks * page_size / kKv4Slot + 4))
         return RMSNORM_ERR_UNSUPPORTED;
     const void *fn = kv4_kernels.attend[ti][di][NT - 1];
     const int smem = kv4_smem((int)D);

@@ -41,8 +41,8 @@
 // warps.
 //
 // Split. The work of a call is a list of stages of 32 tokens of segments
-// (sequence, key head, tile of query rows), with one more entry a segment for
-// what a segment costs besides. Every warp computes from the lengths, which
+// (sequence, key head, tile of query rows), with a few more entries a segment
+// for what it costs besides. Every warp computes from the lengths, which
 // only the device knows, its equal run of the list, so lengths may differ at
 // will and a captured call replays with others. A warp that has the whole of
 // a segment writes its output. A CTA whose eight runs lie in one segment joins
@@ -51,6 +51,15 @@
 // segments are few and short enough to run at once, each gets a cluster of
 // CTAs instead, which joins its sums through distributed shared memory: one
 // launch, no workspace.
+//
+// What bounds it. 16 tokens of a key head are 18 D bytes and, at D = 128, 280
+// warp instructions, of which 64 widen codes and 64 multiply by scales: four
+// warps a scheduler (what the registers allow) issue in 61 % of the cycles.
+// Measured (GB300): 4 sequences of some 116000 tokens, 40 heads on 8, 104 us, 5.3
+// TB/s of the cache; 64 of 1 to 8192, 32 heads on 8, 70 us; one of 4001 8.6 us.
+// Runs of warps, not of CTAs: with units of 256 tokens for whole CTAs, joined
+// after each segment, the 64 sequences took 114 us; with twice the CTAs, so that
+// late ones even out, 80.
 #pragma once
 
 #include "../split.cuh"
@@ -103,12 +112,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 }
 
 // ------------------------------------------------------------ work list
+// What a segment costs besides its stages (q, the ring's first copies, the
+// output), in stages: 64 sequences of 1 to 8192 take 74.8 us with 1, 71.8 with
+// 2, 71.1 with 3, 70.1 with 5; 16 x 5 tokens over 500 to 3000 15.8, 14.8, 14.9
+// and 15.3.
+constexpr int kKv4Extra = 3;
+
 struct Kv4Seq {
     int q0, n;           // first row, rows
     int len;             // tokens in the cache
     int tiles;           // of 8 NT query rows
     int stages;          // of 32 tokens
-    __device__ __forceinline__ int cost() const { return stages + 1; }
+    __device__ __forceinline__ int cost() const { return stages + kKv4Extra; }
     __device__ __forceinline__ uint32_t total(int Hk) const { return (uint32_t)tiles * Hk * cost(); }
 };
 
@@ -215,7 +230,7 @@ __device__ __forceinline__ int kv4_segment_of(const Kv4Params &p, uint32_t id, u
     return -1;
 }
 
-// A segment in the list: its first entry stands for what it costs besides, its
+// A segment in the list: its first entries stand for what it costs besides, its
 // stages follow.
 struct Kv4Segment {
     int h, tile;
@@ -228,7 +243,7 @@ __device__ __forceinline__ Kv4Segment kv4_segment(const Kv4Seq &s, uint32_t firs
     Kv4Segment g;
     g.h = (int)(seg / (uint32_t)s.tiles);
     g.tile = (int)seg - g.h * s.tiles;
-    g.at = first + seg * s.cost() + 1;
+    g.at = first + seg * s.cost() + kKv4Extra;
     return g;
 }
 
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         const int to = run1 > g.at ? min(s.stages, (int)(run1 - g.at)) : 0;
         u = g.at + s.stages;                                    // the next segment
         if (from >= to && s.stages > 0)
-            continue;                                           // its first entry alone
+            continue;                                           // its first entries alone
         // pages of the stages ahead
         const int *row = p.table + seq * p.table_ld;
         const int t0 = 2 * from;
@@ -729,7 +744,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         // the row's D / 8 features of this lane: to the output, or to the workspace as a part
         const bool all = from == 0 && to == s.stages;
         const float gv = p.vscale ? __ldg(p.vscale + g.h) : 1.f;
-        float *part = p.ws + kv4_part(gw, g.at - 1 > run0) * kv4_partial(D, NT);
+        float *part = p.ws + kv4_part(gw, g.at - kKv4Extra > run0) * kv4_partial(D, NT);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -944,7 +959,7 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
         return;
     const uint32_t warps = ctas * kKv4Warps, C = (entries + warps - 1) / warps;
     const uint32_t start = first + seg * s.cost(), end = start + s.cost();
-    const uint32_t w0 = (start + 1) / C, w1 = (end - 1) / C;      // the warps that have stages of it
+    const uint32_t w0 = (start + kKv4Extra) / C, w1 = (end - 1) / C;      // the warps that have stages of it
     if (w0 == w1)
         return;                                                 // one warp had all of it
     const uint32_t c0 = w0 / kKv4Warps, c1 = w1 / kKv4Warps;

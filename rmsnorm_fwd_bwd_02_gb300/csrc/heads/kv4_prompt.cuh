@@ -28,6 +28,13 @@
 // That leaves room for keys and values in two buffers each. A row's output is
 // scaled in tensor memory when its reference moves.
 //
+// Measured (GB300): 2 x 512 tokens of 32 heads of 128 on 8 over up to 8192, 118 us,
+// 1.05 PFLOP/s (the kernel for few rows: 607). A tile of 128 tokens takes some
+// 3100 cycles, 2048 of them MMAs at their rate: a tile's softmax (1400), product
+// and next scores wait for one another, and two tiles of rows overlap them. With
+// p in shared memory 227 us; products issued by a lone lane, whose descriptors
+// then go through vector registers, 140.
+//
 // Every wait is bounded; one that runs out sets a flag that ends the others,
 // counts in the timeout counter and leaves the rows unwritten.
 #pragma once
