@@ -179,7 +179,10 @@ def _heads3d(t):
 
 def rms_norm_rope(q, k, positions, freq, wq=None, wk=None, eps: float = 1e-6, interleaved: bool = False,
                   amplitude: float = 1.0):
-    """(yq, yk) of rmsnorm_rope_fwd, differentiable in q, k, wq and wk."""
+    """(yq, yk) of rmsnorm_rope_fwd, differentiable in q, k, wq and wk. As for
+    any function of torch's: a backward that is captured into a CUDA graph
+    wants leaves of which no eager graph is alive (their gradients'
+    accumulation belongs to the stream that it was made on)."""
     return RMSNormRopeFunction.apply(q, k, wq, wk, positions, freq, eps, interleaved, amplitude)
 
 

@@ -217,7 +217,7 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor *dy[2] = {&dyq, dyk}, *x[2] = {q, k}, *w[2] = {wq, wk}, *dx[2] = {dq, dk};
     static const char *const kDy[2] = {"dyq", "dyk"}, *const kX[2] = {"q", "k"}, *const kW[2] = {"wq", "wk"},
                                    *const kDx[2] = {"dq", "dk"};
-    size_t total = 0;
+    size_t total = 0, small = 0;
     for (int i = 0; i < 2; ++i) {
         if (dy[i] == nullptr)
             continue;
@@ -231,14 +231,15 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
             heads(*x[i], kX[i], T, g[i].heads, D, dtype, dev, g[i].x_token, g[i].x_head);
             g[i].x = x[i]->data_ptr();
         }
-        total += (dx[i] ? 0 : bytes_of(dy[i]->numel(), dtype)) + (w[i] ? bytes_of(D, at::kFloat) : 0);
+        total += dx[i] ? 0 : bytes_of(dy[i]->numel(), dtype);
+        small += w[i] ? bytes_of(D, at::kFloat) : 0;
     }
     const int64_t H = g[0].heads + g[1].heads;
     if (rstd)
         fp32(*rstd, "rstd", {T, H}, dev);
 
     const c10::cuda::CUDAGuard guard(dev);
-    Outputs made(total);
+    Outputs made(total), sums(small);       // the weights' gradients share an allocation
     Tensor out_dx[2], out_dw[2];
     for (int i = 0; i < 2; ++i) {
         if (dy[i] == nullptr)
@@ -249,7 +250,7 @@ PyObject *rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
         heads(t, kDx[i], T, g[i].heads, D, dtype, dev, g[i].dx_token, g[i].dx_head);
         g[i].dx = t.data_ptr();
         if (w[i]) {
-            out_dw[i] = made.dense({D}, at::kFloat);
+            out_dw[i] = sums.dense({D}, at::kFloat);
             g[i].dw = static_cast<float *>(out_dw[i].data_ptr());
         }
     }

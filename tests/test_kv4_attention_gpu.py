@@ -503,3 +503,97 @@ def test_decode_step_in_a_run():
         assert torch.equal(cache, ref_cache) and torch.equal(captured[2], out)
         check_fwd(yq, heads[:, :Hq], wq, pos, f, False)
         check(out, None, yq, cache, table.cpu(), lens.tolist(), None)
+
+
+@pytest.mark.parametrize("starts", [[0, 0, 0, 0], [5, 5, 5, 5], [9, 4, 2, 0]])
+def test_sequences_without_rows(kernel, starts):
+    """Starts that give no sequence a row: nothing is written."""
+    cache = make_cache(6, 2, 16, 64, 3)
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(3, 2)
+    q, out = normal((9, 4, 64), BF16, 1), torch.full((9, 4, 64), 5.0, dtype=BF16, device=DEV)
+    rn.rmsnorm_kv4_attention(q, cache, table, torch.tensor([20, 30, 1], dtype=torch.int32, device=DEV),
+                             q_starts=torch.tensor(starts, dtype=torch.int32, device=DEV), out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 5).all())
+
+
+def test_many_sequences_in_clusters():
+    """More than 32 sequences, each a cluster of its own; lengths of all sorts."""
+    B, Hk, page, blocks = 70, 2, 16, 30
+    cache = make_cache(B * blocks, Hk, page, 64, 2)
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 481, (B,), generator=g).tolist()
+    rn.set_kv4_test(3)
+    try:
+        run(B, Hk * 7, 64, BF16, cache, table_of(B, blocks, B * blocks, 6), lens)
+    finally:
+        rn.set_kv4_test(0)
+
+
+def test_captured_piece_of_a_prompt():
+    """Replayed with other lengths, starts and rows behind the last sequence."""
+    D, page, Hk, G, T = 128, 64, 8, 4, 700
+    cache = make_cache(60, Hk, page, D, 3)
+    q = normal((T, Hk * G, D), BF16, 40)
+    table = table_of(2, 30, 60, 1)
+    lens = torch.tensor([1900, 1100], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, 500, 690], dtype=torch.int32, device=DEV)
+    dt = table.to(DEV)
+    rn.rmsnorm_kv4_attention(q, cache, dt, lens, q_starts=starts)
+    assert rn.last_path() == rn.PATH_KV4_PROMPT
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = rn.rmsnorm_kv4_attention(q, cache, dt, lens, q_starts=starts, want_lse=True)
+    for new_lens, new_starts in (([1900, 1100], [0, 500, 690]), ([77, 1800], [3, 60, 700]), ([600, 0], [0, 600, 640])):
+        lens.copy_(torch.tensor(new_lens, dtype=torch.int32))
+        starts.copy_(torch.tensor(new_starts, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, lse, q, cache, table, new_lens, new_starts)
+        behind = torch.ones(T, dtype=torch.bool, device=DEV)
+        behind[new_starts[0]:new_starts[2]] = False
+        assert bool((out[behind] == 7).all()) and bool((lse[behind] == 7).all())
+
+
+def test_first_calls_inside_a_capture():
+    """In a process of its own, the library's very first calls are captured."""
+    code = """
+import torch
+from rmsnorm_fwd_bwd_02_gb300 import rmsnorm as rn
+dev = torch.device("cuda:0")
+q, k = torch.randn(64, 4, 128, device=dev).bfloat16(), torch.randn(64, 2, 128, device=dev).bfloat16()
+f, _ = rn.rope_frequencies(128, device=dev)
+pos = torch.arange(64, device=dev)
+cache = rn.kv4_cache(4, 2, 16, 128, device=dev)
+table = torch.arange(4, dtype=torch.int32, device=dev)[None]
+lens, starts = torch.tensor([64], dtype=torch.int32, device=dev), torch.tensor([0, 64], dtype=torch.int32, device=dev)
+torch.cuda.synchronize()
+def chain():
+    y = rn.rmsnorm_rope_append_kv4(k, k, pos, f, pos, cache, q=q)
+    a = rn.rmsnorm_kv4_attention(y[63:], cache, table, lens)[0]
+    rn.set_kv4_test(2)
+    b = rn.rmsnorm_kv4_attention(y, cache, table, lens, q_starts=starts)[0]
+    rn.set_kv4_test(1)
+    c = rn.rmsnorm_kv4_attention(y, cache, table, lens, q_starts=starts)[0]
+    rn.set_kv4_test(0)
+    return (a, b, c) + rn.rmsnorm_rope_bwd(q, q, pos, f, wq=q[0, 0].contiguous())[:1]
+w = q[0, 0].contiguous()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = chain()
+g.replay()
+torch.cuda.synchronize()
+want = chain()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, want))
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
