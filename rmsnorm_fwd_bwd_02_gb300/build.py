@@ -68,7 +68,7 @@ def build_torch(name: str, force: bool = False) -> str:
     if os.path.exists(stamp) and os.path.exists(lib):
         with open(stamp) as f:
             made = f.read()
-    newest = max(os.path.getmtime(f) for f in (src, os.path.join(CSRC, "binding.h"),
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(CSRC, "torch", "binding.h"),
                                                os.path.join(INCLUDE, "rmsnorm.h"),
                                                os.path.abspath(__file__)))
     if not force and made == torch.__version__ and os.path.getmtime(lib) >= newest:

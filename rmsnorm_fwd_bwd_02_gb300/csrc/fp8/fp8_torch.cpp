@@ -10,7 +10,7 @@
 //
 // The module does not link the library: rmsnorm.py hands it the functions'
 // addresses and the Python function that raises a status.
-#include "../binding.h"
+#include "../torch/binding.h"
 
 namespace {
 
