@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
 
     if (warp < 8) {
         // ------------------------------------------------------ the softmax
-        const int t = tid >> 7, r = tid & 127;
+        const int t = tid >> 7;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;     // (32 (warp % 4)) << 16
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         // (a row that sees nothing wants no reference)
