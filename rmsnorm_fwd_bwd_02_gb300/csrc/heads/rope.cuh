@@ -281,11 +281,26 @@ __device__ __forceinline__ uint2 quant4(const float (&x)[16], float g, uint8_t &
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(s8));
     const float d = Half16<f16>::wide1((uint16_t)h2) * g;
     scale = (uint8_t)s8;
+    // Quotients by Markstein's theorem: with r the rounded reciprocal of d and q
+    // the rounded x r, q + r (x - q d) in two fused steps is x / d rounded once.
+    // (A division each takes several times as long; many values of 16 bits lie
+    // right between two codes, so a mere product with r would not do.) Infinities
+    // keep q; scales far from one take the divisions.
+    const float r = __frcp_rn(d);
+    const bool plain = !(d > 1e-18f && d < 1e18f);      // (the residual keeps its bits)
+    const float2 r2 = make_float2(r, r), nd = make_float2(-d, -d);
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t b;
-        const float lo = __fdiv_rn(x[2 * i], d), hi = __fdiv_rn(x[2 * i + 1], d);
+        const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+        const float2 q = __fmul2_rn(v, r2), e = __ffma2_rn(q, nd, v);
+        float2 y = __ffma2_rn(e, r2, q);
+        if (plain) {
+            y.x = __fdiv_rn(v.x, d);
+            y.y = __fdiv_rn(v.y, d);
+        }
+        const float lo = y.x == y.x ? y.x : q.x, hi = y.y == y.y ? y.y : q.y;
         asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
             : "=r"(b)
             : "f"(hi), "f"(lo));

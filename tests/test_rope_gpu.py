@@ -524,3 +524,31 @@ def test_kv4_ties_and_specials():
     assert rv[1, 0, 20] == 6 and rs[1, 0, 1] == 448 and rv[1, 0, 33] == -6
     assert rv[2, 0, 0] == 6 and rs[2, 0, 0] == 448
     assert bool(torch.isfinite(rv).all()) and bool(torch.isfinite(rs).all())
+
+
+@pytest.mark.parametrize("g", [1.0, 0.37, 1e-25, 3e20])
+def test_kv4_quotients_are_rounded_once(g):
+    """Values right between two codes, and next to that, at scales of the
+    heads near one and far from it: the codes of the fp32 division."""
+    H, D, n = 1, 128, 2000
+    gen = torch.Generator().manual_seed(5)
+    gs = torch.tensor([g], dtype=F32)
+    middle = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    x = middle[torch.randint(0, 8, (n, H, D), generator=gen)] * (torch.randint(0, 2, (n, H, D), generator=gen) * 2 - 1)
+    scale = (torch.randint(8, 16, (n, H, D // 16, 1), generator=gen) / 8.0) * \
+        2.0 ** torch.randint(-5, 6, (n, H, D // 16, 1), generator=gen)
+    v = x.view(n, H, D // 16, 16) * scale * gs
+    v = torch.where(torch.rand(v.shape, generator=gen) < 0.3, torch.nextafter(v, torch.zeros(())), v)
+    v[..., 0] = (6.0 * scale * gs)[..., 0]
+    v = v.view(n, H, D)
+    pages = -(-n // 16)
+    cache = rn.kv4_cache(pages, H, 16, D, device=DEV)
+    slots = torch.arange(n, device=DEV)
+    rn.rmsnorm_rope_append_kv4(v.to(DEV), v.to(DEV), None, None, slots, cache, k_scale=gs.to(DEV), v_scale=gs.to(DEV))
+    top = (v.view(n, H, D // 16, 16).abs().amax(-1) / (6.0 * gs)).clamp(2.0 ** -9, 448)
+    sc = top.to(torch.float8_e4m3fn).float()
+    quotient = v.view(n, H, D // 16, 16) / (sc * gs)[..., None]              # fp32, rounded once
+    want = round4(quotient.to(F64)).view(n, H, D)
+    for got, got_s in zip(*[iter(rn.rmsnorm_kv4_read(cache, slots))] * 2):
+        assert torch.equal(got_s.float().cpu(), sc)
+        assert torch.equal(got.float().cpu().to(F64), want)
