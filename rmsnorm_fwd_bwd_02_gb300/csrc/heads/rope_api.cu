@@ -90,21 +90,30 @@ int lane_shift(int E, int64_t D)
     return s;
 }
 
-// Heads a piece: the sines are computed once for a piece, so long ones where
-// the pieces still fill the GPU's lanes, down to single heads for few tokens.
-// Eight at most (32768 x 40 x 128 forward, 16384 x 40 x 128 backward, append of
-// 8192 tokens: 107, 95 and 41 us; four 123, 97 and 44; sixteen 112, 140 and 53:
-// fewer pieces leave more of the lanes idle at the end).
+// Heads a piece: the sines and the map are made once for a piece, at the cost of
+// some 1.2 heads; the groups of lanes take the pieces in rounds, the last of which
+// may leave most of them idle. So the length of the least rounds x (heads + 1.2),
+// of up to eight heads, the longer of two equals. Few tokens come to single heads,
+// and many to eight (32768 x 40 x 128 forward, 16384 x 40 x 128 backward, append of
+// 8192 tokens: eight 107, 95 and 41 us, four 123, 97 and 44, sixteen 112, 140 and
+// 53). Between them the rounds decide: at 4096 x 20 heads with the norm the longest
+// that fills the lanes once takes 13.2 us forward and 26.7 backward for heads of
+// 128, 14.8 and 33.2 for heads of 80; this rule 10.8, 19.6, 13.5 and 23.1.
 int piece(int64_t T, std::initializer_list<int64_t> heads, int64_t groups)
 {
-    for (int hc = 8; hc > 1; hc /= 2) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int hc = 8; hc >= 1; hc /= 2) {
         int64_t n = 0;
         for (int64_t h : heads)
             n += (h + hc - 1) / hc;
-        if (T * n >= groups)
-            return hc;
+        const int64_t cost = (T * n + groups - 1) / groups * (5 * hc + 6);
+        if (cost < least) {
+            least = cost;
+            best = hc;
+        }
     }
-    return 1;
+    return best;
 }
 
 int check_rows(const rmsnorm_heads *r, int64_t T, int64_t D, size_t es, bool has_y)
