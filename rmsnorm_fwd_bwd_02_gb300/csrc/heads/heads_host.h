@@ -56,6 +56,16 @@ inline Span heads_span(const void *p, int64_t T, int64_t heads, int64_t D, int64
     return {p, 1, all, all};
 }
 
+// Whether rows of heads in y may go with those in x: the same rows exactly, or no
+// byte in common. The spans do not say which of their directions the tokens are:
+// of as many tokens as heads, a buffer and its transpose have equal ones.
+inline bool heads_same_or_disjoint(Span y, int64_t yt, int64_t yh, Span x, int64_t xt, int64_t xh, int64_t T,
+                                   int64_t heads)
+{
+    const bool rows = y.p == x.p && (T <= 1 || yt == xt) && (heads <= 1 || yh == xh);
+    return rows || !overlap(y, x);
+}
+
 inline bool dtype_ok(int dtype)
 {
     return dtype == RMSNORM_F32 || dtype == RMSNORM_BF16 || dtype == RMSNORM_F16;

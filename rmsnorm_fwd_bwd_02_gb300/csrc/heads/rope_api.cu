@@ -240,8 +240,9 @@ int append_impl(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsnorm_he
         if (k->y == v->y)
             return RMSNORM_ERR_ALIAS;
     }
-    if (!same_or_disjoint(sy, sx[0]) || overlap(sy, sx[1]) || overlap(sy, sx[2]) ||
-        overlap(sy, index_span(slots, T, slot_bits)) || touches_inputs(sy, rot, T, D, es, wq, k->w))
+    if ((q && !heads_same_or_disjoint(sy, q->y_token, q->y_head, sx[0], q->x_token, q->x_head, T, Hq)) ||
+        overlap(sy, sx[1]) || overlap(sy, sx[2]) || overlap(sy, index_span(slots, T, slot_bits)) ||
+        touches_inputs(sy, rot, T, D, es, wq, k->w))
         return RMSNORM_ERR_ALIAS;
     for (Span o : cache) {
         if (overlap(o, sy) || overlap(o, index_span(slots, T, slot_bits)) ||
@@ -310,8 +311,9 @@ int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsno
                xk = Hk ? heads_span(k->x, T, Hk, D, k->x_token, k->x_head, es) : none,
                yk = Hk ? heads_span(k->y, T, Hk, D, k->y_token, k->y_head, es) : none,
                sr = flat(rstd, (size_t)(T * (q->heads + Hk)) * 4);
-    if (!same_or_disjoint(yq, xq) || !same_or_disjoint(yk, xk) || overlap(yq, yk) || overlap(yq, xk) ||
-        overlap(yk, xq))
+    if (!heads_same_or_disjoint(yq, q->y_token, q->y_head, xq, q->x_token, q->x_head, T, q->heads) ||
+        (Hk && !heads_same_or_disjoint(yk, k->y_token, k->y_head, xk, k->x_token, k->x_head, T, Hk)) ||
+        overlap(yq, yk) || overlap(yq, xk) || overlap(yk, xq))
         return RMSNORM_ERR_ALIAS;
     for (Span o : {yq, yk, sr})
         if (touches_inputs(o, rot, T, D, es, q->w, wk))
@@ -405,8 +407,13 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
     const void *w0 = q->w, *w1 = parts[1] ? parts[1]->w : nullptr;
     for (int i = 0; i < 2; ++i) {
         const int j = 1 - i;
-        if (!same_or_disjoint(sd[i], sy[i]) || !same_or_disjoint(sd[i], sx[i]) || overlap(sd[i], sy[j]) ||
-            overlap(sd[i], sx[j]) || overlap(sd[i], ss) || touches_inputs(sd[i], rot, T, D, es, w0, w1))
+        const rmsnorm_heads_grad *r = parts[i];
+        if ((r && (!heads_same_or_disjoint(sd[i], r->dx_token, r->dx_head, sy[i], r->dy_token, r->dy_head, T,
+                                           r->heads) ||
+                   !heads_same_or_disjoint(sd[i], r->dx_token, r->dx_head, sx[i], r->x_token, r->x_head, T,
+                                           r->heads))) ||
+            overlap(sd[i], sy[j]) || overlap(sd[i], sx[j]) || overlap(sd[i], ss) ||
+            touches_inputs(sd[i], rot, T, D, es, w0, w1))
             return RMSNORM_ERR_ALIAS;
         for (Span o : {sd[0], sd[1], sy[0], sy[1], sx[0], sx[1], ss})
             if (overlap(sw[i], o) || overlap(wsp, o))

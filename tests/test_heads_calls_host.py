@@ -1,0 +1,29 @@
+"""CPU tier: refusals of the entry points on attention heads, beside those of
+test_heads_host.py. Made-up addresses; every call below fails a check (or has
+nothing to do), so nothing is launched."""
+import pytest
+
+from tests.test_abi_host import ALIAS, lib  # noqa: F401
+from tests.test_heads_host import AT, append, append4, bwd, fwd, grad, heads
+
+
+@pytest.mark.parametrize("n", [2, 4, 8])
+def test_a_transposed_buffer_is_not_in_place(lib, n):  # noqa: F811
+    """As many tokens as heads: a buffer and its transpose span the same bytes
+    in rows of one width."""
+    D = 64
+    turned = {"y": AT[0], "y_token": D, "y_head": n * D, "n": n}
+    k = {"x": AT[2], "y": AT[2], "y_token": D, "y_head": n * D, "n": n}
+    assert fwd(lib, q=heads(**turned), T=n) == ALIAS
+    assert fwd(lib, q=heads(n=n), k=heads(**k), T=n) == ALIAS
+    # and the other way round: head-major inputs
+    assert fwd(lib, q=heads(y=AT[0], x_token=D, x_head=n * D, n=n), T=n) == ALIAS
+    for at in (AT[0], AT[1]):                                  # over dy, over x
+        g = grad(dx=at, dx_token=D, dx_head=n * D, n=n)
+        assert bwd(lib, q=g, T=n) == ALIAS
+        other = {a: b for a, b in zip(("dy", "x", "w", "dw"), (AT[10], AT[11], AT[12], AT[13]))}
+        over = AT[10] if at == AT[0] else AT[11]
+        assert bwd(lib, q=grad(n=n), k=grad(**other, dx=over, dx_token=D, dx_head=n * D, n=n), T=n) == ALIAS
+    for call in (append, append4):
+        q = heads(x=AT[6], y=AT[6], y_token=D, y_head=n * D, n=n)
+        assert call(lib, q=q, T=n) == ALIAS
