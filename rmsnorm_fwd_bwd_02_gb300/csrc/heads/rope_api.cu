@@ -241,18 +241,16 @@ int append_impl(const rmsnorm_heads *q, const rmsnorm_heads *k, const rmsnorm_he
             return RMSNORM_ERR_ALIAS;
     }
     if ((q && !heads_same_or_disjoint(sy, q->y_token, q->y_head, sx[0], q->x_token, q->x_head, T, Hq)) ||
-        overlap(sy, sx[1]) || overlap(sy, sx[2]) || overlap(sy, index_span(slots, T, slot_bits)) ||
-        touches_inputs(sy, rot, T, D, es, wq, k->w))
+        overlap(sy, sx[1]) || overlap(sy, sx[2]) || overlap(sy, cache[0]) || overlap(sy, cache[1]))
         return RMSNORM_ERR_ALIAS;
-    for (Span o : cache) {
-        if (overlap(o, sy) || overlap(o, index_span(slots, T, slot_bits)) ||
-            touches_inputs(o, rot, T, D, es, wq, k->w) || overlap(o, flat(c.k_scale, (size_t)Hk * 4)) ||
-            overlap(o, flat(c.v_scale, (size_t)Hk * 4)))
+    for (Span o : {sy, cache[0], cache[1]})
+        if (overlap(o, index_span(slots, T, slot_bits)) || touches_inputs(o, rot, T, D, es, wq, k->w) ||
+            overlap(o, flat(c.k_scale, (size_t)Hk * 4)) || overlap(o, flat(c.v_scale, (size_t)Hk * 4)))
             return RMSNORM_ERR_ALIAS;
+    for (Span o : cache)
         for (Span i : sx)
             if (overlap(o, i))
                 return RMSNORM_ERR_ALIAS;
-    }
 
     RopeParams p = {};
     p.part[0] = rows_of(q);

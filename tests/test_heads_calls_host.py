@@ -3,7 +3,7 @@ test_heads_host.py. Made-up addresses; every call below fails a check (or has
 nothing to do), so nothing is launched."""
 import pytest
 
-from tests.test_abi_host import ALIAS, lib  # noqa: F401
+from tests.test_abi_host import ALIAS, OK, lib  # noqa: F401
 from tests.test_heads_host import AT, append, append4, bwd, fwd, grad, heads
 
 
@@ -27,3 +27,16 @@ def test_a_transposed_buffer_is_not_in_place(lib, n):  # noqa: F811
     for call in (append, append4):
         q = heads(x=AT[6], y=AT[6], y_token=D, y_head=n * D, n=n)
         assert call(lib, q=q, T=n) == ALIAS
+
+
+def test_q_does_not_go_over_the_heads_scales(lib):  # noqa: F811
+    """The append reads the scales while it writes q."""
+    q = heads(x=AT[6], y=AT[7], n=4)
+    for at in (AT[7], AT[7] + 8 * 4 * 64 * 2 - 4, AT[7] - 12):       # the first bytes, the last, half inside
+        assert append4(lib, q=q, ks=at) == ALIAS
+        assert append4(lib, q=q, vs=at) == ALIAS
+
+
+def test_no_tokens_want_no_cache(lib):  # noqa: F811
+    assert append4(lib, T=0, cache=None, slots=None) == OK
+    assert append(lib, T=0, k=heads(x=None, y=None), v=heads(x=None, y=None), slots=None) == OK
