@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
     volatile uint8_t *present = reinterpret_cast<volatile uint8_t *>(sm + L::bar + 8 * L::kBars + 8);   // [4][4]
 
     griddep_wait();
-    griddep_launch_dependents();
     // the segment of this CTA: sequences' segments side by side, a key head's
     // tiles from the last (which sees most) to the first
     int64_t segs = 0, seg = -1;
@@ -285,6 +284,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv4_prompt(Kv4Params p)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = slots[0];
+    // Not before the CTA holds its tensor memory: a dependent's CTA beside it may
+    // take columns first and keep them until this grid ends, which would then
+    // wait for them.
+    griddep_launch_dependents();
 
     if (warp < 8) {
         // ------------------------------------------------------ the softmax

@@ -49,3 +49,36 @@ def test_in_place_where_tokens_and_heads_are_as_many(T, H, head_major):
     dq, _, dw, _ = rn.rmsnorm_rope_bwd(g, base, pos, f, wq=w, dq=g)
     assert dq is g
     check_bwd(dy, base, w, g, dw, pos, f, False)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_pieces_of_prompts_between_other_tensor_memory_kernels(D):
+    """Calls that allocate tensor memory, one right behind the other on a
+    stream, each launched while the one before it ends."""
+    Hk, G, page, T = 2, 4, 16, 400
+    cache = make_cache(60, Hk, page, D, 3)
+    q = normal((T, Hk * G, D), BF16, 1)
+    table = torch.arange(60, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([900], dtype=torch.int32, device=DEV)
+    s = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    x, wn, W = normal((16, 512), BF16, 2), normal((512,), BF16, 3, 0.1, 1.0), normal((1024, 512), BF16, 4)
+    Wq, Ws = rn.rmsnorm_quant_fp8(W, block_rows=128)
+    xq, xs = rn.rmsnorm_fwd_fp8(x, wn)[:2]
+    torch.cuda.synchronize()
+    rn.set_kv4_test(2)
+    try:
+        def chain():
+            a = rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s)[0]
+            b = rn.rmsnorm_gemm_fp8(xq, xs, Wq, Ws)
+            c = rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s)[0]
+            d = rn.rmsnorm_gemv_fwd(x, wn, W)[0]
+            return a, b, c, d
+        want = [t.clone() for t in chain()]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            got = chain()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        check(want[0], None, q, cache, table.cpu(), [900], [0, T])
+    finally:
+        rn.set_kv4_test(0)
