@@ -581,8 +581,9 @@ int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
  *   q_starts[b + 1] - 1; NULL: one token each (T == B, else
  *   RMSNORM_ERR_BAD_SHAPE). Rows of q that belong to no sequence are not
  *   read, and those of out and lse are left as they are.
- * A row that sees no token gives zeros, and lse -infinity. The lengths, starts
- * and table are read on the device: a captured call replays with others.
+ * A row that sees no token gives zeros, and lse -infinity. Rows that a wait
+ * which ran out (rmsnorm_wait_timeouts) has cut off are left as they are. The
+ * lengths, starts and table are read on the device: a captured call replays with others.
  *   workspace: rmsnorm_kv4_attention_workspace_bytes(D) bytes, 16-byte
  *   aligned, the call's own until it is done; nothing in it needs clearing.
  * Limits (else RMSNORM_ERR_UNSUPPORTED): D 64 or 128; page_size a multiple of

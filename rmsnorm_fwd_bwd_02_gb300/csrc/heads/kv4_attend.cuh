@@ -354,6 +354,16 @@ struct Kv4Query {
 // of its run and the last; a CTA that joined its warps' sums uses its first.
 __device__ __forceinline__ int64_t kv4_part(uint32_t warp, bool later) { return 2 * (int64_t)warp + (later ? 1 : 0); }
 
+// A part that a wait which ran out has kept from being made: references of NaN,
+// which no part has otherwise. kv4_combine leaves its rows unwritten.
+template <int D, int NT>
+__device__ __forceinline__ void kv4_mark_lost(const Kv4Params &p, uint32_t warp, bool later)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane < 8 * NT)
+        p.ws[kv4_part(warp, later) * kv4_partial(D, NT) + 8 * NT * D + lane] = __int_as_float(0x7FFFFFFF);
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_attend(Kv4Params p)
 {
@@ -775,8 +785,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         atomicAdd(p.timeouts, 1u);
         sm_bad = 1;
     }
-    if (!joined)
+    if (!joined) {
+        if (!ok)                                                // the parts that this run still owed
+            for (int later = g.at - kKv4Extra > run0; later < 2; ++later)
+                kv4_mark_lost<D, NT>(p, gw, later);
         return;
+    }
 
     // join the warps' sums in their rings, which are empty now
     float *sums = reinterpret_cast<float *>(ring);
@@ -798,8 +812,11 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         }
     __syncthreads();
     const bool several = p.cluster > 1;
-    if (sm_bad && !several)
+    if (sm_bad && !several) {
+        if (p.cluster == 0 && warp == 0)
+            kv4_mark_lost<D, NT>(p, gw, false);
         return;
+    }
     if (p.cluster == 0)
         g = kv4_segment(s, first, cta0);
     const bool all = p.cluster > 0 || (cta0 <= g.at && cta1 == g.at + s.stages);
@@ -992,6 +1009,7 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
             continue;
         float mm = kKv4Least, ll = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool lost = false;
         for (int i = 0; i < parts; i += 8) {
             float m[8], l[8];
             float4 v[8];
@@ -1004,6 +1022,7 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                lost |= m[j] != m[j];
                 if (m[j] == kKv4Least)
                     continue;
                 const float up = fmaxf(mm, m[j]);
@@ -1014,6 +1033,8 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
                 a.z = a.z * f0 + v[j].z * f1; a.w = a.w * f0 + v[j].w * f1;
             }
         }
+        if (lost)
+            continue;
         const int i = qrow / p.G, hq = h * p.G + qrow - i * p.G;
         const float f = ll > 0.f || ll != ll ? gv / ll : 0.f;
         kv4_store<T>(p, s.q0 + i, hq, d, make_float4(a.x * f, a.y * f, a.z * f, a.w * f));

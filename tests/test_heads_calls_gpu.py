@@ -82,3 +82,37 @@ def test_pieces_of_prompts_between_other_tensor_memory_kernels(D):
         check(want[0], None, q, cache, table.cpu(), [900], [0, T])
     finally:
         rn.set_kv4_test(0)
+
+
+@pytest.mark.parametrize("kernel", [1, 3, 2], ids=["list", "clusters", "prompt"])
+@pytest.mark.parametrize("B,Hk", [(1, 1), (60, 4)])
+def test_rows_whose_waits_run_out_are_not_written(kernel, B, Hk):
+    """The test hook makes every stage's wait run out: the rows keep what was
+    there, whatever the workspace held. One sequence is split over many warps;
+    of sixty a warp has several, and parts of some."""
+    D, page, blocks = 128, 16, 60 if B == 1 else 6
+    cache = make_cache(B * blocks, Hk, page, D, 3)
+    table = table_of(B, blocks, B * blocks, 1).to(DEV)
+    g = torch.Generator().manual_seed(3)
+    most = blocks * page
+    lens = torch.randint(most // 2, most + 1, (B,), generator=g).to(torch.int32).to(DEV)
+    n = 1 if kernel == 3 or B > 1 else 2
+    q = normal((B * n, Hk * 4, D), BF16, 4)
+    s = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV)
+    out, lse = torch.full_like(q, 3.0), torch.full((B * n, Hk * 4), 4.0, device=DEV)
+    ws = torch.ones(rn.lib().rmsnorm_kv4_attention_workspace_bytes(D) // 4, device=DEV)
+    rn.wait_timeouts(reset=True)
+    rn.set_kv4_test(kernel)
+    rn.set_stream_test_fault(16, 2000)
+    try:
+        rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, out=out, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        rn.set_stream_test_fault(0, 0)
+    try:
+        assert rn.wait_timeouts(reset=True) > 0
+        assert bool((out == 3).all()) and bool((lse == 4).all())
+        rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, out=out, lse=lse, workspace=ws)
+        check(out, lse, q, cache, table.cpu(), lens.tolist(), s.tolist())
+    finally:
+        rn.set_kv4_test(0)
