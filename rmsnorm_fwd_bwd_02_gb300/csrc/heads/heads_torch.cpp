@@ -173,12 +173,12 @@ PyObject *rope_fwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t H = pq.h.heads + pk.h.heads;
 
     const c10::cuda::CUDAGuard guard(dev);
-    Outputs made((yq ? 0 : bytes_of(q.numel(), dtype)) + (k && !yk ? bytes_of(k->numel(), dtype) : 0) +
-                 (new_rstd ? bytes_of(T * H, at::kFloat) : 0));
+    // rstd has an allocation of its own: torch.save refuses tensors of two types in one storage
+    Outputs made((yq ? 0 : bytes_of(q.numel(), dtype)) + (k && !yk ? bytes_of(k->numel(), dtype) : 0));
     part_out(pq, yq, "yq", made, T, D, dtype, dev);
     if (k)
         part_out(pk, yk, "yk", made, T, D, dtype, dev);
-    const Tensor rstd = new_rstd ? made.dense({T, H}, at::kFloat) : Tensor();
+    const Tensor rstd = new_rstd ? Outputs().dense({T, H}, at::kFloat) : Tensor();
     const int st = g_fwd(&pq.h, k ? &pk.h : nullptr, &r,
                          new_rstd ? static_cast<float *>(rstd.data_ptr()) : nullptr, T, D, (float)eps, code,
                          stream_of(dev));
@@ -459,9 +459,8 @@ PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
 
     const c10::cuda::CUDAGuard guard(dev);
     const bool new_lse = want && !lse_in;
-    Outputs made((out_in ? 0 : bytes_of(q.numel(), dtype)) + (new_lse ? bytes_of(T * H, at::kFloat) : 0));
-    const Tensor out = out_in ? *out_in : made.dense({T, H, D}, dtype);
-    const Tensor lse = lse_in ? *lse_in : new_lse ? made.dense({T, H}, at::kFloat) : Tensor();
+    const Tensor out = out_in ? *out_in : Outputs().dense({T, H, D}, dtype);
+    const Tensor lse = lse_in ? *lse_in : new_lse ? Outputs().dense({T, H}, at::kFloat) : Tensor();
     // the call's own memory of this stream, free again for what runs behind it
     const Tensor ws = ws_in ? *ws_in : Outputs().dense({(int64_t)g_attend_bytes(D)}, at::kByte);
     const int st = g_attend(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,

@@ -106,7 +106,8 @@ float *fp32(const Tensor &t, const char *name, at::IntArrayRef shape, at::Device
 // allocation each, so that none holds back another's. So do those of the
 // quantisation, of any size: a program keeps and saves them as a model's
 // weights, and torch.save refuses tensors of two types in one storage (a
-// small call takes 3.8 us on the host, 3.4 where the two share).
+// small call takes 3.8 us on the host, 3.4 where the two share). The calls on
+// heads share one for outputs of one type only.
 class Outputs {
     static constexpr size_t kShared = 256 * 1024, kAlign = 256;
     c10::Storage shared_;

@@ -603,7 +603,8 @@ def rmsnorm_rope_fwd(q, positions, freq, k=None, wq=None, wk=None, yq=None, yk=N
     in pairs (i, i + rot / 2), or (2i, 2i + 1) when interleaved. positions and
     freq None: no rotation. Returns (yq, yk or None, rstd or None); rstd
     [T, q heads + k heads] is what the backward wants of a norm (rows of heads
-    without one hold anything). Outputs that are not passed are dense and may share one allocation."""
+    without one hold anything). Outputs that are not passed are dense; yq and
+    yk share one allocation where they take 256 KB or less together."""
     if stream is not None:
         with _on_stream(q, stream):
             return _heads().rope_fwd(q, positions, freq, k, wq, wk, yq, yk, eps, interleaved, amplitude,

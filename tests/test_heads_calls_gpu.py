@@ -116,3 +116,26 @@ def test_rows_whose_waits_run_out_are_not_written(kernel, B, Hk):
         check(out, lse, q, cache, table.cpu(), lens.tolist(), s.tolist())
     finally:
         rn.set_kv4_test(0)
+
+
+def saved(**tensors):
+    f = io.BytesIO()
+    torch.save(tensors, f)
+    f.seek(0)
+    back = torch.load(f)
+    assert all(torch.equal(back[k], t) for k, t in tensors.items())
+
+
+def test_small_outputs_can_be_saved_together():
+    """torch.save refuses tensors of two types in one storage."""
+    T, D = 5, 64
+    q, k, w = normal((T, 4, D), BF16, 1), normal((T, 2, D), BF16, 2), normal((D,), BF16, 3, 0.1, 1.0)
+    f, pos = freqs(D), torch.arange(T, device=DEV)
+    yq, yk, rstd = rn.rmsnorm_rope_fwd(q, pos, f, k=k, wq=w, wk=w)
+    saved(yq=yq, yk=yk, rstd=rstd)
+    dq, dk, dwq, dwk = rn.rmsnorm_rope_bwd(q, q, pos, f, dyk=k, k=k, wq=w, wk=w, rstd=rstd)
+    saved(dq=dq, dk=dk, dwq=dwq, dwk=dwk)
+    cache = make_cache(4, 2, 16, D, 3)
+    out, lse = rn.rmsnorm_kv4_attention(q[:1], cache, torch.arange(4, dtype=torch.int32, device=DEV)[None],
+                                        torch.tensor([50], dtype=torch.int32, device=DEV), want_lse=True)
+    saved(out=out, lse=lse)
