@@ -836,7 +836,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rms_rope_bwd(RopeGradParams p
                     rs = rsqrtf(fmaf(lanes_sum(hsum(ss), p.shift), p.inv_d, p.eps));
                 if (!on)
                     rs = 0.f;                            // no row: nothing to add
-                const float k = -rs * rs * rs * (lanes_sum(hsum(sc), p.shift) * p.inv_d);
+                // (rstd c first: rstd cubed alone leaves fp32's range for rows of 1e-13 or 1e15)
+                const float k = -(rs * (lanes_sum(hsum(sc), p.shift) * p.inv_d)) * rs * rs;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll

@@ -139,3 +139,23 @@ def test_small_outputs_can_be_saved_together():
     out, lse = rn.rmsnorm_kv4_attention(q[:1], cache, torch.arange(4, dtype=torch.int32, device=DEV)[None],
                                         torch.tensor([50], dtype=torch.int32, device=DEV), want_lse=True)
     saved(out=out, lse=lse)
+
+
+@pytest.mark.parametrize("size", [1e-18, 1e-15, 1e-13, 1e13, 1e16, 1e18])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keep", [False, True])
+def test_backward_over_the_number_range(size, dtype, keep):
+    """Rows whose 1 / rms cubed leaves fp32's range, with eps 0: as test_rope_gpu's
+    backward bound."""
+    T, H, D = 9, 3, 128
+    f, pos, w = freqs(D), torch.arange(T, device=DEV) * 3, normal((D,), dtype, 1, 0.1, 1.0)
+    x, dy = normal((T, H, D), dtype, 2, size), normal((T, H, D), dtype, 3)
+    rstd = rn.rmsnorm_rope_fwd(x, pos, f, wq=w, eps=0.0)[2]
+    dx, _, dw, _ = rn.rmsnorm_rope_bwd(dy, x, pos, f, wq=w, rstd=rstd if keep else None, eps=0.0)
+    x64, w64 = x.to(F64), w.to(F64)
+    r = 1 / torch.sqrt((x64 * x64).mean(-1, keepdim=True))
+    g, mag = turn(dy.to(F64), pos, f, False, back=True)
+    want = r * (w64 * g - x64 * r * r * (w64 * g * x64).mean(-1, keepdim=True))
+    terms = r * (w64.abs() * mag + x64.abs() * r * r * (w64.abs() * mag * x64.abs()).mean(-1, keepdim=True))
+    close(dx, want, 64 * ULP * terms + half_step(want, dtype))
+    close(dw, (g * x64 * r).sum((0, 1)), (T * H / 64 + 128) * ULP * (mag * (x64 * r).abs()).sum((0, 1)))
