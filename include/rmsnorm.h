@@ -445,7 +445,8 @@ typedef struct {
  * memory. No position loses the angle's fraction, far or negative: freq / 2
  * pi is held as a 64-bit fraction of a turn, and the product with the 64-bit
  * position is taken modulo whole turns, within |position| 2^-64 + 2^-32 of a
- * turn. A NULL rotation, or rot 0, turns nothing.
+ * turn for |freq| up to 2^64 (above, freq's own turns are lost by and by). A
+ * NULL rotation, or rot 0, turns nothing.
  */
 typedef struct {
     const void *positions;      /* [T] int32 or int64 */

@@ -81,8 +81,10 @@ __device__ __forceinline__ int64_t ld_index(const void *p, int64_t i, int wide)
                 : (int64_t)__ldg(static_cast<const int *>(p) + i);
 }
 
-// freq (radians a position) as a fraction of a turn, 2^64 to the turn: its 53
-// bits times 1 / (2 pi) in 66, shifted by its exponent, whole turns dropped.
+// freq (radians a position) as a fraction of a turn, 2^64 to the turn, rounded to
+// the nearest, whole turns dropped: its 53 bits times 2^130 / (2 pi), a constant of
+// 128 bits, shifted by its exponent. The constant is within half a unit, so the
+// fraction within 1/2 + |freq| 2^-67 units of 2^-64 (with 64 bits of it, 2^-3 |freq|).
 // In integers: 64-bit floating point is slow here (one token of 16 heads took
 // 5.0 us with it, 3.6 without).
 __device__ __forceinline__ uint64_t turn_fraction(double freq)
@@ -90,14 +92,19 @@ __device__ __forceinline__ uint64_t turn_fraction(double freq)
     const uint64_t bits = (uint64_t)__double_as_longlong(freq);
     const int e = (int)(bits >> 52) & 0x7FF;
     const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
-    const uint64_t k = 11743562013128004906ull;          // 2^66 / (2 pi)
-    const uint64_t hi = __umul64hi(m, k), lo = m * k;
-    const int right = 1077 - e;                          // of the 128-bit product
-    uint64_t t = right >= 128 ? 0
-                 : right >= 64 ? hi >> (right - 64)
-                 : right > 0   ? hi << (64 - right) | lo >> right
-                 : right > -64 ? lo << -right
-                               : 0;
+    const uint64_t k1 = 11743562013128004905ull, k0 = 18169587780923219393ull;   // 2^130 / (2 pi)
+    const uint64_t w0 = m * k0, lo = m * k1, w1 = lo + __umul64hi(m, k0);
+    const uint64_t w2 = __umul64hi(m, k1) + (w1 < lo ? 1 : 0);
+    auto word = [&](int i) { return i == 0 ? w0 : (i == 1 ? w1 : (i == 2 ? w2 : 0)); };
+    const int right = 1141 - e;                          // of the product's three words
+    uint64_t t = 0;
+    if (right > 0) {
+        const int i = right >> 6, by = right & 63, last = right - 1;
+        t = by ? word(i) >> by | word(i + 1) << (64 - by) : word(i);
+        t += word(last >> 6) >> (last & 63) & 1;
+    } else if (right > -64) {
+        t = w0 << -right;
+    }
     if (e == 0)
         t = 0;                                           // zero and what is no normal number
     return bits >> 63 ? 0 - t : t;

@@ -159,3 +159,20 @@ def test_backward_over_the_number_range(size, dtype, keep):
     terms = r * (w64.abs() * mag + x64.abs() * r * r * (w64.abs() * mag * x64.abs()).mean(-1, keepdim=True))
     close(dx, want, 64 * ULP * terms + half_step(want, dtype))
     close(dw, (g * x64 * r).sum((0, 1)), (T * H / 64 + 128) * ULP * (mag * (x64 * r).abs()).sum((0, 1)))
+
+
+def test_frequencies_of_any_size():
+    """The header's bound against exact rational arithmetic: an angle is within
+    |position| 2^-64 + 2^-32 of a turn for |freq| up to 2^64."""
+    freq = [1e9, -(2.0 ** 40), 12345.678, 1e6 / 3, 2 * math.pi * 2 ** 30, 3e15, 2.0 ** 63, 1e-9]
+    pos = [1, 1 << 20, (1 << 20) + 1, 1 << 40, -(1 << 33) - 5, -77, 1 << 45, 999999937]
+    f = torch.tensor(freq, dtype=F64, device=DEV)
+    for adjacent in (False, True):
+        x = normal((len(pos), 2, 16), F32, 7)
+        y, _, _ = rn.rmsnorm_rope_fwd(x, torch.tensor(pos, device=DEV), f, interleaved=adjacent)
+        for i, t in enumerate(pos):
+            angle = torch.tensor([float(Fraction(w) * t / (2 * PI) % 1 * 2 * PI) for w in freq], dtype=F64,
+                                 device=DEV)
+            want, size = turn(x[i:i + 1].to(F64), torch.ones(1, device=DEV), angle, adjacent)
+            off = (abs(t) * 2.0 ** -64 + 2.0 ** -32) * 2 * math.pi
+            close(y[i:i + 1], want, (24 * ULP + off) * size)
