@@ -488,7 +488,7 @@ int rmsnorm_rope_fwd(const rmsnorm_heads *q, const rmsnorm_heads *k,
  *   16-byte aligned, the call's own until it is done (not read where no part
  *   has a weight; it may then be NULL).
  * Aliasing: dx may be exactly dy or exactly x; nothing else may share a byte.
- * T == 0 sets dw to zero.
+ * T == 0, or a k without heads, sets its dw to zero.
  */
 int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k,
                      const rmsnorm_rotation *rot, const float *rstd,

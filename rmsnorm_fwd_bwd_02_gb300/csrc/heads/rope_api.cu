@@ -122,10 +122,12 @@ int check_rows(const rmsnorm_heads *r, int64_t T, int64_t D, size_t es, bool has
         return RMSNORM_ERR_BAD_SHAPE;
     if (r->heads > INT32_MAX / 2)
         return RMSNORM_ERR_UNSUPPORTED;
+    if (r->heads == 0)
+        return RMSNORM_OK;                      // whatever its strides
     if (!rows_within({T, r->heads, 1}, {r->x_token, r->x_head, 0}, D) ||
         (has_y && !rows_apart({T, r->heads, 1}, {r->y_token, r->y_head, 0}, D)))
         return RMSNORM_ERR_BAD_STRIDE;
-    if (T == 0 || r->heads == 0)
+    if (T == 0)
         return RMSNORM_OK;
     if (!r->x || !r->y)
         return RMSNORM_ERR_NULLPTR;
@@ -358,7 +360,7 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
         return st;
     if (!q)
         return RMSNORM_ERR_NULLPTR;
-    const rmsnorm_heads_grad *parts[2] = {q, k && k->heads != 0 ? k : nullptr};
+    const rmsnorm_heads_grad *parts[2] = {q, k};    // (k without heads: its dw is zero)
     const size_t es = elem_size(dtype);
     if (q->heads < 1 || (k && k->heads < 0))
         return RMSNORM_ERR_BAD_SHAPE;
@@ -373,9 +375,9 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
             return RMSNORM_ERR_UNSUPPORTED;
         const bool norm = r->w != nullptr;
         any_norm |= norm;
-        if (!rows_within({T, r->heads, 1}, {r->dy_token, r->dy_head, 0}, D) ||
-            (norm && !rows_within({T, r->heads, 1}, {r->x_token, r->x_head, 0}, D)) ||
-            !rows_apart({T, r->heads, 1}, {r->dx_token, r->dx_head, 0}, D))
+        if (r->heads > 0 && (!rows_within({T, r->heads, 1}, {r->dy_token, r->dy_head, 0}, D) ||
+                             (norm && !rows_within({T, r->heads, 1}, {r->x_token, r->x_head, 0}, D)) ||
+                             !rows_apart({T, r->heads, 1}, {r->dx_token, r->dx_head, 0}, D)))
             return RMSNORM_ERR_BAD_STRIDE;
         if (norm && !r->dw)
             return RMSNORM_ERR_NULLPTR;
@@ -383,7 +385,7 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
             return RMSNORM_ERR_MISALIGNED;
         if (norm)
             sw[i] = flat(r->dw, (size_t)D * 4);
-        if (T == 0)
+        if (T == 0 || r->heads == 0)
             continue;
         if (!r->dy || !r->dx || (norm && !r->x))
             return RMSNORM_ERR_NULLPTR;
@@ -433,6 +435,8 @@ int rmsnorm_rope_bwd(const rmsnorm_heads_grad *q, const rmsnorm_heads_grad *k, c
             continue;
         p.part[i] = {r->dy, r->dy_token, r->dy_head, r->x, r->x_token, r->x_head, r->w,
                      r->dx, r->dx_token, r->dx_head, r->dw, (int)r->heads, 0};
+        if (r->heads == 0)
+            continue;
         const int64_t t = T > 1, h = r->heads > 1;
         rows[n++] = {r->dy, t * r->dy_token, h * r->dy_head, 0};
         rows[n++] = {r->dx, t * r->dx_token, h * r->dx_head, 0};

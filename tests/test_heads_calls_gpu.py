@@ -176,3 +176,41 @@ def test_frequencies_of_any_size():
             want, size = turn(x[i:i + 1].to(F64), torch.ones(1, device=DEV), angle, adjacent)
             off = (abs(t) * 2.0 ** -64 + 2.0 ** -32) * 2 * math.pi
             close(y[i:i + 1], want, (24 * ULP + off) * size)
+
+
+@pytest.mark.parametrize("norm_q", [False, True])
+def test_gradient_of_a_norm_without_heads(norm_q):
+    """k with no heads: its weight's gradient is a sum over nothing."""
+    T, D = 6, 64
+    q, k, w = normal((T, 2, D), BF16, 1), torch.empty(T, 0, D, dtype=BF16, device=DEV), normal((D,), BF16, 2, 0.1, 1.0)
+    f, pos = freqs(D), torch.arange(T, device=DEV)
+    wq = w if norm_q else None
+    # what the gradients' allocation held before
+    junk = [torch.full((n,), float("nan"), device=DEV) for n in (64, 128, 256, 512)]
+    torch.cuda.synchronize()
+    del junk
+    dq, dk, dwq, dwk = rn.rmsnorm_rope_bwd(q, q if norm_q else None, pos, f, dyk=k, k=k, wq=wq, wk=w)
+    assert dk.shape == k.shape and bool((dwk == 0).all())
+    check_bwd(q, q, wq, dq, dwq, pos, f, False)
+
+
+def test_parts_without_heads():
+    """k, or the append's q, with no heads, made by the call or windows of
+    another tensor."""
+    T, D = 6, 64
+    x, w = normal((T, 5, D), BF16, 1), normal((D,), BF16, 2, 0.1, 1.0)
+    f, pos = freqs(D), torch.arange(T, device=DEV)
+    for none in (torch.empty(T, 0, D, dtype=BF16, device=DEV), x[:, 5:], x[:, 2:2].transpose(0, 1)[:0].transpose(0, 1)):
+        yq, yk, rstd = rn.rmsnorm_rope_fwd(x, pos, f, k=none, wq=w, wk=w)
+        check_fwd(yq, x, w, pos, f, False)
+        assert yk.shape == (T, 0, D) and rstd.shape == (T, 5)
+        leaves = [t.clone().requires_grad_() for t in (x, none, w, w)]
+        yq, yk = autograd.rms_norm_rope(*leaves[:2], pos, f, *leaves[2:])
+        yq.backward(x)
+        check_bwd(x, x, w, leaves[0].grad, rn.rmsnorm_rope_bwd(x, x, pos, f, wq=w)[2], pos, f, False)
+        assert bool((leaves[3].grad == 0).all())
+        cache = rn.kv4_cache(1, 5, 16, D, device=DEV)
+        assert rn.rmsnorm_rope_append_kv4(x, x, pos, f, pos, cache, q=none).shape == (T, 0, D)
+        again = rn.kv4_cache(1, 5, 16, D, device=DEV)
+        rn.rmsnorm_rope_append_kv4(x, x, pos, f, pos, again)
+        assert torch.equal(cache, again) and bool(cache.any())
