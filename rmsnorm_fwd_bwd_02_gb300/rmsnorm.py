@@ -583,6 +583,8 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=None,
     elif scaling == "yarn":
         if original is None or original <= 0:
             raise ValueError("'yarn' needs original, the positions that the model was trained on")
+        if not (base > 1 and beta_fast > 0 and beta_slow > 0):
+            raise ValueError("'yarn' needs a base above 1, beta_fast and beta_slow above 0")
 
         def pair(turns):        # the pair (as a real number) that turns so often in `original`
             return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))

@@ -3,6 +3,7 @@ test_heads_host.py. Made-up addresses; every call below fails a check (or has
 nothing to do), so nothing is launched."""
 import pytest
 
+from rmsnorm_fwd_bwd_02_gb300 import rmsnorm as rn
 from tests.test_abi_host import ALIAS, OK, lib  # noqa: F401
 from tests.test_heads_host import AT, append, append4, bwd, fwd, grad, heads
 
@@ -40,3 +41,13 @@ def test_q_does_not_go_over_the_heads_scales(lib):  # noqa: F811
 def test_no_tokens_want_no_cache(lib):  # noqa: F811
     assert append4(lib, T=0, cache=None, slots=None) == OK
     assert append(lib, T=0, k=heads(x=None, y=None), v=heads(x=None, y=None), slots=None) == OK
+
+
+@pytest.mark.parametrize("bad", [{"base": 1.0}, {"base": 0.5}, {"beta_fast": 0.0}, {"beta_slow": 0.0},
+                                 {"beta_slow": -1.0}, {"original": 0}])
+def test_yarn_refuses_what_has_no_logarithm(bad):
+    """A base of one turns every pair alike: no pair turns so and so often."""
+    args = {"rot": 64, "base": 1e4, "scaling": "yarn", "factor": 4.0, "original": 4096, "device": "cpu"}
+    rn.rope_frequencies(**args)
+    with pytest.raises(ValueError):
+        rn.rope_frequencies(**{**args, **bad})
