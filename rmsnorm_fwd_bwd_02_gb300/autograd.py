@@ -148,18 +148,13 @@ class RMSNormRopeFunction(torch.autograd.Function):
         ctx.save_for_backward(q if wq is not None else None, k if wk is not None else None, wq, wk,
                               positions, freq, rstd)
         ctx.how = (float(eps), interleaved, amplitude)
-        ctx.shapes = (q.shape, k.shape, q.dtype, q.device)
         return yq, yk
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dyq, dyk):
         q, k, wq, wk, positions, freq, rstd = ctx.saved_tensors
-        sq, sk, dtype, dev = ctx.shapes
         eps, interleaved, amplitude = ctx.how
-        # an output that nothing used brings no gradient
-        dyq = torch.zeros(sq, dtype=dtype, device=dev) if dyq is None else dyq
-        dyk = torch.zeros(sk, dtype=dtype, device=dev) if dyk is None else dyk
         dq, dk, dwq, dwk = _rn.rmsnorm_rope_bwd(
             _heads3d(dyq), None if q is None else _heads3d(q), positions, freq, dyk=_heads3d(dyk),
             k=None if k is None else _heads3d(k), wq=wq, wk=wk, rstd=rstd, eps=eps,

@@ -214,3 +214,27 @@ def test_parts_without_heads():
         again = rn.kv4_cache(1, 5, 16, D, device=DEV)
         rn.rmsnorm_rope_append_kv4(x, x, pos, f, pos, again)
         assert torch.equal(cache, again) and bool(cache.any())
+
+
+def test_autograd_gives_each_leaf_its_own_gradient():
+    T, Hq, Hk, D = 19, 4, 2, 64
+    f, pos = freqs(32), torch.arange(T, device=DEV) * 11
+    for interleaved in (False, True):
+        q, k = normal((T, Hq, D), F32, 20).requires_grad_(), normal((T, Hk, D), F32, 21).requires_grad_()
+        wq, wk = normal((D,), F32, 22, 0.3, 1.0).requires_grad_(), normal((D,), F32, 23, 0.3, 2.0).requires_grad_()
+        dyq, dyk = normal((T, Hq, D), F32, 24), normal((T, Hk, D), F32, 25)
+        yq, yk = autograd.rms_norm_rope(q, k, pos, f, wq, wk, interleaved=interleaved, amplitude=1.25)
+        torch.autograd.backward([yq, yk], [dyq, dyk])
+        for x, w, y, dy in ((q, wq, yq, dyq), (k, wk, yk, dyk)):
+            check_fwd(y.detach(), x.detach(), w.detach(), pos, f, interleaved, 1.25)
+            check_bwd(dy, x.detach(), w.detach(), x.grad, w.grad, pos, f, interleaved, 1.25)
+        # outputs that nothing uses: zeros for what depends on them alone
+        for used in (0, 1):
+            leaves = [t.detach().clone().requires_grad_() for t in (q, k, wq, wk)]
+            y = autograd.rms_norm_rope(*leaves[:2], pos, f, *leaves[2:], interleaved=interleaved, amplitude=1.25)
+            y[used].backward((dyq, dyk)[used])
+            for i, (leaf, whole) in enumerate(zip(leaves, (q, k, wq, wk))):
+                if i % 2 == used:
+                    assert torch.equal(leaf.grad, whole.grad)
+                else:
+                    assert bool((leaf.grad == 0).all())
