@@ -20,6 +20,13 @@ decltype(&rmsnorm_fwd_fp8) g_fwd = nullptr;
 decltype(&rmsnorm_quant_fp8) g_quant = nullptr;
 decltype(&rmsnorm_gemm_fp8) g_gemm = nullptr;
 
+ScalarType dtype_of(PyObject *o, const char *name)
+{
+    if (!THPDtype_Check(o))
+        refuse(c10::str(name, " must be a torch.dtype"));
+    return reinterpret_cast<THPDtype *>(o)->scalar_type;
+}
+
 int fp8_code(ScalarType t, const char *name)
 {
     switch (t) {
@@ -28,6 +35,29 @@ int fp8_code(ScalarType t, const char *name)
     default:
         refuse(c10::str(name, " must be float8_e4m3fn or float8_e5m2, got ", t));
     }
+}
+
+void two_d(const Tensor &t, const char *name)
+{
+    if (t.dim() != 2)
+        refuse(c10::str(name, " must be 2-D, got ", t.sizes()));
+    if (!t.is_cuda())
+        refuse(c10::str(name, " must be a CUDA tensor, got ", t.device()));
+}
+
+// Row stride (elements) of a [M, H] tensor with unit column stride; H for
+// one row.
+int64_t row_stride(const Tensor &t, const char *name, int64_t M, int64_t H, ScalarType dtype,
+                   at::Device dev)
+{
+    on_device(t, name, dev);
+    if (t.scalar_type() != dtype)
+        refuse(c10::str(name, " must be ", dtype, ", got ", t.scalar_type()));
+    if (t.dim() != 2 || t.size(0) != M || t.size(1) != H)
+        refuse(c10::str(name, " must be of shape [", M, ", ", H, "], got ", t.sizes()));
+    if (t.stride(1) != 1 && H > 1)
+        refuse(c10::str(name, " must have unit column stride"));
+    return M > 1 ? t.stride(0) : H;
 }
 
 // The row stride of an 8-bit [M, H] output: rows start at multiples of 16

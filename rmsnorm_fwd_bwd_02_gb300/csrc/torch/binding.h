@@ -41,13 +41,6 @@ const Tensor *optional(PyObject *o, const char *name)
     return o == Py_None ? nullptr : &tensor(o, name);
 }
 
-ScalarType dtype_of(PyObject *o, const char *name)
-{
-    if (!THPDtype_Check(o))
-        refuse(c10::str(name, " must be a torch.dtype"));
-    return reinterpret_cast<THPDtype *>(o)->scalar_type;
-}
-
 // rmsnorm_dtype of a row tensor
 int row_code(ScalarType t)
 {
@@ -63,29 +56,6 @@ void on_device(const Tensor &t, const char *name, at::Device dev)
 {
     if (t.device() != dev)
         refuse(c10::str(name, " must be on ", dev, ", got ", t.device()));
-}
-
-void two_d(const Tensor &t, const char *name)
-{
-    if (t.dim() != 2)
-        refuse(c10::str(name, " must be 2-D, got ", t.sizes()));
-    if (!t.is_cuda())
-        refuse(c10::str(name, " must be a CUDA tensor, got ", t.device()));
-}
-
-// Row stride (elements) of a [M, H] tensor with unit column stride; H for
-// one row.
-int64_t row_stride(const Tensor &t, const char *name, int64_t M, int64_t H, ScalarType dtype,
-                   at::Device dev)
-{
-    on_device(t, name, dev);
-    if (t.scalar_type() != dtype)
-        refuse(c10::str(name, " must be ", dtype, ", got ", t.scalar_type()));
-    if (t.dim() != 2 || t.size(0) != M || t.size(1) != H)
-        refuse(c10::str(name, " must be of shape [", M, ", ", H, "], got ", t.sizes()));
-    if (t.stride(1) != 1 && H > 1)
-        refuse(c10::str(name, " must have unit column stride"));
-    return M > 1 ? t.stride(0) : H;
 }
 
 float *fp32(const Tensor &t, const char *name, at::IntArrayRef shape, at::Device dev)

@@ -678,7 +678,9 @@ def rmsnorm_kv4_read(cache, slots, stream=None):
 
 def set_kv4_test(kernel: int):
     """Test hook: attention over a 4-bit cache by the kernel for few rows a
-    sequence (1) or for pieces of prompts (2) at any size (0: by size)."""
+    sequence with its work list (1) or by clusters where the segments are few
+    enough (3), or, with q_starts, by the one for pieces of prompts (2), at
+    any size (0: by size)."""
     lib().rmsnorm_set_kv4_test(int(kernel))
 
 
