@@ -238,3 +238,68 @@ def test_autograd_gives_each_leaf_its_own_gradient():
                     assert torch.equal(leaf.grad, whole.grad)
                 else:
                     assert bool((leaf.grad == 0).all())
+
+
+@pytest.mark.parametrize("kernel", [1, 3], ids=["list", "clusters"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_fp16_rows_keep_their_second_half(kernel, D):
+    """Weights that are nearly equal over values of both signs: a row is small
+    beside the sum of p |v|, and so is its own rounding; a weight rounded to
+    fp16 would show. q has four features that are not zero, so a score is a
+    sum of four products, each within 8 2^-24 of itself with the factors'
+    roundings; less the reference it is rounded at 8, 2^-21; exp2 2^-22; the
+    halves together 2^-22: below 2^-19 of the weight, and twice that for the
+    quotient. Both halves of 32 tokens are four MMAs, each within 17 2^-23 of
+    its magnitudes."""
+    B, Hk, G, page, L = 6, 2, 4, 16, 32
+    cache = rn.kv4_cache(B * 2, Hk, page, D, device=DEV)
+    n = B * 2 * page
+    k = normal((n, Hk, D), F32, 1)
+    size = normal((n // 2, Hk, D), F32, 2)
+    v = torch.stack([size, -size], dim=1).flatten(0, 1)
+    rn.rmsnorm_rope_append_kv4(k, v, None, None, torch.arange(n, device=DEV), cache)
+    q = torch.zeros(B, Hk * G, D, dtype=F16, device=DEV)
+    q[..., 3::D // 4] = normal((B, Hk * G, 4), F16, 3, 0.03)
+    table = torch.arange(B * 2, dtype=torch.int32).view(B, 2)
+    rn.set_kv4_test(kernel)
+    try:
+        out, _ = rn.rmsnorm_kv4_attention(q, cache, table.to(DEV), torch.full((B,), L, dtype=torch.int32, device=DEV))
+    finally:
+        rn.set_kv4_test(0)
+    kk, vv = (t.to(DEV) for t in dense(cache, D))
+    kk, vv = (t[table.to(DEV).long()].transpose(1, 2).reshape(B, Hk, L, D) for t in (kk, vv))
+    x = torch.einsum("bhgd,bhld->bhgl", q.to(F64).view(B, Hk, G, D), kk) / math.sqrt(D)
+    p = torch.exp(x - x.amax(-1, keepdim=True))
+
+    def row(weights):
+        return torch.einsum("bhgl,bhld->bhgd", weights, vv) / p.sum(-1, keepdim=True)
+
+    want, mag = row(p), torch.einsum("bhgl,bhld->bhgd", p, vv.abs()) / p.sum(-1, keepdim=True)
+    tol = (2 * 2.0 ** -19 + 4 * 17 * 2.0 ** -23) * mag + half_step(want, F16)
+    close(out.view_as(want), want, tol)
+    # the bound would show weights of one half
+    one = row((p * 256).to(F16).to(F64) / 256)
+    assert float(((one - want).abs() > tol).double().mean()) > 0.3
+
+
+@pytest.mark.parametrize("byte", [0x7F, 0x80, 0xF8])
+@pytest.mark.parametrize("kernel", [1, 3, 2], ids=["list", "clusters", "prompt"])
+def test_bytes_behind_a_sequence_change_nothing(kernel, byte):
+    """Whole tiles behind the end, and a page that the table does not reach,
+    filled with bytes that are NaN or extreme as scales."""
+    D, page, Hk = 64, 48, 2
+    cache = make_cache(6, Hk, page, D, 7)
+    table = torch.tensor([[3, 5], [2, 4]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([64, 41], dtype=torch.int32, device=DEV)     # 64: page 5's first tile; 41: page 2's third
+    s = torch.tensor([0, 3, 5], dtype=torch.int32, device=DEV)
+    q = normal((5, 4, D), BF16, 1)
+    bad = cache.clone()
+    bad[5, :, 1:], bad[4], bad[0], bad[1] = byte, byte, byte, byte
+    rn.set_kv4_test(kernel)
+    try:
+        a, la = rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, want_lse=True)
+        b, lb = rn.rmsnorm_kv4_attention(q, bad, table, lens, q_starts=s, want_lse=True)
+    finally:
+        rn.set_kv4_test(0)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    check(a, la, q, cache, table.cpu(), [64, 41], [0, 3, 5])
