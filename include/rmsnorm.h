@@ -579,12 +579,15 @@ int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
  *   sequence in order. Tokens in a page outside the cache count as masked;
  *   seq_lens [B] int32: tokens cached, at most blocks * page_size count;
  *   q_starts [B + 1] int32: sequence b has the query tokens q_starts[b] to
- *   q_starts[b + 1] - 1; NULL: one token each (T == B, else
- *   RMSNORM_ERR_BAD_SHAPE). Rows of q that belong to no sequence are not
- *   read, and those of out and lse are left as they are.
+ *   q_starts[b + 1] - 1, where the starts run backwards none; NULL: one token
+ *   each (T == B, else RMSNORM_ERR_BAD_SHAPE). A row belongs to one sequence:
+ *   of one that starts give to several any may be written, or none. Rows of
+ *   q that belong to no sequence are not read, and those of out and lse are
+ *   left as they are.
  * A row that sees no token gives zeros, and lse -infinity. Rows that a wait
  * which ran out (rmsnorm_wait_timeouts) has cut off are left as they are. The
- * lengths, starts and table are read on the device: a captured call replays with others.
+ * lengths, starts and table are read on the device: a captured call replays
+ * with others.
  *   workspace: rmsnorm_kv4_attention_workspace_bytes(D) bytes, 16-byte
  *   aligned, the call's own until it is done; nothing in it needs clearing.
  * Limits (else RMSNORM_ERR_UNSUPPORTED): D 64 or 128; page_size a multiple of

@@ -147,6 +147,12 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const Kv4Params &p, int b)
     return s;
 }
 
+// Sums of entries stop at 2^31 - 1. Sound starts stay below (the host sees to
+// it); rows that several sequences claim, of starts that run back and forth,
+// could pass 2^32 and come to segments that are none. Such a list is not worked on.
+constexpr uint32_t kKv4TooMany = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t kv4_add(uint32_t a, uint32_t b) { return min(a + b, kKv4TooMany); }
+
 // Where in the list (of fewer than 2^31 entries) the sequences begin: the sums
 // of 32 sequences at a time, the last such run of them in the lanes.
 struct Kv4List {
@@ -166,7 +172,7 @@ struct Kv4List {
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if ((threadIdx.x & 31) >= o)
-                sum += t;
+                sum = kv4_add(sum, t);
         }
     }
     __device__ __forceinline__ uint32_t all() const { return __shfl_sync(0xFFFFFFFFu, sum, 31); }
@@ -175,10 +181,10 @@ struct Kv4List {
         before = total = 0;
         for (int from = 32; from < p.B; from += 32) {
             load<NT>(p, from);
-            total += all();
+            total = kv4_add(total, all());
         }
         load<NT>(p, 0);
-        total += all();
+        total = kv4_add(total, all());
     }
     // The sequence that holds entry u < total, and the entries before it.
     template <int NT>
@@ -412,6 +418,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
         run1 = min(run0 + each, 1 + (uint32_t)s.stages);
     } else {
         list.init<NT>(p);
+        if (list.total == kKv4TooMany)
+            return;                                             // for the whole grid
         const uint32_t warps = gridDim.x * kKv4Warps, C = (list.total + warps - 1) / warps;
         // (unsigned sums below 2^31 + 2^15 each)
         cta0 = min(blockIdx.x * kKv4Warps * C, list.total);
@@ -954,8 +962,8 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t a = __shfl_up_sync(0xFFFFFFFFu, sn, o), b = __shfl_up_sync(0xFFFFFFFFu, sv, o);
             if (lane >= o) {
-                sn += a;
-                sv += b;
+                sn = kv4_add(sn, a);
+                sv = kv4_add(sv, b);
             }
         }
         const unsigned at = __ballot_sync(0xFFFFFFFFu, segs + sn > blockIdx.x);
@@ -969,10 +977,10 @@ __global__ void __launch_bounds__(256) kv4_combine(Kv4Params p, int ctas)
             s.tiles = __shfl_sync(0xFFFFFFFFu, t.tiles, l);
             s.stages = __shfl_sync(0xFFFFFFFFu, t.stages, l);
         }
-        segs += __shfl_sync(0xFFFFFFFFu, sn, 31);
-        entries += __shfl_sync(0xFFFFFFFFu, sv, 31);
+        segs = kv4_add(segs, __shfl_sync(0xFFFFFFFFu, sn, 31));
+        entries = kv4_add(entries, __shfl_sync(0xFFFFFFFFu, sv, 31));
     }
-    if (!found || s.stages == 0)
+    if (!found || s.stages == 0 || entries == kKv4TooMany)
         return;
     const uint32_t warps = ctas * kKv4Warps, C = (entries + warps - 1) / warps;
     const uint32_t start = first + seg * s.cost(), end = start + s.cost();

@@ -303,3 +303,30 @@ def test_bytes_behind_a_sequence_change_nothing(kernel, byte):
         rn.set_kv4_test(0)
     assert torch.equal(a, b) and torch.equal(la, lb)
     check(a, la, q, cache, table.cpu(), [64, 41], [0, 3, 5])
+
+
+def test_starts_that_give_every_row_to_thousands_of_sequences():
+    """Starts that run back and forth: the rows of 2048 sequences each make
+    more than 2^32 entries together, and nothing is written. Then the same
+    rows once."""
+    B, T, Hk, G, D, page, blocks = 4096, 1 << 14, 8, 4, 64, 16, 125
+    cache = make_cache(2, Hk, page, D, 3)
+    table = torch.zeros(B, blocks, dtype=torch.int32, device=DEV)
+    lens = torch.full((B,), blocks * page, dtype=torch.int32, device=DEV)
+    tiles, cost = T * G // 8, blocks * page // 32 + 3
+    assert B // 2 * tiles * Hk * cost >= 1 << 32
+    s = torch.tensor([0, T], dtype=torch.int32, device=DEV).repeat(B // 2 + 1)[:B + 1].contiguous()
+    q = normal((T, Hk * G, D), BF16, 1)
+    out, lse = torch.full_like(q, 3.0), torch.full((T, Hk * G), 4.0, device=DEV)
+    rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, out=out, lse=lse)
+    assert rn.last_path() == rn.PATH_KV4_ATTENTION
+    torch.cuda.synchronize()
+    assert bool((out == 3).all()) and bool((lse == 4).all())
+    s = (torch.arange(B + 1, device=DEV) * (T // B)).to(torch.int32)
+    rn.rmsnorm_kv4_attention(q, cache, table, lens, q_starts=s, out=out, lse=lse)
+    assert rn.last_path() == rn.PATH_KV4_ATTENTION
+    first = 8
+    check(out[:first * 4], lse[:first * 4], q[:first * 4], cache, table[:first].cpu(), [blocks * page] * first,
+          s[:first + 1].tolist())
+    # every sequence sees the same tokens
+    assert bool(torch.isfinite(lse).all())
