@@ -469,7 +469,9 @@ typedef struct {
  *   may have a weight each, or one of them none;
  *   rstd [T, q heads + k heads] fp32 out or NULL (rows of heads without a
  *   weight are left as they are).
- * Aliasing: y may be exactly x (same strides); nothing else may share a byte.
+ * Aliasing: y may be exactly x (same start and strides); nothing else may
+ * share a byte. Windows whose heads lie between each other's (q, k and v side by
+ * side for each head) count as sharing bytes where one of them is written.
  * T == 0 launches nothing.
  * Performance: one launch, one pass. See the kernel's notes in rope.cuh.
  */
@@ -568,7 +570,11 @@ int rmsnorm_kv4_read(const void *cache, int64_t pages, int64_t page_size,
  * query tokens is the last one cached (rmsnorm_rope_append_kv4 first, then
  * this call). Products in fp16 on the tensor cores with fp32 sums: the cached
  * values are exact in fp16, q is scaled by a power of two for each row, the
- * softmax's terms are rounded to fp16 in the sum over v (not in their own).
+ * softmax's terms are rounded to fp16 in the sum over v (not in their own):
+ * within 2^-11 of sum p |v|. For fp16 outputs the kernel for few rows a
+ * sequence adds what that lost (2^-22); the one for pieces of prompts does not,
+ * so an fp16 row may differ by its last bit with the number of rows beside it
+ * (error against 64 bits 2.1e-4 and 2.9e-4; bf16 1.7e-3 by both).
  *   q [T, heads, D], out [T, heads, D]: bf16 or fp16 (else
  *   RMSNORM_ERR_BAD_DTYPE), strides as for rmsnorm_heads;
  *   lse [T, heads] fp32 out or NULL: log sum_j exp(scale q . k_j), with which

@@ -117,6 +117,10 @@ int rmsnorm_kv4_attention(const void *q, int64_t q_token, int64_t q_head, void *
     // of 128 on 8): 1 x 128 tokens over 8192 87 / 120 us, 1 x 256 160 / 121; 4 x
     // 32 over 4096 52 / 65, 4 x 64 89 / 70; 16 x 16 over 2048 54 / 39; 14 heads of
     // 64 on 2: 4 x 64 over 4096 36 / 56, 4 x 256 121 / 58, 16 x 64 over 2048 69 / 35.
+    // Pieces of one length each: the starts are on the device, so the rule goes by
+    // their mean. Where one is long and the others single tokens it may be off: 512
+    // tokens beside 63 of one, over 2000 each, take 172 us by the kernel for many,
+    // which it picks, and 130 by the other (two calls, one for the piece: 46 + 42).
     const int64_t wide = B * ((rows + kv4_prompt_kernels.rows - 1) / kv4_prompt_kernels.rows) * kv_heads;
     const int ov = g_test_kv4.load(std::memory_order_relaxed);
     if (q_starts && (ov == 2 || (ov == 0 && T * heads >= (D == 128 ? 4400 : 5800) * ((wide + sms - 1) / sms)))) {

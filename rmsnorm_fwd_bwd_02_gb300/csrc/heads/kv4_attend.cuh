@@ -15,8 +15,11 @@
 // each row and adds p = 2^(x - m + 8). m moves only when some x passes m + 7,
 // which one vote a stage finds: after a row's first stages that is rare, and
 // p stays below 2^15. The denominators add p in fp32; the second product takes
-// it rounded to fp16, 2^-12 relative down to 2^-22 of the row's maximum: its
-// output has 16 bits too.
+// it rounded to fp16, within 2^-11 of itself down to 2^-22 of the row's maximum. For
+// bf16 outputs that is an eighth of the output's own half step (a row's error
+// against 64 bits 1.673e-3, 1.661e-3 with that step alone); for fp16 ones it
+// would be all of it, so they take what the rounding lost as a second half
+// (2.08e-4, which is the output's step alone).
 //
 // Layout. The cache's rows are the MMAs' M, the query rows (up to 8 NT of one
 // key head: G heads times the tokens) their N, since G is small: S^T = K Q^T
@@ -664,9 +667,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas_per_sm(NT)) kv4_atten
                     }
                 }
             }
-            // p, transposed for the second product. One rounding to fp16 is
-            // as large as an fp16 output's own: there a second half holds what
-            // the first has lost, and the weights are good to 2^-22.
+            // p, transposed for the second product; for fp16 outputs in two
+            // halves, with which the weights are good to 2^-22.
             uint32_t pb[NT][2][2], pl[kLow ? NT : 1][2][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {

@@ -2,7 +2,9 @@
 // query rows of a sequence and key head. Same result as kv4_attend.cuh (its
 // mathematics: the cache exact in fp16, q scaled by a power of two a row, the
 // softmax in powers of two with a reference that moves rarely), on the
-// fifth-generation tensor cores.
+// fifth-generation tensor cores. But for fp16 outputs: p is one half here, not
+// two, which would be half as many products again; a row's error against 64 bits
+// is 2.9e-4 with it (2.1e-4 there), for bf16 1.67e-3 by both.
 //
 // Why this shape. With hundreds of rows the products bound the call, and
 // widening the cache's bytes anew for every 16 rows costs more than they do.
